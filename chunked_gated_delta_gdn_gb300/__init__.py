@@ -16,6 +16,11 @@ its thin PyTorch binding:
   :func:`chunk_gated_delta_rule_bwd_fused_gates` and
   :func:`chunk_gated_delta_rule_fused_gates_trainable` -- the same through the fused gates
   (gradients w.r.t. a, b, A_log, dt_bias).
+* :func:`chunk_linear_attn`, :func:`chunk_linear_attn_bwd`, :func:`chunk_linear_attn_trainable`,
+  :func:`linear_attn_decode` -- linear attention with a decay for each head: chunked forward,
+  backward, autograd op and single-token decode on the same slot cache.
+* :func:`group_norm_act`, :func:`group_norm_act_bwd`, :func:`group_norm_act_trainable` -- group
+  norm with an activation or gate, channels last: forward, backward, autograd op.
 
 Device-side errors (bad slot, bad ``cu_seqlens``, a timed-out in-kernel wait) reach the
 caller only through a ``dev_status`` tensor, or as :class:`GdnDeviceError` with ``check=True``.
@@ -26,11 +31,16 @@ from .api import (GdnDeviceError, GdnError, chunk_fwd_path, chunk_gated_delta_pr
                   chunk_gated_delta_rule_trainable, chunk_workspace_size, gated_delta_decode,
                   gated_delta_decode_fused_gates, gated_delta_decode_multi,
                   gated_delta_product_decode)
+from .group_norm import group_norm_act, group_norm_act_bwd, group_norm_act_trainable
+from .linear_attn import (chunk_linear_attn, chunk_linear_attn_bwd, chunk_linear_attn_trainable,
+                          linear_attn_decode)
 
 __all__ = ["chunk_gated_delta_rule", "gated_delta_decode", "gated_delta_decode_multi",
            "chunk_gated_delta_rule_fused_gates", "gated_delta_decode_fused_gates",
            "chunk_gated_delta_product", "gated_delta_product_decode",
            "chunk_gated_delta_rule_bwd", "chunk_gated_delta_rule_trainable",
            "chunk_gated_delta_rule_bwd_fused_gates", "chunk_gated_delta_rule_fused_gates_trainable",
+           "chunk_linear_attn", "chunk_linear_attn_bwd", "chunk_linear_attn_trainable",
+           "linear_attn_decode", "group_norm_act", "group_norm_act_bwd", "group_norm_act_trainable",
            "chunk_workspace_size", "chunk_fwd_path", "GdnError", "GdnDeviceError"]
 __version__ = "0.1.0"

@@ -18,6 +18,7 @@ _lib = None
 GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_LAYOUT = 0, 1, 2, 3, 4
 GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_WORKSPACE = 5, 6, 7
 GDN_F32, GDN_BF16 = 0, 1
+GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
 GDN_DEV_BAD_SLOT, GDN_DEV_BAD_CU_SEQLENS, GDN_DEV_TIMEOUT = 1, 2, 4
 
 EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_path", "gdn_decode",
@@ -25,6 +26,11 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_path"
            "gdn_product_chunk_fwd", "gdn_product_chunk_fwd_workspace_size", "gdn_product_decode",
            "gdn_chunk_bwd", "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd_gated",
            "gdn_chunk_bwd_gated_workspace_size", "gdn_selftest_wait_timeout",
+           "gdn_linear_attn_chunk_fwd", "gdn_linear_attn_chunk_fwd_workspace_size",
+           "gdn_linear_attn_chunk_bwd", "gdn_linear_attn_chunk_bwd_workspace_size",
+           "gdn_linear_attn_decode",
+           "gdn_group_norm_act_fwd", "gdn_group_norm_act_fwd_workspace_size",
+           "gdn_group_norm_act_bwd", "gdn_group_norm_act_bwd_workspace_size",
            "gdn_status_string", "gdn_version")
 
 
@@ -93,6 +99,29 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.gdn_chunk_bwd_gated_workspace_size.restype = sz
         lib.gdn_selftest_wait_timeout.argtypes = [vp, ctypes.c_ulonglong, i, vp, vp]
         lib.gdn_selftest_wait_timeout.restype = i
+        lib.gdn_linear_attn_chunk_fwd.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, i, vp,
+                                                  vp, i, vp, i, vp, vp, sz, vp, vp]
+        lib.gdn_linear_attn_chunk_fwd.restype = i
+        lib.gdn_linear_attn_chunk_bwd.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, vp, i,
+                                                  vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+        lib.gdn_linear_attn_chunk_bwd.restype = i
+        for fn in (lib.gdn_linear_attn_chunk_fwd_workspace_size,
+                   lib.gdn_linear_attn_chunk_bwd_workspace_size):
+            fn.argtypes = [i, i, i, i, i, i, i, i]
+            fn.restype = sz
+        lib.gdn_linear_attn_decode.argtypes = [vp, vp, vp, vp, vp, i, vp, i, i, i, i, i, i, f, vp,
+                                               vp, vp]
+        lib.gdn_linear_attn_decode.restype = i
+        lib.gdn_group_norm_act_fwd.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, f, i, vp, vp, vp,
+                                               vp, sz, vp]
+        lib.gdn_group_norm_act_fwd.restype = i
+        lib.gdn_group_norm_act_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp,
+                                               vp, vp, vp, vp, sz, vp]
+        lib.gdn_group_norm_act_bwd.restype = i
+        for fn in (lib.gdn_group_norm_act_fwd_workspace_size,
+                   lib.gdn_group_norm_act_bwd_workspace_size):
+            fn.argtypes = [i, i, i, i, i]
+            fn.restype = sz
         lib.gdn_status_string.argtypes = [i]
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_version.argtypes = []

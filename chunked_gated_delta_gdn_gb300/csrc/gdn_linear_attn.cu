@@ -1,0 +1,326 @@
+// gdn_linear_attn.cu -- linear attention with a decay for each head on the CUDA cores: the
+// chunked pass for any accepted head dims and type, the single-token decode step, and the sum
+// over the value heads that share a query/key head.
+//
+// A chunk of L <= 64 tokens, with X the K x V state entering it and w_d = gamma^d:
+//   P_ij  = s_in w_{i-j} (q_i . k_j)   for j <= i, else 0           (reverse: w_{j-i}, j >= i)
+//   o_i   = s_out (w_{i+1} X^T q_i + sum_j P_ij v_j)                (reverse: w_{L-1-i})
+//   X    <- w_L X + sum_j s_in w_{L-1-j} k_j v_j^T                  (reverse: w_{j+1})
+#include <atomic>
+
+#include "gdn_linear_attn.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kLaThreads = 256;
+
+// 4 consecutive elements as floats.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 x) {
+  __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+  uint2 u;
+  u.x = *reinterpret_cast<uint32_t*>(&lo);
+  u.y = *reinterpret_cast<uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(p) = u;
+}
+
+__device__ __forceinline__ void fma4(float4& a, float s, const float4& x) {
+  a.x = fmaf(s, x.x, a.x); a.y = fmaf(s, x.y, a.y);
+  a.z = fmaf(s, x.z, a.z); a.w = fmaf(s, x.w, a.w);
+}
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float acc) {
+  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, acc))));
+}
+
+// Shared floats of the chunked pass: q, k rows padded by 4 (the rows that 16 threads read at
+// one column fall into different banks), v, the state, P padded by 4, the decay table.
+__host__ __device__ inline int la_smem_floats(int K, int V) {
+  return 2 * kChunk * (K + 4) + kChunk * V + K * V + kChunk * (kChunk + 4) + 80;
+}
+
+// One CTA per (sequence, head), 256 threads as 16 x 16; the state stays in shared memory for the
+// whole sequence.  Every product is register-blocked: P 4 x 4 a thread, o 4 x 8, X 8 x 8.
+template <typename T, typename TO>
+__global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const LinAttnPass p) {
+  extern __shared__ __align__(16) float sm[];
+  const int K = p.K, V = p.V, KS = K + 4;
+  float* sQ = sm;
+  float* sK = sQ + kChunk * KS;
+  float* sV = sK + kChunk * KS;
+  float* sX = sV + kChunk * V;
+  float* sP = sX + K * V;                 // [64][68]
+  float* sW = sP + kChunk * (kChunk + 4);   // gamma^0 .. gamma^64
+  constexpr int PS = kChunk + 4;
+  const int h = blockIdx.x % p.H, n = blockIdx.x / p.H;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const LaChain c = la_chain(p, n, h, tid == 0 && h == 0);
+  const int T_total = p.cu_seqlens ? p.T : p.B * p.T;
+  la_zero_rows(p, h, c.tail, T_total, tid, kLaThreads);
+  if (c.skip) return;
+  if (c.padding) {
+    la_zero_rows(p, h, c.bos, c.eos, tid, kLaThreads);
+    return;
+  }
+  const float ld = clamp_log_decay(p.log_decay[h]);
+  if (tid <= kChunk) sW[tid] = decay_pow(ld, (float)tid);
+  for (int e = tid; e < K * V; e += kLaThreads) {
+    const int kk = e / V, vv = e - kk * V;
+    sX[e] = c.init ? c.init[p.initial_t ? vv * K + kk : e] : 0.f;
+  }
+  const int nch = (c.eos - c.bos + kChunk - 1) / kChunk;
+  const int K4 = K / 4, V4 = V / 4;
+  const T* gq = reinterpret_cast<const T*>(p.q);
+  const T* gk = reinterpret_cast<const T*>(p.k);
+  const T* gv = reinterpret_cast<const T*>(p.v);
+  const int hq = h / (p.H / p.Hq), hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
+  for (int cc = 0; cc < nch; ++cc) {
+    const int ch = p.reverse ? nch - 1 - cc : cc;
+    const int t0 = c.bos + ch * kChunk, L = min(kChunk, c.eos - t0);
+    __syncthreads();
+    for (int e = tid; e < kChunk * K4; e += kLaThreads) {
+      const int t = e / K4, d = 4 * (e - t * K4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (t < L) {
+        x = load4(gq + ((size_t)(t0 + t) * p.Hq + hq) * K + d);
+        y = load4(gk + ((size_t)(t0 + t) * p.Hk + hk) * K + d);
+      }
+      *reinterpret_cast<float4*>(sQ + t * KS + d) = x;
+      *reinterpret_cast<float4*>(sK + t * KS + d) = y;
+    }
+    for (int e = tid; e < kChunk * V4; e += kLaThreads) {
+      const int t = e / V4, d = 4 * (e - t * V4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < L) x = load4(gv + ((size_t)(t0 + t) * p.Hv + hv) * V + d);
+      *reinterpret_cast<float4*>(sV + t * V + d) = x;
+    }
+    __syncthreads();
+    {   // P: rows ty + 16 a, columns tx + 16 b
+      float acc[4][4] = {};
+      for (int d = 0; d < K; d += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          a[m] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * m) * KS + d);
+          b[m] = *reinterpret_cast<const float4*>(sK + (tx + 16 * m) * KS + d);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = ty + 16 * i, s = tx + 16 * j, dist = p.reverse ? s - r : r - s;
+          sP[r * PS + s] = dist >= 0 ? p.s_in * sW[dist] * acc[i][j] : 0.f;
+        }
+    }
+    __syncthreads();
+    // o: rows 4 ty .. 4 ty + 3, columns 4 tx + 64 m .. + 3
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const int col = 4 * tx + 64 * m;
+      if (col >= V) break;
+      float4 acc[4] = {};
+      for (int d = 0; d < K; d += 4) {
+        float4 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * KS + d);
+#pragma unroll
+        for (int dd = 0; dd < 4; ++dd) {
+          const float4 x = *reinterpret_cast<const float4*>(sX + (d + dd) * V + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        const float w = sW[p.reverse ? max(0, L - 1 - r) : r + 1];
+        acc[i].x *= w; acc[i].y *= w; acc[i].z *= w; acc[i].w *= w;
+      }
+      for (int j = 0; j < L; j += 4) {   // P is zero from L on
+        float4 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * PS + j);
+#pragma unroll
+        for (int dd = 0; dd < 4; ++dd) {
+          const float4 x = *reinterpret_cast<const float4*>(sV + (j + dd) * V + col);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (r >= L) continue;
+        float4 x = acc[i];
+        x.x *= p.s_out; x.y *= p.s_out; x.z *= p.s_out; x.w *= p.s_out;
+        store4(reinterpret_cast<TO*>(p.o) + ((size_t)(t0 + r) * p.H + h) * V + col, x);
+      }
+    }
+    __syncthreads();   // the state has been read
+    // X: rows 4 ty + 64 a .. + 3, columns 4 tx + 64 b .. + 3
+    const float2 gl = decay_pow2(ld, L);
+#pragma unroll
+    for (int ma = 0; ma < 2; ++ma) {
+      const int row = 4 * ty + 64 * ma;
+      if (row >= K) break;
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb) {
+        const int col = 4 * tx + 64 * mb;
+        if (col >= V) break;
+        float4 acc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 x = *reinterpret_cast<const float4*>(sX + (row + i) * V + col);
+          acc[i] = make_float4(mul2(x.x, gl), mul2(x.y, gl), mul2(x.z, gl), mul2(x.w, gl));
+        }
+        for (int j = 0; j < L; ++j) {
+          float4 kk = *reinterpret_cast<const float4*>(sK + j * KS + row);
+          const float4 x = *reinterpret_cast<const float4*>(sV + j * V + col);
+          const float w = p.s_in * sW[p.reverse ? j + 1 : L - 1 - j];
+          fma4(acc[0], kk.x * w, x);
+          fma4(acc[1], kk.y * w, x);
+          fma4(acc[2], kk.z * w, x);
+          fma4(acc[3], kk.w * w, x);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(sX + (row + i) * V + col) = acc[i];
+      }
+    }
+  }
+  __syncthreads();
+  if (c.fin)
+    for (int e = tid; e < K * V; e += kLaThreads) c.fin[e] = sX[e];
+}
+
+// Sum of the value heads that share a query/key head: one thread per 4 elements.
+template <typename T>
+__global__ void linear_attn_fold_kernel(const float* part, T* out, long long rows, int group, int D) {
+  const int D4 = D / 4;
+  const long long n = rows * D4;
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n;
+       e += (long long)gridDim.x * blockDim.x) {
+    const long long r = e / D4;
+    const int d = 4 * (int)(e - r * D4);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j = 0; j < group; ++j) {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(part + (r * group + j) * D + d));
+      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+    }
+    store4(out + r * D + d, s);
+  }
+}
+
+// One CTA per (request, head): S <- gamma S + k v^T, o = scale S^T q, the state read and written
+// once.  Thread t owns the float4 column group t % (V / 4) of every (threads / (V / 4))-th row.
+template <typename T>
+__global__ void __launch_bounds__(kLaThreads) linear_attn_decode_kernel(const LinAttnDecodeArgs a) {
+  __shared__ float sq[GDN_MAX_HEAD_DIM], sk[GDN_MAX_HEAD_DIM];
+  __shared__ float4 red[kLaThreads];
+  const int K = a.K, V = a.V, V4 = V / 4;
+  const int h = blockIdx.x % a.Hv, i = blockIdx.x / a.Hv, tid = threadIdx.x;
+  const int slot = a.batch_indices ? a.batch_indices[i] : i;
+  T* o = reinterpret_cast<T*>(a.o) + ((size_t)i * a.Hv + h) * V;
+  if (slot < 0 || slot >= a.num_slots) {
+    if (slot != -1 && tid == 0) report(a.dev_status, GDN_DEV_BAD_SLOT);
+    for (int d = tid; d < V; d += kLaThreads) store_elem(o, d, 0.f, a.io_dtype);
+    return;
+  }
+  const int hq = h / (a.Hv / a.Hqk);
+  const size_t qk = ((size_t)i * a.Hqk + hq) * K;
+  if (tid < K) {
+    sq[tid] = load_elem(a.q, qk + tid, a.io_dtype) * a.scale;
+    sk[tid] = load_elem(a.k, qk + tid, a.io_dtype);
+  }
+  const float g = expf(a.log_decay[h]);
+  __syncthreads();
+  const int G = kLaThreads / V4, c = tid % V4, r0 = tid / V4;
+  float* S = a.state + ((size_t)slot * a.Hv + h) * (size_t)K * V;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r0 < G) {
+    const float4 v = load4(reinterpret_cast<const T*>(a.v) + ((size_t)i * a.Hv + h) * V + 4 * c);
+    for (int r = r0; r < K; r += G) {
+      float4* s = reinterpret_cast<float4*>(S + (size_t)r * V) + c;
+      float4 x = *s;
+      const float k = sk[r], q = sq[r];
+      x.x = fmaf(k, v.x, g * x.x); x.y = fmaf(k, v.y, g * x.y);
+      x.z = fmaf(k, v.z, g * x.z); x.w = fmaf(k, v.w, g * x.w);
+      *s = x;
+      fma4(acc, q, x);
+    }
+  }
+  red[tid] = acc;
+  __syncthreads();
+  if (tid < V4) {
+    for (int r = 1; r < G; ++r) {
+      const float4 x = red[r * V4 + tid];
+      acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+    }
+    store4(o + 4 * tid, acc);
+  }
+}
+
+template <typename T, typename TO>
+cudaError_t launch_pass(const LinAttnPass& p) {
+  const long long blocks = (long long)p.num_seqs * p.H;
+  if (blocks <= 0) return cudaSuccess;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  static std::atomic<bool> attr_set[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
+    err = cudaFuncSetAttribute(linear_attn_kernel<T, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               la_smem_floats(GDN_MAX_HEAD_DIM, GDN_MAX_HEAD_DIM) * (int)sizeof(float));
+    if (err != cudaSuccess) return err;
+    if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
+  }
+  linear_attn_kernel<T, TO><<<(unsigned)blocks, kLaThreads, la_smem_floats(p.K, p.V) * sizeof(float),
+                              p.stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_attn_generic(const LinAttnPass& p) {
+  if (p.io_dtype == GDN_F32) return launch_pass<float, float>(p);
+  return p.o_f32 ? launch_pass<__nv_bfloat16, float>(p) : launch_pass<__nv_bfloat16, __nv_bfloat16>(p);
+}
+
+cudaError_t launch_linear_attn_fold(const float* part, void* out, long long T_total, int Hqk,
+                                    int group, int D, int io_dtype, cudaStream_t stream) {
+  const long long rows = T_total * Hqk, n = rows * (D / 4);
+  if (n == 0) return cudaSuccess;
+  const unsigned grid = (unsigned)min((n + 255) / 256, 152LL * 16);
+  if (io_dtype == GDN_F32)
+    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part, reinterpret_cast<float*>(out), rows, group, D);
+  else
+    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part, reinterpret_cast<__nv_bfloat16*>(out), rows,
+                                                      group, D);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear_attn_decode(const LinAttnDecodeArgs& a) {
+  const long long blocks = (long long)a.n * a.Hv;
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (a.io_dtype == GDN_F32)
+    linear_attn_decode_kernel<float><<<(unsigned)blocks, kLaThreads, 0, a.stream>>>(a);
+  else
+    linear_attn_decode_kernel<__nv_bfloat16><<<(unsigned)blocks, kLaThreads, 0, a.stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -1,0 +1,69 @@
+// gdn_linear_attn.h -- launchers of linear attention with a decay for each head (not public).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gdn.h"
+
+namespace gdn {
+
+// One pass of decayed linear attention over every (sequence n, value head h).  With
+// gamma = exp(log_decay[h]) and X the K x V state, forwards in time
+//   X_t = gamma X_{t-1} + s_in k_t v_t^T,      o_t = s_out X_t^T q_t,
+// and, reverse != 0, backwards in time with the decay after the read-out (the adjoint order)
+//   Y_t = X_{t+1} + s_in k_t v_t^T,  o_t = s_out Y_t^T q_t,  X_t = gamma Y_t.
+// The backward is three such passes: dq reads (d_o, v, k), dv reads (k, q, d_o) and dk reads
+// (v, d_o, q), the last two in reverse.  q, k, v, o here are the roles in the pass, each with
+// its own head count (H / heads value heads share a row).
+struct LinAttnPass {
+  const void* q;             // [T, Hq, K]
+  const void* k;             // [T, Hk, K]
+  const void* v;             // [T, Hv, V]
+  int Hq, Hk, Hv;
+  int K, V;
+  int H;                     // value heads of the operator (chains per sequence)
+  const float* log_decay;    // [H]
+  int B, T;                  // uniform rows; with cu_seqlens B = 1 and T the packed token count
+  const int32_t* cu_seqlens;
+  int num_seqs;
+  const int32_t* state_indices;
+  int num_slots;
+  const float* initial;      // fp32 [N or slots, H, K, V] ([.., V, K] with initial_t), or NULL
+  int initial_t;
+  float* final_state;        // fp32 [N or slots, H, K, V], or NULL
+  float s_in, s_out;
+  int reverse;
+  void* o;                   // [T, H, V]: io_dtype, or fp32 with o_f32
+  int o_f32;
+  int io_dtype;
+  int* dev_status;
+  cudaStream_t stream;
+};
+
+cudaError_t launch_linear_attn_generic(const LinAttnPass& p);
+
+// out[t, hq, :] = sum over the group's value heads of part[t, hq * group + j, :] (fp32 in, io
+// dtype out, heads added in order).
+cudaError_t launch_linear_attn_fold(const float* part, void* out, long long T_total, int Hqk,
+                                    int group, int D, int io_dtype, cudaStream_t stream);
+
+struct LinAttnDecodeArgs {
+  const void* q;             // [n, Hqk, K]
+  const void* k;             // [n, Hqk, K]
+  const void* v;             // [n, Hv, V]
+  const float* log_decay;    // [Hv]
+  float* state;              // [num_slots, Hv, K, V]
+  int num_slots;
+  const int32_t* batch_indices;
+  int n, Hqk, Hv, K, V;
+  int io_dtype;
+  float scale;
+  void* o;                   // [n, Hv, V]
+  int* dev_status;
+  cudaStream_t stream;
+};
+cudaError_t launch_linear_attn_decode(const LinAttnDecodeArgs& a);
+
+}  // namespace gdn

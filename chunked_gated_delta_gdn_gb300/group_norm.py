@@ -1,0 +1,125 @@
+"""Group norm with an activation, channels last: the PyTorch binding of ``gdn_group_norm_act_*``.
+
+For each row and group of C / G channels, mean and (biased) variance over the positions and the
+group's channels; ``u`` is the normalised, scaled and shifted value, and
+
+    y = act(u)              without a gate,
+    y = u * act(gate)       with one.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _lib
+from .api import _DT, _need, _ptr, _stream
+from .linear_attn import _scratch
+
+__all__ = ["group_norm_act", "group_norm_act_bwd", "group_norm_act_trainable"]
+
+_ACT = {None: _lib.GDN_ACT_NONE, "none": _lib.GDN_ACT_NONE, "silu": _lib.GDN_ACT_SILU}
+
+
+def _inputs(x, num_groups, weight, bias, activation, gate):
+    """Checks shared by the calls; returns (N, L, C, G, wb dtype code, act code)."""
+    _need(x, "x", (torch.float32, torch.bfloat16))
+    if x.dim() < 2:
+        raise ValueError("x must be [N, ..., C]")
+    N, C, G = x.shape[0], x.shape[-1], int(num_groups)
+    if G < 1 or C < 1 or C % G:
+        raise ValueError("%d channels do not split into %d groups" % (C, G))
+    if activation not in _ACT:
+        raise ValueError("activation must be None or 'silu' (got %r)" % (activation,))
+    L = 1
+    for s in x.shape[1:-1]:
+        L *= s
+    wb = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is not None:
+            _need(t, name, (x.dtype, torch.float32) if wb is None else wb, x.device, (C,))
+            wb = t.dtype
+    if gate is not None:
+        _need(gate, "gate", x.dtype, x.device, x.shape)
+    return N, L, C, G, _DT[wb or torch.float32], _ACT[activation]
+
+
+def group_norm_act(x, num_groups, weight=None, bias=None, eps=1e-5, activation="silu", gate=None, *,
+                   out=None, return_stats=False, workspace=None):
+    """Forward through ``gdn_group_norm_act_fwd``.
+
+    x [N, ..., C] contiguous (channels last; the middle dims are the positions, and x [N, C]
+    normalises each row by itself, as behind linear attention: N tokens, C = H V, G = H);
+    weight, bias [C] in fp32 or x's dtype, or None; activation "silu" or None; gate like x or
+    None.  Returns y, or ``(y, mean, rstd)`` with ``return_stats`` (both [N, G] fp32, what
+    :func:`group_norm_act_bwd` takes).
+    """
+    N, L, C, G, wb, act = _inputs(x, num_groups, weight, bias, activation, gate)
+    dev = x.device
+    if out is None:
+        out = torch.empty_like(x)
+    _need(out, "out", x.dtype, dev, x.shape)
+    mean = rstd = None
+    if return_stats:
+        mean = torch.zeros((N, G), dtype=torch.float32, device=dev) if L == 0 else \
+            torch.empty((N, G), dtype=torch.float32, device=dev)
+        rstd = torch.empty_like(mean) if L else torch.zeros_like(mean)
+    lib = _lib.load()
+    need = lib.gdn_group_norm_act_fwd_workspace_size(N, L, C, G, _DT[x.dtype])
+    workspace, ws_bytes = _scratch(need, "gdn_group_norm_act_fwd", workspace, dev)
+    st = lib.gdn_group_norm_act_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), N, L, C, G,
+                                    _DT[x.dtype], wb, float(eps), act, _ptr(out), _ptr(mean),
+                                    _ptr(rstd), _ptr(workspace), ws_bytes, _stream(dev))
+    _lib.check("gdn_group_norm_act_fwd", st)
+    return (out, mean, rstd) if return_stats else out
+
+
+def group_norm_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, activation="silu",
+                       gate=None, *, need_params=True, workspace=None):
+    """Gradients of :func:`group_norm_act` through ``gdn_group_norm_act_bwd``: ``(dx, dweight,
+    dbias, dgate)``, dx and dgate in x's dtype, dweight and dbias fp32 [C] (None without
+    ``need_params``), dgate None without a gate."""
+    N, L, C, G, wb, act = _inputs(x, num_groups, weight, bias, activation, gate)
+    dev = x.device
+    _need(dy, "dy", x.dtype, dev, x.shape)
+    _need(mean, "mean", torch.float32, dev, (N, G))
+    _need(rstd, "rstd", torch.float32, dev, (N, G))
+    dx = torch.empty_like(x)
+    dgate = None if gate is None else torch.empty_like(x)
+    dw = torch.empty(C, dtype=torch.float32, device=dev) if need_params else None
+    db = torch.empty(C, dtype=torch.float32, device=dev) if need_params else None
+    lib = _lib.load()
+    need = lib.gdn_group_norm_act_bwd_workspace_size(N, L, C, G, _DT[x.dtype])
+    workspace, ws_bytes = _scratch(need, "gdn_group_norm_act_bwd", workspace, dev)
+    st = lib.gdn_group_norm_act_bwd(_ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
+                                    _ptr(mean), _ptr(rstd), N, L, C, G, _DT[x.dtype], wb, act,
+                                    _ptr(dx), _ptr(dgate), _ptr(dw), _ptr(db), _ptr(workspace),
+                                    ws_bytes, _stream(dev))
+    _lib.check("gdn_group_norm_act_bwd", st)
+    return dx, dw, db, dgate
+
+
+class _GroupNormAct(torch.autograd.Function):
+    """gdn_group_norm_act_fwd forward, gdn_group_norm_act_bwd backward."""
+
+    @staticmethod
+    def forward(ctx, x, num_groups, weight, bias, eps, activation, gate):
+        y, mean, rstd = group_norm_act(x, num_groups, weight, bias, eps, activation, gate,
+                                       return_stats=True)
+        ctx.save_for_backward(x, weight, bias, gate, mean, rstd)
+        ctx.num_groups, ctx.activation = num_groups, activation
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, gate, mean, rstd = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db, dgate = group_norm_act_bwd(dy.contiguous(), x, mean, rstd, ctx.num_groups,
+                                               weight, bias, ctx.activation, gate,
+                                               need_params=need[2] or need[3])
+        return (dx, None, dw.to(weight.dtype) if need[2] else None,
+                db.to(bias.dtype) if need[3] else None, None, None, dgate)
+
+
+def group_norm_act_trainable(x, num_groups, weight=None, bias=None, eps=1e-5, activation="silu",
+                             gate=None):
+    """:func:`group_norm_act` as a differentiable op (torch autograd) in x, weight, bias, gate."""
+    return _GroupNormAct.apply(x, num_groups, weight, bias, eps, activation, gate)

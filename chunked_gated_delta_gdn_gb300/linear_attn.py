@@ -1,0 +1,205 @@
+"""Linear attention with a decay for each head: the PyTorch binding of the ``gdn_linear_attn_*``
+entry points (argument checks, outputs and scratch; every computation runs in the kernels).
+
+    S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,    o_t = scale S_t^T q_t
+
+per (sequence, value head h) with a K x V fp32 state in the layout of the gated delta rule's, so
+both kinds of layer share a slot cache.  ``log_decay`` is a constant of the layer: no gradient.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from .api import (DEVICE_ERRORS_DOC, _DT, _need, _ptr, _raise_on_status, _scale, _status, _stream)
+
+__all__ = ["chunk_linear_attn", "chunk_linear_attn_bwd", "chunk_linear_attn_trainable",
+           "linear_attn_decode"]
+
+
+def _inputs(q, k, v, log_decay, cu_seqlens):
+    """Checks shared by the chunked calls; returns (device, dtype, sizes, N)."""
+    _need(q, "q", (torch.float32, torch.bfloat16))
+    dev, dt = q.device, q.dtype
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, Hqk, K]")
+    _need(k, "k", dt, dev, q.shape)
+    _need(v, "v", dt, dev)
+    if v.dim() != 4 or v.shape[:2] != q.shape[:2]:
+        raise ValueError("v must be [B, T, Hv, V]")
+    B, T, Hqk, K = q.shape
+    Hv, V = v.shape[2], v.shape[3]
+    _need(log_decay, "log_decay", torch.float32, dev, (Hv,))
+    N = B
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if B != 1:
+            raise ValueError("cu_seqlens requires B == 1")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [num_seqs + 1]")
+        N = cu_seqlens.numel() - 1
+    return dev, dt, (B, T, Hqk, Hv, K, V), N
+
+
+def _scratch(need, name, workspace, dev):
+    """The workspace to pass on: the caller's when it is large enough, else a new one."""
+    if need == (1 << 64) - 1:
+        raise ValueError("sizes rejected by %s" % name)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def chunk_linear_attn(q, k, v, log_decay, scale=None, initial_state=None, output_final_state=False,
+                      cu_seqlens=None, *, state_indices=None, out=None, final_state=None,
+                      workspace=None, dev_status=None, check=False
+                      ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Chunked forward through ``gdn_linear_attn_chunk_fwd``.
+
+    q, k [B, T, Hqk, K]; v [B, T, Hv, V]; log_decay [Hv] fp32; scale None -> 1/sqrt(K).  Returns
+    ``(o, final_state or None)``.  ``cu_seqlens`` ([N + 1] int32, B == 1), ``state_indices`` (a
+    slot cache, -1 = padding, updated in place by default), ``out``, ``final_state``,
+    ``workspace``, ``dev_status`` and ``check`` as in :func:`chunk_gated_delta_rule`.
+    """
+    dev, dt, (B, T, Hqk, Hv, K, V), N = _inputs(q, k, v, log_decay, cu_seqlens)
+    num_slots = 0
+    st_shape = (N, Hv, K, V)
+    if state_indices is not None:
+        _need(state_indices, "state_indices", torch.int32, dev, (N,))
+        cache = initial_state if initial_state is not None else final_state
+        if cache is None:
+            raise ValueError("state_indices needs initial_state or final_state (the slot cache)")
+        num_slots = cache.shape[0]
+        st_shape = (num_slots, Hv, K, V)
+        if output_final_state and final_state is None:
+            final_state = initial_state
+    if initial_state is not None:
+        _need(initial_state, "initial_state", torch.float32, dev, st_shape)
+    if output_final_state:
+        if final_state is None:
+            final_state = torch.empty(st_shape, dtype=torch.float32, device=dev)
+        _need(final_state, "final_state", torch.float32, dev, st_shape)
+    else:
+        final_state = None
+    if out is None:
+        out = torch.empty((B, T, Hv, V), dtype=dt, device=dev)
+    _need(out, "out", dt, dev, (B, T, Hv, V))
+    L = _lib.load()
+    need = L.gdn_linear_attn_chunk_fwd_workspace_size(B, T, Hqk, Hv, K, V, N, _DT[dt])
+    workspace, ws_bytes = _scratch(need, "gdn_linear_attn_chunk_fwd", workspace, dev)
+    dev_status = _status(dev_status, check, dev)
+    st = L.gdn_linear_attn_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), B, T, Hqk, Hv, K, V,
+                                     _DT[dt], _scale(scale), _ptr(initial_state),
+                                     int(bool(output_final_state)), _ptr(final_state),
+                                     _ptr(cu_seqlens), N, _ptr(state_indices), num_slots, _ptr(out),
+                                     _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(dev))
+    _lib.check("gdn_linear_attn_chunk_fwd", st)
+    _raise_on_status("gdn_linear_attn_chunk_fwd", dev_status, check)
+    return out, final_state
+
+
+def chunk_linear_attn_bwd(q, k, v, log_decay, d_o, d_final_state=None, scale=None,
+                          initial_state=None, cu_seqlens=None, *, need_d_initial_state=True,
+                          workspace=None, dev_status=None, check=False):
+    """Gradients of :func:`chunk_linear_attn` (no slot cache) through
+    ``gdn_linear_attn_chunk_bwd``: ``(dq, dk, dv, d_initial_state)``, the first three in q's
+    dtype, the last fp32 [N, Hv, K, V] (None when ``need_d_initial_state`` is False)."""
+    dev, dt, (B, T, Hqk, Hv, K, V), N = _inputs(q, k, v, log_decay, cu_seqlens)
+    _need(d_o, "d_o", dt, dev, (B, T, Hv, V))
+    st_shape = (N, Hv, K, V)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", torch.float32, dev, st_shape)
+    if d_final_state is not None:
+        _need(d_final_state, "d_final_state", torch.float32, dev, st_shape)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dh0 = torch.empty(st_shape, dtype=torch.float32, device=dev) if need_d_initial_state else None
+    L = _lib.load()
+    need = L.gdn_linear_attn_chunk_bwd_workspace_size(B, T, Hqk, Hv, K, V, N, _DT[dt])
+    workspace, ws_bytes = _scratch(need, "gdn_linear_attn_chunk_bwd", workspace, dev)
+    dev_status = _status(dev_status, check, dev)
+    st = L.gdn_linear_attn_chunk_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), B, T, Hqk, Hv, K, V,
+                                     _DT[dt], _scale(scale), _ptr(initial_state), _ptr(cu_seqlens),
+                                     N, _ptr(d_o), _ptr(d_final_state), _ptr(dq), _ptr(dk),
+                                     _ptr(dv), _ptr(dh0), _ptr(workspace), ws_bytes,
+                                     _ptr(dev_status), _stream(dev))
+    _lib.check("gdn_linear_attn_chunk_bwd", st)
+    _raise_on_status("gdn_linear_attn_chunk_bwd", dev_status, check)
+    return dq, dk, dv, dh0
+
+
+class _ChunkLinearAttn(torch.autograd.Function):
+    """gdn_linear_attn_chunk_fwd forward, gdn_linear_attn_chunk_bwd backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, initial_state, scale, output_final_state, cu_seqlens):
+        o, fin = chunk_linear_attn(q, k, v, log_decay, scale=scale, initial_state=initial_state,
+                                   output_final_state=output_final_state, cu_seqlens=cu_seqlens)
+        ctx.save_for_backward(q, k, v, log_decay, initial_state, cu_seqlens)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, fin
+
+    @staticmethod
+    def backward(ctx, d_o, d_fin):
+        q, k, v, log_decay, init, cu = ctx.saved_tensors
+        d_o = torch.zeros_like(v) if d_o is None else d_o.contiguous()
+        dq, dk, dv, dh0 = chunk_linear_attn_bwd(
+            q, k, v, log_decay, d_o, None if d_fin is None else d_fin.contiguous(),
+            scale=ctx.scale, initial_state=init, cu_seqlens=cu,
+            need_d_initial_state=init is not None and ctx.needs_input_grad[4])
+        return dq, dk, dv, None, dh0, None, None, None
+
+
+def chunk_linear_attn_trainable(q, k, v, log_decay, scale=None, initial_state=None,
+                                output_final_state=False, cu_seqlens=None):
+    """:func:`chunk_linear_attn` as a differentiable op (torch autograd) in q, k, v and
+    ``initial_state``.  Returns ``(o, final_state or None)``."""
+    if log_decay.requires_grad:
+        raise ValueError("log_decay is a constant of the layer: it has no gradient")
+    return _ChunkLinearAttn.apply(q, k, v, log_decay, initial_state, scale,
+                                  bool(output_final_state), cu_seqlens)
+
+
+def linear_attn_decode(q, k, v, log_decay, ssm_state, batch_indices=None, scale=None, *, out=None,
+                       dev_status=None, check=False) -> torch.Tensor:
+    """One token per request through ``gdn_linear_attn_decode`` (the recurrent form);
+    ``ssm_state`` is updated in place.
+
+    q, k [n, Hqk, K]; v [n, Hv, V]; log_decay [Hv] fp32; ssm_state [num_slots, Hv, K, V] fp32;
+    batch_indices [n] int32 (-1 = padding: a zero row) or None (request i uses slot i).  Returns
+    o [n, Hv, V].
+    """
+    _need(q, "q", (torch.float32, torch.bfloat16))
+    dev, dt = q.device, q.dtype
+    if q.dim() != 3:
+        raise ValueError("q must be [n, Hqk, K]")
+    n, Hqk, K = q.shape
+    _need(k, "k", dt, dev, q.shape)
+    _need(v, "v", dt, dev)
+    if v.dim() != 3 or v.shape[0] != n:
+        raise ValueError("v must be [n, Hv, V]")
+    Hv, V = v.shape[1], v.shape[2]
+    _need(log_decay, "log_decay", torch.float32, dev, (Hv,))
+    _need(ssm_state, "ssm_state", torch.float32, dev)
+    if ssm_state.dim() != 4 or tuple(ssm_state.shape[1:]) != (Hv, K, V):
+        raise ValueError("ssm_state must be [num_slots, Hv, K, V]")
+    if batch_indices is not None:
+        _need(batch_indices, "batch_indices", torch.int32, dev, (n,))
+    if out is None:
+        out = torch.empty((n, Hv, V), dtype=dt, device=dev)
+    _need(out, "out", dt, dev, (n, Hv, V))
+    dev_status = _status(dev_status, check, dev)
+    st = _lib.load().gdn_linear_attn_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+                                            _ptr(ssm_state), ssm_state.shape[0],
+                                            _ptr(batch_indices), n, Hqk, Hv, K, V, _DT[dt],
+                                            _scale(scale), _ptr(out), _ptr(dev_status),
+                                            _stream(dev))
+    _lib.check("gdn_linear_attn_decode", st)
+    _raise_on_status("gdn_linear_attn_decode", dev_status, check)
+    return out
+
+
+for _f in (chunk_linear_attn, chunk_linear_attn_bwd, linear_attn_decode):
+    _f.__doc__ += DEVICE_ERRORS_DOC

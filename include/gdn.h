@@ -1,5 +1,6 @@
 /*
- * gdn.h -- C ABI of libgdn, the GB300 (sm_103a) gated delta rule library.
+ * gdn.h -- C ABI of libgdn, the GB300 (sm_103a) gated delta rule library, with linear
+ * attention with a decay for each head and group norm with an activation beside it.
  *
  * The gated delta rule, per (sequence, value head h) with a K x V fp32 state S:
  *
@@ -417,6 +418,117 @@ gdn_status_t gdn_chunk_bwd_gated(const void* q, const void* k, const void* v, co
 /* Workspace (bytes) of gdn_chunk_bwd_gated; (size_t)-1 for sizes it would reject. */
 size_t gdn_chunk_bwd_gated_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
                                           int num_seqs, gdn_dtype_t io_dtype);
+
+/*
+ * Linear attention with a decay for each head.  Per (sequence, value head h), with
+ * gamma = exp(log_decay[h]) and a K x V fp32 state S:
+ *
+ *     S   <- gamma S + k_t v_t^T
+ *     o_t  = scale * S^T q_t
+ *
+ * value head h reading query/key head h / (Hv / Hqk).  The state has the layout of the gated
+ * delta rule's, so the two kinds of layer share a slot cache.  The decay is a constant of the
+ * layer; a log_decay of -inf keeps nothing (o_t = scale (q_t . k_t) v_t).
+ *
+ * gdn_linear_attn_chunk_fwd -- chunked forward (prompts, training).
+ *   q, k        [B, T, Hqk, K] io_dtype, device.      v, o  [B, T, Hv, V] io_dtype, device.
+ *   log_decay   [Hv] fp32, device.
+ *   K, V        1..GDN_MAX_HEAD_DIM, rows a multiple of 16 bytes.
+ *   scale       read-out scale; NaN selects 1/sqrt(K).
+ *   initial_state, output_final_state, final_state, cu_seqlens, num_seqs, state_indices,
+ *   num_slots, dev_status, stream  as gdn_chunk_fwd: slot -1 is padding (zero rows, no state
+ *               access), sequences may be empty, final_state may be initial_state.
+ *   o           written completely; tokens past the last sequence get zero rows.  A sequence
+ *               whose cu_seqlens entries are not monotone within [0, T] (or whose first is not
+ *               0) is skipped and reported as GDN_DEV_BAD_CU_SEQLENS.
+ *   workspace   gdn_linear_attn_chunk_fwd_workspace_size(...) bytes, 256-byte aligned; NULL when
+ *               that is 0.
+ * A NaN or infinity in a token's q, k or v reaches that token's 64-token chunk and what follows
+ * it in its sequence, and no other sequence.
+ */
+size_t gdn_linear_attn_chunk_fwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
+                                                int num_seqs, gdn_dtype_t io_dtype);
+
+gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void* v,
+                                       const float* log_decay, int B, int T, int Hqk, int Hv, int K,
+                                       int V, gdn_dtype_t io_dtype, float scale,
+                                       const float* initial_state, int output_final_state,
+                                       float* final_state, const int32_t* cu_seqlens, int num_seqs,
+                                       const int32_t* state_indices, int num_slots, void* o,
+                                       void* workspace, size_t workspace_bytes, int* dev_status,
+                                       void* stream);
+
+/*
+ * gdn_linear_attn_chunk_bwd -- gradients of gdn_linear_attn_chunk_fwd (no slot cache).
+ *   d_o          [B, T, Hv, V] io_dtype.    d_final_state  [N, Hv, K, V] fp32 or NULL (zero).
+ *   dq, dk       [B, T, Hqk, K] io_dtype, the value heads of a query/key head summed in fp32
+ *                in order.   dv  [B, T, Hv, V] io_dtype.   All written completely, zero past the
+ *                last sequence.
+ *   d_initial_state  [N, Hv, K, V] fp32 or NULL.
+ *   workspace    gdn_linear_attn_chunk_bwd_workspace_size(...) bytes, 256-byte aligned.
+ * No atomics: bitwise identical from run to run.  log_decay has no gradient.
+ */
+size_t gdn_linear_attn_chunk_bwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
+                                                int num_seqs, gdn_dtype_t io_dtype);
+
+gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void* v,
+                                       const float* log_decay, int B, int T, int Hqk, int Hv, int K,
+                                       int V, gdn_dtype_t io_dtype, float scale,
+                                       const float* initial_state, const int32_t* cu_seqlens,
+                                       int num_seqs, const void* d_o, const float* d_final_state,
+                                       void* dq, void* dk, void* dv, float* d_initial_state,
+                                       void* workspace, size_t workspace_bytes, int* dev_status,
+                                       void* stream);
+
+/*
+ * gdn_linear_attn_decode -- one token per request on a slot cache, in place: the recurrent form.
+ * Slots, padding (-1: a zero row, the state untouched), errors and layouts as gdn_decode:
+ *   q, k [n, Hqk, K];  v, o [n, Hv, V];  ssm_state [num_slots, Hv, K, V] fp32.
+ */
+gdn_status_t gdn_linear_attn_decode(const void* q, const void* k, const void* v,
+                                    const float* log_decay, float* ssm_state, int num_slots,
+                                    const int32_t* batch_indices, int n, int Hqk, int Hv, int K,
+                                    int V, gdn_dtype_t io_dtype, float scale, void* o,
+                                    int* dev_status, void* stream);
+
+/*
+ * Group norm with an activation, channels last.  For each row n and each group of C / G
+ * channels, mean and variance (biased) over the L positions and the group's channels, then
+ *
+ *     u = (x - mean) / sqrt(var + eps) * weight + bias,
+ *     y = act(u)            without a gate,
+ *     y = u * act(gate)     with one.
+ *
+ *   x, y, gate  [N, L, C] io_dtype, device (gate may be NULL).  A norm of each token's heads, as
+ *               behind linear attention, has L = 1, N the tokens, C = H V and G = H.
+ *   weight, bias  [C] wb_dtype (GDN_F32 or io_dtype), each may be NULL (1, 0).
+ *   mean, rstd  [N, G] fp32, device, written; each may be NULL.  The backward reads them.
+ *   workspace   the matching _workspace_size(...) bytes, 256-byte aligned; NULL when that is 0.
+ * N * L = 0 writes nothing.  eps >= 0.  x, y, gate (dy, dx, dgate) start on 16-byte boundaries.
+ */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_act_t;
+
+size_t gdn_group_norm_act_fwd_workspace_size(int N, int L, int C, int G, gdn_dtype_t io_dtype);
+
+gdn_status_t gdn_group_norm_act_fwd(const void* x, const void* weight, const void* bias,
+                                    const void* gate, int N, int L, int C, int G,
+                                    gdn_dtype_t io_dtype, gdn_dtype_t wb_dtype, float eps,
+                                    gdn_act_t act, void* y, float* mean, float* rstd,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward, from dy, the forward's inputs and its mean and rstd: dx (and, with a gate,
+ * dgate) in io_dtype; dweight, dbias [C] fp32, each may be NULL.  No atomics: bitwise identical
+ * from run to run.
+ */
+size_t gdn_group_norm_act_bwd_workspace_size(int N, int L, int C, int G, gdn_dtype_t io_dtype);
+
+gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* weight,
+                                    const void* bias, const void* gate, const float* mean,
+                                    const float* rstd, int N, int L, int C, int G,
+                                    gdn_dtype_t io_dtype, gdn_dtype_t wb_dtype, gdn_act_t act,
+                                    void* dx, void* dgate, float* dweight, float* dbias,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * gdn_selftest_wait_timeout -- the bounded wait of the fused kernels, run on its own.
