@@ -765,24 +765,31 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
   return fn;
 }
 
-// [T_total, H, 128] bf16 -> 3-D map with 64 x 1 x 64 boxes, 128-byte swizzle,
-// zero fill past the last token.
-bool encode_map(CUtensorMap* m, const void* base, int H, int T_total) {
+// [T_total, H, D] bf16 -> 3-D map with 64 x 1 x 64 boxes, 128-byte swizzle,
+// zero fill past the last token (and past column D).
+bool encode_map(CUtensorMap* m, const void* base, int H, int T_total, int D = 128) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode_fn();
   if (!enc) return false;
-  cuuint64_t dims[3] = {128, (cuuint64_t)H, (cuuint64_t)T_total};
-  cuuint64_t strides[2] = {128 * 2, (cuuint64_t)H * 128 * 2};
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T_total};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
   cuuint32_t box[3] = {64, 1, 64};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&]() {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // The encoder is a driver call and wants a current context, which a thread that has made no
+  // runtime call yet (autograd's, say) does not have: make the device's current and try again.
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 }  // namespace
 
-bool encode_rows_map_bf16(CUtensorMap* m, const void* base, int H, int T_total) {
-  return encode_map(m, base, H, T_total);
+bool encode_rows_map_bf16(CUtensorMap* m, const void* base, int H, int T_total, int D) {
+  return encode_map(m, base, H, T_total, D);
 }
 
 bool chunk_tc_supported(int K, int V, int io_dtype, int beta_dtype) {

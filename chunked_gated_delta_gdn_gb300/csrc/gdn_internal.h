@@ -163,9 +163,10 @@ cudaError_t launch_chunk_bwd(const ChunkArgs& a, const BwdArgs& b);
 
 // Fused tcgen05 / TMEM / TMA path (bf16, K = V = 128).
 bool chunk_tc_supported(int K, int V, int io_dtype, int beta_dtype);
-// TMA map of a [T_total, H, 128] bf16 tensor with 64 x 1 x 64 boxes (64 features of one head
-// for 64 tokens, 128-byte swizzled), zero fill past the last token.
-bool encode_rows_map_bf16(CUtensorMap* m, const void* base, int H, int T_total);
+// TMA map of a [T_total, H, D] bf16 tensor with 64 x 1 x 64 boxes (64 features of one head
+// for 64 tokens, 128-byte swizzled), zero fill past the last token and past column D (D a
+// multiple of 8).
+bool encode_rows_map_bf16(CUtensorMap* m, const void* base, int H, int T_total, int D = 128);
 cudaError_t launch_chunk_tc(const ChunkArgs& a);
 // The planned forward (a.workspace): sequences sorted longest first, and, when the batch has
 // too few (sequence, head) chains to fill the GPU, sequences of at least 2 s chunks split into

@@ -42,7 +42,10 @@ struct LinAttnPass {
   cudaStream_t stream;
 };
 
+// CUDA cores: any accepted head dims, either type.
 cudaError_t launch_linear_attn_generic(const LinAttnPass& p);
+// Tensor cores: bf16 (o may be fp32), any accepted head dims.
+cudaError_t launch_linear_attn_tc(const LinAttnPass& p);
 
 // out[t, hq, :] = sum over the group's value heads of part[t, hq * group + j, :] (fp32 in, io
 // dtype out, heads added in order).

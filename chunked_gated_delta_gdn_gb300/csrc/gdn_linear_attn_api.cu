@@ -39,7 +39,10 @@ gdn::LinAttnPass base_pass(const float* log_decay, int B, int T, int Hv, gdn_dty
   return p;
 }
 
-cudaError_t run_pass(const gdn::LinAttnPass& p) { return gdn::launch_linear_attn_generic(p); }
+// bf16 runs on the tensor cores; fp32, whose 24-bit products they do not offer, on the CUDA cores.
+cudaError_t run_pass(const gdn::LinAttnPass& p) {
+  return p.io_dtype == GDN_BF16 ? gdn::launch_linear_attn_tc(p) : gdn::launch_linear_attn_generic(p);
+}
 
 // Scratch of the backward: per-value-head dq and dk (fp32) where value heads share a query/key
 // head.  One buffer serves both, one after the other.

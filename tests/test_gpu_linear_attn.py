@@ -283,6 +283,23 @@ def test_runs_are_bitwise_equal_and_on_any_stream():
     assert all(torch.equal(u, v) for u, v in zip(a, b))
 
 
+def test_first_call_of_a_thread():
+    """A thread that has made no CUDA call yet (as autograd's) has no current context."""
+    import threading
+    x = on_gpu(make(B=1, T=100, Hqk=1, Hv=1, dtype=BF16, seed=55, h0=False))
+    want = gdn.chunk_linear_attn_bwd(x["q"], x["k"], x["v"], x["log_decay"], x["v"])
+    spare = [torch.empty_like(t) for t in want if t is not None]
+    torch.cuda.synchronize()
+    del spare       # blocks for the thread's outputs, so that it allocates nothing on the device
+    got = []
+    t = threading.Thread(target=lambda: got.append(
+        gdn.chunk_linear_attn_bwd(x["q"], x["k"], x["v"], x["log_decay"], x["v"])))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert len(got) == 1 and all(torch.equal(a, b) for a, b in zip(got[0], want))
+
+
 def test_graph_capture():
     x = on_gpu(make(lens=[100, 0, 37], Hqk=2, Hv=2, dtype=BF16, seed=61))
     o = torch.empty_like(x["v"])
