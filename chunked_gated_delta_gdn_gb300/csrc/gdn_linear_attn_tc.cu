@@ -7,10 +7,10 @@
 // exponents, see gdn_linear_attn.h):
 //
 //   D    = [Q; K] K^T                      M=128 N=64  (rows 0-63 are Q K^T)
-//   P_ij = s_in w_{i-j} D_ij, j <= i       bf16, shared memory
+//   P_ij = s_in s_out w_{i-j} D_ij, j <= i bf16, shared memory
 //   O1^T = X^T Q^T                         M=128 (value features) N=64 (tokens)
 //   O2^T = V^T P^T                         M=128 N=64
-//   o_i  = s_out (w_{i+1} O1_i + O2_i)
+//   o_i  = s_out w_{i+1} O1_i + O2_i
 //   U^T  = V^T K~, K~_j = s_in w_{L-1-j} k_j     M=128 N=K
 //   X   <- w_L X + U
 //
@@ -48,13 +48,15 @@ constexpr uint32_t kStage = 49152;                 // [k half][Q 64 rows | K 64 
 constexpr uint32_t kStageV = 32768;                // [v half][64 tokens][128 B]
 constexpr uint32_t OFF_KT = 2 * kStage;            // 2 buffers x 3 terms of K~, tiles as K's
 constexpr uint32_t kKtTerm = 16384, kKtBuf = 3 * kKtTerm;
-constexpr uint32_t OFF_P = OFF_KT + 2 * kKtBuf;    // 2 x [64 i][64 j] bf16
-constexpr uint32_t OFF_O = OFF_P + 2 * 8192;       // output tile, [v half][64 tokens][128 B]
+constexpr uint32_t OFF_P = OFF_KT + 2 * kKtBuf;    // [64 i][64 j] bf16
+constexpr uint32_t OFF_O = OFF_P + 8192;       // output tile, [v half][64 tokens][128 B]
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
-constexpr uint32_t OFF_G = OFF_W + 288;            // float2[2]: decay of a full / the partial chunk
+constexpr uint32_t OFF_WP = OFF_W + 288;           // factors of P, see fill_p_table
+constexpr uint32_t kWpStride = 136;                // floats of one copy
+constexpr uint32_t OFF_G = OFF_WP + 4 * 4 * kWpStride;   // float2[2]: decay of a full / the partial chunk
 constexpr uint32_t OFF_BAR = OFF_G + 32;
 constexpr uint32_t SMEM_USED = OFF_BAR + 256;
-constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;
+constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;   // slack for aligning the base
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 // TMEM columns.
@@ -84,9 +86,19 @@ struct Unit {
   float* fin;
 };
 
+// A bounded wait that reads the clock only now and then (the failing polls of fifteen warps
+// share the issue slots with the work they wait for).
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitNs) return false;
+  }
+}
 // Every lane of the warp waits; the answer is the same for all of them.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, kWaitNs));
+  return __all_sync(0xffffffffu, wait_bar(bar, parity));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
@@ -95,6 +107,32 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&b);
+}
+// Two fp32 multiply-adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2v(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+// The upper halves of two fp32 values: both truncated to bf16, packed.
+__device__ __forceinline__ uint32_t top2(float2 x) {
+  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+}
+// What that truncation leaves (exact).
+__device__ __forceinline__ float2 rest2(float2 x) {
+  const float2 t = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+  return fma2(t, make_float2(-1.f, -1.f), x);
 }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -117,7 +155,7 @@ __device__ void load_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint
   const int kh = (p.K + 63) >> 6, vh = (p.V + 63) >> 6;
   for (int c = u.c0; c < u.c1; ++c) {
     const int i = c - u.c0, s = i & 1;
-    if (i >= 2 && !mbar_wait(&bars[B_EMPTY + s], (uint32_t)((i - 2) >> 1) & 1u, kWaitNs)) return;
+    if (i >= 2 && !wait_bar(&bars[B_EMPTY + s], (uint32_t)((i - 2) >> 1) & 1u)) return;
     const int t0 = chunk_at(p, u, c).t0;
     uint8_t* st = sm + s * kStage;
     mbar_arrive_expect_tx(&bars[B_FULL + s], (uint32_t)(2 * kh + vh) * 8192u);
@@ -131,98 +169,121 @@ __device__ void load_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint
 }
 
 // ------------------------------------------------------------------ MMAs (one thread)
-__device__ __forceinline__ void issue_d(uint32_t tbase, uint32_t st, int kh, uint64_t* bar) {
-  const uint32_t id = idesc_bf16(128, 64, false, false);
-  for (int ks = 0; ks < 4 * kh; ++ks) {
-    const uint32_t at = st + (ks >> 2) * 16384 + (ks & 3) * 32;
-    mma_bf16(tbase + COL_D, sdesc_sw128(at, 16, 1024), sdesc_sw128(at + 8192, 16, 1024), id, ks > 0);
+// `steps` MMAs of 16 K elements each; the descriptors advance by whole tiles' rows (units of 16
+// bytes), and by `skip` more after every fourth (the second 64-element half of a K-major tile).
+// The loops stay rolled: this code runs once a chunk between fifteen other warps' and is fetched
+// anew each time, so what it costs is its length.
+__device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int steps,
+                                      uint32_t step_a, uint32_t step_b, uint32_t skip_a, uint32_t skip_b) {
+#pragma unroll 1
+  for (int h = 0; h < steps; h += 4) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) mma_bf16(d, a + ks * step_a, b + ks * step_b, id, h + ks > 0);
+    a += skip_a;
+    b += skip_b;
   }
-  mma_commit(bar);
 }
 
 __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint32_t tbase,
                          uint64_t* bars, int terms) {
-  const int kh = (p.K + 63) >> 6, n = u.c1 - u.c0;
-  const uint32_t idU = idesc_bf16(128, 64 * kh, true, true);
-  const uint32_t idO1 = idesc_bf16(128, 64, false, false), idO2 = idesc_bf16(128, 64, true, false);
-  if (!mbar_wait(&bars[B_FULL], 0u, kWaitNs)) return false;
+  const int kh = p.K > 64 ? 2 : 1, n = u.c1 - u.c0;
+  constexpr uint32_t kS16 = kStage >> 4;
+  const uint64_t dQ = sdesc_sw128(sb, 16, 1024), dK = sdesc_sw128(sb + 8192, 16, 1024),
+                 dV = sdesc_sw128(sb + kStageV, 8192, 1024), dT = sdesc_sw128(sb + OFF_KT, 8192, 1024),
+                 dP = sdesc_sw128(sb + OFF_P, 16, 1024);
+  const uint32_t idU = kh == 2 ? idesc_bf16(128, 128, true, true) : idesc_bf16(128, 64, true, true);
+  constexpr uint32_t idO1 = idesc_bf16(128, 64, false, false), idO2 = idesc_bf16(128, 64, true, false);
+  if (!wait_bar(&bars[B_FULL], 0u)) return false;
   tc_fence_after();
-  issue_d(tbase, sb, kh, &bars[B_D]);
+  issue(tbase + COL_D, dQ, dK, idO1, 4 * kh, 2, 2, 1024, 1024);
+  mma_commit(&bars[B_D]);
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int s = i & 1;
     const uint32_t par = (uint32_t)i & 1u, par2 = (uint32_t)(i >> 1) & 1u;
-    const uint32_t st = sb + s * kStage, v = st + kStageV;
+    const uint64_t q = dQ + s * kS16, v = dV + s * kS16;
     // U^T = V^T K~
-    if (!mbar_wait(&bars[B_KT + s], par2, kWaitNs)) return false;
-    if (i > 0 && !mbar_wait(&bars[B_UFREE], par ^ 1u, kWaitNs)) return false;
+    if (!wait_bar(&bars[B_KT + s], par2)) return false;
+    if (i > 0 && !wait_bar(&bars[B_UFREE], par ^ 1u)) return false;
     tc_fence_after();
-    for (int t = 0; t < terms; ++t) {
-      const uint32_t kt = sb + OFF_KT + s * kKtBuf + t * kKtTerm;
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        mma_bf16(tbase + COL_U, sdesc_sw128(v + ks * 2048, 8192, 1024),
-                 sdesc_sw128(kt + ks * 2048, 8192, 1024), idU, t + ks > 0);
-    }
+    issue(tbase + COL_U, v, dT + s * (kKtBuf >> 4), idU, 4 * terms, 128, 128, 0, kKtTerm >> 4);
     mma_commit(&bars[B_U]);
     // O1^T = X^T Q^T
-    if (!mbar_wait(&bars[B_X], par, kWaitNs)) return false;
-    if (i >= 2 && !mbar_wait(&bars[B_OFREE + s], par2 ^ 1u, kWaitNs)) return false;
+    if (!wait_bar(&bars[B_X], par)) return false;
+    if (i >= 2 && !wait_bar(&bars[B_OFREE + s], par2 ^ 1u)) return false;
     tc_fence_after();
-    for (int ks = 0; ks < 4 * kh; ++ks)
-      mma_bf16_ta(tbase + COL_O1 + 64 * s, tbase + COL_X + 8 * ks,
-                  sdesc_sw128(st + (ks >> 2) * 16384 + (ks & 3) * 32, 16, 1024), idO1, ks > 0);
+#pragma unroll 1
+    for (int h = 0; h < kh; ++h)
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_bf16_ta(tbase + COL_O1 + 64 * s, tbase + COL_X + 32 * h + 8 * ks, q + 1024 * h + 2 * ks, idO1,
+                    h + ks > 0);
     if (i + 1 < n) mma_commit(&bars[B_XFREE]);
     // O2^T = V^T P^T
-    if (!mbar_wait(&bars[B_P], par, kWaitNs)) return false;
+    if (!wait_bar(&bars[B_P], par)) return false;
     tc_fence_after();
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks)
-      mma_bf16(tbase + COL_O2 + 64 * s, sdesc_sw128(v + ks * 2048, 8192, 1024),
-               sdesc_sw128(sb + OFF_P + s * 8192 + ks * 32, 16, 1024), idO2, ks > 0);
+    issue(tbase + COL_O2 + 64 * s, v, dP, idO2, 4, 128, 2, 0, 0);
     if (i + 2 < n) mma_commit(&bars[B_EMPTY + s]);
     mma_commit(&bars[B_O + s]);
     if (i + 1 < n) {
       const int s1 = s ^ 1;
-      if (!mbar_wait(&bars[B_FULL + s1], (uint32_t)((i + 1) >> 1) & 1u, kWaitNs)) return false;
+      if (!wait_bar(&bars[B_FULL + s1], (uint32_t)((i + 1) >> 1) & 1u)) return false;
       tc_fence_after();
-      issue_d(tbase, sb + s1 * kStage, kh, &bars[B_D]);
+      issue(tbase + COL_D, dQ + s1 * kS16, dK + s1 * kS16, idO1, 4 * kh, 2, 2, 1024, 1024);
+      mma_commit(&bars[B_D]);
     }
   }
   return true;
 }
 
 // ------------------------------------------------------------------ P (warps 12, 13)
+// The factor of P_ij depends on j - i alone: f[x] for x = j - i + 63 in 0 .. 126, zero where the
+// mask is.  Row i reads f[63 - i ..], four at a time: four copies shifted by one float each keep
+// those reads 16-byte aligned whatever i is, and their stride of 8 banks keeps them apart.
+__device__ __forceinline__ void fill_p_table(const LinAttnPass& p, float ld, float* wp, int tid) {
+  for (int e = tid; e < 4 * (int)kWpStride; e += kThreads) {
+    const int copy = e / (int)kWpStride, x = e - copy * (int)kWpStride + copy;   // copy[y] = f[y + copy]
+    const int dist = p.reverse ? x - 63 : 63 - x;
+    wp[e] = (dist >= 0 && dist < kChunk) ? p.s_in * p.s_out * decay_pow(ld, (float)dist) : 0.f;
+  }
+}
+
 __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase,
                        uint64_t* bars) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 1, row = 32 * wq + lane;
   const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
-  const float* w = reinterpret_cast<const float*>(sm + OFF_W);
+  const int shift = (63 - row) & 3;
+  const float4* f4 = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm + OFF_WP) +
+                                                     shift * kWpStride + (63 - row - shift));
+#pragma unroll 1
   for (int c = u.c0; c < u.c1; ++c) {
-    const int i = c - u.c0, s = i & 1;
+    const int i = c - u.c0;
     const int L = chunk_at(p, u, c).L;
-    if (i >= 2 && !wait_warp(&bars[B_O + s], (uint32_t)((i - 2) >> 1) & 1u)) return false;
+    // (D of a chunk is issued after O2 of the one before, so P has been read when it is complete)
     if (!wait_warp(&bars[B_D], (uint32_t)i & 1u)) return false;
     tc_fence_after();
-    // entries j with 0 <= sign (row - j), both inside the chunk
-    const int j_lo = p.reverse ? row : 0, j_hi = row >= L ? -1 : (p.reverse ? L - 1 : row);
-#pragma unroll
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       float x[32];
       tmem_ld32(tbase + lane_off + COL_D + 32 * half, x);
+      if (L < kChunk) {   // rows and columns past the end may hold anything
 #pragma unroll
-      for (int jj = 0; jj < 32; ++jj) {
-        const int j = 32 * half + jj;
-        const float f = p.s_in * w[abs(row - j)];
-        x[jj] = (j >= j_lo && j <= j_hi) ? f * x[jj] : 0.f;
+        for (int jj = 0; jj < 32; ++jj)
+          if (row >= L || 32 * half + jj >= L) x[jj] = 0.f;
       }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
+        const float4 a = f4[8 * half + 2 * g], b = f4[8 * half + 2 * g + 1];
         uint4 q;
-        q.x = pack2(x[8 * g], x[8 * g + 1]);
-        q.y = pack2(x[8 * g + 2], x[8 * g + 3]);
-        q.z = pack2(x[8 * g + 4], x[8 * g + 5]);
-        q.w = pack2(x[8 * g + 6], x[8 * g + 7]);
-        *reinterpret_cast<uint4*>(sm + OFF_P + s * 8192 + sw128_offset(row, 32 * half + 8 * g)) = q;
+        float2 t = mul2v(make_float2(a.x, a.y), make_float2(x[8 * g], x[8 * g + 1]));
+        q.x = pack2(t.x, t.y);
+        t = mul2v(make_float2(a.z, a.w), make_float2(x[8 * g + 2], x[8 * g + 3]));
+        q.y = pack2(t.x, t.y);
+        t = mul2v(make_float2(b.x, b.y), make_float2(x[8 * g + 4], x[8 * g + 5]));
+        q.z = pack2(t.x, t.y);
+        t = mul2v(make_float2(b.z, b.w), make_float2(x[8 * g + 6], x[8 * g + 7]));
+        q.w = pack2(t.x, t.y);
+        *reinterpret_cast<uint4*>(sm + OFF_P + sw128_offset(row, 32 * half + 8 * g)) = q;
       }
     }
     tc_fence_before();
@@ -234,40 +295,40 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
 
 // ------------------------------------------------------------------ state (warps 0-7)
 // K~ of one chunk: each 16-byte piece of a K row scaled by its token's weight and split into
-// `terms` bf16 tiles.  Rows past the chunk's end become zero, and so do V's (they belong to
-// another sequence, or to none, and a NaN there must not meet the zero).
-__device__ __forceinline__ void make_kt(const LinAttnPass& p, uint8_t* sm, int s, int L, int terms,
-                                        int kh, int tid) {
+// bf16 tiles by truncation: three 8-bit pieces hold all 24 bits; with two, the second is rounded.
+// Rows past the chunk's end become zero, and so do V's (they belong to another sequence, or to
+// none, and a NaN there must not meet the zero).
+template <int kTerms>
+__device__ __forceinline__ void make_kt(const LinAttnPass& p, uint8_t* sm, int s, int L, int kh, int tid) {
   const float* w = reinterpret_cast<const float*>(sm + OFF_W);
   uint8_t* st = sm + s * kStage;
   uint8_t* kt = sm + OFF_KT + s * kKtBuf;
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int e = tid + 256 * m, half = e >> 9, t = (e >> 3) & 63;
-    if (half >= kh) break;
+#pragma unroll 2
+  for (int e = tid; e < 512 * kh; e += 256) {
+    const int half = e >> 9, t = (e >> 3) & 63;
     const uint32_t at = (uint32_t)(t * 128 + (e & 7) * 16);
-    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a, d = a;
+    uint32_t o[3][4] = {};
     if (t < L) {
       const uint4 k4 = *reinterpret_cast<const uint4*>(st + half * 16384 + 8192 + at);
       const float f = p.s_in * w[p.reverse ? t + 1 : L - 1 - t];
       const uint32_t in[4] = {k4.x, k4.y, k4.z, k4.w};
-      uint32_t o0[4], o1[4], o2[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float x = f * lo_f(in[j]), y = f * hi_f(in[j]);
-        o0[j] = pack2(x, y);
-        x -= lo_f(o0[j]); y -= hi_f(o0[j]);
-        o1[j] = pack2(x, y);
-        x -= lo_f(o1[j]); y -= hi_f(o1[j]);
-        o2[j] = pack2(x, y);
+        float2 x = mul2v(make_float2(f, f), make_float2(lo_f(in[j]), hi_f(in[j])));
+        o[0][j] = top2(x);
+        x = rest2(x);
+        if (kTerms == 3) {
+          o[1][j] = top2(x);
+          o[2][j] = top2(rest2(x));
+        } else {
+          o[1][j] = pack2(x.x, x.y);
+        }
       }
-      a = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-      b = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-      d = make_uint4(o2[0], o2[1], o2[2], o2[3]);
     }
-    *reinterpret_cast<uint4*>(kt + half * 8192 + at) = a;
-    *reinterpret_cast<uint4*>(kt + kKtTerm + half * 8192 + at) = b;
-    if (terms == 3) *reinterpret_cast<uint4*>(kt + 2 * kKtTerm + half * 8192 + at) = d;
+#pragma unroll
+    for (int m = 0; m < kTerms; ++m)
+      *reinterpret_cast<uint4*>(kt + m * kKtTerm + half * 8192 + at) =
+          make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
   }
   if (L < kChunk) {
     for (int e = tid; e < 1024; e += 256) {
@@ -279,38 +340,41 @@ __device__ __forceinline__ void make_kt(const LinAttnPass& p, uint8_t* sm, int s
   }
 }
 
+template <int kTerms>
 __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase,
-                           uint64_t* bars, int terms) {
+                           uint64_t* bars) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int dv = 32 * (warp & 3) + lane, dk0 = 64 * (warp >> 2);   // this thread's 64 elements
   const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
   const int kh = (p.K + 63) >> 6, n = u.c1 - u.c0;
   const bool mine = dk0 < 64 * kh;
   const float2* g = reinterpret_cast<const float2*>(sm + OFF_G);
-  float X[64];
-#pragma unroll
-  for (int j = 0; j < 64; ++j) {
+  float2 X[32];
+  auto at = [&](int j) -> float {
     const int k = dk0 + j;
-    X[j] = (u.init && dv < p.V && k < p.K)
+    return (u.init && dv < p.V && k < p.K)
                ? u.init[p.initial_t ? (size_t)dv * p.K + k : (size_t)k * p.V + dv] : 0.f;
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < 32; ++j) X[j] = make_float2(at(2 * j), at(2 * j + 1));
   // the X operand of the next O1
   auto put_x = [&]() {
     if (mine) {
       float r[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(pack2(X[2 * j], X[2 * j + 1]));
+      for (int j = 0; j < 32; ++j) r[j] = __uint_as_float(pack2(X[j].x, X[j].y));
       tmem_st32(tbase + lane_off + COL_X + (dk0 >> 1), r);
     }
     tc_fence_before();
     warp_arrive(&bars[B_X], lane);
   };
   put_x();
+#pragma unroll 1
   for (int i = -1; i < n; ++i) {
     if (i + 1 < n) {   // K~ of the next chunk, while the MMAs of this one run
       const int s = (i + 1) & 1;
       if (!wait_warp(&bars[B_FULL + s], (uint32_t)((i + 1) >> 1) & 1u)) return false;
-      make_kt(p, sm, s, chunk_at(p, u, u.c0 + i + 1).L, terms, kh, tid);
+      make_kt<kTerms>(p, sm, s, chunk_at(p, u, u.c0 + i + 1).L, kh, tid);
       fence_proxy_async_smem();
       warp_arrive(&bars[B_KT + s], lane);
     }
@@ -318,13 +382,17 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     const float2 gl = g[chunk_at(p, u, u.c0 + i).L < kChunk];
     if (!wait_warp(&bars[B_U], (uint32_t)i & 1u)) return false;
     tc_fence_after();
-    if (mine) {
+    if (mine) {   // X <- X (hi + lo) + U
+      const float2 hi = make_float2(gl.x, gl.x), lo = make_float2(gl.y, gl.y);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         float x[32];
         tmem_ld32(tbase + lane_off + COL_U + dk0 + 32 * half, x);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) X[32 * half + j] = mul2(X[32 * half + j], gl) + x[j];
+        for (int j = 0; j < 16; ++j) {
+          float2& a = X[16 * half + j];
+          a = fma2(a, hi, fma2(a, lo, make_float2(x[2 * j], x[2 * j + 1])));
+        }
       }
     }
     tc_fence_before();
@@ -338,7 +406,8 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
   if (u.fin) {
 #pragma unroll
     for (int j = 0; j < 64; ++j)
-      if (dv < p.V && dk0 + j < p.K) u.fin[(size_t)(dk0 + j) * p.V + dv] = X[j];
+      if (dv < p.V && dk0 + j < p.K)
+        u.fin[(size_t)(dk0 + j) * p.V + dv] = (j & 1) ? X[j >> 1].y : X[j >> 1].x;
   }
   return true;
 }
@@ -356,7 +425,7 @@ __device__ __noinline__ void store_rows(const LinAttnPass& p, const float* w, co
       const int t = 32 * half + jj;
       if (t < ch.L && dv < p.V)
         store_elem(p.o, ((size_t)(ch.t0 + t) * p.H + h) * p.V + dv,
-                   p.s_out * fmaf(w[p.reverse ? ch.L - 1 - t : t + 1], x[jj], y[jj]),
+                   fmaf(p.s_out * w[p.reverse ? ch.L - 1 - t : t + 1], x[jj], y[jj]),
                    p.o_f32 ? GDN_F32 : GDN_BF16);
     }
   }
@@ -369,6 +438,7 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
   const float* w = reinterpret_cast<const float*>(sm + OFF_W);
   const bool leader = tid == 0;
   bool ok = true;
+#pragma unroll 1
   for (int c = u.c0; c < u.c1; ++c) {
     const int i = c - u.c0, s = i & 1;
     const ChunkAt ch = chunk_at(p, u, c);
@@ -406,15 +476,17 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int t = 32 * pass + 8 * j + 2 * (lane & 3);
-        const float w0 = w[p.reverse ? 63 - t : t + 1], w1 = w[p.reverse ? 62 - t : t + 2];
+        const float2 wt = make_float2(p.s_out * w[p.reverse ? 63 - t : t + 1],
+                                      p.s_out * w[p.reverse ? 62 - t : t + 2]);
         uint32_t f[4];
 #pragma unroll
         for (int mm = 0; mm < 4; ++mm) {
           const uint32_t* x = (mm >> 1) ? a1 : a0;
           const uint32_t* y = (mm >> 1) ? b1 : b0;
           const int e = 4 * j + 2 * (mm & 1);
-          f[mm] = pack2(p.s_out * fmaf(w0, __uint_as_float(x[e]), __uint_as_float(y[e])),
-                        p.s_out * fmaf(w1, __uint_as_float(x[e + 1]), __uint_as_float(y[e + 1])));
+          const float2 o = fma2(wt, make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
+          f[mm] = pack2(o.x, o.y);
         }
         stmatrix_x4_trans(st_base + (4 * pass + j) * 1024, f);
       }
@@ -468,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const float ld = clamp_log_decay(p.log_decay[u.h]);
   if (tid <= kChunk) reinterpret_cast<float*>(sm + OFF_W)[tid] = decay_pow(ld, (float)tid);
+  fill_p_table(p, ld, reinterpret_cast<float*>(sm + OFF_WP), tid);
   if (tid >= 128 && tid < 192 && lane == 0) {
     const int L = warp == 4 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
     reinterpret_cast<float2*>(sm + OFF_G)[warp - 4] = decay_pow2(ld, L);
@@ -494,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   bool ok = true;
   if (warp < kStateWarps) {
-    ok = state_role(p, u, sm, tbase, bars, terms);
+    ok = terms == 3 ? state_role<3>(p, u, sm, tbase, bars) : state_role<2>(p, u, sm, tbase, bars);
   } else if (warp < kStateWarps + kOutWarps) {
     ok = out_role(p, u, sm, tbase, bars, &tmO);
   } else if (warp < kMmaWarp) {
