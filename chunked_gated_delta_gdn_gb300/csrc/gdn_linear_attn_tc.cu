@@ -2,28 +2,32 @@
 // the tcgen05 tensor cores: bf16 I/O, any accepted head dims (padded to 64 or 128 by the TMA
 // loads' zero fill).
 //
-// One CTA per (sequence, head, segment), chunks of 64 tokens in order.  Per chunk, with X the
-// K x V state entering it and w_d = gamma^d (forward in time; the reverse pass mirrors the
-// exponents, see gdn_linear_attn.h):
+// One CTA per (sequence, head), chunks of 64 tokens in order.  Per chunk, with X the K x V state
+// entering it and w_d = gamma^d (forward in time; the reverse pass mirrors the exponents, see
+// gdn_linear_attn.h):
 //
 //   D    = [Q; K] K^T                      M=128 N=64  (rows 0-63 are Q K^T)
 //   P_ij = s_in s_out w_{i-j} D_ij, j <= i bf16, shared memory
 //   O1^T = X^T Q^T                         M=128 (value features) N=64 (tokens)
 //   O2^T = V^T P^T                         M=128 N=64
 //   o_i  = s_out w_{i+1} O1_i + O2_i
-//   U^T  = V^T K~, K~_j = s_in w_{L-1-j} k_j     M=128 N=K
+//   U^T  = V~^T K, V~_j = s_in w_{L-1-j} v_j     M=128 N=K
 //   X   <- w_L X + U
 //
 // The running state lives in fp32 registers of the state warps (value feature = TMEM lane, key
 // feature = column), so a chunk's only serial work on it is one multiply-add per element; the
-// tensor cores see it as the bf16 A operand of O1, read from TMEM.  V is the exact input; K~ is
-// not representable in bf16, so it is split into a sum of bf16 terms: two (error 2^-18, far
+// tensor cores see it as the bf16 A operand of O1, read from TMEM.  K is the exact input; V~ is
+// not representable in bf16, so it is split into a sum of bf16 terms: two (error 2^-17, far
 // below the bf16 outputs) where only outputs leave, three (24 bits, all of fp32) where the state
-// does.  P and the X operand are rounded to bf16 once, like the output itself.
+// does.  The terms go to TMEM as the A operand of U, which leaves the shared memory to four
+// stages of Q, K, V in flight (scaled K tiles in shared memory left room for two, and a chunk
+// took 4050 cycles: a stage's life is a memory latency of 2300 plus its way through the roles).
+// P and the X operand are rounded to bf16 once, like the output itself.
 //
-// Roles: warps 0-7 state (K~ of chunk c + 1, then the update of chunk c), warps 8-11 output,
-// warps 12-13 P, warp 14 issues the MMAs, warp 15 the loads.  They meet through mbarriers; every
-// wait is bounded: a timeout sets GDN_DEV_TIMEOUT, every role leaves, TMEM is freed.
+// Roles: warps 0-7 state (V~ of a chunk while U of the one before runs, then the update), warps
+// 8-11 output, warps 12-13 P, warp 14 issues the MMAs, warp 15 the loads.  They meet through
+// mbarriers; every wait is bounded: a timeout sets GDN_DEV_TIMEOUT, every role leaves, TMEM is
+// freed.
 #include <cuda.h>
 
 #include <atomic>
@@ -40,18 +44,18 @@ using namespace sm100;
 
 constexpr int kThreads = 512;
 constexpr int kStateWarps = 8, kOutWarps = 4, kPWarps = 2;
-constexpr int kMmaWarp = 14, kLoadWarp = 15;
+constexpr int kMmaWarp = 14;   // (warp 15 loads)
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Shared memory (bytes from a 1024-byte-aligned base).
+constexpr int kStages = 4;
 constexpr uint32_t kStage = 49152;                 // [k half][Q 64 rows | K 64 rows][128 B], V
 constexpr uint32_t kStageV = 32768;                // [v half][64 tokens][128 B]
-constexpr uint32_t OFF_KT = 2 * kStage;            // 2 buffers x 3 terms of K~, tiles as K's
-constexpr uint32_t kKtTerm = 16384, kKtBuf = 3 * kKtTerm;
-constexpr uint32_t OFF_P = OFF_KT + 2 * kKtBuf;    // [64 i][64 j] bf16
-constexpr uint32_t OFF_O = OFF_P + 8192;       // output tile, [v half][64 tokens][128 B]
+constexpr uint32_t OFF_P = kStages * kStage;       // [64 i][64 j] bf16
+constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 tokens][128 B]
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
-constexpr uint32_t OFF_WP = OFF_W + 288;           // factors of P, see fill_p_table
+constexpr uint32_t OFF_F = OFF_W + 288;            // float[64]: the weights of V~ in a full chunk
+constexpr uint32_t OFF_WP = OFF_F + 256;           // factors of P, see fill_p_table
 constexpr uint32_t kWpStride = 136;                // floats of one copy
 constexpr uint32_t OFF_G = OFF_WP + 4 * 4 * kWpStride;   // float2[2]: decay of a full / the partial chunk
 constexpr uint32_t OFF_BAR = OFF_G + 32;
@@ -60,24 +64,29 @@ constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;   // slack for aligning the ba
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 // TMEM columns.
-constexpr uint32_t COL_U = 0, COL_D = 128, COL_X = 192, COL_O1 = 256 /* 2 x 64 */,
-                   COL_O2 = 384 /* 2 x 64 */, TMEM_COLS = 512;
+constexpr uint32_t COL_U = 0, COL_D = 128, COL_X = 192, COL_O1 = 256, COL_O2 = 320,
+                   COL_VT = 384 /* 2 buffers x 2 terms x 32, or 3 terms x 32 */, TMEM_COLS = 512;
 
 enum {
-  B_FULL = 0,     // [2] stage landed
-  B_EMPTY = 2,    // [2] stage free (MMA commit)
-  B_KT = 4,       // [2] K~ written (state warps)
-  B_U = 6,        // U of a chunk complete (commit)
-  B_UFREE = 7,    // U read (state warps)
-  B_X = 8,        // X operand written (state warps)
-  B_XFREE = 9,    // O1 complete (commit): X operand read
-  B_D = 10,       // D complete (commit)
-  B_P = 11,       // P written, D read (P warps)
-  B_O = 12,       // [2] O1, O2 complete (commit)
-  B_OFREE = 14,   // [2] O1, O2 read (output warps)
-  B_COUNT = 16
+  B_FULL = 0,     // [4] stage landed
+  B_EMPTY = 4,    // [4] stage free (MMA commit)
+  B_VT = 8,       // [2] V~ written (state warps)
+  B_U = 10,       // U of a chunk complete (commit): V~ read too
+  B_UFREE = 11,   // U read (state warps)
+  B_X = 12,       // X operand written (state warps)
+  B_XFREE = 13,   // O1 complete (commit): X operand read
+  B_D = 14,       // D complete (commit)
+  B_P = 15,       // P written, D read (P warps)
+  B_O = 16,       // O1, O2 complete (commit)
+  B_OFREE = 17,   // O1, O2 read (output warps)
+  B_COUNT = 18
 };
 constexpr uint32_t OFF_FLAG = OFF_BAR + 8 * B_COUNT, OFF_TSLOT = OFF_FLAG + 8;
+
+// The columns of V~ of chunk i: two terms have two buffers, three have one.
+__device__ __forceinline__ uint32_t vt_col(int i, int terms) {
+  return COL_VT + (terms == 2 ? 64u * (i & 1) : 0u);
+}
 
 struct Unit {
   int h, bos, eos;       // the sequence
@@ -86,15 +95,18 @@ struct Unit {
   float* fin;
 };
 
-// A bounded wait that reads the clock only now and then (the failing polls of fifteen warps
-// share the issue slots with the work they wait for).
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+// A bounded wait; the slow path is out of line and reads the clock only now and then (the code of
+// sixteen warps in five roles has to fit the instruction caches, and failing polls share the
+// issue slots with the work they wait for).
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitNs) return false;
   }
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity);
 }
 // Every lane of the warp waits; the answer is the same for all of them.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
@@ -154,8 +166,8 @@ __device__ void load_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint
   const int hq = u.h / (p.H / p.Hq), hk = u.h / (p.H / p.Hk), hv = u.h / (p.H / p.Hv);
   const int kh = (p.K + 63) >> 6, vh = (p.V + 63) >> 6;
   for (int c = u.c0; c < u.c1; ++c) {
-    const int i = c - u.c0, s = i & 1;
-    if (i >= 2 && !wait_bar(&bars[B_EMPTY + s], (uint32_t)((i - 2) >> 1) & 1u)) return;
+    const int i = c - u.c0, s = i % kStages;
+    if (i >= kStages && !wait_bar(&bars[B_EMPTY + s], (uint32_t)(i / kStages - 1) & 1u)) return;
     const int t0 = chunk_at(p, u, c).t0;
     uint8_t* st = sm + s * kStage;
     mbar_arrive_expect_tx(&bars[B_FULL + s], (uint32_t)(2 * kh + vh) * 8192u);
@@ -168,20 +180,26 @@ __device__ void load_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint
   }
 }
 
-// ------------------------------------------------------------------ MMAs (one thread)
-// `steps` MMAs of 16 K elements each; the descriptors advance by whole tiles' rows (units of 16
-// bytes), and by `skip` more after every fourth (the second 64-element half of a K-major tile).
-// The loops stay rolled: this code runs once a chunk between fifteen other warps' and is fetched
-// anew each time, so what it costs is its length.
-__device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int steps,
-                                      uint32_t step_a, uint32_t step_b, uint32_t skip_a, uint32_t skip_b) {
-#pragma unroll 1
-  for (int h = 0; h < steps; h += 4) {
+// ------------------------------------------------------------------ MMAs (one warp)
+// Four MMAs (64 K elements) with A and B in shared memory; step_*: descriptor units (16 bytes)
+// from one to the next.  The whole warp walks the loops and one elected lane issues.
+__device__ __forceinline__ void issue4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t step_a,
+                                       uint32_t step_b, uint32_t acc) {
+  if (elect_one()) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) mma_bf16(d, a + ks * step_a, b + ks * step_b, id, h + ks > 0);
-    a += skip_a;
-    b += skip_b;
+    for (int ks = 0; ks < 4; ++ks) mma_bf16(d, a + ks * step_a, b + ks * step_b, id, ks > 0 ? 1u : acc);
   }
+}
+// The same with A in TMEM (eight columns an MMA).
+__device__ __forceinline__ void issue4_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t step_b,
+                                          uint32_t acc) {
+  if (elect_one()) {
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(d, a + 8 * ks, b + ks * step_b, id, ks > 0 ? 1u : acc);
+  }
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (elect_one()) mma_commit(bar);
 }
 
 __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint32_t tbase,
@@ -189,48 +207,49 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
   const int kh = p.K > 64 ? 2 : 1, n = u.c1 - u.c0;
   constexpr uint32_t kS16 = kStage >> 4;
   const uint64_t dQ = sdesc_sw128(sb, 16, 1024), dK = sdesc_sw128(sb + 8192, 16, 1024),
-                 dV = sdesc_sw128(sb + kStageV, 8192, 1024), dT = sdesc_sw128(sb + OFF_KT, 8192, 1024),
+                 dKm = sdesc_sw128(sb + 8192, 16384, 1024), dV = sdesc_sw128(sb + kStageV, 8192, 1024),
                  dP = sdesc_sw128(sb + OFF_P, 16, 1024);
-  const uint32_t idU = kh == 2 ? idesc_bf16(128, 128, true, true) : idesc_bf16(128, 64, true, true);
+  const uint32_t idU = kh == 2 ? idesc_bf16(128, 128, false, true) : idesc_bf16(128, 64, false, true);
   constexpr uint32_t idO1 = idesc_bf16(128, 64, false, false), idO2 = idesc_bf16(128, 64, true, false);
-  if (!wait_bar(&bars[B_FULL], 0u)) return false;
+  if (!wait_warp(&bars[B_FULL], 0u)) return false;
   tc_fence_after();
-  issue(tbase + COL_D, dQ, dK, idO1, 4 * kh, 2, 2, 1024, 1024);
-  mma_commit(&bars[B_D]);
+#pragma unroll 1
+  for (int h = 0; h < kh; ++h) issue4(tbase + COL_D, dQ + 1024 * h, dK + 1024 * h, idO1, 2, 2, h);
+  commit(&bars[B_D]);
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const int s = i & 1;
-    const uint32_t par = (uint32_t)i & 1u, par2 = (uint32_t)(i >> 1) & 1u;
-    const uint64_t q = dQ + s * kS16, v = dV + s * kS16;
-    // U^T = V^T K~
-    if (!wait_bar(&bars[B_KT + s], par2)) return false;
-    if (i > 0 && !wait_bar(&bars[B_UFREE], par ^ 1u)) return false;
+    const int s = i % kStages;
+    const uint32_t par = (uint32_t)i & 1u;
+    // U^T = V~^T K
+    if (!wait_warp(&bars[B_VT + par], (uint32_t)(i >> 1) & 1u)) return false;
+    if (i > 0 && !wait_warp(&bars[B_UFREE], par ^ 1u)) return false;
     tc_fence_after();
-    issue(tbase + COL_U, v, dT + s * (kKtBuf >> 4), idU, 4 * terms, 128, 128, 0, kKtTerm >> 4);
-    mma_commit(&bars[B_U]);
+#pragma unroll 1
+    for (int t = 0; t < terms; ++t)
+      issue4_ta(tbase + COL_U, tbase + vt_col(i, terms) + 32 * t, dKm + s * kS16, idU, 128, t);
+    commit(&bars[B_U]);
     // O1^T = X^T Q^T
-    if (!wait_bar(&bars[B_X], par)) return false;
-    if (i >= 2 && !wait_bar(&bars[B_OFREE + s], par2 ^ 1u)) return false;
+    if (!wait_warp(&bars[B_X], par)) return false;
+    if (i > 0 && !wait_warp(&bars[B_OFREE], par ^ 1u)) return false;
     tc_fence_after();
 #pragma unroll 1
     for (int h = 0; h < kh; ++h)
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        mma_bf16_ta(tbase + COL_O1 + 64 * s, tbase + COL_X + 32 * h + 8 * ks, q + 1024 * h + 2 * ks, idO1,
-                    h + ks > 0);
-    if (i + 1 < n) mma_commit(&bars[B_XFREE]);
+      issue4_ta(tbase + COL_O1, tbase + COL_X + 32 * h, dQ + s * kS16 + 1024 * h, idO1, 2, h);
+    if (i + 1 < n) commit(&bars[B_XFREE]);
     // O2^T = V^T P^T
-    if (!wait_bar(&bars[B_P], par)) return false;
+    if (!wait_warp(&bars[B_P], par)) return false;
     tc_fence_after();
-    issue(tbase + COL_O2 + 64 * s, v, dP, idO2, 4, 128, 2, 0, 0);
-    if (i + 2 < n) mma_commit(&bars[B_EMPTY + s]);
-    mma_commit(&bars[B_O + s]);
+    issue4(tbase + COL_O2, dV + s * kS16, dP, idO2, 128, 2, 0);
+    if (i + kStages < n) commit(&bars[B_EMPTY + s]);
+    commit(&bars[B_O]);
     if (i + 1 < n) {
-      const int s1 = s ^ 1;
-      if (!wait_bar(&bars[B_FULL + s1], (uint32_t)((i + 1) >> 1) & 1u)) return false;
+      const int s1 = (i + 1) % kStages;
+      if (!wait_warp(&bars[B_FULL + s1], (uint32_t)((i + 1) / kStages) & 1u)) return false;
       tc_fence_after();
-      issue(tbase + COL_D, dQ + s1 * kS16, dK + s1 * kS16, idO1, 4 * kh, 2, 2, 1024, 1024);
-      mma_commit(&bars[B_D]);
+#pragma unroll 1
+      for (int h = 0; h < kh; ++h)
+        issue4(tbase + COL_D, dQ + s1 * kS16 + 1024 * h, dK + s1 * kS16 + 1024 * h, idO1, 2, 2, h);
+      commit(&bars[B_D]);
     }
   }
   return true;
@@ -294,60 +313,80 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
 }
 
 // ------------------------------------------------------------------ state (warps 0-7)
-// K~ of one chunk: each 16-byte piece of a K row scaled by its token's weight and split into
-// bf16 tiles by truncation: three 8-bit pieces hold all 24 bits; with two, the second is rounded.
-// Rows past the chunk's end become zero, and so do V's (they belong to another sequence, or to
-// none, and a NaN there must not meet the zero).
+// Rows L .. 63 of a stage's K and V become zero: they belong to another sequence, or to none, and
+// a NaN there must not meet the zero weights.  Each state warp clears the 16 V columns that it
+// reads itself and every eighth row of K.
+__device__ __noinline__ void clear_rows(uint8_t* st, int L, int vt0, int warp, int lane) {
+  uint8_t* v = st + kStageV + (vt0 >> 6) * 8192;
+  for (int e = lane; e < 128; e += 32) {
+    const int t = e >> 1;
+    if (t >= L)
+      *reinterpret_cast<uint4*>(v + t * 128 + (((((vt0 & 63) >> 3) + (e & 1)) ^ (t & 7)) << 4)) =
+          make_uint4(0u, 0u, 0u, 0u);
+  }
+  for (int e = lane; e < 128; e += 32) {
+    const int t = 8 * (e >> 4) + warp;
+    if (t >= L)
+      *reinterpret_cast<uint4*>(st + 8192 + ((e >> 3) & 1) * 16384 + t * 128 + (e & 7) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// This warp's 16 value features of V~^T as TMEM fragments.  Fragment register 4 g + r of thread t
+// holds features t/4 (r < 2) or t/4 + 8 and TMEM column 8 g + 2 (t%4) + (r & 1), that is tokens
+// 16 g + 4 (t%4) + 2 (r & 1) and the next; ldmatrix .trans delivers exactly that when its row
+// addresses name the tokens 0, 1, 4, 5, 8, 9, 12, 13 (r even) or 2, 3, 6, .. (odd).  Each value
+// is scaled and split by truncation: three 8-bit pieces hold all 24 bits; with two, the second is
+// rounded.
 template <int kTerms>
-__device__ __forceinline__ void make_kt(const LinAttnPass& p, uint8_t* sm, int s, int L, int kh, int tid) {
+__device__ __forceinline__ void make_vt(const LinAttnPass& p, const uint8_t* sm, uint32_t v_tile, int d0,
+                                        int L, int lane, uint32_t dst) {
   const float* w = reinterpret_cast<const float*>(sm + OFF_W);
-  uint8_t* st = sm + s * kStage;
-  uint8_t* kt = sm + OFF_KT + s * kKtBuf;
-#pragma unroll 2
-  for (int e = tid; e < 512 * kh; e += 256) {
-    const int half = e >> 9, t = (e >> 3) & 63;
-    const uint32_t at = (uint32_t)(t * 128 + (e & 7) * 16);
-    uint32_t o[3][4] = {};
-    if (t < L) {
-      const uint4 k4 = *reinterpret_cast<const uint4*>(st + half * 16384 + 8192 + at);
-      const float f = p.s_in * w[p.reverse ? t + 1 : L - 1 - t];
-      const uint32_t in[4] = {k4.x, k4.y, k4.z, k4.w};
+  const float4* f4 = reinterpret_cast<const float4*>(sm + OFF_F) + (lane & 3);
+  const int r = lane >> 3, j = lane & 7;              // matrix (register) this lane addresses, row
+  const int tok0 = 4 * (j >> 1) + 2 * (r & 1) + (j & 1), d = d0 + 8 * (r >> 1);
+  const uint32_t tile = v_tile + (d >> 6) * 8192 + (uint32_t)tok0 * 128u + ((((d & 63) >> 3) ^ (tok0 & 7)) << 4);
+#pragma unroll 1
+  for (int g = 0; g < 4; ++g) {
+    uint32_t x[4], o[kTerms][4];
+    ldmatrix_x4_trans(tile + g * 2048, x);
+    float4 f = f4[4 * g];
+    if (L < kChunk && !p.reverse) {
+      const int t = L - 1 - 16 * g - 4 * (lane & 3);
+      f = make_float4(p.s_in * w[max(t, 0)], p.s_in * w[max(t - 1, 0)], p.s_in * w[max(t - 2, 0)],
+                      p.s_in * w[max(t - 3, 0)]);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 x = mul2v(make_float2(f, f), make_float2(lo_f(in[j]), hi_f(in[j])));
-        o[0][j] = top2(x);
-        x = rest2(x);
-        if (kTerms == 3) {
-          o[1][j] = top2(x);
-          o[2][j] = top2(rest2(x));
-        } else {
-          o[1][j] = pack2(x.x, x.y);
-        }
+    for (int m = 0; m < 4; ++m) {
+      float2 y = mul2v((m & 1) ? make_float2(f.z, f.w) : make_float2(f.x, f.y),
+                       make_float2(lo_f(x[m]), hi_f(x[m])));
+      o[0][m] = top2(y);
+      y = rest2(y);
+      if (kTerms == 3) {
+        o[1][m] = top2(y);
+        o[kTerms - 1][m] = top2(rest2(y));
+      } else {
+        o[1][m] = pack2(y.x, y.y);
       }
     }
 #pragma unroll
-    for (int m = 0; m < kTerms; ++m)
-      *reinterpret_cast<uint4*>(kt + m * kKtTerm + half * 8192 + at) =
-          make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
+    for (int t = 0; t < kTerms; ++t) tmem_st16x256b_x1(dst + 32 * t + 8 * g, o[t]);
   }
-  if (L < kChunk) {
-    for (int e = tid; e < 1024; e += 256) {
-      const int t = (e >> 3) & 63;
-      if (t >= L)
-        *reinterpret_cast<uint4*>(st + kStageV + (e >> 9) * 8192 + t * 128 + (e & 7) * 16) =
-            make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
+  tmem_wait_st();
 }
 
 template <int kTerms>
 __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase,
                            uint64_t* bars) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int dv = 32 * (warp & 3) + lane, dk0 = 64 * (warp >> 2);   // this thread's 64 elements
-  const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-  const int kh = (p.K + 63) >> 6, n = u.c1 - u.c0;
-  const bool mine = dk0 < 64 * kh;
+  const int dv = 32 * (warp & 3) + lane, dk0 = 64 * (warp >> 2);   // this thread's 64 state elements
+  const int vt0 = 32 * (warp & 3) + 16 * (warp >> 2);              // this warp's 16 rows of V~^T
+  const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16, vt_off = (uint32_t)vt0 << 16;
+  const uint32_t sb = smem_u32(sm);
+  const int n = u.c1 - u.c0;
+  const bool mine = dk0 < p.K, mine_v = vt0 < p.V;   // (features past the head dim: nothing to do)
   const float2* g = reinterpret_cast<const float2*>(sm + OFF_G);
   float2 X[32];
   auto at = [&](int j) -> float {
@@ -369,20 +408,10 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     warp_arrive(&bars[B_X], lane);
   };
   put_x();
-#pragma unroll 1
-  for (int i = -1; i < n; ++i) {
-    if (i + 1 < n) {   // K~ of the next chunk, while the MMAs of this one run
-      const int s = (i + 1) & 1;
-      if (!wait_warp(&bars[B_FULL + s], (uint32_t)((i + 1) >> 1) & 1u)) return false;
-      make_kt<kTerms>(p, sm, s, chunk_at(p, u, u.c0 + i + 1).L, kh, tid);
-      fence_proxy_async_smem();
-      warp_arrive(&bars[B_KT + s], lane);
-    }
-    if (i < 0) continue;
-    const float2 gl = g[chunk_at(p, u, u.c0 + i).L < kChunk];
-    if (!wait_warp(&bars[B_U], (uint32_t)i & 1u)) return false;
-    tc_fence_after();
-    if (mine) {   // X <- X (hi + lo) + U
+  // X <- X (hi + lo) + U of chunk i
+  auto update = [&](int i) {
+    if (mine) {
+      const float2 gl = g[chunk_at(p, u, u.c0 + i).L < kChunk];
       const float2 hi = make_float2(gl.x, gl.x), lo = make_float2(gl.y, gl.y);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -397,11 +426,37 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     }
     tc_fence_before();
     warp_arrive(&bars[B_UFREE], lane);
-    if (i + 1 < n) {
-      if (!wait_warp(&bars[B_XFREE], (uint32_t)i & 1u)) return false;
+  };
+  // With two terms V~ of chunk i is made while U of chunk i - 1 runs; with three, whose columns
+  // have no room for a second buffer, after it.
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int s = i % kStages, L = chunk_at(p, u, u.c0 + i).L;
+    if (kTerms == 3 && i > 0) {
+      if (!wait_warp(&bars[B_U], (uint32_t)(i - 1) & 1u)) return false;
       tc_fence_after();
-      put_x();
+      update(i - 1);
     }
+    if (!wait_warp(&bars[B_FULL + s], (uint32_t)(i / kStages) & 1u)) return false;
+    if (L < kChunk) clear_rows(sm + s * kStage, L, vt0, warp, lane);
+    if (mine_v)
+      make_vt<kTerms>(p, sm, sb + s * kStage + kStageV, vt0, L, lane, tbase + vt_off + vt_col(i, kTerms));
+    tc_fence_before();
+    warp_arrive(&bars[B_VT + (i & 1)], lane);
+    if (i == 0) continue;
+    if (kTerms == 2) {
+      if (!wait_warp(&bars[B_U], (uint32_t)(i - 1) & 1u)) return false;
+      tc_fence_after();
+      update(i - 1);
+    }
+    if (!wait_warp(&bars[B_XFREE], (uint32_t)(i - 1) & 1u)) return false;
+    tc_fence_after();
+    put_x();
+  }
+  if (u.fin) {
+    if (!wait_warp(&bars[B_U], (uint32_t)(n - 1) & 1u)) return false;
+    tc_fence_after();
+    update(n - 1);
   }
   if (u.fin) {
 #pragma unroll
@@ -440,11 +495,11 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
   bool ok = true;
 #pragma unroll 1
   for (int c = u.c0; c < u.c1; ++c) {
-    const int i = c - u.c0, s = i & 1;
+    const int i = c - u.c0;
     const ChunkAt ch = chunk_at(p, u, c);
-    const uint32_t o1 = tbase + lane_off + COL_O1 + 64 * s, o2 = tbase + lane_off + COL_O2 + 64 * s;
+    const uint32_t o1 = tbase + lane_off + COL_O1, o2 = tbase + lane_off + COL_O2;
     if (leader) tma_store_wait_read();   // the previous tile has left the staging
-    ok = wait_warp(&bars[B_O + s], (uint32_t)(i >> 1) & 1u);
+    ok = wait_warp(&bars[B_O], (uint32_t)i & 1u);
     if (group_sync_or(1, 32 * kOutWarps, !ok)) {
       ok = false;
       break;
@@ -453,7 +508,7 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
     if (ch.L < kChunk || p.o_f32) {
       store_rows(p, w, ch, o1, o2, u.h, 32 * wq + lane);
       tc_fence_before();
-      warp_arrive(&bars[B_OFREE + s], lane);
+      warp_arrive(&bars[B_OFREE], lane);
       continue;
     }
     // 16x256b loads give each thread value features (t/4, t/4 + 8) x tokens (2 (t%4), + 1): the
@@ -471,7 +526,7 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
       tmem_wait_ld();
       if (pass == 1) {
         tc_fence_before();
-        warp_arrive(&bars[B_OFREE + s], lane);
+        warp_arrive(&bars[B_OFREE], lane);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -540,6 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const float ld = clamp_log_decay(p.log_decay[u.h]);
   if (tid <= kChunk) reinterpret_cast<float*>(sm + OFF_W)[tid] = decay_pow(ld, (float)tid);
+  if (tid < kChunk)
+    reinterpret_cast<float*>(sm + OFF_F)[tid] =
+        p.s_in * decay_pow(ld, p.reverse ? (float)(tid + 1) : (float)(kChunk - 1 - tid));
   fill_p_table(p, ld, reinterpret_cast<float*>(sm + OFF_WP), tid);
   if (tid >= 128 && tid < 192 && lane == 0) {
     const int L = warp == 4 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
@@ -547,9 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const int count = (i == B_KT || i == B_KT + 1 || i == B_UFREE || i == B_X) ? kStateWarps
-                        : i == B_P ? kPWarps
-                        : (i == B_OFREE || i == B_OFREE + 1) ? kOutWarps : 1;
+      const int count = (i == B_VT || i == B_VT + 1 || i == B_UFREE || i == B_X) ? kStateWarps
+                        : i == B_P ? kPWarps : i == B_OFREE ? kOutWarps : 1;
       mbar_init(&bars[i], count);
     }
     *flag = 0;
@@ -573,8 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kMmaWarp) {
     ok = p_role(p, u, sm, tbase, bars);
   } else if (warp == kMmaWarp) {
-    if (lane == 0) ok = mma_role(p, u, smem_u32(sm), tbase, bars, terms);
-    __syncwarp();
+    ok = mma_role(p, u, smem_u32(sm), tbase, bars, terms);
   } else {
     if (lane == 0) load_role(p, u, sm, bars, &tmQ, &tmK, &tmV);
     __syncwarp();

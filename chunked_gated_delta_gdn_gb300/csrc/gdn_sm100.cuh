@@ -248,6 +248,12 @@ __device__ __forceinline__ void tmem_st16x256b_x4(uint32_t taddr, const uint32_t
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// One repetition: eight columns (4 registers, no wait).
+__device__ __forceinline__ void tmem_st16x256b_x1(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -315,6 +321,15 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_u32(bar))
       : "memory");
+}
+
+// True in one lane of a converged warp.  A branch on it, around instructions whose operands are
+// the same for the whole warp, lets the compiler keep those in uniform registers: MMAs issued so
+// take 48 cycles each, under a lane == 0 test 57-72 (N = 64, one GB300 SM).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
+  return p != 0;
 }
 
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D, dense.
