@@ -17,17 +17,23 @@
 // The running state lives in fp32 registers of the state warps (value feature = TMEM lane, key
 // feature = column), so a chunk's only serial work on it is one multiply-add per element; the
 // tensor cores see it as the bf16 A operand of O1, read from TMEM.  K is the exact input; V~ is
-// not representable in bf16, so it is split into a sum of bf16 terms: two (error 2^-17, far
-// below the bf16 outputs) where only outputs leave, three (24 bits, all of fp32) where the state
-// does.  The terms go to TMEM as the A operand of U, which leaves the shared memory to four
+// not representable in bf16, so it is a sum of bf16 terms, formed by packed bf16 multiply-adds
+// alone.  With the weight f = f1 + f2 + f3 in bf16 pieces (exact), h = f1 v rounded and
+// r = f1 v - h (exact: a product of two 8-bit values has 16 bits):
+//   two terms    h, r + f2 v           error 2^-17, far below the bf16 outputs: where only those leave
+//   four terms   h, r, a = f2 v rounded, (f2 v - a) + f3 v     error 2^-25, as fp32: where the
+//                                                              state leaves too
+// (three instructions for two values where scaling and splitting in fp32 took eight, and the
+// state warps, which do this, are what a chunk waits for).  The terms go to TMEM as the A operand of U, which leaves the shared memory to four
 // stages of Q, K, V in flight (scaled K tiles in shared memory left room for two, and a chunk
 // took 4050 cycles: a stage's life is a memory latency of 2300 plus its way through the roles).
 // P and the X operand are rounded to bf16 once, like the output itself.
 //
 // Roles: warps 0-7 state (V~ of a chunk while U of the one before runs, then the update), warps
-// 8-11 output, warps 12-13 P, warp 14 issues the MMAs, warp 15 the loads.  They meet through
-// mbarriers; every wait is bounded: a timeout sets GDN_DEV_TIMEOUT, every role leaves, TMEM is
-// freed.
+// 8-11 output, warps 12-13 P, warp 14 issues the MMAs, warp 15 the loads.  (Two issuing warps,
+// one for U and O1 and one for D and O2, measured slower: 1.9 us a chunk instead of 1.5.)  They
+// meet through mbarriers; every wait is bounded: a timeout sets GDN_DEV_TIMEOUT, every role
+// leaves, TMEM is freed.
 #include <cuda.h>
 
 #include <atomic>
@@ -54,8 +60,9 @@ constexpr uint32_t kStageV = 32768;                // [v half][64 tokens][128 B]
 constexpr uint32_t OFF_P = kStages * kStage;       // [64 i][64 j] bf16
 constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 tokens][128 B]
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
-constexpr uint32_t OFF_F = OFF_W + 288;            // float[64]: the weights of V~ in a full chunk
-constexpr uint32_t OFF_WP = OFF_F + 256;           // factors of P, see fill_p_table
+constexpr uint32_t OFF_F = OFF_W + 288;            // Weights4[16]: the weights of V~ in a full chunk
+constexpr uint32_t OFF_R = OFF_F + 16 * 24;           // float[64]: the factors of O1 in a full chunk
+constexpr uint32_t OFF_WP = OFF_R + 256;           // factors of P, see fill_p_table
 constexpr uint32_t kWpStride = 136;                // floats of one copy
 constexpr uint32_t OFF_G = OFF_WP + 4 * 4 * kWpStride;   // float2[2]: decay of a full / the partial chunk
 constexpr uint32_t OFF_BAR = OFF_G + 32;
@@ -65,11 +72,11 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 // TMEM columns.
 constexpr uint32_t COL_U = 0, COL_D = 128, COL_X = 192, COL_O1 = 256, COL_O2 = 320,
-                   COL_VT = 384 /* 2 buffers x 2 terms x 32, or 3 terms x 32 */, TMEM_COLS = 512;
+                   COL_VT = 384 /* 2 buffers x 2 terms x 32, or 4 terms x 32 */, TMEM_COLS = 512;
 
 enum {
   B_FULL = 0,     // [4] stage landed
-  B_EMPTY = 4,    // [4] stage free (MMA commit)
+  B_EMPTY = 4,    // [4] stage free (an output warp, once O1 and O2 are complete)
   B_VT = 8,       // [2] V~ written (state warps)
   B_U = 10,       // U of a chunk complete (commit): V~ read too
   B_UFREE = 11,   // U read (state warps)
@@ -77,13 +84,13 @@ enum {
   B_XFREE = 13,   // O1 complete (commit): X operand read
   B_D = 14,       // D complete (commit)
   B_P = 15,       // P written, D read (P warps)
-  B_O = 16,       // O1, O2 complete (commit)
+  B_O = 16,       // O1, O2 complete (commit): the chunk's stage has been read
   B_OFREE = 17,   // O1, O2 read (output warps)
   B_COUNT = 18
 };
 constexpr uint32_t OFF_FLAG = OFF_BAR + 8 * B_COUNT, OFF_TSLOT = OFF_FLAG + 8;
 
-// The columns of V~ of chunk i: two terms have two buffers, three have one.
+// The columns of V~ of chunk i: two terms have two buffers, four have one.
 __device__ __forceinline__ uint32_t vt_col(int i, int terms) {
   return COL_VT + (terms == 2 ? 64u * (i & 1) : 0u);
 }
@@ -136,19 +143,41 @@ __device__ __forceinline__ float2 mul2v(float2 a, float2 b) {
       : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
   return d;
 }
-// The upper halves of two fp32 values: both truncated to bf16, packed.
-__device__ __forceinline__ uint32_t top2(float2 x) {
-  return __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+// Packed bf16 arithmetic, each result rounded once.
+__device__ __forceinline__ uint32_t bf_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
 }
-// What that truncation leaves (exact).
-__device__ __forceinline__ float2 rest2(float2 x) {
-  const float2 t = make_float2(__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
-                               __uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
-  return fma2(t, make_float2(-1.f, -1.f), x);
+__device__ __forceinline__ uint32_t bf_mul(uint32_t a, uint32_t b) {   // (-0: keeps a product's sign)
+  return bf_fma(a, b, 0x80008000u);
 }
-__device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-
+__device__ __forceinline__ uint32_t bf_neg(uint32_t a) { return a ^ 0x80008000u; }
+// fp32 as a sum of three bf16 values (exact), as bits.
+__device__ __forceinline__ void split3(float x, uint32_t (&o)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    o[i] = __bfloat16_as_ushort(h);
+    x -= __bfloat162float(h);
+  }
+}
+// The three pieces of the weights of four consecutive tokens, two to a register.
+struct Weights4 {
+  uint32_t f[3][2];
+};
+__device__ __forceinline__ Weights4 pack_weights(const float (&x)[4]) {
+  Weights4 w;
+  uint32_t o[4][3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split3(x[i], o[i]);
+#pragma unroll
+  for (int m = 0; m < 3; ++m) {
+    w.f[m][0] = o[0][m] | (o[1][m] << 16);
+    w.f[m][1] = o[2][m] | (o[3][m] << 16);
+  }
+  return w;
+}
 struct ChunkAt {
   int t0, L;
 };
@@ -165,37 +194,46 @@ __device__ void load_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint
                           const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tv) {
   const int hq = u.h / (p.H / p.Hq), hk = u.h / (p.H / p.Hk), hv = u.h / (p.H / p.Hv);
   const int kh = (p.K + 63) >> 6, vh = (p.V + 63) >> 6;
+#pragma unroll 1
   for (int c = u.c0; c < u.c1; ++c) {
-    const int i = c - u.c0, s = i % kStages;
+    const int i = c - u.c0, s = i & (kStages - 1);
     if (i >= kStages && !wait_bar(&bars[B_EMPTY + s], (uint32_t)(i / kStages - 1) & 1u)) return;
     const int t0 = chunk_at(p, u, c).t0;
     uint8_t* st = sm + s * kStage;
     mbar_arrive_expect_tx(&bars[B_FULL + s], (uint32_t)(2 * kh + vh) * 8192u);
+#pragma unroll 1
     for (int x = 0; x < kh; ++x) {
       tma_load_3d(st + x * 16384 + 8192, tk, &bars[B_FULL + s], 64 * x, hk, t0);
       tma_load_3d(st + x * 16384, tq, &bars[B_FULL + s], 64 * x, hq, t0);
     }
+#pragma unroll 1
     for (int x = 0; x < vh; ++x)
       tma_load_3d(st + kStageV + x * 8192, tv, &bars[B_FULL + s], 64 * x, hv, t0);
   }
 }
 
 // ------------------------------------------------------------------ MMAs (one warp)
-// Four MMAs (64 K elements) with A and B in shared memory; step_*: descriptor units (16 bytes)
-// from one to the next.  The whole warp walks the loops and one elected lane issues.
-__device__ __forceinline__ void issue4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t step_a,
-                                       uint32_t step_b, uint32_t acc) {
-  if (elect_one()) {
+// 4 n MMAs (64 n K elements) with A in shared memory or TMEM and B in shared memory.  a, b
+// advance by step_* an MMA within a group of four and by skip_* from group to group (descriptor
+// units of 16 bytes, or TMEM columns).  The whole warp walks the loops and one elected lane issues.
+struct Operands {
+  uint32_t step_a, step_b, skip_a, skip_b;
+};
+template <bool kTmemA>
+__device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int n, Operands o,
+                                      uint32_t acc = 0) {
+#pragma unroll 1
+  for (int h = 0; h < n; ++h) {
+    if (elect_one()) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) mma_bf16(d, a + ks * step_a, b + ks * step_b, id, ks > 0 ? 1u : acc);
-  }
-}
-// The same with A in TMEM (eight columns an MMA).
-__device__ __forceinline__ void issue4_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t step_b,
-                                          uint32_t acc) {
-  if (elect_one()) {
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(d, a + 8 * ks, b + ks * step_b, id, ks > 0 ? 1u : acc);
+      for (int ks = 0; ks < 4; ++ks) {
+        if (kTmemA) mma_bf16_ta(d, (uint32_t)a + ks * o.step_a, b + ks * o.step_b, id, ks > 0 ? 1u : acc);
+        else mma_bf16(d, a + ks * o.step_a, b + ks * o.step_b, id, ks > 0 ? 1u : acc);
+      }
+    }
+    acc = 1;
+    a += o.skip_a;
+    b += o.skip_b;
   }
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -210,45 +248,36 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
                  dKm = sdesc_sw128(sb + 8192, 16384, 1024), dV = sdesc_sw128(sb + kStageV, 8192, 1024),
                  dP = sdesc_sw128(sb + OFF_P, 16, 1024);
   const uint32_t idU = kh == 2 ? idesc_bf16(128, 128, false, true) : idesc_bf16(128, 64, false, true);
-  constexpr uint32_t idO1 = idesc_bf16(128, 64, false, false), idO2 = idesc_bf16(128, 64, true, false);
-  if (!wait_warp(&bars[B_FULL], 0u)) return false;
-  tc_fence_after();
+  constexpr uint32_t idS = idesc_bf16(128, 64, false, false), idO2 = idesc_bf16(128, 64, true, false);
+  // chunk -1 has only the next one's D
 #pragma unroll 1
-  for (int h = 0; h < kh; ++h) issue4(tbase + COL_D, dQ + 1024 * h, dK + 1024 * h, idO1, 2, 2, h);
-  commit(&bars[B_D]);
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const int s = i % kStages;
+  for (int i = -1; i < n; ++i) {
+    const int s = i & (kStages - 1);
     const uint32_t par = (uint32_t)i & 1u;
-    // U^T = V~^T K
-    if (!wait_warp(&bars[B_VT + par], (uint32_t)(i >> 1) & 1u)) return false;
-    if (i > 0 && !wait_warp(&bars[B_UFREE], par ^ 1u)) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int t = 0; t < terms; ++t)
-      issue4_ta(tbase + COL_U, tbase + vt_col(i, terms) + 32 * t, dKm + s * kS16, idU, 128, t);
-    commit(&bars[B_U]);
-    // O1^T = X^T Q^T
-    if (!wait_warp(&bars[B_X], par)) return false;
-    if (i > 0 && !wait_warp(&bars[B_OFREE], par ^ 1u)) return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int h = 0; h < kh; ++h)
-      issue4_ta(tbase + COL_O1, tbase + COL_X + 32 * h, dQ + s * kS16 + 1024 * h, idO1, 2, h);
-    if (i + 1 < n) commit(&bars[B_XFREE]);
-    // O2^T = V^T P^T
-    if (!wait_warp(&bars[B_P], par)) return false;
-    tc_fence_after();
-    issue4(tbase + COL_O2, dV + s * kS16, dP, idO2, 128, 2, 0);
-    if (i + kStages < n) commit(&bars[B_EMPTY + s]);
-    commit(&bars[B_O]);
+    if (i >= 0) {
+      // U^T = V~^T K
+      if (!wait_warp(&bars[B_VT + par], (uint32_t)(i >> 1) & 1u)) return false;
+      if (i > 0 && !wait_warp(&bars[B_UFREE], par ^ 1u)) return false;
+      tc_fence_after();
+      issue<true>(tbase + COL_U, tbase + vt_col(i, terms), dKm + s * kS16, idU, terms, {8, 128, 32, 0});
+      commit(&bars[B_U]);
+      // O1^T = X^T Q^T
+      if (!wait_warp(&bars[B_X], par)) return false;
+      if (i > 0 && !wait_warp(&bars[B_OFREE], par ^ 1u)) return false;
+      tc_fence_after();
+      issue<true>(tbase + COL_O1, tbase + COL_X, dQ + s * kS16, idS, kh, {8, 2, 32, 1024});
+      if (i + 1 < n) commit(&bars[B_XFREE]);
+      // O2^T = V^T P^T
+      if (!wait_warp(&bars[B_P], par)) return false;
+      tc_fence_after();
+      issue<false>(tbase + COL_O2, dV + s * kS16, dP, idO2, 1, {128, 2, 0, 0});
+      commit(&bars[B_O]);
+    }
     if (i + 1 < n) {
-      const int s1 = (i + 1) % kStages;
+      const int s1 = (i + 1) & (kStages - 1);
       if (!wait_warp(&bars[B_FULL + s1], (uint32_t)((i + 1) / kStages) & 1u)) return false;
       tc_fence_after();
-#pragma unroll 1
-      for (int h = 0; h < kh; ++h)
-        issue4(tbase + COL_D, dQ + s1 * kS16 + 1024 * h, dK + s1 * kS16 + 1024 * h, idO1, 2, 2, h);
+      issue<false>(tbase + COL_D, dQ + s1 * kS16, dK + s1 * kS16, idS, kh, {2, 2, 1024, 1024});
       commit(&bars[B_D]);
     }
   }
@@ -267,6 +296,13 @@ __device__ __forceinline__ void fill_p_table(const LinAttnPass& p, float ld, flo
   }
 }
 
+// Row `row` of P from column L on: zero, whatever the rows past the chunk's end held.
+__device__ __noinline__ void clear_columns(uint8_t* tile, int row, int L) {
+#pragma unroll 1
+  for (int j = L; j < kChunk; ++j)
+    *reinterpret_cast<uint16_t*>(tile + sw128_offset(row, j)) = (uint16_t)0;
+}
+
 __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase,
                        uint64_t* bars) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 1, row = 32 * wq + lane;
@@ -278,18 +314,13 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
   for (int c = u.c0; c < u.c1; ++c) {
     const int i = c - u.c0;
     const int L = chunk_at(p, u, c).L;
-    // (D of a chunk is issued after O2 of the one before, so P has been read when it is complete)
     if (!wait_warp(&bars[B_D], (uint32_t)i & 1u)) return false;
+    // (D of a chunk is issued after O2 of the one before, so P has been read when it is complete)
     tc_fence_after();
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       float x[32];
       tmem_ld32(tbase + lane_off + COL_D + 32 * half, x);
-      if (L < kChunk) {   // rows and columns past the end may hold anything
-#pragma unroll
-        for (int jj = 0; jj < 32; ++jj)
-          if (row >= L || 32 * half + jj >= L) x[jj] = 0.f;
-      }
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const float4 a = f4[8 * half + 2 * g], b = f4[8 * half + 2 * g + 1];
@@ -305,6 +336,7 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
         *reinterpret_cast<uint4*>(sm + OFF_P + sw128_offset(row, 32 * half + 8 * g)) = q;
       }
     }
+    if (L < kChunk) clear_columns(sm + OFF_P, row, L);
     tc_fence_before();
     fence_proxy_async_smem();
     warp_arrive(&bars[B_P], lane);
@@ -334,41 +366,45 @@ __device__ __noinline__ void clear_rows(uint8_t* st, int L, int vt0, int warp, i
   __syncwarp();
 }
 
+// The weights of tokens t0 .. t0 + 3 in the partial chunk of L tokens (forward: they count back
+// from its end; the rows past it are clear, whatever their weight).
+__device__ __noinline__ Weights4 partial_weights(const float* w, float s_in, int L, int t0) {
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = s_in * w[max(L - 1 - t0 - i, 0)];
+  return pack_weights(x);
+}
+
 // This warp's 16 value features of V~^T as TMEM fragments.  Fragment register 4 g + r of thread t
 // holds features t/4 (r < 2) or t/4 + 8 and TMEM column 8 g + 2 (t%4) + (r & 1), that is tokens
 // 16 g + 4 (t%4) + 2 (r & 1) and the next; ldmatrix .trans delivers exactly that when its row
-// addresses name the tokens 0, 1, 4, 5, 8, 9, 12, 13 (r even) or 2, 3, 6, .. (odd).  Each value
-// is scaled and split by truncation: three 8-bit pieces hold all 24 bits; with two, the second is
-// rounded.
+// addresses name the tokens 0, 1, 4, 5, 8, 9, 12, 13 (r even) or 2, 3, 6, .. (odd).
 template <int kTerms>
 __device__ __forceinline__ void make_vt(const LinAttnPass& p, const uint8_t* sm, uint32_t v_tile, int d0,
                                         int L, int lane, uint32_t dst) {
-  const float* w = reinterpret_cast<const float*>(sm + OFF_W);
-  const float4* f4 = reinterpret_cast<const float4*>(sm + OFF_F) + (lane & 3);
+  const Weights4* fw = reinterpret_cast<const Weights4*>(sm + OFF_F) + (lane & 3);
   const int r = lane >> 3, j = lane & 7;              // matrix (register) this lane addresses, row
   const int tok0 = 4 * (j >> 1) + 2 * (r & 1) + (j & 1), d = d0 + 8 * (r >> 1);
   const uint32_t tile = v_tile + (d >> 6) * 8192 + (uint32_t)tok0 * 128u + ((((d & 63) >> 3) ^ (tok0 & 7)) << 4);
-#pragma unroll 1
+#pragma unroll 2
   for (int g = 0; g < 4; ++g) {
     uint32_t x[4], o[kTerms][4];
     ldmatrix_x4_trans(tile + g * 2048, x);
-    float4 f = f4[4 * g];
-    if (L < kChunk && !p.reverse) {
-      const int t = L - 1 - 16 * g - 4 * (lane & 3);
-      f = make_float4(p.s_in * w[max(t, 0)], p.s_in * w[max(t - 1, 0)], p.s_in * w[max(t - 2, 0)],
-                      p.s_in * w[max(t - 3, 0)]);
-    }
+    Weights4 f = fw[4 * g];
+    if (L < kChunk && !p.reverse)
+      f = partial_weights(reinterpret_cast<const float*>(sm + OFF_W), p.s_in, L, 16 * g + 4 * (lane & 3));
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-      float2 y = mul2v((m & 1) ? make_float2(f.z, f.w) : make_float2(f.x, f.y),
-                       make_float2(lo_f(x[m]), hi_f(x[m])));
-      o[0][m] = top2(y);
-      y = rest2(y);
-      if (kTerms == 3) {
-        o[1][m] = top2(y);
-        o[kTerms - 1][m] = top2(rest2(y));
+      const uint32_t f1 = f.f[0][m & 1], f2 = f.f[1][m & 1], f3 = f.f[2][m & 1];
+      const uint32_t h = bf_mul(x[m], f1), rest = bf_fma(x[m], f1, bf_neg(h));
+      o[0][m] = h;
+      if (kTerms == 2) {
+        o[1][m] = bf_fma(x[m], f2, rest);
       } else {
-        o[1][m] = pack2(y.x, y.y);
+        const uint32_t a = bf_mul(x[m], f2);
+        o[1][m] = rest;
+        o[kTerms - 2][m] = a;
+        o[kTerms - 1][m] = bf_fma(x[m], f3, bf_fma(x[m], f2, bf_neg(a)));
       }
     }
 #pragma unroll
@@ -389,13 +425,17 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
   const bool mine = dk0 < p.K, mine_v = vt0 < p.V;   // (features past the head dim: nothing to do)
   const float2* g = reinterpret_cast<const float2*>(sm + OFF_G);
   float2 X[32];
-  auto at = [&](int j) -> float {
-    const int k = dk0 + j;
-    return (u.init && dv < p.V && k < p.K)
-               ? u.init[p.initial_t ? (size_t)dv * p.K + k : (size_t)k * p.V + dv] : 0.f;
-  };
 #pragma unroll
-  for (int j = 0; j < 32; ++j) X[j] = make_float2(at(2 * j), at(2 * j + 1));
+  for (int j = 0; j < 32; ++j) X[j] = make_float2(0.f, 0.f);
+  if (u.init && dv < p.V) {
+    const size_t step = p.initial_t ? 1 : p.V;
+    const float* src = u.init + (p.initial_t ? (size_t)dv * p.K + dk0 : (size_t)dk0 * p.V + dv);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {   // (K is even)
+      if (dk0 + 2 * j < p.K) X[j] = make_float2(src[0], src[step]);
+      src += 2 * step;
+    }
+  }
   // the X operand of the next O1
   auto put_x = [&]() {
     if (mine) {
@@ -427,12 +467,12 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     tc_fence_before();
     warp_arrive(&bars[B_UFREE], lane);
   };
-  // With two terms V~ of chunk i is made while U of chunk i - 1 runs; with three, whose columns
+  // With two terms V~ of chunk i is made while U of chunk i - 1 runs; with four, whose columns
   // have no room for a second buffer, after it.
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const int s = i % kStages, L = chunk_at(p, u, u.c0 + i).L;
-    if (kTerms == 3 && i > 0) {
+    const int s = i & (kStages - 1), L = chunk_at(p, u, u.c0 + i).L;
+    if (kTerms == 4 && i > 0) {
       if (!wait_warp(&bars[B_U], (uint32_t)(i - 1) & 1u)) return false;
       tc_fence_after();
       update(i - 1);
@@ -459,10 +499,15 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     update(n - 1);
   }
   if (u.fin) {
+    float* dst = u.fin + (size_t)dk0 * p.V + dv;
 #pragma unroll
-    for (int j = 0; j < 64; ++j)
-      if (dv < p.V && dk0 + j < p.K)
-        u.fin[(size_t)(dk0 + j) * p.V + dv] = (j & 1) ? X[j >> 1].y : X[j >> 1].x;
+    for (int j = 0; j < 32; ++j) {
+      if (dv < p.V && dk0 + 2 * j < p.K) {
+        dst[0] = X[j].x;
+        dst[p.V] = X[j].y;
+      }
+      dst += 2 * p.V;
+    }
   }
   return true;
 }
@@ -491,6 +536,8 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
   const int tid = threadIdx.x - 32 * kStateWarps, lane = tid & 31, wq = tid >> 5;
   const uint32_t lane_off = (uint32_t)(32 * wq) << 16, sbase = smem_u32(sm);
   const float* w = reinterpret_cast<const float*>(sm + OFF_W);
+  // the factors of O1 in a full chunk, of this lane's tokens 2 (lane % 4) and the next
+  const float2* rf = reinterpret_cast<const float2*>(sm + OFF_R) + (lane & 3);
   const bool leader = tid == 0;
   bool ok = true;
 #pragma unroll 1
@@ -505,6 +552,7 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
       break;
     }
     tc_fence_after();
+    if (leader) mbar_arrive(&bars[B_EMPTY + (i & (kStages - 1))]);   // O2 is a chunk's last MMA
     if (ch.L < kChunk || p.o_f32) {
       store_rows(p, w, ch, o1, o2, u.h, 32 * wq + lane);
       tc_fence_before();
@@ -517,35 +565,31 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
     const int mblk = lane >> 3, rr = lane & 7, d0 = 32 * wq + 8 * mblk;
     const uint32_t st_base = sbase + OFF_O + (d0 >> 6) * 8192 + rr * 128 + ((((d0 & 63) >> 3) ^ rr) << 4);
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {   // tokens 32 pass .. + 31
-      uint32_t a0[16], a1[16], b0[16], b1[16];
-      tmem_ld16x256b_x4(o1 + 32 * pass, a0);
-      tmem_ld16x256b_x4(o1 + (16u << 16) + 32 * pass, a1);
-      tmem_ld16x256b_x4(o2 + 32 * pass, b0);
-      tmem_ld16x256b_x4(o2 + (16u << 16) + 32 * pass, b1);
+    for (int pass = 0; pass < 4; ++pass) {   // tokens 16 pass .. + 15
+      uint32_t a0[8], a1[8], b0[8], b1[8];
+      tmem_ld16x256b_x2(o1 + 16 * pass, a0);
+      tmem_ld16x256b_x2(o1 + (16u << 16) + 16 * pass, a1);
+      tmem_ld16x256b_x2(o2 + 16 * pass, b0);
+      tmem_ld16x256b_x2(o2 + (16u << 16) + 16 * pass, b1);
+      const float2 wt[2] = {rf[8 * pass], rf[8 * pass + 4]};
       tmem_wait_ld();
-      if (pass == 1) {
-        tc_fence_before();
-        warp_arrive(&bars[B_OFREE], lane);
-      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = 32 * pass + 8 * j + 2 * (lane & 3);
-        const float2 wt = make_float2(p.s_out * w[p.reverse ? 63 - t : t + 1],
-                                      p.s_out * w[p.reverse ? 62 - t : t + 2]);
+      for (int j = 0; j < 2; ++j) {
         uint32_t f[4];
 #pragma unroll
         for (int mm = 0; mm < 4; ++mm) {
           const uint32_t* x = (mm >> 1) ? a1 : a0;
           const uint32_t* y = (mm >> 1) ? b1 : b0;
           const int e = 4 * j + 2 * (mm & 1);
-          const float2 o = fma2(wt, make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+          const float2 o = fma2(wt[j], make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
                                 make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
           f[mm] = pack2(o.x, o.y);
         }
-        stmatrix_x4_trans(st_base + (4 * pass + j) * 1024, f);
+        stmatrix_x4_trans(st_base + (2 * pass + j) * 1024, f);
       }
     }
+    tc_fence_before();
+    warp_arrive(&bars[B_OFREE], lane);
     fence_proxy_async_smem();
     group_sync(1, 32 * kOutWarps);
     if (leader) {
@@ -596,8 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const float ld = clamp_log_decay(p.log_decay[u.h]);
   if (tid <= kChunk) reinterpret_cast<float*>(sm + OFF_W)[tid] = decay_pow(ld, (float)tid);
   if (tid < kChunk)
-    reinterpret_cast<float*>(sm + OFF_F)[tid] =
-        p.s_in * decay_pow(ld, p.reverse ? (float)(tid + 1) : (float)(kChunk - 1 - tid));
+    reinterpret_cast<float*>(sm + OFF_R)[tid] =
+        p.s_out * decay_pow(ld, p.reverse ? (float)(kChunk - 1 - tid) : (float)(tid + 1));
+  if (tid >= 64 && tid < 80) {
+    const int t = 4 * (tid - 64);
+    float x[4];
+    for (int i = 0; i < 4; ++i)
+      x[i] = p.s_in * decay_pow(ld, p.reverse ? (float)(t + i + 1) : (float)(kChunk - 1 - t - i));
+    reinterpret_cast<Weights4*>(sm + OFF_F)[tid - 64] = pack_weights(x);
+  }
   fill_p_table(p, ld, reinterpret_cast<float*>(sm + OFF_WP), tid);
   if (tid >= 128 && tid < 192 && lane == 0) {
     const int L = warp == 4 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
@@ -620,11 +671,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const int terms = p.final_state ? 3 : 2;
+  const int terms = p.final_state ? 4 : 2;
 
   bool ok = true;
   if (warp < kStateWarps) {
-    ok = terms == 3 ? state_role<3>(p, u, sm, tbase, bars) : state_role<2>(p, u, sm, tbase, bars);
+    ok = terms == 4 ? state_role<4>(p, u, sm, tbase, bars) : state_role<2>(p, u, sm, tbase, bars);
   } else if (warp < kStateWarps + kOutWarps) {
     ok = out_role(p, u, sm, tbase, bars, &tmO);
   } else if (warp < kMmaWarp) {
