@@ -7,12 +7,16 @@
 // gdn_linear_attn.h):
 //
 //   D    = [Q; K] K^T                      M=128 N=64  (rows 0-63 are Q K^T)
-//   P_ij = s_in s_out w_{i-j} D_ij, j <= i bf16, shared memory
-//   O1^T = X^T Q^T                         M=128 (value features) N=64 (tokens)
-//   O2^T = V^T P^T                         M=128 N=64
-//   o_i  = s_out w_{i+1} O1_i + O2_i
+//   P_ij = s_in w_{i-j} / R_i D_ij, j <= i bf16, shared memory; R_i = max(w_{i+1}, 2^-60)
+//   O^T  = X^T Q^T + V^T P^T               M=128 (value features) N=64 (tokens)
+//   o_i  = s_out R_i O_i
 //   U^T  = V~^T K, V~_j = s_in w_{L-1-j} v_j     M=128 N=K
 //   X   <- w_L X + U
+//
+// The read-out of the state and the in-chunk sum share one accumulator by taking the row's decay
+// R_i out of both (two accumulators, combined at the end, left no columns for a second output
+// buffer, and the MMAs waited for the output warps: 1330 ns a chunk).  Where w_{i+1} is below
+// 2^-60 the state's share of the row is below that too, and stands with 2^-60 in its place.
 //
 // The running state lives in fp32 registers of the state warps (value feature = TMEM lane, key
 // feature = column), so a chunk's only serial work on it is one multiply-add per element; the
@@ -60,8 +64,9 @@ constexpr uint32_t kStageV = 32768;                // [v half][64 tokens][128 B]
 constexpr uint32_t OFF_P = kStages * kStage;       // [64 i][64 j] bf16
 constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 tokens][128 B]
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
-constexpr uint32_t OFF_F = OFF_W + 288;            // Weights4[16]: the weights of V~ in a full chunk
-constexpr uint32_t OFF_R = OFF_F + 16 * 24;           // float[64]: the factors of O1 in a full chunk
+constexpr uint32_t OFF_F = OFF_W + 288;            // Weights4[2][16]: the weights of V~ in a full and
+                                                   // in the partial chunk
+constexpr uint32_t OFF_R = OFF_F + 2 * 16 * 24;           // float[64]: s_out R of a full chunk's rows
 constexpr uint32_t OFF_WP = OFF_R + 256;           // factors of P, see fill_p_table
 constexpr uint32_t kWpStride = 136;                // floats of one copy
 constexpr uint32_t OFF_G = OFF_WP + 4 * 4 * kWpStride;   // float2[2]: decay of a full / the partial chunk
@@ -70,30 +75,33 @@ constexpr uint32_t SMEM_USED = OFF_BAR + 256;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;   // slack for aligning the base
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
-// TMEM columns.
-constexpr uint32_t COL_U = 0, COL_D = 128, COL_X = 192, COL_O1 = 256, COL_O2 = 320,
-                   COL_VT = 384 /* 2 buffers x 2 terms x 32, or 4 terms x 32 */, TMEM_COLS = 512;
+// TMEM columns.  O and V~ share the upper half: two terms of V~ have two buffers (128 columns) and
+// so has O; of four terms the first two have two buffers, the others one, and O has one.
+constexpr uint32_t COL_U = 0, COL_D = 128, COL_X = 192, COL_O = 256, TMEM_COLS = 512;
 
 enum {
   B_FULL = 0,     // [4] stage landed
-  B_EMPTY = 4,    // [4] stage free (an output warp, once O1 and O2 are complete)
-  B_VT = 8,       // [2] V~ written (state warps)
-  B_U = 10,       // U of a chunk complete (commit): V~ read too
-  B_UFREE = 11,   // U read (state warps)
-  B_X = 12,       // X operand written (state warps)
-  B_XFREE = 13,   // O1 complete (commit): X operand read
-  B_D = 14,       // D complete (commit)
-  B_P = 15,       // P written, D read (P warps)
-  B_O = 16,       // O1, O2 complete (commit): the chunk's stage has been read
-  B_OFREE = 17,   // O1, O2 read (output warps)
+  B_EMPTY = 4,    // [4] stage free (an output warp, once O is complete)
+  B_V = 8,        // V~ written and U of the chunk before read (state warps)
+  B_U = 9,        // U complete (commit): V~ read
+  B_X = 10,       // X operand written (state warps)
+  B_XFREE = 11,   // X^T Q^T complete (commit): the X operand read
+  B_D = 12,       // D complete (commit)
+  B_P = 13,       // P written, D read (P warps)
+  B_O = 14,       // [2] O complete (commit): the chunk's stage has been read
+  B_OFREE = 16,   // [2] O read (output warps)
   B_COUNT = 18
 };
 constexpr uint32_t OFF_FLAG = OFF_BAR + 8 * B_COUNT, OFF_TSLOT = OFF_FLAG + 8;
 
-// The columns of V~ of chunk i: two terms have two buffers, four have one.
-__device__ __forceinline__ uint32_t vt_col(int i, int terms) {
-  return COL_VT + (terms == 2 ? 64u * (i & 1) : 0u);
+__device__ __forceinline__ uint32_t o_col(int i, int terms) {
+  return COL_O + (terms == 2 ? 64u * (i & 1) : 0u);
 }
+// The columns of the first two terms of V~ of chunk i, and of the other two.
+__device__ __forceinline__ uint32_t vt_col(int i, int terms) {
+  return COL_O + (terms == 2 ? 128u : 64u) + 64u * (i & 1);
+}
+constexpr uint32_t COL_VT_LATE = COL_O + 192;
 
 struct Unit {
   int h, bos, eos;       // the sequence
@@ -102,22 +110,25 @@ struct Unit {
   float* fin;
 };
 
-// A bounded wait; the slow path is out of line and reads the clock only now and then (the code of
-// sixteen warps in five roles has to fit the instruction caches, and failing polls share the
-// issue slots with the work they wait for).
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0 && globaltimer_ns() - t0 > kWaitNs) return false;
-  }
-}
+// A bounded wait, short: the roles' loops are fetched anew every chunk (five roles' code does not
+// fit the innermost instruction caches), so an instruction costs some five cycles wherever it
+// stands.  4 million tries are 40 ms at the very least.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity);
+  uint32_t tries = 0;
+  while (!mbar_try_wait(bar, parity))
+    if (++tries > (1u << 22)) return false;
+  return true;
 }
-// Every lane of the warp waits; the answer is the same for all of them.
+// The same for a whole warp, asleep between the tries (the tries of fourteen warps would take
+// issue slots from the work they wait for: 1730 instead of 1560 ns a chunk with the state kept);
+// the answer is the same for all lanes.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity));
+  uint32_t tries = 0;
+  while (!mbar_try_wait(bar, parity)) {
+    __nanosleep(20);
+    if (++tries > (1u << 22)) break;
+  }
+  return __all_sync(0xffffffffu, tries <= (1u << 22));
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
@@ -178,6 +189,9 @@ __device__ __forceinline__ Weights4 pack_weights(const float (&x)[4]) {
   }
   return w;
 }
+// R of a row whose decay is gamma^e.
+__device__ __forceinline__ float row_factor(const float* w, int e) { return fmaxf(w[e], 0x1p-60f); }
+
 struct ChunkAt {
   int t0, L;
 };
@@ -212,87 +226,94 @@ __device__ void load_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint
   }
 }
 
-// ------------------------------------------------------------------ MMAs (one warp)
-// 4 n MMAs (64 n K elements) with A in shared memory or TMEM and B in shared memory.  a, b
-// advance by step_* an MMA within a group of four and by skip_* from group to group (descriptor
-// units of 16 bytes, or TMEM columns).  The whole warp walks the loops and one elected lane issues.
-struct Operands {
-  uint32_t step_a, step_b, skip_a, skip_b;
-};
-template <bool kTmemA>
-__device__ __forceinline__ void issue(uint32_t d, uint64_t a, uint64_t b, uint32_t id, int n, Operands o,
-                                      uint32_t acc = 0) {
-#pragma unroll 1
-  for (int h = 0; h < n; ++h) {
-    if (elect_one()) {
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        if (kTmemA) mma_bf16_ta(d, (uint32_t)a + ks * o.step_a, b + ks * o.step_b, id, ks > 0 ? 1u : acc);
-        else mma_bf16(d, a + ks * o.step_a, b + ks * o.step_b, id, ks > 0 ? 1u : acc);
-      }
-    }
-    acc = 1;
-    a += o.skip_a;
-    b += o.skip_b;
-  }
+// ------------------------------------------------------------------ MMAs (one elected thread)
+// Descriptors by their low words (address and leading offset); the high word is the same for all.
+constexpr uint32_t kDescHi = (uint32_t)((((uint64_t)(1024 >> 4)) << 32 | (1ull << 46) | (2ull << 61)) >> 32);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  if (elect_one()) mma_commit(bar);
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n setp.ne.b32 p, %4, 0;\n mov.b64 da, {%1, %5};\n"
+      " mov.b64 db, {%2, %5};\n tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n setp.ne.b32 p, %4, 0;\n mov.b64 db, {%2, %5};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(kDescHi)
+      : "memory");
 }
 
 __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint32_t tbase,
                          uint64_t* bars, int terms) {
   const int kh = p.K > 64 ? 2 : 1, n = u.c1 - u.c0;
   constexpr uint32_t kS16 = kStage >> 4;
-  const uint64_t dQ = sdesc_sw128(sb, 16, 1024), dK = sdesc_sw128(sb + 8192, 16, 1024),
-                 dKm = sdesc_sw128(sb + 8192, 16384, 1024), dV = sdesc_sw128(sb + kStageV, 8192, 1024),
-                 dP = sdesc_sw128(sb + OFF_P, 16, 1024);
+  const uint32_t dQ = desc_lo(sb, 16), dK = desc_lo(sb + 8192, 16), dKm = desc_lo(sb + 8192, 16384),
+                 dV = desc_lo(sb + kStageV, 8192), dP = desc_lo(sb + OFF_P, 16);
   const uint32_t idU = kh == 2 ? idesc_bf16(128, 128, false, true) : idesc_bf16(128, 64, false, true);
   constexpr uint32_t idS = idesc_bf16(128, 64, false, false), idO2 = idesc_bf16(128, 64, true, false);
   // chunk -1 has only the next one's D
 #pragma unroll 1
   for (int i = -1; i < n; ++i) {
-    const int s = i & (kStages - 1);
-    const uint32_t par = (uint32_t)i & 1u;
-    if (i >= 0) {
-      // U^T = V~^T K
-      if (!wait_warp(&bars[B_VT + par], (uint32_t)(i >> 1) & 1u)) return false;
-      if (i > 0 && !wait_warp(&bars[B_UFREE], par ^ 1u)) return false;
+    const uint32_t so = (uint32_t)(i & (kStages - 1)) * kS16, par = (uint32_t)i & 1u;
+    if (i >= 0) {   // U^T = V~^T K
+      if (!wait_bar(&bars[B_V], par)) return false;
       tc_fence_after();
-      issue<true>(tbase + COL_U, tbase + vt_col(i, terms), dKm + s * kS16, idU, terms, {8, 128, 32, 0});
-      commit(&bars[B_U]);
-      // O1^T = X^T Q^T
-      if (!wait_warp(&bars[B_X], par)) return false;
-      if (i > 0 && !wait_warp(&bars[B_OFREE], par ^ 1u)) return false;
+#pragma unroll 1
+      for (int t = 0; t < terms; ++t) {
+        const uint32_t a = tbase + (t < 2 ? vt_col(i, terms) + 32 * t : COL_VT_LATE + 32 * (t - 2));
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ts(tbase + COL_U, a + 8 * ks, dKm + so + 128 * ks, idU, (uint32_t)(t | ks));
+      }
+      mma_commit(&bars[B_U]);
+      // O^T = X^T Q^T + V^T P^T
+      const uint32_t o = tbase + o_col(i, terms);
+      if (!wait_bar(&bars[B_X], par)) return false;
+      const int before = terms == 2 ? i - 2 : i - 1;   // the chunk whose output had these columns
+      if (before >= 0 && !wait_bar(&bars[B_OFREE + (before & 1)], (uint32_t)(before >> 1) & 1u)) return false;
       tc_fence_after();
-      issue<true>(tbase + COL_O1, tbase + COL_X, dQ + s * kS16, idS, kh, {8, 2, 32, 1024});
-      if (i + 1 < n) commit(&bars[B_XFREE]);
-      // O2^T = V^T P^T
-      if (!wait_warp(&bars[B_P], par)) return false;
+#pragma unroll 1
+      for (int h = 0; h < kh; ++h)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_ts(o, tbase + COL_X + 32 * h + 8 * ks, dQ + so + 1024 * h + 2 * ks, idS, (uint32_t)(h | ks));
+      mma_commit(&bars[B_XFREE]);
+      if (!wait_bar(&bars[B_P], par)) return false;
       tc_fence_after();
-      issue<false>(tbase + COL_O2, dV + s * kS16, dP, idO2, 1, {128, 2, 0, 0});
-      commit(&bars[B_O]);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) mma_ss(o, dV + so + 128 * ks, dP + 2 * ks, idO2, 1);
+      mma_commit(&bars[B_O + par]);
     }
-    if (i + 1 < n) {
-      const int s1 = (i + 1) & (kStages - 1);
-      if (!wait_warp(&bars[B_FULL + s1], (uint32_t)((i + 1) / kStages) & 1u)) return false;
+    if (i + 1 < n) {   // D = [Q; K] K^T of the next chunk
+      const uint32_t s1 = (uint32_t)(i + 1) & (kStages - 1);
+      if (!wait_bar(&bars[B_FULL + s1], (uint32_t)((i + 1) / kStages) & 1u)) return false;
       tc_fence_after();
-      issue<false>(tbase + COL_D, dQ + s1 * kS16, dK + s1 * kS16, idS, kh, {2, 2, 1024, 1024});
-      commit(&bars[B_D]);
+#pragma unroll 1
+      for (int h = 0; h < kh; ++h)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          const uint32_t off = s1 * kS16 + 1024 * h + 2 * ks;
+          mma_ss(tbase + COL_D, dQ + off, dK + off, idS, (uint32_t)(h | ks));
+        }
+      mma_commit(&bars[B_D]);
     }
   }
   return true;
 }
 
 // ------------------------------------------------------------------ P (warps 12, 13)
-// The factor of P_ij depends on j - i alone: f[x] for x = j - i + 63 in 0 .. 126, zero where the
+// The factor s_in w_{i-j} of P_ij depends on j - i alone: f[x] for x = j - i + 63 in 0 .. 126, zero where the
 // mask is.  Row i reads f[63 - i ..], four at a time: four copies shifted by one float each keep
 // those reads 16-byte aligned whatever i is, and their stride of 8 banks keeps them apart.
 __device__ __forceinline__ void fill_p_table(const LinAttnPass& p, float ld, float* wp, int tid) {
   for (int e = tid; e < 4 * (int)kWpStride; e += kThreads) {
     const int copy = e / (int)kWpStride, x = e - copy * (int)kWpStride + copy;   // copy[y] = f[y + copy]
     const int dist = p.reverse ? x - 63 : 63 - x;
-    wp[e] = (dist >= 0 && dist < kChunk) ? p.s_in * p.s_out * decay_pow(ld, (float)dist) : 0.f;
+    wp[e] = (dist >= 0 && dist < kChunk) ? p.s_in * decay_pow(ld, (float)dist) : 0.f;
   }
 }
 
@@ -307,6 +328,7 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
                        uint64_t* bars) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 1, row = 32 * wq + lane;
   const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
+  const float* w = reinterpret_cast<const float*>(sm + OFF_W);
   const int shift = (63 - row) & 3;
   const float4* f4 = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm + OFF_WP) +
                                                      shift * kWpStride + (63 - row - shift));
@@ -315,8 +337,9 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
     const int i = c - u.c0;
     const int L = chunk_at(p, u, c).L;
     if (!wait_warp(&bars[B_D], (uint32_t)i & 1u)) return false;
-    // (D of a chunk is issued after O2 of the one before, so P has been read when it is complete)
+    // (D of a chunk is issued after V^T P^T of the one before: P has been read when it is complete)
     tc_fence_after();
+    const float inv = 1.f / row_factor(w, p.reverse ? max(L - 1 - row, 0) : row + 1);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
       float x[32];
@@ -325,13 +348,13 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
       for (int g = 0; g < 4; ++g) {
         const float4 a = f4[8 * half + 2 * g], b = f4[8 * half + 2 * g + 1];
         uint4 q;
-        float2 t = mul2v(make_float2(a.x, a.y), make_float2(x[8 * g], x[8 * g + 1]));
+        float2 t = mul2v(make_float2(a.x, a.y), make_float2(inv * x[8 * g], inv * x[8 * g + 1]));
         q.x = pack2(t.x, t.y);
-        t = mul2v(make_float2(a.z, a.w), make_float2(x[8 * g + 2], x[8 * g + 3]));
+        t = mul2v(make_float2(a.z, a.w), make_float2(inv * x[8 * g + 2], inv * x[8 * g + 3]));
         q.y = pack2(t.x, t.y);
-        t = mul2v(make_float2(b.x, b.y), make_float2(x[8 * g + 4], x[8 * g + 5]));
+        t = mul2v(make_float2(b.x, b.y), make_float2(inv * x[8 * g + 4], inv * x[8 * g + 5]));
         q.z = pack2(t.x, t.y);
-        t = mul2v(make_float2(b.z, b.w), make_float2(x[8 * g + 6], x[8 * g + 7]));
+        t = mul2v(make_float2(b.z, b.w), make_float2(inv * x[8 * g + 6], inv * x[8 * g + 7]));
         q.w = pack2(t.x, t.y);
         *reinterpret_cast<uint4*>(sm + OFF_P + sw128_offset(row, 32 * half + 8 * g)) = q;
       }
@@ -366,33 +389,22 @@ __device__ __noinline__ void clear_rows(uint8_t* st, int L, int vt0, int warp, i
   __syncwarp();
 }
 
-// The weights of tokens t0 .. t0 + 3 in the partial chunk of L tokens (forward: they count back
-// from its end; the rows past it are clear, whatever their weight).
-__device__ __noinline__ Weights4 partial_weights(const float* w, float s_in, int L, int t0) {
-  float x[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = s_in * w[max(L - 1 - t0 - i, 0)];
-  return pack_weights(x);
-}
-
 // This warp's 16 value features of V~^T as TMEM fragments.  Fragment register 4 g + r of thread t
 // holds features t/4 (r < 2) or t/4 + 8 and TMEM column 8 g + 2 (t%4) + (r & 1), that is tokens
 // 16 g + 4 (t%4) + 2 (r & 1) and the next; ldmatrix .trans delivers exactly that when its row
 // addresses name the tokens 0, 1, 4, 5, 8, 9, 12, 13 (r even) or 2, 3, 6, .. (odd).
 template <int kTerms>
-__device__ __forceinline__ void make_vt(const LinAttnPass& p, const uint8_t* sm, uint32_t v_tile, int d0,
-                                        int L, int lane, uint32_t dst) {
-  const Weights4* fw = reinterpret_cast<const Weights4*>(sm + OFF_F) + (lane & 3);
+__device__ __forceinline__ void make_vt(const uint8_t* sm, uint32_t v_tile, int d0,
+                                        int L, int lane, uint32_t dst, uint32_t (&late)[2][16]) {
+  const Weights4* fw = reinterpret_cast<const Weights4*>(sm + OFF_F) + (L < kChunk ? 16 : 0) + (lane & 3);
   const int r = lane >> 3, j = lane & 7;              // matrix (register) this lane addresses, row
   const int tok0 = 4 * (j >> 1) + 2 * (r & 1) + (j & 1), d = d0 + 8 * (r >> 1);
   const uint32_t tile = v_tile + (d >> 6) * 8192 + (uint32_t)tok0 * 128u + ((((d & 63) >> 3) ^ (tok0 & 7)) << 4);
-#pragma unroll 2
+#pragma unroll(kTerms == 2 ? 2 : 4)
   for (int g = 0; g < 4; ++g) {
-    uint32_t x[4], o[kTerms][4];
+    uint32_t x[4], o[2][4];
     ldmatrix_x4_trans(tile + g * 2048, x);
-    Weights4 f = fw[4 * g];
-    if (L < kChunk && !p.reverse)
-      f = partial_weights(reinterpret_cast<const float*>(sm + OFF_W), p.s_in, L, 16 * g + 4 * (lane & 3));
+    const Weights4 f = fw[4 * g];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
       const uint32_t f1 = f.f[0][m & 1], f2 = f.f[1][m & 1], f3 = f.f[2][m & 1];
@@ -403,14 +415,13 @@ __device__ __forceinline__ void make_vt(const LinAttnPass& p, const uint8_t* sm,
       } else {
         const uint32_t a = bf_mul(x[m], f2);
         o[1][m] = rest;
-        o[kTerms - 2][m] = a;
-        o[kTerms - 1][m] = bf_fma(x[m], f3, bf_fma(x[m], f2, bf_neg(a)));
+        late[0][4 * g + m] = a;
+        late[1][4 * g + m] = bf_fma(x[m], f3, bf_fma(x[m], f2, bf_neg(a)));
       }
     }
-#pragma unroll
-    for (int t = 0; t < kTerms; ++t) tmem_st16x256b_x1(dst + 32 * t + 8 * g, o[t]);
+    tmem_st16x256b_x1(dst + 8 * g, o[0]);
+    tmem_st16x256b_x1(dst + 32 + 8 * g, o[1]);
   }
-  tmem_wait_st();
 }
 
 template <int kTerms>
@@ -464,34 +475,34 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
         }
       }
     }
-    tc_fence_before();
-    warp_arrive(&bars[B_UFREE], lane);
   };
-  // With two terms V~ of chunk i is made while U of chunk i - 1 runs; with four, whose columns
-  // have no room for a second buffer, after it.
+  // V~ of chunk i is made while U of chunk i - 1 runs; the terms that have no second buffer wait
+  // for its end in registers.
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int s = i & (kStages - 1), L = chunk_at(p, u, u.c0 + i).L;
-    if (kTerms == 4 && i > 0) {
-      if (!wait_warp(&bars[B_U], (uint32_t)(i - 1) & 1u)) return false;
-      tc_fence_after();
-      update(i - 1);
-    }
+    uint32_t late[2][16];
     if (!wait_warp(&bars[B_FULL + s], (uint32_t)(i / kStages) & 1u)) return false;
     if (L < kChunk) clear_rows(sm + s * kStage, L, vt0, warp, lane);
     if (mine_v)
-      make_vt<kTerms>(p, sm, sb + s * kStage + kStageV, vt0, L, lane, tbase + vt_off + vt_col(i, kTerms));
-    tc_fence_before();
-    warp_arrive(&bars[B_VT + (i & 1)], lane);
-    if (i == 0) continue;
-    if (kTerms == 2) {
+      make_vt<kTerms>(sm, sb + s * kStage + kStageV, vt0, L, lane, tbase + vt_off + vt_col(i, kTerms), late);
+    if (i > 0) {
       if (!wait_warp(&bars[B_U], (uint32_t)(i - 1) & 1u)) return false;
       tc_fence_after();
-      update(i - 1);
     }
-    if (!wait_warp(&bars[B_XFREE], (uint32_t)(i - 1) & 1u)) return false;
-    tc_fence_after();
-    put_x();
+    if (kTerms == 4 && mine_v) {
+      tmem_st16x256b_x4(tbase + vt_off + COL_VT_LATE, late[0]);
+      tmem_st16x256b_x4(tbase + vt_off + COL_VT_LATE + 32, late[1]);
+    }
+    if (i > 0) update(i - 1);
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(&bars[B_V], lane);
+    if (i > 0) {
+      if (!wait_warp(&bars[B_XFREE], (uint32_t)(i - 1) & 1u)) return false;
+      tc_fence_after();
+      put_x();
+    }
   }
   if (u.fin) {
     if (!wait_warp(&bars[B_U], (uint32_t)(n - 1) & 1u)) return false;
@@ -514,29 +525,28 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
 
 // ------------------------------------------------------------------ output (warps 8-11)
 __device__ __noinline__ void store_rows(const LinAttnPass& p, const float* w, const ChunkAt& ch,
-                                        uint32_t o1, uint32_t o2, int h, int dv) {
+                                        uint32_t o, int h, int dv) {
+  const size_t row0 = ((size_t)ch.t0 * p.H + h) * p.V + dv, step = (size_t)p.H * p.V;
 #pragma unroll 1
-  for (int half = 0; half < 2; ++half) {
-    float x[32], y[32];
-    tmem_ld32(o1 + 32 * half, x);
-    tmem_ld32(o2 + 32 * half, y);
+  for (int t0 = 0; t0 < ch.L; t0 += 32) {
+    float x[32];
+    tmem_ld32(o + t0, x);
 #pragma unroll
     for (int jj = 0; jj < 32; ++jj) {
-      const int t = 32 * half + jj;
+      const int t = t0 + jj;
       if (t < ch.L && dv < p.V)
-        store_elem(p.o, ((size_t)(ch.t0 + t) * p.H + h) * p.V + dv,
-                   fmaf(p.s_out * w[p.reverse ? ch.L - 1 - t : t + 1], x[jj], y[jj]),
+        store_elem(p.o, row0 + t * step, p.s_out * row_factor(w, p.reverse ? ch.L - 1 - t : t + 1) * x[jj],
                    p.o_f32 ? GDN_F32 : GDN_BF16);
     }
   }
 }
 
 __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase,
-                         uint64_t* bars, const CUtensorMap* to) {
+                         uint64_t* bars, int terms, const CUtensorMap* to) {
   const int tid = threadIdx.x - 32 * kStateWarps, lane = tid & 31, wq = tid >> 5;
   const uint32_t lane_off = (uint32_t)(32 * wq) << 16, sbase = smem_u32(sm);
   const float* w = reinterpret_cast<const float*>(sm + OFF_W);
-  // the factors of O1 in a full chunk, of this lane's tokens 2 (lane % 4) and the next
+  // the factors s_out R of a full chunk's rows, of this lane's tokens 2 (lane % 4) and the next
   const float2* rf = reinterpret_cast<const float2*>(sm + OFF_R) + (lane & 3);
   const bool leader = tid == 0;
   bool ok = true;
@@ -544,19 +554,19 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
   for (int c = u.c0; c < u.c1; ++c) {
     const int i = c - u.c0;
     const ChunkAt ch = chunk_at(p, u, c);
-    const uint32_t o1 = tbase + lane_off + COL_O1, o2 = tbase + lane_off + COL_O2;
+    const uint32_t par = (uint32_t)i & 1u, o = tbase + lane_off + o_col(i, terms);
     if (leader) tma_store_wait_read();   // the previous tile has left the staging
-    ok = wait_warp(&bars[B_O], (uint32_t)i & 1u);
+    ok = wait_warp(&bars[B_O + par], (uint32_t)(i >> 1) & 1u);
     if (group_sync_or(1, 32 * kOutWarps, !ok)) {
       ok = false;
       break;
     }
     tc_fence_after();
-    if (leader) mbar_arrive(&bars[B_EMPTY + (i & (kStages - 1))]);   // O2 is a chunk's last MMA
+    if (leader) mbar_arrive(&bars[B_EMPTY + (i & (kStages - 1))]);   // (a chunk's last MMAs)
     if (ch.L < kChunk || p.o_f32) {
-      store_rows(p, w, ch, o1, o2, u.h, 32 * wq + lane);
+      store_rows(p, w, ch, o, u.h, 32 * wq + lane);
       tc_fence_before();
-      warp_arrive(&bars[B_OFREE], lane);
+      warp_arrive(&bars[B_OFREE + par], lane);
       continue;
     }
     // 16x256b loads give each thread value features (t/4, t/4 + 8) x tokens (2 (t%4), + 1): the
@@ -565,31 +575,27 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
     const int mblk = lane >> 3, rr = lane & 7, d0 = 32 * wq + 8 * mblk;
     const uint32_t st_base = sbase + OFF_O + (d0 >> 6) * 8192 + rr * 128 + ((((d0 & 63) >> 3) ^ rr) << 4);
 #pragma unroll 1
-    for (int pass = 0; pass < 4; ++pass) {   // tokens 16 pass .. + 15
-      uint32_t a0[8], a1[8], b0[8], b1[8];
-      tmem_ld16x256b_x2(o1 + 16 * pass, a0);
-      tmem_ld16x256b_x2(o1 + (16u << 16) + 16 * pass, a1);
-      tmem_ld16x256b_x2(o2 + 16 * pass, b0);
-      tmem_ld16x256b_x2(o2 + (16u << 16) + 16 * pass, b1);
-      const float2 wt[2] = {rf[8 * pass], rf[8 * pass + 4]};
+    for (int pass = 0; pass < 2; ++pass) {   // tokens 32 pass .. + 31
+      uint32_t a0[16], a1[16];
+      tmem_ld16x256b_x4(o + 32 * pass, a0);
+      tmem_ld16x256b_x4(o + (16u << 16) + 32 * pass, a1);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < 4; ++j) {
+        const float2 wt = rf[16 * pass + 4 * j];
         uint32_t f[4];
 #pragma unroll
         for (int mm = 0; mm < 4; ++mm) {
           const uint32_t* x = (mm >> 1) ? a1 : a0;
-          const uint32_t* y = (mm >> 1) ? b1 : b0;
           const int e = 4 * j + 2 * (mm & 1);
-          const float2 o = fma2(wt[j], make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                make_float2(__uint_as_float(y[e]), __uint_as_float(y[e + 1])));
-          f[mm] = pack2(o.x, o.y);
+          const float2 y = mul2v(wt, make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])));
+          f[mm] = pack2(y.x, y.y);
         }
-        stmatrix_x4_trans(st_base + (2 * pass + j) * 1024, f);
+        stmatrix_x4_trans(st_base + (4 * pass + j) * 1024, f);
       }
     }
     tc_fence_before();
-    warp_arrive(&bars[B_OFREE], lane);
+    warp_arrive(&bars[B_OFREE + par], lane);
     fence_proxy_async_smem();
     group_sync(1, 32 * kOutWarps);
     if (leader) {
@@ -641,12 +647,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid <= kChunk) reinterpret_cast<float*>(sm + OFF_W)[tid] = decay_pow(ld, (float)tid);
   if (tid < kChunk)
     reinterpret_cast<float*>(sm + OFF_R)[tid] =
-        p.s_out * decay_pow(ld, p.reverse ? (float)(kChunk - 1 - tid) : (float)(tid + 1));
-  if (tid >= 64 && tid < 80) {
-    const int t = 4 * (tid - 64);
+        p.s_out * fmaxf(decay_pow(ld, p.reverse ? (float)(kChunk - 1 - tid) : (float)(tid + 1)), 0x1p-60f);
+  if (tid >= 64 && tid < 96) {   // (rows past the partial chunk's end are clear, whatever their weight)
+    const int t = 4 * (tid & 15), L = tid < 80 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
     float x[4];
     for (int i = 0; i < 4; ++i)
-      x[i] = p.s_in * decay_pow(ld, p.reverse ? (float)(t + i + 1) : (float)(kChunk - 1 - t - i));
+      x[i] = p.s_in * decay_pow(ld, p.reverse ? (float)(t + i + 1) : (float)max(L - 1 - t - i, 0));
     reinterpret_cast<Weights4*>(sm + OFF_F)[tid - 64] = pack_weights(x);
   }
   fill_p_table(p, ld, reinterpret_cast<float*>(sm + OFF_WP), tid);
@@ -656,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
-      const int count = (i == B_VT || i == B_VT + 1 || i == B_UFREE || i == B_X) ? kStateWarps
-                        : i == B_P ? kPWarps : i == B_OFREE ? kOutWarps : 1;
+      const int count = (i == B_V || i == B_X) ? kStateWarps
+                        : i == B_P ? kPWarps : (i == B_OFREE || i == B_OFREE + 1) ? kOutWarps : 1;
       mbar_init(&bars[i], count);
     }
     *flag = 0;
@@ -677,11 +683,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kStateWarps) {
     ok = terms == 4 ? state_role<4>(p, u, sm, tbase, bars) : state_role<2>(p, u, sm, tbase, bars);
   } else if (warp < kStateWarps + kOutWarps) {
-    ok = out_role(p, u, sm, tbase, bars, &tmO);
+    ok = out_role(p, u, sm, tbase, bars, terms, &tmO);
   } else if (warp < kMmaWarp) {
     ok = p_role(p, u, sm, tbase, bars);
   } else if (warp == kMmaWarp) {
-    ok = mma_role(p, u, smem_u32(sm), tbase, bars, terms);
+    if (elect_one()) ok = mma_role(p, u, smem_u32(sm), tbase, bars, terms);
+    __syncwarp();
   } else {
     if (lane == 0) load_role(p, u, sm, bars, &tmQ, &tmK, &tmV);
     __syncwarp();
