@@ -6,6 +6,7 @@
 //   P_ij  = s_in w_{i-j} (q_i . k_j)   for j <= i, else 0           (reverse: w_{j-i}, j >= i)
 //   o_i   = s_out (w_{i+1} X^T q_i + sum_j P_ij v_j)                (reverse: w_{L-1-i})
 //   X    <- w_L X + sum_j s_in w_{L-1-j} k_j v_j^T                  (reverse: w_{j+1})
+#include <algorithm>
 #include <atomic>
 
 #include "gdn_linear_attn.cuh"
@@ -207,7 +208,10 @@ __global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const LinAtt
 
 // Sum of the value heads that share a query/key head: one thread per 4 elements.
 template <typename T>
-__global__ void linear_attn_fold_kernel(const float* part, T* out, long long rows, int group, int D) {
+__global__ void linear_attn_fold_kernel(const float* part0, const float* part1, T* out0, T* out1, long long rows,
+                                        int group, int D) {
+  const float* part = blockIdx.y ? part1 : part0;
+  T* out = blockIdx.y ? out1 : out0;
   const int D4 = D / 4;
   const long long n = rows * D4;
   for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n;
@@ -299,16 +303,18 @@ cudaError_t launch_linear_attn_generic(const LinAttnPass& p) {
   return p.o_f32 ? launch_pass<__nv_bfloat16, float>(p) : launch_pass<__nv_bfloat16, __nv_bfloat16>(p);
 }
 
-cudaError_t launch_linear_attn_fold(const float* part, void* out, long long T_total, int Hqk,
-                                    int group, int D, int io_dtype, cudaStream_t stream) {
+cudaError_t launch_linear_attn_fold(const float* const (&part)[2], void* const (&out)[2], long long T_total,
+                                    int Hqk, int group, int D, int io_dtype, cudaStream_t stream) {
   const long long rows = T_total * Hqk, n = rows * (D / 4);
   if (n == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)min((n + 255) / 256, 152LL * 16);
+  const dim3 grid((unsigned)std::min((n + 255) / 256, 152LL * 16), 2);
   if (io_dtype == GDN_F32)
-    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part, reinterpret_cast<float*>(out), rows, group, D);
+    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part[0], part[1], reinterpret_cast<float*>(out[0]),
+                                                      reinterpret_cast<float*>(out[1]), rows, group, D);
   else
-    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part, reinterpret_cast<__nv_bfloat16*>(out), rows,
-                                                      group, D);
+    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part[0], part[1],
+                                                      reinterpret_cast<__nv_bfloat16*>(out[0]),
+                                                      reinterpret_cast<__nv_bfloat16*>(out[1]), rows, group, D);
   return cudaGetLastError();
 }
 

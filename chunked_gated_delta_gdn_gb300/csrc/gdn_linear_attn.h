@@ -44,13 +44,19 @@ struct LinAttnPass {
 
 // CUDA cores: any accepted head dims, either type.
 cudaError_t launch_linear_attn_generic(const LinAttnPass& p);
-// Tensor cores: bf16 (o may be fp32), any accepted head dims.
-cudaError_t launch_linear_attn_tc(const LinAttnPass& p);
+// Tensor cores: bf16 (o may be fp32), any accepted head dims; up to three passes over the same
+// sequences and heads in one launch, each chain cut into `segs` segments (then `local` is scratch
+// of linear_attn_tc_workspace_bytes).  The number of segments goes by what the host knows: the
+// chains, the SMs and the most tokens that a sequence can have.
+constexpr int kLaMaxPasses = 3, kLaMaxSegments = 16, kLaMinSegmentChunks = 4;
+int linear_attn_tc_segments(int num_passes, int num_seqs, int H, long long most_tokens, int num_sms);
+size_t linear_attn_tc_workspace_bytes(int num_passes, int num_seqs, int H, int segs);
+cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* local);
 
-// out[t, hq, :] = sum over the group's value heads of part[t, hq * group + j, :] (fp32 in, io
-// dtype out, heads added in order).
-cudaError_t launch_linear_attn_fold(const float* part, void* out, long long T_total, int Hqk,
-                                    int group, int D, int io_dtype, cudaStream_t stream);
+// out[i][t, hq, :] = sum over the group's value heads of part[i][t, hq * group + j, :], i = 0, 1
+// (fp32 in, io dtype out, heads added in order).
+cudaError_t launch_linear_attn_fold(const float* const (&part)[2], void* const (&out)[2], long long T_total,
+                                    int Hqk, int group, int D, int io_dtype, cudaStream_t stream);
 
 struct LinAttnDecodeArgs {
   const void* q;             // [n, Hqk, K]

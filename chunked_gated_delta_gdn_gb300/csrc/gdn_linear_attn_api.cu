@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "gdn.h"
+#include "gdn_internal.h"
 #include "gdn_linear_attn.h"
 
 namespace {
@@ -39,15 +40,49 @@ gdn::LinAttnPass base_pass(const float* log_decay, int B, int T, int Hv, gdn_dty
   return p;
 }
 
-// bf16 runs on the tensor cores; fp32, whose 24-bit products they do not offer, on the CUDA cores.
-cudaError_t run_pass(const gdn::LinAttnPass& p) {
-  return p.io_dtype == GDN_BF16 ? gdn::launch_linear_attn_tc(p) : gdn::launch_linear_attn_generic(p);
+int sm_count() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return gdn::device_sm_count(dev);
 }
 
-// Scratch of the backward: per-value-head dq and dk (fp32) where value heads share a query/key
-// head.  One buffer serves both, one after the other.
-size_t bwd_part_bytes(long long T_total, int Hqk, int Hv, int K) {
-  return Hqk == Hv ? 0 : align256((size_t)T_total * Hv * K * sizeof(float));
+// Scratch of a call: the segments' contributions, then (backward) per-value-head dq and dk in
+// fp32 where value heads share a query/key head.
+struct Scratch {
+  int segs;
+  size_t local, part, total;   // bytes; part: one of the two
+};
+Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk, int Hv, int K,
+                int io_dtype) {
+  Scratch s{1, 0, 0, 0};
+  if (io_dtype == GDN_BF16) {
+    const long long most = packed ? (long long)B * T : T;
+    s.segs = gdn::linear_attn_tc_segments(num_passes, num_seqs, Hv, most, sm_count());
+    s.local = align256(gdn::linear_attn_tc_workspace_bytes(num_passes, num_seqs, Hv, s.segs));
+  }
+  if (num_passes > 1 && Hqk != Hv) s.part = align256((size_t)B * T * Hv * K * sizeof(float));
+  s.total = s.local + 2 * s.part;
+  return s;
+}
+
+// bf16 runs on the tensor cores; fp32, whose 24-bit products they do not offer, on the CUDA cores.
+cudaError_t run_passes(const gdn::LinAttnPass* p, int n, int segs, void* local) {
+  if (p[0].io_dtype == GDN_BF16)
+    return gdn::launch_linear_attn_tc(p, n, segs, reinterpret_cast<float*>(local));
+  for (int i = 0; i < n; ++i) {
+    const cudaError_t err = gdn::launch_linear_attn_generic(p[i]);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+gdn_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return GDN_OK;
+  if (!ws || bytes < need) return GDN_ERR_WORKSPACE;
+  return ((uintptr_t)ws & 255u) ? GDN_ERR_LAYOUT : GDN_OK;
 }
 
 }  // namespace
@@ -57,7 +92,8 @@ extern "C" {
 size_t gdn_linear_attn_chunk_fwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
                                                 int num_seqs, gdn_dtype_t io_dtype) {
   if (check_shapes(B, T, Hqk, Hv, K, V, io_dtype) != GDN_OK || num_seqs < 0) return (size_t)-1;
-  return 0;
+  // (a batch of one row needs as much whether it is packed or not)
+  return scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype).total;
 }
 
 gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void* v,
@@ -102,15 +138,15 @@ gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void*
   p.final_state = output_final_state ? final_state : nullptr;
   p.s_out = resolve_scale(scale, K);
   p.o = o;
-  (void)workspace;
-  (void)workspace_bytes;
-  return run_pass(p) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  const Scratch sc = scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype);
+  if ((st = check_workspace(workspace, workspace_bytes, sc.total)) != GDN_OK) return st;
+  return run_passes(&p, 1, sc.segs, workspace) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 size_t gdn_linear_attn_chunk_bwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
                                                 int num_seqs, gdn_dtype_t io_dtype) {
   if (check_shapes(B, T, Hqk, Hv, K, V, io_dtype) != GDN_OK || num_seqs < 0) return (size_t)-1;
-  return bwd_part_bytes((long long)B * T, Hqk, Hv, K);
+  return scratch(3, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype).total;
 }
 
 gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void* v,
@@ -138,11 +174,8 @@ gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void*
       (d_final_state && !aligned16(d_final_state)) ||
       (d_initial_state && !aligned16(d_initial_state)))
     return GDN_ERR_LAYOUT;
-  const size_t need = gdn_linear_attn_chunk_bwd_workspace_size(B, T, Hqk, Hv, K, V, num_seqs, io_dtype);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return GDN_ERR_WORKSPACE;
-    if ((uintptr_t)workspace & 255u) return GDN_ERR_LAYOUT;
-  }
+  const Scratch ws = scratch(3, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype);
+  if ((st = check_workspace(workspace, workspace_bytes, num_seqs > 0 ? ws.total : 0)) != GDN_OK) return st;
   const gdn::LinAttnPass base =
       base_pass(log_decay, B, T, Hv, io_dtype, cu_seqlens, num_seqs, dev_status, stream);
   if (num_seqs == 0) {
@@ -155,53 +188,54 @@ gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void*
   }
   const float sc = resolve_scale(scale, K);
   const int group = Hv / Hqk;
-  cudaError_t err;
+  float* part[2] = {nullptr, nullptr};   // per-value-head dq, dk
+  if (group > 1) {
+    part[0] = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + ws.local);
+    part[1] = part[0] + ws.part / sizeof(float);
+  }
+  gdn::LinAttnPass p[3] = {base, base, base};
   // dq_i = scale (sum_{j <= i} gamma^{i-j} (d_o_i . v_j) k_j + gamma^{i+1} S_0 d_o_i): the forward
   // pass over (d_o, v, k) with the state transposed
-  gdn::LinAttnPass p = base;
-  p.q = d_o; p.k = v; p.v = k;
-  p.Hq = p.Hk = Hv;
-  p.Hv = Hqk;
-  p.K = V; p.V = K;
-  p.initial = initial_state;
-  p.initial_t = 1;
-  p.s_out = sc;
-  p.o = group > 1 ? workspace : dq;
-  p.o_f32 = group > 1;
-  if ((err = run_pass(p)) != cudaSuccess) return GDN_ERR_CUDA;
-  if (group > 1 && gdn::launch_linear_attn_fold(reinterpret_cast<const float*>(workspace), dq, T_total,
-                                                Hqk, group, K, io_dtype, p.stream) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  p[0].q = d_o; p[0].k = v; p[0].v = k;
+  p[0].Hq = p[0].Hk = Hv;
+  p[0].Hv = Hqk;
+  p[0].K = V; p[0].V = K;
+  p[0].initial = initial_state;
+  p[0].initial_t = 1;
+  p[0].s_out = sc;
+  p[0].o = group > 1 ? part[0] : dq;
+  p[0].o_f32 = group > 1;
   // dk_j = sum_{i >= j} gamma^{i-j} (v_j . d_o_i) scale q_i + ..: backwards over (v, d_o, q), the
   // state being dS^T
-  p = base;
-  p.q = v; p.k = d_o; p.v = q;
-  p.Hq = p.Hk = Hv;
-  p.Hv = Hqk;
-  p.K = V; p.V = K;
-  p.initial = d_final_state;
-  p.initial_t = 1;
-  p.s_in = sc;
-  p.reverse = 1;
-  p.o = group > 1 ? workspace : dk;
-  p.o_f32 = group > 1;
-  if ((err = run_pass(p)) != cudaSuccess) return GDN_ERR_CUDA;
-  if (group > 1 && gdn::launch_linear_attn_fold(reinterpret_cast<const float*>(workspace), dk, T_total,
-                                                Hqk, group, K, io_dtype, p.stream) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  p[1].q = v; p[1].k = d_o; p[1].v = q;
+  p[1].Hq = p[1].Hk = Hv;
+  p[1].Hv = Hqk;
+  p[1].K = V; p[1].V = K;
+  p[1].initial = d_final_state;
+  p[1].initial_t = 1;
+  p[1].s_in = sc;
+  p[1].reverse = 1;
+  p[1].o = group > 1 ? part[1] : dk;
+  p[1].o_f32 = group > 1;
   // dv_j = sum_{i >= j} gamma^{i-j} (k_j . q_i) scale d_o_i + ..: backwards over (k, q, d_o); its
   // state is dS, which ends as the gradient of the initial state
-  p = base;
-  p.q = k; p.k = q; p.v = d_o;
-  p.Hq = p.Hk = Hqk;
-  p.Hv = Hv;
-  p.K = K; p.V = V;
-  p.initial = d_final_state;
-  p.final_state = d_initial_state;
-  p.s_in = sc;
-  p.reverse = 1;
-  p.o = dv;
-  return run_pass(p) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  p[2].q = k; p[2].k = q; p[2].v = d_o;
+  p[2].Hq = p[2].Hk = Hqk;
+  p[2].Hv = Hv;
+  p[2].K = K; p[2].V = V;
+  p[2].initial = d_final_state;
+  p[2].final_state = d_initial_state;
+  p[2].s_in = sc;
+  p[2].reverse = 1;
+  p[2].o = dv;
+  if (run_passes(p, 3, ws.segs, workspace) != cudaSuccess) return GDN_ERR_CUDA;
+  if (group > 1) {
+    const float* const in[2] = {part[0], part[1]};
+    void* const out[2] = {dq, dk};
+    if (gdn::launch_linear_attn_fold(in, out, T_total, Hqk, group, K, io_dtype, base.stream) != cudaSuccess)
+      return GDN_ERR_CUDA;
+  }
+  return GDN_OK;
 }
 
 gdn_status_t gdn_linear_attn_decode(const void* q, const void* k, const void* v,

@@ -2,7 +2,7 @@
 // the tcgen05 tensor cores: bf16 I/O, any accepted head dims (padded to 64 or 128 by the TMA
 // loads' zero fill).
 //
-// One CTA per (sequence, head), chunks of 64 tokens in order.  Per chunk, with X the K x V state
+// One CTA per (sequence, head, segment), chunks of 64 tokens in order.  Per chunk, with X the K x V state
 // entering it and w_d = gamma^d (forward in time; the reverse pass mirrors the exponents, see
 // gdn_linear_attn.h):
 //
@@ -33,6 +33,12 @@
 // took 4050 cycles: a stage's life is a memory latency of 2300 plus its way through the roles).
 // P and the X operand are rounded to bf16 once, like the output itself.
 //
+// Where there are too few (sequence, head) chains to fill the GPU, each is cut into segments of
+// whole chunks: a first launch makes every segment's own contribution to the state (K, V and U
+// only), and in the second each segment starts from X = sum of the contributions before it, each
+// decayed over the tokens in between, and the given state.  Several passes (the backward's three)
+// run as one launch.
+//
 // Roles: warps 0-7 state (V~ of a chunk while U of the one before runs, then the update), warps
 // 8-11 output, warps 12-13 P, warp 14 issues the MMAs, warp 15 the loads.  (Two issuing warps,
 // one for U and O1 and one for D and O2, measured slower: 1.9 us a chunk instead of 1.5.)  They
@@ -40,6 +46,7 @@
 // leaves, TMEM is freed.
 #include <cuda.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstring>
 
@@ -70,7 +77,8 @@ constexpr uint32_t OFF_R = OFF_F + 2 * 16 * 24;           // float[64]: s_out R 
 constexpr uint32_t OFF_WP = OFF_R + 256;           // factors of P, see fill_p_table
 constexpr uint32_t kWpStride = 136;                // floats of one copy
 constexpr uint32_t OFF_G = OFF_WP + 4 * 4 * kWpStride;   // float2[2]: decay of a full / the partial chunk
-constexpr uint32_t OFF_BAR = OFF_G + 32;
+constexpr uint32_t OFF_SG = OFF_G + 32;            // float2[16]: decay over a whole earlier segment
+constexpr uint32_t OFF_BAR = OFF_SG + 8 * kLaMaxSegments;
 constexpr uint32_t SMEM_USED = OFF_BAR + 256;
 constexpr uint32_t SMEM_BYTES = SMEM_USED + 1024;   // slack for aligning the base
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
@@ -107,7 +115,12 @@ struct Unit {
   int h, bos, eos;       // the sequence
   int nch, c0, c1;       // its chunks, and the range (in order of processing) of this CTA
   const float* init;
-  float* fin;
+  float* fin;            // exit state, when the range ends the sequence
+  const float* local;    // this chain's scratch: the entry state, then the contributions of the
+                         // segments in order, [V 128][K 128] each
+  int before;            // segments before this one
+  float* store;          // where this segment's contribution goes (and nothing else is made), or NULL
+  float* copy;           // where the entry state is copied to first, or NULL
 };
 
 // A bounded wait, short: the roles' loops are fetched anew every chunk (five roles' code does not
@@ -214,11 +227,11 @@ __device__ void load_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint
     if (i >= kStages && !wait_bar(&bars[B_EMPTY + s], (uint32_t)(i / kStages - 1) & 1u)) return;
     const int t0 = chunk_at(p, u, c).t0;
     uint8_t* st = sm + s * kStage;
-    mbar_arrive_expect_tx(&bars[B_FULL + s], (uint32_t)(2 * kh + vh) * 8192u);
+    mbar_arrive_expect_tx(&bars[B_FULL + s], (uint32_t)((u.store ? 1 : 2) * kh + vh) * 8192u);
 #pragma unroll 1
     for (int x = 0; x < kh; ++x) {
       tma_load_3d(st + x * 16384 + 8192, tk, &bars[B_FULL + s], 64 * x, hk, t0);
-      tma_load_3d(st + x * 16384, tq, &bars[B_FULL + s], 64 * x, hq, t0);
+      if (!u.store) tma_load_3d(st + x * 16384, tq, &bars[B_FULL + s], 64 * x, hq, t0);
     }
 #pragma unroll 1
     for (int x = 0; x < vh; ++x)
@@ -261,6 +274,7 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
     const uint32_t so = (uint32_t)(i & (kStages - 1)) * kS16, par = (uint32_t)i & 1u;
     if (i >= 0) {   // U^T = V~^T K
       if (!wait_bar(&bars[B_V], par)) return false;
+      if (u.store && !wait_bar(&bars[B_FULL + (i & (kStages - 1))], (uint32_t)(i / kStages) & 1u)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int t = 0; t < terms; ++t) {
@@ -268,6 +282,11 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_ts(tbase + COL_U, a + 8 * ks, dKm + so + 128 * ks, idU, (uint32_t)(t | ks));
+      }
+      if (u.store) {
+        if (i + kStages < n) mma_commit(&bars[B_EMPTY + (i & (kStages - 1))]);
+        mma_commit(&bars[B_U]);
+        continue;
       }
       mma_commit(&bars[B_U]);
       // O^T = X^T Q^T + V^T P^T
@@ -288,7 +307,7 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
       for (int ks = 0; ks < 4; ++ks) mma_ss(o, dV + so + 128 * ks, dP + 2 * ks, idO2, 1);
       mma_commit(&bars[B_O + par]);
     }
-    if (i + 1 < n) {   // D = [Q; K] K^T of the next chunk
+    if (!u.store && i + 1 < n) {   // D = [Q; K] K^T of the next chunk
       const uint32_t s1 = (uint32_t)(i + 1) & (kStages - 1);
       if (!wait_bar(&bars[B_FULL + s1], (uint32_t)((i + 1) / kStages) & 1u)) return false;
       tc_fence_after();
@@ -447,6 +466,32 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
       src += 2 * step;
     }
   }
+  auto slot = [&](const float* base, int r) {   // this thread's 64 elements in slot r
+    return reinterpret_cast<float4*>(const_cast<float*>(base) + ((size_t)r * 128 + dv) * 128 + dk0);
+  };
+  auto put_slot = [&](float4* dst) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) dst[j] = make_float4(X[2 * j].x, X[2 * j].y, X[2 * j + 1].x, X[2 * j + 1].y);
+  };
+  if (u.copy) put_slot(slot(u.copy, 0));
+  if (u.store) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) X[j] = make_float2(0.f, 0.f);
+  } else if (u.local) {   // X <- X (hi + lo) + slot r
+    const float2* sg = reinterpret_cast<const float2*>(sm + OFF_SG);
+#pragma unroll 1
+    for (int r = 0; r <= u.before; ++r) {
+      const float4* src = slot(u.local, r);
+      const float2 gr = r > 0 ? sg[r - 1] : make_float2(0.f, 0.f);
+      const float2 hi = make_float2(gr.x, gr.x), lo = make_float2(gr.y, gr.y);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float4 x = __ldcg(src + j);
+        X[2 * j] = fma2(X[2 * j], hi, fma2(X[2 * j], lo, make_float2(x.x, x.y)));
+        X[2 * j + 1] = fma2(X[2 * j + 1], hi, fma2(X[2 * j + 1], lo, make_float2(x.z, x.w)));
+      }
+    }
+  }
   // the X operand of the next O1
   auto put_x = [&]() {
     if (mine) {
@@ -458,7 +503,7 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     tc_fence_before();
     warp_arrive(&bars[B_X], lane);
   };
-  put_x();
+  if (!u.store) put_x();
   // X <- X (hi + lo) + U of chunk i
   auto update = [&](int i) {
     if (mine) {
@@ -498,16 +543,20 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     tmem_wait_st();
     tc_fence_before();
     warp_arrive(&bars[B_V], lane);
-    if (i > 0) {
+    if (i > 0 && !u.store) {
       if (!wait_warp(&bars[B_XFREE], (uint32_t)(i - 1) & 1u)) return false;
       tc_fence_after();
       put_x();
     }
   }
-  if (u.fin) {
+  if (u.fin || u.store) {
     if (!wait_warp(&bars[B_U], (uint32_t)(n - 1) & 1u)) return false;
     tc_fence_after();
     update(n - 1);
+  }
+  if (u.store) {
+    put_slot(slot(u.store, 0));
+  } else if (u.fin) {
   }
   if (u.fin) {
     float* dst = u.fin + (size_t)dk0 * p.V + dv;
@@ -563,7 +612,36 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
     }
     tc_fence_after();
     if (leader) mbar_arrive(&bars[B_EMPTY + (i & (kStages - 1))]);   // (a chunk's last MMAs)
-    if (ch.L < kChunk || p.o_f32) {
+    if (ch.L == kChunk && p.o_f32) {
+      // fp32 rows: this lane's value feature of each token, 128 bytes a warp and store
+      const int dv = 32 * wq + lane;
+      float* dst = reinterpret_cast<float*>(p.o) + ((size_t)ch.t0 * p.H + u.h) * p.V + dv;
+      const size_t step = (size_t)p.H * p.V;
+      const float4* r4 = reinterpret_cast<const float4*>(sm + OFF_R);
+#pragma unroll 1
+      for (int t0 = 0; t0 < kChunk; t0 += 32) {
+        float x[32];
+        tmem_ld32(o + t0, x);
+        if (t0 > 0) {
+          tc_fence_before();
+          warp_arrive(&bars[B_OFREE + par], lane);
+        }
+        if (dv < p.V) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 r = r4[(t0 >> 2) + j];
+            dst[0] = r.x * x[4 * j];
+            dst[step] = r.y * x[4 * j + 1];
+            dst[2 * step] = r.z * x[4 * j + 2];
+            dst[3 * step] = r.w * x[4 * j + 3];
+            dst += 4 * step;
+          }
+        }
+        __syncwarp();
+      }
+      continue;
+    }
+    if (ch.L < kChunk) {
       store_rows(p, w, ch, o, u.h, 32 * wq + lane);
       tc_fence_before();
       warp_arrive(&bars[B_OFREE + par], lane);
@@ -608,38 +686,59 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
   return ok;
 }
 
-__global__ void __launch_bounds__(kThreads, 1)
-    linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                          const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                          const LinAttnPass p) {
+struct LaLaunch {
+  CUtensorMap map[kLaMaxPasses][4];   // q, k, v, o
+  LinAttnPass pass[kLaMaxPasses];
+  int segs;
+  int local_only;      // the first launch of a segmented run
+  float* local;        // [pass][n][h][segs][128][128]
+};
+
+__global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __grid_constant__ LaLaunch a) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
   volatile int* flag = reinterpret_cast<volatile int*>(sm + OFF_FLAG);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TSLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n = blockIdx.x / p.H;
   Unit u;
-  u.h = blockIdx.x % p.H;
-  const LaChain c = la_chain(p, n, u.h, tid == 0 && u.h == 0);
-  la_zero_rows(p, u.h, c.tail, p.cu_seqlens ? p.T : p.B * p.T, tid, kThreads);
-  if (c.skip) return;
-  if (c.padding) {
-    la_zero_rows(p, u.h, c.bos, c.eos, tid, kThreads);
-    return;
+  int e = blockIdx.x;   // heads vary fastest: those that share a row of q or k run side by side
+  u.h = e % a.pass[0].H;
+  e /= a.pass[0].H;
+  const int n = e % a.pass[0].num_seqs;
+  e /= a.pass[0].num_seqs;
+  const int segs = a.local_only ? a.segs - 1 : a.segs;
+  const int seg = e % segs, pi = e / segs;
+  const LinAttnPass p = a.pass[pi];
+  const LaChain c = la_chain(p, n, u.h, tid == 0 && u.h == 0 && seg == 0);
+  if (seg == 0 && !a.local_only) {
+    la_zero_rows(p, u.h, c.tail, p.cu_seqlens ? p.T : p.B * p.T, tid, kThreads);
+    if (c.padding) la_zero_rows(p, u.h, c.bos, c.eos, tid, kThreads);
   }
+  if (c.skip || c.padding) return;
   u.bos = c.bos;
   u.eos = c.eos;
   u.nch = (c.eos - c.bos + kChunk - 1) / kChunk;
-  u.c0 = 0;
-  u.c1 = u.nch;
-  u.init = c.init;
-  u.fin = c.fin;
-  if (u.nch == 0) {   // empty sequence: the state passes through
-    if (u.fin)
-      for (int e = tid; e < p.K * p.V; e += kThreads) {
-        const int kk = e / p.V, vv = e - kk * p.V;
-        u.fin[e] = u.init ? u.init[p.initial_t ? vv * p.K + kk : e] : 0.f;
+  const int per = max((u.nch + a.segs - 1) / a.segs, kLaMinSegmentChunks);
+  u.c0 = min(seg * per, u.nch);
+  u.c1 = min(u.c0 + per, u.nch);
+  const bool whole = seg == 0 && u.c1 == u.nch;   // (no other CTA works on this chain)
+  if (a.local_only && u.c1 == u.nch) return;       // (its contribution is nobody's entry state)
+  // The entry state comes from the scratch where another CTA of the second launch may be writing
+  // the exit state to the same place.
+  float* local = whole ? nullptr
+                       : a.local + ((size_t)(pi * p.num_seqs + n) * p.H + u.h) * (size_t)a.segs * 16384;
+  u.init = whole || (a.local_only && seg == 0) ? c.init : nullptr;
+  u.fin = a.local_only || u.c1 < u.nch ? nullptr : c.fin;
+  u.before = seg;
+  u.local = local;
+  u.store = a.local_only ? local + (size_t)(seg + 1) * 16384 : nullptr;
+  u.copy = a.local_only && seg == 0 ? local : nullptr;
+  if (u.c0 == u.c1) {
+    if (whole && u.fin)   // empty sequence: the state passes through
+      for (int x = tid; x < p.K * p.V; x += kThreads) {
+        const int kk = x / p.V, vv = x - kk * p.V;
+        u.fin[x] = u.init ? u.init[p.initial_t ? vv * p.K + kk : x] : 0.f;
       }
     return;
   }
@@ -660,6 +759,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int L = warp == 4 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
     reinterpret_cast<float2*>(sm + OFF_G)[warp - 4] = decay_pow2(ld, L);
   }
+  if (!a.local_only && tid >= 256 && tid < 256 + u.before) {   // (backwards the first segment holds the partial chunk)
+    const int r = tid - 256, last = c.eos - c.bos - (u.nch - 1) * kChunk;
+    reinterpret_cast<float2*>(sm + OFF_SG)[r] =
+        decay_pow2(ld, per * kChunk - (p.reverse && r == 0 ? kChunk - last : 0));
+  }
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       const int count = (i == B_V || i == B_X) ? kStateWarps
@@ -677,20 +781,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  const int terms = p.final_state ? 4 : 2;
+  // a segment's contribution may end in a final state; the passes from it to there add nothing
+  const int terms = u.fin || (u.store && p.final_state) ? 4 : 2;
 
   bool ok = true;
   if (warp < kStateWarps) {
     ok = terms == 4 ? state_role<4>(p, u, sm, tbase, bars) : state_role<2>(p, u, sm, tbase, bars);
   } else if (warp < kStateWarps + kOutWarps) {
-    ok = out_role(p, u, sm, tbase, bars, terms, &tmO);
+    if (!u.store) ok = out_role(p, u, sm, tbase, bars, terms, &a.map[pi][3]);
   } else if (warp < kMmaWarp) {
-    ok = p_role(p, u, sm, tbase, bars);
+    if (!u.store) ok = p_role(p, u, sm, tbase, bars);
   } else if (warp == kMmaWarp) {
     if (elect_one()) ok = mma_role(p, u, smem_u32(sm), tbase, bars, terms);
     __syncwarp();
   } else {
-    if (lane == 0) load_role(p, u, sm, bars, &tmQ, &tmK, &tmV);
+    if (lane == 0) load_role(p, u, sm, bars, &a.map[pi][0], &a.map[pi][1], &a.map[pi][2]);
     __syncwarp();
   }
   if (!ok) *flag = 1;
@@ -708,21 +813,35 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_linear_attn_tc(const LinAttnPass& p) {
-  const long long blocks = (long long)p.num_seqs * p.H;
-  if (blocks <= 0) return cudaSuccess;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const int T_total = p.cu_seqlens ? p.T : p.B * p.T;
-  CUtensorMap mq, mk, mv, mo;
-  memset(&mq, 0, sizeof(mq));
-  memset(&mk, 0, sizeof(mk));
-  memset(&mv, 0, sizeof(mv));
-  memset(&mo, 0, sizeof(mo));
-  if (T_total > 0) {   // fp32 rows are stored without a map
-    if (!encode_rows_map_bf16(&mq, p.q, p.Hq, T_total, p.K) ||
-        !encode_rows_map_bf16(&mk, p.k, p.Hk, T_total, p.K) ||
-        !encode_rows_map_bf16(&mv, p.v, p.Hv, T_total, p.V) ||
-        (!p.o_f32 && !encode_rows_map_bf16(&mo, p.o, p.H, T_total, p.V)))
+int linear_attn_tc_segments(int num_passes, int num_seqs, int H, long long most_tokens, int num_sms) {
+  const long long chains = (long long)num_passes * num_seqs * H;
+  if (chains <= 0 || num_sms <= 0) return 1;
+  const long long chunks = (most_tokens + kChunk - 1) / kChunk;
+  return (int)std::max(1LL, std::min({(long long)kLaMaxSegments, num_sms / chains, chunks / kLaMinSegmentChunks}));
+}
+
+size_t linear_attn_tc_workspace_bytes(int num_passes, int num_seqs, int H, int segs) {
+  return (size_t)num_passes * num_seqs * H * (segs > 1 ? segs : 0) * 16384 * sizeof(float);
+}
+
+cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* local) {
+  const LinAttnPass& p0 = passes[0];
+  const long long chains = (long long)num_passes * p0.num_seqs * p0.H;
+  if (chains <= 0) return cudaSuccess;
+  if (num_passes > kLaMaxPasses || segs < 1 || segs > kLaMaxSegments || chains * segs > 0x7fffffffLL)
+    return cudaErrorInvalidConfiguration;
+  const int T_total = p0.cu_seqlens ? p0.T : p0.B * p0.T;
+  LaLaunch a;
+  memset(&a, 0, sizeof(a));
+  a.segs = segs;
+  a.local = local;
+  for (int i = 0; i < num_passes; ++i) {
+    const LinAttnPass& p = a.pass[i] = passes[i];
+    if (T_total > 0 &&   // (fp32 rows are stored without a map)
+        (!encode_rows_map_bf16(&a.map[i][0], p.q, p.Hq, T_total, p.K) ||
+         !encode_rows_map_bf16(&a.map[i][1], p.k, p.Hk, T_total, p.K) ||
+         !encode_rows_map_bf16(&a.map[i][2], p.v, p.Hv, T_total, p.V) ||
+         (!p.o_f32 && !encode_rows_map_bf16(&a.map[i][3], p.o, p.H, T_total, p.V))))
       return cudaErrorInvalidValue;
   }
   static std::atomic<bool> attr_set[64];
@@ -735,7 +854,13 @@ cudaError_t launch_linear_attn_tc(const LinAttnPass& p) {
     if (err != cudaSuccess) return err;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  linear_attn_tc_kernel<<<(unsigned)blocks, kThreads, SMEM_BYTES, p.stream>>>(mq, mk, mv, mo, p);
+  if (segs > 1) {
+    a.local_only = 1;
+    linear_attn_tc_kernel<<<(unsigned)(chains * (segs - 1)), kThreads, SMEM_BYTES, p0.stream>>>(a);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    a.local_only = 0;
+  }
+  linear_attn_tc_kernel<<<(unsigned)(chains * segs), kThreads, SMEM_BYTES, p0.stream>>>(a);
   return cudaGetLastError();
 }
 
