@@ -4,8 +4,10 @@
 //   xhat = (x - mean) rstd,  u = xhat w + b,  y = act(u), or u act(z) with a gate z.
 //
 // Bound by bytes: x (and z) read once, y written once is the floor.  Two forms:
-//   L = 1 and groups of up to 1024 channels: a group lives in the registers of up to 32 lanes,
-//     which read it once, take mean and variance over two register passes and write it.
+//   single positions (and small slabs) with groups of up to 1024 values: a group lives in the
+//     registers of up to 32 lanes, which read it once, the next one being on its way meanwhile,
+//     take mean and variance over two register passes and write it; each lane keeps its channels'
+//     weights.
 //   else: a launch for each slab's mean and squared deviations (merged pairwise from batches of
 //     registers, never as E[x^2] - E[x]^2), and one that merges the slabs' and applies; the second
 //     reading of x comes from L2 where the tensor fits it.
@@ -14,130 +16,149 @@
 namespace gdn {
 namespace {
 
-// ------------------------------------------------------------------ L = 1, groups in registers
+// ------------------------------------------------------------------ groups in registers
+constexpr int kRowSteps = 4;
+
 template <typename T, int V, int VPT, bool kGate>
-__global__ void __launch_bounds__(kGnThreads) gn_row_fwd_kernel(const GroupNormArgs a, int lanes) {
-  const int D = a.C / a.G, DV = D / V;
-  const int l = threadIdx.x & (lanes - 1);
-  const long long items = (long long)a.N * a.G, per = (long long)gridDim.x * (kGnThreads / lanes);
-  const float inv = 1.f / (float)D;
+__global__ void __launch_bounds__(kGnThreads) gn_row_fwd_kernel(const GroupNormArgs a, const RowPlan q) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kIn = kGate ? 2 : 1;
+  Ring<T, V, VPT * kIn, kRowSteps> ring(smem);
+  const RowPlace p = row_place(q, a.G);
+  const RowVectors<V, VPT> at(q, p, a.L, a.C, a.G);
+  const float inv = 1.f / ((float)a.L * (float)(a.C / a.G));
+  float w[VPT][V], b[VPT][V];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      w[k][j] = at.in[k] ? param(a.weight, at.c[k] + j, a.wb_dtype, 1.f) : 0.f;
+      b[k][j] = at.in[k] ? param(a.bias, at.c[k] + j, a.wb_dtype, 0.f) : 0.f;
+    }
+  const size_t row = (size_t)a.L * a.C, col = (size_t)p.g * (a.C / a.G);
+  const long long step = (long long)q.sets * q.down;
+  long long n = (long long)p.set * q.down + p.down;
+  auto load = [&](int ahead) {
+    const long long m = n + ahead * step;
+    if (m < a.N) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+        if (at.in[k]) {
+          ring.put(ahead, kIn * k, a.x, m * row + col + at.off[k]);
+          if (kGate) ring.put(ahead, kIn * k + kIn - 1, a.gate, m * row + col + at.off[k]);
+        }
+    }
+    ring.commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kRowSteps - 1; ++i) load(i);
   // (every lane of a warp runs the same number of turns: the shuffles want them all)
-  const long long first = (long long)blockIdx.x * (kGnThreads / lanes) + threadIdx.x / lanes;
-  const long long warp_first = first - (threadIdx.x & 31) / lanes;
-  for (long long base = 0; warp_first + base < items; base += per) {
-    const long long item = first + base;
-    const bool on = item < items;
-    const int g = (int)((on ? item : 0) % a.G);
-    const size_t at = (size_t)(on ? item : 0) * D;
-    float x[VPT][V], z[VPT][V];
+  const int turns = (int)((a.N + step - 1) / step);
+  for (int t = 0; t < turns; ++t, n += step, ring.next()) {
+    load(kRowSteps - 1);
+    ring.wait();
+    float v[VPT][V];
+    // mean from the first element, then the squared deviations
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v = l + k * lanes;
-      const bool in = on && v < DV;
-      const Pack<T, V> p = in ? load_pack<T, V>(a.x, at + (size_t)v * V) : Pack<T, V>{};
-      const Pack<T, V> q = kGate && in ? load_pack<T, V>(a.gate, at + (size_t)v * V) : Pack<T, V>{};
+      const Pack<T, V> x = ring.get(kIn * k);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        x[k][j] = to_f(p.e[j]);
-        if (kGate) z[k][j] = to_f(q.e[j]);
-      }
+      for (int j = 0; j < V; ++j) v[k][j] = to_f(x.e[j]);
     }
-    // mean from the first element, then the squared deviations
-    const float x0 = __shfl_sync(0xffffffffu, x[0][0], 0, lanes);
+    const float x0 = __shfl_sync(0xffffffffu, v[0][0], 0, q.lanes);
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
-      if (l + k * lanes < DV) {
+      if (at.in[k]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) s += x[k][j] - x0;
+        for (int j = 0; j < V; ++j) s += v[k][j] - x0;
       }
-    const float mean = x0 + sub_sum(s, lanes) * inv;
+    const float mean = x0 + sub_sum(s, q.lanes) * inv;
     s = 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
-      if (l + k * lanes < DV) {
+      if (at.in[k]) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float d = x[k][j] - mean;
-          s = fmaf(d, d, s);
+          v[k][j] -= mean;
+          s = fmaf(v[k][j], v[k][j], s);
         }
       }
-    const float rstd = rsqrtf(fmaf(sub_sum(s, lanes), inv, a.eps));
-    if (!on) continue;
-    if (l == 0) {
-      if (a.mean) a.mean[item] = mean;
-      if (a.rstd) a.rstd[item] = rstd;
+    const float rstd = rsqrtf(fmaf(sub_sum(s, q.lanes), inv, a.eps));
+    if (n >= a.N || !p.live) continue;
+    if (p.l == 0) {
+      if (a.mean) a.mean[n * a.G + p.g] = mean;
+      if (a.rstd) a.rstd[n * a.G + p.g] = rstd;
     }
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int v = l + k * lanes;
-      if (v >= DV) continue;
-      Pack<T, V> o;
+    for (int k = 0; k < VPT; ++k)
+      if (at.in[k]) {
+        Pack<T, V> y;
+        if (kGate) y = ring.get(kIn * k + kIn - 1);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c = g * D + v * V + j;
-        const float u = fmaf((x[k][j] - mean) * rstd, param(a.weight, c, a.wb_dtype, 1.f),
-                             param(a.bias, c, a.wb_dtype, 0.f));
-        from_f(o.e[j], kGate ? u * act_value(z[k][j], a.act) : act_value(u, a.act));
+        for (int j = 0; j < V; ++j) {
+          const float u = fmaf(v[k][j] * rstd, w[k][j], b[k][j]);
+          from_f(y.e[j], kGate ? u * act_value(to_f(y.e[j]), a.act) : act_value(u, a.act));
+        }
+        store_pack<T, V>(a.y, n * row + col + at.off[k], y);
       }
-      store_pack<T, V>(a.y, at + (size_t)v * V, o);
-    }
   }
 }
 
 // ------------------------------------------------------------------ slabs
-// Mean and squared deviations of `n` values merged with those of `m` more.
+// Mean and squared deviations of values; merged with those of n more (a.n = 0: taken over).
 struct Moments {
   float n, mean, m2;
 };
 __device__ __forceinline__ void merge(Moments& a, float n, float mean, float m2) {
-  const float t = a.n + n, d = mean - a.mean, f = n / t;
+  const float t = a.n + n, d = mean - a.mean, f = __fdividef(n, t);
   a.mean = fmaf(d, f, a.mean);
   a.m2 += m2 + d * d * a.n * f;
   a.n = t;
 }
 
+// Rows of a thread's column in its ring: about 32 KB a CTA.
+template <int kPacks>
+constexpr int slab_steps = kPacks == 1 ? 8 : 4;
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kGnThreads) gn_slab_stats_kernel(const GroupNormArgs a, const SlabPlan s,
                                                                    float2* part) {
   __shared__ float sn[kGnThreads], sm[kGnThreads], sq[kGnThreads];
+  extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
   const int2 rr = slab_rows(s, p, a.L);
   Moments mo{0.f, 0.f, 0.f};
   if (p.on) {
+    constexpr int kSlabSteps = slab_steps<1>;
+    Ring<T, V, 1, kSlabSteps> ring(smem);
     const size_t base = (size_t)p.n * a.L * a.C + p.c;
-    for (int r = rr.x + p.row; r < rr.y; r += 4 * p.step) {
-      Pack<T, V> v[4];
-      float x[4][V];
-      const int k = min(4, (rr.y - r + p.step - 1) / p.step);
+    int r = rr.x + p.row;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < k) v[i] = load_pack<T, V>(a.x, base + (size_t)(r + i * p.step) * a.C);
+    for (int i = 0; i < kSlabSteps - 1; ++i) {
+      if (r + i * p.step < rr.y) ring.put(i, 0, a.x, base + (size_t)(r + i * p.step) * a.C);
+      ring.commit();
+    }
+    for (; r < rr.y; r += p.step, ring.next()) {
+      const int ahead = r + (kSlabSteps - 1) * p.step;
+      if (ahead < rr.y) ring.put(kSlabSteps - 1, 0, a.x, base + (size_t)ahead * a.C);
+      ring.commit();
+      ring.wait();
+      const Pack<T, V> x = ring.get(0);
+      float v[V], t = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[i][j] = i < k ? to_f(v[i].e[j]) : 0.f;
-      const float x0 = x[0][0], n = (float)(k * V);
-      float t = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < k) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) t += x[i][j] - x0;
-        }
-      const float mean = x0 + t / n;
+      for (int j = 0; j < V; ++j) {
+        v[j] = to_f(x.e[j]);
+        t += v[j];
+      }
+      const float mean = t * (1.f / V);   // (V is a power of two)
       t = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < k) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float d = x[i][j] - mean;
-            t = fmaf(d, d, t);
-          }
-        }
-      if (mo.n == 0.f) mo = Moments{n, mean, t};
-      else merge(mo, n, mean, t);
+      for (int j = 0; j < V; ++j) {
+        const float d = v[j] - mean;
+        t = fmaf(d, d, t);
+      }
+      merge(mo, (float)V, mean, t);
     }
   }
   sn[threadIdx.x] = mo.n;
@@ -187,6 +208,7 @@ template <typename T, int V, bool kGate>
 __global__ void __launch_bounds__(kGnThreads) gn_slab_fwd_kernel(const GroupNormArgs a, const SlabPlan s,
                                                                  const float2* part) {
   __shared__ float2 stats[kGnThreads];   // mean, rstd of the column block's groups
+  extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
   const int lane = threadIdx.x & 31, Q = s.chunks * s.parts;
   const float count = (float)a.L * (float)(a.C / a.G);
@@ -222,60 +244,75 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_fwd_kernel(const GroupNorm
     b[j] = param(a.bias, p.c + j, a.wb_dtype, 0.f);
   }
   const size_t base = (size_t)p.n * a.L * a.C + p.c;
-  for (int r = rr.x + p.row; r < rr.y; r += 4 * p.step) {
-    Pack<T, V> v[4], z[4];
-    const int k = min(4, (rr.y - r + p.step - 1) / p.step);
+  constexpr int kIn = kGate ? 2 : 1, kSlabSteps = slab_steps<kIn>;
+  Ring<T, V, kIn, kSlabSteps> ring(smem);
+  int r = rr.x + p.row;
+  auto load = [&](int i) {
+    const int m = r + i * p.step;
+    if (m < rr.y) {
+      ring.put(i, 0, a.x, base + (size_t)m * a.C);
+      if (kGate) ring.put(i, kIn - 1, a.gate, base + (size_t)m * a.C);
+    }
+    ring.commit();
+  };
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < k) {
-        v[i] = load_pack<T, V>(a.x, base + (size_t)(r + i * p.step) * a.C);
-        if (kGate) z[i] = load_pack<T, V>(a.gate, base + (size_t)(r + i * p.step) * a.C);
-      }
+  for (int i = 0; i < kSlabSteps - 1; ++i) load(i);
+  for (; r < rr.y; r += p.step, ring.next()) {
+    load(kSlabSteps - 1);
+    ring.wait();
+    const Pack<T, V> x = ring.get(0);
+    Pack<T, V> y;
+    if (kGate) y = ring.get(kIn - 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < k) {
-        Pack<T, V> o;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float u = fmaf((to_f(v[i].e[j]) - st.x) * st.y, w[j], b[j]);
-          from_f(o.e[j], kGate ? u * act_value(to_f(z[i].e[j]), a.act) : act_value(u, a.act));
-        }
-        store_pack<T, V>(a.y, base + (size_t)(r + i * p.step) * a.C, o);
-      }
+    for (int j = 0; j < V; ++j) {
+      const float u = fmaf((to_f(x.e[j]) - st.x) * st.y, w[j], b[j]);
+      from_f(y.e[j], kGate ? u * act_value(to_f(y.e[j]), a.act) : act_value(u, a.act));
+    }
+    store_pack<T, V>(a.y, base + (size_t)r * a.C, y);
   }
 }
 
 constexpr int kRowValues = 32;   // values a lane holds in the row form
+constexpr int kRowPerSm = 5;     // its CTAs an SM (registers)
+
+template <typename T, int V, int VPT, bool kGate>
+cudaError_t launch_row_fwd(const GroupNormArgs& a, const RowPlan& r) {
+  constexpr int kShared = Ring<T, V, VPT * (kGate ? 2 : 1), kRowSteps>::kShared;
+  const cudaError_t err = allow_shared<gn_row_fwd_kernel<T, V, VPT, kGate>, kShared>();
+  if (err != cudaSuccess) return err;
+  gn_row_fwd_kernel<T, V, VPT, kGate><<<(unsigned)(r.sets * r.across), kGnThreads, kShared, a.stream>>>(a, r);
+  return cudaGetLastError();
+}
 
 template <typename T, int V, bool kGate>
-void launch_fwd(const GroupNormArgs& a) {
-  const RowPlan r = row_plan(a.C, a.G, a.io_dtype, kRowValues);
-  if (a.L == 1 && r.lanes > 0) {
-    const long long ctas = ((long long)a.N * a.G * r.lanes + kGnThreads - 1) / kGnThreads;
-    const unsigned grid = (unsigned)(ctas < 152 * 32 ? ctas : 152 * 32);
-    if (r.VPT == 1) gn_row_fwd_kernel<T, V, 1, kGate><<<grid, kGnThreads, 0, a.stream>>>(a, r.lanes);
-    else if (r.VPT <= kRowValues / V / 2)
-      gn_row_fwd_kernel<T, V, (kRowValues / V / 2), kGate><<<grid, kGnThreads, 0, a.stream>>>(a, r.lanes);
-    else gn_row_fwd_kernel<T, V, kRowValues / V, kGate><<<grid, kGnThreads, 0, a.stream>>>(a, r.lanes);
-    return;
+cudaError_t launch_fwd(const GroupNormArgs& a) {
+  const RowPlan r = row_plan(a.N, a.L, a.C, a.G, a.io_dtype, kRowValues, kRowPerSm);
+  if (r.lanes > 0) {
+    if (r.VPT == 1) return launch_row_fwd<T, V, 1, kGate>(a, r);
+    if (r.VPT <= kRowValues / V / 2) return launch_row_fwd<T, V, kRowValues / V / 2, kGate>(a, r);
+    return launch_row_fwd<T, V, kRowValues / V, kGate>(a, r);
   }
   const SlabPlan s = slab_plan(a.N, a.L, a.C, a.G, a.io_dtype);
   const unsigned grid = (unsigned)((long long)a.N * s.NCB * s.chunks);
   float2* part = reinterpret_cast<float2*>(a.workspace);
-  gn_slab_stats_kernel<T, V><<<grid, kGnThreads, 0, a.stream>>>(a, s, part);
-  gn_slab_fwd_kernel<T, V, kGate><<<grid, kGnThreads, 0, a.stream>>>(a, s, part);
+  constexpr int kStats = Ring<T, V, 1, slab_steps<1>>::kShared;
+  constexpr int kApply = Ring<T, V, kGate ? 2 : 1, slab_steps<kGate ? 2 : 1>>::kShared;
+  const cudaError_t err = allow_shared<gn_slab_fwd_kernel<T, V, kGate>, kApply>();
+  if (err != cudaSuccess) return err;
+  gn_slab_stats_kernel<T, V><<<grid, kGnThreads, kStats, a.stream>>>(a, s, part);
+  gn_slab_fwd_kernel<T, V, kGate><<<grid, kGnThreads, kApply, a.stream>>>(a, s, part);
+  return cudaGetLastError();
 }
 
 template <typename T, int V>
-void launch_fwd(const GroupNormArgs& a) {
-  if (a.gate) launch_fwd<T, V, true>(a);
-  else launch_fwd<T, V, false>(a);
+cudaError_t launch_fwd(const GroupNormArgs& a) {
+  return a.gate ? launch_fwd<T, V, true>(a) : launch_fwd<T, V, false>(a);
 }
 
 }  // namespace
 
 size_t group_norm_fwd_workspace_bytes(int N, int L, int C, int G, int io_dtype) {
-  if (N == 0 || L == 0 || (L == 1 && row_plan(C, G, io_dtype, kRowValues).lanes > 0)) return 0;
+  if (N == 0 || L == 0 || row_plan(N, L, C, G, io_dtype, kRowValues, kRowPerSm).lanes > 0) return 0;
   const SlabPlan s = slab_plan(N, L, C, G, io_dtype);
   return (size_t)N * G * s.chunks * s.parts * sizeof(float2);
 }
@@ -285,19 +322,17 @@ cudaError_t launch_group_norm_fwd(const GroupNormArgs& a) {
   if ((long long)a.N * s.NCB * s.chunks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (a.io_dtype == GDN_F32) {
     switch (s.V) {
-      case 4: launch_fwd<float, 4>(a); break;
-      case 2: launch_fwd<float, 2>(a); break;
-      default: launch_fwd<float, 1>(a);
-    }
-  } else {
-    switch (s.V) {
-      case 8: launch_fwd<__nv_bfloat16, 8>(a); break;
-      case 4: launch_fwd<__nv_bfloat16, 4>(a); break;
-      case 2: launch_fwd<__nv_bfloat16, 2>(a); break;
-      default: launch_fwd<__nv_bfloat16, 1>(a);
+      case 4: return launch_fwd<float, 4>(a);
+      case 2: return launch_fwd<float, 2>(a);
+      default: return launch_fwd<float, 1>(a);
     }
   }
-  return cudaGetLastError();
+  switch (s.V) {
+    case 8: return launch_fwd<__nv_bfloat16, 8>(a);
+    case 4: return launch_fwd<__nv_bfloat16, 4>(a);
+    case 2: return launch_fwd<__nv_bfloat16, 2>(a);
+    default: return launch_fwd<__nv_bfloat16, 1>(a);
+  }
 }
 
 }  // namespace gdn

@@ -3,6 +3,9 @@
 
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_group_norm.h"
@@ -40,6 +43,42 @@ __device__ __forceinline__ void store_pack(void* base, size_t at, const Pack<T, 
   using R = typename Raw<V * sizeof(T)>::type;
   *reinterpret_cast<R*>(reinterpret_cast<T*>(base) + at) = *reinterpret_cast<const R*>(&p);
 }
+
+// A thread's own ring of packs in shared memory, filled by asynchronous copies (no registers and
+// no other thread involved: only its own group count is waited for).  kPacks packs a step, kSteps
+// steps deep, of which kSteps - 1 are on their way while one is used.  2-byte packs, which such
+// copies do not move, are copied at once.
+template <typename T, int V, int kPacks, int kSteps>
+struct Ring {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  static constexpr int kShared = kSteps * kPacks * kBytes * kGnThreads;
+  uint8_t* mine;
+  int at = 0;   // the step that `get` reads and the next `put` ends up behind
+  __device__ __forceinline__ explicit Ring(void* smem) : mine(reinterpret_cast<uint8_t*>(smem) + threadIdx.x * kBytes) {}
+  __device__ __forceinline__ uint8_t* slot(int step, int i) const {
+    return mine + (step * kPacks + i) * kBytes * kGnThreads;
+  }
+  // Pack i of a step that is `ahead` steps behind the one read now.
+  __device__ __forceinline__ void put(int ahead, int i, const void* base, size_t elem) {
+    int st = at + ahead;
+    if (st >= kSteps) st -= kSteps;
+    const T* src = reinterpret_cast<const T*>(base) + elem;
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot(st, i));
+    if (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else if (kBytes >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes < 4 ? 4 : kBytes) : "memory");
+    else *reinterpret_cast<Pack<T, V>*>(slot(st, i)) = load_pack<T, V>(base, elem);
+  }
+  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+  // Waits for the step to be read (all but the kSteps - 1 newest groups).
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 1) : "memory"); }
+  __device__ __forceinline__ Pack<T, V> get(int i) const {
+    Pack<T, V> p;
+    using R = typename Raw<kBytes>::type;
+    *reinterpret_cast<R*>(&p) = *reinterpret_cast<const R*>(slot(at, i));
+    return p;
+  }
+  __device__ __forceinline__ void next() { at = at + 1 == kSteps ? 0 : at + 1; }
+};
 
 // weight (default 1) or bias (default 0) of channel c.
 __device__ __forceinline__ float param(const void* p, int c, int dtype, float none) {
@@ -91,8 +130,8 @@ inline SlabPlan slab_plan(int N, int L, int C, int G, int io_dtype) {
   }
   const int cols = s.parts == 1 ? s.GPB * s.DV : kGnThreads;
   const int step = kGnThreads / cols;               // rows that a CTA takes at a time
-  // about four CTAs an SM, each thread at least four rows
-  const long long want = 152LL * 4 / ((long long)N * s.NCB) + 1;
+  // one wave of five CTAs an SM, each thread at least four rows
+  const long long want = std::max(1LL, 152LL * 5 / ((long long)N * s.NCB));
   const long long most = (L + 4LL * step - 1) / (4LL * step);
   const long long chunks = want < most ? want : most;
   s.rows = (int)((L + chunks - 1) / chunks);
@@ -143,22 +182,80 @@ __device__ __forceinline__ int2 slab_rows(const SlabPlan& s, const SlabPlace& p,
   return make_int2(p.chunk * s.rows, min(L, (p.chunk + 1) * s.rows));
 }
 
-// Groups that a warp (or part of one) holds in registers, for L = 1: lanes a group (a power of
-// two), vectors a lane; 0 lanes where the group is too wide.
+// Groups that up to 32 lanes hold in registers: lanes a group (a power of two), vectors a lane
+// (the group's L DV vectors in order); 0 lanes where that does not serve.
 struct RowPlan {
   int V, lanes, VPT;
+  // A CTA's J lane groups take all G channel groups of `down` rows n at a time, or, where J < G, J
+  // channel groups of one row; then the CTA's next rows.  What a CTA sums over its rows is a set.
+  int J, across, down, sets;   // lane groups; CTAs across the groups; rows at a time; sets
 };
-inline RowPlan row_plan(int C, int G, int io_dtype, int most_values) {
-  RowPlan r{vector_width(C / G, io_dtype == GDN_BF16 ? 8 : 4), 0, 1};
-  const int DV = C / G / r.V;
+// It serves groups of up to `most` values a lane, for one position, or for slabs so small that a
+// CTA of the slab form would stand mostly idle on one.
+inline RowPlan row_plan(int N, int L, int C, int G, int io_dtype, int most, int per_sm) {
+  RowPlan r{vector_width(C / G, io_dtype == GDN_BF16 ? 8 : 4), 0, 1, 0, 0, 0, 0};
+  if (L > 1 && (long long)L * C > 8192) return r;
+  const long long vecs = (long long)L * (C / G / r.V);
   int lanes = 1;
-  while (lanes < 32 && lanes < DV) lanes *= 2;
-  const int vpt = (DV + lanes - 1) / lanes;
-  if (vpt * r.V <= most_values) {
-    r.lanes = lanes;
-    r.VPT = vpt;
-  }
+  while (lanes < 32 && lanes < vecs) lanes *= 2;
+  if ((vecs + lanes - 1) / lanes * r.V > most) return r;
+  r.lanes = lanes;
+  r.VPT = (int)((vecs + lanes - 1) / lanes);
+  r.J = kGnThreads / lanes;
+  r.across = r.J >= G ? 1 : (G + r.J - 1) / r.J;
+  r.down = r.J >= G ? r.J / G : 1;
+  // one wave of `per_sm` CTAs an SM, and no more than the rows need
+  const long long need = ((long long)N + r.down - 1) / r.down, want = std::max(1, 152 * per_sm / r.across);
+  r.sets = (int)std::min(need, want);
   return r;
+}
+
+// A thread's place in the row form.
+struct RowPlace {
+  int l, set, down, g;
+  bool live;
+};
+__device__ __forceinline__ RowPlace row_place(const RowPlan& q, int G) {
+  RowPlace p;
+  const int j = threadIdx.x / q.lanes;
+  p.l = threadIdx.x & (q.lanes - 1);
+  p.set = blockIdx.x / q.across;
+  p.g = q.across == 1 ? j % G : (blockIdx.x % q.across) * q.J + j;
+  p.down = q.across == 1 ? j / G : 0;
+  p.live = p.g < G && p.down < q.down;
+  if (!p.live) p.g = 0;
+  return p;
+}
+// Where this lane's vectors stand in a group (from its first element), their channels, and whether
+// they are in it.
+template <int V, int VPT>
+struct RowVectors {
+  int off[VPT], c[VPT];
+  bool in[VPT];
+  __device__ __forceinline__ RowVectors(const RowPlan& q, const RowPlace& p, int L, int C, int G) {
+    const int D = C / G, DV = D / V;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int v = p.l + k * q.lanes, r = v / DV, e = (v - r * DV) * V;
+      in[k] = p.live && r < L;
+      off[k] = r * C + e;
+      c[k] = p.g * D + e;
+    }
+  }
+};
+
+// Lets a kernel have kBytes of dynamic shared memory beside its static arrays of up to 8 KB (set
+// once a device and kernel).
+template <auto kKernel, int kBytes>
+cudaError_t allow_shared() {
+  if (kBytes <= 40 * 1024) return cudaSuccess;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed))) return err;
+  err = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (err == cudaSuccess && dev < 64) done[dev].store(true, std::memory_order_relaxed);
+  return err;
 }
 
 __device__ __forceinline__ float sub_sum(float x, int lanes) {

@@ -7,8 +7,9 @@
 // A thread keeps its channels and sums du and du xhat for each of them (A, B): those are its share
 // of db and dw, and sum_c w_c A_c, sum_c w_c B_c its share of m1 and m2.  Every sum is made in a
 // fixed order.  Bound by bytes: x, dy (and z) read once, dx (and dz) written once is the floor.
-//   L = 1 and groups of up to 512 channels: one launch reads each row once, its groups in
-//     registers, and leaves A, B of each set of rows; a second adds the sets.
+//   single positions (and small slabs) with groups of up to 512 values: one launch reads each row
+//     once, its groups in registers, the next row being on its way, and leaves A, B of each set of
+//     rows; a second adds the sets.
 //   else: a launch for A, B and the slab's share of m1, m2, a second that reads x, dy (and z) again
 //     and applies, its last CTAs adding A, B up.
 #include "gdn_group_norm.cuh"
@@ -61,62 +62,74 @@ __global__ void __launch_bounds__(1024) gn_sum_sets_kernel(const GroupNormArgs a
   sum_sets<32>(a, part, sets, blockIdx.x);
 }
 
-// ------------------------------------------------------------------ L = 1, groups in registers
-// A CTA's J lane groups take all G channel groups of J / G rows at a time, or, where J < G, J
-// channel groups of one row; then the CTA's next rows.  A, B of the CTA's rows are one set.
-struct RowSets {
-  int J, across, down, sets;   // lane groups; CTAs across the groups; rows at a time; sets
-};
+// ------------------------------------------------------------------ groups in registers
+constexpr int kRowSteps = 3;
 
 template <typename T, int V, int VPT, bool kGate>
-__global__ void __launch_bounds__(kGnThreads) gn_row_bwd_kernel(const GroupNormArgs a, int lanes, const RowSets q,
-                                                                float* part) {
-  __shared__ float acc[2][kGnThreads * 16];
-  const int D = a.C / a.G, DV = D / V;
-  const int l = threadIdx.x & (lanes - 1), j0 = threadIdx.x / lanes;
-  const int set = blockIdx.x / q.across;
-  const int g_raw = q.across == 1 ? j0 % a.G : (blockIdx.x % q.across) * q.J + j0;
-  const int down = q.across == 1 ? j0 / a.G : 0;
-  const bool live = g_raw < a.G && down < q.down;
-  const int g = live ? g_raw : 0;
-  const float inv = 1.f / (float)D;
+__global__ void __launch_bounds__(kGnThreads) gn_row_bwd_kernel(const GroupNormArgs a, const RowPlan q, float* part) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kIn = kGate ? 3 : 2;
+  Ring<T, V, VPT * kIn, kRowSteps> ring(smem);
+  const RowPlace p = row_place(q, a.G);
+  const RowVectors<V, VPT> at(q, p, a.L, a.C, a.G);
+  const int D = a.C / a.G;
+  const float inv = 1.f / ((float)a.L * (float)D);
   float w[VPT][V], b[VPT][V], A[VPT][V], B[VPT][V];
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int v = l + k * lanes, c = g * D + v * V + j;
-      w[k][j] = v < DV ? param(a.weight, c, a.wb_dtype, 1.f) : 0.f;
-      b[k][j] = v < DV ? param(a.bias, c, a.wb_dtype, 0.f) : 0.f;
+      w[k][j] = at.in[k] ? param(a.weight, at.c[k] + j, a.wb_dtype, 1.f) : 0.f;
+      b[k][j] = at.in[k] ? param(a.bias, at.c[k] + j, a.wb_dtype, 0.f) : 0.f;
       A[k][j] = B[k][j] = 0.f;
     }
-  // (every lane of a warp runs the same number of turns: the shuffles want them all)
+  const size_t row = (size_t)a.L * a.C, col = (size_t)p.g * D;
   const long long step = (long long)q.sets * q.down;
-  const int turns = (int)((a.N + step - 1) / step);
-  for (int t = 0; t < turns; ++t) {
-    const long long n = t * step + (long long)set * q.down + down;
-    const bool on = live && n < a.N;
-    const size_t at = ((size_t)(on ? n : 0) * a.G + g) * D;   // (n >= N: nothing is touched)
-    const float mean = on ? a.mean[(size_t)n * a.G + g] : 0.f, rstd = on ? a.rstd[(size_t)n * a.G + g] : 0.f;
-    Pack<T, V> x[VPT], dy[VPT], z[VPT];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int v = l + k * lanes;
-      const bool in = on && v < DV;
-      x[k] = in ? load_pack<T, V>(a.x, at + (size_t)v * V) : Pack<T, V>{};
-      dy[k] = in ? load_pack<T, V>(a.dy, at + (size_t)v * V) : Pack<T, V>{};
-      if (kGate) z[k] = in ? load_pack<T, V>(a.gate, at + (size_t)v * V) : Pack<T, V>{};
+  long long n = (long long)p.set * q.down + p.down;
+  float nmean = 0.f, nrstd = 0.f;
+  auto load_stats = [&](long long m) {
+    if (m < a.N && p.live) {
+      nmean = a.mean[m * a.G + p.g];
+      nrstd = a.rstd[m * a.G + p.g];
     }
+  };
+  auto load = [&](int ahead) {
+    const long long m = n + ahead * step;
+    if (m < a.N) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+        if (at.in[k]) {
+          const size_t e = m * row + col + at.off[k];
+          ring.put(ahead, kIn * k, a.x, e);
+          ring.put(ahead, kIn * k + 1, a.dy, e);
+          if (kGate) ring.put(ahead, kIn * k + kIn - 1, a.gate, e);
+        }
+    }
+    ring.commit();
+  };
+  load_stats(n);
+#pragma unroll
+  for (int i = 0; i < kRowSteps - 1; ++i) load(i);
+  // (every lane of a warp runs the same number of turns: the shuffles want them all)
+  const int turns = (int)((a.N + step - 1) / step);
+  for (int t = 0; t < turns; ++t, n += step, ring.next()) {
+    const bool on = n < a.N;
+    const float mean = nmean, rstd = nrstd;
+    load_stats(n + step);
+    load(kRowSteps - 1);
+    ring.wait();
     float xh[VPT][V], d[VPT][V], s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const bool in = on && l + k * lanes < DV;
-      Pack<T, V> o;
+      const bool in = on && at.in[k];
+      const Pack<T, V> x = ring.get(kIn * k), dy = ring.get(kIn * k + 1);
+      Pack<T, V> z{}, o;
+      if (kGate) z = ring.get(kIn * k + kIn - 1);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float dz = 0.f;
-        const float du = grad_u<kGate>(to_f(x[k].e[j]), to_f(dy[k].e[j]), kGate ? to_f(z[k].e[j]) : 0.f, mean,
-                                       rstd, w[k][j], b[k][j], a.act, &xh[k][j], &dz);
+        const float du = grad_u<kGate>(to_f(x.e[j]), to_f(dy.e[j]), to_f(z.e[j]), mean, rstd, w[k][j], b[k][j],
+                                       a.act, &xh[k][j], &dz);
         if (kGate) from_f(o.e[j], dz);
         if (in) {
           A[k][j] += du;
@@ -126,52 +139,43 @@ __global__ void __launch_bounds__(kGnThreads) gn_row_bwd_kernel(const GroupNormA
           s2 = fmaf(d[k][j], xh[k][j], s2);
         }
       }
-      if (kGate && in) store_pack<T, V>(a.dgate, at + (size_t)(l + k * lanes) * V, o);
+      if (kGate && in) store_pack<T, V>(a.dgate, n * row + col + at.off[k], o);
     }
-    const float m1 = sub_sum(s1, lanes) * inv, m2 = sub_sum(s2, lanes) * inv;
+    const float m1 = sub_sum(s1, q.lanes) * inv, m2 = sub_sum(s2, q.lanes) * inv;
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
-      if (on && l + k * lanes < DV) {
+      if (on && at.in[k]) {
         Pack<T, V> o;
 #pragma unroll
         for (int j = 0; j < V; ++j) from_f(o.e[j], rstd * (d[k][j] - m1 - xh[k][j] * m2));
-        store_pack<T, V>(a.dx, at + (size_t)(l + k * lanes) * V, o);
+        store_pack<T, V>(a.dx, n * row + col + at.off[k], o);
       }
   }
   if (!part) return;
-  float* out = part + (size_t)set * 2 * a.C;
-  if (q.down == 1) {
+  // A, B over the CTA's rows and positions: every value through shared memory, summed in order
+  // (256 lanes of VPT V values each; the rings are done with).  First channel, channels of the CTA:
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  float(*acc)[kGnThreads * VPT * V] = reinterpret_cast<float(*)[kGnThreads * VPT * V]>(smem);
+  const int c0 = q.across == 1 ? 0 : (blockIdx.x % q.across) * q.J * D;
+  const int nc = q.across == 1 ? a.C : min(q.J * D, a.C - c0);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int v = l + k * lanes;
-      if (live && v < DV) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          out[g * D + v * V + j] = A[k][j];
-          out[a.C + g * D + v * V + j] = B[k][j];
-        }
-      }
-    }
-    return;
-  }
-  // (down C <= J lanes VPT V <= 256 * 16)
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int v = l + k * lanes;
-    if (live && v < DV) {
+  for (int k = 0; k < VPT; ++k)
+    if (at.in[k]) {
+      const int r = p.down * a.L + at.off[k] / a.C, e = r * nc + at.c[k] - c0;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        acc[0][down * a.C + g * D + v * V + j] = A[k][j];
-        acc[1][down * a.C + g * D + v * V + j] = B[k][j];
+        acc[0][e + j] = A[k][j];
+        acc[1][e + j] = B[k][j];
       }
     }
-  }
   __syncthreads();
-  for (int c = threadIdx.x; c < a.C; c += kGnThreads) {
+  float* out = part + (size_t)p.set * 2 * a.C + c0;
+  for (int c = threadIdx.x; c < nc; c += kGnThreads) {
     float x = 0.f, y = 0.f;
-    for (int r = 0; r < q.down; ++r) {
-      x += acc[0][r * a.C + c];
-      y += acc[1][r * a.C + c];
+    for (int r = 0; r < q.down * a.L; ++r) {
+      x += acc[0][r * nc + c];
+      y += acc[1][r * nc + c];
     }
     out[c] = x;
     out[a.C + c] = y;
@@ -179,11 +183,49 @@ __global__ void __launch_bounds__(kGnThreads) gn_row_bwd_kernel(const GroupNormA
 }
 
 // ------------------------------------------------------------------ slabs
+constexpr int kSlabSteps = 4;   // rows of a thread's column in its ring
+
+// Walks down a thread's column of x, dy (and z), their copies three rows ahead.
+template <typename T, int V, bool kGate>
+struct SlabReader {
+  static constexpr int kIn = kGate ? 3 : 2;
+  const GroupNormArgs& a;
+  size_t base;
+  int r, step, end;
+  Ring<T, V, kIn, kSlabSteps> ring;
+  __device__ __forceinline__ SlabReader(const GroupNormArgs& a, const SlabPlace& p, int2 rr, size_t base, void* smem)
+      : a(a), base(base), r(rr.x + p.row), step(p.step), end(rr.y), ring(smem) {
+#pragma unroll
+    for (int i = 0; i < kSlabSteps - 1; ++i) load(i);
+  }
+  __device__ __forceinline__ void load(int ahead) {
+    const int m = r + ahead * step;
+    if (m < end) {
+      const size_t at = base + (size_t)m * a.C;
+      ring.put(ahead, 0, a.x, at);
+      ring.put(ahead, 1, a.dy, at);
+      if (kGate) ring.put(ahead, kIn - 1, a.gate, at);
+    }
+    ring.commit();
+  }
+  __device__ __forceinline__ void get(Pack<T, V>& x, Pack<T, V>& dy, Pack<T, V>& z) {
+    load(kSlabSteps - 1);
+    ring.wait();
+    x = ring.get(0);
+    dy = ring.get(1);
+    if (kGate) z = ring.get(kIn - 1);
+  }
+  __device__ __forceinline__ void next() {
+    r += step;
+    ring.next();
+  }
+};
+
 // part [n][chunk][2][C]: A, B; share [n][g][chunk][parts]: (sum du w, sum du w xhat) of the slab.
 template <typename T, int V, bool kGate>
 __global__ void __launch_bounds__(kGnThreads) gn_slab_grad_kernel(const GroupNormArgs a, const SlabPlan s,
                                                                   float* part, float2* share) {
-  __shared__ float sa[kGnThreads * V], sb[kGnThreads * V];
+  extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
   const int2 rr = slab_rows(s, p, a.L);
   float A[V], B[V];
@@ -198,31 +240,23 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_grad_kernel(const GroupNor
       b[j] = param(a.bias, p.c + j, a.wb_dtype, 0.f);
     }
     const size_t base = (size_t)p.n * a.L * a.C + p.c;
-    for (int r = rr.x + p.row; r < rr.y; r += 2 * p.step) {
-      Pack<T, V> x[2], dy[2], z[2];
-      const int k = min(2, (rr.y - r + p.step - 1) / p.step);
+    for (SlabReader<T, V, kGate> in(a, p, rr, base, smem); in.r < in.end; in.next()) {
+      Pack<T, V> x, dy, z{};
+      in.get(x, dy, z);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (i < k) {
-          const size_t at = base + (size_t)(r + i * p.step) * a.C;
-          x[i] = load_pack<T, V>(a.x, at);
-          dy[i] = load_pack<T, V>(a.dy, at);
-          if (kGate) z[i] = load_pack<T, V>(a.gate, at);
-        }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (i < k) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            float xh, dz;
-            const float du = grad_u<kGate>(to_f(x[i].e[j]), to_f(dy[i].e[j]), kGate ? to_f(z[i].e[j]) : 0.f, mean,
-                                           rstd, w[j], b[j], a.act, &xh, &dz);
-            A[j] += du;
-            B[j] = fmaf(du, xh, B[j]);
-          }
-        }
+      for (int j = 0; j < V; ++j) {
+        float xh, dz;
+        const float du = grad_u<kGate>(to_f(x.e[j]), to_f(dy.e[j]), to_f(z.e[j]), mean, rstd, w[j], b[j], a.act,
+                                       &xh, &dz);
+        A[j] += du;
+        B[j] = fmaf(du, xh, B[j]);
+      }
     }
   }
+  // (the rings are done with; a thread's own copies have landed)
+  __syncthreads();
+  float* sa = reinterpret_cast<float*>(smem);
+  float* sb = sa + kGnThreads * V;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     sa[j * kGnThreads + threadIdx.x] = A[j];
@@ -282,6 +316,7 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_bwd_kernel(const GroupNorm
     return;
   }
   __shared__ float2 means[kGnThreads];
+  extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
   const int lane = threadIdx.x & 31, Q = s.chunks * s.parts;
   const float inv = 1.f / ((float)a.L * (float)(a.C / a.G));
@@ -309,87 +344,81 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_bwd_kernel(const GroupNorm
     b[j] = param(a.bias, p.c + j, a.wb_dtype, 0.f);
   }
   const size_t base = (size_t)p.n * a.L * a.C + p.c;
-  for (int r = rr.x + p.row; r < rr.y; r += 2 * p.step) {
-    Pack<T, V> x[2], dy[2], z[2];
-    const int k = min(2, (rr.y - r + p.step - 1) / p.step);
+  for (SlabReader<T, V, kGate> in(a, p, rr, base, smem); in.r < in.end; in.next()) {
+    Pack<T, V> x, dy, z{}, o, oz;
+    in.get(x, dy, z);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (i < k) {
-        const size_t at = base + (size_t)(r + i * p.step) * a.C;
-        x[i] = load_pack<T, V>(a.x, at);
-        dy[i] = load_pack<T, V>(a.dy, at);
-        if (kGate) z[i] = load_pack<T, V>(a.gate, at);
-      }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (i < k) {
-        const size_t at = base + (size_t)(r + i * p.step) * a.C;
-        Pack<T, V> o, oz;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float xh, dz = 0.f;
-          const float du = grad_u<kGate>(to_f(x[i].e[j]), to_f(dy[i].e[j]), kGate ? to_f(z[i].e[j]) : 0.f, mean,
-                                         rstd, w[j], b[j], a.act, &xh, &dz);
-          from_f(o.e[j], rstd * (du * w[j] - m.x - xh * m.y));
-          if (kGate) from_f(oz.e[j], dz);
-        }
-        store_pack<T, V>(a.dx, at, o);
-        if (kGate) store_pack<T, V>(a.dgate, at, oz);
-      }
+    for (int j = 0; j < V; ++j) {
+      float xh, dz = 0.f;
+      const float du = grad_u<kGate>(to_f(x.e[j]), to_f(dy.e[j]), to_f(z.e[j]), mean, rstd, w[j], b[j], a.act, &xh,
+                                     &dz);
+      from_f(o.e[j], rstd * (du * w[j] - m.x - xh * m.y));
+      if (kGate) from_f(oz.e[j], dz);
+    }
+    const size_t at = base + (size_t)in.r * a.C;
+    store_pack<T, V>(a.dx, at, o);
+    if (kGate) store_pack<T, V>(a.dgate, at, oz);
   }
 }
 
 constexpr int kRowValues = 16;   // values a lane holds in the row form
-
-// The row form's CTAs: about six an SM, and no more than the rows need.
-RowSets row_sets(int N, int G, int lanes) {
-  RowSets q;
-  q.J = kGnThreads / lanes;
-  q.across = q.J >= G ? 1 : (G + q.J - 1) / q.J;
-  q.down = q.J >= G ? q.J / G : 1;
-  const long long most = ((long long)N + q.down - 1) / q.down, want = 152LL * 6 / q.across + 1;
-  q.sets = (int)(want < most ? want : most);
-  return q;
-}
+constexpr int kRowPerSm = 3;     // its CTAs an SM (registers)
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+template <typename T, int V, int VPT, bool kGate>
+cudaError_t launch_row_bwd(const GroupNormArgs& a, const RowPlan& r, float* part) {
+  constexpr int kRing = Ring<T, V, VPT * (kGate ? 3 : 2), kRowSteps>::kShared;
+  constexpr int kSums = 2 * kGnThreads * VPT * V * (int)sizeof(float);
+  constexpr int kShared = kRing > kSums ? kRing : kSums;
+  const cudaError_t err = allow_shared<gn_row_bwd_kernel<T, V, VPT, kGate>, kShared>();
+  if (err != cudaSuccess) return err;
+  gn_row_bwd_kernel<T, V, VPT, kGate><<<(unsigned)(r.sets * r.across), kGnThreads, kShared, a.stream>>>(a, r, part);
+  return cudaGetLastError();
+}
+
 template <typename T, int V, bool kGate>
-void launch_bwd(const GroupNormArgs& a) {
+cudaError_t launch_bwd(const GroupNormArgs& a) {
   const bool params = a.dweight || a.dbias;
-  const RowPlan r = row_plan(a.C, a.G, a.io_dtype, kRowValues);
+  const RowPlan r = row_plan(a.N, a.L, a.C, a.G, a.io_dtype, kRowValues, kRowPerSm);
   float* part = reinterpret_cast<float*>(a.workspace);
   const unsigned sum_ctas = (unsigned)((a.C + 31) / 32);
-  if (a.L == 1 && r.lanes > 0) {
-    const RowSets q = row_sets(a.N, a.G, r.lanes);
-    const unsigned grid = (unsigned)(q.sets * q.across);
+  cudaError_t err;
+  if (r.lanes > 0) {
     float* to = params ? part : nullptr;
-    if (r.VPT == 1) gn_row_bwd_kernel<T, V, 1, kGate><<<grid, kGnThreads, 0, a.stream>>>(a, r.lanes, q, to);
-    else gn_row_bwd_kernel<T, V, kRowValues / V, kGate><<<grid, kGnThreads, 0, a.stream>>>(a, r.lanes, q, to);
-    if (params) gn_sum_sets_kernel<<<sum_ctas, 1024, 0, a.stream>>>(a, part, q.sets);
-    return;
+    err = r.VPT == 1 ? launch_row_bwd<T, V, 1, kGate>(a, r, to)
+                     : launch_row_bwd<T, V, kRowValues / V, kGate>(a, r, to);
+    if (err != cudaSuccess || !params) return err;
+    gn_sum_sets_kernel<<<sum_ctas, 1024, 0, a.stream>>>(a, part, r.sets);
+    return cudaGetLastError();
   }
   const SlabPlan s = slab_plan(a.N, a.L, a.C, a.G, a.io_dtype);
   const int slabs = a.N * s.NCB * s.chunks;
   float2* share = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(a.workspace) +
                                             align256((size_t)a.N * s.chunks * 2 * a.C * sizeof(float)));
-  gn_slab_grad_kernel<T, V, kGate><<<slabs, kGnThreads, 0, a.stream>>>(a, s, part, share);
-  gn_slab_bwd_kernel<T, V, kGate><<<slabs + (params ? sum_ctas : 0), kGnThreads, 0, a.stream>>>(a, s, slabs, part,
-                                                                                            share);
+  constexpr int kRing = SlabReader<T, V, kGate>::kIn * kSlabSteps * V * (int)sizeof(T) * kGnThreads;
+  constexpr int kSums = 2 * kGnThreads * V * (int)sizeof(float);
+  constexpr int kGrad = kRing > kSums ? kRing : kSums;
+  if ((err = allow_shared<gn_slab_grad_kernel<T, V, kGate>, kGrad>()) != cudaSuccess ||
+      (err = allow_shared<gn_slab_bwd_kernel<T, V, kGate>, kRing>()) != cudaSuccess)
+    return err;
+  gn_slab_grad_kernel<T, V, kGate><<<slabs, kGnThreads, kGrad, a.stream>>>(a, s, part, share);
+  gn_slab_bwd_kernel<T, V, kGate><<<slabs + (params ? sum_ctas : 0), kGnThreads, kRing, a.stream>>>(a, s, slabs,
+                                                                                                part, share);
+  return cudaGetLastError();
 }
 
 template <typename T, int V>
-void launch_bwd(const GroupNormArgs& a) {
-  if (a.gate) launch_bwd<T, V, true>(a);
-  else launch_bwd<T, V, false>(a);
+cudaError_t launch_bwd(const GroupNormArgs& a) {
+  return a.gate ? launch_bwd<T, V, true>(a) : launch_bwd<T, V, false>(a);
 }
 
 }  // namespace
 
 size_t group_norm_bwd_workspace_bytes(int N, int L, int C, int G, int io_dtype) {
   if (N == 0 || L == 0) return 0;
-  const RowPlan r = row_plan(C, G, io_dtype, kRowValues);
-  if (L == 1 && r.lanes > 0) return align256((size_t)row_sets(N, G, r.lanes).sets * 2 * C * sizeof(float));
+  const RowPlan r = row_plan(N, L, C, G, io_dtype, kRowValues, kRowPerSm);
+  if (r.lanes > 0) return align256((size_t)r.sets * 2 * C * sizeof(float));
   const SlabPlan s = slab_plan(N, L, C, G, io_dtype);
   return align256((size_t)N * s.chunks * 2 * C * sizeof(float)) +
          align256((size_t)N * G * s.chunks * s.parts * sizeof(float2));
@@ -400,19 +429,17 @@ cudaError_t launch_group_norm_bwd(const GroupNormArgs& a) {
   if ((long long)a.N * s.NCB * s.chunks + a.C > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (a.io_dtype == GDN_F32) {
     switch (s.V) {
-      case 4: launch_bwd<float, 4>(a); break;
-      case 2: launch_bwd<float, 2>(a); break;
-      default: launch_bwd<float, 1>(a);
-    }
-  } else {
-    switch (s.V) {
-      case 8: launch_bwd<__nv_bfloat16, 8>(a); break;
-      case 4: launch_bwd<__nv_bfloat16, 4>(a); break;
-      case 2: launch_bwd<__nv_bfloat16, 2>(a); break;
-      default: launch_bwd<__nv_bfloat16, 1>(a);
+      case 4: return launch_bwd<float, 4>(a);
+      case 2: return launch_bwd<float, 2>(a);
+      default: return launch_bwd<float, 1>(a);
     }
   }
-  return cudaGetLastError();
+  switch (s.V) {
+    case 8: return launch_bwd<__nv_bfloat16, 8>(a);
+    case 4: return launch_bwd<__nv_bfloat16, 4>(a);
+    case 2: return launch_bwd<__nv_bfloat16, 2>(a);
+    default: return launch_bwd<__nv_bfloat16, 1>(a);
+  }
 }
 
 }  // namespace gdn

@@ -86,6 +86,14 @@ def test_shapes(shape, G, gate, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("shape,G", [((511, 8, 4), 4), ((300, 2, 16), 2), ((97, 3, 5, 48), 3), ((40, 7, 21), 3),
+                                     ((9, 4, 2048), 32), ((5000, 9, 8), 1), ((2, 31, 264), 2)])
+def test_many_small_slabs(shape, G, gate, dtype):
+    check(shape, G, dtype, gate=gate)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_options(dtype):
     for gate in (False, True):
         check((6, 10, 64), 8, dtype, act=None, gate=gate)
