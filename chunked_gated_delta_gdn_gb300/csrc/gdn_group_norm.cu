@@ -8,9 +8,9 @@
 //     registers of up to 32 lanes, which read it once, the next one being on its way meanwhile,
 //     take mean and variance over two register passes and write it; each lane keeps its channels'
 //     weights.
-//   else: a launch for each slab's mean and squared deviations (merged pairwise from batches of
-//     registers, never as E[x^2] - E[x]^2), and one that merges the slabs' and applies; the second
-//     reading of x comes from L2 where the tensor fits it.
+//   else: a launch for each slab's mean and squared deviations (merged pairwise from registers,
+//     never as E[x^2] - E[x]^2), a small one that merges the slabs', and one that applies; the
+//     second reading of x comes from L2 where the tensor fits it.
 #include "gdn_group_norm.cuh"
 
 namespace gdn {
@@ -204,39 +204,43 @@ __device__ __forceinline__ float slab_count(const SlabPlan& s, int L, int q) {
   return (float)(min(s.rows, L - chunk * s.rows)) * (float)(cols * s.V);
 }
 
+// Mean and rstd of every group from its slabs, a warp a group.  (Merged by each CTA of the second
+// launch instead, 250 slabs of 32 groups took it longer than the rest of its work.)
+__global__ void __launch_bounds__(kGnThreads) gn_slab_merge_kernel(const GroupNormArgs a, const SlabPlan s,
+                                                                   const float2* part, float2* stats) {
+  const int lane = threadIdx.x & 31, Q = s.chunks * s.parts;
+  const long long i = (long long)blockIdx.x * (kGnThreads / 32) + (threadIdx.x >> 5);
+  if (i >= (long long)a.N * a.G) return;
+  const float count = (float)a.L * (float)(a.C / a.G);
+  const float2* q = part + i * Q;
+  const float m0 = q[0].x;
+  float t = 0.f;
+#pragma unroll 4
+  for (int k = lane; k < Q; k += 32) t = fmaf(slab_count(s, a.L, k), q[k].x - m0, t);
+  const float mean = m0 + warp_sum(t) / count;
+  t = 0.f;
+#pragma unroll 4
+  for (int k = lane; k < Q; k += 32) {
+    const float2 v = q[k];
+    const float d = v.x - mean;
+    t += v.y + slab_count(s, a.L, k) * d * d;
+  }
+  const float rstd = rsqrtf(warp_sum(t) / count + a.eps);
+  if (lane == 0) {
+    stats[i] = make_float2(mean, rstd);
+    if (a.mean) a.mean[i] = mean;
+    if (a.rstd) a.rstd[i] = rstd;
+  }
+}
+
 template <typename T, int V, bool kGate>
 __global__ void __launch_bounds__(kGnThreads) gn_slab_fwd_kernel(const GroupNormArgs a, const SlabPlan s,
-                                                                 const float2* part) {
-  __shared__ float2 stats[kGnThreads];   // mean, rstd of the column block's groups
+                                                                 const float2* stats) {
   extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
-  const int lane = threadIdx.x & 31, Q = s.chunks * s.parts;
-  const float count = (float)a.L * (float)(a.C / a.G);
-  for (int g = threadIdx.x >> 5; g < p.groups; g += kGnThreads / 32) {
-    const size_t i = (size_t)p.n * a.G + p.g0 + g;
-    const float2* q = part + i * Q;
-    const float m0 = q[0].x;
-    float t = 0.f;
-    for (int k = lane; k < Q; k += 32) t = fmaf(slab_count(s, a.L, k), q[k].x - m0, t);
-    const float mean = m0 + warp_sum(t) / count;
-    t = 0.f;
-    for (int k = lane; k < Q; k += 32) {
-      const float d = q[k].x - mean;
-      t += q[k].y + slab_count(s, a.L, k) * d * d;
-    }
-    const float rstd = rsqrtf(warp_sum(t) / count + a.eps);
-    if (lane == 0) {
-      stats[g] = make_float2(mean, rstd);
-      if (p.chunk == 0 && (s.parts == 1 || p.cb == p.g0 * s.parts)) {
-        if (a.mean) a.mean[i] = mean;
-        if (a.rstd) a.rstd[i] = rstd;
-      }
-    }
-  }
-  __syncthreads();
   if (!p.on) return;
   const int2 rr = slab_rows(s, p, a.L);
-  const float2 st = stats[p.g - p.g0];
+  const float2 st = stats[(size_t)p.n * a.G + p.g];
   float w[V], b[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -300,7 +304,10 @@ cudaError_t launch_fwd(const GroupNormArgs& a) {
   const cudaError_t err = allow_shared<gn_slab_fwd_kernel<T, V, kGate>, kApply>();
   if (err != cudaSuccess) return err;
   gn_slab_stats_kernel<T, V><<<grid, kGnThreads, kStats, a.stream>>>(a, s, part);
-  gn_slab_fwd_kernel<T, V, kGate><<<grid, kGnThreads, kApply, a.stream>>>(a, s, part);
+  float2* stats = part + (size_t)a.N * a.G * s.chunks * s.parts;
+  const unsigned warps = kGnThreads / 32, merge_grid = (unsigned)(((long long)a.N * a.G + warps - 1) / warps);
+  gn_slab_merge_kernel<<<merge_grid, kGnThreads, 0, a.stream>>>(a, s, part, stats);
+  gn_slab_fwd_kernel<T, V, kGate><<<grid, kGnThreads, kApply, a.stream>>>(a, s, stats);
   return cudaGetLastError();
 }
 
@@ -314,7 +321,7 @@ cudaError_t launch_fwd(const GroupNormArgs& a) {
 size_t group_norm_fwd_workspace_bytes(int N, int L, int C, int G, int io_dtype) {
   if (N == 0 || L == 0 || row_plan(N, L, C, G, io_dtype, kRowValues, kRowPerSm).lanes > 0) return 0;
   const SlabPlan s = slab_plan(N, L, C, G, io_dtype);
-  return (size_t)N * G * s.chunks * s.parts * sizeof(float2);
+  return (size_t)N * G * (s.chunks * s.parts + 1) * sizeof(float2);
 }
 
 cudaError_t launch_group_norm_fwd(const GroupNormArgs& a) {

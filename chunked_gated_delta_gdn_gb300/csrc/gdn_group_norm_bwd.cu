@@ -10,8 +10,8 @@
 //   single positions (and small slabs) with groups of up to 512 values: one launch reads each row
 //     once, its groups in registers, the next row being on its way, and leaves A, B of each set of
 //     rows; a second adds the sets.
-//   else: a launch for A, B and the slab's share of m1, m2, a second that reads x, dy (and z) again
-//     and applies, its last CTAs adding A, B up.
+//   else: a launch for A, B and the slab's share of m1, m2, a small one that adds the shares up, and
+//     one that reads x, dy (and z) again and applies, its last CTAs adding A, B up.
 #include "gdn_group_norm.cuh"
 
 namespace gdn {
@@ -308,35 +308,38 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_grad_kernel(const GroupNor
   }
 }
 
+// m1, m2 of every group from its slabs' shares, a warp a group.
+__global__ void __launch_bounds__(kGnThreads) gn_slab_means_kernel(const GroupNormArgs a, int Q, const float2* share,
+                                                                   float2* means) {
+  const int lane = threadIdx.x & 31;
+  const long long i = (long long)blockIdx.x * (kGnThreads / 32) + (threadIdx.x >> 5);
+  if (i >= (long long)a.N * a.G) return;
+  const float inv = 1.f / ((float)a.L * (float)(a.C / a.G));
+  float x = 0.f, y = 0.f;
+#pragma unroll 4
+  for (int k = lane; k < Q; k += 32) {
+    const float2 v = share[i * Q + k];
+    x += v.x;
+    y += v.y;
+  }
+  x = warp_sum(x);
+  y = warp_sum(y);
+  if (lane == 0) means[i] = make_float2(x * inv, y * inv);
+}
+
 template <typename T, int V, bool kGate>
 __global__ void __launch_bounds__(kGnThreads) gn_slab_bwd_kernel(const GroupNormArgs a, const SlabPlan s, int slabs,
-                                                                 const float* part, const float2* share) {
+                                                                 const float* part, const float2* means) {
   if ((int)blockIdx.x >= slabs) {
     sum_sets<kGnThreads / 32>(a, part, a.N * s.chunks, blockIdx.x - slabs);
     return;
   }
-  __shared__ float2 means[kGnThreads];
   extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
-  const int lane = threadIdx.x & 31, Q = s.chunks * s.parts;
-  const float inv = 1.f / ((float)a.L * (float)(a.C / a.G));
-  for (int g = threadIdx.x >> 5; g < p.groups; g += kGnThreads / 32) {
-    const float2* q = share + ((size_t)p.n * a.G + p.g0 + g) * Q;
-    float x = 0.f, y = 0.f;
-    for (int k = lane; k < Q; k += 32) {
-      const float2 v = q[k];
-      x += v.x;
-      y += v.y;
-    }
-    x = warp_sum(x);
-    y = warp_sum(y);
-    if (lane == 0) means[g] = make_float2(x * inv, y * inv);
-  }
-  __syncthreads();
   if (!p.on) return;
   const int2 rr = slab_rows(s, p, a.L);
   const float mean = a.mean[(size_t)p.n * a.G + p.g], rstd = a.rstd[(size_t)p.n * a.G + p.g];
-  const float2 m = means[p.g - p.g0];
+  const float2 m = means[(size_t)p.n * a.G + p.g];
   float w[V], b[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -403,8 +406,12 @@ cudaError_t launch_bwd(const GroupNormArgs& a) {
       (err = allow_shared<gn_slab_bwd_kernel<T, V, kGate>, kRing>()) != cudaSuccess)
     return err;
   gn_slab_grad_kernel<T, V, kGate><<<slabs, kGnThreads, kGrad, a.stream>>>(a, s, part, share);
+  const int Q = s.chunks * s.parts;
+  float2* means = share + (size_t)a.N * a.G * Q;
+  const unsigned warps = kGnThreads / 32, means_grid = (unsigned)(((long long)a.N * a.G + warps - 1) / warps);
+  gn_slab_means_kernel<<<means_grid, kGnThreads, 0, a.stream>>>(a, Q, share, means);
   gn_slab_bwd_kernel<T, V, kGate><<<slabs + (params ? sum_ctas : 0), kGnThreads, kRing, a.stream>>>(a, s, slabs,
-                                                                                                part, share);
+                                                                                                part, means);
   return cudaGetLastError();
 }
 
@@ -421,7 +428,7 @@ size_t group_norm_bwd_workspace_bytes(int N, int L, int C, int G, int io_dtype) 
   if (r.lanes > 0) return align256((size_t)r.sets * 2 * C * sizeof(float));
   const SlabPlan s = slab_plan(N, L, C, G, io_dtype);
   return align256((size_t)N * s.chunks * 2 * C * sizeof(float)) +
-         align256((size_t)N * G * s.chunks * s.parts * sizeof(float2));
+         align256((size_t)N * G * (s.chunks * s.parts + 1) * sizeof(float2));
 }
 
 cudaError_t launch_group_norm_bwd(const GroupNormArgs& a) {
