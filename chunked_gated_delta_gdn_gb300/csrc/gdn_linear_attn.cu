@@ -41,15 +41,21 @@ __device__ __forceinline__ float dot4(const float4& a, const float4& b, float ac
 }
 
 // Shared floats of the chunked pass: q, k rows padded by 4 (the rows that 16 threads read at
-// one column fall into different banks), v, the state, P padded by 4, the decay table.
+// one column fall into different banks), v, the state, P padded by 4, the decay tables.
 __host__ __device__ inline int la_smem_floats(int K, int V) {
-  return 2 * kChunk * (K + 4) + kChunk * V + K * V + kChunk * (kChunk + 4) + 80;
+  return 2 * kChunk * (K + 4) + kChunk * V + K * V + kChunk * (kChunk + 4) + 80 + 2 * (kLaMaxSegments + 2);
 }
 
-// One CTA per (sequence, head), 256 threads as 16 x 16; the state stays in shared memory for the
-// whole sequence.  Every product is register-blocked: P 4 x 4 a thread, o 4 x 8, X 8 x 8.
+// One CTA per (sequence, head, segment), 256 threads as 16 x 16; the state stays in shared memory.
+// Every product is register-blocked: P 4 x 4 a thread, o 4 x 8, X 8 x 8; what the mask takes away
+// of P and P V is left out by blocks.  Bound by the fp32 units (2.7 M multiply-adds a chunk at K =
+// V = 128, about 21k cycles of them).  Chains that do not fill the GPU are cut into segments as on
+// the tensor cores: a launch (`local_only`) for each segment's own contribution to the state, and
+// one from the entry states.  A chain's scratch holds a copy of its entry state (the exit state may
+// go to the same place), then the contributions in order, [K][V] each.
 template <typename T, typename TO>
-__global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const LinAttnPass p) {
+__global__ void __launch_bounds__(kLaThreads, 1)
+    linear_attn_kernel(const LinAttnPass p, int segs, int local_only, float* scratch) {
   extern __shared__ __align__(16) float sm[];
   const int K = p.K, V = p.V, KS = K + 4;
   float* sQ = sm;
@@ -59,29 +65,62 @@ __global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const LinAtt
   float* sP = sX + K * V;                 // [64][68]
   float* sW = sP + kChunk * (kChunk + 4);   // gamma^0 .. gamma^64
   constexpr int PS = kChunk + 4;
-  const int h = blockIdx.x % p.H, n = blockIdx.x / p.H;
+  int unit = blockIdx.x;
+  const int h = unit % p.H;
+  unit /= p.H;
+  const int n = unit % p.num_seqs, seg = unit / p.num_seqs;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const LaChain c = la_chain(p, n, h, tid == 0 && h == 0);
+  const LaChain c = la_chain(p, n, h, tid == 0 && h == 0 && seg == 0);
   const int T_total = p.cu_seqlens ? p.T : p.B * p.T;
-  la_zero_rows(p, h, c.tail, T_total, tid, kLaThreads);
-  if (c.skip) return;
-  if (c.padding) {
-    la_zero_rows(p, h, c.bos, c.eos, tid, kLaThreads);
-    return;
+  if (seg == 0 && !local_only) {
+    la_zero_rows(p, h, c.tail, T_total, tid, kLaThreads);
+    if (c.padding) la_zero_rows(p, h, c.bos, c.eos, tid, kLaThreads);
   }
-  const float ld = clamp_log_decay(p.log_decay[h]);
-  if (tid <= kChunk) sW[tid] = decay_pow(ld, (float)tid);
-  for (int e = tid; e < K * V; e += kLaThreads) {
-    const int kk = e / V, vv = e - kk * V;
-    sX[e] = c.init ? c.init[p.initial_t ? vv * K + kk : e] : 0.f;
-  }
+  if (c.skip || c.padding) return;
   const int nch = (c.eos - c.bos + kChunk - 1) / kChunk;
+  const int per = max(1, (nch + segs - 1) / segs);
+  const int c0 = min(seg * per, nch), c1 = min(c0 + per, nch);
+  const bool last = c1 == nch, whole = seg == 0 && last;
+  if (local_only ? last : (c0 == c1 && !whole)) return;
+  const float ld = clamp_log_decay(p.log_decay[h]);
+  // decay over a full chunk, the partial chunk and each segment before this one (by one thread each:
+  // they are made in 64 bits)
+  float2* sG = reinterpret_cast<float2*>(sW + 80);
+  if (tid <= kChunk) sW[tid] = decay_pow(ld, (float)tid);
+  if (tid < seg + 2) {
+    const int rest = nch * kChunk - (c.eos - c.bos);   // tokens that the partial chunk lacks
+    const int tokens = tid == 0 ? kChunk : tid == 1 ? kChunk - rest
+                       : per * kChunk - (p.reverse && tid == 2 ? rest : 0);   // (backwards it is first)
+    sG[tid] = decay_pow2(ld, tokens);
+  }
+  __syncthreads();
+  float* slots = scratch + (size_t)(n * p.H + h) * segs * (size_t)(K * V);   // (segs > 1 only)
+  {   // the entry state
+    const float* init = whole || (local_only && seg == 0) ? c.init : nullptr;
+    for (int e = tid; e < K * V; e += kLaThreads) {
+      const int kk = e / V, vv = e - kk * V;
+      float x = init ? init[p.initial_t ? vv * K + kk : e] : 0.f;
+      if (local_only) {
+        if (seg == 0) slots[e] = x;
+        x = 0.f;
+      } else if (!whole) {
+        x = __ldcg(slots + e);
+      }
+      sX[e] = x;
+    }
+    if (!local_only && !whole)
+      for (int r = 0; r < seg; ++r) {
+        const float2 g = sG[r + 2];
+        const float* src = slots + (size_t)(r + 1) * K * V;
+        for (int e = tid; e < K * V; e += kLaThreads) sX[e] = mul2(sX[e], g) + __ldcg(src + e);
+      }
+  }
   const int K4 = K / 4, V4 = V / 4;
   const T* gq = reinterpret_cast<const T*>(p.q);
   const T* gk = reinterpret_cast<const T*>(p.k);
   const T* gv = reinterpret_cast<const T*>(p.v);
   const int hq = h / (p.H / p.Hq), hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
-  for (int cc = 0; cc < nch; ++cc) {
+  for (int cc = c0; cc < c1; ++cc) {
     const int ch = p.reverse ? nch - 1 - cc : cc;
     const int t0 = c.bos + ch * kChunk, L = min(kChunk, c.eos - t0);
     __syncthreads();
@@ -89,7 +128,7 @@ __global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const LinAtt
       const int t = e / K4, d = 4 * (e - t * K4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (t < L) {
-        x = load4(gq + ((size_t)(t0 + t) * p.Hq + hq) * K + d);
+        if (!local_only) x = load4(gq + ((size_t)(t0 + t) * p.Hq + hq) * K + d);
         y = load4(gk + ((size_t)(t0 + t) * p.Hk + hk) * K + d);
       }
       *reinterpret_cast<float4*>(sQ + t * KS + d) = x;
@@ -102,108 +141,138 @@ __global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const LinAtt
       *reinterpret_cast<float4*>(sV + t * V + d) = x;
     }
     __syncthreads();
-    {   // P: rows ty + 16 a, columns tx + 16 b
-      float acc[4][4] = {};
-      for (int d = 0; d < K; d += 4) {
-        float4 a[4], b[4];
+    if (!local_only) {
+      {   // P: rows ty + 16 i, columns tx + 16 j; blocks beyond the diagonal are masked
+        float acc[4][4] = {};
+        for (int d = 0; d < K; d += 4) {
+          float4 a[4], b[4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          a[m] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * m) * KS + d);
-          b[m] = *reinterpret_cast<const float4*>(sK + (tx + 16 * m) * KS + d);
+          for (int m = 0; m < 4; ++m) {
+            a[m] = *reinterpret_cast<const float4*>(sQ + (ty + 16 * m) * KS + d);
+            b[m] = *reinterpret_cast<const float4*>(sK + (tx + 16 * m) * KS + d);
+          }
+          if (p.reverse) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = i; j < 4; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j <= i; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
+          for (int j = 0; j < 4; ++j) {
+            const int r = ty + 16 * i, s = tx + 16 * j, dist = p.reverse ? s - r : r - s;
+            sP[r * PS + s] = dist >= 0 ? p.s_in * sW[dist] * acc[i][j] : 0.f;
+          }
       }
+      __syncthreads();
+      // o: rows 4 ty .. 4 ty + 3, columns 4 tx + 64 m .. + 3
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int m = 0; m < 2; ++m) {
+        const int col = 4 * tx + 64 * m;
+        if (col >= V) break;
+        float4 acc[4] = {};
+        for (int d = 0; d < K; d += 4) {
+          float4 a[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = ty + 16 * i, s = tx + 16 * j, dist = p.reverse ? s - r : r - s;
-          sP[r * PS + s] = dist >= 0 ? p.s_in * sW[dist] * acc[i][j] : 0.f;
+          for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * KS + d);
+#pragma unroll
+          for (int dd = 0; dd < 4; ++dd) {
+            const float4 x = *reinterpret_cast<const float4*>(sX + (d + dd) * V + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * ty + i;
+          const float w = sW[p.reverse ? max(0, L - 1 - r) : r + 1];
+          acc[i].x *= w; acc[i].y *= w; acc[i].z *= w; acc[i].w *= w;
+        }
+        // (P is zero on the far side of the diagonal, and from L on)
+        const int j0 = p.reverse ? 4 * ty : 0, j1 = p.reverse ? L : min(L, 4 * ty + 4);
+        for (int j = j0; j < j1; j += 4) {
+          float4 a[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * PS + j);
+#pragma unroll
+          for (int dd = 0; dd < 4; ++dd) {
+            const float4 x = *reinterpret_cast<const float4*>(sV + (j + dd) * V + col);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * ty + i;
+          if (r >= L) continue;
+          float4 x = acc[i];
+          x.x *= p.s_out; x.y *= p.s_out; x.z *= p.s_out; x.w *= p.s_out;
+          store4(reinterpret_cast<TO*>(p.o) + ((size_t)(t0 + r) * p.H + h) * V + col, x);
+        }
+      }
+      if (last && cc + 1 == c1 && !c.fin) break;   // nobody wants the state any more
+      __syncthreads();   // the state has been read
     }
-    __syncthreads();
-    // o: rows 4 ty .. 4 ty + 3, columns 4 tx + 64 m .. + 3
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      const int col = 4 * tx + 64 * m;
-      if (col >= V) break;
-      float4 acc[4] = {};
-      for (int d = 0; d < K; d += 4) {
-        float4 a[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * KS + d);
-#pragma unroll
-        for (int dd = 0; dd < 4; ++dd) {
-          const float4 x = *reinterpret_cast<const float4*>(sX + (d + dd) * V + col);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
-        const float w = sW[p.reverse ? max(0, L - 1 - r) : r + 1];
-        acc[i].x *= w; acc[i].y *= w; acc[i].z *= w; acc[i].w *= w;
-      }
-      for (int j = 0; j < L; j += 4) {   // P is zero from L on
-        float4 a[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * PS + j);
-#pragma unroll
-        for (int dd = 0; dd < 4; ++dd) {
-          const float4 x = *reinterpret_cast<const float4*>(sV + (j + dd) * V + col);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
-        if (r >= L) continue;
-        float4 x = acc[i];
-        x.x *= p.s_out; x.y *= p.s_out; x.z *= p.s_out; x.w *= p.s_out;
-        store4(reinterpret_cast<TO*>(p.o) + ((size_t)(t0 + r) * p.H + h) * V + col, x);
-      }
-    }
-    __syncthreads();   // the state has been read
     // X: rows 4 ty + 64 a .. + 3, columns 4 tx + 64 b .. + 3
-    const float2 gl = decay_pow2(ld, L);
+    const float2 gl = sG[L == kChunk ? 0 : 1];
 #pragma unroll
     for (int ma = 0; ma < 2; ++ma) {
       const int row = 4 * ty + 64 * ma;
       if (row >= K) break;
+      float4 acc[2][4];
 #pragma unroll
       for (int mb = 0; mb < 2; ++mb) {
         const int col = 4 * tx + 64 * mb;
-        if (col >= V) break;
-        float4 acc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(sX + (row + i) * V + col);
-          acc[i] = make_float4(mul2(x.x, gl), mul2(x.y, gl), mul2(x.z, gl), mul2(x.w, gl));
+          const float4 x = col < V ? *reinterpret_cast<const float4*>(sX + (row + i) * V + col)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+          acc[mb][i] = make_float4(mul2(x.x, gl), mul2(x.y, gl), mul2(x.z, gl), mul2(x.w, gl));
         }
-        for (int j = 0; j < L; ++j) {
-          float4 kk = *reinterpret_cast<const float4*>(sK + j * KS + row);
-          const float4 x = *reinterpret_cast<const float4*>(sV + j * V + col);
-          const float w = p.s_in * sW[p.reverse ? j + 1 : L - 1 - j];
-          fma4(acc[0], kk.x * w, x);
-          fma4(acc[1], kk.y * w, x);
-          fma4(acc[2], kk.z * w, x);
-          fma4(acc[3], kk.w * w, x);
+      }
+      const bool two = 4 * tx + 64 < V, one = 4 * tx < V;
+      for (int j = 0; j < L; ++j) {
+        float4 kk = *reinterpret_cast<const float4*>(sK + j * KS + row);
+        const float w = p.s_in * sW[p.reverse ? j + 1 : L - 1 - j];
+        kk.x *= w; kk.y *= w; kk.z *= w; kk.w *= w;
+        if (one) {
+          const float4 x = *reinterpret_cast<const float4*>(sV + j * V + 4 * tx);
+          fma4(acc[0][0], kk.x, x);
+          fma4(acc[0][1], kk.y, x);
+          fma4(acc[0][2], kk.z, x);
+          fma4(acc[0][3], kk.w, x);
         }
+        if (two) {
+          const float4 x = *reinterpret_cast<const float4*>(sV + j * V + 4 * tx + 64);
+          fma4(acc[1][0], kk.x, x);
+          fma4(acc[1][1], kk.y, x);
+          fma4(acc[1][2], kk.z, x);
+          fma4(acc[1][3], kk.w, x);
+        }
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(sX + (row + i) * V + col) = acc[i];
+      for (int mb = 0; mb < 2; ++mb) {
+        const int col = 4 * tx + 64 * mb;
+        if (col < V) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(sX + (row + i) * V + col) = acc[mb][i];
+        }
       }
     }
   }
   __syncthreads();
-  if (c.fin)
-    for (int e = tid; e < K * V; e += kLaThreads) c.fin[e] = sX[e];
+  float* out = local_only ? slots + (size_t)(seg + 1) * K * V : last ? c.fin : nullptr;
+  if (out)
+    for (int e = tid; e < K * V; e += kLaThreads) out[e] = sX[e];
 }
 
 // Sum of the value heads that share a query/key head: one thread per 4 elements.
@@ -277,10 +346,10 @@ __global__ void __launch_bounds__(kLaThreads) linear_attn_decode_kernel(const Li
 }
 
 template <typename T, typename TO>
-cudaError_t launch_pass(const LinAttnPass& p) {
-  const long long blocks = (long long)p.num_seqs * p.H;
-  if (blocks <= 0) return cudaSuccess;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+cudaError_t launch_pass(const LinAttnPass& p, int segs, float* scratch) {
+  const long long chains = (long long)p.num_seqs * p.H;
+  if (chains <= 0) return cudaSuccess;
+  if (segs < 1 || chains * segs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -291,16 +360,25 @@ cudaError_t launch_pass(const LinAttnPass& p) {
     if (err != cudaSuccess) return err;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  linear_attn_kernel<T, TO><<<(unsigned)blocks, kLaThreads, la_smem_floats(p.K, p.V) * sizeof(float),
-                              p.stream>>>(p);
+  const size_t smem = la_smem_floats(p.K, p.V) * sizeof(float);
+  if (segs > 1) {
+    linear_attn_kernel<T, TO><<<(unsigned)(chains * (segs - 1)), kLaThreads, smem, p.stream>>>(p, segs, 1, scratch);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  }
+  linear_attn_kernel<T, TO><<<(unsigned)(chains * segs), kLaThreads, smem, p.stream>>>(p, segs, 0, scratch);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_linear_attn_generic(const LinAttnPass& p) {
-  if (p.io_dtype == GDN_F32) return launch_pass<float, float>(p);
-  return p.o_f32 ? launch_pass<__nv_bfloat16, float>(p) : launch_pass<__nv_bfloat16, __nv_bfloat16>(p);
+int linear_attn_segments(long long chains, long long most_tokens, int num_sms, int min_chunks) {
+  if (chains <= 0 || num_sms <= 0) return 1;
+  const long long chunks = (most_tokens + kChunk - 1) / kChunk;
+  return (int)std::max(1LL, std::min({(long long)kLaMaxSegments, num_sms / chains, chunks / min_chunks}));
+}
+
+cudaError_t launch_linear_attn_generic(const LinAttnPass& p, int segs, float* scratch) {
+  return launch_pass<float, float>(p, segs, scratch);
 }
 
 cudaError_t launch_linear_attn_fold(const float* const (&part)[2], void* const (&out)[2], long long T_total,

@@ -42,16 +42,17 @@ struct LinAttnPass {
   cudaStream_t stream;
 };
 
-// CUDA cores: any accepted head dims, either type.
-cudaError_t launch_linear_attn_generic(const LinAttnPass& p);
-// Tensor cores: bf16 (o may be fp32), any accepted head dims; up to three passes over the same
-// sequences and heads in one launch, each chain cut into `segs` segments (then `local` is scratch
-// of linear_attn_tc_workspace_bytes).  The number of segments goes by what the host knows: the
-// chains, the SMs and the most tokens that a sequence can have.
+// Segments that each chain is cut into where there are too few to fill the GPU (1: none): by what
+// the host knows, the chains of a launch, the most tokens that a sequence can have, and the chunks
+// that a segment needs to be worth its share of the two launches.
 constexpr int kLaMaxPasses = 3, kLaMaxSegments = 16, kLaMinSegmentChunks = 4;
-int linear_attn_tc_segments(int num_passes, int num_seqs, int H, long long most_tokens, int num_sms);
-size_t linear_attn_tc_workspace_bytes(int num_passes, int num_seqs, int H, int segs);
-cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* local);
+int linear_attn_segments(long long chains, long long most_tokens, int num_sms, int min_chunks);
+
+// CUDA cores: fp32, any accepted head dims.  scratch: segs > 1: segs K V floats a chain.
+cudaError_t launch_linear_attn_generic(const LinAttnPass& p, int segs, float* scratch);
+// Tensor cores: bf16 (o may be fp32), any accepted head dims; up to three passes over the same
+// sequences and heads in one launch.  scratch: segs > 1: segs 128 128 floats a chain and pass.
+cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* scratch);
 
 // out[i][t, hq, :] = sum over the group's value heads of part[i][t, hq * group + j, :], i = 0, 1
 // (fp32 in, io dtype out, heads added in order).

@@ -49,20 +49,23 @@ int sm_count() {
   return gdn::device_sm_count(dev);
 }
 
-// Scratch of a call: the segments' contributions, then (backward) per-value-head dq and dk in
-// fp32 where value heads share a query/key head.
+// Scratch of a call: the segments' states, then (backward) per-value-head dq and dk in fp32 where
+// value heads share a query/key head.
 struct Scratch {
   int segs;
   size_t local, part, total;   // bytes; part: one of the two
 };
-Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk, int Hv, int K,
+Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk, int Hv, int K, int V,
                 int io_dtype) {
   Scratch s{1, 0, 0, 0};
-  if (io_dtype == GDN_BF16) {
-    const long long most = packed ? (long long)B * T : T;
-    s.segs = gdn::linear_attn_tc_segments(num_passes, num_seqs, Hv, most, sm_count());
-    s.local = align256(gdn::linear_attn_tc_workspace_bytes(num_passes, num_seqs, Hv, s.segs));
-  }
+  const long long most = packed ? (long long)B * T : T, chains = (long long)num_seqs * Hv;
+  // the tensor cores run all passes at once and pad the state to 128 x 128; the CUDA cores run one
+  // after the other, each chunk of which takes long enough to stand alone
+  const bool tc = io_dtype == GDN_BF16;
+  s.segs = gdn::linear_attn_segments(tc ? chains * num_passes : chains, most, sm_count(),
+                                     tc ? gdn::kLaMinSegmentChunks : 1);
+  if (s.segs > 1)
+    s.local = align256((size_t)s.segs * chains * (tc ? num_passes * 16384 : K * V) * sizeof(float));
   if (num_passes > 1 && Hqk != Hv) s.part = align256((size_t)B * T * Hv * K * sizeof(float));
   s.total = s.local + 2 * s.part;
   return s;
@@ -73,7 +76,7 @@ cudaError_t run_passes(const gdn::LinAttnPass* p, int n, int segs, void* local) 
   if (p[0].io_dtype == GDN_BF16)
     return gdn::launch_linear_attn_tc(p, n, segs, reinterpret_cast<float*>(local));
   for (int i = 0; i < n; ++i) {
-    const cudaError_t err = gdn::launch_linear_attn_generic(p[i]);
+    const cudaError_t err = gdn::launch_linear_attn_generic(p[i], segs, reinterpret_cast<float*>(local));
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -93,7 +96,7 @@ size_t gdn_linear_attn_chunk_fwd_workspace_size(int B, int T, int Hqk, int Hv, i
                                                 int num_seqs, gdn_dtype_t io_dtype) {
   if (check_shapes(B, T, Hqk, Hv, K, V, io_dtype) != GDN_OK || num_seqs < 0) return (size_t)-1;
   // (a batch of one row needs as much whether it is packed or not)
-  return scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype).total;
+  return scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, V, io_dtype).total;
 }
 
 gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void* v,
@@ -138,7 +141,7 @@ gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void*
   p.final_state = output_final_state ? final_state : nullptr;
   p.s_out = resolve_scale(scale, K);
   p.o = o;
-  const Scratch sc = scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype);
+  const Scratch sc = scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, V, io_dtype);
   if ((st = check_workspace(workspace, workspace_bytes, sc.total)) != GDN_OK) return st;
   return run_passes(&p, 1, sc.segs, workspace) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -146,7 +149,7 @@ gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void*
 size_t gdn_linear_attn_chunk_bwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
                                                 int num_seqs, gdn_dtype_t io_dtype) {
   if (check_shapes(B, T, Hqk, Hv, K, V, io_dtype) != GDN_OK || num_seqs < 0) return (size_t)-1;
-  return scratch(3, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype).total;
+  return scratch(3, B, T, num_seqs, B == 1, Hqk, Hv, K, V, io_dtype).total;
 }
 
 gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void* v,
@@ -174,7 +177,7 @@ gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void*
       (d_final_state && !aligned16(d_final_state)) ||
       (d_initial_state && !aligned16(d_initial_state)))
     return GDN_ERR_LAYOUT;
-  const Scratch ws = scratch(3, B, T, num_seqs, B == 1, Hqk, Hv, K, io_dtype);
+  const Scratch ws = scratch(3, B, T, num_seqs, B == 1, Hqk, Hv, K, V, io_dtype);
   if ((st = check_workspace(workspace, workspace_bytes, num_seqs > 0 ? ws.total : 0)) != GDN_OK) return st;
   const gdn::LinAttnPass base =
       base_pass(log_decay, B, T, Hv, io_dtype, cu_seqlens, num_seqs, dev_status, stream);

@@ -46,7 +46,6 @@
 // leaves, TMEM is freed.
 #include <cuda.h>
 
-#include <algorithm>
 #include <atomic>
 #include <cstring>
 
@@ -812,17 +811,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
 }
 
 }  // namespace
-
-int linear_attn_tc_segments(int num_passes, int num_seqs, int H, long long most_tokens, int num_sms) {
-  const long long chains = (long long)num_passes * num_seqs * H;
-  if (chains <= 0 || num_sms <= 0) return 1;
-  const long long chunks = (most_tokens + kChunk - 1) / kChunk;
-  return (int)std::max(1LL, std::min({(long long)kLaMaxSegments, num_sms / chains, chunks / kLaMinSegmentChunks}));
-}
-
-size_t linear_attn_tc_workspace_bytes(int num_passes, int num_seqs, int H, int segs) {
-  return (size_t)num_passes * num_seqs * H * (segs > 1 ? segs : 0) * 16384 * sizeof(float);
-}
 
 cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* local) {
   const LinAttnPass& p0 = passes[0];

@@ -11,8 +11,8 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .api import _DT, _need, _ptr, _stream
-from .linear_attn import _scratch
+from .api import _DT, _need, _ptr
+from .linear_attn import _fit, _scratch, _stream
 
 __all__ = ["group_norm_act", "group_norm_act_bwd", "group_norm_act_trainable"]
 
@@ -21,7 +21,10 @@ _ACT = {None: _lib.GDN_ACT_NONE, "none": _lib.GDN_ACT_NONE, "silu": _lib.GDN_ACT
 
 def _inputs(x, num_groups, weight, bias, activation, gate):
     """Checks shared by the calls; returns (N, L, C, G, wb dtype code, act code)."""
-    _need(x, "x", (torch.float32, torch.bfloat16))
+    quick = (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() >= 2 and x.dtype in _DT
+             and x.is_contiguous())
+    if not quick:
+        _need(x, "x", (torch.float32, torch.bfloat16))
     if x.dim() < 2:
         raise ValueError("x must be [N, ..., C]")
     N, C, G = x.shape[0], x.shape[-1], int(num_groups)
@@ -32,6 +35,12 @@ def _inputs(x, num_groups, weight, bias, activation, gate):
     L = 1
     for s in x.shape[1:-1]:
         L *= s
+    if quick:
+        wb = weight.dtype if isinstance(weight, torch.Tensor) else \
+            bias.dtype if isinstance(bias, torch.Tensor) else torch.float32
+        if (wb is torch.float32 or wb is x.dtype) and \
+                _fit(x.device, (weight, wb, (C,)), (bias, wb, (C,)), (gate, x.dtype, x.shape)):
+            return N, L, C, G, _DT[wb], _ACT[activation]
     wb = None
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is not None:
@@ -56,12 +65,12 @@ def group_norm_act(x, num_groups, weight=None, bias=None, eps=1e-5, activation="
     dev = x.device
     if out is None:
         out = torch.empty_like(x)
-    _need(out, "out", x.dtype, dev, x.shape)
+    elif not _fit(dev, (out, x.dtype, x.shape)):
+        _need(out, "out", x.dtype, dev, x.shape)
     mean = rstd = None
     if return_stats:
-        mean = torch.zeros((N, G), dtype=torch.float32, device=dev) if L == 0 else \
-            torch.empty((N, G), dtype=torch.float32, device=dev)
-        rstd = torch.empty_like(mean) if L else torch.zeros_like(mean)
+        make = torch.empty if L else torch.zeros
+        mean, rstd = make((2, N, G), dtype=torch.float32, device=dev).unbind(0)
     lib = _lib.load()
     need = lib.gdn_group_norm_act_fwd_workspace_size(N, L, C, G, _DT[x.dtype])
     workspace, ws_bytes = _scratch(need, "gdn_group_norm_act_fwd", workspace, dev)
@@ -79,13 +88,16 @@ def group_norm_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, ac
     ``need_params``), dgate None without a gate."""
     N, L, C, G, wb, act = _inputs(x, num_groups, weight, bias, activation, gate)
     dev = x.device
-    _need(dy, "dy", x.dtype, dev, x.shape)
-    _need(mean, "mean", torch.float32, dev, (N, G))
-    _need(rstd, "rstd", torch.float32, dev, (N, G))
+    if dy is None or mean is None or rstd is None or not _fit(
+            dev, (dy, x.dtype, x.shape), (mean, torch.float32, (N, G)), (rstd, torch.float32, (N, G))):
+        _need(dy, "dy", x.dtype, dev, x.shape)
+        _need(mean, "mean", torch.float32, dev, (N, G))
+        _need(rstd, "rstd", torch.float32, dev, (N, G))
     dx = torch.empty_like(x)
     dgate = None if gate is None else torch.empty_like(x)
-    dw = torch.empty(C, dtype=torch.float32, device=dev) if need_params else None
-    db = torch.empty(C, dtype=torch.float32, device=dev) if need_params else None
+    dw = db = None
+    if need_params:
+        dw, db = torch.empty((2, C), dtype=torch.float32, device=dev).unbind(0)
     lib = _lib.load()
     need = lib.gdn_group_norm_act_bwd_workspace_size(N, L, C, G, _DT[x.dtype])
     workspace, ws_bytes = _scratch(need, "gdn_group_norm_act_bwd", workspace, dev)

@@ -13,14 +13,45 @@ from typing import Optional, Tuple
 import torch
 
 from . import _lib
-from .api import (DEVICE_ERRORS_DOC, _DT, _need, _ptr, _raise_on_status, _scale, _status, _stream)
+from .api import DEVICE_ERRORS_DOC, _DT, _need, _ptr, _raise_on_status, _scale, _status
 
 __all__ = ["chunk_linear_attn", "chunk_linear_attn_bwd", "chunk_linear_attn_trainable",
            "linear_attn_decode"]
 
 
+def _fit(dev, *wanted) -> bool:
+    """Whether every (tensor or None, dtype, shape) is contiguous, on ``dev`` and as said.  One quick
+    test for the usual case (a decode step's call takes longer on the host than on the device);
+    where it fails, the caller goes through ``_need`` one by one for the message."""
+    try:
+        for t, dtype, shape in wanted:
+            if t is not None and not (t.dtype is dtype and t.shape == shape and t.device == dev
+                                      and t.is_contiguous()):
+                return False
+        return True
+    except AttributeError:
+        return False
+
+
+def _stream(dev) -> int:
+    """The current stream's handle (without a Stream object around it)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _inputs(q, k, v, log_decay, cu_seqlens):
     """Checks shared by the chunked calls; returns (device, dtype, sizes, N)."""
+    if (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 4 and q.dtype in _DT
+            and isinstance(v, torch.Tensor) and v.dim() == 4):
+        dev, dt = q.device, q.dtype
+        B, T, Hqk, K = q.shape
+        Hv, V = v.shape[2:]
+        if _fit(dev, (q, dt, (B, T, Hqk, K)), (k, dt, (B, T, Hqk, K)), (v, dt, (B, T, Hv, V)),
+                (log_decay, torch.float32, (Hv,))) and log_decay is not None and k is not None:
+            if cu_seqlens is None:
+                return dev, dt, (B, T, Hqk, Hv, K, V), B
+            if B == 1 and _fit(dev, (cu_seqlens, torch.int32, cu_seqlens.shape)) \
+                    and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] > 0:
+                return dev, dt, (B, T, Hqk, Hv, K, V), cu_seqlens.shape[0] - 1
     _need(q, "q", (torch.float32, torch.bfloat16))
     dev, dt = q.device, q.dtype
     if q.dim() != 4:
@@ -75,17 +106,19 @@ def chunk_linear_attn(q, k, v, log_decay, scale=None, initial_state=None, output
         st_shape = (num_slots, Hv, K, V)
         if output_final_state and final_state is None:
             final_state = initial_state
-    if initial_state is not None:
-        _need(initial_state, "initial_state", torch.float32, dev, st_shape)
-    if output_final_state:
-        if final_state is None:
-            final_state = torch.empty(st_shape, dtype=torch.float32, device=dev)
-        _need(final_state, "final_state", torch.float32, dev, st_shape)
-    else:
+    if not output_final_state:
         final_state = None
+    if not _fit(dev, (initial_state, torch.float32, st_shape), (final_state, torch.float32, st_shape),
+                (out, dt, v.shape)):
+        for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
+            if t is not None:
+                _need(t, name, torch.float32, dev, st_shape)
+        if out is not None:
+            _need(out, "out", dt, dev, v.shape)
+    if output_final_state and final_state is None:
+        final_state = torch.empty(st_shape, dtype=torch.float32, device=dev)
     if out is None:
-        out = torch.empty((B, T, Hv, V), dtype=dt, device=dev)
-    _need(out, "out", dt, dev, (B, T, Hv, V))
+        out = torch.empty_like(v)
     L = _lib.load()
     need = L.gdn_linear_attn_chunk_fwd_workspace_size(B, T, Hqk, Hv, K, V, N, _DT[dt])
     workspace, ws_bytes = _scratch(need, "gdn_linear_attn_chunk_fwd", workspace, dev)
@@ -107,12 +140,13 @@ def chunk_linear_attn_bwd(q, k, v, log_decay, d_o, d_final_state=None, scale=Non
     ``gdn_linear_attn_chunk_bwd``: ``(dq, dk, dv, d_initial_state)``, the first three in q's
     dtype, the last fp32 [N, Hv, K, V] (None when ``need_d_initial_state`` is False)."""
     dev, dt, (B, T, Hqk, Hv, K, V), N = _inputs(q, k, v, log_decay, cu_seqlens)
-    _need(d_o, "d_o", dt, dev, (B, T, Hv, V))
     st_shape = (N, Hv, K, V)
-    if initial_state is not None:
-        _need(initial_state, "initial_state", torch.float32, dev, st_shape)
-    if d_final_state is not None:
-        _need(d_final_state, "d_final_state", torch.float32, dev, st_shape)
+    if d_o is None or not _fit(dev, (d_o, dt, v.shape), (initial_state, torch.float32, st_shape),
+                               (d_final_state, torch.float32, st_shape)):
+        _need(d_o, "d_o", dt, dev, (B, T, Hv, V))
+        for t, name in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
+            if t is not None:
+                _need(t, name, torch.float32, dev, st_shape)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     dh0 = torch.empty(st_shape, dtype=torch.float32, device=dev) if need_d_initial_state else None
     L = _lib.load()
@@ -171,25 +205,38 @@ def linear_attn_decode(q, k, v, log_decay, ssm_state, batch_indices=None, scale=
     batch_indices [n] int32 (-1 = padding: a zero row) or None (request i uses slot i).  Returns
     o [n, Hv, V].
     """
-    _need(q, "q", (torch.float32, torch.bfloat16))
-    dev, dt = q.device, q.dtype
-    if q.dim() != 3:
-        raise ValueError("q must be [n, Hqk, K]")
-    n, Hqk, K = q.shape
-    _need(k, "k", dt, dev, q.shape)
-    _need(v, "v", dt, dev)
-    if v.dim() != 3 or v.shape[0] != n:
-        raise ValueError("v must be [n, Hv, V]")
-    Hv, V = v.shape[1], v.shape[2]
-    _need(log_decay, "log_decay", torch.float32, dev, (Hv,))
-    _need(ssm_state, "ssm_state", torch.float32, dev)
-    if ssm_state.dim() != 4 or tuple(ssm_state.shape[1:]) != (Hv, K, V):
-        raise ValueError("ssm_state must be [num_slots, Hv, K, V]")
-    if batch_indices is not None:
-        _need(batch_indices, "batch_indices", torch.int32, dev, (n,))
+    usual = False
+    if isinstance(q, torch.Tensor) and isinstance(v, torch.Tensor) and q.dim() == 3 and v.dim() == 3:
+        dev, dt = q.device, q.dtype
+        n, Hqk, K = q.shape
+        Hv, V = v.shape[1:]
+        usual = (q.is_cuda and dt in _DT and k is not None and log_decay is not None
+                 and isinstance(ssm_state, torch.Tensor) and ssm_state.dim() == 4
+                 and _fit(dev, (q, dt, (n, Hqk, K)), (k, dt, (n, Hqk, K)), (v, dt, (n, Hv, V)),
+                          (log_decay, torch.float32, (Hv,)), (out, dt, (n, Hv, V)),
+                          (ssm_state, torch.float32, (ssm_state.shape[0], Hv, K, V)),
+                          (batch_indices, torch.int32, (n,))))
+    if not usual:
+        _need(q, "q", (torch.float32, torch.bfloat16))
+        dev, dt = q.device, q.dtype
+        if q.dim() != 3:
+            raise ValueError("q must be [n, Hqk, K]")
+        n, Hqk, K = q.shape
+        _need(k, "k", dt, dev, q.shape)
+        _need(v, "v", dt, dev)
+        if v.dim() != 3 or v.shape[0] != n:
+            raise ValueError("v must be [n, Hv, V]")
+        Hv, V = v.shape[1], v.shape[2]
+        _need(log_decay, "log_decay", torch.float32, dev, (Hv,))
+        _need(ssm_state, "ssm_state", torch.float32, dev)
+        if ssm_state.dim() != 4 or tuple(ssm_state.shape[1:]) != (Hv, K, V):
+            raise ValueError("ssm_state must be [num_slots, Hv, K, V]")
+        if batch_indices is not None:
+            _need(batch_indices, "batch_indices", torch.int32, dev, (n,))
+        if out is not None:
+            _need(out, "out", dt, dev, (n, Hv, V))
     if out is None:
-        out = torch.empty((n, Hv, V), dtype=dt, device=dev)
-    _need(out, "out", dt, dev, (n, Hv, V))
+        out = torch.empty_like(v)
     dev_status = _status(dev_status, check, dev)
     st = _lib.load().gdn_linear_attn_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
                                             _ptr(ssm_state), ssm_state.shape[0],
