@@ -36,8 +36,44 @@ __device__ __forceinline__ void fma4(float4& a, float s, const float4& x) {
   a.x = fmaf(s, x.x, a.x); a.y = fmaf(s, x.y, a.y);
   a.z = fmaf(s, x.z, a.z); a.w = fmaf(s, x.w, a.w);
 }
-__device__ __forceinline__ float dot4(const float4& a, const float4& b, float acc) {
-  return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, acc))));
+// Packed fp32: two multiply-adds an instruction.
+__device__ __forceinline__ float2 f2_fma(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+struct F4 {
+  float2 a, b;
+};
+__device__ __forceinline__ F4 f4(const float* p) {
+  const float4 x = *reinterpret_cast<const float4*>(p);
+  return F4{make_float2(x.x, x.y), make_float2(x.z, x.w)};
+}
+__device__ __forceinline__ void put4(float* p, const F4& x) {
+  *reinterpret_cast<float4*>(p) = make_float4(x.a.x, x.a.y, x.b.x, x.b.y);
+}
+__device__ __forceinline__ void fma4(F4& acc, float s, const F4& x) {
+  const float2 ss = make_float2(s, s);
+  acc.a = f2_fma(ss, x.a, acc.a);
+  acc.b = f2_fma(ss, x.b, acc.b);
+}
+__device__ __forceinline__ void scale4(F4& x, float s) {
+  x.a.x *= s; x.a.y *= s; x.b.x *= s; x.b.y *= s;
+}
+// The dot product of four pairs, its even and odd terms apart.
+__device__ __forceinline__ float2 dot4x2(const float4& a, const float4& b, float2 acc) {
+  acc = f2_fma(make_float2(a.x, a.y), make_float2(b.x, b.y), acc);
+  return f2_fma(make_float2(a.z, a.w), make_float2(b.z, b.w), acc);
+}
+
+// 16 bytes to shared memory asynchronously, or zeros (the source is not touched then).
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if (in) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else *reinterpret_cast<float4*>(dst) = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // Shared floats of the chunked pass: q, k rows padded by 4 (the rows that 16 threads read at
@@ -47,13 +83,14 @@ __host__ __device__ inline int la_smem_floats(int K, int V) {
 }
 
 // One CTA per (sequence, head, segment), 256 threads as 16 x 16; the state stays in shared memory.
-// Every product is register-blocked: P 4 x 4 a thread, o 4 x 8, X 8 x 8; what the mask takes away
-// of P and P V is left out by blocks.  Bound by the fp32 units (2.7 M multiply-adds a chunk at K =
+// Every product is register-blocked (P 4 x 4 a thread, o 4 x 8, X 8 x 8) in packed fp32, two
+// multiply-adds an instruction: two warps a scheduler, which is what the shared memory leaves, do
+// not hide the latencies of twice as many (34 us a chunk, now 23; 512 threads with half the block
+// each 39).  What the mask takes away of P and P V is left out by blocks.  Bound by the fp32 units (2.7 M multiply-adds a chunk at K =
 // V = 128, about 21k cycles of them).  Chains that do not fill the GPU are cut into segments as on
 // the tensor cores: a launch (`local_only`) for each segment's own contribution to the state, and
 // one from the entry states.  A chain's scratch holds a copy of its entry state (the exit state may
 // go to the same place), then the contributions in order, [K][V] each.
-template <typename T, typename TO>
 __global__ void __launch_bounds__(kLaThreads, 1)
     linear_attn_kernel(const LinAttnPass p, int segs, int local_only, float* scratch) {
   extern __shared__ __align__(16) float sm[];
@@ -116,34 +153,31 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
   }
   const int K4 = K / 4, V4 = V / 4;
-  const T* gq = reinterpret_cast<const T*>(p.q);
-  const T* gk = reinterpret_cast<const T*>(p.k);
-  const T* gv = reinterpret_cast<const T*>(p.v);
+  const float* gq = reinterpret_cast<const float*>(p.q);
+  const float* gk = reinterpret_cast<const float*>(p.k);
+  const float* gv = reinterpret_cast<const float*>(p.v);
   const int hq = h / (p.H / p.Hq), hk = h / (p.H / p.Hk), hv = h / (p.H / p.Hv);
   for (int cc = c0; cc < c1; ++cc) {
     const int ch = p.reverse ? nch - 1 - cc : cc;
     const int t0 = c.bos + ch * kChunk, L = min(kChunk, c.eos - t0);
     __syncthreads();
-    for (int e = tid; e < kChunk * K4; e += kLaThreads) {
-      const int t = e / K4, d = 4 * (e - t * K4);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (t < L) {
-        if (!local_only) x = load4(gq + ((size_t)(t0 + t) * p.Hq + hq) * K + d);
-        y = load4(gk + ((size_t)(t0 + t) * p.Hk + hk) * K + d);
-      }
-      *reinterpret_cast<float4*>(sQ + t * KS + d) = x;
-      *reinterpret_cast<float4*>(sK + t * KS + d) = y;
+    // q, k, v of the chunk, all copies in flight at once; rows past its end zero
+    for (int t = tid / K4; t < kChunk; t += kLaThreads / K4) {
+      const int d = 4 * (tid % K4);
+      if (tid / K4 >= kLaThreads / K4) break;   // (threads beyond the last whole row)
+      if (!local_only) copy16(sQ + t * KS + d, gq + ((size_t)(t0 + t) * p.Hq + hq) * K + d, t < L);
+      copy16(sK + t * KS + d, gk + ((size_t)(t0 + t) * p.Hk + hk) * K + d, t < L);
     }
-    for (int e = tid; e < kChunk * V4; e += kLaThreads) {
-      const int t = e / V4, d = 4 * (e - t * V4);
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (t < L) x = load4(gv + ((size_t)(t0 + t) * p.Hv + hv) * V + d);
-      *reinterpret_cast<float4*>(sV + t * V + d) = x;
+    for (int t = tid / V4; t < kChunk; t += kLaThreads / V4) {
+      const int d = 4 * (tid % V4);
+      if (tid / V4 >= kLaThreads / V4) break;
+      copy16(sV + t * V + d, gv + ((size_t)(t0 + t) * p.Hv + hv) * V + d, t < L);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     if (!local_only) {
       {   // P: rows ty + 16 i, columns tx + 16 j; blocks beyond the diagonal are masked
-        float acc[4][4] = {};
+        float2 acc[4][4] = {};
         for (int d = 0; d < K; d += 4) {
           float4 a[4], b[4];
 #pragma unroll
@@ -155,12 +189,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int j = i; j < 4; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
+              for (int j = i; j < 4; ++j) acc[i][j] = dot4x2(a[i], b[j], acc[i][j]);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int j = 0; j <= i; ++j) acc[i][j] = dot4(a[i], b[j], acc[i][j]);
+              for (int j = 0; j <= i; ++j) acc[i][j] = dot4x2(a[i], b[j], acc[i][j]);
           }
         }
 #pragma unroll
@@ -168,105 +202,95 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r = ty + 16 * i, s = tx + 16 * j, dist = p.reverse ? s - r : r - s;
-            sP[r * PS + s] = dist >= 0 ? p.s_in * sW[dist] * acc[i][j] : 0.f;
+            sP[r * PS + s] = dist >= 0 ? p.s_in * sW[dist] * (acc[i][j].x + acc[i][j].y) : 0.f;
           }
       }
       __syncthreads();
-      // o: rows 4 ty .. 4 ty + 3, columns 4 tx + 64 m .. + 3
+      // o: rows 4 ty .. + 3, columns 4 tx + 64 m .. + 3
+      {
+        const bool two = 4 * tx + 64 < V, one = 4 * tx < V;
+        F4 acc[2][4] = {};
+        auto rows = [&](const float* left, int stride, const float* right, int d0, int d1) {
+#pragma unroll 2
+          for (int d = d0; d < d1; d += 4) {
+            float4 a[4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const int col = 4 * tx + 64 * m;
-        if (col >= V) break;
-        float4 acc[4] = {};
-        for (int d = 0; d < K; d += 4) {
-          float4 a[4];
+            for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(left + (4 * ty + i) * stride + d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * KS + d);
+            for (int dd = 0; dd < 4; ++dd) {
+              const float* x = right + (d + dd) * V + 4 * tx;
+              const F4 x0 = one ? f4(x) : F4{}, x1 = two ? f4(x + 64) : F4{};
 #pragma unroll
-          for (int dd = 0; dd < 4; ++dd) {
-            const float4 x = *reinterpret_cast<const float4*>(sX + (d + dd) * V + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
+              for (int i = 0; i < 4; ++i) {
+                const float e = dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w;
+                fma4(acc[0][i], e, x0);
+                if (two) fma4(acc[1][i], e, x1);
+              }
+            }
           }
-        }
+        };
+        rows(sQ, KS, sX, 0, K);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * ty + i;
           const float w = sW[p.reverse ? max(0, L - 1 - r) : r + 1];
-          acc[i].x *= w; acc[i].y *= w; acc[i].z *= w; acc[i].w *= w;
+          scale4(acc[0][i], w);
+          scale4(acc[1][i], w);
         }
         // (P is zero on the far side of the diagonal, and from L on)
-        const int j0 = p.reverse ? 4 * ty : 0, j1 = p.reverse ? L : min(L, 4 * ty + 4);
-        for (int j = j0; j < j1; j += 4) {
-          float4 a[4];
+        rows(sP, PS, sV, p.reverse ? 4 * ty : 0, p.reverse ? L : min(L, 4 * ty + 4));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * PS + j);
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-          for (int dd = 0; dd < 4; ++dd) {
-            const float4 x = *reinterpret_cast<const float4*>(sV + (j + dd) * V + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              fma4(acc[i], dd == 0 ? a[i].x : dd == 1 ? a[i].y : dd == 2 ? a[i].z : a[i].w, x);
+          for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i, col = 4 * tx + 64 * m;
+            if (r >= L || col >= V) continue;
+            scale4(acc[m][i], p.s_out);
+            put4(reinterpret_cast<float*>(p.o) + ((size_t)(t0 + r) * p.H + h) * V + col, acc[m][i]);
           }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 4 * ty + i;
-          if (r >= L) continue;
-          float4 x = acc[i];
-          x.x *= p.s_out; x.y *= p.s_out; x.z *= p.s_out; x.w *= p.s_out;
-          store4(reinterpret_cast<TO*>(p.o) + ((size_t)(t0 + r) * p.H + h) * V + col, x);
-        }
       }
       if (last && cc + 1 == c1 && !c.fin) break;   // nobody wants the state any more
       __syncthreads();   // the state has been read
     }
-    // X: rows 4 ty + 64 a .. + 3, columns 4 tx + 64 b .. + 3
+    // X: rows 4 ty + 64 a .. + 3, columns 4 tx + 64 m .. + 3
     const float2 gl = sG[L == kChunk ? 0 : 1];
+    const bool two = 4 * tx + 64 < V, one = 4 * tx < V;
 #pragma unroll
     for (int ma = 0; ma < 2; ++ma) {
       const int row = 4 * ty + 64 * ma;
       if (row >= K) break;
-      float4 acc[2][4];
+      F4 acc[2][4];
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb) {
-        const int col = 4 * tx + 64 * mb;
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 x = col < V ? *reinterpret_cast<const float4*>(sX + (row + i) * V + col)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-          acc[mb][i] = make_float4(mul2(x.x, gl), mul2(x.y, gl), mul2(x.z, gl), mul2(x.w, gl));
+          const F4 x = (m ? two : one) ? f4(sX + (row + i) * V + 4 * tx + 64 * m) : F4{};
+          acc[m][i] = F4{make_float2(mul2(x.a.x, gl), mul2(x.a.y, gl)), make_float2(mul2(x.b.x, gl), mul2(x.b.y, gl))};
         }
-      }
-      const bool two = 4 * tx + 64 < V, one = 4 * tx < V;
+#pragma unroll 4
       for (int j = 0; j < L; ++j) {
         float4 kk = *reinterpret_cast<const float4*>(sK + j * KS + row);
         const float w = p.s_in * sW[p.reverse ? j + 1 : L - 1 - j];
         kk.x *= w; kk.y *= w; kk.z *= w; kk.w *= w;
-        if (one) {
-          const float4 x = *reinterpret_cast<const float4*>(sV + j * V + 4 * tx);
-          fma4(acc[0][0], kk.x, x);
-          fma4(acc[0][1], kk.y, x);
-          fma4(acc[0][2], kk.z, x);
-          fma4(acc[0][3], kk.w, x);
-        }
+        const float* x = sV + j * V + 4 * tx;
+        const F4 x0 = one ? f4(x) : F4{}, x1 = two ? f4(x + 64) : F4{};
+        fma4(acc[0][0], kk.x, x0);
+        fma4(acc[0][1], kk.y, x0);
+        fma4(acc[0][2], kk.z, x0);
+        fma4(acc[0][3], kk.w, x0);
         if (two) {
-          const float4 x = *reinterpret_cast<const float4*>(sV + j * V + 4 * tx + 64);
-          fma4(acc[1][0], kk.x, x);
-          fma4(acc[1][1], kk.y, x);
-          fma4(acc[1][2], kk.z, x);
-          fma4(acc[1][3], kk.w, x);
+          fma4(acc[1][0], kk.x, x1);
+          fma4(acc[1][1], kk.y, x1);
+          fma4(acc[1][2], kk.z, x1);
+          fma4(acc[1][3], kk.w, x1);
         }
       }
 #pragma unroll
-      for (int mb = 0; mb < 2; ++mb) {
-        const int col = 4 * tx + 64 * mb;
-        if (col < V) {
+      for (int m = 0; m < 2; ++m)
+        if (m ? two : one) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) *reinterpret_cast<float4*>(sX + (row + i) * V + col) = acc[mb][i];
+          for (int i = 0; i < 4; ++i) put4(sX + (row + i) * V + 4 * tx + 64 * m, acc[m][i]);
         }
-      }
     }
   }
   __syncthreads();
@@ -345,7 +369,6 @@ __global__ void __launch_bounds__(kLaThreads) linear_attn_decode_kernel(const Li
   }
 }
 
-template <typename T, typename TO>
 cudaError_t launch_pass(const LinAttnPass& p, int segs, float* scratch) {
   const long long chains = (long long)p.num_seqs * p.H;
   if (chains <= 0) return cudaSuccess;
@@ -355,17 +378,17 @@ cudaError_t launch_pass(const LinAttnPass& p, int segs, float* scratch) {
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev >= 64 || !attr_set[dev].load(std::memory_order_relaxed)) {
-    err = cudaFuncSetAttribute(linear_attn_kernel<T, TO>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    err = cudaFuncSetAttribute(linear_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                la_smem_floats(GDN_MAX_HEAD_DIM, GDN_MAX_HEAD_DIM) * (int)sizeof(float));
     if (err != cudaSuccess) return err;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
   const size_t smem = la_smem_floats(p.K, p.V) * sizeof(float);
   if (segs > 1) {
-    linear_attn_kernel<T, TO><<<(unsigned)(chains * (segs - 1)), kLaThreads, smem, p.stream>>>(p, segs, 1, scratch);
+    linear_attn_kernel<<<(unsigned)(chains * (segs - 1)), kLaThreads, smem, p.stream>>>(p, segs, 1, scratch);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
   }
-  linear_attn_kernel<T, TO><<<(unsigned)(chains * segs), kLaThreads, smem, p.stream>>>(p, segs, 0, scratch);
+  linear_attn_kernel<<<(unsigned)(chains * segs), kLaThreads, smem, p.stream>>>(p, segs, 0, scratch);
   return cudaGetLastError();
 }
 
@@ -378,7 +401,7 @@ int linear_attn_segments(long long chains, long long most_tokens, int num_sms, i
 }
 
 cudaError_t launch_linear_attn_generic(const LinAttnPass& p, int segs, float* scratch) {
-  return launch_pass<float, float>(p, segs, scratch);
+  return launch_pass(p, segs, scratch);
 }
 
 cudaError_t launch_linear_attn_fold(const float* const (&part)[2], void* const (&out)[2], long long T_total,
