@@ -31,7 +31,8 @@
 // state warps, which do this, are what a chunk waits for).  The terms go to TMEM as the A operand of U, which leaves the shared memory to four
 // stages of Q, K, V in flight (scaled K tiles in shared memory left room for two, and a chunk
 // took 4050 cycles: a stage's life is a memory latency of 2300 plus its way through the roles).
-// P and the X operand are rounded to bf16 once, like the output itself.
+// P and the X operand are rounded to bf16 once, like the output itself (P of a sequence of one chunk
+// has a second term, see write_p_rest).
 //
 // Where there are too few (sequence, head) chains to fill the GPU, each is cut into segments of
 // whole chunks: a first launch makes every segment's own contribution to the state (K, V and U
@@ -68,6 +69,7 @@ constexpr int kStages = 4;
 constexpr uint32_t kStage = 49152;                 // [k half][Q 64 rows | K 64 rows][128 B], V
 constexpr uint32_t kStageV = 32768;                // [v half][64 tokens][128 B]
 constexpr uint32_t OFF_P = kStages * kStage;       // [64 i][64 j] bf16
+constexpr uint32_t OFF_P_REST = kStage;   // (a sequence of one chunk leaves the second stage empty)
 constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 tokens][128 B]
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
 constexpr uint32_t OFF_F = OFF_W + 288;            // Weights4[2][16]: the weights of V~ in a full and
@@ -304,6 +306,11 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
       tc_fence_after();
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks) mma_ss(o, dV + so + 128 * ks, dP + 2 * ks, idO2, 1);
+      if (u.nch == 1) {
+        const uint32_t dR = desc_lo(sb + OFF_P_REST, 16);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_ss(o, dV + 128 * ks, dR + 2 * ks, idO2, 1);
+      }
       mma_commit(&bars[B_O + par]);
     }
     if (!u.store && i + 1 < n) {   // D = [Q; K] K^T of the next chunk
@@ -342,6 +349,27 @@ __device__ __noinline__ void clear_columns(uint8_t* tile, int row, int L) {
     *reinterpret_cast<uint16_t*>(tile + sw128_offset(row, j)) = (uint16_t)0;
 }
 
+// What the rounding of P left, as a second tile: for a sequence of one chunk, whose outputs have as
+// few entries of P as factors as they have tokens before them (one token: one), so that its error
+// would not average out.  (A second term for every chunk took 9 to 17% more time.)
+__device__ __noinline__ void write_p_rest(uint8_t* sm, uint32_t d, int row, const float4* f4, float inv) {
+#pragma unroll 1
+  for (int half = 0; half < 2; ++half) {
+    float x[32];
+    tmem_ld32(d + 32 * half, x);
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const float4 f = f4[8 * half + g];
+      const float t[4] = {f.x * (inv * x[4 * g]), f.y * (inv * x[4 * g + 1]), f.z * (inv * x[4 * g + 2]),
+                          f.w * (inv * x[4 * g + 3])};
+      uint2 q;
+      q.x = pack2(t[0] - __bfloat162float(__float2bfloat16_rn(t[0])), t[1] - __bfloat162float(__float2bfloat16_rn(t[1])));
+      q.y = pack2(t[2] - __bfloat162float(__float2bfloat16_rn(t[2])), t[3] - __bfloat162float(__float2bfloat16_rn(t[3])));
+      *reinterpret_cast<uint2*>(sm + OFF_P_REST + sw128_offset(row, 32 * half + 4 * g)) = q;
+    }
+  }
+}
+
 __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase,
                        uint64_t* bars) {
   const int lane = threadIdx.x & 31, wq = (threadIdx.x >> 5) & 1, row = 32 * wq + lane;
@@ -378,6 +406,10 @@ __device__ bool p_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_
       }
     }
     if (L < kChunk) clear_columns(sm + OFF_P, row, L);
+    if (u.nch == 1) {
+      write_p_rest(sm, tbase + lane_off + COL_D, row, f4, inv);
+      clear_columns(sm + OFF_P_REST, row, L);
+    }
     tc_fence_before();
     fence_proxy_async_smem();
     warp_arrive(&bars[B_P], lane);
