@@ -18,91 +18,83 @@ namespace {
 
 // ------------------------------------------------------------------ groups in registers
 constexpr int kRowSteps = 4;
+constexpr int kRowValues = 32;   // values a lane holds
+constexpr int kRowPerSm = 4;     // CTAs an SM (registers)
 
 template <typename T, int V, int VPT, bool kGate>
-__global__ void __launch_bounds__(kGnThreads) gn_row_fwd_kernel(const GroupNormArgs a, const RowPlan q) {
+__global__ void __launch_bounds__(kGnThreads, VPT == 1 ? kRowPerSm : 1) gn_row_fwd_kernel(const GroupNormArgs a, const RowPlan q) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kIn = kGate ? 2 : 1;
-  Ring<T, V, VPT * kIn, kRowSteps> ring(smem);
+  using P = Pair<V>;
+  constexpr int kIn = kGate ? 2 : 1, kP = kPairs<V>;
   const RowPlace p = row_place(q, a.G);
   const RowVectors<V, VPT> at(q, p, a.L, a.C, a.G);
   const float inv = 1.f / ((float)a.L * (float)(a.C / a.G));
-  float w[VPT][V], b[VPT][V];
+  P w[VPT][kP], b[VPT][kP];
+  const RowRange rg = row_range(q, p, a.N);
+  size_t from[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k)
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      w[k][j] = at.in[k] ? param(a.weight, at.c[k] + j, a.wb_dtype, 1.f) : 0.f;
-      b[k][j] = at.in[k] ? param(a.bias, at.c[k] + j, a.wb_dtype, 0.f) : 0.f;
+  for (int k = 0; k < VPT; ++k) {
+    from[k] = (size_t)rg.n0 * a.L * a.C + (size_t)p.g * (a.C / a.G) + at.off[k];
+    if (at.in[k]) {
+      params<V>(a.weight, at.c[k], a.wb_dtype, 1.f, w[k]);
+      params<V>(a.bias, at.c[k], a.wb_dtype, 0.f, b[k]);
     }
-  const size_t row = (size_t)a.L * a.C, col = (size_t)p.g * (a.C / a.G);
-  const long long step = (long long)q.sets * q.down;
-  long long n = (long long)p.set * q.down + p.down;
-  auto load = [&](int ahead) {
-    const long long m = n + ahead * step;
-    if (m < a.N) {
+  }
+  const void* src[kIn];
+  src[0] = a.x;
+  if (kGate) src[kIn - 1] = a.gate;
+  const size_t stride = (size_t)rg.step * a.L * a.C;
+  walk<T, V, VPT, kIn, kRowSteps>(smem, src, from, at.in, stride, rg.mine, rg.turns, [&](auto& ring, int u, int t, size_t here) {
+    // about the group's first value: the mean, then the squared deviations
+    P v[VPT][kP];
 #pragma unroll
-      for (int k = 0; k < VPT; ++k)
-        if (at.in[k]) {
-          ring.put(ahead, kIn * k, a.x, m * row + col + at.off[k]);
-          if (kGate) ring.put(ahead, kIn * k + kIn - 1, a.gate, m * row + col + at.off[k]);
-        }
-    }
-    ring.commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kRowSteps - 1; ++i) load(i);
-  // (every lane of a warp runs the same number of turns: the shuffles want them all)
-  const int turns = (int)((a.N + step - 1) / step);
-  for (int t = 0; t < turns; ++t, n += step, ring.next()) {
-    load(kRowSteps - 1);
-    ring.wait();
-    float v[VPT][V];
-    // mean from the first element, then the squared deviations
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const Pack<T, V> x = ring.get(kIn * k);
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[k][j] = to_f(x.e[j]);
-    }
-    const float x0 = __shfl_sync(0xffffffffu, v[0][0], 0, q.lanes);
-    float s = 0.f;
+    for (int k = 0; k < VPT; ++k) unpack<V>(ring.get(u, kIn * k), v[k]);
+    float x0;
+    if constexpr (V == 1) x0 = v[0][0];
+    else x0 = v[0][0].x;
+    x0 = __shfl_sync(0xffffffffu, x0, 0, q.lanes);
+    P s = both<P>(0.f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
       if (at.in[k]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) s += v[k][j] - x0;
+        for (int i = 0; i < kP; ++i) {
+          v[k][i] = add(v[k][i], both<P>(-x0));
+          s = add(s, v[k][i]);
+        }
       }
-    const float mean = x0 + sub_sum(s, q.lanes) * inv;
-    s = 0.f;
+    const float d = sub_sum(sum(s), q.lanes) * inv;
+    s = both<P>(0.f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
       if (at.in[k]) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          v[k][j] -= mean;
-          s = fmaf(v[k][j], v[k][j], s);
+        for (int i = 0; i < kP; ++i) {
+          v[k][i] = add(v[k][i], both<P>(-d));
+          s = fma(v[k][i], v[k][i], s);
         }
       }
-    const float rstd = rsqrtf(fmaf(sub_sum(s, q.lanes), inv, a.eps));
-    if (n >= a.N || !p.live) continue;
+    const float rstd = rsqrtf(fmaf(sub_sum(sum(s), q.lanes), inv, a.eps));
+    if (t >= rg.mine || !p.live) return;
     if (p.l == 0) {
-      if (a.mean) a.mean[n * a.G + p.g] = mean;
+      const long long n = rg.n0 + (long long)t * rg.step;
+      if (a.mean) a.mean[n * a.G + p.g] = x0 + d;
       if (a.rstd) a.rstd[n * a.G + p.g] = rstd;
     }
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
       if (at.in[k]) {
         Pack<T, V> y;
-        if (kGate) y = ring.get(kIn * k + kIn - 1);
+        P z[kP];
+        if (kGate) unpack<V>(ring.get(u, kIn * k + kIn - 1), z);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float u = fmaf(v[k][j] * rstd, w[k][j], b[k][j]);
-          from_f(y.e[j], kGate ? u * act_value(to_f(y.e[j]), a.act) : act_value(u, a.act));
+        for (int i = 0; i < kP; ++i) {
+          const P h = fma(mul(v[k][i], both<P>(rstd)), w[k][i], b[k][i]);
+          pack<V>(y, i, kGate ? mul(h, act_value(z[i], a.act)) : act_value(h, a.act));
         }
-        store_pack<T, V>(a.y, n * row + col + at.off[k], y);
+        store_pack<T, V>(a.y, from[k] + here, y);
       }
-  }
+  });
 }
 
 // ------------------------------------------------------------------ slabs
@@ -122,44 +114,49 @@ template <int kPacks>
 constexpr int slab_steps = kPacks == 1 ? 8 : 4;
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kGnThreads) gn_slab_stats_kernel(const GroupNormArgs a, const SlabPlan s,
+__global__ void __launch_bounds__(kGnThreads, kSlabPerSm) gn_slab_stats_kernel(const GroupNormArgs a, const SlabPlan s,
                                                                    float2* part) {
   __shared__ float sn[kGnThreads], sm[kGnThreads], sq[kGnThreads];
   extern __shared__ __align__(16) uint8_t smem[];
+  using P = Pair<V>;
+  constexpr int kP = kPairs<V>;
   const SlabPlace p = slab_place(s, a.C, a.G);
-  const int2 rr = slab_rows(s, p, a.L);
+  const SlabRange rr = slab_range(s, p, a.L, a.C);
   Moments mo{0.f, 0.f, 0.f};
   if (p.on) {
-    constexpr int kSlabSteps = slab_steps<1>;
-    Ring<T, V, 1, kSlabSteps> ring(smem);
-    const size_t base = (size_t)p.n * a.L * a.C + p.c;
-    int r = rr.x + p.row;
+    // Eight rows at a time: sums and squares about the mean of the first pack (so that squares much
+    // larger than the deviations cannot stand in one block), then merged.
+    float pivot = 0.f, n = 0.f;
+    P s1 = both<P>(0.f), s2 = both<P>(0.f);
+    auto close = [&] {
+      const float t = sum(s1), f = __fdividef(1.f, n);
+      merge(mo, n, fmaf(t, f, pivot), fmaxf(fmaf(-t * f, t, sum(s2)), 0.f));
+    };
+    const void* src[1] = {a.x};
+    const size_t from[1] = {rr.from};
+    const bool in[1] = {true};
+    walk<T, V, 1, 1, slab_steps<1>>(smem, src, from, in, rr.stride, rr.rows, rr.rows,
+                                    [&](auto& ring, int u, int t, size_t) {
+      P v[kP];
+      unpack<V>(ring.get(u, 0), v);
+      if (u == 0) {
+        if (t > 0) close();
+        P m = v[0];
 #pragma unroll
-    for (int i = 0; i < kSlabSteps - 1; ++i) {
-      if (r + i * p.step < rr.y) ring.put(i, 0, a.x, base + (size_t)(r + i * p.step) * a.C);
-      ring.commit();
-    }
-    for (; r < rr.y; r += p.step, ring.next()) {
-      const int ahead = r + (kSlabSteps - 1) * p.step;
-      if (ahead < rr.y) ring.put(kSlabSteps - 1, 0, a.x, base + (size_t)ahead * a.C);
-      ring.commit();
-      ring.wait();
-      const Pack<T, V> x = ring.get(0);
-      float v[V], t = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        v[j] = to_f(x.e[j]);
-        t += v[j];
+        for (int i = 1; i < kP; ++i) m = add(m, v[i]);
+        pivot = sum(m) * (1.f / V);
+        s1 = s2 = both<P>(0.f);
+        n = 0.f;
       }
-      const float mean = t * (1.f / V);   // (V is a power of two)
-      t = 0.f;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float d = v[j] - mean;
-        t = fmaf(d, d, t);
+      for (int i = 0; i < kP; ++i) {
+        const P d = add(v[i], both<P>(-pivot));
+        s1 = add(s1, d);
+        s2 = fma(d, d, s2);
       }
-      merge(mo, (float)V, mean, t);
-    }
+      n += (float)V;
+    });
+    if (rr.rows > 0) close();
   }
   sn[threadIdx.x] = mo.n;
   sm[threadIdx.x] = mo.mean;
@@ -234,50 +231,40 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_merge_kernel(const GroupNo
 }
 
 template <typename T, int V, bool kGate>
-__global__ void __launch_bounds__(kGnThreads) gn_slab_fwd_kernel(const GroupNormArgs a, const SlabPlan s,
+__global__ void __launch_bounds__(kGnThreads, kSlabPerSm) gn_slab_fwd_kernel(const GroupNormArgs a, const SlabPlan s,
                                                                  const float2* stats) {
   extern __shared__ __align__(16) uint8_t smem[];
+  using P = Pair<V>;
+  constexpr int kIn = kGate ? 2 : 1, kP = kPairs<V>;
   const SlabPlace p = slab_place(s, a.C, a.G);
   if (!p.on) return;
-  const int2 rr = slab_rows(s, p, a.L);
+  const SlabRange rr = slab_range(s, p, a.L, a.C);
   const float2 st = stats[(size_t)p.n * a.G + p.g];
-  float w[V], b[V];
+  P w[kP], b[kP];
+  params<V>(a.weight, p.c, a.wb_dtype, 1.f, w);
+  params<V>(a.bias, p.c, a.wb_dtype, 0.f, b);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    w[j] = param(a.weight, p.c + j, a.wb_dtype, 1.f);
-    b[j] = param(a.bias, p.c + j, a.wb_dtype, 0.f);
-  }
-  const size_t base = (size_t)p.n * a.L * a.C + p.c;
-  constexpr int kIn = kGate ? 2 : 1, kSlabSteps = slab_steps<kIn>;
-  Ring<T, V, kIn, kSlabSteps> ring(smem);
-  int r = rr.x + p.row;
-  auto load = [&](int i) {
-    const int m = r + i * p.step;
-    if (m < rr.y) {
-      ring.put(i, 0, a.x, base + (size_t)m * a.C);
-      if (kGate) ring.put(i, kIn - 1, a.gate, base + (size_t)m * a.C);
-    }
-    ring.commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kSlabSteps - 1; ++i) load(i);
-  for (; r < rr.y; r += p.step, ring.next()) {
-    load(kSlabSteps - 1);
-    ring.wait();
-    const Pack<T, V> x = ring.get(0);
+  for (int i = 0; i < kP; ++i) w[i] = mul(w[i], both<P>(st.y));
+  const void* src[kIn];
+  src[0] = a.x;
+  if (kGate) src[kIn - 1] = a.gate;
+  const size_t from[1] = {rr.from};
+  const bool in[1] = {true};
+  walk<T, V, 1, kIn, slab_steps<kIn>>(smem, src, from, in, rr.stride, rr.rows, rr.rows,
+                                      [&](auto& ring, int u, int, size_t here) {
+    P v[kP], z[kP];
+    unpack<V>(ring.get(u, 0), v);
+    if (kGate) unpack<V>(ring.get(u, kIn - 1), z);
     Pack<T, V> y;
-    if (kGate) y = ring.get(kIn - 1);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float u = fmaf((to_f(x.e[j]) - st.x) * st.y, w[j], b[j]);
-      from_f(y.e[j], kGate ? u * act_value(to_f(y.e[j]), a.act) : act_value(u, a.act));
+    for (int i = 0; i < kP; ++i) {
+      const P h = fma(add(v[i], both<P>(-st.x)), w[i], b[i]);
+      pack<V>(y, i, kGate ? mul(h, act_value(z[i], a.act)) : act_value(h, a.act));
     }
-    store_pack<T, V>(a.y, base + (size_t)r * a.C, y);
-  }
+    store_pack<T, V>(a.y, rr.from + here, y);
+  });
 }
 
-constexpr int kRowValues = 32;   // values a lane holds in the row form
-constexpr int kRowPerSm = 5;     // its CTAs an SM (registers)
 
 template <typename T, int V, int VPT, bool kGate>
 cudaError_t launch_row_fwd(const GroupNormArgs& a, const RowPlan& r) {

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "gdn.h"
 #include "gdn_common.cuh"
@@ -14,6 +15,7 @@ namespace gdn {
 namespace {
 
 constexpr int kGnThreads = 256;
+constexpr int kSlabPerSm = 4;   // CTAs an SM in the slab form (registers)
 
 // V consecutive elements in one load: V sizeof(T) is 2, 4, 8 or 16 bytes.
 template <int kBytes> struct Raw;
@@ -26,10 +28,100 @@ template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
   T e[V];
 };
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f(float& d, float x) { d = x; }
-__device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+// The arithmetic, on pairs (two values an instruction), or on one where a pack holds one.
+template <int V> using Pair = std::conditional_t<V == 1, float, float2>;
+template <int V> constexpr int kPairs = V == 1 ? 1 : V / 2;
+__device__ __forceinline__ unsigned long long bits(float2 a) { return *reinterpret_cast<unsigned long long*>(&a); }
+__device__ __forceinline__ float2 pair_of(unsigned long long a) { return *reinterpret_cast<float2*>(&a); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair_of(d);
+}
+__device__ __forceinline__ float2 mul(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair_of(d);
+}
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair_of(d);
+}
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float sum(float2 a) { return a.x + a.y; }
+__device__ __forceinline__ float sum(float a) { return a; }
+template <typename P> __device__ __forceinline__ P both(float x);
+template <> __device__ __forceinline__ float2 both<float2>(float x) { return make_float2(x, x); }
+template <> __device__ __forceinline__ float both<float>(float x) { return x; }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
+
+// 1 / (1 + 2^(-x log2 e)); and the activation's value and slope s (1 + x (1 - s)).
+template <typename P>
+__device__ __forceinline__ P sigmoid(P x) {
+  return rcp(add(ex2(mul(x, both<P>(-1.4426950408889634f))), both<P>(1.f)));
+}
+template <typename P>
+__device__ __forceinline__ P act_value(P x, int act) {
+  return act == GDN_ACT_SILU ? mul(x, sigmoid(x)) : x;
+}
+template <typename P>
+__device__ __forceinline__ P act_both(P x, int act, P* slope) {
+  if (act != GDN_ACT_SILU) {
+    *slope = both<P>(1.f);
+    return x;
+  }
+  const P s = sigmoid(x), v = mul(x, s);
+  *slope = fma(v, fma(s, both<P>(-1.f), both<P>(1.f)), s);
+  return v;
+}
+
+template <int V>
+__device__ __forceinline__ void unpack(const Pack<float, V>& p, Pair<V> (&v)[kPairs<V>]) {
+  if constexpr (V == 1) v[0] = p.e[0];
+  else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = make_float2(p.e[2 * i], p.e[2 * i + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, V>& p, Pair<V> (&v)[kPairs<V>]) {
+  if constexpr (V == 1) v[0] = __bfloat162float(p.e[0]);
+  else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const uint32_t u = reinterpret_cast<const uint32_t*>(p.e)[i];
+      v[i] = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void pack(Pack<float, V>& p, int i, Pair<V> v) {
+  if constexpr (V == 1) p.e[0] = v;
+  else {
+    p.e[2 * i] = v.x;
+    p.e[2 * i + 1] = v.y;
+  }
+}
+template <int V>
+__device__ __forceinline__ void pack(Pack<__nv_bfloat16, V>& p, int i, Pair<V> v) {
+  if constexpr (V == 1) p.e[0] = __float2bfloat16_rn(v);
+  else reinterpret_cast<__nv_bfloat162*>(p.e)[i] = __float22bfloat162_rn(v);
+}
 
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load_pack(const void* base, size_t at) {
@@ -46,54 +138,72 @@ __device__ __forceinline__ void store_pack(void* base, size_t at, const Pack<T, 
 
 // A thread's own ring of packs in shared memory, filled by asynchronous copies (no registers and
 // no other thread involved: only its own group count is waited for).  kPacks packs a step, kSteps
-// steps deep, of which kSteps - 1 are on their way while one is used.  2-byte packs, which such
-// copies do not move, are copied at once.
+// steps deep.  2-byte packs, which such copies do not move, are copied at once.
 template <typename T, int V, int kPacks, int kSteps>
 struct Ring {
   static constexpr int kBytes = V * (int)sizeof(T);
   static constexpr int kShared = kSteps * kPacks * kBytes * kGnThreads;
   uint8_t* mine;
-  int at = 0;   // the step that `get` reads and the next `put` ends up behind
   __device__ __forceinline__ explicit Ring(void* smem) : mine(reinterpret_cast<uint8_t*>(smem) + threadIdx.x * kBytes) {}
   __device__ __forceinline__ uint8_t* slot(int step, int i) const {
     return mine + (step * kPacks + i) * kBytes * kGnThreads;
   }
-  // Pack i of a step that is `ahead` steps behind the one read now.
-  __device__ __forceinline__ void put(int ahead, int i, const void* base, size_t elem) {
-    int st = at + ahead;
-    if (st >= kSteps) st -= kSteps;
-    const T* src = reinterpret_cast<const T*>(base) + elem;
-    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot(st, i));
+  __device__ __forceinline__ void put(int step, int i, const T* src) {
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot(step, i));
     if (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else if (kBytes >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes < 4 ? 4 : kBytes) : "memory");
-    else *reinterpret_cast<Pack<T, V>*>(slot(st, i)) = load_pack<T, V>(base, elem);
+    else *reinterpret_cast<Pack<T, V>*>(slot(step, i)) = load_pack<T, V>(src, 0);
   }
-  __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-  // Waits for the step to be read (all but the kSteps - 1 newest groups).
-  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 1) : "memory"); }
-  __device__ __forceinline__ Pack<T, V> get(int i) const {
-    Pack<T, V> p;
-    using R = typename Raw<kBytes>::type;
-    *reinterpret_cast<R*>(&p) = *reinterpret_cast<const R*>(slot(at, i));
-    return p;
-  }
-  __device__ __forceinline__ void next() { at = at + 1 == kSteps ? 0 : at + 1; }
+  __device__ __forceinline__ Pack<T, V> get(int step, int i) const { return load_pack<T, V>(slot(step, i), 0); }
 };
 
-// weight (default 1) or bias (default 0) of channel c.
-__device__ __forceinline__ float param(const void* p, int c, int dtype, float none) {
-  return p ? load_elem(p, c, dtype) : none;
+// Walks over `turns` turns of VPT places, `stride` elements from one turn to the next, with kIn
+// tensors a place: f(ring, step, turn, distance) finds tensor i of place k as ring.get(step, kIn k
+// + i).  Of each place `mine` turns are read, and only where in[k]; the copies run kSteps - 1 turns
+// ahead.  (Unrolled over the ring, so that its steps are constants.)
+template <typename T, int V, int VPT, int kIn, int kSteps, class F>
+__device__ __forceinline__ void walk(void* smem, const void* const (&src)[kIn], const size_t (&at)[VPT],
+                                     const bool (&in)[VPT], size_t stride, int mine, int turns, F&& f) {
+  Ring<T, V, VPT * kIn, kSteps> ring(smem);
+  size_t ahead = 0, here = 0;   // distances of the next copies, and of the turn at hand
+  auto load = [&](int step, int t) {
+    if (t < mine) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+        if (in[k]) {
+#pragma unroll
+          for (int i = 0; i < kIn; ++i)
+            ring.put(step, kIn * k + i, reinterpret_cast<const T*>(src[i]) + (at[k] + ahead));
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += stride;
+  };
+#pragma unroll
+  for (int i = 0; i < kSteps - 1; ++i) load(i, i);
+  for (int t0 = 0; t0 < turns; t0 += kSteps) {
+#pragma unroll
+    for (int u = 0; u < kSteps; ++u) {
+      if (t0 + u >= turns) break;
+      load((u + kSteps - 1) % kSteps, t0 + u + kSteps - 1);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 1) : "memory");
+      f(ring, u, t0 + u, here);
+      here += stride;
+    }
+  }
 }
 
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float act_value(float x, int act) {
-  return act == GDN_ACT_SILU ? x * sigmoid_fast(x) : x;
-}
-// Value and slope.
-__device__ __forceinline__ float2 act_both(float x, int act) {
-  if (act != GDN_ACT_SILU) return make_float2(x, 1.f);
-  const float s = sigmoid_fast(x);
-  return make_float2(x * s, s * (1.f + x * (1.f - s)));
+// weight (default 1) or bias (default 0) of the V channels from c.
+template <int V>
+__device__ __forceinline__ void params(const void* p, int c, int dtype, float none, Pair<V> (&v)[kPairs<V>]) {
+  float x[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = p ? load_elem(p, c + j, dtype) : none;
+  if constexpr (V == 1) v[0] = x[0];
+  else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) v[i] = make_float2(x[2 * i], x[2 * i + 1]);
+  }
 }
 
 // How the slabs of L > 1 positions (or groups too wide for a warp) are cut.  A CTA takes `rows`
@@ -130,8 +240,8 @@ inline SlabPlan slab_plan(int N, int L, int C, int G, int io_dtype) {
   }
   const int cols = s.parts == 1 ? s.GPB * s.DV : kGnThreads;
   const int step = kGnThreads / cols;               // rows that a CTA takes at a time
-  // one wave of five CTAs an SM, each thread at least four rows
-  const long long want = std::max(1LL, 152LL * 5 / ((long long)N * s.NCB));
+  // one wave, each thread at least four rows
+  const long long want = std::max(1LL, 152LL * kSlabPerSm / ((long long)N * s.NCB));
   const long long most = (L + 4LL * step - 1) / (4LL * step);
   const long long chunks = want < most ? want : most;
   s.rows = (int)((L + chunks - 1) / chunks);
@@ -177,9 +287,14 @@ __device__ __forceinline__ SlabPlace slab_place(const SlabPlan& s, int C, int G)
   p.g = s.parts == 1 ? p.g0 + p.col / s.DV : p.g0;
   return p;
 }
-// Positions [r0, r1) of a chunk.
-__device__ __forceinline__ int2 slab_rows(const SlabPlan& s, const SlabPlace& p, int L) {
-  return make_int2(p.chunk * s.rows, min(L, (p.chunk + 1) * s.rows));
+// A thread's rows: its first element, elements from a row to its next, how many.
+struct SlabRange {
+  size_t from, stride;
+  int rows;
+};
+__device__ __forceinline__ SlabRange slab_range(const SlabPlan& s, const SlabPlace& p, int L, int C) {
+  const int r = p.chunk * s.rows + p.row, end = min(L, (p.chunk + 1) * s.rows);
+  return SlabRange{((size_t)p.n * L + r) * C + p.c, (size_t)p.step * C, r < end ? (end - r + p.step - 1) / p.step : 0};
 }
 
 // Groups that up to 32 lanes hold in registers: lanes a group (a power of two), vectors a lane
@@ -226,6 +341,20 @@ __device__ __forceinline__ RowPlace row_place(const RowPlan& q, int G) {
   if (!p.live) p.g = 0;
   return p;
 }
+// Its rows n0, n0 + step, ...: how many, and how many turns its CTA takes (every lane of a warp runs
+// the same number of them: the shuffles want them all).
+struct RowRange {
+  long long n0, step;
+  int mine, turns;
+};
+__device__ __forceinline__ RowRange row_range(const RowPlan& q, const RowPlace& p, int N) {
+  RowRange r;
+  r.step = (long long)q.sets * q.down;
+  r.n0 = (long long)p.set * q.down + p.down;
+  r.turns = (int)((N + r.step - 1) / r.step);
+  r.mine = r.n0 < N ? (int)((N - r.n0 + r.step - 1) / r.step) : 0;
+  return r;
+}
 // Where this lane's vectors stand in a group (from its first element), their channels, and whether
 // they are in it.
 template <int V, int VPT>
@@ -259,7 +388,9 @@ cudaError_t allow_shared() {
 }
 
 __device__ __forceinline__ float sub_sum(float x, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
 

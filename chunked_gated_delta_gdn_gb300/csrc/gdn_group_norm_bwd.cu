@@ -18,17 +18,15 @@ namespace gdn {
 namespace {
 
 // xhat and du of one element (and dz).
-template <bool kGate>
-__device__ __forceinline__ float grad_u(float x, float dy, float z, float mean, float rstd, float w, float b,
-                                        int act, float* xhat, float* dz) {
-  const float xh = (x - mean) * rstd, u = fmaf(xh, w, b);
+template <bool kGate, typename P>
+__device__ __forceinline__ P grad_u(P x, P dy, P z, float mean, float rstd, P w, P b, int act, P* xhat, P* dz) {
+  const P xh = mul(add(x, both<P>(-mean)), both<P>(rstd)), u = fma(xh, w, b);
+  P slope;
   *xhat = xh;
-  if (kGate) {
-    const float2 s = act_both(z, act);
-    *dz = dy * u * s.y;
-    return dy * s.x;
-  }
-  return dy * act_both(u, act).y;
+  const P value = act_both(kGate ? z : u, act, &slope);
+  if (!kGate) return mul(dy, slope);
+  *dz = mul(mul(dy, u), slope);
+  return mul(dy, value);
 }
 
 // Adds up part[set][2][C] over the sets in a fixed order: channel c0 + threadIdx.x % 32, every
@@ -64,93 +62,85 @@ __global__ void __launch_bounds__(1024) gn_sum_sets_kernel(const GroupNormArgs a
 
 // ------------------------------------------------------------------ groups in registers
 constexpr int kRowSteps = 3;
+constexpr int kRowValues = 16;   // values a lane holds
+constexpr int kRowPerSm = 3;     // CTAs an SM (registers)
 
 template <typename T, int V, int VPT, bool kGate>
-__global__ void __launch_bounds__(kGnThreads) gn_row_bwd_kernel(const GroupNormArgs a, const RowPlan q, float* part) {
+__global__ void __launch_bounds__(kGnThreads, VPT == 1 ? kRowPerSm : 1) gn_row_bwd_kernel(const GroupNormArgs a, const RowPlan q, float* part) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kIn = kGate ? 3 : 2;
-  Ring<T, V, VPT * kIn, kRowSteps> ring(smem);
+  using P = Pair<V>;
+  constexpr int kIn = kGate ? 3 : 2, kP = kPairs<V>;
   const RowPlace p = row_place(q, a.G);
   const RowVectors<V, VPT> at(q, p, a.L, a.C, a.G);
   const int D = a.C / a.G;
   const float inv = 1.f / ((float)a.L * (float)D);
-  float w[VPT][V], b[VPT][V], A[VPT][V], B[VPT][V];
+  P w[VPT][kP], b[VPT][kP], A[VPT][kP], B[VPT][kP];
+  const RowRange rg = row_range(q, p, a.N);
+  size_t from[VPT];
 #pragma unroll
-  for (int k = 0; k < VPT; ++k)
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      w[k][j] = at.in[k] ? param(a.weight, at.c[k] + j, a.wb_dtype, 1.f) : 0.f;
-      b[k][j] = at.in[k] ? param(a.bias, at.c[k] + j, a.wb_dtype, 0.f) : 0.f;
-      A[k][j] = B[k][j] = 0.f;
+  for (int k = 0; k < VPT; ++k) {
+    from[k] = (size_t)rg.n0 * a.L * a.C + (size_t)p.g * D + at.off[k];
+    if (at.in[k]) {
+      params<V>(a.weight, at.c[k], a.wb_dtype, 1.f, w[k]);
+      params<V>(a.bias, at.c[k], a.wb_dtype, 0.f, b[k]);
     }
-  const size_t row = (size_t)a.L * a.C, col = (size_t)p.g * D;
-  const long long step = (long long)q.sets * q.down;
-  long long n = (long long)p.set * q.down + p.down;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) A[k][i] = B[k][i] = both<P>(0.f);
+  }
   float nmean = 0.f, nrstd = 0.f;
-  auto load_stats = [&](long long m) {
-    if (m < a.N && p.live) {
-      nmean = a.mean[m * a.G + p.g];
-      nrstd = a.rstd[m * a.G + p.g];
+  auto load_stats = [&](int t) {
+    if (t < rg.mine && p.live) {
+      const long long i = (rg.n0 + t * rg.step) * a.G + p.g;
+      nmean = a.mean[i];
+      nrstd = a.rstd[i];
     }
   };
-  auto load = [&](int ahead) {
-    const long long m = n + ahead * step;
-    if (m < a.N) {
-#pragma unroll
-      for (int k = 0; k < VPT; ++k)
-        if (at.in[k]) {
-          const size_t e = m * row + col + at.off[k];
-          ring.put(ahead, kIn * k, a.x, e);
-          ring.put(ahead, kIn * k + 1, a.dy, e);
-          if (kGate) ring.put(ahead, kIn * k + kIn - 1, a.gate, e);
-        }
-    }
-    ring.commit();
-  };
-  load_stats(n);
-#pragma unroll
-  for (int i = 0; i < kRowSteps - 1; ++i) load(i);
-  // (every lane of a warp runs the same number of turns: the shuffles want them all)
-  const int turns = (int)((a.N + step - 1) / step);
-  for (int t = 0; t < turns; ++t, n += step, ring.next()) {
-    const bool on = n < a.N;
+  load_stats(0);
+  const void* src[kIn];
+  src[0] = a.x;
+  src[1] = a.dy;
+  if (kGate) src[kIn - 1] = a.gate;
+  const size_t stride = (size_t)rg.step * a.L * a.C;
+  walk<T, V, VPT, kIn, kRowSteps>(smem, src, from, at.in, stride, rg.mine, rg.turns,
+                                  [&](auto& ring, int u, int t, size_t here) {
+    const bool on = t < rg.mine;
     const float mean = nmean, rstd = nrstd;
-    load_stats(n + step);
-    load(kRowSteps - 1);
-    ring.wait();
-    float xh[VPT][V], d[VPT][V], s1 = 0.f, s2 = 0.f;
+    load_stats(t + 1);
+    P xh[VPT][kP], d[VPT][kP], s1 = both<P>(0.f), s2 = both<P>(0.f);
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const bool in = on && at.in[k];
-      const Pack<T, V> x = ring.get(kIn * k), dy = ring.get(kIn * k + 1);
-      Pack<T, V> z{}, o;
-      if (kGate) z = ring.get(kIn * k + kIn - 1);
+    for (int k = 0; k < VPT; ++k)
+      if (on && at.in[k]) {
+        P x[kP], dy[kP], z[kP];
+        unpack<V>(ring.get(u, kIn * k), x);
+        unpack<V>(ring.get(u, kIn * k + 1), dy);
+        if (kGate) unpack<V>(ring.get(u, kIn * k + kIn - 1), z);
+        Pack<T, V> o;
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float dz = 0.f;
-        const float du = grad_u<kGate>(to_f(x.e[j]), to_f(dy.e[j]), to_f(z.e[j]), mean, rstd, w[k][j], b[k][j],
-                                       a.act, &xh[k][j], &dz);
-        if (kGate) from_f(o.e[j], dz);
-        if (in) {
-          A[k][j] += du;
-          B[k][j] = fmaf(du, xh[k][j], B[k][j]);
-          d[k][j] = du * w[k][j];
-          s1 += d[k][j];
-          s2 = fmaf(d[k][j], xh[k][j], s2);
+        for (int i = 0; i < kP; ++i) {
+          P dz;
+          const P du = grad_u<kGate>(x[i], dy[i], z[i], mean, rstd, w[k][i], b[k][i], a.act, &xh[k][i], &dz);
+          if (kGate) pack<V>(o, i, dz);
+          A[k][i] = add(A[k][i], du);
+          B[k][i] = fma(du, xh[k][i], B[k][i]);
+          d[k][i] = mul(du, w[k][i]);
+          s1 = add(s1, d[k][i]);
+          s2 = fma(d[k][i], xh[k][i], s2);
         }
+        if (kGate) store_pack<T, V>(a.dgate, from[k] + here, o);
       }
-      if (kGate && in) store_pack<T, V>(a.dgate, n * row + col + at.off[k], o);
-    }
-    const float m1 = sub_sum(s1, q.lanes) * inv, m2 = sub_sum(s2, q.lanes) * inv;
+    const float m1 = sub_sum(sum(s1), q.lanes) * inv, m2 = sub_sum(sum(s2), q.lanes) * inv;
 #pragma unroll
     for (int k = 0; k < VPT; ++k)
       if (on && at.in[k]) {
         Pack<T, V> o;
 #pragma unroll
-        for (int j = 0; j < V; ++j) from_f(o.e[j], rstd * (d[k][j] - m1 - xh[k][j] * m2));
-        store_pack<T, V>(a.dx, n * row + col + at.off[k], o);
+        for (int i = 0; i < kP; ++i) {
+          const P e = fma(xh[k][i], both<P>(-m2), add(d[k][i], both<P>(-m1)));
+          pack<V>(o, i, mul(e, both<P>(rstd)));
+        }
+        store_pack<T, V>(a.dx, from[k] + here, o);
       }
-  }
+  });
   if (!part) return;
   // A, B over the CTA's rows and positions: every value through shared memory, summed in order
   // (256 lanes of VPT V values each; the rings are done with).  First channel, channels of the CTA:
@@ -165,8 +155,8 @@ __global__ void __launch_bounds__(kGnThreads) gn_row_bwd_kernel(const GroupNormA
       const int r = p.down * a.L + at.off[k] / a.C, e = r * nc + at.c[k] - c0;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        acc[0][e + j] = A[k][j];
-        acc[1][e + j] = B[k][j];
+        acc[0][e + j] = reinterpret_cast<const float*>(A[k])[j];
+        acc[1][e + j] = reinterpret_cast<const float*>(B[k])[j];
       }
     }
   __syncthreads();
@@ -185,73 +175,57 @@ __global__ void __launch_bounds__(kGnThreads) gn_row_bwd_kernel(const GroupNormA
 // ------------------------------------------------------------------ slabs
 constexpr int kSlabSteps = 4;   // rows of a thread's column in its ring
 
-// Walks down a thread's column of x, dy (and z), their copies three rows ahead.
-template <typename T, int V, bool kGate>
-struct SlabReader {
-  static constexpr int kIn = kGate ? 3 : 2;
-  const GroupNormArgs& a;
-  size_t base;
-  int r, step, end;
-  Ring<T, V, kIn, kSlabSteps> ring;
-  __device__ __forceinline__ SlabReader(const GroupNormArgs& a, const SlabPlace& p, int2 rr, size_t base, void* smem)
-      : a(a), base(base), r(rr.x + p.row), step(p.step), end(rr.y), ring(smem) {
-#pragma unroll
-    for (int i = 0; i < kSlabSteps - 1; ++i) load(i);
-  }
-  __device__ __forceinline__ void load(int ahead) {
-    const int m = r + ahead * step;
-    if (m < end) {
-      const size_t at = base + (size_t)m * a.C;
-      ring.put(ahead, 0, a.x, at);
-      ring.put(ahead, 1, a.dy, at);
-      if (kGate) ring.put(ahead, kIn - 1, a.gate, at);
-    }
-    ring.commit();
-  }
-  __device__ __forceinline__ void get(Pack<T, V>& x, Pack<T, V>& dy, Pack<T, V>& z) {
-    load(kSlabSteps - 1);
-    ring.wait();
-    x = ring.get(0);
-    dy = ring.get(1);
-    if (kGate) z = ring.get(kIn - 1);
-  }
-  __device__ __forceinline__ void next() {
-    r += step;
-    ring.next();
-  }
-};
+// Walks down a thread's column: f(x, dy, z, distance).
+template <typename T, int V, bool kGate, class F>
+__device__ __forceinline__ void walk_slab(const GroupNormArgs& a, const SlabRange& rr, void* smem, F&& f) {
+  constexpr int kIn = kGate ? 3 : 2, kP = kPairs<V>;
+  const void* src[kIn];
+  src[0] = a.x;
+  src[1] = a.dy;
+  if (kGate) src[kIn - 1] = a.gate;
+  const size_t from[1] = {rr.from};
+  const bool in[1] = {true};
+  walk<T, V, 1, kIn, kSlabSteps>(smem, src, from, in, rr.stride, rr.rows, rr.rows,
+                                 [&](auto& ring, int u, int, size_t here) {
+    Pair<V> x[kP], dy[kP], z[kP];
+    unpack<V>(ring.get(u, 0), x);
+    unpack<V>(ring.get(u, 1), dy);
+    if (kGate) unpack<V>(ring.get(u, kIn - 1), z);
+    f(x, dy, z, here);
+  });
+}
 
 // part [n][chunk][2][C]: A, B; share [n][g][chunk][parts]: (sum du w, sum du w xhat) of the slab.
 template <typename T, int V, bool kGate>
-__global__ void __launch_bounds__(kGnThreads) gn_slab_grad_kernel(const GroupNormArgs a, const SlabPlan s,
+__global__ void __launch_bounds__(kGnThreads, kSlabPerSm) gn_slab_grad_kernel(const GroupNormArgs a, const SlabPlan s,
                                                                   float* part, float2* share) {
   extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
-  const int2 rr = slab_rows(s, p, a.L);
-  float A[V], B[V];
+  using P = Pair<V>;
+  constexpr int kP = kPairs<V>;
+  P Ap[kP], Bp[kP];
 #pragma unroll
-  for (int j = 0; j < V; ++j) A[j] = B[j] = 0.f;
+  for (int i = 0; i < kP; ++i) Ap[i] = Bp[i] = both<P>(0.f);
   if (p.on) {
     const float mean = a.mean[(size_t)p.n * a.G + p.g], rstd = a.rstd[(size_t)p.n * a.G + p.g];
-    float w[V], b[V];
+    P w[kP], b[kP];
+    params<V>(a.weight, p.c, a.wb_dtype, 1.f, w);
+    params<V>(a.bias, p.c, a.wb_dtype, 0.f, b);
+    walk_slab<T, V, kGate>(a, slab_range(s, p, a.L, a.C), smem, [&](P(&x)[kP], P(&dy)[kP], P(&z)[kP], size_t) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      w[j] = param(a.weight, p.c + j, a.wb_dtype, 1.f);
-      b[j] = param(a.bias, p.c + j, a.wb_dtype, 0.f);
-    }
-    const size_t base = (size_t)p.n * a.L * a.C + p.c;
-    for (SlabReader<T, V, kGate> in(a, p, rr, base, smem); in.r < in.end; in.next()) {
-      Pack<T, V> x, dy, z{};
-      in.get(x, dy, z);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float xh, dz;
-        const float du = grad_u<kGate>(to_f(x.e[j]), to_f(dy.e[j]), to_f(z.e[j]), mean, rstd, w[j], b[j], a.act,
-                                       &xh, &dz);
-        A[j] += du;
-        B[j] = fmaf(du, xh, B[j]);
+      for (int i = 0; i < kP; ++i) {
+        P xh, dz;
+        const P du = grad_u<kGate>(x[i], dy[i], z[i], mean, rstd, w[i], b[i], a.act, &xh, &dz);
+        Ap[i] = add(Ap[i], du);
+        Bp[i] = fma(du, xh, Bp[i]);
       }
-    }
+    });
+  }
+  float A[V], B[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    A[j] = reinterpret_cast<const float*>(Ap)[j];
+    B[j] = reinterpret_cast<const float*>(Bp)[j];
   }
   // (the rings are done with; a thread's own copies have landed)
   __syncthreads();
@@ -275,7 +249,7 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_grad_kernel(const GroupNor
       }
       q[j] = x;
       q[a.C + j] = y;
-      const float w = param(a.weight, p.c + j, a.wb_dtype, 1.f);
+      const float w = a.weight ? load_elem(a.weight, p.c + j, a.wb_dtype) : 1.f;
       A[j] = x * w;
       B[j] = y * w;
     }
@@ -328,7 +302,7 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_means_kernel(const GroupNo
 }
 
 template <typename T, int V, bool kGate>
-__global__ void __launch_bounds__(kGnThreads) gn_slab_bwd_kernel(const GroupNormArgs a, const SlabPlan s, int slabs,
+__global__ void __launch_bounds__(kGnThreads, kSlabPerSm) gn_slab_bwd_kernel(const GroupNormArgs a, const SlabPlan s, int slabs,
                                                                  const float* part, const float2* means) {
   if ((int)blockIdx.x >= slabs) {
     sum_sets<kGnThreads / 32>(a, part, a.N * s.chunks, blockIdx.x - slabs);
@@ -337,35 +311,29 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_bwd_kernel(const GroupNorm
   extern __shared__ __align__(16) uint8_t smem[];
   const SlabPlace p = slab_place(s, a.C, a.G);
   if (!p.on) return;
-  const int2 rr = slab_rows(s, p, a.L);
+  using P = Pair<V>;
+  constexpr int kP = kPairs<V>;
+  const SlabRange rr = slab_range(s, p, a.L, a.C);
   const float mean = a.mean[(size_t)p.n * a.G + p.g], rstd = a.rstd[(size_t)p.n * a.G + p.g];
   const float2 m = means[(size_t)p.n * a.G + p.g];
-  float w[V], b[V];
+  P w[kP], b[kP];
+  params<V>(a.weight, p.c, a.wb_dtype, 1.f, w);
+  params<V>(a.bias, p.c, a.wb_dtype, 0.f, b);
+  walk_slab<T, V, kGate>(a, rr, smem, [&](P(&x)[kP], P(&dy)[kP], P(&z)[kP], size_t here) {
+    Pack<T, V> o, oz;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    w[j] = param(a.weight, p.c + j, a.wb_dtype, 1.f);
-    b[j] = param(a.bias, p.c + j, a.wb_dtype, 0.f);
-  }
-  const size_t base = (size_t)p.n * a.L * a.C + p.c;
-  for (SlabReader<T, V, kGate> in(a, p, rr, base, smem); in.r < in.end; in.next()) {
-    Pack<T, V> x, dy, z{}, o, oz;
-    in.get(x, dy, z);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float xh, dz = 0.f;
-      const float du = grad_u<kGate>(to_f(x.e[j]), to_f(dy.e[j]), to_f(z.e[j]), mean, rstd, w[j], b[j], a.act, &xh,
-                                     &dz);
-      from_f(o.e[j], rstd * (du * w[j] - m.x - xh * m.y));
-      if (kGate) from_f(oz.e[j], dz);
+    for (int i = 0; i < kP; ++i) {
+      P xh, dz;
+      const P du = grad_u<kGate>(x[i], dy[i], z[i], mean, rstd, w[i], b[i], a.act, &xh, &dz);
+      const P e = fma(xh, both<P>(-m.y), fma(du, w[i], both<P>(-m.x)));
+      pack<V>(o, i, mul(e, both<P>(rstd)));
+      if (kGate) pack<V>(oz, i, dz);
     }
-    const size_t at = base + (size_t)in.r * a.C;
-    store_pack<T, V>(a.dx, at, o);
-    if (kGate) store_pack<T, V>(a.dgate, at, oz);
-  }
+    store_pack<T, V>(a.dx, rr.from + here, o);
+    if (kGate) store_pack<T, V>(a.dgate, rr.from + here, oz);
+  });
 }
 
-constexpr int kRowValues = 16;   // values a lane holds in the row form
-constexpr int kRowPerSm = 3;     // its CTAs an SM (registers)
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -399,7 +367,7 @@ cudaError_t launch_bwd(const GroupNormArgs& a) {
   const int slabs = a.N * s.NCB * s.chunks;
   float2* share = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(a.workspace) +
                                             align256((size_t)a.N * s.chunks * 2 * a.C * sizeof(float)));
-  constexpr int kRing = SlabReader<T, V, kGate>::kIn * kSlabSteps * V * (int)sizeof(T) * kGnThreads;
+  constexpr int kRing = Ring<T, V, kGate ? 3 : 2, kSlabSteps>::kShared;
   constexpr int kSums = 2 * kGnThreads * V * (int)sizeof(float);
   constexpr int kGrad = kRing > kSums ? kRing : kSums;
   if ((err = allow_shared<gn_slab_grad_kernel<T, V, kGate>, kGrad>()) != cudaSuccess ||
