@@ -15,7 +15,7 @@ namespace gdn {
 namespace {
 
 constexpr int kGnThreads = 256;
-constexpr int kSlabPerSm = 4;   // CTAs an SM in the slab form (registers)
+constexpr int kSlabPerSm = 3;   // CTAs an SM in the slab form (registers)
 
 // V consecutive elements in one load: V sizeof(T) is 2, 4, 8 or 16 bytes.
 template <int kBytes> struct Raw;

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(1024) gn_sum_sets_kernel(const GroupNormArgs a
 // ------------------------------------------------------------------ groups in registers
 constexpr int kRowSteps = 3;
 constexpr int kRowValues = 16;   // values a lane holds
-constexpr int kRowPerSm = 3;     // CTAs an SM (registers)
+constexpr int kRowPerSm = 2;     // CTAs an SM (registers)
 
 template <typename T, int V, int VPT, bool kGate>
 __global__ void __launch_bounds__(kGnThreads, VPT == 1 ? kRowPerSm : 1) gn_row_bwd_kernel(const GroupNormArgs a, const RowPlan q, float* part) {

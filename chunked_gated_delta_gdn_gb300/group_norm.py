@@ -70,7 +70,8 @@ def group_norm_act(x, num_groups, weight=None, bias=None, eps=1e-5, activation="
     mean = rstd = None
     if return_stats:
         make = torch.empty if L else torch.zeros
-        mean, rstd = make((2, N, G), dtype=torch.float32, device=dev).unbind(0)
+        mean = make((N, G), dtype=torch.float32, device=dev)
+        rstd = make((N, G), dtype=torch.float32, device=dev)
     lib = _lib.load()
     need = lib.gdn_group_norm_act_fwd_workspace_size(N, L, C, G, _DT[x.dtype])
     workspace, ws_bytes = _scratch(need, "gdn_group_norm_act_fwd", workspace, dev)
@@ -97,7 +98,8 @@ def group_norm_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, ac
     dgate = None if gate is None else torch.empty_like(x)
     dw = db = None
     if need_params:
-        dw, db = torch.empty((2, C), dtype=torch.float32, device=dev).unbind(0)
+        dw = torch.empty(C, dtype=torch.float32, device=dev)
+        db = torch.empty(C, dtype=torch.float32, device=dev)
     lib = _lib.load()
     need = lib.gdn_group_norm_act_bwd_workspace_size(N, L, C, G, _DT[x.dtype])
     workspace, ws_bytes = _scratch(need, "gdn_group_norm_act_bwd", workspace, dev)
