@@ -91,9 +91,22 @@ __host__ __device__ inline int la_smem_floats(int K, int V) {
 // the tensor cores: a launch (`local_only`) for each segment's own contribution to the state, and
 // one from the entry states.  A chain's scratch holds a copy of its entry state (the exit state may
 // go to the same place), then the contributions in order, [K][V] each.
-__global__ void __launch_bounds__(kLaThreads, 1)
-    linear_attn_kernel(const LinAttnPass p, int segs, int local_only, float* scratch) {
+struct LaPasses {
+  LinAttnPass pass[kLaMaxPasses];
+  int segs, local_only;
+  float* scratch;        // [pass][n][h][segs][K][V]
+};
+
+__global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const __grid_constant__ LaPasses a) {
   extern __shared__ __align__(16) float sm[];
+  const int segs = a.segs, local_only = a.local_only;
+  int unit = blockIdx.x;   // heads vary fastest, then sequences, segments, passes
+  const int h = unit % a.pass[0].H;
+  unit /= a.pass[0].H;
+  const int n = unit % a.pass[0].num_seqs;
+  unit /= a.pass[0].num_seqs;
+  const int parts = local_only ? segs - 1 : segs, seg = unit % parts, pi = unit / parts;
+  const LinAttnPass p = a.pass[pi];
   const int K = p.K, V = p.V, KS = K + 4;
   float* sQ = sm;
   float* sK = sQ + kChunk * KS;
@@ -102,10 +115,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   float* sP = sX + K * V;                 // [64][68]
   float* sW = sP + kChunk * (kChunk + 4);   // gamma^0 .. gamma^64
   constexpr int PS = kChunk + 4;
-  int unit = blockIdx.x;
-  const int h = unit % p.H;
-  unit /= p.H;
-  const int n = unit % p.num_seqs, seg = unit / p.num_seqs;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const LaChain c = la_chain(p, n, h, tid == 0 && h == 0 && seg == 0);
   const int T_total = p.cu_seqlens ? p.T : p.B * p.T;
@@ -131,7 +140,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     sG[tid] = decay_pow2(ld, tokens);
   }
   __syncthreads();
-  float* slots = scratch + (size_t)(n * p.H + h) * segs * (size_t)(K * V);   // (segs > 1 only)
+  float* slots = a.scratch + ((size_t)(pi * p.num_seqs + n) * p.H + h) * segs * (size_t)(K * V);   // (segs > 1 only)
   {   // the entry state
     const float* init = whole || (local_only && seg == 0) ? c.init : nullptr;
     for (int e = tid; e < K * V; e += kLaThreads) {
@@ -369,10 +378,20 @@ __global__ void __launch_bounds__(kLaThreads) linear_attn_decode_kernel(const Li
   }
 }
 
-cudaError_t launch_pass(const LinAttnPass& p, int segs, float* scratch) {
-  const long long chains = (long long)p.num_seqs * p.H;
+}  // namespace
+
+int linear_attn_segments(long long chains, long long most_tokens, int num_sms, int min_chunks) {
+  if (chains <= 0 || num_sms <= 0) return 1;
+  const long long chunks = (most_tokens + kChunk - 1) / kChunk;
+  return (int)std::max(1LL, std::min({(long long)kLaMaxSegments, num_sms / chains, chunks / min_chunks}));
+}
+
+cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes, int segs, float* scratch) {
+  const LinAttnPass& p0 = passes[0];
+  const long long chains = (long long)num_passes * p0.num_seqs * p0.H;
   if (chains <= 0) return cudaSuccess;
-  if (segs < 1 || chains * segs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (num_passes > kLaMaxPasses || segs < 1 || segs > kLaMaxSegments || chains * segs > 0x7fffffffLL)
+    return cudaErrorInvalidConfiguration;
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
@@ -383,25 +402,22 @@ cudaError_t launch_pass(const LinAttnPass& p, int segs, float* scratch) {
     if (err != cudaSuccess) return err;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  const size_t smem = la_smem_floats(p.K, p.V) * sizeof(float);
-  if (segs > 1) {
-    linear_attn_kernel<<<(unsigned)(chains * (segs - 1)), kLaThreads, smem, p.stream>>>(p, segs, 1, scratch);
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+  LaPasses a{};
+  size_t smem = 0;
+  for (int i = 0; i < num_passes; ++i) {
+    a.pass[i] = passes[i];
+    smem = std::max(smem, la_smem_floats(passes[i].K, passes[i].V) * sizeof(float));
   }
-  linear_attn_kernel<<<(unsigned)(chains * segs), kLaThreads, smem, p.stream>>>(p, segs, 0, scratch);
+  a.segs = segs;
+  a.scratch = scratch;
+  if (segs > 1) {
+    a.local_only = 1;
+    linear_attn_kernel<<<(unsigned)(chains * (segs - 1)), kLaThreads, smem, p0.stream>>>(a);
+    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    a.local_only = 0;
+  }
+  linear_attn_kernel<<<(unsigned)(chains * segs), kLaThreads, smem, p0.stream>>>(a);
   return cudaGetLastError();
-}
-
-}  // namespace
-
-int linear_attn_segments(long long chains, long long most_tokens, int num_sms, int min_chunks) {
-  if (chains <= 0 || num_sms <= 0) return 1;
-  const long long chunks = (most_tokens + kChunk - 1) / kChunk;
-  return (int)std::max(1LL, std::min({(long long)kLaMaxSegments, num_sms / chains, chunks / min_chunks}));
-}
-
-cudaError_t launch_linear_attn_generic(const LinAttnPass& p, int segs, float* scratch) {
-  return launch_pass(p, segs, scratch);
 }
 
 cudaError_t launch_linear_attn_fold(const float* const (&part)[2], void* const (&out)[2], long long T_total,

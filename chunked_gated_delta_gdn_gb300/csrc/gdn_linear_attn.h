@@ -48,10 +48,11 @@ struct LinAttnPass {
 constexpr int kLaMaxPasses = 3, kLaMaxSegments = 16, kLaMinSegmentChunks = 4;
 int linear_attn_segments(long long chains, long long most_tokens, int num_sms, int min_chunks);
 
-// CUDA cores: fp32, any accepted head dims.  scratch: segs > 1: segs K V floats a chain.
-cudaError_t launch_linear_attn_generic(const LinAttnPass& p, int segs, float* scratch);
-// Tensor cores: bf16 (o may be fp32), any accepted head dims; up to three passes over the same
-// sequences and heads in one launch.  scratch: segs > 1: segs 128 128 floats a chain and pass.
+// Up to three passes over the same sequences and heads, with the same product K V, in one launch.
+// CUDA cores: fp32, any accepted head dims.  scratch: segs > 1: segs K V floats a chain and pass.
+cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes, int segs, float* scratch);
+// Tensor cores: bf16 (o may be fp32), any accepted head dims.  scratch: segs > 1: segs 128 128
+// floats a chain and pass.
 cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* scratch);
 
 // out[i][t, hq, :] = sum over the group's value heads of part[i][t, hq * group + j, :], i = 0, 1

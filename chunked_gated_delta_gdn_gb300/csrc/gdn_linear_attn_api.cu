@@ -59,13 +59,12 @@ Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk
                 int io_dtype) {
   Scratch s{1, 0, 0, 0};
   const long long most = packed ? (long long)B * T : T, chains = (long long)num_seqs * Hv;
-  // the tensor cores run all passes at once and pad the state to 128 x 128; the CUDA cores run one
-  // after the other, each chunk of which takes long enough to stand alone
+  // the tensor cores pad the state to 128 x 128; on the CUDA cores a chunk takes long enough to
+  // stand alone
   const bool tc = io_dtype == GDN_BF16;
-  s.segs = gdn::linear_attn_segments(tc ? chains * num_passes : chains, most, sm_count(),
-                                     tc ? gdn::kLaMinSegmentChunks : 1);
+  s.segs = gdn::linear_attn_segments(chains * num_passes, most, sm_count(), tc ? gdn::kLaMinSegmentChunks : 1);
   if (s.segs > 1)
-    s.local = align256((size_t)s.segs * chains * (tc ? num_passes * 16384 : K * V) * sizeof(float));
+    s.local = align256((size_t)s.segs * chains * num_passes * (tc ? 16384 : K * V) * sizeof(float));
   if (num_passes > 1 && Hqk != Hv) s.part = align256((size_t)B * T * Hv * K * sizeof(float));
   s.total = s.local + 2 * s.part;
   return s;
@@ -75,11 +74,7 @@ Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk
 cudaError_t run_passes(const gdn::LinAttnPass* p, int n, int segs, void* local) {
   if (p[0].io_dtype == GDN_BF16)
     return gdn::launch_linear_attn_tc(p, n, segs, reinterpret_cast<float*>(local));
-  for (int i = 0; i < n; ++i) {
-    const cudaError_t err = gdn::launch_linear_attn_generic(p[i], segs, reinterpret_cast<float*>(local));
-    if (err != cudaSuccess) return err;
-  }
-  return cudaSuccess;
+  return gdn::launch_linear_attn_generic(p, n, segs, reinterpret_cast<float*>(local));
 }
 
 gdn_status_t check_workspace(const void* ws, size_t bytes, size_t need) {

@@ -118,7 +118,7 @@ struct Unit {
   const float* init;
   float* fin;            // exit state, when the range ends the sequence
   const float* local;    // this chain's scratch: the entry state, then the contributions of the
-                         // segments in order, [V 128][K 128] each
+                         // segments in order, 128 x 128 floats each
   int before;            // segments before this one
   float* store;          // where this segment's contribution goes (and nothing else is made), or NULL
   float* copy;           // where the entry state is copied to first, or NULL
@@ -497,12 +497,13 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
       src += 2 * step;
     }
   }
-  auto slot = [&](const float* base, int r) {   // this thread's 64 elements in slot r
-    return reinterpret_cast<float4*>(const_cast<float*>(base) + ((size_t)r * 128 + dv) * 128 + dk0);
+  constexpr int kStep = 32 * kStateWarps;       // a slot holds the threads' elements side by side
+  auto slot = [&](const float* base, int r) {   // this thread's, 4 every kStep, in slot r
+    return reinterpret_cast<float4*>(const_cast<float*>(base) + (size_t)r * 16384) + tid;
   };
   auto put_slot = [&](float4* dst) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) dst[j] = make_float4(X[2 * j].x, X[2 * j].y, X[2 * j + 1].x, X[2 * j + 1].y);
+    for (int j = 0; j < 16; ++j) dst[j * kStep] = make_float4(X[2 * j].x, X[2 * j].y, X[2 * j + 1].x, X[2 * j + 1].y);
   };
   if (u.copy) put_slot(slot(u.copy, 0));
   if (u.store) {
@@ -517,7 +518,7 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
       const float2 hi = make_float2(gr.x, gr.x), lo = make_float2(gr.y, gr.y);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const float4 x = __ldcg(src + j);
+        const float4 x = __ldcg(src + j * kStep);
         X[2 * j] = fma2(X[2 * j], hi, fma2(X[2 * j], lo, make_float2(x.x, x.y)));
         X[2 * j + 1] = fma2(X[2 * j + 1], hi, fma2(X[2 * j + 1], lo, make_float2(x.z, x.w)));
       }
@@ -588,8 +589,6 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
   if (u.store) {
     put_slot(slot(u.store, 0));
   } else if (u.fin) {
-  }
-  if (u.fin) {
     float* dst = u.fin + (size_t)dk0 * p.V + dv;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -717,10 +716,28 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
   return ok;
 }
 
+// The sequence that stands at `place` by length, longest first (equals by number): CTAs start in
+// order, and a long chain that starts among the last keeps the others waiting.
+constexpr int kMaxSorted = 128;
+__device__ __forceinline__ int sequence_by_length(const int32_t* cu, int n, int place, int* len) {
+  const int t = threadIdx.x;
+  if (t < n) len[t] = cu[t + 1] - cu[t];
+  __syncthreads();
+  if (t < n) {
+    const int mine = len[t];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += len[j] > mine || (len[j] == mine && j < t);
+    if (rank == place) len[kMaxSorted] = t;
+  }
+  __syncthreads();
+  return len[kMaxSorted];
+}
+
 struct LaLaunch {
   CUtensorMap map[kLaMaxPasses][4];   // q, k, v, o
   LinAttnPass pass[kLaMaxPasses];
   int segs;
+  int longest_first;
   int local_only;      // the first launch of a segmented run
   float* local;        // [pass][n][h][segs][128][128]
 };
@@ -736,8 +753,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   int e = blockIdx.x;   // heads vary fastest: those that share a row of q or k run side by side
   u.h = e % a.pass[0].H;
   e /= a.pass[0].H;
-  const int n = e % a.pass[0].num_seqs;
+  int n = e % a.pass[0].num_seqs;
   e /= a.pass[0].num_seqs;
+  if (a.longest_first) n = sequence_by_length(a.pass[0].cu_seqlens, a.pass[0].num_seqs, n, reinterpret_cast<int*>(sm));
   const int segs = a.local_only ? a.segs - 1 : a.segs;
   const int seg = e % segs, pi = e / segs;
   const LinAttnPass p = a.pass[pi];
@@ -855,6 +873,8 @@ cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int
   memset(&a, 0, sizeof(a));
   a.segs = segs;
   a.local = local;
+  // (with up to a hundred sequences finding one's place takes a CTA less than a microsecond)
+  a.longest_first = p0.cu_seqlens && p0.num_seqs > 1 && p0.num_seqs <= kMaxSorted;
   for (int i = 0; i < num_passes; ++i) {
     const LinAttnPass& p = a.pass[i] = passes[i];
     if (T_total > 0 &&   // (fp32 rows are stored without a map)
