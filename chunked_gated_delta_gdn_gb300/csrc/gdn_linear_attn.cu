@@ -97,7 +97,7 @@ struct LaPasses {
   float* scratch;        // [pass][n][h][segs][K][V]
 };
 
-__global__ void __launch_bounds__(kLaThreads, 1) linear_attn_kernel(const __grid_constant__ LaPasses a) {
+__global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid_constant__ LaPasses a) {
   extern __shared__ __align__(16) float sm[];
   const int segs = a.segs, local_only = a.local_only;
   int unit = blockIdx.x;   // heads vary fastest, then sequences, segments, passes
@@ -380,10 +380,14 @@ __global__ void __launch_bounds__(kLaThreads) linear_attn_decode_kernel(const Li
 
 }  // namespace
 
-int linear_attn_segments(long long chains, long long most_tokens, int num_sms, int min_chunks) {
-  if (chains <= 0 || num_sms <= 0) return 1;
+int linear_attn_segments(long long chains, long long most_tokens, int places, int min_chunks) {
+  if (chains <= 0 || places <= 0) return 1;
   const long long chunks = (most_tokens + kChunk - 1) / kChunk;
-  return (int)std::max(1LL, std::min({(long long)kLaMaxSegments, num_sms / chains, chunks / min_chunks}));
+  return (int)std::max(1LL, std::min({(long long)kLaMaxSegments, places / chains, chunks / min_chunks}));
+}
+
+int linear_attn_generic_per_sm(int K, int V) {
+  return la_smem_floats(K, V) * sizeof(float) + 1024 <= 113 * 1024 ? 2 : 1;
 }
 
 cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes, int segs, float* scratch) {

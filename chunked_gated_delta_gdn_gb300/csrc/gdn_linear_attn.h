@@ -43,14 +43,16 @@ struct LinAttnPass {
 };
 
 // Segments that each chain is cut into where there are too few to fill the GPU (1: none): by what
-// the host knows, the chains of a launch, the most tokens that a sequence can have, and the chunks
-// that a segment needs to be worth its share of the two launches.
+// the host knows, the chains of a launch, the most tokens that a sequence can have, the CTAs that
+// run at a time, and the chunks that a segment needs to be worth its share of the two launches.
 constexpr int kLaMaxPasses = 3, kLaMaxSegments = 16, kLaMinSegmentChunks = 4;
-int linear_attn_segments(long long chains, long long most_tokens, int num_sms, int min_chunks);
+int linear_attn_segments(long long chains, long long most_tokens, int places, int min_chunks);
 
 // Up to three passes over the same sequences and heads, with the same product K V, in one launch.
 // CUDA cores: fp32, any accepted head dims.  scratch: segs > 1: segs K V floats a chain and pass.
 cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes, int segs, float* scratch);
+// Its CTAs an SM (shared memory).
+int linear_attn_generic_per_sm(int K, int V);
 // Tensor cores: bf16 (o may be fp32), any accepted head dims.  scratch: segs > 1: segs 128 128
 // floats a chain and pass.
 cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* scratch);

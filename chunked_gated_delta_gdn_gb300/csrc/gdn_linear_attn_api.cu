@@ -62,7 +62,8 @@ Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk
   // the tensor cores pad the state to 128 x 128; on the CUDA cores a chunk takes long enough to
   // stand alone
   const bool tc = io_dtype == GDN_BF16;
-  s.segs = gdn::linear_attn_segments(chains * num_passes, most, sm_count(), tc ? gdn::kLaMinSegmentChunks : 1);
+  const int places = sm_count() * (tc ? 1 : gdn::linear_attn_generic_per_sm(K, V));
+  s.segs = gdn::linear_attn_segments(chains * num_passes, most, places, tc ? gdn::kLaMinSegmentChunks : 1);
   if (s.segs > 1)
     s.local = align256((size_t)s.segs * chains * num_passes * (tc ? 16384 : K * V) * sizeof(float));
   if (num_passes > 1 && Hqk != Hv) s.part = align256((size_t)B * T * Hv * K * sizeof(float));
