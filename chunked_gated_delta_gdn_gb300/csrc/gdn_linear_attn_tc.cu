@@ -74,8 +74,8 @@ constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 t
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
 constexpr uint32_t OFF_F = OFF_W + 288;            // Weights4[2][16]: the weights of V~ in a full and
                                                    // in the partial chunk
-constexpr uint32_t OFF_R = OFF_F + 2 * 16 * 24;           // float[64]: s_out R of a full chunk's rows
-constexpr uint32_t OFF_WP = OFF_R + 256;           // factors of P, see fill_p_table
+constexpr uint32_t OFF_R = OFF_F + 2 * 16 * 24;   // float[2][64]: s_out R of a full and of the partial chunk's rows
+constexpr uint32_t OFF_WP = OFF_R + 512;           // factors of P, see fill_p_table
 constexpr uint32_t kWpStride = 136;                // floats of one copy
 constexpr uint32_t OFF_G = OFF_WP + 4 * 4 * kWpStride;   // float2[2]: decay of a full / the partial chunk
 constexpr uint32_t OFF_SG = OFF_G + 32;            // float2[16]: decay over a whole earlier segment
@@ -603,20 +603,29 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
 }
 
 // ------------------------------------------------------------------ output (warps 8-11)
-__device__ __noinline__ void store_rows(const LinAttnPass& p, const float* w, const ChunkAt& ch,
-                                        uint32_t o, int h, int dv) {
-  const size_t row0 = ((size_t)ch.t0 * p.H + h) * p.V + dv, step = (size_t)p.H * p.V;
+// The first L rows of the staged tile (a partial chunk; the tile's TMA store would write all 64).
+__device__ __noinline__ void store_rows(const LinAttnPass& p, const uint8_t* tile, const ChunkAt& ch, int h, int tid) {
+  __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + ((size_t)ch.t0 * p.H + h) * p.V;
+  const int per = p.V / 8;   // 16-byte pieces a row
+#pragma unroll 1
+  for (int e = tid; e < ch.L * per; e += 32 * kOutWarps) {
+    const int t = e / per, d = e - t * per;
+    *reinterpret_cast<uint4*>(dst + (size_t)t * p.H * p.V + 8 * d) =
+        *reinterpret_cast<const uint4*>(tile + (d >> 3) * 8192 + t * 128 + (((d & 7) ^ (t & 7)) << 4));
+  }
+}
+
+// A partial chunk's rows in fp32, from the accumulator.
+__device__ __noinline__ void store_rows_f32(const LinAttnPass& p, const ChunkAt& ch, const float* factor, uint32_t o,
+                                            int h, int dv) {
+  float* dst = reinterpret_cast<float*>(p.o) + ((size_t)ch.t0 * p.H + h) * p.V + dv;
 #pragma unroll 1
   for (int t0 = 0; t0 < ch.L; t0 += 32) {
     float x[32];
     tmem_ld32(o + t0, x);
 #pragma unroll
-    for (int jj = 0; jj < 32; ++jj) {
-      const int t = t0 + jj;
-      if (t < ch.L && dv < p.V)
-        store_elem(p.o, row0 + t * step, p.s_out * row_factor(w, p.reverse ? ch.L - 1 - t : t + 1) * x[jj],
-                   p.o_f32 ? GDN_F32 : GDN_BF16);
-    }
+    for (int t = 0; t < 32; ++t)
+      if (t0 + t < ch.L && dv < p.V) dst[(size_t)(t0 + t) * p.H * p.V] = factor[t0 + t] * x[t];
   }
 }
 
@@ -624,9 +633,6 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
                          uint64_t* bars, int terms, const CUtensorMap* to) {
   const int tid = threadIdx.x - 32 * kStateWarps, lane = tid & 31, wq = tid >> 5;
   const uint32_t lane_off = (uint32_t)(32 * wq) << 16, sbase = smem_u32(sm);
-  const float* w = reinterpret_cast<const float*>(sm + OFF_W);
-  // the factors s_out R of a full chunk's rows, of this lane's tokens 2 (lane % 4) and the next
-  const float2* rf = reinterpret_cast<const float2*>(sm + OFF_R) + (lane & 3);
   const bool leader = tid == 0;
   bool ok = true;
 #pragma unroll 1
@@ -642,7 +648,13 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
     }
     tc_fence_after();
     if (leader) mbar_arrive(&bars[B_EMPTY + (i & (kStages - 1))]);   // (a chunk's last MMAs)
-    if (ch.L == kChunk && p.o_f32) {
+    if (p.o_f32 && ch.L < kChunk) {
+      store_rows_f32(p, ch, reinterpret_cast<const float*>(sm + OFF_R) + kChunk, o, u.h, 32 * wq + lane);
+      tc_fence_before();
+      warp_arrive(&bars[B_OFREE + par], lane);
+      continue;
+    }
+    if (p.o_f32) {
       // fp32 rows: this lane's value feature of each token, 128 bytes a warp and store
       const int dv = 32 * wq + lane;
       float* dst = reinterpret_cast<float*>(p.o) + ((size_t)ch.t0 * p.H + u.h) * p.V + dv;
@@ -671,12 +683,8 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
       }
       continue;
     }
-    if (ch.L < kChunk) {
-      store_rows(p, w, ch, o, u.h, 32 * wq + lane);
-      tc_fence_before();
-      warp_arrive(&bars[B_OFREE + par], lane);
-      continue;
-    }
+    // the factors s_out R of this lane's tokens 2 (lane % 4) and the next
+    const float2* rf = reinterpret_cast<const float2*>(sm + OFF_R) + (ch.L < kChunk ? 32 : 0) + (lane & 3);
     // 16x256b loads give each thread value features (t/4, t/4 + 8) x tokens (2 (t%4), + 1): the
     // fragment that stmatrix .trans writes as 16-byte rows (8 features of one token) of the
     // 128-byte-swizzled tile.  Lane l addresses feature block l / 8, token l % 8.
@@ -704,6 +712,12 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
     }
     tc_fence_before();
     warp_arrive(&bars[B_OFREE + par], lane);
+    if (ch.L < kChunk) {
+      group_sync(1, 32 * kOutWarps);
+      store_rows(p, sm + OFF_O, ch, u.h, tid);
+      group_sync(1, 32 * kOutWarps);   // (the tile is free again)
+      continue;
+    }
     fence_proxy_async_smem();
     group_sync(1, 32 * kOutWarps);
     if (leader) {
@@ -793,9 +807,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   }
   const float ld = clamp_log_decay(p.log_decay[u.h]);
   if (tid <= kChunk) reinterpret_cast<float*>(sm + OFF_W)[tid] = decay_pow(ld, (float)tid);
-  if (tid < kChunk)
+  if (tid < 2 * kChunk) {
+    const int t = tid & (kChunk - 1), L = tid < kChunk ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
     reinterpret_cast<float*>(sm + OFF_R)[tid] =
-        p.s_out * fmaxf(decay_pow(ld, p.reverse ? (float)(kChunk - 1 - tid) : (float)(tid + 1)), 0x1p-60f);
+        p.s_out * fmaxf(decay_pow(ld, p.reverse ? (float)max(L - 1 - t, 0) : (float)(t + 1)), 0x1p-60f);
+  }
   if (tid >= 64 && tid < 96) {   // (rows past the partial chunk's end are clear, whatever their weight)
     const int t = 4 * (tid & 15), L = tid < 80 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
     float x[4];
