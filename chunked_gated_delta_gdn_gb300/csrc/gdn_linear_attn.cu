@@ -308,24 +308,32 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
     for (int e = tid; e < K * V; e += kLaThreads) out[e] = sX[e];
 }
 
-// Sum of the value heads that share a query/key head: one thread per 4 elements.
+// Sum of the value heads that share a query/key head.  A thread keeps its 4 channels and walks over
+// rows, four at a time (their loads in flight together).  Bound by bytes.
+constexpr int kFoldRows = 4;
 template <typename T>
-__global__ void linear_attn_fold_kernel(const float* part0, const float* part1, T* out0, T* out1, long long rows,
-                                        int group, int D) {
+__global__ void __launch_bounds__(kLaThreads) linear_attn_fold_kernel(const float* part0, const float* part1, T* out0,
+                                                                      T* out1, long long rows, int group, int D) {
   const float* part = blockIdx.y ? part1 : part0;
   T* out = blockIdx.y ? out1 : out0;
-  const int D4 = D / 4;
-  const long long n = rows * D4;
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n;
-       e += (long long)gridDim.x * blockDim.x) {
-    const long long r = e / D4;
-    const int d = 4 * (int)(e - r * D4);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int D4 = D / 4, per = kLaThreads / D4, d = 4 * (threadIdx.x % D4), row = threadIdx.x / D4;
+  if (row >= per) return;
+  const long long step = (long long)gridDim.x * per;
+  for (long long r = (long long)blockIdx.x * per + row; r < rows; r += kFoldRows * step) {
+    float4 s[kFoldRows];
+#pragma unroll
+    for (int i = 0; i < kFoldRows; ++i) s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int j = 0; j < group; ++j) {
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(part + (r * group + j) * D + d));
-      s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+#pragma unroll
+      for (int i = 0; i < kFoldRows; ++i)
+        if (r + i * step < rows) {
+          const float4 x = __ldcs(reinterpret_cast<const float4*>(part + ((r + i * step) * group + j) * D + d));
+          s[i].x += x.x; s[i].y += x.y; s[i].z += x.z; s[i].w += x.w;
+        }
     }
-    store4(out + r * D + d, s);
+#pragma unroll
+    for (int i = 0; i < kFoldRows; ++i)
+      if (r + i * step < rows) store4(out + (r + i * step) * D + d, s[i]);
   }
 }
 
@@ -426,14 +434,14 @@ cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes
 
 cudaError_t launch_linear_attn_fold(const float* const (&part)[2], void* const (&out)[2], long long T_total,
                                     int Hqk, int group, int D, int io_dtype, cudaStream_t stream) {
-  const long long rows = T_total * Hqk, n = rows * (D / 4);
-  if (n == 0) return cudaSuccess;
-  const dim3 grid((unsigned)std::min((n + 255) / 256, 152LL * 16), 2);
+  const long long rows = T_total * Hqk, per = kLaThreads / (D / 4);
+  if (rows == 0) return cudaSuccess;
+  const dim3 grid((unsigned)std::min((rows + per - 1) / per, 152LL * 8), 2);
   if (io_dtype == GDN_F32)
-    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part[0], part[1], reinterpret_cast<float*>(out[0]),
+    linear_attn_fold_kernel<<<grid, kLaThreads, 0, stream>>>(part[0], part[1], reinterpret_cast<float*>(out[0]),
                                                       reinterpret_cast<float*>(out[1]), rows, group, D);
   else
-    linear_attn_fold_kernel<<<grid, 256, 0, stream>>>(part[0], part[1],
+    linear_attn_fold_kernel<<<grid, kLaThreads, 0, stream>>>(part[0], part[1],
                                                       reinterpret_cast<__nv_bfloat16*>(out[0]),
                                                       reinterpret_cast<__nv_bfloat16*>(out[1]), rows, group, D);
   return cudaGetLastError();
