@@ -99,7 +99,8 @@ enum {
   B_P = 13,       // P written, D read (P warps)
   B_O = 14,       // [2] O complete (commit): the chunk's stage has been read
   B_OFREE = 16,   // [2] O read (output warps)
-  B_COUNT = 18
+  B_P2 = 18,      // (local contributions: the odd chunks' weights)
+  B_COUNT = 19
 };
 constexpr uint32_t OFF_FLAG = OFF_BAR + 8 * B_COUNT, OFF_TSLOT = OFF_FLAG + 8;
 
@@ -275,7 +276,6 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
     const uint32_t so = (uint32_t)(i & (kStages - 1)) * kS16, par = (uint32_t)i & 1u;
     if (i >= 0) {   // U^T = V~^T K
       if (!wait_bar(&bars[B_V], par)) return false;
-      if (u.store && !wait_bar(&bars[B_FULL + (i & (kStages - 1))], (uint32_t)(i / kStages) & 1u)) return false;
       tc_fence_after();
 #pragma unroll 1
       for (int t = 0; t < terms; ++t) {
@@ -283,11 +283,6 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           mma_ts(tbase + COL_U, a + 8 * ks, dKm + so + 128 * ks, idU, (uint32_t)(t | ks));
-      }
-      if (u.store) {
-        if (i + kStages < n) mma_commit(&bars[B_EMPTY + (i & (kStages - 1))]);
-        mma_commit(&bars[B_U]);
-        continue;
       }
       mma_commit(&bars[B_U]);
       // O^T = X^T Q^T + V^T P^T
@@ -313,7 +308,7 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
       }
       mma_commit(&bars[B_O + par]);
     }
-    if (!u.store && i + 1 < n) {   // D = [Q; K] K^T of the next chunk
+    if (i + 1 < n) {   // D = [Q; K] K^T of the next chunk
       const uint32_t s1 = (uint32_t)(i + 1) & (kStages - 1);
       if (!wait_bar(&bars[B_FULL + s1], (uint32_t)((i + 1) / kStages) & 1u)) return false;
       tc_fence_after();
@@ -326,6 +321,61 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
         }
       mma_commit(&bars[B_D]);
     }
+  }
+  return true;
+}
+
+// ------------------------------------------------------------------ a segment's own contribution
+// sum_i gamma^(64 (n - 1 - i)) V~_i^T K_i over its n chunks (the last one to be processed is full):
+// the decay goes into the weights of V~, which the P warps make for each chunk, and the sum stays in
+// TMEM, so that nothing runs in series but the MMAs.  V~ and the weights have two buffers each, and
+// everything that says so two barriers, for even and odd chunks (no wait falls two phases behind).
+__device__ __forceinline__ uint64_t* local_v(uint64_t* bars, int i) { return &bars[(i & 1) ? B_X : B_V]; }
+__device__ __forceinline__ uint64_t* local_w(uint64_t* bars, int i) { return &bars[(i & 1) ? B_P2 : B_P]; }
+__device__ __forceinline__ uint32_t local_col(int i) { return COL_O + 128u * (i & 1); }
+
+__device__ bool local_weights_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint64_t* bars) {
+  const int lane = threadIdx.x & 31, e = 8 * ((threadIdx.x >> 5) - kStateWarps - kOutWarps) + lane;
+  const double lg = (double)clamp_log_decay(p.log_decay[u.h]) * 1.4426950408889634;
+  const float hi = (float)lg, lo = (float)(lg - (double)hi);
+  const float* w = reinterpret_cast<const float*>(sm + OFF_W);
+  const int n = u.c1 - u.c0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    if (i >= 2 && !wait_warp(local_v(bars, i), (uint32_t)((i - 2) >> 1) & 1u)) return false;
+    const int L = chunk_at(p, u, u.c0 + i).L, after = kChunk * (n - 1 - i);
+    if (lane < 8) {
+      // gamma^after = 2^(a + b), a rounded and b the rest
+      const float a = hi * (float)after, b = fmaf(hi, (float)after, -a) + lo * (float)after;
+      const float g = exp2f(a), f = p.s_in * fmaf(g, b * 0.69314718f, g);
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = f * w[p.reverse ? 4 * e + j + 1 : max(L - 1 - 4 * e - j, 0)];
+      reinterpret_cast<Weights4*>(sm + OFF_F)[16 * (i & 1) + e] = pack_weights(x);
+    }
+    warp_arrive(local_w(bars, i), lane);
+  }
+  return true;
+}
+
+__device__ bool local_mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint32_t tbase, uint64_t* bars,
+                               int terms) {
+  const int n = u.c1 - u.c0;
+  const uint32_t dKm = desc_lo(sb + 8192, 16384), id = idesc_bf16(128, p.K > 64 ? 128 : 64, false, true);
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int s = i & (kStages - 1);
+    if (!wait_bar(local_v(bars, i), (uint32_t)(i >> 1) & 1u)) return false;
+    if (!wait_bar(&bars[B_FULL + s], (uint32_t)(i / kStages) & 1u)) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int t = 0; t < terms; ++t)
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        mma_ts(tbase + COL_U, tbase + local_col(i) + 32 * t + 8 * ks, dKm + s * (kStage >> 4) + 128 * ks, id,
+               (uint32_t)(i | t | ks));
+    if (i + kStages < n) mma_commit(&bars[B_EMPTY + s]);
+    mma_commit(&bars[B_O + (i & 1)]);
   }
   return true;
 }
@@ -445,8 +495,8 @@ __device__ __noinline__ void clear_rows(uint8_t* st, int L, int vt0, int warp, i
 // addresses name the tokens 0, 1, 4, 5, 8, 9, 12, 13 (r even) or 2, 3, 6, .. (odd).
 template <int kTerms>
 __device__ __forceinline__ void make_vt(const uint8_t* sm, uint32_t v_tile, int d0,
-                                        int L, int lane, uint32_t dst, uint32_t (&late)[2][16]) {
-  const Weights4* fw = reinterpret_cast<const Weights4*>(sm + OFF_F) + (L < kChunk ? 16 : 0) + (lane & 3);
+                                        int table, int lane, uint32_t dst, uint32_t (&late)[2][16]) {
+  const Weights4* fw = reinterpret_cast<const Weights4*>(sm + OFF_F) + 16 * table + (lane & 3);
   const int r = lane >> 3, j = lane & 7;              // matrix (register) this lane addresses, row
   const int tok0 = 4 * (j >> 1) + 2 * (r & 1) + (j & 1), d = d0 + 8 * (r >> 1);
   const uint32_t tile = v_tile + (d >> 6) * 8192 + (uint32_t)tok0 * 128u + ((((d & 63) >> 3) ^ (tok0 & 7)) << 4);
@@ -472,6 +522,38 @@ __device__ __forceinline__ void make_vt(const uint8_t* sm, uint32_t v_tile, int 
     tmem_st16x256b_x1(dst + 8 * g, o[0]);
     tmem_st16x256b_x1(dst + 32 + 8 * g, o[1]);
   }
+}
+
+// V~ of a segment's chunks, for its own contribution; returns with the sum complete.
+template <int kTerms>
+__device__ bool local_state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase, uint64_t* bars) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vt0 = 32 * (warp & 3) + 16 * (warp >> 2);
+  const uint32_t vt_off = (uint32_t)vt0 << 16, sb = smem_u32(sm);
+  const int n = u.c1 - u.c0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int s = i & (kStages - 1), L = chunk_at(p, u, u.c0 + i).L;
+    if (!wait_warp(&bars[B_FULL + s], (uint32_t)(i / kStages) & 1u)) return false;
+    if (L < kChunk) clear_rows(sm + s * kStage, L, vt0, warp, lane);
+    if (i >= 2 && !wait_warp(&bars[B_O + (i & 1)], (uint32_t)((i - 2) >> 1) & 1u)) return false;
+    if (!wait_warp(local_w(bars, i), (uint32_t)(i >> 1) & 1u)) return false;
+    tc_fence_after();
+    if (vt0 < p.V) {
+      uint32_t late[2][16];
+      const uint32_t dst = tbase + vt_off + local_col(i);
+      make_vt<kTerms>(sm, sb + s * kStage + kStageV, vt0, i & 1, lane, dst, late);
+      if (kTerms == 4) {
+        tmem_st16x256b_x4(dst + 64, late[0]);
+        tmem_st16x256b_x4(dst + 96, late[1]);
+      }
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    warp_arrive(local_v(bars, i), lane);
+  }
+  if (!wait_warp(&bars[B_O + ((n - 1) & 1)], (uint32_t)((n - 1) >> 1) & 1u)) return false;
+  tc_fence_after();
+  return true;
 }
 
 template <int kTerms>
@@ -507,9 +589,22 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
   };
   if (u.copy) put_slot(slot(u.copy, 0));
   if (u.store) {
+    if (!local_state_role<kTerms>(p, u, sm, tbase, bars)) return false;
 #pragma unroll
     for (int j = 0; j < 32; ++j) X[j] = make_float2(0.f, 0.f);
-  } else if (u.local) {   // X <- X (hi + lo) + slot r
+    if (mine) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float x[32];
+        tmem_ld32(tbase + lane_off + COL_U + dk0 + 32 * half, x);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) X[16 * half + j] = make_float2(x[2 * j], x[2 * j + 1]);
+      }
+    }
+    put_slot(slot(u.store, 0));
+    return true;
+  }
+  if (u.local) {   // X <- X (hi + lo) + slot r
     const float2* sg = reinterpret_cast<const float2*>(sm + OFF_SG);
 #pragma unroll 1
     for (int r = 0; r <= u.before; ++r) {
@@ -535,7 +630,7 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     tc_fence_before();
     warp_arrive(&bars[B_X], lane);
   };
-  if (!u.store) put_x();
+  put_x();
   // X <- X (hi + lo) + U of chunk i
   auto update = [&](int i) {
     if (mine) {
@@ -562,7 +657,7 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     if (!wait_warp(&bars[B_FULL + s], (uint32_t)(i / kStages) & 1u)) return false;
     if (L < kChunk) clear_rows(sm + s * kStage, L, vt0, warp, lane);
     if (mine_v)
-      make_vt<kTerms>(sm, sb + s * kStage + kStageV, vt0, L, lane, tbase + vt_off + vt_col(i, kTerms), late);
+      make_vt<kTerms>(sm, sb + s * kStage + kStageV, vt0, L < kChunk, lane, tbase + vt_off + vt_col(i, kTerms), late);
     if (i > 0) {
       if (!wait_warp(&bars[B_U], (uint32_t)(i - 1) & 1u)) return false;
       tc_fence_after();
@@ -575,20 +670,16 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     tmem_wait_st();
     tc_fence_before();
     warp_arrive(&bars[B_V], lane);
-    if (i > 0 && !u.store) {
+    if (i > 0) {
       if (!wait_warp(&bars[B_XFREE], (uint32_t)(i - 1) & 1u)) return false;
       tc_fence_after();
       put_x();
     }
   }
-  if (u.fin || u.store) {
+  if (u.fin) {
     if (!wait_warp(&bars[B_U], (uint32_t)(n - 1) & 1u)) return false;
     tc_fence_after();
     update(n - 1);
-  }
-  if (u.store) {
-    put_slot(slot(u.store, 0));
-  } else if (u.fin) {
     float* dst = u.fin + (size_t)dk0 * p.V + dv;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -832,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) {
       const int count = (i == B_V || i == B_X) ? kStateWarps
-                        : i == B_P ? kPWarps : (i == B_OFREE || i == B_OFREE + 1) ? kOutWarps : 1;
+                        : i == B_P || i == B_P2 ? kPWarps : (i == B_OFREE || i == B_OFREE + 1) ? kOutWarps : 1;
       mbar_init(&bars[i], count);
     }
     *flag = 0;
@@ -855,9 +946,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   } else if (warp < kStateWarps + kOutWarps) {
     if (!u.store) ok = out_role(p, u, sm, tbase, bars, terms, &a.map[pi][3]);
   } else if (warp < kMmaWarp) {
-    if (!u.store) ok = p_role(p, u, sm, tbase, bars);
+    ok = u.store ? local_weights_role(p, u, sm, bars) : p_role(p, u, sm, tbase, bars);
   } else if (warp == kMmaWarp) {
-    if (elect_one()) ok = mma_role(p, u, smem_u32(sm), tbase, bars, terms);
+    if (elect_one())
+      ok = u.store ? local_mma_role(p, u, smem_u32(sm), tbase, bars, terms)
+                   : mma_role(p, u, smem_u32(sm), tbase, bars, terms);
     __syncwarp();
   } else {
     if (lane == 0) load_role(p, u, sm, bars, &a.map[pi][0], &a.map[pi][1], &a.map[pi][2]);
