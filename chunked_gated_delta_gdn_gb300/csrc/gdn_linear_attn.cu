@@ -398,6 +398,33 @@ int linear_attn_generic_per_sm(int K, int V) {
   return la_smem_floats(K, V) * sizeof(float) + 1024 <= 113 * 1024 ? 2 : 1;
 }
 
+LaPlan linear_attn_plan(long long chains, long long most_tokens, bool uniform, int places) {
+  const int few = linear_attn_segments(chains, most_tokens, places, kLaMinSegmentChunks);
+  LaPlan best{few > 1 ? 0 : chains, few};
+  if (!uniform || few > 1 || chains <= places || chains > 4LL * places) return best;
+  // More chains than places: the last, partly empty wave of whole ones costs as much as a full one
+  // (192 chains on 152 SMs: 350 us; cut, see below, 290).  Costs in chunks: a CTA's start 8, a
+  // chunk of a segment's own contribution 0.5.  Beside `rem` whole chains of a wave the others'
+  // contributions are made.
+  const double chunks = (double)((most_tokens + kChunk - 1) / kChunk), start = 8.0;
+  const auto waves = [&](long long n) { return (double)((n + places - 1) / places); };
+  double least = 0.95 * waves(chains) * (chunks + start);
+  for (int s = 2; s <= kLaMaxSegments && chunks >= s * (double)kLaMinSegmentChunks; ++s) {
+    const double part = chunks / s + start, own = 0.5 * chunks / s + start;
+    for (int full = 1; full <= s; ++full) {   // (of the second launch's waves)
+      const long long cut = std::min(chains, (long long)full * places / s), whole = chains - cut, rem = whole % places;
+      const long long beside = rem > 0 ? (places - rem) * (long long)((chunks + start) / own) : 0;
+      const double first = waves(whole) * (chunks + start) + waves(std::max(0LL, cut * (s - 1) - beside)) * own;
+      const double total = first + waves(cut * s) * part;
+      if (total < least) {
+        least = total;
+        best = LaPlan{whole, s};
+      }
+    }
+  }
+  return best;
+}
+
 cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes, int segs, float* scratch) {
   const LinAttnPass& p0 = passes[0];
   const long long chains = (long long)num_passes * p0.num_seqs * p0.H;

@@ -47,6 +47,14 @@ struct LinAttnPass {
 // run at a time, and the chunks that a segment needs to be worth its share of the two launches.
 constexpr int kLaMaxPasses = 3, kLaMaxSegments = 16, kLaMinSegmentChunks = 4;
 int linear_attn_segments(long long chains, long long most_tokens, int places, int min_chunks);
+// How a run on the tensor cores is launched: the first `whole` chains uncut, in the first launch,
+// the others in `segs` segments each (1: all whole, one launch).
+struct LaPlan {
+  long long whole;
+  int segs;
+};
+// For `uniform` chains, all of most_tokens, the plan that would end first.
+LaPlan linear_attn_plan(long long chains, long long most_tokens, bool uniform, int places);
 
 // Up to three passes over the same sequences and heads, with the same product K V, in one launch.
 // CUDA cores: fp32, any accepted head dims.  scratch: segs > 1: segs K V floats a chain and pass.
@@ -54,8 +62,8 @@ cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes
 // Its CTAs an SM (shared memory).
 int linear_attn_generic_per_sm(int K, int V);
 // Tensor cores: bf16 (o may be fp32), any accepted head dims.  scratch: segs > 1: segs 128 128
-// floats a chain and pass.
-cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* scratch);
+// floats a chain that is cut.
+cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, LaPlan plan, float* scratch);
 
 // out[i][t, hq, :] = sum over the group's value heads of part[i][t, hq * group + j, :], i = 0, 1
 // (fp32 in, io dtype out, heads added in order).

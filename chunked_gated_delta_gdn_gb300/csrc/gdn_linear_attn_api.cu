@@ -52,30 +52,30 @@ int sm_count() {
 // Scratch of a call: the segments' states, then (backward) per-value-head dq and dk in fp32 where
 // value heads share a query/key head.
 struct Scratch {
-  int segs;
+  gdn::LaPlan plan;
   size_t local, part, total;   // bytes; part: one of the two
 };
 Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk, int Hv, int K, int V,
                 int io_dtype) {
-  Scratch s{1, 0, 0, 0};
-  const long long most = packed ? (long long)B * T : T, chains = (long long)num_seqs * Hv;
+  Scratch s{{0, 1}, 0, 0, 0};
+  const long long most = packed ? (long long)B * T : T, chains = (long long)num_seqs * Hv * num_passes;
   // the tensor cores pad the state to 128 x 128; on the CUDA cores a chunk takes long enough to
   // stand alone
   const bool tc = io_dtype == GDN_BF16;
-  const int places = sm_count() * (tc ? 1 : gdn::linear_attn_generic_per_sm(K, V));
-  s.segs = gdn::linear_attn_segments(chains * num_passes, most, places, tc ? gdn::kLaMinSegmentChunks : 1);
-  if (s.segs > 1)
-    s.local = align256((size_t)s.segs * chains * num_passes * (tc ? 16384 : K * V) * sizeof(float));
+  if (tc) s.plan = gdn::linear_attn_plan(chains, most, !packed, sm_count());
+  else s.plan.segs = gdn::linear_attn_segments(chains, most, sm_count() * gdn::linear_attn_generic_per_sm(K, V), 1);
+  if (s.plan.segs > 1)
+    s.local = align256((size_t)s.plan.segs * (chains - s.plan.whole) * (tc ? 16384 : K * V) * sizeof(float));
   if (num_passes > 1 && Hqk != Hv) s.part = align256((size_t)B * T * Hv * K * sizeof(float));
   s.total = s.local + 2 * s.part;
   return s;
 }
 
 // bf16 runs on the tensor cores; fp32, whose 24-bit products they do not offer, on the CUDA cores.
-cudaError_t run_passes(const gdn::LinAttnPass* p, int n, int segs, void* local) {
+cudaError_t run_passes(const gdn::LinAttnPass* p, int n, const gdn::LaPlan& plan, void* local) {
   if (p[0].io_dtype == GDN_BF16)
-    return gdn::launch_linear_attn_tc(p, n, segs, reinterpret_cast<float*>(local));
-  return gdn::launch_linear_attn_generic(p, n, segs, reinterpret_cast<float*>(local));
+    return gdn::launch_linear_attn_tc(p, n, plan, reinterpret_cast<float*>(local));
+  return gdn::launch_linear_attn_generic(p, n, plan.segs, reinterpret_cast<float*>(local));
 }
 
 gdn_status_t check_workspace(const void* ws, size_t bytes, size_t need) {
@@ -139,7 +139,7 @@ gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void*
   p.o = o;
   const Scratch sc = scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, V, io_dtype);
   if ((st = check_workspace(workspace, workspace_bytes, sc.total)) != GDN_OK) return st;
-  return run_passes(&p, 1, sc.segs, workspace) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return run_passes(&p, 1, sc.plan, workspace) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 size_t gdn_linear_attn_chunk_bwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
@@ -227,7 +227,7 @@ gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void*
   p[2].s_in = sc;
   p[2].reverse = 1;
   p[2].o = dv;
-  if (run_passes(p, 3, ws.segs, workspace) != cudaSuccess) return GDN_ERR_CUDA;
+  if (run_passes(p, 3, ws.plan, workspace) != cudaSuccess) return GDN_ERR_CUDA;
   if (group > 1) {
     const float* const in[2] = {part[0], part[1]};
     void* const out[2] = {dq, dk};

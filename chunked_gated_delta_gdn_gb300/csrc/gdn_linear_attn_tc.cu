@@ -841,10 +841,12 @@ __device__ __forceinline__ int sequence_by_length(const int32_t* cu, int n, int 
 struct LaLaunch {
   CUtensorMap map[kLaMaxPasses][4];   // q, k, v, o
   LinAttnPass pass[kLaMaxPasses];
-  int segs;
   int longest_first;
+  int whole;           // this launch's CTAs for chains that are not cut, before the others
+  int first_cut, cut;  // the chains that are cut, and in how many
+  int segs;
   int local_only;      // the first launch of a segmented run
-  float* local;        // [pass][n][h][segs][128][128]
+  float* local;        // [chain that is cut][segs][128][128]
 };
 
 __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __grid_constant__ LaLaunch a) {
@@ -855,17 +857,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TSLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Unit u;
-  int e = blockIdx.x;   // heads vary fastest: those that share a row of q or k run side by side
+  // chains by heads (those that share a row of q or k run side by side), sequences, passes
+  int e = blockIdx.x, seg = 0, segs = 1, chain_cut = 0;
+  bool local_only = false;
+  if (e >= a.whole) {
+    e -= a.whole;
+    seg = e / a.cut;
+    chain_cut = e - seg * a.cut;
+    e = a.first_cut + chain_cut;
+    segs = a.segs;
+    local_only = a.local_only;
+  }
   u.h = e % a.pass[0].H;
   e /= a.pass[0].H;
   int n = e % a.pass[0].num_seqs;
   e /= a.pass[0].num_seqs;
   if (a.longest_first) n = sequence_by_length(a.pass[0].cu_seqlens, a.pass[0].num_seqs, n, reinterpret_cast<int*>(sm));
-  const int segs = a.local_only ? a.segs - 1 : a.segs;
-  const int seg = e % segs, pi = e / segs;
+  const int pi = e;
   const LinAttnPass p = a.pass[pi];
   const LaChain c = la_chain(p, n, u.h, tid == 0 && u.h == 0 && seg == 0);
-  if (seg == 0 && !a.local_only) {
+  if (seg == 0 && !local_only) {
     la_zero_rows(p, u.h, c.tail, p.cu_seqlens ? p.T : p.B * p.T, tid, kThreads);
     if (c.padding) la_zero_rows(p, u.h, c.bos, c.eos, tid, kThreads);
   }
@@ -873,21 +884,20 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   u.bos = c.bos;
   u.eos = c.eos;
   u.nch = (c.eos - c.bos + kChunk - 1) / kChunk;
-  const int per = max((u.nch + a.segs - 1) / a.segs, kLaMinSegmentChunks);
+  const int per = max((u.nch + segs - 1) / segs, kLaMinSegmentChunks);
   u.c0 = min(seg * per, u.nch);
   u.c1 = min(u.c0 + per, u.nch);
   const bool whole = seg == 0 && u.c1 == u.nch;   // (no other CTA works on this chain)
-  if (a.local_only && u.c1 == u.nch) return;       // (its contribution is nobody's entry state)
+  if (local_only && u.c1 == u.nch) return;       // (its contribution is nobody's entry state)
   // The entry state comes from the scratch where another CTA of the second launch may be writing
   // the exit state to the same place.
-  float* local = whole ? nullptr
-                       : a.local + ((size_t)(pi * p.num_seqs + n) * p.H + u.h) * (size_t)a.segs * 16384;
-  u.init = whole || (a.local_only && seg == 0) ? c.init : nullptr;
-  u.fin = a.local_only || u.c1 < u.nch ? nullptr : c.fin;
+  float* local = whole ? nullptr : a.local + (size_t)chain_cut * segs * 16384;
+  u.init = whole || (local_only && seg == 0) ? c.init : nullptr;
+  u.fin = local_only || u.c1 < u.nch ? nullptr : c.fin;
   u.before = seg;
   u.local = local;
-  u.store = a.local_only ? local + (size_t)(seg + 1) * 16384 : nullptr;
-  u.copy = a.local_only && seg == 0 ? local : nullptr;
+  u.store = local_only ? local + (size_t)(seg + 1) * 16384 : nullptr;
+  u.copy = local_only && seg == 0 ? local : nullptr;
   if (u.c0 == u.c1) {
     if (whole && u.fin)   // empty sequence: the state passes through
       for (int x = tid; x < p.K * p.V; x += kThreads) {
@@ -915,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
     const int L = warp == 4 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
     reinterpret_cast<float2*>(sm + OFF_G)[warp - 4] = decay_pow2(ld, L);
   }
-  if (!a.local_only && tid >= 256 && tid < 256 + u.before) {   // (backwards the first segment holds the partial chunk)
+  if (!local_only && tid >= 256 && tid < 256 + u.before) {   // (backwards the first segment holds the partial chunk)
     const int r = tid - 256, last = c.eos - c.bos - (u.nch - 1) * kChunk;
     reinterpret_cast<float2*>(sm + OFF_SG)[r] =
         decay_pow2(ld, per * kChunk - (p.reverse && r == 0 ? kChunk - last : 0));
@@ -971,15 +981,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
 
 }  // namespace
 
-cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int segs, float* local) {
+cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, LaPlan plan, float* local) {
   const LinAttnPass& p0 = passes[0];
   const long long chains = (long long)num_passes * p0.num_seqs * p0.H;
   if (chains <= 0) return cudaSuccess;
-  if (num_passes > kLaMaxPasses || segs < 1 || segs > kLaMaxSegments || chains * segs > 0x7fffffffLL)
+  const long long cut = chains - plan.whole;
+  const int segs = plan.segs;
+  if (num_passes > kLaMaxPasses || segs < 1 || segs > kLaMaxSegments || cut < 0 || (segs == 1 && cut > 0) ||
+      plan.whole + cut * segs > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
   const int T_total = p0.cu_seqlens ? p0.T : p0.B * p0.T;
   LaLaunch a;
   memset(&a, 0, sizeof(a));
+  a.whole = (int)plan.whole;
+  a.first_cut = (int)plan.whole;
+  a.cut = (int)cut;
   a.segs = segs;
   a.local = local;
   // (with up to a hundred sequences finding one's place takes a CTA less than a microsecond)
@@ -1003,13 +1019,14 @@ cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, int
     if (err != cudaSuccess) return err;
     if (dev < 64) attr_set[dev].store(true, std::memory_order_relaxed);
   }
-  if (segs > 1) {
+  if (cut > 0) {
     a.local_only = 1;
-    linear_attn_tc_kernel<<<(unsigned)(chains * (segs - 1)), kThreads, SMEM_BYTES, p0.stream>>>(a);
+    linear_attn_tc_kernel<<<(unsigned)(plan.whole + cut * (segs - 1)), kThreads, SMEM_BYTES, p0.stream>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     a.local_only = 0;
+    a.whole = 0;
   }
-  linear_attn_tc_kernel<<<(unsigned)(chains * segs), kThreads, SMEM_BYTES, p0.stream>>>(a);
+  linear_attn_tc_kernel<<<(unsigned)(cut > 0 ? cut * segs : plan.whole), kThreads, SMEM_BYTES, p0.stream>>>(a);
   return cudaGetLastError();
 }
 
