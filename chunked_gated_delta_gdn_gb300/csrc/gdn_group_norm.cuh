@@ -144,14 +144,17 @@ struct Ring {
   static constexpr int kBytes = V * (int)sizeof(T);
   static constexpr int kShared = kSteps * kPacks * kBytes * kGnThreads;
   uint8_t* mine;
-  __device__ __forceinline__ explicit Ring(void* smem) : mine(reinterpret_cast<uint8_t*>(smem) + threadIdx.x * kBytes) {}
+  __device__ __forceinline__ explicit Ring(void* smem)
+      : mine(reinterpret_cast<uint8_t*>(smem) + threadIdx.x * kBytes) {}
   __device__ __forceinline__ uint8_t* slot(int step, int i) const {
     return mine + (step * kPacks + i) * kBytes * kGnThreads;
   }
   __device__ __forceinline__ void put(int step, int i, const T* src) {
     const uint32_t dst = (uint32_t)__cvta_generic_to_shared(slot(step, i));
     if (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else if (kBytes >= 4) asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes < 4 ? 4 : kBytes) : "memory");
+    else if (kBytes >= 4)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes < 4 ? 4 : kBytes)
+                   : "memory");
     else *reinterpret_cast<Pack<T, V>*>(slot(step, i)) = load_pack<T, V>(src, 0);
   }
   __device__ __forceinline__ Pack<T, V> get(int step, int i) const { return load_pack<T, V>(slot(step, i), 0); }

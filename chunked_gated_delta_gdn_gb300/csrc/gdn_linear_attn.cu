@@ -84,13 +84,14 @@ __host__ __device__ inline int la_smem_floats(int K, int V) {
 
 // One CTA per (sequence, head, segment), 256 threads as 16 x 16; the state stays in shared memory.
 // Every product is register-blocked (P 4 x 4 a thread, o 4 x 8, X 8 x 8) in packed fp32, two
-// multiply-adds an instruction: two warps a scheduler, which is what the shared memory leaves, do
-// not hide the latencies of twice as many (34 us a chunk, now 23; 512 threads with half the block
-// each 39).  What the mask takes away of P and P V is left out by blocks.  Bound by the fp32 units (2.7 M multiply-adds a chunk at K =
-// V = 128, about 21k cycles of them).  Chains that do not fill the GPU are cut into segments as on
-// the tensor cores: a launch (`local_only`) for each segment's own contribution to the state, and
-// one from the entry states.  A chain's scratch holds a copy of its entry state (the exit state may
-// go to the same place), then the contributions in order, [K][V] each.
+// multiply-adds an instruction: the two warps a scheduler that shared memory leaves at K = V = 128
+// do not hide the latencies of twice as many (34 us a chunk, now 23; 512 threads with half the
+// block each 39).  Smaller head dims run two CTAs an SM.  What the mask takes away of P and P V is
+// left out by blocks.  Bound by the fp32 units (2.7 M multiply-adds a chunk at K = V = 128, about
+// 21k cycles of them).  Chains that do not fill the GPU are cut into segments as on the tensor
+// cores: a launch (`local_only`) for each segment's own contribution, and one from the entry
+// states.  A chain's scratch holds a copy of its entry state (the exit state may go to the same
+// place), then the contributions in order, [K][V] each.
 struct LaPasses {
   LinAttnPass pass[kLaMaxPasses];
   int segs, local_only;
@@ -140,7 +141,8 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
     sG[tid] = decay_pow2(ld, tokens);
   }
   __syncthreads();
-  float* slots = a.scratch + ((size_t)(pi * p.num_seqs + n) * p.H + h) * segs * (size_t)(K * V);   // (segs > 1 only)
+  float* slots =   // (segs > 1 only)
+      a.scratch + ((size_t)(pi * p.num_seqs + n) * p.H + h) * segs * (size_t)(K * V);
   {   // the entry state
     const float* init = whole || (local_only && seg == 0) ? c.init : nullptr;
     for (int e = tid; e < K * V; e += kLaThreads) {
@@ -274,7 +276,8 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const F4 x = (m ? two : one) ? f4(sX + (row + i) * V + 4 * tx + 64 * m) : F4{};
-          acc[m][i] = F4{make_float2(mul2(x.a.x, gl), mul2(x.a.y, gl)), make_float2(mul2(x.b.x, gl), mul2(x.b.y, gl))};
+          acc[m][i] = F4{make_float2(mul2(x.a.x, gl), mul2(x.a.y, gl)),
+                         make_float2(mul2(x.b.x, gl), mul2(x.b.y, gl))};
         }
 #pragma unroll 4
       for (int j = 0; j < L; ++j) {
@@ -309,11 +312,13 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
 }
 
 // Sum of the value heads that share a query/key head.  A thread keeps its 4 channels and walks over
-// rows, four at a time (their loads in flight together).  Bound by bytes.
+// rows, four at a time (their loads in flight together).  Bound by bytes: 98 us for
+// 671 MB (6.8 TB/s).
 constexpr int kFoldRows = 4;
 template <typename T>
-__global__ void __launch_bounds__(kLaThreads) linear_attn_fold_kernel(const float* part0, const float* part1, T* out0,
-                                                                      T* out1, long long rows, int group, int D) {
+__global__ void __launch_bounds__(kLaThreads)
+    linear_attn_fold_kernel(const float* part0, const float* part1, T* out0, T* out1, long long rows, int group,
+                            int D) {
   const float* part = blockIdx.y ? part1 : part0;
   T* out = blockIdx.y ? out1 : out0;
   const int D4 = D / 4, per = kLaThreads / D4, d = 4 * (threadIdx.x % D4), row = threadIdx.x / D4;
@@ -338,7 +343,8 @@ __global__ void __launch_bounds__(kLaThreads) linear_attn_fold_kernel(const floa
 }
 
 // One CTA per (request, head): S <- gamma S + k v^T, o = scale S^T q, the state read and written
-// once.  Thread t owns the float4 column group t % (V / 4) of every (threads / (V / 4))-th row.
+// once.  Bound by those bytes: 166 us for 230 requests' 967 MB (5.8 TB/s).  Thread t owns the
+// float4 column group t % (V / 4) of every (threads / (V / 4))-th row.
 template <typename T>
 __global__ void __launch_bounds__(kLaThreads) linear_attn_decode_kernel(const LinAttnDecodeArgs a) {
   __shared__ float sq[GDN_MAX_HEAD_DIM], sk[GDN_MAX_HEAD_DIM];
@@ -412,7 +418,8 @@ LaPlan linear_attn_plan(long long chains, long long most_tokens, bool uniform, i
   for (int s = 2; s <= kLaMaxSegments && chunks >= s * (double)kLaMinSegmentChunks; ++s) {
     const double part = chunks / s + start, own = 0.5 * chunks / s + start;
     for (int full = 1; full <= s; ++full) {   // (of the second launch's waves)
-      const long long cut = std::min(chains, (long long)full * places / s), whole = chains - cut, rem = whole % places;
+      const long long cut = std::min(chains, (long long)full * places / s), whole = chains - cut;
+      const long long rem = whole % places;
       const long long beside = rem > 0 ? (places - rem) * (long long)((chunks + start) / own) : 0;
       const double first = waves(whole) * (chunks + start) + waves(std::max(0LL, cut * (s - 1) - beside)) * own;
       const double total = first + waves(cut * s) * part;

@@ -63,7 +63,9 @@ Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk
   // stand alone
   const bool tc = io_dtype == GDN_BF16;
   if (tc) s.plan = gdn::linear_attn_plan(chains, most, !packed, sm_count());
-  else s.plan.segs = gdn::linear_attn_segments(chains, most, sm_count() * gdn::linear_attn_generic_per_sm(K, V), 1);
+  else
+    s.plan.segs =
+        gdn::linear_attn_segments(chains, most, sm_count() * gdn::linear_attn_generic_per_sm(K, V), 1);
   if (s.plan.segs > 1)
     s.local = align256((size_t)s.plan.segs * (chains - s.plan.whole) * (tc ? 16384 : K * V) * sizeof(float));
   if (num_passes > 1 && Hqk != Hv) s.part = align256((size_t)B * T * Hv * K * sizeof(float));

@@ -2,8 +2,8 @@
 // the tcgen05 tensor cores: bf16 I/O, any accepted head dims (padded to 64 or 128 by the TMA
 // loads' zero fill).
 //
-// One CTA per (sequence, head, segment), chunks of 64 tokens in order.  Per chunk, with X the K x V state
-// entering it and w_d = gamma^d (forward in time; the reverse pass mirrors the exponents, see
+// One CTA per (sequence, head, segment), chunks of 64 tokens in order.  Per chunk, with X the K x V
+// state entering it and w_d = gamma^d (forward in time; the reverse pass mirrors the exponents, see
 // gdn_linear_attn.h):
 //
 //   D    = [Q; K] K^T                      M=128 N=64  (rows 0-63 are Q K^T)
@@ -28,17 +28,23 @@
 //   four terms   h, r, a = f2 v rounded, (f2 v - a) + f3 v     error 2^-25, as fp32: where the
 //                                                              state leaves too
 // (three instructions for two values where scaling and splitting in fp32 took eight, and the
-// state warps, which do this, are what a chunk waits for).  The terms go to TMEM as the A operand of U, which leaves the shared memory to four
-// stages of Q, K, V in flight (scaled K tiles in shared memory left room for two, and a chunk
-// took 4050 cycles: a stage's life is a memory latency of 2300 plus its way through the roles).
-// P and the X operand are rounded to bf16 once, like the output itself (P of a sequence of one chunk
-// has a second term, see write_p_rest).
+// state warps, which do this, are what a chunk waits for).  The terms go to TMEM as the A operand
+// of U, which leaves the shared memory to four stages of Q, K, V in flight (scaled K tiles in
+// shared memory left room for two, and a chunk took 4050 cycles: a stage's life is a memory
+// latency of 2300 plus its way through the roles).  P and the X operand are rounded to bf16 once,
+// like the output itself (P of a sequence of one chunk has a second term, see write_p_rest).
 //
-// Where there are too few (sequence, head) chains to fill the GPU, each is cut into segments of
-// whole chunks: a first launch makes every segment's own contribution to the state (K, V and U
-// only), and in the second each segment starts from X = sum of the contributions before it, each
-// decayed over the tokens in between, and the given state.  Several passes (the backward's three)
-// run as one launch.
+// Where chains are too few to fill the GPU, or their last wave would leave most of it idle, they
+// (or those of that wave) are cut into segments of whole chunks: a first launch makes every
+// segment's own contribution to the state (K, V and U only), and in the second each segment starts
+// from X = sum of the contributions before it, each decayed over the tokens in between, and the
+// given state.  Several passes (the backward's three) run as one launch.
+//
+// Measured at K = V = 128 with 152 SMs busy: 1.55 us a chunk where the state leaves, 1.34 where
+// only outputs do, 0.7 for a segment's own contribution.  64 KB a chunk and SM are 6.3 and 7.3 TB/s
+// (grouped heads find a part of theirs in L2); what bounds it is a chunk's way through the roles,
+// and of that the instructions fetched anew for each chunk.  Every piece of a role's loop is
+// therefore written for few instructions rather than few steps.
 //
 // Roles: warps 0-7 state (V~ of a chunk while U of the one before runs, then the update), warps
 // 8-11 output, warps 12-13 P, warp 14 issues the MMAs, warp 15 the loads.  (Two issuing warps,
@@ -74,7 +80,8 @@ constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 t
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
 constexpr uint32_t OFF_F = OFF_W + 288;            // Weights4[2][16]: the weights of V~ in a full and
                                                    // in the partial chunk
-constexpr uint32_t OFF_R = OFF_F + 2 * 16 * 24;   // float[2][64]: s_out R of a full and of the partial chunk's rows
+constexpr uint32_t OFF_R = OFF_F + 2 * 16 * 24;   // float[2][64]: s_out R of the rows of a full and
+                                                  // of the partial chunk
 constexpr uint32_t OFF_WP = OFF_R + 512;           // factors of P, see fill_p_table
 constexpr uint32_t kWpStride = 136;                // floats of one copy
 constexpr uint32_t OFF_G = OFF_WP + 4 * 4 * kWpStride;   // float2[2]: decay of a full / the partial chunk
@@ -327,9 +334,16 @@ __device__ bool mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint3
 
 // ------------------------------------------------------------------ a segment's own contribution
 // sum_i gamma^(64 (n - 1 - i)) V~_i^T K_i over its n chunks (the last one to be processed is full):
-// the decay goes into the weights of V~, which the P warps make for each chunk, and the sum stays in
-// TMEM, so that nothing runs in series but the MMAs.  V~ and the weights have two buffers each, and
-// everything that says so two barriers, for even and odd chunks (no wait falls two phases behind).
+// the decay goes into the weights of V~, which the P warps make for each chunk, so that nothing runs
+// in series but the MMAs.  Where the state leaves (four terms) the sum stays in TMEM for two chunks
+// and is then added to fp32 registers while the next two fill a second accumulator: the MMAs'
+// accumulation does not round to nearest, and over a whole segment of 32 chunks the state's error
+// grew to 2e-6 (eight at a time 1.2e-6 to 1.7e-6, four 1.0e-6, two 7e-7; 34, 37, 38, 39 us for
+// 8192 tokens of 32 heads).  Where only bf16 outputs do, it stays there to the segment's end.  V~
+// and the weights have two buffers each, and everything that says so two barriers, for even and
+// odd chunks (no wait falls two phases behind).
+__host__ __device__ constexpr int local_run(int terms) { return terms == 4 ? 2 : 1 << 24; }
+__device__ __forceinline__ uint32_t local_sum(int i, int run) { return COL_U + 128u * ((i / run) & 1); }
 __device__ __forceinline__ uint64_t* local_v(uint64_t* bars, int i) { return &bars[(i & 1) ? B_X : B_V]; }
 __device__ __forceinline__ uint64_t* local_w(uint64_t* bars, int i) { return &bars[(i & 1) ? B_P2 : B_P]; }
 __device__ __forceinline__ uint32_t local_col(int i) { return COL_O + 128u * (i & 1); }
@@ -360,7 +374,7 @@ __device__ bool local_weights_role(const LinAttnPass& p, const Unit& u, uint8_t*
 
 __device__ bool local_mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb, uint32_t tbase, uint64_t* bars,
                                int terms) {
-  const int n = u.c1 - u.c0;
+  const int n = u.c1 - u.c0, run = local_run(terms);
   const uint32_t dKm = desc_lo(sb + 8192, 16384), id = idesc_bf16(128, p.K > 64 ? 128 : 64, false, true);
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
@@ -372,8 +386,8 @@ __device__ bool local_mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb,
     for (int t = 0; t < terms; ++t)
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        mma_ts(tbase + COL_U, tbase + local_col(i) + 32 * t + 8 * ks, dKm + s * (kStage >> 4) + 128 * ks, id,
-               (uint32_t)(i | t | ks));
+        mma_ts(tbase + local_sum(i, run), tbase + local_col(i) + 32 * t + 8 * ks, dKm + s * (kStage >> 4) + 128 * ks,
+               id, (uint32_t)((i % run) | t | ks));
     if (i + kStages < n) mma_commit(&bars[B_EMPTY + s]);
     mma_commit(&bars[B_O + (i & 1)]);
   }
@@ -381,8 +395,8 @@ __device__ bool local_mma_role(const LinAttnPass& p, const Unit& u, uint32_t sb,
 }
 
 // ------------------------------------------------------------------ P (warps 12, 13)
-// The factor s_in w_{i-j} of P_ij depends on j - i alone: f[x] for x = j - i + 63 in 0 .. 126, zero where the
-// mask is.  Row i reads f[63 - i ..], four at a time: four copies shifted by one float each keep
+// The factor s_in w_{i-j} of P_ij depends on j - i alone: f[x] for x = j - i + 63 in 0 .. 126, zero
+// where the mask is.  Row i reads f[63 - i ..], four at a time: four copies shifted by one float each keep
 // those reads 16-byte aligned whatever i is, and their stride of 8 banks keeps them apart.
 __device__ __forceinline__ void fill_p_table(const LinAttnPass& p, float ld, float* wp, int tid) {
   for (int e = tid; e < 4 * (int)kWpStride; e += kThreads) {
@@ -413,8 +427,11 @@ __device__ __noinline__ void write_p_rest(uint8_t* sm, uint32_t d, int row, cons
       const float t[4] = {f.x * (inv * x[4 * g]), f.y * (inv * x[4 * g + 1]), f.z * (inv * x[4 * g + 2]),
                           f.w * (inv * x[4 * g + 3])};
       uint2 q;
-      q.x = pack2(t[0] - __bfloat162float(__float2bfloat16_rn(t[0])), t[1] - __bfloat162float(__float2bfloat16_rn(t[1])));
-      q.y = pack2(t[2] - __bfloat162float(__float2bfloat16_rn(t[2])), t[3] - __bfloat162float(__float2bfloat16_rn(t[3])));
+      float rest[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rest[k] = t[k] - __bfloat162float(__float2bfloat16_rn(t[k]));
+      q.x = pack2(rest[0], rest[1]);
+      q.y = pack2(rest[2], rest[3]);
       *reinterpret_cast<uint2*>(sm + OFF_P_REST + sw128_offset(row, 32 * half + 4 * g)) = q;
     }
   }
@@ -524,12 +541,29 @@ __device__ __forceinline__ void make_vt(const uint8_t* sm, uint32_t v_tile, int 
   }
 }
 
-// V~ of a segment's chunks, for its own contribution; returns with the sum complete.
+// V~ of a segment's chunks, for its own contribution, which is left in X.
 template <int kTerms>
-__device__ bool local_state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase, uint64_t* bars) {
+__device__ bool local_state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint32_t tbase, uint64_t* bars,
+                                 float2 (&X)[32]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vt0 = 32 * (warp & 3) + 16 * (warp >> 2);
   const uint32_t vt_off = (uint32_t)vt0 << 16, sb = smem_u32(sm);
-  const int n = u.c1 - u.c0;
+  const int n = u.c1 - u.c0, dk0 = 64 * (warp >> 2);
+  constexpr int kRun = local_run(kTerms);
+  auto add_run = [&](int i) {   // the run that ended with chunk i
+    if (dk0 >= p.K) return;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float x[32];
+      tmem_ld32(tbase + ((uint32_t)(32 * (warp & 3)) << 16) + local_sum(i, kRun) + dk0 + 32 * half, x);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float2& a = X[16 * half + j];
+        a = make_float2(a.x + x[2 * j], a.y + x[2 * j + 1]);
+      }
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < 32; ++j) X[j] = make_float2(0.f, 0.f);
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int s = i & (kStages - 1), L = chunk_at(p, u, u.c0 + i).L;
@@ -550,9 +584,13 @@ __device__ bool local_state_role(const LinAttnPass& p, const Unit& u, uint8_t* s
     tmem_wait_st();
     tc_fence_before();
     warp_arrive(local_v(bars, i), lane);
+    // (chunk i - 2 is complete; the MMAs come back to its accumulator after another run's V~)
+    if (kTerms == 4 && i >= 2 && (i - 2) % kRun == kRun - 1) add_run(i - 2);
   }
   if (!wait_warp(&bars[B_O + ((n - 1) & 1)], (uint32_t)((n - 1) >> 1) & 1u)) return false;
   tc_fence_after();
+  if (kTerms == 4 && n >= 2 && (n - 2) % kRun == kRun - 1) add_run(n - 2);
+  add_run(n - 1);
   return true;
 }
 
@@ -589,18 +627,7 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
   };
   if (u.copy) put_slot(slot(u.copy, 0));
   if (u.store) {
-    if (!local_state_role<kTerms>(p, u, sm, tbase, bars)) return false;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) X[j] = make_float2(0.f, 0.f);
-    if (mine) {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float x[32];
-        tmem_ld32(tbase + lane_off + COL_U + dk0 + 32 * half, x);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) X[16 * half + j] = make_float2(x[2 * j], x[2 * j + 1]);
-      }
-    }
+    if (!local_state_role<kTerms>(p, u, sm, tbase, bars, X)) return false;
     put_slot(slot(u.store, 0));
     return true;
   }
@@ -657,7 +684,8 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
     if (!wait_warp(&bars[B_FULL + s], (uint32_t)(i / kStages) & 1u)) return false;
     if (L < kChunk) clear_rows(sm + s * kStage, L, vt0, warp, lane);
     if (mine_v)
-      make_vt<kTerms>(sm, sb + s * kStage + kStageV, vt0, L < kChunk, lane, tbase + vt_off + vt_col(i, kTerms), late);
+      make_vt<kTerms>(sm, sb + s * kStage + kStageV, vt0, L < kChunk, lane,
+                      tbase + vt_off + vt_col(i, kTerms), late);
     if (i > 0) {
       if (!wait_warp(&bars[B_U], (uint32_t)(i - 1) & 1u)) return false;
       tc_fence_after();
@@ -695,7 +723,8 @@ __device__ bool state_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uin
 
 // ------------------------------------------------------------------ output (warps 8-11)
 // The first L rows of the staged tile (a partial chunk; the tile's TMA store would write all 64).
-__device__ __noinline__ void store_rows(const LinAttnPass& p, const uint8_t* tile, const ChunkAt& ch, int h, int tid) {
+__device__ __noinline__ void store_rows(const LinAttnPass& p, const uint8_t* tile, const ChunkAt& ch, int h,
+                                        int tid) {
   __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + ((size_t)ch.t0 * p.H + h) * p.V;
   const int per = p.V / 8;   // 16-byte pieces a row
 #pragma unroll 1
@@ -707,8 +736,8 @@ __device__ __noinline__ void store_rows(const LinAttnPass& p, const uint8_t* til
 }
 
 // A partial chunk's rows in fp32, from the accumulator.
-__device__ __noinline__ void store_rows_f32(const LinAttnPass& p, const ChunkAt& ch, const float* factor, uint32_t o,
-                                            int h, int dv) {
+__device__ __noinline__ void store_rows_f32(const LinAttnPass& p, const ChunkAt& ch, const float* factor,
+                                            uint32_t o, int h, int dv) {
   float* dst = reinterpret_cast<float*>(p.o) + ((size_t)ch.t0 * p.H + h) * p.V + dv;
 #pragma unroll 1
   for (int t0 = 0; t0 < ch.L; t0 += 32) {
@@ -872,7 +901,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   e /= a.pass[0].H;
   int n = e % a.pass[0].num_seqs;
   e /= a.pass[0].num_seqs;
-  if (a.longest_first) n = sequence_by_length(a.pass[0].cu_seqlens, a.pass[0].num_seqs, n, reinterpret_cast<int*>(sm));
+  if (a.longest_first)
+    n = sequence_by_length(a.pass[0].cu_seqlens, a.pass[0].num_seqs, n, reinterpret_cast<int*>(sm));
   const int pi = e;
   const LinAttnPass p = a.pass[pi];
   const LaChain c = la_chain(p, n, u.h, tid == 0 && u.h == 0 && seg == 0);
@@ -925,7 +955,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
     const int L = warp == 4 ? kChunk : c.eos - c.bos - (u.nch - 1) * kChunk;
     reinterpret_cast<float2*>(sm + OFF_G)[warp - 4] = decay_pow2(ld, L);
   }
-  if (!local_only && tid >= 256 && tid < 256 + u.before) {   // (backwards the first segment holds the partial chunk)
+  if (!local_only && tid >= 256 && tid < 256 + u.before) {
+    // (backwards the first segment holds the partial chunk)
     const int r = tid - 256, last = c.eos - c.bos - (u.nch - 1) * kChunk;
     reinterpret_cast<float2*>(sm + OFF_SG)[r] =
         decay_pow2(ld, per * kChunk - (p.reverse && r == 0 ? kChunk - last : 0));
