@@ -94,6 +94,14 @@ def group_norm_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, ac
         _need(dy, "dy", x.dtype, dev, x.shape)
         _need(mean, "mean", torch.float32, dev, (N, G))
         _need(rstd, "rstd", torch.float32, dev, (N, G))
+    return _backward(dy, x, _ptr(mean), _ptr(rstd), (N, L, C, G, wb, act), weight, bias, gate,
+                     need_params, workspace)
+
+
+def _backward(dy, x, mean, rstd, sizes, weight, bias, gate, need_params, workspace):
+    """The backward's outputs, scratch and call; mean, rstd as addresses."""
+    N, L, C, G, wb, act = sizes
+    dev = x.device
     dx = torch.empty_like(x)
     dgate = None if gate is None else torch.empty_like(x)
     dw = db = None
@@ -104,31 +112,49 @@ def group_norm_act_bwd(dy, x, mean, rstd, num_groups, weight=None, bias=None, ac
     need = lib.gdn_group_norm_act_bwd_workspace_size(N, L, C, G, _DT[x.dtype])
     workspace, ws_bytes = _scratch(need, "gdn_group_norm_act_bwd", workspace, dev)
     st = lib.gdn_group_norm_act_bwd(_ptr(dy), _ptr(x), _ptr(weight), _ptr(bias), _ptr(gate),
-                                    _ptr(mean), _ptr(rstd), N, L, C, G, _DT[x.dtype], wb, act,
-                                    _ptr(dx), _ptr(dgate), _ptr(dw), _ptr(db), _ptr(workspace),
-                                    ws_bytes, _stream(dev))
+                                    mean, rstd, N, L, C, G, _DT[x.dtype], wb, act, _ptr(dx),
+                                    _ptr(dgate), _ptr(dw), _ptr(db), _ptr(workspace), ws_bytes,
+                                    _stream(dev))
     _lib.check("gdn_group_norm_act_bwd", st)
     return dx, dw, db, dgate
 
 
 class _GroupNormAct(torch.autograd.Function):
-    """gdn_group_norm_act_fwd forward, gdn_group_norm_act_bwd backward."""
+    """gdn_group_norm_act_fwd forward, gdn_group_norm_act_bwd backward.  (For small inputs the
+    host's part is most of both: mean, rstd and the forward's scratch share one allocation, and the
+    backward does not check again what the forward has checked.)"""
 
     @staticmethod
     def forward(ctx, x, num_groups, weight, bias, eps, activation, gate):
-        y, mean, rstd = group_norm_act(x, num_groups, weight, bias, eps, activation, gate,
-                                       return_stats=True)
-        ctx.save_for_backward(x, weight, bias, gate, mean, rstd)
-        ctx.num_groups, ctx.activation = num_groups, activation
+        sizes = N, L, C, G, wb, act = _inputs(x, num_groups, weight, bias, activation, gate)
+        dev = x.device
+        lib = _lib.load()
+        need = lib.gdn_group_norm_act_fwd_workspace_size(N, L, C, G, _DT[x.dtype])
+        if need == (1 << 64) - 1:
+            raise ValueError("sizes rejected by gdn_group_norm_act_fwd")
+        y = torch.empty_like(x)
+        at = (8 * N * G + 255) // 256 * 256      # where the scratch starts
+        stats = torch.empty(at + need, dtype=torch.uint8, device=dev)
+        mean = stats.data_ptr()
+        st = lib.gdn_group_norm_act_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(gate), N, L, C, G,
+                                        _DT[x.dtype], wb, float(eps), act, _ptr(y), mean,
+                                        mean + 4 * N * G, mean + at if need else None, need,
+                                        _stream(dev))
+        _lib.check("gdn_group_norm_act_fwd", st)
+        ctx.save_for_backward(x, weight, bias, gate, stats)
+        ctx.sizes = sizes
         return y
 
     @staticmethod
     def backward(ctx, dy):
-        x, weight, bias, gate, mean, rstd = ctx.saved_tensors
-        need = ctx.needs_input_grad
-        dx, dw, db, dgate = group_norm_act_bwd(dy.contiguous(), x, mean, rstd, ctx.num_groups,
-                                               weight, bias, ctx.activation, gate,
-                                               need_params=need[2] or need[3])
+        x, weight, bias, gate, stats = ctx.saved_tensors
+        need, sizes = ctx.needs_input_grad, ctx.sizes
+        dy = dy.contiguous()
+        if not _fit(x.device, (dy, x.dtype, x.shape)):
+            _need(dy, "dy", x.dtype, x.device, x.shape)
+        mean = stats.data_ptr()
+        dx, dw, db, dgate = _backward(dy, x, mean, mean + 4 * sizes[0] * sizes[3], sizes, weight,
+                                      bias, gate, need[2] or need[3], None)
         return (dx, None, dw.to(weight.dtype) if need[2] else None,
                 db.to(bias.dtype) if need[3] else None, None, None, dgate)
 
