@@ -41,7 +41,7 @@
 // given state.  Several passes (the backward's three) run as one launch.
 //
 // Measured at K = V = 128 with 152 SMs busy: 1.55 us a chunk where the state leaves, 1.34 where
-// only outputs do, 0.7 for a segment's own contribution.  64 KB a chunk and SM are 6.3 and 7.3 TB/s
+// only outputs do, 1.0 and 0.65 for a segment's own contribution.  64 KB a chunk and SM are 6.3 and 7.3 TB/s
 // (grouped heads find a part of theirs in L2); what bounds it is a chunk's way through the roles,
 // and of that the instructions fetched anew for each chunk.  Every piece of a role's loop is
 // therefore written for few instructions rather than few steps.
