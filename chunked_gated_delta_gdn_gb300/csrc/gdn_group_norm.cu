@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kGnThreads, kSlabPerSm)
   constexpr int kP = kPairs<V>;
   const SlabPlace p = slab_place(s, a.C, a.G);
   const SlabRange rr = slab_range(s, p, a.L, a.C);
+  next_may_start();
   Moments mo{0.f, 0.f, 0.f};
   if (p.on) {
     // Eight rows at a time: sums and squares about the mean of the first pack (so that squares much
@@ -211,6 +212,8 @@ __device__ __forceinline__ float slab_count(const SlabPlan& s, int L, int q) {
 // launch instead, 250 slabs of 32 groups took it longer than the rest of its work.)
 __global__ void __launch_bounds__(kGnThreads) gn_slab_merge_kernel(const GroupNormArgs a, const SlabPlan s,
                                                                    const float2* part, float2* stats) {
+  next_may_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, Q = s.chunks * s.parts;
   const long long i = (long long)blockIdx.x * (kGnThreads / 32) + (threadIdx.x >> 5);
   if (i >= (long long)a.N * a.G) return;
@@ -243,12 +246,15 @@ __global__ void __launch_bounds__(kGnThreads, kSlabPerSm)
   using P = Pair<V>;
   constexpr int kIn = kGate ? 2 : 1, kP = kPairs<V>;
   const SlabPlace p = slab_place(s, a.C, a.G);
+  P w[kP], b[kP];
+  if (p.on) {
+    params<V>(a.weight, p.c, a.wb_dtype, 1.f, w);
+    params<V>(a.bias, p.c, a.wb_dtype, 0.f, b);
+  }
+  wait_for_previous();
   if (!p.on) return;
   const SlabRange rr = slab_range(s, p, a.L, a.C);
   const float2 st = stats[(size_t)p.n * a.G + p.g];
-  P w[kP], b[kP];
-  params<V>(a.weight, p.c, a.wb_dtype, 1.f, w);
-  params<V>(a.bias, p.c, a.wb_dtype, 0.f, b);
 #pragma unroll
   for (int i = 0; i < kP; ++i) w[i] = mul(w[i], both<P>(st.y));
   const void* src[kIn];
@@ -294,14 +300,15 @@ cudaError_t launch_fwd(const GroupNormArgs& a) {
   float2* part = reinterpret_cast<float2*>(a.workspace);
   constexpr int kStats = Ring<T, V, 1, slab_steps<1>>::kShared;
   constexpr int kApply = Ring<T, V, kGate ? 2 : 1, slab_steps<kGate ? 2 : 1>>::kShared;
-  const cudaError_t err = allow_shared<gn_slab_fwd_kernel<T, V, kGate>, kApply>();
+  cudaError_t err = allow_shared<gn_slab_fwd_kernel<T, V, kGate>, kApply>();
   if (err != cudaSuccess) return err;
   gn_slab_stats_kernel<T, V><<<grid, kGnThreads, kStats, a.stream>>>(a, s, part);
   float2* stats = part + (size_t)a.N * a.G * s.chunks * s.parts;
   const unsigned warps = kGnThreads / 32, merge_grid = (unsigned)(((long long)a.N * a.G + warps - 1) / warps);
-  gn_slab_merge_kernel<<<merge_grid, kGnThreads, 0, a.stream>>>(a, s, part, stats);
-  gn_slab_fwd_kernel<T, V, kGate><<<grid, kGnThreads, kApply, a.stream>>>(a, s, stats);
-  return cudaGetLastError();
+  if ((err = cudaGetLastError()) != cudaSuccess ||
+      (err = launch_behind(gn_slab_merge_kernel, merge_grid, kGnThreads, 0, a.stream, a, s, part, stats)) != cudaSuccess)
+    return err;
+  return launch_behind(gn_slab_fwd_kernel<T, V, kGate>, grid, kGnThreads, kApply, a.stream, a, s, stats);
 }
 
 template <typename T, int V>

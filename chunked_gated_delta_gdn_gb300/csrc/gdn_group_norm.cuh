@@ -10,6 +10,7 @@
 #include "gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_group_norm.h"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace {

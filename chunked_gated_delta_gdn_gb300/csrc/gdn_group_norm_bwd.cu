@@ -58,6 +58,7 @@ __device__ void sum_sets(const GroupNormArgs& a, const float* part, int sets, in
   }
 }
 __global__ void __launch_bounds__(1024) gn_sum_sets_kernel(const GroupNormArgs a, const float* part, int sets) {
+  wait_for_previous();
   sum_sets<32>(a, part, sets, blockIdx.x);
 }
 
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(kGnThreads, VPT == 1 ? kRowPerSm : 1)
   extern __shared__ __align__(16) uint8_t smem[];
   using P = Pair<V>;
   constexpr int kIn = kGate ? 3 : 2, kP = kPairs<V>;
+  next_may_start();
   const RowPlace p = row_place(q, a.G);
   const RowVectors<V, VPT> at(q, p, a.L, a.C, a.G);
   const int D = a.C / a.G;
@@ -205,6 +207,7 @@ __global__ void __launch_bounds__(kGnThreads, kSlabPerSm)
   const SlabPlace p = slab_place(s, a.C, a.G);
   using P = Pair<V>;
   constexpr int kP = kPairs<V>;
+  next_may_start();
   P Ap[kP], Bp[kP];
 #pragma unroll
   for (int i = 0; i < kP; ++i) Ap[i] = Bp[i] = both<P>(0.f);
@@ -287,6 +290,8 @@ __global__ void __launch_bounds__(kGnThreads, kSlabPerSm)
 // m1, m2 of every group from its slabs' shares, a warp a group.
 __global__ void __launch_bounds__(kGnThreads) gn_slab_means_kernel(const GroupNormArgs a, int Q, const float2* share,
                                                                    float2* means) {
+  next_may_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const long long i = (long long)blockIdx.x * (kGnThreads / 32) + (threadIdx.x >> 5);
   if (i >= (long long)a.N * a.G) return;
@@ -306,6 +311,7 @@ __global__ void __launch_bounds__(kGnThreads) gn_slab_means_kernel(const GroupNo
 template <typename T, int V, bool kGate>
 __global__ void __launch_bounds__(kGnThreads, kSlabPerSm)
     gn_slab_bwd_kernel(const GroupNormArgs a, const SlabPlan s, int slabs, const float* part, const float2* means) {
+  wait_for_previous();
   if ((int)blockIdx.x >= slabs) {
     sum_sets<kGnThreads / 32>(a, part, a.N * s.chunks, blockIdx.x - slabs);
     return;
@@ -362,8 +368,7 @@ cudaError_t launch_bwd(const GroupNormArgs& a) {
     err = r.VPT == 1 ? launch_row_bwd<T, V, 1, kGate>(a, r, to)
                      : launch_row_bwd<T, V, kRowValues / V, kGate>(a, r, to);
     if (err != cudaSuccess || !params) return err;
-    gn_sum_sets_kernel<<<sum_ctas, 1024, 0, a.stream>>>(a, part, r.sets);
-    return cudaGetLastError();
+    return launch_behind(gn_sum_sets_kernel, sum_ctas, 1024, 0, a.stream, a, part, r.sets);
   }
   const SlabPlan s = slab_plan(a.N, a.L, a.C, a.G, a.io_dtype);
   const int slabs = a.N * s.NCB * s.chunks;
@@ -379,10 +384,12 @@ cudaError_t launch_bwd(const GroupNormArgs& a) {
   const int Q = s.chunks * s.parts;
   float2* means = share + (size_t)a.N * a.G * Q;
   const unsigned warps = kGnThreads / 32, means_grid = (unsigned)(((long long)a.N * a.G + warps - 1) / warps);
-  gn_slab_means_kernel<<<means_grid, kGnThreads, 0, a.stream>>>(a, Q, share, means);
-  gn_slab_bwd_kernel<T, V, kGate><<<slabs + (params ? sum_ctas : 0), kGnThreads, kRing, a.stream>>>(a, s, slabs,
-                                                                                                part, means);
-  return cudaGetLastError();
+  if ((err = cudaGetLastError()) != cudaSuccess ||
+      (err = launch_behind(gn_slab_means_kernel, means_grid, kGnThreads, 0, a.stream, a, Q, share, means)) !=
+          cudaSuccess)
+    return err;
+  return launch_behind(gn_slab_bwd_kernel<T, V, kGate>, slabs + (params ? sum_ctas : 0), kGnThreads, kRing, a.stream,
+                       a, s, slabs, part, means);
 }
 
 template <typename T, int V>

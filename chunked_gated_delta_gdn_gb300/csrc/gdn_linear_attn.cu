@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "gdn_launch.cuh"
 #include "gdn_linear_attn.cuh"
 
 namespace gdn {
@@ -117,18 +118,25 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
   float* sW = sP + kChunk * (kChunk + 4);   // gamma^0 .. gamma^64
   constexpr int PS = kChunk + 4;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  if (local_only) next_may_start();
   const LaChain c = la_chain(p, n, h, tid == 0 && h == 0 && seg == 0);
   const int T_total = p.cu_seqlens ? p.T : p.B * p.T;
   if (seg == 0 && !local_only) {
     la_zero_rows(p, h, c.tail, T_total, tid, kLaThreads);
     if (c.padding) la_zero_rows(p, h, c.bos, c.eos, tid, kLaThreads);
   }
-  if (c.skip || c.padding) return;
+  if (c.skip || c.padding) {
+    wait_for_previous();
+    return;
+  }
   const int nch = (c.eos - c.bos + kChunk - 1) / kChunk;
   const int per = max(1, (nch + segs - 1) / segs);
   const int c0 = min(seg * per, nch), c1 = min(c0 + per, nch);
   const bool last = c1 == nch, whole = seg == 0 && last;
-  if (local_only ? last : (c0 == c1 && !whole)) return;
+  if (local_only ? last : (c0 == c1 && !whole)) {
+    wait_for_previous();
+    return;
+  }
   const float ld = clamp_log_decay(p.log_decay[h]);
   // decay over a full chunk, the partial chunk and each segment before this one (by one thread each:
   // they are made in 64 bits)
@@ -143,6 +151,7 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
   __syncthreads();
   float* slots =   // (segs > 1 only)
       a.scratch + ((size_t)(pi * p.num_seqs + n) * p.H + h) * segs * (size_t)(K * V);
+  wait_for_previous();
   {   // the entry state
     const float* init = whole || (local_only && seg == 0) ? c.init : nullptr;
     for (int e = tid; e < K * V; e += kLaThreads) {
@@ -461,8 +470,9 @@ cudaError_t launch_linear_attn_generic(const LinAttnPass* passes, int num_passes
     linear_attn_kernel<<<(unsigned)(chains * (segs - 1)), kLaThreads, smem, p0.stream>>>(a);
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     a.local_only = 0;
+    return launch_behind(linear_attn_kernel, (unsigned)(chains * segs), kLaThreads, smem, p0.stream, a);
   }
-  linear_attn_kernel<<<(unsigned)(chains * segs), kLaThreads, smem, p0.stream>>>(a);
+  linear_attn_kernel<<<(unsigned)chains, kLaThreads, smem, p0.stream>>>(a);
   return cudaGetLastError();
 }
 

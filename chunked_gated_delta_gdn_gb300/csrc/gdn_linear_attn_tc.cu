@@ -57,6 +57,7 @@
 #include <cstring>
 
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 #include "gdn_linear_attn.cuh"
 #include "gdn_sm100.cuh"
 
@@ -885,6 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   volatile int* flag = reinterpret_cast<volatile int*>(sm + OFF_FLAG);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + OFF_TSLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (a.local_only) next_may_start();   // (the second launch's CTAs, as SMs come free)
   Unit u;
   // chains by heads (those that share a row of q or k run side by side), sequences, passes
   int e = blockIdx.x, seg = 0, segs = 1, chain_cut = 0;
@@ -910,7 +912,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
     la_zero_rows(p, u.h, c.tail, p.cu_seqlens ? p.T : p.B * p.T, tid, kThreads);
     if (c.padding) la_zero_rows(p, u.h, c.bos, c.eos, tid, kThreads);
   }
-  if (c.skip || c.padding) return;
+  if (c.skip || c.padding) {
+    wait_for_previous();
+    return;
+  }
   u.bos = c.bos;
   u.eos = c.eos;
   u.nch = (c.eos - c.bos + kChunk - 1) / kChunk;
@@ -929,6 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   u.store = local_only ? local + (size_t)(seg + 1) * 16384 : nullptr;
   u.copy = local_only && seg == 0 ? local : nullptr;
   if (u.c0 == u.c1) {
+    wait_for_previous();
     if (whole && u.fin)   // empty sequence: the state passes through
       for (int x = tid; x < p.K * p.V; x += kThreads) {
         const int kk = x / p.V, vv = x - kk * p.V;
@@ -978,6 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
+  wait_for_previous();
   // a segment's contribution may end in a final state; the passes from it to there add nothing
   const int terms = u.fin || (u.store && p.final_state) ? 4 : 2;
 
@@ -1056,8 +1063,9 @@ cudaError_t launch_linear_attn_tc(const LinAttnPass* passes, int num_passes, LaP
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
     a.local_only = 0;
     a.whole = 0;
+    return launch_behind(linear_attn_tc_kernel, (unsigned)(cut * segs), kThreads, SMEM_BYTES, p0.stream, a);
   }
-  linear_attn_tc_kernel<<<(unsigned)(cut > 0 ? cut * segs : plan.whole), kThreads, SMEM_BYTES, p0.stream>>>(a);
+  linear_attn_tc_kernel<<<(unsigned)plan.whole, kThreads, SMEM_BYTES, p0.stream>>>(a);
   return cudaGetLastError();
 }
 
