@@ -77,7 +77,8 @@ constexpr uint32_t kStage = 49152;                 // [k half][Q 64 rows | K 64 
 constexpr uint32_t kStageV = 32768;                // [v half][64 tokens][128 B]
 constexpr uint32_t OFF_P = kStages * kStage;       // [64 i][64 j] bf16
 constexpr uint32_t OFF_P_REST = kStage;   // (a sequence of one chunk leaves the second stage empty)
-constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 tokens][128 B]
+constexpr uint32_t OFF_O = OFF_P + 8192;           // output tile, [v half][64 tokens][128 B]; before its
+                                                   // first use the lengths of packed sequences
 constexpr uint32_t OFF_W = OFF_O + 16384;          // float[72]: w_0 .. w_64
 constexpr uint32_t OFF_F = OFF_W + 288;            // Weights4[2][16]: the weights of V~ in a full and
                                                    // in the partial chunk
@@ -852,8 +853,11 @@ __device__ bool out_role(const LinAttnPass& p, const Unit& u, uint8_t* sm, uint3
 }
 
 // The sequence that stands at `place` by length, longest first (equals by number): CTAs start in
-// order, and a long chain that starts among the last keeps the others waiting.
+// order, and a long chain that starts among the last keeps the others waiting.  `len` must be shared
+// memory that no load lands in: nothing orders these ordinary accesses before the asynchronous writes
+// of the first chunk.
 constexpr int kMaxSorted = 128;
+static_assert(OFF_O >= kStages * kStage && 4 * (kMaxSorted + 1) <= 16384, "lengths in the output tile");
 __device__ __forceinline__ int sequence_by_length(const int32_t* cu, int n, int place, int* len) {
   const int t = threadIdx.x;
   if (t < n) len[t] = cu[t + 1] - cu[t];
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_attn_tc_kernel(const __gri
   int n = e % a.pass[0].num_seqs;
   e /= a.pass[0].num_seqs;
   if (a.longest_first)
-    n = sequence_by_length(a.pass[0].cu_seqlens, a.pass[0].num_seqs, n, reinterpret_cast<int*>(sm));
+    n = sequence_by_length(a.pass[0].cu_seqlens, a.pass[0].num_seqs, n, reinterpret_cast<int*>(sm + OFF_O));
   const int pi = e;
   const LinAttnPass p = a.pass[pi];
   const LaChain c = la_chain(p, n, u.h, tid == 0 && u.h == 0 && seg == 0);
