@@ -21,9 +21,12 @@ namespace gdn {
 namespace {
 
 // ------------------------------------------------------------------ groups in registers
-constexpr int kRowSteps = 4;
 constexpr int kRowValues = 32;   // values a lane holds
 constexpr int kRowPerSm = 4;     // CTAs an SM (registers)
+// Steps of a lane's ring: four, or what a CTA's shared memory holds (three of 64 KB for 32 fp32 values
+// a lane with a gate).
+template <typename T, int V, int VPT, bool kGate>
+constexpr int row_steps = std::min(4, kMaxDynamic / (VPT * (kGate ? 2 : 1) * V * (int)sizeof(T) * kGnThreads));
 
 template <typename T, int V, int VPT, bool kGate>
 __global__ void __launch_bounds__(kGnThreads, VPT == 1 ? kRowPerSm : 1)
@@ -49,8 +52,8 @@ __global__ void __launch_bounds__(kGnThreads, VPT == 1 ? kRowPerSm : 1)
   src[0] = a.x;
   if (kGate) src[kIn - 1] = a.gate;
   const size_t stride = (size_t)rg.step * a.L * a.C;
-  walk<T, V, VPT, kIn, kRowSteps>(smem, src, from, at.in, stride, rg.mine, rg.turns,
-                                  [&](auto& ring, int u, int t, size_t here) {
+  walk<T, V, VPT, kIn, row_steps<T, V, VPT, kGate>>(smem, src, from, at.in, stride, rg.mine, rg.turns,
+                                                    [&](auto& ring, int u, int t, size_t here) {
     // about the group's first value: the mean, then the squared deviations
     P v[VPT][kP];
 #pragma unroll
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kGnThreads, kSlabPerSm)
 
 template <typename T, int V, int VPT, bool kGate>
 cudaError_t launch_row_fwd(const GroupNormArgs& a, const RowPlan& r) {
-  constexpr int kShared = Ring<T, V, VPT * (kGate ? 2 : 1), kRowSteps>::kShared;
+  constexpr int kShared = Ring<T, V, VPT * (kGate ? 2 : 1), row_steps<T, V, VPT, kGate>>::kShared;
   const cudaError_t err = allow_shared<gn_row_fwd_kernel<T, V, VPT, kGate>, kShared>();
   if (err != cudaSuccess) return err;
   gn_row_fwd_kernel<T, V, VPT, kGate><<<(unsigned)(r.sets * r.across), kGnThreads, kShared, a.stream>>>(a, r);

@@ -379,8 +379,10 @@ struct RowVectors {
 
 // Lets a kernel have kBytes of dynamic shared memory beside its static arrays of up to 8 KB (set
 // once a device and kernel).
+constexpr int kMaxDynamic = 232448 - 8 * 1024;
 template <auto kKernel, int kBytes>
 cudaError_t allow_shared() {
+  static_assert(kBytes <= kMaxDynamic, "more shared memory than a CTA can have");
   if (kBytes <= 40 * 1024) return cudaSuccess;
   static std::atomic<bool> done[64];
   int dev = 0;
