@@ -5,6 +5,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_status.h"
 
 namespace {
 
@@ -148,7 +149,7 @@ static gdn_status_t chunk_impl(const void* q, const void* k, const void* v, cons
     if (!aligned16(workspace)) return GDN_ERR_LAYOUT;
     err = gdn::launch_chunk_generic(a);
   }
-  return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::status_of(err);
 }
 
 gdn_status_t gdn_chunk_fwd(const void* q, const void* k, const void* v, const float* g,
@@ -257,7 +258,7 @@ gdn_status_t gdn_chunk_bwd(const void* q, const void* k, const void* v, const fl
   b.d_final = d_final_state;
   b.dq = dq; b.dk = dk; b.dv = dv; b.dg = dg; b.dbeta = dbeta;
   b.d_initial = d_initial_state;
-  return gdn::launch_chunk_bwd(a, b) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::status_of(gdn::launch_chunk_bwd(a, b));
 }
 
 size_t gdn_chunk_bwd_gated_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
@@ -313,15 +314,14 @@ gdn_status_t gdn_chunk_bwd_gated(const void* q, const void* k, const void* v, co
   gates.ab_dtype = ab_dtype;
   gates.A_log = A_log;
   gates.dt_bias = dt_bias;
-  if (gdn::launch_gates_materialise(gates, T_total, Hv, g, beta, s) != cudaSuccess) return GDN_ERR_CUDA;
+  st = gdn::status_of(gdn::launch_gates_materialise(gates, T_total, Hv, g, beta, s));
+  if (st != GDN_OK) return st;
   st = gdn_chunk_bwd(q, k, v, g, beta, B, T, Hqk, Hv, K, V, io_dtype, GDN_F32, scale, chunk_size,
                      initial_state, use_qk_l2norm, cu_seqlens, num_seqs, d_o, d_final_state, dq,
                      dk, dv, dg, dbeta, d_initial_state, workspace, inner, dev_status, stream);
   if (st != GDN_OK) return st;
-  return gdn::launch_gates_bwd(gates, dg, dbeta, T_total, Hv, da, db, dA_log, ddt_bias, partial,
-                               s) == cudaSuccess
-             ? GDN_OK
-             : GDN_ERR_CUDA;
+  return gdn::status_of(
+      gdn::launch_gates_bwd(gates, dg, dbeta, T_total, Hv, da, db, dA_log, ddt_bias, partial, s));
 }
 
 static gdn_status_t decode_impl(const void* q, const void* k, const void* v, const float* g,
@@ -361,7 +361,7 @@ static gdn_status_t decode_impl(const void* q, const void* k, const void* v, con
   a.L = L;
   a.intermediate = intermediate;
   a.product = product;
-  return gdn::launch_decode(a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::status_of(gdn::launch_decode(a));
 }
 
 gdn_status_t gdn_decode(const void* q, const void* k, const void* v, const float* g,
@@ -476,18 +476,16 @@ gdn_status_t gdn_product_chunk_fwd(const void* q, const void* k, const void* v, 
   int32_t* cu_exp = reinterpret_cast<int32_t*>(w + align256(te * Hqk * K * es) +
                                                align256(te * Hv * 4) + align256(te * Hv * V * es));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (gdn::launch_product_expand(q, g, q_exp, g_exp, cu_seqlens, cu_exp, T_total, n_h, Hqk, Hv,
-                                 K, io_dtype, num_seqs, s) != cudaSuccess)
-    return GDN_ERR_CUDA;
+  st = gdn::status_of(gdn::launch_product_expand(q, g, q_exp, g_exp, cu_seqlens, cu_exp, T_total, n_h,
+                                                 Hqk, Hv, K, io_dtype, num_seqs, s));
+  if (st != GDN_OK) return st;
   st = chunk_impl(q_exp, k, v, g_exp, beta, B, T * n_h, Hqk, Hv, K, V, io_dtype, beta_dtype,
                   scale, chunk_size, initial_state, output_final_state, final_state,
                   use_qk_l2norm, cu_seqlens ? cu_exp : nullptr, num_seqs, state_indices,
                   num_slots, o_exp, w + inner_off, workspace_bytes - inner_off, dev_status,
                   stream, gates);
   if (st != GDN_OK) return st;
-  return gdn::launch_product_gather(o_exp, o, T_total, n_h, Hv, V, io_dtype, s) == cudaSuccess
-             ? GDN_OK
-             : GDN_ERR_CUDA;
+  return gdn::status_of(gdn::launch_product_gather(o_exp, o, T_total, n_h, Hv, V, io_dtype, s));
 }
 
 gdn_status_t gdn_product_decode(const void* q, const void* k, const void* v, const float* g,

@@ -5,6 +5,7 @@
 
 #include "gdn.h"
 #include "gdn_group_norm.h"
+#include "gdn_status.h"
 
 namespace {
 
@@ -64,7 +65,7 @@ gdn_status_t gdn_group_norm_act_fwd(const void* x, const void* weight, const voi
   a.y = y; a.mean = mean; a.rstd = rstd;
   a.workspace = workspace;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
-  return gdn::launch_group_norm_fwd(a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::status_of(gdn::launch_group_norm_fwd(a));
 }
 
 size_t gdn_group_norm_act_bwd_workspace_size(int N, int L, int C, int G, gdn_dtype_t io_dtype) {
@@ -84,10 +85,9 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (!aligned_to(dweight, 4) || !aligned_to(dbias, 4)) return GDN_ERR_LAYOUT;
   if ((long long)N * L == 0) {   // no element: the parameters' gradients are zero
-    const bool ok =
-        (!dweight || cudaMemsetAsync(dweight, 0, sizeof(float) * C, s) == cudaSuccess) &&
-        (!dbias || cudaMemsetAsync(dbias, 0, sizeof(float) * C, s) == cudaSuccess);
-    return ok ? GDN_OK : GDN_ERR_CUDA;
+    if (dweight) st = gdn::status_of(cudaMemsetAsync(dweight, 0, sizeof(float) * C, s));
+    if (st == GDN_OK && dbias) st = gdn::status_of(cudaMemsetAsync(dbias, 0, sizeof(float) * C, s));
+    return st;
   }
   if (!dy || !x || !mean || !rstd || !dx || (gate && !dgate)) return GDN_ERR_NULL;
   if (!aligned_to(dy, 16) || !aligned_to(x, 16) || !aligned_to(gate, 16) || !aligned_to(dx, 16) ||
@@ -109,7 +109,7 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
   a.dx = dx; a.dgate = dgate; a.dweight = dweight; a.dbias = dbias;
   a.workspace = workspace;
   a.stream = s;
-  return gdn::launch_group_norm_bwd(a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::status_of(gdn::launch_group_norm_bwd(a));
 }
 
 }  // extern "C"

@@ -6,6 +6,7 @@
 #include "gdn.h"
 #include "gdn_internal.h"
 #include "gdn_linear_attn.h"
+#include "gdn_status.h"
 
 namespace {
 
@@ -125,10 +126,9 @@ gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void*
   gdn::LinAttnPass p =
       base_pass(log_decay, B, T, Hv, io_dtype, cu_seqlens, num_seqs, dev_status, stream);
   if (num_seqs == 0)   // no sequence: no token belongs to one
-    return T_total == 0 || cudaMemsetAsync(o, 0, (size_t)T_total * Hv * V * elem_size(io_dtype),
-                                           p.stream) == cudaSuccess
-               ? GDN_OK
-               : GDN_ERR_CUDA;
+    return T_total == 0 ? GDN_OK
+                        : gdn::status_of(cudaMemsetAsync(
+                              o, 0, (size_t)T_total * Hv * V * elem_size(io_dtype), p.stream));
   p.q = q; p.k = k; p.v = v;
   p.Hq = p.Hk = Hqk;
   p.Hv = Hv;
@@ -141,7 +141,7 @@ gdn_status_t gdn_linear_attn_chunk_fwd(const void* q, const void* k, const void*
   p.o = o;
   const Scratch sc = scratch(1, B, T, num_seqs, B == 1, Hqk, Hv, K, V, io_dtype);
   if ((st = check_workspace(workspace, workspace_bytes, sc.total)) != GDN_OK) return st;
-  return run_passes(&p, 1, sc.plan, workspace) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::status_of(run_passes(&p, 1, sc.plan, workspace));
 }
 
 size_t gdn_linear_attn_chunk_bwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
@@ -181,11 +181,11 @@ gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void*
       base_pass(log_decay, B, T, Hv, io_dtype, cu_seqlens, num_seqs, dev_status, stream);
   if (num_seqs == 0) {
     const size_t es = elem_size(io_dtype) * (size_t)T_total;
-    const bool ok = T_total == 0 ||
-                    (cudaMemsetAsync(dq, 0, es * Hqk * K, base.stream) == cudaSuccess &&
-                     cudaMemsetAsync(dk, 0, es * Hqk * K, base.stream) == cudaSuccess &&
-                     cudaMemsetAsync(dv, 0, es * Hv * V, base.stream) == cudaSuccess);
-    return ok ? GDN_OK : GDN_ERR_CUDA;
+    if (T_total == 0) return GDN_OK;
+    st = gdn::status_of(cudaMemsetAsync(dq, 0, es * Hqk * K, base.stream));
+    if (st == GDN_OK) st = gdn::status_of(cudaMemsetAsync(dk, 0, es * Hqk * K, base.stream));
+    if (st == GDN_OK) st = gdn::status_of(cudaMemsetAsync(dv, 0, es * Hv * V, base.stream));
+    return st;
   }
   const float sc = resolve_scale(scale, K);
   const int group = Hv / Hqk;
@@ -229,14 +229,15 @@ gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void*
   p[2].s_in = sc;
   p[2].reverse = 1;
   p[2].o = dv;
-  if (run_passes(p, 3, ws.plan, workspace) != cudaSuccess) return GDN_ERR_CUDA;
+  st = gdn::status_of(run_passes(p, 3, ws.plan, workspace));
+  if (st != GDN_OK) return st;
   if (group > 1) {
     const float* const in[2] = {part[0], part[1]};
     void* const out[2] = {dq, dk};
-    if (gdn::launch_linear_attn_fold(in, out, T_total, Hqk, group, K, io_dtype, base.stream) != cudaSuccess)
-      return GDN_ERR_CUDA;
+    st = gdn::status_of(
+        gdn::launch_linear_attn_fold(in, out, T_total, Hqk, group, K, io_dtype, base.stream));
   }
-  return GDN_OK;
+  return st;
 }
 
 gdn_status_t gdn_linear_attn_decode(const void* q, const void* k, const void* v,
@@ -264,7 +265,7 @@ gdn_status_t gdn_linear_attn_decode(const void* q, const void* k, const void* v,
   a.o = o;
   a.dev_status = dev_status;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
-  return gdn::launch_linear_attn_decode(a) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return gdn::status_of(gdn::launch_linear_attn_decode(a));
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@
 // device array instead, so nothing is allocated per call.
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_status.h"
 
 namespace {
 
@@ -32,8 +33,8 @@ cudaError_t scratch_on_current_device(void** out) {
 bool stream_on_current_device(void* stream) {
   if (!stream) return true;
   int cur = 0, sdev = 0;
-  if (cudaGetDevice(&cur) != cudaSuccess) return false;
-  if (cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &sdev) != cudaSuccess) return false;
+  if (gdn::status_of(cudaGetDevice(&cur)) != GDN_OK) return false;
+  if (gdn::status_of(cudaStreamGetDevice(static_cast<cudaStream_t>(stream), &sdev)) != GDN_OK) return false;
   return sdev == cur;
 }
 
@@ -60,7 +61,8 @@ extern "C" gdn_status_t gdn_chunk_fwd_noalloc(
     return GDN_ERR_WORKSPACE;
   if (!stream_on_current_device(stream)) return GDN_ERR_CUDA;
   void* scratch = nullptr;
-  if (scratch_on_current_device(&scratch) != cudaSuccess) return GDN_ERR_CUDA;
+  const gdn_status_t st = gdn::status_of(scratch_on_current_device(&scratch));
+  if (st != GDN_OK) return st;
   return gdn_chunk_fwd(q, k, v, g, beta, B, T, Hqk, Hv, K, V, io_dtype, beta_dtype, scale,
                        chunk_size, initial_state, output_final_state, final_state, use_qk_l2norm,
                        cu_seqlens, num_seqs, state_indices, num_slots, o, scratch,
