@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from .api import _DT, _need, _ptr
-from .linear_attn import _fit, _scratch, _stream
+from .linear_attn import _first_only, _fit, _scratch, _stream
 
 __all__ = ["group_norm_act", "group_norm_act_bwd", "group_norm_act_trainable"]
 
@@ -155,11 +155,16 @@ class _GroupNormAct(torch.autograd.Function):
         mean = stats.data_ptr()
         dx, dw, db, dgate = _backward(dy, x, mean, mean + 4 * sizes[0] * sizes[3], sizes, weight,
                                       bias, gate, need[2] or need[3], None)
-        return (dx, None, dw.to(weight.dtype) if need[2] else None,
-                db.to(bias.dtype) if need[3] else None, None, None, dgate)
+        grads = (dx, dw.to(weight.dtype) if need[2] else None, db.to(bias.dtype) if need[3] else None,
+                 dgate)
+        if torch.is_grad_enabled():
+            grads = _first_only("group_norm_act_trainable", grads, (x, weight, bias, gate, dy))
+        dx, dw, db, dgate = grads
+        return dx, None, dw, db, None, None, dgate
 
 
 def group_norm_act_trainable(x, num_groups, weight=None, bias=None, eps=1e-5, activation="silu",
                              gate=None):
-    """:func:`group_norm_act` as a differentiable op (torch autograd) in x, weight, bias, gate."""
+    """:func:`group_norm_act` as a differentiable op (torch autograd) in x, weight, bias, gate; a second
+    derivative is refused."""
     return _GroupNormAct.apply(x, num_groups, weight, bias, eps, activation, gate)

@@ -163,6 +163,27 @@ def chunk_linear_attn_bwd(q, k, v, log_decay, d_o, d_final_state=None, scale=Non
     return dq, dk, dv, dh0
 
 
+class _FirstOnly(torch.autograd.Function):
+    """Hands ``count`` gradients on and stands between them and what they depend on, for a second
+    derivative to meet: without it they would be constants, and its terms would be missing."""
+
+    @staticmethod
+    def forward(ctx, name, count, *tensors):
+        ctx.name = name
+        return tensors[:count]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("%s has no second derivative" % ctx.name)
+
+
+def _first_only(name, grads, inputs):
+    """What a backward returns under ``create_graph``: ``grads``, made from ``inputs``."""
+    made = [g for g in grads if g is not None]
+    made = iter(_FirstOnly.apply(name, len(made), *made, *inputs))
+    return tuple(None if g is None else next(made) for g in grads)
+
+
 class _ChunkLinearAttn(torch.autograd.Function):
     """gdn_linear_attn_chunk_fwd forward, gdn_linear_attn_chunk_bwd backward."""
 
@@ -179,17 +200,20 @@ class _ChunkLinearAttn(torch.autograd.Function):
     def backward(ctx, d_o, d_fin):
         q, k, v, log_decay, init, cu = ctx.saved_tensors
         d_o = torch.zeros_like(v) if d_o is None else d_o.contiguous()
-        dq, dk, dv, dh0 = chunk_linear_attn_bwd(
+        grads = chunk_linear_attn_bwd(
             q, k, v, log_decay, d_o, None if d_fin is None else d_fin.contiguous(),
             scale=ctx.scale, initial_state=init, cu_seqlens=cu,
             need_d_initial_state=init is not None and ctx.needs_input_grad[4])
+        if torch.is_grad_enabled():
+            grads = _first_only("chunk_linear_attn_trainable", grads, (q, k, v, init, d_o, d_fin))
+        dq, dk, dv, dh0 = grads
         return dq, dk, dv, None, dh0, None, None, None
 
 
 def chunk_linear_attn_trainable(q, k, v, log_decay, scale=None, initial_state=None,
                                 output_final_state=False, cu_seqlens=None):
     """:func:`chunk_linear_attn` as a differentiable op (torch autograd) in q, k, v and
-    ``initial_state``.  Returns ``(o, final_state or None)``."""
+    ``initial_state``; a second derivative is refused.  Returns ``(o, final_state or None)``."""
     if log_decay.requires_grad:
         raise ValueError("log_decay is a constant of the layer: it has no gradient")
     return _ChunkLinearAttn.apply(q, k, v, log_decay, initial_state, scale,
