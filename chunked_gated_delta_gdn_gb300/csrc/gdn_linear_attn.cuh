@@ -26,6 +26,17 @@ __device__ __forceinline__ float2 decay_pow2(float ld, int n) {
   return make_float2(hi, isinf(hi) ? 0.f : (float)(g - (double)hi));
 }
 __device__ __forceinline__ float mul2(float x, float2 g) { return fmaf(x, g.x, x * g.y); }
+// x g + y, rounded once but for y's own size.
+__device__ __forceinline__ float mul2_add(float x, float2 g, float y) { return fmaf(x, g.x, fmaf(x, g.y, y)); }
+
+// gamma as hi + lo without 64 bits (those take a decode step 4 us of 170): 1 + (gamma - 1), the
+// difference to 24 bits, is off by 2^-24 |gamma - 1|, so by some 2^-24 over the whole memory of
+// 1 / |gamma - 1| tokens.  Below exp(-0.7) a memory is a few tokens and 24 bits of gamma serve.
+__device__ __forceinline__ float2 decay_pair(float ld) {
+  if (fabsf(ld) >= 0.7f) return make_float2(expf(ld), 0.f);
+  const float d = expm1f(ld), hi = 1.f + d;
+  return make_float2(hi, d - (hi - 1.f));
+}
 
 // What one (sequence, head) chain works on.
 struct LaChain {

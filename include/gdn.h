@@ -484,6 +484,9 @@ gdn_status_t gdn_linear_attn_chunk_bwd(const void* q, const void* k, const void*
  * gdn_linear_attn_decode -- one token per request on a slot cache, in place: the recurrent form.
  * Slots, padding (-1: a zero row, the state untouched), errors and layouts as gdn_decode:
  *   q, k [n, Hqk, K];  v, o [n, Hv, V];  ssm_state [num_slots, Hv, K, V] fp32.
+ * The new state is rounded to fp32 once and the decay is exact to far less than that, so that a
+ * state does not drift from the chunked forward's over thousands of tokens.  (An infinite
+ * element of a state becomes NaN at the next token, as in the chunked forward.)
  */
 gdn_status_t gdn_linear_attn_decode(const void* q, const void* k, const void* v,
                                     const float* log_decay, float* ssm_state, int num_slots,
