@@ -272,22 +272,15 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
       if (last && cc + 1 == c1 && !c.fin) break;   // nobody wants the state any more
       __syncthreads();   // the state has been read
     }
-    // X: rows 4 ty + 64 a .. + 3, columns 4 tx + 64 m .. + 3
+    // X: rows 4 ty + 64 a .. + 3, columns 4 tx + 64 m .. + 3; the chunk's products are summed first, so
+    // that the state is rounded once a chunk (over a memory of 4096 tokens 4 u of error instead of 11)
     const float2 gl = sG[L == kChunk ? 0 : 1];
     const bool two = 4 * tx + 64 < V, one = 4 * tx < V;
 #pragma unroll
     for (int ma = 0; ma < 2; ++ma) {
       const int row = 4 * ty + 64 * ma;
       if (row >= K) break;
-      F4 acc[2][4];
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const F4 x = (m ? two : one) ? f4(sX + (row + i) * V + 4 * tx + 64 * m) : F4{};
-          acc[m][i] = F4{make_float2(mul2(x.a.x, gl), mul2(x.a.y, gl)),
-                         make_float2(mul2(x.b.x, gl), mul2(x.b.y, gl))};
-        }
+      F4 acc[2][4] = {};
 #pragma unroll 4
       for (int j = 0; j < L; ++j) {
         float4 kk = *reinterpret_cast<const float4*>(sK + j * KS + row);
@@ -310,7 +303,12 @@ __global__ void __launch_bounds__(kLaThreads, 2) linear_attn_kernel(const __grid
       for (int m = 0; m < 2; ++m)
         if (m ? two : one) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) put4(sX + (row + i) * V + 4 * tx + 64 * m, acc[m][i]);
+          for (int i = 0; i < 4; ++i) {
+            float* at = sX + (row + i) * V + 4 * tx + 64 * m;
+            const F4 x = f4(at), u = acc[m][i];
+            put4(at, F4{make_float2(mul2_add(x.a.x, gl, u.a.x), mul2_add(x.a.y, gl, u.a.y)),
+                        make_float2(mul2_add(x.b.x, gl, u.b.x), mul2_add(x.b.y, gl, u.b.y))});
+          }
         }
     }
   }

@@ -46,3 +46,25 @@ def test_decode_for_thousands_of_tokens(dtype):
     assert max(errs) <= 5e-6
     assert all(e <= 5e-6 for e, x in zip(exact, ld.tolist()) if x <= -1e-6 or x == 0)
     assert ref.rel(o[0], (q[-1, 0].double() @ R)[:, 0] / K ** 0.5) <= (5e-6 if dtype == torch.float32 else 4e-3)
+
+
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 96)])
+def test_fp32_state_is_rounded_once_a_chunk(K, V):
+    """A chunk's 64 products are summed and then added to the state, which is rounded once: with a
+    memory of 4096 tokens, 32 chunks in the mean square, 0.42 u sqrt(32) = 2.4 u; the chunk's sum, 0.18
+    of the state, by 0.42 u sqrt(32) of itself a chunk, the same again; the decay table's 1 u: about 4 u.
+    10 u allowed.  (Added to the state one by one they err by 0.42 u sqrt(2048) = 19 u.)"""
+    g = torch.Generator().manual_seed(6)
+    T = 8192
+    q, k, v = (torch.randn(1, T, 1, D, generator=g).cuda() for D in (K, K, V))
+    ld = torch.tensor([-2.0 ** -12], device="cuda")
+    h0 = 45 * torch.randn(1, 1, K, V, generator=g).cuda()     # as 2048 tokens leave it
+    _, fin = gdn.chunk_linear_attn(q, k, v, ld, initial_state=h0, output_final_state=True)
+    # the recurrence in 64 bits, 256 tokens at a time
+    S, t = h0[0, 0].double(), torch.arange(256, device="cuda", dtype=torch.float64)
+    left = torch.exp((255 - t) * ld.double())[:, None]
+    for b in range(0, T, 256):
+        S = torch.exp(256 * ld.double()) * S + (k[0, b:b + 256, 0].double() * left).T @ v[0, b:b + 256, 0].double()
+    e = ref.rel(fin[0, 0], S)
+    print("%.2f u" % (e * 2 ** 24))
+    assert e <= 10 * 2.0 ** -24
