@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from .api import _DT, _need, _ptr
-from .linear_attn import _first_only, _fit, _scratch, _stream
+from .linear_attn import _first_only, _fit, _incoming, _scratch, _stream
 
 __all__ = ["group_norm_act", "group_norm_act_bwd", "group_norm_act_trainable"]
 
@@ -149,7 +149,7 @@ class _GroupNormAct(torch.autograd.Function):
     def backward(ctx, dy):
         x, weight, bias, gate, stats = ctx.saved_tensors
         need, sizes = ctx.needs_input_grad, ctx.sizes
-        dy = dy.contiguous()
+        dy = _incoming(dy)
         if not _fit(x.device, (dy, x.dtype, x.shape)):
             _need(dy, "dy", x.dtype, x.device, x.shape)
         mean = stats.data_ptr()

@@ -163,6 +163,13 @@ def chunk_linear_attn_bwd(q, k, v, log_decay, d_o, d_final_state=None, scale=Non
     return dq, dk, dv, dh0
 
 
+def _incoming(t):
+    """An incoming gradient as the kernels take it: contiguous, on a 16-byte boundary (a part of a
+    larger gradient may start anywhere)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _FirstOnly(torch.autograd.Function):
     """Hands ``count`` gradients on and stands between them and what they depend on, for a second
     derivative to meet: without it they would be constants, and its terms would be missing."""
@@ -199,9 +206,9 @@ class _ChunkLinearAttn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, d_o, d_fin):
         q, k, v, log_decay, init, cu = ctx.saved_tensors
-        d_o = torch.zeros_like(v) if d_o is None else d_o.contiguous()
+        d_o = torch.zeros_like(v) if d_o is None else _incoming(d_o)
         grads = chunk_linear_attn_bwd(
-            q, k, v, log_decay, d_o, None if d_fin is None else d_fin.contiguous(),
+            q, k, v, log_decay, d_o, None if d_fin is None else _incoming(d_fin),
             scale=ctx.scale, initial_state=init, cu_seqlens=cu,
             need_d_initial_state=init is not None and ctx.needs_input_grad[4])
         if torch.is_grad_enabled():
