@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from .api import _DT, _need, _ptr
-from .linear_attn import _first_only, _fit, _incoming, _scratch, _stream
+from .linear_attn import _first_only, _fit, _incoming, _int32, _scratch, _stream
 
 __all__ = ["group_norm_act", "group_norm_act_bwd", "group_norm_act_trainable"]
 
@@ -35,6 +35,7 @@ def _inputs(x, num_groups, weight, bias, activation, gate):
     L = 1
     for s in x.shape[1:-1]:
         L *= s
+    _int32("group norm", N, L, C)
     if quick:
         wb = weight.dtype if isinstance(weight, torch.Tensor) else \
             bias.dtype if isinstance(bias, torch.Tensor) else torch.float32

@@ -38,6 +38,12 @@ def _stream(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _int32(name, *sizes):
+    """Refuses what the C interface's integers do not hold (ctypes would cut it down to 32 bits)."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError("sizes beyond 2^31 - 1 rejected by %s: %s" % (name, sizes))
+
+
 def _inputs(q, k, v, log_decay, cu_seqlens):
     """Checks shared by the chunked calls; returns (device, dtype, sizes, N)."""
     if (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 4 and q.dtype in _DT
@@ -45,12 +51,14 @@ def _inputs(q, k, v, log_decay, cu_seqlens):
         dev, dt = q.device, q.dtype
         B, T, Hqk, K = q.shape
         Hv, V = v.shape[2:]
+        _int32("linear attention", B, T, Hqk, K, Hv, V)
         if _fit(dev, (q, dt, (B, T, Hqk, K)), (k, dt, (B, T, Hqk, K)), (v, dt, (B, T, Hv, V)),
                 (log_decay, torch.float32, (Hv,))) and log_decay is not None and k is not None:
             if cu_seqlens is None:
                 return dev, dt, (B, T, Hqk, Hv, K, V), B
             if B == 1 and _fit(dev, (cu_seqlens, torch.int32, cu_seqlens.shape)) \
                     and cu_seqlens.dim() == 1 and cu_seqlens.shape[0] > 0:
+                _int32("linear attention", cu_seqlens.shape[0])
                 return dev, dt, (B, T, Hqk, Hv, K, V), cu_seqlens.shape[0] - 1
     _need(q, "q", (torch.float32, torch.bfloat16))
     dev, dt = q.device, q.dtype
@@ -103,6 +111,7 @@ def chunk_linear_attn(q, k, v, log_decay, scale=None, initial_state=None, output
         if cache is None:
             raise ValueError("state_indices needs initial_state or final_state (the slot cache)")
         num_slots = cache.shape[0]
+        _int32("linear attention", num_slots)
         st_shape = (num_slots, Hv, K, V)
         if output_final_state and final_state is None:
             final_state = initial_state
@@ -266,6 +275,7 @@ def linear_attn_decode(q, k, v, log_decay, ssm_state, batch_indices=None, scale=
             _need(batch_indices, "batch_indices", torch.int32, dev, (n,))
         if out is not None:
             _need(out, "out", dt, dev, (n, Hv, V))
+    _int32("linear attention", n, Hqk, K, Hv, V, ssm_state.shape[0])
     if out is None:
         out = torch.empty_like(v)
     dev_status = _status(dev_status, check, dev)
