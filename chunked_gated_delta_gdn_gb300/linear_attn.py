@@ -86,6 +86,8 @@ def _scratch(need, name, workspace, dev):
     """The workspace to pass on: the caller's when it is large enough, else a new one."""
     if need == (1 << 64) - 1:
         raise ValueError("sizes rejected by %s" % name)
+    if workspace is not None:
+        _need(workspace, "workspace", None, dev)
     if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
