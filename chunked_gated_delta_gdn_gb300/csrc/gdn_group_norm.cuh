@@ -245,7 +245,7 @@ inline SlabPlan slab_plan(int N, int L, int C, int G, int io_dtype) {
   const int cols = s.parts == 1 ? s.GPB * s.DV : kGnThreads;
   const int step = kGnThreads / cols;               // rows that a CTA takes at a time
   // one wave, each thread at least four rows
-  const long long want = std::max(1LL, 152LL * kSlabPerSm / ((long long)N * s.NCB));
+  const long long want = std::max(1LL, (long long)current_sm_count() * kSlabPerSm / ((long long)N * s.NCB));
   const long long most = (L + 4LL * step - 1) / (4LL * step);
   const long long chunks = want < most ? want : most;
   s.rows = (int)((L + chunks - 1) / chunks);
@@ -324,7 +324,7 @@ inline RowPlan row_plan(int N, int L, int C, int G, int io_dtype, int most, int 
   r.across = r.J >= G ? 1 : (G + r.J - 1) / r.J;
   r.down = r.J >= G ? r.J / G : 1;
   // one wave of `per_sm` CTAs an SM, and no more than the rows need
-  const long long need = ((long long)N + r.down - 1) / r.down, want = std::max(1, 152 * per_sm / r.across);
+  const long long need = ((long long)N + r.down - 1) / r.down, want = std::max(1, current_sm_count() * per_sm / r.across);
   r.sets = (int)std::min(need, want);
   return r;
 }

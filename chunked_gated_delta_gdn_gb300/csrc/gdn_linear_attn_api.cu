@@ -5,6 +5,7 @@
 
 #include "gdn.h"
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 #include "gdn_linear_attn.h"
 #include "gdn_status.h"
 
@@ -41,15 +42,6 @@ gdn::LinAttnPass base_pass(const float* log_decay, int B, int T, int Hv, gdn_dty
   return p;
 }
 
-int sm_count() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  return gdn::device_sm_count(dev);
-}
-
 // Scratch of a call: the segments' states, then (backward) per-value-head dq and dk in fp32 where
 // value heads share a query/key head.
 struct Scratch {
@@ -63,10 +55,11 @@ Scratch scratch(int num_passes, int B, int T, int num_seqs, bool packed, int Hqk
   // the tensor cores pad the state to 128 x 128; on the CUDA cores a chunk takes long enough to
   // stand alone
   const bool tc = io_dtype == GDN_BF16;
-  if (tc) s.plan = gdn::linear_attn_plan(chains, most, !packed, sm_count());
+  const int sms = gdn::current_sm_count();
+  if (tc) s.plan = gdn::linear_attn_plan(chains, most, !packed, sms);
   else
     s.plan.segs =
-        gdn::linear_attn_segments(chains, most, sm_count() * gdn::linear_attn_generic_per_sm(K, V), 1);
+        gdn::linear_attn_segments(chains, most, sms * gdn::linear_attn_generic_per_sm(K, V), 1);
   if (s.plan.segs > 1)
     s.local = align256((size_t)s.plan.segs * (chains - s.plan.whole) * (tc ? 16384 : K * V) * sizeof(float));
   if (num_passes > 1 && Hqk != Hv) s.part = align256((size_t)B * T * Hv * K * sizeof(float));
