@@ -103,6 +103,9 @@ def chunk_linear_attn(q, k, v, log_decay, scale=None, initial_state=None, output
     ``(o, final_state or None)``.  ``cu_seqlens`` ([N + 1] int32, B == 1), ``state_indices`` (a
     slot cache, -1 = padding, updated in place by default), ``out``, ``final_state``,
     ``workspace``, ``dev_status`` and ``check`` as in :func:`chunk_gated_delta_rule`.
+
+    A NaN or infinity in a token reaches its whole 64-token chunk, also the tokens before it there,
+    and what follows in its sequence and head; nothing else.
     """
     dev, dt, (B, T, Hqk, Hv, K, V), N = _inputs(q, k, v, log_decay, cu_seqlens)
     num_slots = 0

@@ -443,8 +443,9 @@ size_t gdn_chunk_bwd_gated_workspace_size(int B, int T, int Hqk, int Hv, int K, 
  *               0) is skipped and reported as GDN_DEV_BAD_CU_SEQLENS.
  *   workspace   gdn_linear_attn_chunk_fwd_workspace_size(...) bytes, 256-byte aligned; NULL when
  *               that is 0.
- * A NaN or infinity in a token's q, k or v reaches that token's 64-token chunk and what follows
- * it in its sequence, and no other sequence.
+ * A NaN or infinity in a token's q, k or v reaches that token's 64-token chunk (the tokens before
+ * it too: the chunk's mask multiplies by zero) and what follows it in its sequence and head, and
+ * nothing else; backwards in time, in the gradients, likewise.  An infinity may arrive as a NaN.
  */
 size_t gdn_linear_attn_chunk_fwd_workspace_size(int B, int T, int Hqk, int Hv, int K, int V,
                                                 int num_seqs, gdn_dtype_t io_dtype);
