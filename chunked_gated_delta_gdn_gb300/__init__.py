@@ -19,6 +19,11 @@ its thin PyTorch binding:
 * :func:`chunk_linear_attn`, :func:`chunk_linear_attn_bwd`, :func:`chunk_linear_attn_trainable`,
   :func:`linear_attn_decode` -- linear attention with a decay for each head: chunked forward,
   backward, autograd op and single-token decode on the same slot cache.
+* :func:`gated_linear_recurrence`, ``*_bwd``, ``*_trainable``, ``*_decode`` and each with
+  ``_fused_gates`` -- the gated linear recurrence of each channel: forward over dense or packed
+  sequences, backward, autograd op, single-token decode on a slot cache.
+* :func:`qk_norm_rotate`, :func:`qk_norm_rotate_bwd`, :func:`qk_norm_rotate_trainable` -- the norm of
+  each head's queries and keys with the rotation of their positions (one or several axes).
 * :func:`group_norm_act`, :func:`group_norm_act_bwd`, :func:`group_norm_act_trainable` -- group
   norm with an activation or gate, channels last: forward, backward, autograd op.
 
@@ -34,6 +39,11 @@ from .api import (GdnDeviceError, GdnError, chunk_fwd_path, chunk_gated_delta_pr
 from .group_norm import group_norm_act, group_norm_act_bwd, group_norm_act_trainable
 from .linear_attn import (chunk_linear_attn, chunk_linear_attn_bwd, chunk_linear_attn_trainable,
                           linear_attn_decode)
+from .qk_rotate import qk_norm_rotate, qk_norm_rotate_bwd, qk_norm_rotate_trainable
+from .recurrence import (gated_linear_recurrence, gated_linear_recurrence_bwd,
+                         gated_linear_recurrence_bwd_fused_gates, gated_linear_recurrence_decode,
+                         gated_linear_recurrence_decode_fused_gates, gated_linear_recurrence_fused_gates,
+                         gated_linear_recurrence_fused_gates_trainable, gated_linear_recurrence_trainable)
 
 __all__ = ["chunk_gated_delta_rule", "gated_delta_decode", "gated_delta_decode_multi",
            "chunk_gated_delta_rule_fused_gates", "gated_delta_decode_fused_gates",
@@ -42,5 +52,10 @@ __all__ = ["chunk_gated_delta_rule", "gated_delta_decode", "gated_delta_decode_m
            "chunk_gated_delta_rule_bwd_fused_gates", "chunk_gated_delta_rule_fused_gates_trainable",
            "chunk_linear_attn", "chunk_linear_attn_bwd", "chunk_linear_attn_trainable",
            "linear_attn_decode", "group_norm_act", "group_norm_act_bwd", "group_norm_act_trainable",
+           "gated_linear_recurrence", "gated_linear_recurrence_fused_gates",
+           "gated_linear_recurrence_bwd", "gated_linear_recurrence_bwd_fused_gates",
+           "gated_linear_recurrence_trainable", "gated_linear_recurrence_fused_gates_trainable",
+           "gated_linear_recurrence_decode", "gated_linear_recurrence_decode_fused_gates",
+           "qk_norm_rotate", "qk_norm_rotate_bwd", "qk_norm_rotate_trainable",
            "chunk_workspace_size", "chunk_fwd_path", "GdnError", "GdnDeviceError"]
 __version__ = "0.1.0"

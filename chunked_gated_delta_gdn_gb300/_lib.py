@@ -19,6 +19,7 @@ GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_LAYOUT = 0, 1, 2, 3,
 GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_WORKSPACE = 5, 6, 7
 GDN_F32, GDN_BF16 = 0, 1
 GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
+GDN_NORM_NONE, GDN_NORM_RMS, GDN_NORM_L2 = 0, 1, 2
 GDN_DEV_BAD_SLOT, GDN_DEV_BAD_CU_SEQLENS, GDN_DEV_TIMEOUT = 1, 2, 4
 
 EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_path", "gdn_decode",
@@ -31,6 +32,10 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_path"
            "gdn_linear_attn_decode",
            "gdn_group_norm_act_fwd", "gdn_group_norm_act_fwd_workspace_size",
            "gdn_group_norm_act_bwd", "gdn_group_norm_act_bwd_workspace_size",
+           "gdn_linear_recurrence_carries_size", "gdn_linear_recurrence_fwd",
+           "gdn_linear_recurrence_bwd_workspace_size", "gdn_linear_recurrence_bwd",
+           "gdn_linear_recurrence_decode",
+           "gdn_qk_norm_rotate_fwd", "gdn_qk_norm_rotate_bwd_workspace_size", "gdn_qk_norm_rotate_bwd",
            "gdn_status_string", "gdn_version")
 
 
@@ -122,6 +127,28 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                    lib.gdn_group_norm_act_bwd_workspace_size):
             fn.argtypes = [i, i, i, i, i]
             fn.restype = sz
+        ll = ctypes.c_longlong
+        lib.gdn_linear_recurrence_carries_size.argtypes = [i, i, i]
+        lib.gdn_linear_recurrence_carries_size.restype = sz
+        lib.gdn_linear_recurrence_bwd_workspace_size.argtypes = [i, i, i, i, i]
+        lib.gdn_linear_recurrence_bwd_workspace_size.restype = sz
+        lib.gdn_linear_recurrence_fwd.argtypes = [vp, vp, vp, vp, f, ll, ll, ll, i, i, i, i, i, vp, i, vp,
+                                                  vp, i, vp, i, vp, vp, vp, vp]
+        lib.gdn_linear_recurrence_fwd.restype = i
+        lib.gdn_linear_recurrence_bwd.argtypes = [vp, vp, vp, vp, f, ll, ll, ll, i, i, i, i, i, vp, vp, i,
+                                                  vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+        lib.gdn_linear_recurrence_bwd.restype = i
+        lib.gdn_linear_recurrence_decode.argtypes = [vp, vp, vp, vp, f, ll, ll, ll, i, i, i, i, vp, i, vp,
+                                                     vp, vp, vp]
+        lib.gdn_linear_recurrence_decode.restype = i
+        lib.gdn_qk_norm_rotate_fwd.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, vp, i, vp, vp,
+                                               i, vp, i, vp, vp, vp]
+        lib.gdn_qk_norm_rotate_fwd.restype = i
+        lib.gdn_qk_norm_rotate_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
+        lib.gdn_qk_norm_rotate_bwd_workspace_size.restype = sz
+        lib.gdn_qk_norm_rotate_bwd.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp, vp, i,
+                                               vp, vp, i, vp, i, vp, vp, vp, vp, vp, sz, vp]
+        lib.gdn_qk_norm_rotate_bwd.restype = i
         lib.gdn_status_string.argtypes = [i]
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_version.argtypes = []

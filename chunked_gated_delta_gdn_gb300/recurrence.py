@@ -1,0 +1,316 @@
+"""Gated linear recurrence: the PyTorch binding of the ``gdn_linear_recurrence_*`` entry points.
+
+    h_t = a_t h_{t-1} + b_t,    y_t = h_t      per channel, with an fp32 state h [N, D]
+
+gates given:  a_t = exp(g_t), b_t = x_t;
+fused gates:  a_t = exp(-c softplus(lam) sigmoid(r_t)), b_t = sqrt(1 - a_t^2) sigmoid(i_t) x_t.
+
+x, g, r, i may be slices of a wider projection along the last axis: their rows need not be next to
+each other.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from . import _lib
+from .api import DEVICE_ERRORS_DOC, _DT, _need, _ptr, _raise_on_status, _status
+from .linear_attn import _first_only, _fit, _int32, _scratch, _stream
+
+__all__ = ["gated_linear_recurrence", "gated_linear_recurrence_fused_gates",
+           "gated_linear_recurrence_bwd", "gated_linear_recurrence_bwd_fused_gates",
+           "gated_linear_recurrence_trainable", "gated_linear_recurrence_fused_gates_trainable",
+           "gated_linear_recurrence_decode", "gated_linear_recurrence_decode_fused_gates"]
+
+
+def _pitch(t, name, dtype, dev, shape):
+    """Elements from one token of t to the next, after the checks: t [..., D] of ``shape`` whose rows
+    are evenly spaced over all its leading axes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.device != dev:
+        if t.device.type != "cuda":
+            raise ValueError("%s must be a CUDA tensor (got %s)" % (name, t.device))
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    D = shape[-1]
+    if t.is_contiguous():
+        return D
+    pitch, tokens = None, 1
+    for size, stride in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if pitch is None:
+            pitch = stride
+        elif stride != pitch * tokens:
+            raise ValueError("%s must have evenly spaced rows" % name)
+        tokens *= size
+    if (D > 1 and t.stride(-1) != 1) or (pitch is not None and pitch < D):
+        raise ValueError("%s must have contiguous rows that do not overlap" % name)
+    return D if pitch is None else pitch
+
+
+def _inputs(x, g, i, lam, c, dims, g_name):
+    """Checks shared by the calls; returns (device, (x, g, i pitches), c)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    if x.device.type != "cuda":
+        raise ValueError("x must be a CUDA tensor (got %s)" % x.device)
+    if x.dim() != dims:
+        raise ValueError("x must be %s" % ("[B, T, D]" if dims == 3 else "[n, D]"))
+    dev, shape = x.device, x.shape
+    if shape[-1] < 1:
+        raise ValueError("x has no channels")
+    _int32("gated linear recurrence", *shape)
+    px = _pitch(x, "x", (torch.float32, torch.bfloat16), dev, shape)
+    pg = _pitch(g, g_name, (x.dtype, torch.float32), dev, shape)
+    if lam is None:
+        return dev, (px, pg, 0), 0.0
+    pi = _pitch(i, "i", g.dtype, dev, shape)
+    if not _fit(dev, (lam, torch.float32, shape[-1:])):
+        _need(lam, "lam", torch.float32, dev, shape[-1:])
+    c = float(c)
+    if not 0.0 <= c <= 3.0e38:
+        raise ValueError("c must be finite and not negative (got %r)" % c)
+    return dev, (px, pg, pi), c
+
+
+def _sequences(x, cu_seqlens):
+    """The number of sequences."""
+    if cu_seqlens is None:
+        return x.shape[0]
+    _need(cu_seqlens, "cu_seqlens", torch.int32, x.device)
+    if x.shape[0] != 1:
+        raise ValueError("cu_seqlens requires B == 1")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be [num_seqs + 1]")
+    _int32("gated linear recurrence", cu_seqlens.numel())
+    return cu_seqlens.numel() - 1
+
+
+def _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices, out,
+             final_state, return_carries, dev_status, check, g_name):
+    dev, pitches, c = _inputs(x, g, i, lam, c, 3, g_name)
+    B, T, D = x.shape
+    N = _sequences(x, cu_seqlens)
+    num_slots = 0
+    st_shape = (N, D)
+    if state_indices is not None:
+        _need(state_indices, "state_indices", torch.int32, dev, (N,))
+        cache = initial_state if initial_state is not None else final_state
+        if cache is None:
+            raise ValueError("state_indices needs initial_state or final_state (the slot cache)")
+        num_slots = cache.shape[0]
+        _int32("gated linear recurrence", num_slots)
+        st_shape = (num_slots, D)
+        if output_final_state and final_state is None:
+            final_state = initial_state
+    if not output_final_state:
+        final_state = None
+    if not _fit(dev, (initial_state, torch.float32, st_shape), (final_state, torch.float32, st_shape),
+                (out, x.dtype, x.shape)):
+        for t, name in ((initial_state, "initial_state"), (final_state, "final_state")):
+            if t is not None:
+                _need(t, name, torch.float32, dev, st_shape)
+        if out is not None:
+            _need(out, "out", x.dtype, dev, x.shape)
+    if output_final_state and final_state is None:
+        final_state = torch.empty(st_shape, dtype=torch.float32, device=dev)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    L = _lib.load()
+    carries = None
+    if return_carries:
+        need = L.gdn_linear_recurrence_carries_size(B, T, D)
+        if need == (1 << 64) - 1:
+            raise ValueError("sizes rejected by gdn_linear_recurrence_fwd")
+        carries = torch.empty((need // (4 * D), D), dtype=torch.float32, device=dev)
+    dev_status = _status(dev_status, check, dev)
+    st = L.gdn_linear_recurrence_fwd(_ptr(x), _ptr(g), _ptr(i), _ptr(lam), c, *pitches, B, T, D,
+                                     _DT[x.dtype], _DT[g.dtype], _ptr(initial_state),
+                                     int(bool(output_final_state)), _ptr(final_state), _ptr(cu_seqlens),
+                                     N, _ptr(state_indices), num_slots, _ptr(out), _ptr(carries),
+                                     _ptr(dev_status), _stream(dev))
+    _lib.check("gdn_linear_recurrence_fwd", st)
+    _raise_on_status("gdn_linear_recurrence_fwd", dev_status, check)
+    return out, final_state, carries
+
+
+def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, cu_seqlens=None, *,
+                            state_indices=None, out=None, final_state=None, return_carries=False,
+                            dev_status=None, check=False
+                            ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Forward through ``gdn_linear_recurrence_fwd`` with given log-decays g (at most 0).
+
+    x [B, T, D]; g [B, T, D] in fp32 or x's dtype.  Returns ``(y, final_state or None)``, and with
+    ``return_carries`` also what :func:`gated_linear_recurrence_bwd` starts from.  Also with a slot
+    cache ``state_indices`` [N] (-1 = padding) on states [num_slots, D], ``cu_seqlens``, ``out``,
+    ``final_state``, ``dev_status`` and ``check`` as in :func:`chunk_gated_delta_rule`; a bad
+    ``cu_seqlens`` leaves zero rows and every state as it was.
+    """
+    y, fin, carries = _forward(x, g, None, None, 0.0, initial_state, output_final_state, cu_seqlens,
+                               state_indices, out, final_state, return_carries, dev_status, check, "g")
+    return (y, fin, carries) if return_carries else (y, fin)
+
+
+def gated_linear_recurrence_fused_gates(x, r, i, lam, c=8.0, initial_state=None, output_final_state=False,
+                                        cu_seqlens=None, *, state_indices=None, out=None, final_state=None,
+                                        return_carries=False, dev_status=None, check=False
+                                        ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """:func:`gated_linear_recurrence` with its gates computed in the kernel: r, i [B, T, D] in fp32 or
+    x's dtype, lam [D] fp32, c a constant of the layer."""
+    _need(lam, "lam")
+    y, fin, carries = _forward(x, r, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices,
+                               out, final_state, return_carries, dev_status, check, "r")
+    return (y, fin, carries) if return_carries else (y, fin)
+
+
+def _backward(x, g, i, lam, c, d_y, d_final_state, initial_state, cu_seqlens, need_lam,
+              need_d_initial_state, carries, workspace, dev_status, check, g_name):
+    dev, pitches, c = _inputs(x, g, i, lam, c, 3, g_name)
+    B, T, D = x.shape
+    N = _sequences(x, cu_seqlens)
+    fused = lam is not None
+    if d_y is None or not _fit(dev, (d_y, x.dtype, x.shape), (initial_state, torch.float32, (N, D)),
+                               (d_final_state, torch.float32, (N, D)),
+                               (carries, torch.float32, (-(-B * T // 128), D))):
+        _need(d_y, "d_y", x.dtype, dev, x.shape)
+        for t, name in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
+            if t is not None:
+                _need(t, name, torch.float32, dev, (N, D))
+        if carries is not None:
+            _need(carries, "carries", torch.float32, dev, (-(-B * T // 128), D))
+    L = _lib.load()
+    need = L.gdn_linear_recurrence_bwd_workspace_size(B, T, D, N, int(fused))
+    workspace, ws_bytes = _scratch(need, "gdn_linear_recurrence_bwd", workspace, dev)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dg = torch.empty(x.shape, dtype=g.dtype, device=dev)
+    di = torch.empty(x.shape, dtype=g.dtype, device=dev) if fused else None
+    dlam = torch.empty(D, dtype=torch.float32, device=dev) if fused and need_lam else None
+    dh0 = torch.empty((N, D), dtype=torch.float32, device=dev) if need_d_initial_state else None
+    dev_status = _status(dev_status, check, dev)
+    st = L.gdn_linear_recurrence_bwd(_ptr(x), _ptr(g), _ptr(i), _ptr(lam), c, *pitches, B, T, D,
+                                     _DT[x.dtype], _DT[g.dtype], _ptr(initial_state), _ptr(cu_seqlens), N,
+                                     _ptr(d_y), _ptr(d_final_state), _ptr(carries), _ptr(dx), _ptr(dg),
+                                     _ptr(di), _ptr(dlam), _ptr(dh0), _ptr(workspace), ws_bytes,
+                                     _ptr(dev_status), _stream(dev))
+    _lib.check("gdn_linear_recurrence_bwd", st)
+    _raise_on_status("gdn_linear_recurrence_bwd", dev_status, check)
+    return dx, dg, di, dlam, dh0
+
+
+def gated_linear_recurrence_bwd(x, g, d_y, d_final_state=None, initial_state=None, cu_seqlens=None, *,
+                                need_d_initial_state=True, carries=None, workspace=None, dev_status=None,
+                                check=False):
+    """Gradients of :func:`gated_linear_recurrence` (no slot cache) through
+    ``gdn_linear_recurrence_bwd``: ``(dx, dg, d_initial_state)``, each in its input's dtype, the last
+    fp32 [N, D] (None when ``need_d_initial_state`` is False).  Without ``carries`` of the same inputs'
+    forward they are made again."""
+    dx, dg, _, _, dh0 = _backward(x, g, None, None, 0.0, d_y, d_final_state, initial_state, cu_seqlens, False,
+                                  need_d_initial_state, carries, workspace, dev_status, check, "g")
+    return dx, dg, dh0
+
+
+def gated_linear_recurrence_bwd_fused_gates(x, r, i, lam, d_y, d_final_state=None, c=8.0, initial_state=None,
+                                            cu_seqlens=None, *, need_d_initial_state=True, carries=None,
+                                            workspace=None, dev_status=None, check=False):
+    """Gradients of :func:`gated_linear_recurrence_fused_gates`: ``(dx, dr, di, dlam,
+    d_initial_state)``, dlam fp32 [D]."""
+    _need(lam, "lam")
+    return _backward(x, r, i, lam, c, d_y, d_final_state, initial_state, cu_seqlens, True,
+                     need_d_initial_state, carries, workspace, dev_status, check, "r")
+
+
+class _Recurrence(torch.autograd.Function):
+    """gdn_linear_recurrence_fwd forward, gdn_linear_recurrence_bwd backward."""
+
+    @staticmethod
+    def forward(ctx, x, g, i, lam, initial_state, c, output_final_state, cu_seqlens):
+        y, fin, carries = _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, None, None,
+                                   None, any(ctx.needs_input_grad), None, False, "g" if lam is None else "r")
+        ctx.save_for_backward(x, g, i, lam, initial_state, cu_seqlens, carries)
+        ctx.c = c
+        ctx.set_materialize_grads(False)
+        return y, fin
+
+    @staticmethod
+    def backward(ctx, d_y, d_fin):
+        x, g, i, lam, init, cu, carries = ctx.saved_tensors
+        d_y = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if d_y is None else d_y.contiguous()
+        if d_fin is not None:
+            d_fin = d_fin.contiguous()
+        grads = _backward(x, g, i, lam, ctx.c, d_y, d_fin, init, cu, ctx.needs_input_grad[3],
+                          init is not None and ctx.needs_input_grad[4], carries, None, None, False,
+                          "g" if lam is None else "r")
+        if torch.is_grad_enabled():
+            grads = _first_only("gated_linear_recurrence_trainable", grads, (x, g, i, lam, init, d_y, d_fin))
+        dx, dg, di, dlam, dh0 = grads
+        return dx, dg, di, dlam, dh0, None, None, None
+
+
+def gated_linear_recurrence_trainable(x, g, initial_state=None, output_final_state=False, cu_seqlens=None):
+    """:func:`gated_linear_recurrence` as a differentiable op (torch autograd) in x, g and
+    ``initial_state``; a second derivative is refused.  Returns ``(y, final_state or None)``."""
+    return _Recurrence.apply(x, g, None, None, initial_state, 0.0, bool(output_final_state), cu_seqlens)
+
+
+def gated_linear_recurrence_fused_gates_trainable(x, r, i, lam, c=8.0, initial_state=None,
+                                                  output_final_state=False, cu_seqlens=None):
+    """:func:`gated_linear_recurrence_fused_gates` as a differentiable op in x, r, i, lam and
+    ``initial_state``; a second derivative is refused.  Returns ``(y, final_state or None)``."""
+    _need(lam, "lam")
+    return _Recurrence.apply(x, r, i, lam, initial_state, float(c), bool(output_final_state), cu_seqlens)
+
+
+def _decode(x, g, i, lam, c, state, batch_indices, out, dev_status, check, g_name):
+    dev, pitches, c = _inputs(x, g, i, lam, c, 2, g_name)
+    n, D = x.shape
+    if not (isinstance(state, torch.Tensor) and state.dim() == 2
+            and _fit(dev, (state, torch.float32, (state.shape[0], D)), (batch_indices, torch.int32, (n,)),
+                     (out, x.dtype, x.shape))):
+        _need(state, "state", torch.float32, dev)
+        if state.dim() != 2 or state.shape[1] != D:
+            raise ValueError("state must be [num_slots, D]")
+        if batch_indices is not None:
+            _need(batch_indices, "batch_indices", torch.int32, dev, (n,))
+        if out is not None:
+            _need(out, "out", x.dtype, dev, x.shape)
+    _int32("gated linear recurrence", state.shape[0])
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    dev_status = _status(dev_status, check, dev)
+    st = _lib.load().gdn_linear_recurrence_decode(_ptr(x), _ptr(g), _ptr(i), _ptr(lam), c, *pitches, n, D,
+                                                  _DT[x.dtype], _DT[g.dtype], _ptr(state), state.shape[0],
+                                                  _ptr(batch_indices), _ptr(out), _ptr(dev_status),
+                                                  _stream(dev))
+    _lib.check("gdn_linear_recurrence_decode", st)
+    _raise_on_status("gdn_linear_recurrence_decode", dev_status, check)
+    return out
+
+
+def gated_linear_recurrence_decode(x, g, state, batch_indices=None, *, out=None, dev_status=None,
+                                   check=False) -> torch.Tensor:
+    """One token per request through ``gdn_linear_recurrence_decode``; ``state`` [num_slots, D] fp32 is
+    updated in place.
+
+    x [n, D]; g [n, D] in fp32 or x's dtype; batch_indices [n] int32 (-1 = padding: a zero row) or
+    None (request i uses slot i).  Returns y [n, D].
+    """
+    return _decode(x, g, None, None, 0.0, state, batch_indices, out, dev_status, check, "g")
+
+
+def gated_linear_recurrence_decode_fused_gates(x, r, i, lam, state, batch_indices=None, c=8.0, *, out=None,
+                                               dev_status=None, check=False) -> torch.Tensor:
+    """:func:`gated_linear_recurrence_decode` with its gates computed in the kernel: r, i [n, D], lam [D]."""
+    _need(lam, "lam")
+    return _decode(x, r, i, lam, c, state, batch_indices, out, dev_status, check, "r")
+
+
+for _f in (gated_linear_recurrence, gated_linear_recurrence_fused_gates, gated_linear_recurrence_bwd,
+           gated_linear_recurrence_bwd_fused_gates, gated_linear_recurrence_decode,
+           gated_linear_recurrence_decode_fused_gates):
+    _f.__doc__ += DEVICE_ERRORS_DOC

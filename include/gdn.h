@@ -1,6 +1,7 @@
 /*
  * gdn.h -- C ABI of libgdn, the GB300 (sm_103a) gated delta rule library, with linear
- * attention with a decay for each head and group norm with an activation beside it.
+ * attention with a decay for each head, the gated linear recurrence, the norm of queries and keys
+ * with the rotation of their positions, and group norm with an activation beside it.
  *
  * The gated delta rule, per (sequence, value head h) with a K x V fp32 state S:
  *
@@ -533,6 +534,143 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
                                     gdn_dtype_t io_dtype, gdn_dtype_t wb_dtype, gdn_act_t act,
                                     void* dx, void* dgate, float* dweight, float* dbias,
                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gated linear recurrence, per channel d of D with an fp32 state h:
+ *
+ *     h_t = a_t h_{t-1} + b_t,    y_t = h_t
+ *
+ *   gates given (lam NULL, i NULL):   a_t = exp(g_t),  b_t = x_t
+ *   fused gates (lam given):          a_t = exp(-c softplus(lam) sigmoid(g_t)),
+ *                                     b_t = sqrt(1 - a_t^2) sigmoid(i_t) x_t
+ *
+ * gdn_linear_recurrence_fwd -- forward (prompts, training).
+ *   x           [B, T, D] io_dtype, device: token t of the flat axis [B * T] starts x_pitch
+ *               elements behind the one before it (x_pitch >= D), so x may be a part of a wider
+ *               projection.
+ *   g, i        [B, T, D] g_dtype (GDN_F32 or io_dtype), likewise with g_pitch, i_pitch.  Given g
+ *               are log-decays: at most 0, -inf keeps nothing (larger ones are taken as they are;
+ *               the product of any 4096 successive a_t has to stay finite).
+ *   lam         [D] fp32, device, and c >= 0: the fused gates' form.
+ *   B, T, D     with cu_seqlens B is 1 and T the packed token count.  Any D >= 1; element
+ *               alignment serves, and rows of whole 4-byte (fp32: 8-byte) pairs that start on their size
+ *               are read faster.
+ *   initial_state, output_final_state, final_state, cu_seqlens, num_seqs, state_indices,
+ *   num_slots, stream  as gdn_chunk_fwd, states [N, D] or slots [num_slots, D] fp32: slot -1 is
+ *               padding (zero rows, no state access), sequences may be empty, final_state may be
+ *               initial_state.
+ *   y           [B, T, D] io_dtype, contiguous, written completely: tokens past the last sequence
+ *               get zeros.  NULL where only carries are wanted.
+ *   carries     gdn_linear_recurrence_carries_size(...) bytes, or NULL: the state in front of
+ *               every 128th token, which the backward starts from.
+ * A cu_seqlens that is not monotone from 0 to at most T is reported as GDN_DEV_BAD_CU_SEQLENS: y
+ * is zero then and no state is read or written.  A NaN or infinity reaches what follows in its
+ * sequence and channel and nothing else; an infinity may arrive as a NaN.
+ */
+size_t gdn_linear_recurrence_carries_size(int B, int T, int D);
+
+gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void* i, const float* lam,
+                                       float c, long long x_pitch, long long g_pitch,
+                                       long long i_pitch, int B, int T, int D, gdn_dtype_t io_dtype,
+                                       gdn_dtype_t g_dtype, const float* initial_state,
+                                       int output_final_state, float* final_state,
+                                       const int32_t* cu_seqlens, int num_seqs,
+                                       const int32_t* state_indices, int num_slots, void* y,
+                                       float* carries, int* dev_status, void* stream);
+
+/*
+ * gdn_linear_recurrence_bwd -- gradients of gdn_linear_recurrence_fwd (no slot cache).
+ *   d_y         [B, T, D] io_dtype, contiguous.    d_final_state  [N, D] fp32 or NULL (zero).
+ *   carries     what the forward of the same inputs wrote, or NULL: made again in the workspace.
+ *   dx          [B, T, D] io_dtype; dg, di  [B, T, D] g_dtype (of g, which is r with fused gates,
+ *               and i): contiguous, written completely, zero past the last sequence.
+ *   dlam        [D] fp32 or NULL.    d_initial_state  [N, D] fp32 or NULL.
+ *   workspace   gdn_linear_recurrence_bwd_workspace_size(...) bytes, 256-byte aligned.
+ * No atomics: bitwise identical from run to run.  Where a channel does not decay at all (a = 1,
+ * the square root's slope is infinite) the root's part of its gradients counts as zero, their
+ * limit.  A bad cu_seqlens is reported and every gradient is zero.
+ */
+size_t gdn_linear_recurrence_bwd_workspace_size(int B, int T, int D, int num_seqs, int fused_gates);
+
+gdn_status_t gdn_linear_recurrence_bwd(const void* x, const void* g, const void* i, const float* lam,
+                                       float c, long long x_pitch, long long g_pitch,
+                                       long long i_pitch, int B, int T, int D, gdn_dtype_t io_dtype,
+                                       gdn_dtype_t g_dtype, const float* initial_state,
+                                       const int32_t* cu_seqlens, int num_seqs, const void* d_y,
+                                       const float* d_final_state, const float* carries, void* dx,
+                                       void* dg, void* di, float* dlam, float* d_initial_state,
+                                       void* workspace, size_t workspace_bytes, int* dev_status,
+                                       void* stream);
+
+/*
+ * gdn_linear_recurrence_decode -- one token per request on a slot cache [num_slots, D] fp32, in
+ * place.  Slots, padding (-1: a zero row, the state untouched) and errors as gdn_decode; x, g, i
+ * [n, D] with their pitches, y [n, D] contiguous.
+ */
+gdn_status_t gdn_linear_recurrence_decode(const void* x, const void* g, const void* i,
+                                          const float* lam, float c, long long x_pitch,
+                                          long long g_pitch, long long i_pitch, int n, int D,
+                                          gdn_dtype_t io_dtype, gdn_dtype_t g_dtype, float* state,
+                                          int num_slots, const int32_t* batch_indices, void* y,
+                                          int* dev_status, void* stream);
+
+/*
+ * Norm of queries and keys for each head with the rotation of their positions, in one pass.  For
+ * every head x (K values) of q and k:
+ *
+ *     n = x r w,  r = 1 / sqrt(mean(x^2) + eps)  (GDN_NORM_RMS)
+ *                     1 / sqrt(sum(x^2) + eps)   (GDN_NORM_L2)
+ *                     1                          (GDN_NORM_NONE)
+ *
+ * and the first R values of n turn in pairs: pair j = 0 .. R/2 - 1, values (j, j + R/2) or with
+ * `interleaved` (2 j, 2 j + 1), by the angle phi = position * inv_freq[j]:
+ *
+ *     (u, v) -> (u cos phi - v sin phi, v cos phi + u sin phi)
+ *
+ *   q, k        [B, T, Hq, K], [B, T, Hk, K] io_dtype, device, values of a head next to each other;
+ *               q_strides, k_strides (host, three each) are the elements from one batch row, token
+ *               and head to the next.  Element alignment serves; wider alignment is read faster.
+ *   K, R        K 1..256; R even, 0 (no rotation) .. K.
+ *   q_weight, k_weight  [K] w_dtype (GDN_F32 or io_dtype), each may be NULL (1).
+ *   inv_freq    [R / 2] fp32, device, finite; NULL when R is 0.  The angles are exact to fp32
+ *               rounding for every int32 position.
+ *   positions   [num_axes, B, T] int32, device, or NULL: token t of each row has position t on
+ *               every axis.
+ *   num_axes, sections  1..4; sections (host, num_axes integers, each >= 0, together R / 2): the
+ *               first sections[0] pairs turn by axis 0, the next ones by axis 1 ...; NULL with one axis.
+ *   q_out, k_out  [B, T, Hq, K], [B, T, Hk, K] io_dtype, contiguous; each may be its input where
+ *               that is contiguous.
+ */
+typedef enum { GDN_NORM_NONE = 0, GDN_NORM_RMS = 1, GDN_NORM_L2 = 2 } gdn_norm_t;
+
+#define GDN_MAX_ROTATE_DIM 256
+#define GDN_MAX_AXES 4
+
+gdn_status_t gdn_qk_norm_rotate_fwd(const void* q, const void* k, const long long* q_strides,
+                                    const long long* k_strides, int B, int T, int Hq, int Hk, int K,
+                                    int R, gdn_dtype_t io_dtype, gdn_norm_t norm, float eps,
+                                    const void* q_weight, const void* k_weight, gdn_dtype_t w_dtype,
+                                    const float* inv_freq, const int32_t* positions, int num_axes,
+                                    const int* sections, int interleaved, void* q_out, void* k_out,
+                                    void* stream);
+
+/*
+ * Its backward, from the gradients d_q, d_k of q_out, k_out (contiguous) and the forward's inputs:
+ * dq, dk in io_dtype, contiguous; dq_weight, dk_weight [K] fp32, each may be NULL.  dq may be d_q
+ * and dk may be d_k.  No atomics: bitwise identical from run to run.
+ *   workspace   gdn_qk_norm_rotate_bwd_workspace_size(...) bytes, 256-byte aligned; NULL when 0.
+ */
+size_t gdn_qk_norm_rotate_bwd_workspace_size(int B, int T, int Hq, int Hk, int K, int need_weights);
+
+gdn_status_t gdn_qk_norm_rotate_bwd(const void* d_q, const void* d_k, const void* q, const void* k,
+                                    const long long* q_strides, const long long* k_strides, int B,
+                                    int T, int Hq, int Hk, int K, int R, gdn_dtype_t io_dtype,
+                                    gdn_norm_t norm, float eps, const void* q_weight,
+                                    const void* k_weight, gdn_dtype_t w_dtype, const float* inv_freq,
+                                    const int32_t* positions, int num_axes, const int* sections,
+                                    int interleaved, void* dq, void* dk, float* dq_weight,
+                                    float* dk_weight, void* workspace, size_t workspace_bytes,
+                                    void* stream);
 
 /*
  * gdn_selftest_wait_timeout -- the bounded wait of the fused kernels, run on its own.
