@@ -19,7 +19,7 @@ gdn_status_t check(const void* x, const void* g, const void* i, const float* lam
                    long long g_pitch, long long i_pitch, long long tokens, int D, int io_dtype, int g_dtype) {
   if (!is_dtype(io_dtype) || !is_dtype(g_dtype) || (g_dtype != GDN_F32 && g_dtype != io_dtype))
     return GDN_ERR_DTYPE;
-  if (D <= 0 || tokens < 0 || tokens > 0x7fffff00LL) return GDN_ERR_SHAPE;
+  if (D <= 0 || tokens < 0 || tokens > 0x7fff0000LL) return GDN_ERR_SHAPE;
   if (tokens > 0 && (x_pitch < D || g_pitch < D || (lam && i_pitch < D))) return GDN_ERR_SHAPE;
   if (lam && !(c >= 0.f && c <= 3.0e38f)) return GDN_ERR_SHAPE;
   if (tokens > 0 && (!x || !g || (lam && !i))) return GDN_ERR_NULL;
@@ -44,7 +44,7 @@ gdn_status_t check_batch(int B, int T, const int32_t* cu_seqlens, int num_seqs, 
 extern "C" {
 
 size_t gdn_linear_recurrence_carries_size(int B, int T, int D) {
-  if (B < 0 || T < 0 || D <= 0 || (long long)B * T > 0x7fffff00LL) return (size_t)-1;
+  if (B < 0 || T < 0 || D <= 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
   return gdn::recurrence_carries_bytes((long long)B * T, D);
 }
 
@@ -86,7 +86,7 @@ gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void*
 }
 
 size_t gdn_linear_recurrence_bwd_workspace_size(int B, int T, int D, int num_seqs, int fused_gates) {
-  if (B < 0 || T < 0 || D <= 0 || num_seqs < 0 || (long long)B * T > 0x7fffff00LL) return (size_t)-1;
+  if (B < 0 || T < 0 || D <= 0 || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
   return gdn::recurrence_bwd_workspace_bytes(B, T, D, num_seqs, fused_gates != 0);
 }
 

@@ -48,15 +48,15 @@ __global__ void recurrence_bwd_kernel(RecurrenceArgs a, float* states, float* pa
     if (part) part[at] = 0.f;
     return;
   }
-  const float rate = a.lam ? -a.c * softplus_f(a.lam[d]) : 0.f;
+  const float rate = a.lam ? gate_rate(a.c, a.lam[d], false) : 0.f;
   float h = a.initial_state ? a.initial_state[at] : 0.f;
   for (int t = bos; t < eos; ++t) {
     states[(size_t)t * a.D + d] = h;
     float la = load_elem(a.g, (size_t)t * a.g_pitch + d, a.g_dtype);
     float b = load_elem(a.x, (size_t)t * a.x_pitch + d, a.io_dtype);
     if (a.lam) {
-      const FusedGate f = fused_gate(la, load_elem(a.i, (size_t)t * a.i_pitch + d, a.g_dtype), rate);
-      la = f.la;
+      const FusedGate<false> f(la, load_elem(a.i, (size_t)t * a.i_pitch + d, a.g_dtype), rate);
+      la = f.l;
       b *= f.s * f.si;
     }
     h = decayed(la, h, b);
@@ -73,14 +73,14 @@ __global__ void recurrence_bwd_kernel(RecurrenceArgs a, float* states, float* pa
       store_elem(a.dx, o, delta, a.io_dtype);
       store_elem(a.dg, o, e * states[o], a.g_dtype);
     } else {
-      const FusedGate f = fused_gate(g, load_elem(a.i, (size_t)t * a.i_pitch + d, a.g_dtype), rate);
-      e = decayed(f.la, delta, 0.f);
+      const FusedGate<false> f(g, load_elem(a.i, (size_t)t * a.i_pitch + d, a.g_dtype), rate);
+      e = decayed(f.l, delta, 0.f);
       const float u = f.si * x;
       // where nothing decays, s = 0 and what multiplies 1 / s below goes to 0 faster
-      const float dla = e * (states[o] - (f.s > 0.f ? u * expf(f.la) / f.s : 0.f));
+      const float dla = e * (states[o] - (f.s > 0.f ? u * expf(f.l) / f.s : 0.f));
       sum += dla * f.sr;
       store_elem(a.dx, o, delta * f.s * f.si, a.io_dtype);
-      store_elem(a.dg, o, dla * f.la * (1.f - f.sr), a.g_dtype);
+      store_elem(a.dg, o, dla * f.l * (1.f - f.sr), a.g_dtype);
       store_elem(a.di, o, delta * f.s * u * (1.f - f.si), a.g_dtype);
     }
   }
