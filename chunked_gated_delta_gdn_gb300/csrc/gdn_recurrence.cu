@@ -283,31 +283,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   copies_wait<0>();
 }
 
-RecurrencePlan plan_of(const RecurrenceArgs& a, int width) {
-  const long long tokens = (long long)a.B * a.T;
-  const int sms = std::max(1, current_sm_count());
-  const long long want = 2LL * sms;
-  RecurrencePlan p;
-  p.blocks = (a.D + width - 1) / width;
-  const long long tiles = std::max(1LL, (tokens + kTile - 1) / kTile);
-  if (!a.cu_seqlens) {
-    p.parts = (int)std::min<long long>(std::max(1, a.num_seqs), std::max(1LL, (2 * want + p.blocks - 1) / p.blocks));
-    p.parts = (int)std::min<long long>(p.parts, tiles);
-    p.S = 1;
-    while (p.S < kMaxCluster && (long long)p.blocks * p.parts * p.S < want && 2LL * p.S * p.parts <= tiles) p.S *= 2;
-  } else {
-    p.S = 1;
-    while (p.S < kMaxCluster && 2 * p.S <= tiles) p.S *= 2;
-    p.parts = (int)std::min<long long>(std::max(1, a.num_seqs),
-                                       std::max(1LL, (want + (long long)p.blocks * p.S - 1) / ((long long)p.blocks * p.S)));
-    p.parts = (int)std::min<long long>(p.parts, std::max(1LL, tiles / p.S));
-  }
-  return p;
-}
-
 template <typename T, typename G, bool kFused, int kCh>
 cudaError_t launch_fwd(const RecurrenceArgs& a) {
-  const RecurrencePlan p = plan_of(a, 32 * kCh);
+  const RecurrencePlan p = recurrence_plan((long long)a.B * a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, 32 * kCh,
+                                           kTile, kMaxCluster, 2);
   auto* const kernel = recurrence_fwd_kernel<T, G, kFused, kCh>;
   const size_t shared = sizeof(FwdShared<T, G, kFused, kCh>);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);

@@ -9,7 +9,7 @@
 // does not add up over a long memory.
 #pragma once
 
-#include <type_traits>
+#include <algorithm>
 
 #include "gdn_common.cuh"
 #include "gdn_launch.cuh"
@@ -301,6 +301,28 @@ __device__ __forceinline__ void store_peer(unsigned at, int x) {
 struct RecurrencePlan {
   int blocks, parts, S;
 };
+
+// For kernels of `width` channels and `tile` tokens a CTA, `per_sm` CTAs an SM.
+inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile, int max_S,
+                                      int per_sm) {
+  const long long want = (long long)std::max(1, current_sm_count()) * per_sm;
+  RecurrencePlan p;
+  p.blocks = (D + width - 1) / width;
+  N = std::max(1, N);
+  const long long tiles = std::max(1LL, (tokens + tile - 1) / tile);
+  auto parts_for = [&](long long ctas) {   // of all blocks together
+    return (int)std::min<long long>({(long long)N, tiles, std::max(1LL, (ctas + p.blocks - 1) / p.blocks)});
+  };
+  p.S = 1;
+  if (!packed) {
+    p.parts = parts_for(2 * want);
+    while (p.S < max_S && (long long)p.blocks * p.parts * p.S < want && 2LL * p.S * p.parts <= tiles) p.S *= 2;
+  } else {
+    while (p.S < max_S && 2 * p.S <= tiles) p.S *= 2;
+    p.parts = std::min<long long>(parts_for((want + p.S - 1) / p.S), std::max(1LL, tiles / p.S));
+  }
+  return p;
+}
 
 inline int copy_unit(const void* p, long long pitch, int D, int elem) {
   const unsigned long long all = reinterpret_cast<uintptr_t>(p) | (unsigned long long)pitch * elem |
