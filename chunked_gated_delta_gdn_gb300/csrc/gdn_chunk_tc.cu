@@ -788,6 +788,8 @@ bool encode_map(CUtensorMap* m, const void* base, int H, int T_total, int D = 12
 
 }  // namespace
 
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return get_encode_fn(); }
+
 bool encode_rows_map_bf16(CUtensorMap* m, const void* base, int H, int T_total, int D) {
   return encode_map(m, base, H, T_total, D);
 }

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -166,6 +167,7 @@ bool chunk_tc_supported(int K, int V, int io_dtype, int beta_dtype);
 // TMA map of a [T_total, H, D] bf16 tensor with 64 x 1 x 64 boxes (64 features of one head
 // for 64 tokens, 128-byte swizzled), zero fill past the last token and past column D (D a
 // multiple of 8).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();   // NULL where the driver has none
 bool encode_rows_map_bf16(CUtensorMap* m, const void* base, int H, int T_total, int D = 128);
 cudaError_t launch_chunk_tc(const ChunkArgs& a);
 // The planned forward (a.workspace): sequences sorted longest first, and, when the batch has

@@ -5,9 +5,8 @@
 //
 // Forward: one reading of the inputs.  A cluster of S CTAs walks a part's tokens S tiles at a time, a
 // CTA a tile of kWarps windows.  Each warp turns its window's inputs, which were copied ahead into
-// shared memory, into a and b in registers and into the window's (A, L, H); windows and tiles are joined
-// through shared memory of the CTA and of the cluster; with the state that enters its window each warp
-// then walks its tokens.
+// shared memory, into a and b in registers and into the window's (L, H), is handed the state in front of
+// its window and walks its tokens.
 #include <algorithm>
 
 #include "gdn_recurrence.cuh"
@@ -15,61 +14,47 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kTau = 16;
+constexpr int kWarps = 16;
 constexpr int kTile = kWarps * kTau;
 constexpr int kStages = 2;
-constexpr int kMaxCluster = 8;
 
-// One window's or tile's effect on a state, for a lane's channels.
-template <int kCh>
-struct Step {
-  float A[kCh], L[kCh], H[kCh];
-};
-
-template <typename T, typename G, bool kFused, int kCh>
+template <typename T, typename G, bool kFused, int N>
 struct FwdShared {
-  static constexpr int kTensors = kFused ? 3 : 2;
-  static constexpr int kRowX = 32 * kCh * sizeof(T), kRowG = 32 * kCh * sizeof(G);
-  static constexpr int kWindow = kTau * (kRowX + (kTensors - 1) * kRowG);
+  static constexpr int W = 32 * N;
+  static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
+  static constexpr int kAtG = kTau * kRowX, kAtI = kAtG + kTau * kRowG;
+  static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
-  // the windows' steps: of every other round in `odd` where a CTA is alone; in a cluster its barrier
-  // stands between a round's reads and the next one's writes, and the tiles' steps are there
-  Step<kCh> even[kWarps][32];
-  union {
-    Step<kCh> odd[kWarps][32];
-    struct {
-      float L[2][kMaxCluster][kCh][32], H[2][kMaxCluster][kCh][32];
-    } tile;
-  };
-  int warp_reset[2][kWarps];
-  int tile_reset[2][kMaxCluster];
+  Chain<kWarps, N> chain;
+  uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-template <typename T, typename G, bool kFused, int kCh>
-__global__ void __launch_bounds__(kThreads, 2)
-    recurrence_fwd_kernel(RecurrenceArgs a, int parts, int x_unit, int g_unit, int i_unit, bool whole) {
-  using Shared = FwdShared<T, G, kFused, kCh>;
-  constexpr bool kFast = sizeof(T) == 2;
-  extern __shared__ char shared_bytes[];
+// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  kCluster: S may be above 1.
+template <typename T, typename G, bool kFused, int N, bool kEngine, bool kCluster>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    recurrence_fwd_kernel(RecurrenceArgs a, int parts, int S, int x_unit, int g_unit, int i_unit,
+                          const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap g_map,
+                          const __grid_constant__ CUtensorMap i_map) {
+  using Shared = FwdShared<T, G, kFused, N>;
+  using Values = Lanes<N>;
+  constexpr int W = Shared::W;
+  extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int S = cluster_size(), rank = cluster_rank();
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+  const bool clustered = kCluster && S > 1;
+  const int rank = clustered ? cluster_rank() : 0;
   const int part_index = blockIdx.x / S % parts, block = blockIdx.x / S / parts;
-  const int ch = block * 32 * kCh + lane * kCh;   // this lane's first channel
-  const int mine = max(0, min(kCh, a.D - ch));
-  const int left = a.D - block * 32 * kCh;
+  const int ch = block * W + lane * N;   // this lane's first channel
+  const int mine = max(0, min(N, a.D - ch));
   WindowFinder finder;
   finder.seq = Sequences{a.cu_seqlens, a.num_seqs, a.T, a.cu_seqlens ? a.T : a.B * a.T};
   finder.slots = a.state_indices;
   finder.num_slots = a.num_slots;
-  if (a.cu_seqlens && !packed_lengths_fit(a.cu_seqlens, a.num_seqs, a.T)) {
-    // no sequence: every row is zero
+  if (a.cu_seqlens && !packed_lengths_fit(a.cu_seqlens, a.num_seqs, a.T)) {   // every row is zero
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.dev_status, GDN_DEV_BAD_CU_SEQLENS);
-    finder.seq.N = 0;
-    finder.part = Part{0, 0, (int)((long long)a.T * part_index / parts), (int)((long long)a.T * (part_index + 1) / parts)};
-    for (int t = finder.part.t0 + rank * kWarps + warp; t < finder.part.t1 && a.y; t += S * kWarps)
-      for (int c = 0; c < mine; ++c) static_cast<T*>(a.y)[(size_t)t * a.D + ch + c] = (T)0.f;
+    for (long long t = (part_index * S + rank) * kWarps + warp; t < a.T && a.y; t += parts * S * kWarps)
+      write_row<false>(static_cast<T*>(a.y) + (size_t)t * a.D + ch, fill<N>(0.f), mine);
     return;
   }
   finder.part = part_of(finder.seq, part_index, parts);
@@ -85,230 +70,152 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (finder.seq.end(n) > finder.seq.begin(n) || !a.final_state) continue;
-    for (int c = 0; c < mine; ++c) {
-      const size_t at = (size_t)row * a.D + ch + c;
-      a.final_state[at] = a.initial_state ? a.initial_state[at] : 0.f;
-    }
+    const size_t at = (size_t)row * a.D + ch;
+    write_state(a.final_state + at, read_state<N>(a.initial_state ? a.initial_state + at : nullptr, mine), mine);
   }
-  float rate[kCh];
-#pragma unroll
-  for (int c = 0; c < kCh; ++c) rate[c] = kFused && c < mine ? gate_rate(a.c, a.lam[ch + c], kFast) : 0.f;
+  const Values rate = each([&](float lam) { return gate_rate(a.c, lam); }, read_state<N>(kFused ? a.lam + ch : nullptr, mine));
 
   const int tile0 = part.t0 / kTile;
   const int rounds = part.t1 > part.t0 ? ((part.t1 + kTile - 1) / kTile - tile0 + S - 1) / S : 0;
-  const long long px = a.x_pitch * (long long)sizeof(T), pg = a.g_pitch * (long long)sizeof(G),
-                  pi = a.i_pitch * (long long)sizeof(G);
   auto window_start = [&](int round) { return (tile0 + round * S + rank) * kTile + warp * kTau; };
   auto fetch = [&](int round) {
-    if (round < rounds) {
-      const int w0 = window_start(round), lo = max(0, part.t0 - w0), hi = min(kTau, part.t1 - w0);
-      char* const to = sh.ring[round % kStages][warp];
-      const size_t first = (size_t)block * 32 * kCh;
-      copy_window<Shared::kRowX>(to, static_cast<const char*>(a.x) + w0 * px + first * sizeof(T), px, lo, hi,
-                                 left * (int)sizeof(T), x_unit, lane);
-      copy_window<Shared::kRowG>(to + kTau * Shared::kRowX, static_cast<const char*>(a.g) + w0 * pg + first * sizeof(G),
-                                 pg, lo, hi, left * (int)sizeof(G), g_unit, lane);
-      if (kFused)
-        copy_window<Shared::kRowG>(to + kTau * (Shared::kRowX + Shared::kRowG),
-                                   static_cast<const char*>(a.i) + w0 * pi + first * sizeof(G), pi, lo, hi,
-                                   left * (int)sizeof(G), i_unit, lane);
+    char* const to = sh.ring[round % kStages][warp];
+    if constexpr (kEngine) {
+      if (round < rounds && lane == 0) {
+        uint64_t* const bar = &sh.arrived[round % kStages][warp];
+        const int w0 = window_start(round);
+        mbar_arrive_expect_tx(bar, Shared::kWindow);
+        tma_window(to, &x_map, bar, block * W, w0);
+        tma_window(to + Shared::kAtG, &g_map, bar, block * W, w0);
+        if (kFused) tma_window(to + Shared::kAtI, &i_map, bar, block * W, w0);
+      }
+    } else {
+      if (round < rounds) {
+        const int w0 = window_start(round), lo = part.t0 - w0, hi = part.t1 - w0, left = a.D - block * W;
+        auto copy = [&](auto type, int at, const void* base, long long pitch, int unit) {
+          using E = decltype(type);
+          copy_window<kTau, W * sizeof(E)>(to + at, reinterpret_cast<const char*>(static_cast<const E*>(base) + w0 * pitch + block * W),
+                                           pitch * (long long)sizeof(E), lo, hi, left * (int)sizeof(E), unit, lane);
+        };
+        copy(T{}, 0, a.x, a.x_pitch, x_unit);
+        copy(G{}, Shared::kAtG, a.g, a.g_pitch, g_unit);
+        if (kFused) copy(G{}, Shared::kAtI, a.i, a.i_pitch, i_unit);
+      }
+      copies_close();
     }
-    copies_close();
   };
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kStages * kWarps; ++k) mbar_init(&sh.arrived[0][k], 1);
+    sh.chain.init();
+  }
+  if (clustered) cluster_sync();   // (the peers' shared memory is there once they run)
+  else __syncthreads();
 #pragma unroll
   for (int k = 0; k < kStages; ++k) fetch(k);
 
-  if (S > 1) {   // the peers' shared memory is there once they run
-    cluster_arrive();
-    cluster_wait();
-  }
-  float carry[kCh];   // the state in front of the round's tiles
-#pragma unroll
-  for (int c = 0; c < kCh; ++c) carry[c] = 0.f;
+  Values base = fill<N>(0.f);
+  bool lost = false;
   for (int round = 0; round < rounds; ++round) {
-    const int w0 = window_start(round), par = round & 1;
-    const Window w = finder.find<false>(w0, lane);
+    const int w0 = window_start(round);
+    const Window w = finder.template find<kTau, false>(w0, lane);
     const unsigned reset = w.first | w.dead;
-    copies_wait<kStages - 1>();
-    __syncwarp();
-    // a and b of the window's tokens
-    float da[kTau][kCh], db[kTau][kCh];
-    Step<kCh> step;
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) step.L[c] = 0.f;
+    if constexpr (kEngine) {
+      wait_or_report(&sh.arrived[round % kStages][warp], round / kStages & 1, &lost, a.dev_status);
+    } else {
+      copies_wait<kStages - 1>();
+      __syncwarp();
+    }
+    // a and b of the window's tokens, and what they do together
+    Values da[kTau], db[kTau], L = fill<N>(0.f), H = fill<N>(0.f);
     const char* const from = sh.ring[round % kStages][warp];
 #pragma unroll
     for (int j = 0; j < kTau; ++j) {
-      float x[kCh], g[kCh], i[kCh];
-      read_row<T, kCh>(from + j * Shared::kRowX, lane, x);
-      read_row<G, kCh>(from + kTau * Shared::kRowX + j * Shared::kRowG, lane, g);
-      if (kFused) read_row<G, kCh>(from + kTau * (Shared::kRowX + Shared::kRowG) + j * Shared::kRowG, lane, i);
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        if (kFused) {
-          const FusedGate<kFast> f(g[c], i[c], rate[c]);
-          step.L[c] += f.l;
-          da[j][c] = f.a;
-          db[j][c] = f.s * f.si * x[c];
-        } else {
-          const float l = kFast ? g[c] * kLog2e : g[c];
-          step.L[c] += l;
-          da[j][c] = decay_of<kFast>(l);
-          db[j][c] = x[c];
-        }
+      const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
+      const Values g = read_row<G, N>(from + Shared::kAtG + j * Shared::kRowG, lane);
+      Values l;
+      if (kFused) {
+        const Values i = read_row<G, N>(from + Shared::kAtI + j * Shared::kRowG, lane);
+        l = each([](float r, float rt) { return rt * gate_sigmoid(r); }, g, rate);
+        da[j] = ex2(l);
+        db[j] = each([](float l, float a, float i, float x) { return sqrt_approx(one_minus_square(l, a)) * gate_sigmoid(i) * x; },
+                     l, da[j], i, x);
+      } else {
+        l = g * kLog2e;
+        da[j] = ex2(l);
+        db[j] = x;
       }
+      L = L + l;
+      H = fma(da[j], H, db[j]);
     }
     __syncwarp();
     fetch(round + kStages);
     if (reset) {   // a first token takes its sequence's state in, a dead one nothing
 #pragma unroll
       for (int j = 0; j < kTau; ++j) {
-        if (!(reset >> j & 1)) continue;
-        const int row = __shfl_sync(~0u, w.row, j);
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          if (w.dead >> j & 1) db[j][c] = 0.f;
-          else if (a.initial_state && c < mine)
-            db[j][c] = fmaf(da[j][c], a.initial_state[(size_t)row * a.D + ch + c], db[j][c]);
-        }
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) {
-      step.A[c] = decay_of<kFast>(step.L[c]);
-      step.H[c] = 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < kTau; ++j)
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) step.H[c] = reset >> j & 1 ? db[j][c] : fmaf(da[j][c], step.H[c], db[j][c]);
-    Step<kCh>(*const windows)[32] = S == 1 && par ? sh.odd : sh.even;
-    windows[warp][lane] = step;
-    if (lane == 0) sh.warp_reset[par][warp] = reset != 0;
-    __syncthreads();
-    // the windows of the tile up to this one, and all of them
-    float h[kCh], all[kCh], before[kCh], total[kCh];
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) h[c] = all[c] = before[c] = total[c] = 0.f;
-    bool h_reset = false, all_reset = false;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k == warp) {
-        h_reset = all_reset;
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          h[c] = all[c];
-          before[c] = total[c];
-        }
-      }
-      const Step<kCh> o = windows[k][lane];
-      const bool r = sh.warp_reset[par][k];
-      all_reset |= r;
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        all[c] = r ? o.H[c] : fmaf(o.A[c], all[c], o.H[c]);
-        total[c] += o.L[c];
-      }
-    }
-    if (S > 1) {
-      if (warp < S) {
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          store_peer(peer_address(&sh.tile.L[par][rank][c][lane], warp), total[c]);
-          store_peer(peer_address(&sh.tile.H[par][rank][c][lane], warp), all[c]);
-        }
-        if (lane == 0) store_peer(peer_address(&sh.tile_reset[par][rank], warp), (int)all_reset);
-      }
-      cluster_arrive();
-      cluster_wait();
-      float into[kCh], sum[kCh], run[kCh];
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) into[c] = sum[c] = run[c] = 0.f;
-      bool r = false;
-      for (int k = 0; k < S; ++k) {
-        if (k == rank) {
-#pragma unroll
-          for (int c = 0; c < kCh; ++c) into[c] = r ? run[c] : fmaf(decay_of<kFast>(sum[c]), carry[c], run[c]);
-        }
-        const bool here = sh.tile_reset[par][k];
-        r |= here;
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          const float L = sh.tile.L[par][k][c][lane], H = sh.tile.H[par][k][c][lane];
-          run[c] = here ? H : fmaf(decay_of<kFast>(L), run[c], H);
-          sum[c] += L;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        h[c] = h_reset ? h[c] : fmaf(decay_of<kFast>(before[c]), into[c], h[c]);
-        carry[c] = r ? run[c] : fmaf(decay_of<kFast>(sum[c]), carry[c], run[c]);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        h[c] = h_reset ? h[c] : fmaf(decay_of<kFast>(before[c]), carry[c], h[c]);
-        carry[c] = all_reset ? all[c] : fmaf(decay_of<kFast>(total[c]), carry[c], all[c]);
-      }
-    }
-    // the window's tokens from the state in front of it
-    if (a.carries && w0 % kRecCarry == 0 && (w.in & 1)) {
-#pragma unroll
-      for (int c = 0; c < kCh; ++c)
-        if (c < mine) a.carries[(size_t)(w0 / kRecCarry) * a.D + ch + c] = h[c];
-    }
-    T* const y = static_cast<T*>(a.y) + (size_t)w0 * a.D + ch;
-    if (w.plain) {
-#pragma unroll
-      for (int j = 0; j < kTau; ++j) {
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) h[c] = fmaf(da[j][c], h[c], db[j][c]);
-        if (a.y) write_row<T, kCh>(y + (size_t)j * a.D, h, mine, whole && mine == kCh);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kTau; ++j) {
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) h[c] = reset >> j & 1 ? db[j][c] : fmaf(da[j][c], h[c], db[j][c]);
-        if (a.y && (w.in >> j & 1)) write_row<T, kCh>(y + (size_t)j * a.D, h, mine, whole && mine == kCh);
-        if (a.final_state && (w.last >> j & 1)) {
+        if (reset >> j & 1) {
           const int row = __shfl_sync(~0u, w.row, j);
+          db[j] = w.dead >> j & 1
+                      ? fill<N>(0.f)
+                      : fma(da[j], read_state<N>(a.initial_state ? a.initial_state + (size_t)row * a.D + ch : nullptr, mine), db[j]);
+          H = db[j];
+        } else {
+          H = fma(da[j], H, db[j]);
+        }
+      }
+    }
+    Values h = clustered ? sh.chain.together(warp, round, S, rank, lane, L, H, reset != 0, &base, &lost, a.dev_status)
+                        : sh.chain.alone(warp, round, rounds, lane, L, H, reset != 0, &lost, a.dev_status);
+    // the window's tokens from the state in front of it
+    if (a.carries && w0 % kRecCarry == 0 && (w.in & 1)) write_state(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, h, mine);
+    T* const y = static_cast<T*>(a.y) + (size_t)w0 * a.D + ch;
+    if (w.plain && a.y) {
 #pragma unroll
-          for (int c = 0; c < kCh; ++c)
-            if (c < mine) a.final_state[(size_t)row * a.D + ch + c] = h[c];
+      for (int j = 0; j < kTau; ++j) {
+        h = fma(da[j], h, db[j]);
+        write_row<kEngine>(y + (size_t)j * a.D, h, mine);
+      }
+    } else if (!w.plain) {
+#pragma unroll
+      for (int j = 0; j < kTau; ++j) {
+        h = reset >> j & 1 ? db[j] : fma(da[j], h, db[j]);
+        if (a.y && (w.in >> j & 1)) write_row<kEngine>(y + (size_t)j * a.D, h, mine);
+        if (w.last >> j & 1) {
+          const int row = __shfl_sync(~0u, w.row, j);
+          if (a.final_state) write_state(a.final_state + (size_t)row * a.D + ch, h, mine);
         }
       }
     }
   }
-  copies_wait<0>();
+  if (!kEngine) copies_wait<0>();
+  if (clustered) cluster_sync();   // no CTA ends while a peer's stores are on their way
 }
 
-template <typename T, typename G, bool kFused, int kCh>
+template <typename T, typename G, bool kFused, int N>
 cudaError_t launch_fwd(const RecurrenceArgs& a) {
-  const RecurrencePlan p = recurrence_plan((long long)a.B * a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, 32 * kCh,
-                                           kTile, kMaxCluster, 2);
-  auto* const kernel = recurrence_fwd_kernel<T, G, kFused, kCh>;
-  const size_t shared = sizeof(FwdShared<T, G, kFused, kCh>);
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-  if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {(unsigned)p.S, 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.blocks * p.parts * p.S);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = a.stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const bool whole = a.D % kCh == 0 && reinterpret_cast<uintptr_t>(a.y) % (kCh * sizeof(T)) == 0;
-  return cudaLaunchKernelEx(&cfg, kernel, a, p.parts, copy_unit(a.x, a.x_pitch, a.D, sizeof(T)),
-                            copy_unit(a.g, a.g_pitch, a.D, sizeof(G)), copy_unit(a.i, a.i_pitch, a.D, sizeof(G)), whole);
+  constexpr int W = 32 * N;
+  const long long tokens = (long long)a.B * a.T;
+  const RecurrencePlan p = recurrence_plan(tokens, a.D, a.num_seqs, a.cu_seqlens != nullptr, W, kTile);
+  const size_t shared = sizeof(FwdShared<T, G, kFused, N>);
+  const int x_unit = copy_unit(a.x, a.x_pitch, a.D, sizeof(T)), g_unit = copy_unit(a.g, a.g_pitch, a.D, sizeof(G)),
+            i_unit = copy_unit(a.i, a.i_pitch, a.D, sizeof(G));
+  CUtensorMap mx{}, mg{}, mi{};
+  const bool engine = tokens > 0 && engine_rows(a.x, a.x_pitch, a.D, sizeof(T)) && engine_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
+                      (!kFused || engine_rows(a.i, a.i_pitch, a.D, sizeof(G))) &&
+                      reinterpret_cast<uintptr_t>(a.y) % (N * sizeof(T)) == 0;
+  if (!engine)
+    return launch_clusters(recurrence_fwd_kernel<T, G, kFused, N, false, true>, p, kWarps * 32, shared, a.stream, a, p.parts,
+                           p.S, x_unit, g_unit, i_unit, mx, mg, mi);
+  if (!rows_map(&mx, a.x, tokens, a.D, a.x_pitch, sizeof(T), W, kTau) ||
+      !rows_map(&mg, a.g, tokens, a.D, a.g_pitch, sizeof(G), W, kTau) ||
+      (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau)))
+    return cudaErrorInvalidValue;
+  return launch_clusters(p.S > 1 ? recurrence_fwd_kernel<T, G, kFused, N, true, true> : recurrence_fwd_kernel<T, G, kFused, N, true, false>,
+                         p, kWarps * 32, shared, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, mx, mg, mi);
 }
 
-template <typename T, typename G, int kCh>
+template <typename T, typename G, int N>
 cudaError_t launch_fwd(const RecurrenceArgs& a) {
-  return a.lam ? launch_fwd<T, G, true, kCh>(a) : launch_fwd<T, G, false, kCh>(a);
+  return a.lam ? launch_fwd<T, G, true, N>(a) : launch_fwd<T, G, false, N>(a);
 }
 
 constexpr int kDecodeThreads = 128;
@@ -325,9 +232,9 @@ __global__ void recurrence_decode_kernel(RecurrenceArgs a) {
   float la = load_elem(a.g, (size_t)n * a.g_pitch + d, a.g_dtype);
   float b = load_elem(a.x, (size_t)n * a.x_pitch + d, a.io_dtype);
   if (a.lam) {
-    const FusedGate<false> f(la, load_elem(a.i, (size_t)n * a.i_pitch + d, a.g_dtype), gate_rate(a.c, a.lam[d], false));
-    la = f.l;
-    b *= f.s * f.si;
+    const DecodeGate f(la, load_elem(a.i, (size_t)n * a.i_pitch + d, a.g_dtype), -a.c * softplus_f(a.lam[d]));
+    la = f.la;
+    b *= f.into;
   }
   float* const state = a.state + (size_t)slot * a.D + d;
   const float h = decayed(la, *state, b);

@@ -1,33 +1,76 @@
 // gdn_recurrence.cuh -- what the kernels of the gated linear recurrence share: the gates, packed
-// lengths, a warp's window of tokens and its copies, what CTAs of a cluster tell one another.
+// lengths, a warp's window of tokens and its copies, what warps and CTAs tell one another.
 //
-// The tokens of all sequences stand on one axis.  A CTA holds W = 32 kCh channels (a lane kCh of them)
-// and walks tiles of it; a warp has kTau successive tokens of a tile.  What a window does to a state is
-// h -> A h + H, A = exp(L): windows are joined by that, and sequences' starts by "reset", which
-// takes H alone (a NaN in front of it stays there).  L is a sum of logarithms: A is rounded once for
-// all the tokens that it stands for, not once a token, and an error that always has the same sign
-// does not add up over a long memory.
+// The tokens of all sequences stand on one axis.  A CTA holds W = 32 kCh channels (a lane kCh of them,
+// bf16 in pairs) and walks tiles of the axis; a warp has kTau successive tokens of a tile, its window.
+// What a window does to a state is h -> 2^L h + H: windows are joined by that, and sequences' starts by
+// "reset", which takes H alone (a NaN in front of it stays there).  L is a sum of logarithms: its power is
+// rounded once for all the tokens that it stands for, not once a token, and an error that always
+// has the same sign does not add up over a long memory.
+//
+// A window's warp knows L and H without its neighbours.  It then gets what is in front of it from the
+// warp of the window before, passes on what is behind it, and walks its tokens: no barrier of the
+// CTA, a chain of short hand-overs through shared memory that runs ahead of the walking.
 #pragma once
 
 #include <algorithm>
 
 #include "gdn_common.cuh"
+#include "gdn_internal.h"
 #include "gdn_launch.cuh"
 #include "gdn_recurrence.h"
+#include "gdn_sm100.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kTau = 16;   // tokens of a warp's window
+using namespace sm100;
 
 // ---------------------------------------------------------------- gates
 
-__device__ __forceinline__ float ex2_approx(float x) {
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// A lane's values of a token, one for each of its channels.
+template <int N>
+struct Lanes {
+  float v[N];
+};
+template <typename F, int N, typename... More>
+__device__ __forceinline__ Lanes<N> each(F f, const Lanes<N>& x, const More&... more) {
+  Lanes<N> r;
+#pragma unroll
+  for (int c = 0; c < N; ++c) r.v[c] = f(x.v[c], more.v[c]...);
+  return r;
+}
+template <int N> __device__ __forceinline__ Lanes<N> fill(float x) {
+  Lanes<N> r;
+#pragma unroll
+  for (int c = 0; c < N; ++c) r.v[c] = x;
+  return r;
+}
+template <int N> __device__ __forceinline__ Lanes<N> operator+(const Lanes<N>& a, const Lanes<N>& b) {
+  return each([](float x, float y) { return x + y; }, a, b);
+}
+template <int N> __device__ __forceinline__ Lanes<N> operator*(const Lanes<N>& a, const Lanes<N>& b) {
+  return each([](float x, float y) { return x * y; }, a, b);
+}
+template <int N> __device__ __forceinline__ Lanes<N> operator*(const Lanes<N>& a, float b) {
+  return each([=](float x) { return x * b; }, a);
+}
+template <int N>
+__device__ __forceinline__ Lanes<N> fma(const Lanes<N>& a, const Lanes<N>& b, const Lanes<N>& c) {
+  return each([](float x, float y, float z) { return fmaf(x, y, z); }, a, b, c);
+}
+
+__device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float rcp_approx(float x) {
+template <int N> __device__ __forceinline__ Lanes<N> ex2(const Lanes<N>& x) {
+  return each([](float v) { return ex2(v); }, x);
+}
+__device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
@@ -37,45 +80,34 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-
-// Logarithms of decays are to base 2 where the outputs are bf16 (the hardware's exponential, off by
-// 2^-22, is enough for them), natural ones with the full functions for fp32.
-template <bool kFast> __device__ __forceinline__ float decay_of(float l) { return kFast ? ex2_approx(l) : expf(l); }
-template <bool kFast> __device__ __forceinline__ float gate_sigmoid(float x) {
-  return kFast ? rcp_approx(1.f + ex2_approx(x * -kLog2e)) : sigmoid_f(x);
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// 1 - a^2 of a = decay_of(l): a short series where a is near 1 and the difference would lose its digits.
-template <bool kFast>
+// 1 / (1 + e^-x).
+__device__ __forceinline__ float gate_sigmoid(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
+
+// 1 - a^2 of a = 2^l.  Where a is near 1 the difference would lose its digits: there (1 - e^-z) / z, z = -2 ln a
+// in [0, 1/8], as the polynomial of degree 2 with the least error (2.4e-6 of it), here in powers of l.
+// Behind the border a's own error, 2^-22, makes at most 4e-6 of it.  (Its root has half of either.)
 __device__ __forceinline__ float one_minus_square(float l, float a) {
-  if (!kFast) return -expm1f(2.f * l);
-  const float z = l * (2.f * kLn2);
-  float p = fmaf(z, 1.f / 720.f, 1.f / 120.f);
-  p = fmaf(z, p, 1.f / 24.f);
-  p = fmaf(z, p, 1.f / 6.f);
-  p = fmaf(z, p, 0.5f);
-  p = fmaf(z, p, 1.f);
-  return z > -0.25f ? -z * p : fmaf(-a, a, 1.f);
+  const float near = l * fmaf(l, fmaf(l, -0.42383318f, -0.96023068f), -1.386291f);
+  return l > -0.09016844f ? near : fmaf(-a, a, 1.f);
 }
 
-// Everything that one token of one channel has from its fused gates; rate is a_t's logarithm at an
-// open recurrence gate.
-template <bool kFast>
-struct FusedGate {
-  float l, a, sr, si, s;
-  __device__ __forceinline__ FusedGate(float r, float i, float rate) {
-    sr = gate_sigmoid<kFast>(r);
-    si = gate_sigmoid<kFast>(i);
-    l = rate * sr;
-    a = decay_of<kFast>(l);
-    const float q = one_minus_square<kFast>(l, a);
-    s = kFast ? sqrt_approx(q) : sqrtf(q);
+// The logarithm (to base 2) of a_t at an open recurrence gate.
+__device__ __forceinline__ float gate_rate(float c, float lam) { return -c * softplus_f(lam) * kLog2e; }
+
+// Decode's token of one channel, by the full functions: log a = la, and s sigmoid(i).
+struct DecodeGate {
+  float la, into;
+  __device__ __forceinline__ DecodeGate(float r, float i, float minus_c_softplus) {
+    la = minus_c_softplus * sigmoid_f(r);
+    into = sqrtf(-expm1f(2.f * la)) * sigmoid_f(i);
   }
 };
-__device__ __forceinline__ float gate_rate(float c, float lam, bool fast) {
-  return -c * softplus_f(lam) * (fast ? kLog2e : 1.f);
-}
 
 // a h + b, a = exp(la), for a state that is rounded at every token (decode): without the error that
 // rounding a makes in the same direction at every token of a long memory (1 - a to 24 bits instead of
@@ -141,7 +173,7 @@ __device__ __forceinline__ Part part_of(const Sequences& s, int p, int parts) {
   return r;
 }
 
-// What a warp knows of its window's tokens [w0, w0 + kTau), one bit a token.
+// What a warp knows of its window's tokens [w0, w0 + kTau), one bit a token (kTau 8 or 16).
 struct Window {
   unsigned in;      // of this part
   unsigned dead;    // not in this part, in no sequence, or in a padding one: its row is zero
@@ -157,19 +189,21 @@ struct WindowFinder {
   Part part;
   const int32_t* slots;   // NULL: states are the sequences'
   int num_slots;
-  int* dev_status;
   int bos = 0, eos = 0;   // of the sequence that a neighbouring window lies in
 
-  template <bool kLeftwards>
+  template <int kTau, bool kLeftwards>
   __device__ __forceinline__ Window find(int w0, int lane) {
     Window w;
     w.plain = w0 > bos && w0 + kTau < eos;
-    if (w.plain) {
-      w.in = (1u << kTau) - 1;
-      w.dead = w.first = w.last = 0;
-      w.row = 0;
-      return w;
-    }
+    w.in = (1u << kTau) - 1;
+    w.dead = w.first = w.last = 0;
+    w.row = 0;
+    if (!w.plain) look<kTau, kLeftwards>(w0, lane, &w);
+    return w;
+  }
+
+  template <int kTau, bool kLeftwards>
+  __device__ __forceinline__ void look(int w0, int lane, Window* w) {
     const int t = w0 + (lane & (kTau - 1));
     const bool in = t >= part.t0 && t < part.t1;
     const int n = in ? seq.of(t) : -1;
@@ -182,59 +216,54 @@ struct WindowFinder {
         if (row < 0 || row >= num_slots) row = -1;
       }
     }
-    w.in = __ballot_sync(~0u, in) & ((1u << kTau) - 1);
-    w.dead = __ballot_sync(~0u, row < 0) & ((1u << kTau) - 1);
-    w.first = __ballot_sync(~0u, row >= 0 && t == b) & ((1u << kTau) - 1);
-    w.last = __ballot_sync(~0u, row >= 0 && t + 1 == e) & ((1u << kTau) - 1);
-    w.row = row;
+    constexpr unsigned all = (1u << kTau) - 1;
+    w->in = __ballot_sync(~0u, in) & all;
+    w->dead = __ballot_sync(~0u, row < 0) & all;
+    w->first = __ballot_sync(~0u, row >= 0 && t == b) & all;
+    w->last = __ballot_sync(~0u, row >= 0 && t + 1 == e) & all;
+    w->row = row;
     const int at = kLeftwards ? 0 : kTau - 1;
     const bool live = __shfl_sync(~0u, row, at) >= 0;
     bos = __shfl_sync(~0u, b, at);
-    eos = live ? __shfl_sync(~0u, e, at) : 0;
-    return w;
+    eos = __shfl_sync(~0u, live ? e : 0, at);
   }
 };
 
 // ---------------------------------------------------------------- copies
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src)
-               : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src)
-               : "memory");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft> __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// One warp's window of one tensor: rows lo <= j < hi of kTau, kRow bytes each (`left` of them inside the
-// tensor), to dst [kTau][kRow].  unit: the bytes that every row's start and end is a multiple of, 16,
-// 4 or 2 (then by loads and stores: asynchronous copies have at least four bytes).
-template <int kRow>
+// One warp's window of one tensor where its rows do not allow the copy engine: rows lo <= j < hi of kTau, kRow
+// bytes each (`left` of them inside the tensor), to dst [kTau][kRow].  unit: the bytes that every row's
+// start and end is a multiple of, 16, 4 or 2 (then by loads and stores: asynchronous copies have at
+// least four bytes).
+template <int kTau, int kRow>
 __device__ __forceinline__ void copy_window(char* dst, const char* src, long long pitch, int lo, int hi, int left,
                                             int unit, int lane) {
   if (unit == 16) {
     constexpr int kPer = kRow / 16;
     const int c = lane % kPer * 16;
-#pragma unroll
-    for (int k = 0; k < kTau * kPer / 32; ++k) {
-      const int row = lane / kPer + k * (32 / kPer);
+#pragma unroll 2
+    for (int row = lane / kPer; row < kTau; row += 32 / kPer)
       if (row >= lo && row < hi && c < left) copy_async16(dst + row * kRow + c, src + row * pitch + c);
-    }
   } else if (unit == 4) {
     constexpr int kPer = kRow / 4;
-    constexpr int kStep = kPer >= 32 ? 1 : 32 / kPer;
-#pragma unroll
-    for (int k = 0; k < kTau / kStep; ++k) {
-      const int row = lane / kPer + k * kStep, c = lane % kPer * 4;
+    const int c = lane % kPer * 4;
+#pragma unroll 4
+    for (int row = lane / kPer; row < kTau; row += 32 / kPer)
       if (row >= lo && row < hi && c < left) copy_async4(dst + row * kRow + c, src + row * pitch + c);
-    }
   } else {
 #pragma unroll 4
-    for (int row = lo; row < hi; ++row)
+    for (int row = max(lo, 0); row < min(hi, kTau); ++row)
 #pragma unroll
       for (int c = lane * 2; c < kRow; c += 64)
         if (c < left)
@@ -242,58 +271,201 @@ __device__ __forceinline__ void copy_window(char* dst, const char* src, long lon
   }
 }
 
-// A lane's kCh values of a row in shared memory.
-template <typename T, int kCh>
-__device__ __forceinline__ void read_row(const char* row, int lane, float (&x)[kCh]) {
-  if constexpr (sizeof(T) == 2 && kCh == 2) {
-    const float2 v = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(row)[lane]);
-    x[0] = v.x;
-    x[1] = v.y;
-  } else {
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) x[c] = (float)reinterpret_cast<const T*>(row)[lane * kCh + c];
-  }
-}
-// ... to global memory; n: how many of them are inside the tensor, whole: they may go in one store.
-template <typename T, int kCh>
-__device__ __forceinline__ void write_row(T* row, const float (&x)[kCh], int n, bool whole) {
-  if constexpr (sizeof(T) == 2 && kCh == 2) {
-    if (whole) {
-      *reinterpret_cast<__nv_bfloat162*>(row) = __floats2bfloat162_rn(x[0], x[1]);
-      return;
-    }
-  }
-#pragma unroll
-  for (int c = 0; c < kCh; ++c)
-    if (c < n) row[c] = (T)x[c];
+// The same by the copy engine: the box [kTau][W] of a map made by rows_map; one thread.
+__device__ __forceinline__ void tma_window(char* dst, const CUtensorMap* map, uint64_t* bar, int channel, int token) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(channel), "r"(token)
+      : "memory");
 }
 
-// ---------------------------------------------------------------- clusters
+// A lane's values of a row in shared memory, and to global memory: n of them are inside the tensor; whole:
+// all or none, and they may go in one store.
+template <typename T, int N>
+__device__ __forceinline__ Lanes<N> read_row(const char* row, int lane) {
+  Lanes<N> x;
+  if constexpr (N == 2 && sizeof(T) == 2) {
+    const float2 v = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(row)[lane]);
+    x.v[0] = v.x;
+    x.v[1] = v.y;
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c) x.v[c] = (float)reinterpret_cast<const T*>(row)[lane * N + c];
+  }
+  return x;
+}
+template <bool kWhole, typename T, int N>
+__device__ __forceinline__ void write_row(T* row, const Lanes<N>& x, int n) {
+  if constexpr (kWhole && N == 2 && sizeof(T) == 2) {
+    if (n > 0) *reinterpret_cast<__nv_bfloat162*>(row) = __floats2bfloat162_rn(x.v[0], x.v[1]);
+  } else {
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+      if (c < n) row[c] = (T)x.v[c];
+  }
+}
+// ... of fp32 states; zero where there is no tensor.
+template <int N>
+__device__ __forceinline__ Lanes<N> read_state(const float* row, int n) {
+  Lanes<N> x;
+#pragma unroll
+  for (int c = 0; c < N; ++c) x.v[c] = row && c < n ? row[c] : 0.f;
+  return x;
+}
+template <int N>
+__device__ __forceinline__ void write_state(float* row, const Lanes<N>& x, int n) {
+#pragma unroll
+  for (int c = 0; c < N; ++c)
+    if (c < n) row[c] = x.v[c];
+}
+
+// ---------------------------------------------------------------- hand-overs
+
+// A wait of at most this many tries (seconds); one that has run out is reported, and none follows it:
+// what the launch writes is then not to be used.
+constexpr int kTries = 1 << 25;
+__device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, bool* lost, int* dev_status) {
+  if (*lost) return;
+  for (int k = 0; k < kTries; ++k)
+    if (mbar_try_wait(bar, parity)) return;
+  *lost = true;
+  report(dev_status, GDN_DEV_TIMEOUT);
+}
+
+// The state in front of a window: 2^L base + H.
+template <int N>
+struct Front {
+  Lanes<N> base, L, H;
+  __device__ __forceinline__ Lanes<N> value() const { return fma(ex2(L), base, H); }
+};
 
 __device__ __forceinline__ int cluster_rank() {
   int r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ int cluster_size() {
-  int r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
+// (Cluster instructions are for launches of clusters alone; of one CTA they are not.)
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// p's counterpart in the CTA of that rank.
-__device__ __forceinline__ unsigned peer_address(const void* p, int rank) {
-  unsigned r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((unsigned)__cvta_generic_to_shared(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void store_peer(unsigned at, float x) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(x) : "memory");
-}
-__device__ __forceinline__ void store_peer(unsigned at, int x) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(x) : "memory");
-}
+
+constexpr int kMaxCluster = 8;
+constexpr float kReset = __builtin_huge_valf();   // in L's place: "reset"
+
+// What a CTA's warps hand to one another, and the CTAs of a cluster.
+//
+// Alone, windows stand in one chain: `front` goes from warp to warp and from the last one to the first
+// one's next round.  In a cluster the chain starts anew in every tile, from nothing; its end, the
+// tile's (L, H), goes to every CTA's box by asynchronous stores that the receiver's barrier counts (no
+// fence waits for the outputs on their way to memory).  Every warp joins the round's tiles for itself:
+// the state in front of its own CTA's tile and, behind them all, the next round's.
+//
+// A slot is written again one round later, by a warp that has had its own message of that round: for
+// that, the ring of messages (alone) or the round's boxes (which have passed through every warp) have
+// gone round since the slot was read.  Boxes stand in two sets in turn: a peer sends the round after the
+// next one only after it has had the next one's, which this CTA's warps sent on after reading.
+template <int kWarps, int N>
+struct Chain {
+  Front<N> slot[kWarps][32];
+  struct alignas(8 * N) Box { Lanes<N> L, H; } box[2][kMaxCluster][32];
+  alignas(8) uint64_t full[kWarps];
+  uint64_t boxes[2];
+
+  __device__ __forceinline__ void init() {   // one thread; a barrier follows
+    for (int k = 0; k < kWarps; ++k) mbar_init(&full[k], 1);
+    mbar_init(&boxes[0], 1);
+    mbar_init(&boxes[1], 1);
+    fence_mbar_init();
+  }
+
+  // The state in front of this warp's window (L, H), after handing on what is behind it.  `order`: the
+  // window's place in its tile.
+  __device__ __forceinline__ Lanes<N> alone(int order, int round, int rounds, int lane, const Lanes<N>& L,
+                                            const Lanes<N>& H, bool reset, bool* lost, int* dev_status) {
+    Front<N> f{fill<N>(0.f), fill<N>(0.f), fill<N>(0.f)};
+    if (order > 0 || round > 0) {
+      wait_or_report(&full[order], (round - (order == 0)) & 1, lost, dev_status);
+      f = slot[order][lane];
+    }
+    const Lanes<N> h = f.value();
+    f.H = fma(ex2(L), f.H, H);
+    f.L = f.L + L;
+    if (reset) {
+      f.H = H;
+      f.L = f.base = fill<N>(0.f);
+    }
+    if (order + 1 < kWarps) {
+      send(order + 1, lane, f);
+    } else if (round + 1 < rounds) {
+      f.base = f.value();
+      f.L = f.H = fill<N>(0.f);
+      send(0, lane, f);
+    }
+    return h;
+  }
+
+  // The same in a cluster of S; `base`: the state in front of the round's tiles (kept from call to call, zero
+  // at first).
+  __device__ __forceinline__ Lanes<N> together(int order, int round, int S, int rank, int lane, const Lanes<N>& L,
+                                               const Lanes<N>& H, bool reset, Lanes<N>* base, bool* lost,
+                                               int* dev_status) {
+    Front<N> f{fill<N>(0.f), fill<N>(0.f), fill<N>(0.f)};
+    if (order > 0) {
+      wait_or_report(&full[order], round & 1, lost, dev_status);
+      f = slot[order][lane];
+    }
+    const Front<N> mine = f;
+    f.L = reset ? fill<N>(kReset) : sum(f.L, L);
+    f.H = reset ? H : fma(ex2(L), f.H, H);
+    const int set = round & 1;
+    if (order + 1 < kWarps) {
+      send(order + 1, lane, f);
+    } else {
+      if (lane == 0) mbar_arrive_expect_tx(&boxes[set], S * 32 * sizeof(Box));
+      const unsigned at = smem_u32(&box[set][rank][lane]), to = smem_u32(&boxes[set]);
+      for (int k = 0; k < S; ++k) {
+        unsigned peer_at, peer_bar;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_at) : "r"(at), "r"(k));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_bar) : "r"(to), "r"(k));
+        if constexpr (N == 2)
+          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                           peer_at),
+                       "f"(f.L.v[0]), "f"(f.L.v[1]), "f"(f.H.v[0]), "f"(f.H.v[1]), "r"(peer_bar)
+                       : "memory");
+        else
+          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(peer_at),
+                       "f"(f.L.v[0]), "f"(f.H.v[0]), "r"(peer_bar)
+                       : "memory");
+      }
+    }
+    wait_or_report(&boxes[set], round >> 1 & 1, lost, dev_status);
+    Lanes<N> into = *base, run = fill<N>(0.f), all = fill<N>(0.f);
+    for (int k = 0; k < S; ++k) {
+      if (k == rank) into = joined(all, *base, run);
+      const Box o = box[set][k][lane];
+      run = joined(o.L, run, o.H);
+      all = sum(all, o.L);
+    }
+    *base = joined(all, *base, run);
+    return joined(mine.L, into, mine.H);
+  }
+
+ private:
+  __device__ __forceinline__ void send(int to, int lane, const Front<N>& f) {
+    slot[to][lane] = f;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[to]);
+  }
+  static __device__ __forceinline__ Lanes<N> sum(const Lanes<N>& a, const Lanes<N>& b) {
+    return each([](float x, float y) { return x == kReset || y == kReset ? kReset : x + y; }, a, b);
+  }
+  static __device__ __forceinline__ Lanes<N> joined(const Lanes<N>& L, const Lanes<N>& base, const Lanes<N>& H) {
+    return each([](float l, float x, float h) { return l == kReset ? h : fmaf(ex2(l), x, h); }, L, base, H);
+  }
+};
 
 // ---------------------------------------------------------------- launches
 
@@ -302,32 +474,80 @@ struct RecurrencePlan {
   int blocks, parts, S;
 };
 
-// For kernels of `width` channels and `tile` tokens a CTA, `per_sm` CTAs an SM.
-inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile, int max_S,
-                                      int per_sm) {
-  const long long want = (long long)std::max(1, current_sm_count()) * per_sm;
-  RecurrencePlan p;
-  p.blocks = (D + width - 1) / width;
+// For kernels of `width` channels and `tile` tokens a CTA, one CTA an SM.  The plan with the least time: waves
+// of CTAs, each as many rounds as its longest part has (a round more than that to start), a round of a
+// cluster counting as two of a CTA alone (1 x 32768 x 2048: 6.4 us against 2.8).  Parts are whole
+// sequences: of equal ones the longest part is known, of packed ones (whose lengths the host does not
+// know) it is taken to be longer than the mean by half a mean sequence.
+inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile) {
+  const long long slots = std::max(1, current_sm_count());
+  RecurrencePlan best{(D + width - 1) / width, 1, 1};
+  double least = 1e300;
   N = std::max(1, N);
-  const long long tiles = std::max(1LL, (tokens + tile - 1) / tile);
-  auto parts_for = [&](long long ctas) {   // of all blocks together
-    return (int)std::min<long long>({(long long)N, tiles, std::max(1LL, (ctas + p.blocks - 1) / p.blocks)});
-  };
-  p.S = 1;
-  if (!packed) {
-    p.parts = parts_for(2 * want);
-    while (p.S < max_S && (long long)p.blocks * p.parts * p.S < want && 2LL * p.S * p.parts <= tiles) p.S *= 2;
-  } else {
-    while (p.S < max_S && 2 * p.S <= tiles) p.S *= 2;
-    p.parts = std::min<long long>(parts_for((want + p.S - 1) / p.S), std::max(1LL, tiles / p.S));
+  const int most = (int)std::min<long long>({(long long)N, 64, std::max(1LL, 4 * slots / best.blocks), std::max(1LL, tokens / tile)});
+  for (int parts = 1; parts <= most; ++parts) {
+    const double each = packed ? (double)tokens / parts + (parts > 1 ? 0.5 * (double)tokens / N : 0.)
+                               : (double)tokens / N * ((N + parts - 1) / parts);
+    for (int S = 1; S <= kMaxCluster; ++S) {
+      const long long rounds = (long long)(each / ((double)tile * S)) + 1;
+      const long long waves = ((long long)best.blocks * parts * S + slots - 1) / slots;
+      const double time = (double)waves * (double)(rounds + 1) * (S > 1 ? 2. : 1.);
+      if (time < 0.98 * least) {
+        least = time;
+        best.parts = parts;
+        best.S = S;
+      }
+    }
   }
-  return p;
+  return best;
 }
 
 inline int copy_unit(const void* p, long long pitch, int D, int elem) {
   const unsigned long long all = reinterpret_cast<uintptr_t>(p) | (unsigned long long)pitch * elem |
                                  (unsigned long long)D * elem;
   return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
+}
+
+// Whether the copy engine takes rows as they are: starts, ends and distances in multiples of 16 bytes.
+inline bool engine_rows(const void* p, long long pitch, int D, int elem) {
+  return copy_unit(p, pitch, D, elem) == 16 && pitch * elem < (1LL << 40);
+}
+
+// The map of rows [tokens, D] `pitch` elements apart for boxes of `box` tokens of `width` channels.
+inline bool rows_map(CUtensorMap* m, const void* p, long long tokens, int D, long long pitch, int elem, int width, int box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode_tiled = tensor_map_encoder();
+  if (!encode_tiled) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)tokens}, strides[1] = {(cuuint64_t)pitch * elem};
+  const cuuint32_t size[2] = {(cuuint32_t)width, (cuuint32_t)box}, step[2] = {1, 1};
+  auto encode = [&]() {
+    return encode_tiled(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                        const_cast<void*>(p), dims, strides, size, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // a thread that has made no runtime call yet (autograd's, say) has no current context
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
+}
+
+// A launch of clusters of S CTAs with `shared` bytes of shared memory each.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), const RecurrencePlan& p, int threads, size_t shared,
+                            cudaStream_t stream, Args&&... args) {
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {(unsigned)p.S, 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)p.blocks * p.parts * p.S));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.S > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 }  // namespace

@@ -8,10 +8,11 @@
 //     dx = delta s sigmoid(i),   di = delta s u (1 - sigmoid(i)),
 //     dlam = sum of d(log a) sigmoid(r), times -c sigmoid(lam).
 //
-// The forward's shape from right to left, one reading of the inputs: a CTA of four windows a tile, which
-// starts from the state that the forward saved in front of it.  Windows' effects on the state (from the
-// left) and on e (from the right) are published at once.  Each lane sums its channels' dlam over its
-// CTA's tokens; a second launch adds the CTAs up in order.
+// The forward's shape from right to left, one reading of the inputs: a CTA walks tiles of kWarps windows,
+// each from the state that the forward saved in front of it.  A window hands on its effects on the state
+// (to the right, inside the tile) and on e (to the left).  The gates' sigmoids stay in shared memory for
+// the second half.  Each lane sums its channels' dlam over its CTA's tokens; a second launch adds the CTAs
+// up in order.
 #include <algorithm>
 
 #include "gdn_recurrence.cuh"
@@ -19,45 +20,44 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = kRecCarry / kTau;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTile = kRecCarry;
+constexpr int kTau = 8;
+constexpr int kWarps = 16;
+constexpr int kTile = kWarps * kTau;
 constexpr int kStages = 2;
-constexpr int kMaxCluster = 8;
+static_assert(kTile == kRecCarry, "a tile starts from a saved state");
 
-// A window's effect on the state in front of it (A, H) and on e behind it (A, E).
-template <int kCh>
-struct BothWays {
-  float A[kCh], L[kCh], H[kCh], E[kCh];
-};
-
-template <typename T, typename G, bool kFused, int kCh>
+template <typename T, typename G, bool kFused, int N>
 struct BwdShared {
-  static constexpr int kRowX = 32 * kCh * sizeof(T), kRowG = 32 * kCh * sizeof(G);
+  static constexpr int W = 32 * N;
+  static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
   static constexpr int kAtDy = kTau * kRowX, kAtG = 2 * kTau * kRowX, kAtI = kAtG + kTau * kRowG;
   static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
-  BothWays<kCh> window[2][kWarps][32];
-  float tile_L[2][kMaxCluster][kCh][32], tile_E[2][kMaxCluster][kCh][32];
-  float dlam[kWarps][kCh][32];
-  int window_reset[2][kWarps];       // 1: of the state, 2: of e
-  int tile_reset[2][kMaxCluster];
+  Lanes<N> sigmoid[kFused ? kWarps : 1][2][kFused ? kTau : 1][32];   // (dlam's sums in the end)
+  Chain<kWarps, N> chain;              // of e, right to left
+  Lanes<N> state[kWarps][32];          // the state in front of each window, left to right in a tile
+  uint64_t state_full[kWarps];
+  uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-template <typename T, typename G, bool kFused, int kCh>
-__global__ void __launch_bounds__(kThreads, 3)
-    recurrence_bwd_kernel(RecurrenceArgs a, int parts, int x_unit, int g_unit, int i_unit, int dy_unit, bool whole_x,
-                          bool whole_g, bool whole_i, float* dlam_part) {
-  using Shared = BwdShared<T, G, kFused, kCh>;
-  constexpr bool kFast = sizeof(T) == 2;
-  extern __shared__ char shared_bytes[];
+// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  kCluster: S may be above 1.
+template <typename T, typename G, bool kFused, int N, bool kEngine, bool kCluster>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    recurrence_bwd_kernel(RecurrenceArgs a, int parts, int S, int x_unit, int g_unit, int i_unit, int dy_unit,
+                          float* dlam_part, const __grid_constant__ CUtensorMap x_map,
+                          const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap g_map,
+                          const __grid_constant__ CUtensorMap i_map) {
+  using Shared = BwdShared<T, G, kFused, N>;
+  using Values = Lanes<N>;
+  constexpr int W = Shared::W;
+  extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int S = cluster_size(), rank = cluster_rank();
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+  const bool clustered = kCluster && S > 1;
+  const int rank = clustered ? cluster_rank() : 0;
   const int part_index = blockIdx.x / S % parts, block = blockIdx.x / S / parts;
-  const int ch = block * 32 * kCh + lane * kCh;
-  const int mine = max(0, min(kCh, a.D - ch));
-  const int left = a.D - block * 32 * kCh;
+  const int ch = block * W + lane * N;
+  const int mine = max(0, min(N, a.D - ch));
   WindowFinder finder;
   finder.seq = Sequences{a.cu_seqlens, a.num_seqs, a.T, a.cu_seqlens ? a.T : a.B * a.T};
   finder.slots = nullptr;
@@ -66,17 +66,16 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (a.cu_seqlens && !packed_lengths_fit(a.cu_seqlens, a.num_seqs, a.T)) {   // every gradient is zero
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.dev_status, GDN_DEV_BAD_CU_SEQLENS);
     const int step = parts * S * kWarps, first = (part_index * S + rank) * kWarps + warp;
-    for (int c = 0; c < mine; ++c) {
-      for (long long t = first; t < a.T; t += step) {
-        const size_t at = (size_t)t * a.D + ch + c;
-        static_cast<T*>(a.dx)[at] = (T)0.f;
-        static_cast<G*>(a.dg)[at] = (G)0.f;
-        if (kFused) static_cast<G*>(a.di)[at] = (G)0.f;
-      }
-      for (long long n = first; n < a.num_seqs && a.d_initial_state; n += step)
-        a.d_initial_state[(size_t)n * a.D + ch + c] = 0.f;
-      if (dlam_row && warp == 0) dlam_row[c] = 0.f;
+    const Values zero = fill<N>(0.f);
+    for (long long t = first; t < a.T; t += step) {
+      const size_t at = (size_t)t * a.D + ch;
+      write_row<false>(static_cast<T*>(a.dx) + at, zero, mine);
+      write_row<false>(static_cast<G*>(a.dg) + at, zero, mine);
+      if (kFused) write_row<false>(static_cast<G*>(a.di) + at, zero, mine);
     }
+    for (long long n = first; n < a.num_seqs && a.d_initial_state; n += step)
+      write_state(a.d_initial_state + (size_t)n * a.D + ch, zero, mine);
+    if (dlam_row && warp == 0) write_state(dlam_row, zero, mine);
     return;
   }
   finder.part = part_of(finder.seq, part_index, parts);
@@ -84,263 +83,201 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (a.d_initial_state) {   // empty sequences
     for (int n = part.n0 + rank * kWarps + warp; n < part.n1; n += S * kWarps) {
       if (finder.seq.end(n) > finder.seq.begin(n)) continue;
-      for (int c = 0; c < mine; ++c) {
-        const size_t at = (size_t)n * a.D + ch + c;
-        a.d_initial_state[at] = a.d_final_state ? a.d_final_state[at] : 0.f;
-      }
+      const size_t at = (size_t)n * a.D + ch;
+      write_state(a.d_initial_state + at, read_state<N>(a.d_final_state ? a.d_final_state + at : nullptr, mine), mine);
     }
   }
-  float rate[kCh], dlam[kCh];
-#pragma unroll
-  for (int c = 0; c < kCh; ++c) {
-    rate[c] = kFused && c < mine ? gate_rate(a.c, a.lam[ch + c], kFast) : 0.f;
-    dlam[c] = 0.f;
-  }
+  const Values rate = each([&](float lam) { return gate_rate(a.c, lam); }, read_state<N>(kFused ? a.lam + ch : nullptr, mine));
+  Values dlam = fill<N>(0.f);
+  auto state_of = [&](const float* states, int row) {   // of a sequence
+    return read_state<N>(states ? states + (size_t)row * a.D + ch : nullptr, mine);
+  };
 
   const int tile_end = part.t1 > part.t0 ? (part.t1 - 1) / kTile : 0;
   const int rounds = part.t1 > part.t0 ? (tile_end - part.t0 / kTile + S) / S : 0;
-  const long long px = a.x_pitch * (long long)sizeof(T), pg = a.g_pitch * (long long)sizeof(G),
-                  pi = a.i_pitch * (long long)sizeof(G), pd = a.D * (long long)sizeof(T);
   auto tile_of = [&](int round) { return tile_end - (round * S + rank); };
   auto fetch = [&](int round) {
-    if (round < rounds) {
-      const int w0 = tile_of(round) * kTile + warp * kTau, lo = max(0, part.t0 - w0), hi = min(kTau, part.t1 - w0);
-      char* const to = sh.ring[round % kStages][warp];
-      const size_t first = (size_t)block * 32 * kCh;
-      copy_window<Shared::kRowX>(to, static_cast<const char*>(a.x) + w0 * px + first * sizeof(T), px, lo, hi,
-                                 left * (int)sizeof(T), x_unit, lane);
-      copy_window<Shared::kRowX>(to + Shared::kAtDy, static_cast<const char*>(a.dy) + w0 * pd + first * sizeof(T), pd, lo,
-                                 hi, left * (int)sizeof(T), dy_unit, lane);
-      copy_window<Shared::kRowG>(to + Shared::kAtG, static_cast<const char*>(a.g) + w0 * pg + first * sizeof(G), pg, lo,
-                                 hi, left * (int)sizeof(G), g_unit, lane);
-      if (kFused)
-        copy_window<Shared::kRowG>(to + Shared::kAtI, static_cast<const char*>(a.i) + w0 * pi + first * sizeof(G), pi, lo,
-                                   hi, left * (int)sizeof(G), i_unit, lane);
+    char* const to = sh.ring[round % kStages][warp];
+    if constexpr (kEngine) {
+      if (round < rounds && lane == 0) {
+        uint64_t* const bar = &sh.arrived[round % kStages][warp];
+        const int w0 = tile_of(round) * kTile + warp * kTau;
+        mbar_arrive_expect_tx(bar, Shared::kWindow);
+        tma_window(to, &x_map, bar, block * W, w0);
+        tma_window(to + Shared::kAtDy, &dy_map, bar, block * W, w0);
+        tma_window(to + Shared::kAtG, &g_map, bar, block * W, w0);
+        if (kFused) tma_window(to + Shared::kAtI, &i_map, bar, block * W, w0);
+      }
+    } else {
+      if (round < rounds) {
+        const int w0 = tile_of(round) * kTile + warp * kTau, lo = part.t0 - w0, hi = part.t1 - w0, left = a.D - block * W;
+        auto copy = [&](auto type, int at, const void* base, long long pitch, int unit) {
+          using E = decltype(type);
+          copy_window<kTau, W * sizeof(E)>(to + at, reinterpret_cast<const char*>(static_cast<const E*>(base) + w0 * pitch + block * W),
+                                           pitch * (long long)sizeof(E), lo, hi, left * (int)sizeof(E), unit, lane);
+        };
+        copy(T{}, 0, a.x, a.x_pitch, x_unit);
+        copy(T{}, Shared::kAtDy, a.dy, a.D, dy_unit);
+        copy(G{}, Shared::kAtG, a.g, a.g_pitch, g_unit);
+        if (kFused) copy(G{}, Shared::kAtI, a.i, a.i_pitch, i_unit);
+      }
+      copies_close();
     }
-    copies_close();
   };
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kStages * kWarps; ++k) mbar_init(&sh.arrived[0][k], 1);
+    for (int k = 0; k < kWarps; ++k) mbar_init(&sh.state_full[k], 1);
+    sh.chain.init();
+  }
+  if (clustered) cluster_sync();   // (the peers' shared memory is there once they run)
+  else __syncthreads();
 #pragma unroll
   for (int k = 0; k < kStages; ++k) fetch(k);
-  if (S > 1) {   // the peers' shared memory is there once they run
-    cluster_arrive();
-    cluster_wait();
-  }
 
-  float carry[kCh];   // e behind the round's tiles
-#pragma unroll
-  for (int c = 0; c < kCh; ++c) carry[c] = 0.f;
+  Values base = fill<N>(0.f);
+  bool lost = false;
   for (int round = 0; round < rounds; ++round) {
-    const int tile = tile_of(round), w0 = tile * kTile + warp * kTau, par = round & 1;
-    const bool whole_tile = tile * (long long)kTile >= part.t0;
-    float h[kCh];   // the state in front of the tile
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) h[c] = whole_tile && c < mine ? a.carries[(size_t)tile * a.D + ch + c] : 0.f;
-    const Window w = finder.find<true>(w0, lane);
+    const int tile = tile_of(round), w0 = tile * kTile + warp * kTau;
+    Values h = fill<N>(0.f);
+    if (warp == 0 && tile * (long long)kTile >= part.t0) h = read_state<N>(a.carries + (size_t)tile * a.D + ch, mine);
+    const Window w = finder.template find<kTau, true>(w0, lane);
     const unsigned reset = w.first | w.dead, reset_e = w.last | w.dead;
-    copies_wait<kStages - 1>();
-    __syncwarp();
+    if constexpr (kEngine) {
+      wait_or_report(&sh.arrived[round % kStages][warp], round / kStages & 1, &lost, a.dev_status);
+    } else {
+      copies_wait<kStages - 1>();
+      __syncwarp();
+    }
     const char* const from = sh.ring[round % kStages][warp];
-    float da[kTau][kCh], db[kTau][kCh];
-    BothWays<kCh> step;
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) step.L[c] = step.H[c] = step.E[c] = 0.f;
+    // a and b of the window's tokens, and what they do together
+    Values da[kTau], db[kTau], L = fill<N>(0.f), H = fill<N>(0.f), E = fill<N>(0.f);
 #pragma unroll
     for (int j = 0; j < kTau; ++j) {
-      float x[kCh], g[kCh], i[kCh];
-      read_row<T, kCh>(from + j * Shared::kRowX, lane, x);
-      read_row<G, kCh>(from + Shared::kAtG + j * Shared::kRowG, lane, g);
-      if (kFused) read_row<G, kCh>(from + Shared::kAtI + j * Shared::kRowG, lane, i);
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        if (kFused) {
-          const FusedGate<kFast> f(g[c], i[c], rate[c]);
-          step.L[c] += f.l;
-          da[j][c] = f.a;
-          db[j][c] = f.s * f.si * x[c];
-        } else {
-          const float l = kFast ? g[c] * kLog2e : g[c];
-          step.L[c] += l;
-          da[j][c] = decay_of<kFast>(l);
-          db[j][c] = x[c];
-        }
+      const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
+      const Values g = read_row<G, N>(from + Shared::kAtG + j * Shared::kRowG, lane);
+      Values l;
+      if (kFused) {
+        const Values i = read_row<G, N>(from + Shared::kAtI + j * Shared::kRowG, lane);
+        const Values sr = each(gate_sigmoid, g), si = each(gate_sigmoid, i);
+        sh.sigmoid[warp][0][j][lane] = sr;
+        sh.sigmoid[warp][1][j][lane] = si;
+        l = rate * sr;
+        da[j] = ex2(l);
+        db[j] = each([](float l, float a) { return sqrt_approx(one_minus_square(l, a)); }, l, da[j]) * si * x;
+      } else {
+        l = g * kLog2e;
+        da[j] = ex2(l);
+        db[j] = x;
       }
+      L = L + l;
+      H = fma(da[j], H, db[j]);
     }
     if (reset) {   // a first token takes its sequence's state in, a dead one nothing
 #pragma unroll
       for (int j = 0; j < kTau; ++j) {
-        if (!(reset >> j & 1)) continue;
-        const int row = __shfl_sync(~0u, w.row, j);
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          if (w.dead >> j & 1) db[j][c] = 0.f;
-          else if (a.initial_state && c < mine)
-            db[j][c] = fmaf(da[j][c], a.initial_state[(size_t)row * a.D + ch + c], db[j][c]);
+        if (reset >> j & 1) {
+          const int row = __shfl_sync(~0u, w.row, j);
+          db[j] = w.dead >> j & 1 ? fill<N>(0.f) : fma(da[j], state_of(a.initial_state, row), db[j]);
+          H = db[j];
+        } else {
+          H = fma(da[j], H, db[j]);
         }
       }
     }
+    if (w.plain) {
 #pragma unroll
-    for (int j = 0; j < kTau; ++j)
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) step.H[c] = reset >> j & 1 ? db[j][c] : fmaf(da[j][c], step.H[c], db[j][c]);
-#pragma unroll
-    for (int j = kTau - 1; j >= 0; --j) {
-      float dy[kCh];
-      read_row<T, kCh>(from + Shared::kAtDy + j * Shared::kRowX, lane, dy);
-      const bool last = w.last >> j & 1, dead = w.dead >> j & 1;
-      const int row = last ? __shfl_sync(~0u, w.row, j) : 0;
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        if (last) step.E[c] = a.d_final_state && c < mine ? a.d_final_state[(size_t)row * a.D + ch + c] : 0.f;
-        step.E[c] = dead ? 0.f : da[j][c] * (dy[c] + step.E[c]);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) step.A[c] = decay_of<kFast>(step.L[c]);
-    sh.window[par][warp][lane] = step;
-    if (lane == 0) sh.window_reset[par][warp] = (reset ? 1 : 0) | (reset_e ? 2 : 0);
-    __syncthreads();
-    // the state through the windows in front of this one; e through those behind it, and through all
-    float e[kCh], all[kCh], before[kCh], total[kCh];
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) e[c] = all[c] = before[c] = total[c] = 0.f;
-    bool e_reset = false, all_reset = false;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      if (k < warp) {
-        const bool r = sh.window_reset[par][k] & 1;
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          const float A = sh.window[par][k][lane].A[c], H = sh.window[par][k][lane].H[c];
-          h[c] = r ? H : fmaf(A, h[c], H);
-        }
-      }
-    }
-#pragma unroll
-    for (int k = kWarps - 1; k >= 0; --k) {
-      if (k == warp) {
-        e_reset = all_reset;
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          e[c] = all[c];
-          before[c] = total[c];
-        }
-      }
-      const bool r = sh.window_reset[par][k] & 2;
-      all_reset |= r;
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        const BothWays<kCh>& o = sh.window[par][k][lane];
-        all[c] = r ? o.E[c] : fmaf(o.A[c], all[c], o.E[c]);
-        total[c] += o.L[c];
-      }
-    }
-    float into[kCh];
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) into[c] = carry[c];
-    if (S > 1) {
-      for (int to = warp; to < S; to += kWarps) {
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          store_peer(peer_address(&sh.tile_L[par][rank][c][lane], to), total[c]);
-          store_peer(peer_address(&sh.tile_E[par][rank][c][lane], to), all[c]);
-        }
-        if (lane == 0) store_peer(peer_address(&sh.tile_reset[par][rank], to), (int)all_reset);
-      }
-      cluster_arrive();
-      cluster_wait();
-      float sum[kCh], run[kCh];
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) sum[c] = run[c] = 0.f;
-      bool r = false;
-      for (int k = 0; k < S; ++k) {
-        if (k == rank) {
-#pragma unroll
-          for (int c = 0; c < kCh; ++c) into[c] = r ? run[c] : fmaf(decay_of<kFast>(sum[c]), carry[c], run[c]);
-        }
-        const bool here = sh.tile_reset[par][k];
-        r |= here;
-#pragma unroll
-        for (int c = 0; c < kCh; ++c) {
-          const float L = sh.tile_L[par][k][c][lane], E = sh.tile_E[par][k][c][lane];
-          run[c] = here ? E : fmaf(decay_of<kFast>(L), run[c], E);
-          sum[c] += L;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) carry[c] = r ? run[c] : fmaf(decay_of<kFast>(sum[c]), carry[c], run[c]);
+      for (int j = kTau - 1; j >= 0; --j) E = da[j] * (read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane) + E);
     } else {
 #pragma unroll
-      for (int c = 0; c < kCh; ++c)
-        carry[c] = all_reset ? all[c] : fmaf(decay_of<kFast>(total[c]), carry[c], all[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) e[c] = e_reset ? e[c] : fmaf(decay_of<kFast>(before[c]), into[c], e[c]);
-    // the state in front of each token, in db's place
-#pragma unroll
-    for (int j = 0; j < kTau; ++j) {
-      const bool first = w.first >> j & 1, r = reset >> j & 1;
-      const int row = first ? __shfl_sync(~0u, w.row, j) : 0;
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        const float b = db[j][c];
-        db[j][c] = !r ? h[c] : first && a.initial_state && c < mine ? a.initial_state[(size_t)row * a.D + ch + c] : 0.f;
-        h[c] = r ? b : fmaf(da[j][c], h[c], b);
+      for (int j = kTau - 1; j >= 0; --j) {
+        if (w.last >> j & 1) E = state_of(a.d_final_state, __shfl_sync(~0u, w.row, j));
+        E = w.dead >> j & 1 ? fill<N>(0.f) : da[j] * (read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane) + E);
       }
     }
-    // the gradients, right to left
+    // (a slot of the state is written again after e has come through its reader)
+    if (warp > 0) {
+      wait_or_report(&sh.state_full[warp], round & 1, &lost, a.dev_status);
+      h = sh.state[warp][lane];
+    }
+    if (warp + 1 < kWarps) {
+      sh.state[warp + 1][lane] = reset ? H : fma(ex2(L), h, H);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.state_full[warp + 1]);
+    }
+    const int order = kWarps - 1 - warp;
+    Values e = clustered ? sh.chain.together(order, round, S, rank, lane, L, E, reset_e != 0, &base, &lost, a.dev_status)
+                        : sh.chain.alone(order, round, rounds, lane, L, E, reset_e != 0, &lost, a.dev_status);
+    // the state in front of each token, in db's place; then the gradients, right to left
+    auto gradients = [&](auto is_plain) {
+      constexpr bool plain = decltype(is_plain)::value;
 #pragma unroll
-    for (int j = kTau - 1; j >= 0; --j) {
-      const bool first = w.first >> j & 1, last = w.last >> j & 1, dead = w.dead >> j & 1;
-      if (!(w.in >> j & 1)) continue;
-      const int row = first || last ? __shfl_sync(~0u, w.row, j) : 0;
-      float x[kCh], g[kCh], i[kCh], dy[kCh], ox[kCh], og[kCh], oi[kCh];
-      read_row<T, kCh>(from + Shared::kAtDy + j * Shared::kRowX, lane, dy);
-      if (kFused) {
-        read_row<T, kCh>(from + j * Shared::kRowX, lane, x);
-        read_row<G, kCh>(from + Shared::kAtG + j * Shared::kRowG, lane, g);
-        read_row<G, kCh>(from + Shared::kAtI + j * Shared::kRowG, lane, i);
-      }
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        if (last) e[c] = a.d_final_state && c < mine ? a.d_final_state[(size_t)row * a.D + ch + c] : 0.f;
-        const float delta = dead ? 0.f : dy[c] + e[c];
-        e[c] = dead ? 0.f : da[j][c] * delta;
-        if (kFused) {
-          const FusedGate<kFast> f(g[c], i[c], rate[c]);
-          const float u = f.si * x[c];
-          // where nothing decays, s = 0, what multiplies 1 / s below goes to 0 faster
-          const float dla = e[c] * (db[j][c] - (f.s > 0.f ? u * f.a / f.s : 0.f));
-          ox[c] = delta * f.s * f.si;
-          og[c] = dla * f.l * (kFast ? kLn2 : 1.f) * (1.f - f.sr);
-          oi[c] = delta * f.s * u * (1.f - f.si);
-          if (dead) ox[c] = og[c] = oi[c] = 0.f;
-          else dlam[c] += dla * f.sr;
+      for (int j = 0; j < kTau; ++j) {
+        const Values b = db[j];
+        if (!plain && (reset >> j & 1)) {
+          const int row = __shfl_sync(~0u, w.row, j);
+          db[j] = row >= 0 ? state_of(a.initial_state, row) : fill<N>(0.f);
+          h = b;
         } else {
-          ox[c] = delta;
-          og[c] = dead ? 0.f : e[c] * db[j][c];
+          db[j] = h;
+          h = fma(da[j], h, b);
         }
-        if (first && a.d_initial_state && c < mine) a.d_initial_state[(size_t)row * a.D + ch + c] = e[c];
       }
-      const size_t at = (size_t)(w0 + j) * a.D + ch;
-      write_row<T, kCh>(static_cast<T*>(a.dx) + at, ox, mine, whole_x && mine == kCh);
-      write_row<G, kCh>(static_cast<G*>(a.dg) + at, og, mine, whole_g && mine == kCh);
-      if (kFused) write_row<G, kCh>(static_cast<G*>(a.di) + at, oi, mine, whole_i && mine == kCh);
-    }
+      const size_t at = (size_t)w0 * a.D + ch;
+      T* const dx = static_cast<T*>(a.dx) + at;
+      G* const dg = static_cast<G*>(a.dg) + at;
+      G* const di = static_cast<G*>(a.di) + at;
+#pragma unroll
+      for (int j = kTau - 1; j >= 0; --j) {
+        if (!plain && !(w.in >> j & 1)) continue;
+        const bool dead = !plain && (w.dead >> j & 1);
+        Values ox, og, oi;
+        if (!plain && (w.last >> j & 1)) e = state_of(a.d_final_state, __shfl_sync(~0u, w.row, j));
+        const Values delta = read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane) + e;
+        e = da[j] * delta;
+        if (kFused) {
+          const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
+          const Values sr = sh.sigmoid[warp][0][j][lane], si = sh.sigmoid[warp][1][j][lane];
+          const Values l = rate * sr, q = each(one_minus_square, l, da[j]);
+          // where nothing decays, s = 0; what multiplies 1 / s below goes to 0 faster
+          const Values inv = each([](float v) { return v >= 1.2e-38f ? rsqrt_approx(v) : 0.f; }, q);
+          const Values ds = delta * (q * inv), u = si * x;
+          const Values dla = e * each([](float u, float a, float inv, float h) { return fmaf(-u * a, inv, h); }, u, da[j], inv, db[j]);
+          ox = ds * si;
+          og = each([](float d, float l, float s) { return d * (l * kLn2) * (1.f - s); }, dla, l, sr);
+          oi = each([](float d, float u, float s) { return d * u * (1.f - s); }, ds, u, si);
+          if (dead) ox = og = oi = fill<N>(0.f);
+          else dlam = fma(dla, sr, dlam);
+        } else {
+          ox = delta;
+          og = e * db[j];
+          if (dead) ox = og = fill<N>(0.f);
+        }
+        if (dead) e = fill<N>(0.f);
+        if (!plain && (w.first >> j & 1)) {
+          const int row = __shfl_sync(~0u, w.row, j);
+          if (a.d_initial_state) write_state(a.d_initial_state + (size_t)row * a.D + ch, e, mine);
+        }
+        write_row<kEngine>(dx + (size_t)j * a.D, ox, mine);
+        write_row<kEngine>(dg + (size_t)j * a.D, og, mine);
+        if (kFused) write_row<kEngine>(di + (size_t)j * a.D, oi, mine);
+      }
+    };
+    if (w.plain) gradients(std::true_type{});
+    else gradients(std::false_type{});
     __syncwarp();
     fetch(round + kStages);
   }
-  copies_wait<0>();
+  if (!kEngine) copies_wait<0>();
+  if (clustered) cluster_sync();   // no CTA ends while a peer's stores are on their way
   if (kFused && dlam_row) {
-#pragma unroll
-    for (int c = 0; c < kCh; ++c) sh.dlam[warp][c][lane] = dlam[c];
+    Lanes<N>(*const sums)[32] = sh.sigmoid[0][0];
+    __syncthreads();
+    sums[warp][lane] = dlam;
     __syncthreads();
     if (warp == 0) {
-#pragma unroll
-      for (int c = 0; c < kCh; ++c) {
-        float x = 0.f;
-        for (int k = 0; k < kWarps; ++k) x += sh.dlam[k][c][lane];
-        if (c < mine) dlam_row[c] = x;
-      }
+      Values x = fill<N>(0.f);
+      for (int k = 0; k < kWarps; ++k) x = x + sums[k][lane];
+      write_state(dlam_row, x, mine);
     }
   }
 }
@@ -364,41 +301,39 @@ __global__ void __launch_bounds__(1024) recurrence_dlam_kernel(RecurrenceArgs a,
 }
 
 RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
-  return recurrence_plan((long long)B * T, D, N, packed, width, kTile, kMaxCluster, 3);
+  return recurrence_plan((long long)B * T, D, N, packed, width, kTile);
 }
 
-template <typename T, typename G, bool kFused, int kCh>
+template <typename T, typename G, bool kFused, int N>
 cudaError_t launch_bwd(const RecurrenceArgs& a, float* part) {
-  const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, 32 * kCh);
-  auto* const kernel = recurrence_bwd_kernel<T, G, kFused, kCh>;
-  const size_t shared = sizeof(BwdShared<T, G, kFused, kCh>);
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-  if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {(unsigned)p.S, 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.blocks * p.parts * p.S);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = a.stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  auto whole = [&](const void* q, size_t elem) {
-    return a.D % kCh == 0 && reinterpret_cast<uintptr_t>(q) % (kCh * elem) == 0;
-  };
-  err = cudaLaunchKernelEx(&cfg, kernel, a, p.parts, copy_unit(a.x, a.x_pitch, a.D, sizeof(T)),
-                           copy_unit(a.g, a.g_pitch, a.D, sizeof(G)), copy_unit(a.i, a.i_pitch, a.D, sizeof(G)),
-                           copy_unit(a.dy, a.D, a.D, sizeof(T)), whole(a.dx, sizeof(T)), whole(a.dg, sizeof(G)),
-                           whole(a.di, sizeof(G)), part);
+  constexpr int W = 32 * N;
+  const long long tokens = (long long)a.B * a.T;
+  const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, W);
+  const size_t shared = sizeof(BwdShared<T, G, kFused, N>);
+  const int x_unit = copy_unit(a.x, a.x_pitch, a.D, sizeof(T)), g_unit = copy_unit(a.g, a.g_pitch, a.D, sizeof(G)),
+            i_unit = copy_unit(a.i, a.i_pitch, a.D, sizeof(G)), dy_unit = copy_unit(a.dy, a.D, a.D, sizeof(T));
+  auto whole = [&](const void* q, size_t elem) { return reinterpret_cast<uintptr_t>(q) % (N * elem) == 0; };
+  const bool engine = tokens > 0 && engine_rows(a.x, a.x_pitch, a.D, sizeof(T)) && engine_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
+                      (!kFused || engine_rows(a.i, a.i_pitch, a.D, sizeof(G))) && engine_rows(a.dy, a.D, a.D, sizeof(T)) &&
+                      whole(a.dx, sizeof(T)) && whole(a.dg, sizeof(G)) && whole(a.di, sizeof(G));
+  CUtensorMap mx{}, md{}, mg{}, mi{};
+  if (engine && (!rows_map(&mx, a.x, tokens, a.D, a.x_pitch, sizeof(T), W, kTau) ||
+                 !rows_map(&md, a.dy, tokens, a.D, a.D, sizeof(T), W, kTau) ||
+                 !rows_map(&mg, a.g, tokens, a.D, a.g_pitch, sizeof(G), W, kTau) ||
+                 (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau))))
+    return cudaErrorInvalidValue;
+  const cudaError_t err =
+      launch_clusters(!engine ? recurrence_bwd_kernel<T, G, kFused, N, false, true>
+                      : p.S > 1 ? recurrence_bwd_kernel<T, G, kFused, N, true, true> : recurrence_bwd_kernel<T, G, kFused, N, true, false>,
+                      p, kWarps * 32, shared, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi);
   if (err != cudaSuccess || !kFused || !part) return err;
   return launch_behind(recurrence_dlam_kernel, (a.D + 31) / 32, 1024, 0, a.stream, a, (const float*)part,
                        p.parts * p.S);
 }
 
-template <typename T, typename G, int kCh>
+template <typename T, typename G, int N>
 cudaError_t launch_bwd(const RecurrenceArgs& a, float* part) {
-  return a.lam ? launch_bwd<T, G, true, kCh>(a, part) : launch_bwd<T, G, false, kCh>(a, part);
+  return a.lam ? launch_bwd<T, G, true, N>(a, part) : launch_bwd<T, G, false, N>(a, part);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
