@@ -4,13 +4,17 @@
 //     backward, with d the gradient turned back and xh = x r:
 //     dw = sum over tokens and heads of d xh,   dx = r (d w - xh mean(d w xh)).
 //
-// A token's heads share its angles, so a warp takes a token (or a part of its heads, where tokens are
-// few), makes the sines and cosines of its own pairs once and walks the heads.  G lanes hold a head,
-// 32 / G heads pass at a time.  A lane's unit is two vectors of V values whose pairs are complete: of
-// the two halves, or, interleaved, two in a row; behind the rotated part two in a row.
+// Bound by bytes: one reading, one writing.  G lanes hold a head and walk the heads of a token (or a run of
+// them, where tokens are few), whose sines and cosines they make once; the 32 / G groups of a warp have
+// tokens of their own.  CTAs work on queries or on keys, in proportion, so that weights and their
+// gradients stay in registers.  A lane's unit is two vectors of V values whose pairs are complete: of the two
+// halves, or, interleaved, two in a row; behind the rotated part two in a row.  Lanes copy heads ahead
+// into rings of their own in shared memory (asynchronous copies, no barrier).
 //
 // Angles: phi / 2 pi as a fraction of 2^64, position * round(2^64 frac(inv_freq / 2 pi)) in integers
-// that wrap, is exact to 2^-11 of fp32's rounding for every position.
+// that wrap, is exact to 2^-11 of fp32's rounding for every position.  What is left is less than half a
+// turn: there the hardware's sine and cosine are off by 2^-21 of a unit at most, which is enough for bf16;
+// fp32 takes the full functions.
 #include "gdn_common.cuh"
 #include "gdn_launch.cuh"
 #include "gdn_qk_rotate.h"
@@ -20,22 +24,31 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kPerSm = 2;
 constexpr int kMaxParts = 1024;   // CTAs of a backward that sums weights' gradients
+constexpr int kFewItems = 8;      // a group's items below which heads are shared out further
 
 template <typename T, int V> struct alignas(V * sizeof(T)) Vec { T e[V]; };
 
-template <typename T, int V>
-__device__ __forceinline__ void load(const T* p, float (&x)[V]) {
-  const Vec<T, V> v = *reinterpret_cast<const Vec<T, V>*>(p);
-#pragma unroll
-  for (int j = 0; j < V; ++j) x[j] = (float)v.e[j];
-}
 template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float (&x)[V]) {
   Vec<T, V> v;
 #pragma unroll
   for (int j = 0; j < V; ++j) v.e[j] = (T)x[j];
   *reinterpret_cast<Vec<T, V>*>(p) = v;
+}
+
+// V values from global to shared memory, asynchronously (but for two bytes, which such copies do not have).
+template <typename T, int V>
+__device__ __forceinline__ void copy_ahead(Vec<T, V>* dst, const T* src) {
+  constexpr int kBytes = V * sizeof(T);
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+  else if constexpr (kBytes >= 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src), "n"(kBytes)
+                 : "memory");
+  else
+    *dst = *reinterpret_cast<const Vec<T, V>*>(src);
 }
 
 // What a lane holds of a head: unit u's two vectors start at o1 and o2.
@@ -68,34 +81,18 @@ __device__ __forceinline__ unsigned long long turn_rate(float f) {
   return (unsigned long long)((t - floor(t)) * 18446744073709551616.0);
 }
 
-// The angle of a position on pair j, as sine and cosine.
+// The angle of a position, as sine and cosine.
+template <bool kFast>
 __device__ __forceinline__ void angle(unsigned long long rate, int position, float* s, float* c) {
-  const unsigned long long turn = rate * (unsigned long long)(long long)position;
-  sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f, s, c);   // 2^-31: half turns
-}
-
-// Turns the pairs of a unit (back: by the negative angle).
-template <int V>
-__device__ __forceinline__ void rotate(float (&x)[V], float (&y)[V], const float (&c)[V], const float (&s)[V],
-                                       bool adjacent, float sign) {
-  if (V > 1 && adjacent) {
-#pragma unroll
-    for (int j = 0; j + 1 < V; j += 2) {
-      const float s1 = sign * s[j / 2], s2 = sign * s[V / 2 + j / 2];
-      const float u = x[j], v = x[j + 1];
-      x[j] = u * c[j / 2] - v * s1;
-      x[j + 1] = v * c[j / 2] + u * s1;
-      const float p = y[j], q = y[j + 1];
-      y[j] = p * c[V / 2 + j / 2] - q * s2;
-      y[j + 1] = q * c[V / 2 + j / 2] + p * s2;
-    }
+  const unsigned p = (unsigned)position, lo = (unsigned)rate;
+  unsigned turn = p * (unsigned)(rate >> 32) + __umulhi(p, lo);   // the product's upper half
+  if (position < 0) turn -= lo;
+  if (kFast) {
+    const float phi = (float)(int)turn * 1.4629180792671596e-9f;   // 2 pi / 2^32
+    *s = __sinf(phi);
+    *c = __cosf(phi);
   } else {
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const float u = x[j], v = y[j], w = sign * s[j];
-      x[j] = u * c[j] - v * w;
-      y[j] = v * c[j] + u * w;
-    }
+    sincospif((float)(int)turn * 4.656612873077393e-10f, s, c);    // half turns
   }
 }
 
@@ -104,35 +101,103 @@ __device__ __forceinline__ float group_sum(float x, int G) {
   return x;
 }
 
+// One side's share of a launch: CTAs [first, first + ctas), items of nh heads.
+struct SidePlan {
+  int first, ctas, splits, nh;
+};
+struct Plan {
+  int G;
+  SidePlan side[2];
+};
+
 template <typename T, int V, int NU, bool kBwd>
-__global__ void __launch_bounds__(kThreads) qk_rotate_kernel(QkRotateArgs a, int G, int splits, float* part) {
-  __shared__ float total[kBwd ? kWarps * 2 * GDN_MAX_ROTATE_DIM : 1];
+struct Ring {
+  static constexpr int kDepth = kBwd ? 4 : 6;
+  static constexpr int kVecs = NU * 2 * (kBwd ? 2 : 1);
+  Vec<T, V> slot[kWarps][kDepth][kVecs][32];
+};
+
+template <typename T, int V, int NU, bool kAdjacent, bool kBwd>
+__global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArgs a, Plan plan, float* part) {
+  constexpr bool kFast = sizeof(T) == 2;
+  constexpr bool kInVector = kAdjacent && V > 1;   // a pair's two values stand in one vector
+  using R = Ring<T, V, NU, kBwd>;
+  extern __shared__ __align__(16) char shared_bytes[];
+  R& ring = *reinterpret_cast<R*>(shared_bytes);
+  __shared__ unsigned long long rates[GDN_MAX_ROTATE_DIM / 2];
+  for (int j = threadIdx.x; j < a.R / 2; j += kThreads) rates[j] = turn_rate(a.inv_freq[j]);
+  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int sub = lane & (G - 1), hs = lane / G, heads = 32 / G;
+  const int sd = (int)blockIdx.x >= plan.side[1].first;
+  const QkSide side = sd ? a.side[1] : a.side[0];
+  const SidePlan sp = sd ? plan.side[1] : plan.side[0];
+  const int G = plan.G, sub = lane & (G - 1), hs = lane / G, groups = 32 / G;
   Unit unit[NU];
-  unsigned long long rate[NU][V];
+  float w[NU][2][V];
 #pragma unroll
   for (int m = 0; m < NU; ++m) {
     unit[m] = unit_of<V>(a, sub + G * m);
 #pragma unroll
-    for (int j = 0; j < V; ++j) rate[m][j] = unit[m].turns ? turn_rate(a.inv_freq[unit[m].pair + j]) : 0;
+    for (int j = 0; j < V; ++j) {
+      w[m][0][j] = side.w && unit[m].on ? load_elem(side.w, unit[m].o1 + j, a.w_dtype) : 1.f;
+      w[m][1][j] = side.w && unit[m].second ? load_elem(side.w, unit[m].o2 + j, a.w_dtype) : 1.f;
+    }
   }
-  const int passes[2] = {(a.side[0].H + heads - 1) / heads, (a.side[1].H + heads - 1) / heads};
-  const int all = passes[0] + passes[1];
   const float mean = a.norm == GDN_NORM_RMS ? 1.f / (float)a.K : 1.f;
-  float acc[2][NU][2][V];
-  if (kBwd) {
+  const long long tokens = (long long)a.B * a.T, items = tokens * sp.splits;
+  const long long stride = (long long)sp.ctas * kWarps * groups;
+  const long long base0 = ((long long)(blockIdx.x - sp.first) * kWarps + warp) * groups;
+  const long long turns = base0 < items ? (items - base0 + stride - 1) / stride : 0;   // items of the warp's first group
+
+  // the copies run kDepth - 1 heads ahead of the work
+  long long ahead_item = base0 + hs;
+  int ahead_h = 0, ahead_slot = 0;
+  long long ahead_left = turns * sp.nh;
+  const T* ahead_x = nullptr;
+  const T* ahead_dy = nullptr;
+  auto copy_head = [&]() {
+    if (ahead_left > 0) {
+      if (ahead_h == 0) {
+        const long long item = ahead_item < items ? ahead_item : items - 1;   // (a spare group reads the last one)
+        const long long token = sp.splits == 1 ? item : item / sp.splits;
+        const int h0 = (int)(item - token * sp.splits) * sp.nh;
+        const int b = (int)token / a.T, t = (int)token - b * a.T;
+        ahead_x = static_cast<const T*>(side.x) + b * side.sb + t * side.st + h0 * side.sh;
+        if (kBwd) ahead_dy = static_cast<const T*>(side.dy) + (token * side.H + h0) * a.K;
+      }
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+      for (int m = 0; m < NU; ++m) {
+        if (unit[m].on) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * m][lane], ahead_x + unit[m].o1);
+        if (unit[m].second) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * m + 1][lane], ahead_x + unit[m].o2);
+        if (kBwd) {
+          if (unit[m].on) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * (NU + m)][lane], ahead_dy + unit[m].o1);
+          if (unit[m].second) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * (NU + m) + 1][lane], ahead_dy + unit[m].o2);
+        }
+      }
+      ahead_x += side.sh;
+      if (kBwd) ahead_dy += a.K;
+      if (++ahead_h == sp.nh) {
+        ahead_h = 0;
+        ahead_item += stride;
+      }
+      if (++ahead_slot == R::kDepth) ahead_slot = 0;
+      --ahead_left;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int k = 0; k < R::kDepth - 1; ++k) copy_head();
+
+  float acc[NU][2][V];
 #pragma unroll
-      for (int m = 0; m < NU; ++m)
+  for (int m = 0; m < NU; ++m)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[s][m][0][j] = acc[s][m][1][j] = 0.f;
-  }
-  const long long tokens = (long long)a.B * a.T, items = tokens * splits;
-  for (long long item = (long long)blockIdx.x * kWarps + warp; item < items; item += (long long)gridDim.x * kWarps) {
-    const int token = (int)(item / splits), split = (int)(item - (long long)token * splits);
-    const int b = token / a.T, t = token - b * a.T;
+    for (int j = 0; j < V; ++j) acc[m][0][j] = acc[m][1][j] = 0.f;
+  int slot = 0;
+  for (long long n = 0; n < turns; ++n) {
+    const long long item = base0 + hs + n * stride;
+    const bool here = item < items;
+    const long long token = here ? (sp.splits == 1 ? item : item / sp.splits) : 0;
+    const int h0 = here ? (int)(item - token * sp.splits) * sp.nh : 0;
     float c[NU][V], s[NU][V];
 #pragma unroll
     for (int m = 0; m < NU; ++m)
@@ -143,127 +208,163 @@ __global__ void __launch_bounds__(kThreads) qk_rotate_kernel(QkRotateArgs a, int
         if (unit[m].turns) {
           const int pair = unit[m].pair + j;
           const int axis = (pair >= a.axis_end[0]) + (pair >= a.axis_end[1]) + (pair >= a.axis_end[2]);
-          angle(rate[m][j], a.positions ? a.positions[axis * tokens + token] : t, &s[m][j], &c[m][j]);
+          const int position = a.positions ? a.positions[axis * tokens + token] : (int)(token % a.T);
+          angle<kFast>(rates[pair], position, &s[m][j], &c[m][j]);
         }
       }
-    const int p0 = (int)((long long)all * split / splits), p1 = (int)((long long)all * (split + 1) / splits);
-#pragma unroll
-    for (int sd = 0; sd < 2; ++sd) {
-      const QkSide& side = a.side[sd];
-      const int from = sd ? max(p0 - passes[0], 0) : p0, to = sd ? p1 - passes[0] : min(p1, passes[0]);
-      if (from >= to) continue;
-      float w[NU][2][V];
+    // forward: the turn's four factors with the weights in them, y1 = r (x1 f1 - x2 f2), y2 = r (x2 f3 + x1 f4)
+    T* out = static_cast<T*>(side.out) + (token * side.H + h0) * a.K;
+    for (int h = 0; h < sp.nh; ++h, out += a.K) {
+      copy_head();
+      asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
+      float x[NU][2][V], ss = 0.f;
 #pragma unroll
       for (int m = 0; m < NU; ++m)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          w[m][0][j] = side.w && unit[m].on ? load_elem(side.w, unit[m].o1 + j, a.w_dtype) : 1.f;
-          w[m][1][j] = side.w && unit[m].second ? load_elem(side.w, unit[m].o2 + j, a.w_dtype) : 1.f;
+        for (int v = 0; v < 2; ++v) {
+          const Vec<T, V> raw = ring.slot[warp][slot][2 * m + v][lane];
+          const bool on = v ? unit[m].second : unit[m].on;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            x[m][v][j] = on ? (float)raw.e[j] : 0.f;
+            ss = fmaf(x[m][v][j], x[m][v][j], ss);
+          }
         }
-      const T* const x0 = static_cast<const T*>(side.x) + b * side.sb + t * side.st;
-      for (int p = from; p < to; ++p) {
-        const int h = p * heads + hs;
-        const bool here = h < side.H;
-        const T* const xh = x0 + h * side.sh;
-        const size_t at = ((size_t)token * side.H + h) * a.K;
-        float x[NU][2][V], d[NU][2][V], ss = 0.f;
+      const float inv = a.norm == GDN_NORM_NONE ? 1.f : rsqrtf(fmaf(group_sum(ss, G), mean, a.eps));
+      if constexpr (!kBwd) {
+#pragma unroll
+        for (int m = 0; m < NU; ++m) {
+          float y[2][V];
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[m][v][j] *= inv * w[m][v][j];
+          if (kInVector) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+              for (int j = 0; j < V; j += 2) {
+                const float cc = c[m][(v * V + j) / 2], sn = s[m][(v * V + j) / 2];
+                y[v][j] = x[m][v][j] * cc - x[m][v][j + 1] * sn;
+                y[v][j + 1] = x[m][v][j + 1] * cc + x[m][v][j] * sn;
+              }
+          } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              y[0][j] = x[m][0][j] * c[m][j] - x[m][1][j] * s[m][j];
+              y[1][j] = x[m][1][j] * c[m][j] + x[m][0][j] * s[m][j];
+            }
+          }
+          if (!unit[m].turns) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              y[0][j] = x[m][0][j];
+              y[1][j] = x[m][1][j];
+            }
+          }
+          if (here && unit[m].on) store<T, V>(out + unit[m].o1, y[0]);
+          if (here && unit[m].second) store<T, V>(out + unit[m].o2, y[1]);
+        }
+      } else {
+        float d[NU][2][V], dot = 0.f;
+#pragma unroll
+        for (int m = 0; m < NU; ++m) {
+          float r[2][V];
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const Vec<T, V> raw = ring.slot[warp][slot][2 * (NU + m) + v][lane];
+            const bool on = here && (v ? unit[m].second : unit[m].on);
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[v][j] = on ? (float)raw.e[j] : 0.f;
+          }
+          if (kInVector) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+              for (int j = 0; j < V; j += 2) {
+                const float cc = c[m][(v * V + j) / 2], sn = s[m][(v * V + j) / 2];
+                d[m][v][j] = r[v][j] * cc + r[v][j + 1] * sn;
+                d[m][v][j + 1] = r[v][j + 1] * cc - r[v][j] * sn;
+              }
+          } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              d[m][0][j] = r[0][j] * c[m][j] + r[1][j] * s[m][j];
+              d[m][1][j] = r[1][j] * c[m][j] - r[0][j] * s[m][j];
+            }
+          }
+          if (!unit[m].turns) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              d[m][0][j] = r[0][j];
+              d[m][1][j] = r[1][j];
+            }
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              x[m][v][j] *= inv;
+              if (here) acc[m][v][j] = fmaf(d[m][v][j], x[m][v][j], acc[m][v][j]);
+              d[m][v][j] *= w[m][v][j];
+              dot = fmaf(d[m][v][j], x[m][v][j], dot);
+            }
+        }
+        dot = a.norm == GDN_NORM_NONE ? 0.f : group_sum(dot, G) * mean;
 #pragma unroll
         for (int m = 0; m < NU; ++m) {
 #pragma unroll
-          for (int j = 0; j < V; ++j) x[m][0][j] = x[m][1][j] = d[m][0][j] = d[m][1][j] = 0.f;
-          if (here && unit[m].on) load<T, V>(xh + unit[m].o1, x[m][0]);
-          if (here && unit[m].second) load<T, V>(xh + unit[m].o2, x[m][1]);
-          if (kBwd) {
-            const T* const dy = static_cast<const T*>(side.dy) + at;
-            if (here && unit[m].on) load<T, V>(dy + unit[m].o1, d[m][0]);
-            if (here && unit[m].second) load<T, V>(dy + unit[m].o2, d[m][1]);
-          }
+          for (int v = 0; v < 2; ++v)
 #pragma unroll
-          for (int j = 0; j < V; ++j) ss += x[m][0][j] * x[m][0][j] + x[m][1][j] * x[m][1][j];
-        }
-        const float inv = a.norm == GDN_NORM_NONE ? 1.f : 1.f / sqrtf(group_sum(ss, G) * mean + a.eps);
-        T* const out = static_cast<T*>(side.out) + at;
-        if (!kBwd) {
-#pragma unroll
-          for (int m = 0; m < NU; ++m) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              x[m][0][j] *= inv * w[m][0][j];
-              x[m][1][j] *= inv * w[m][1][j];
-            }
-            if (unit[m].turns) rotate<V>(x[m][0], x[m][1], c[m], s[m], a.interleaved, 1.f);
-            if (here && unit[m].on) store<T, V>(out + unit[m].o1, x[m][0]);
-            if (here && unit[m].second) store<T, V>(out + unit[m].o2, x[m][1]);
-          }
-        } else {
-          float dot = 0.f;
-#pragma unroll
-          for (int m = 0; m < NU; ++m) {
-            if (unit[m].turns) rotate<V>(d[m][0], d[m][1], c[m], s[m], a.interleaved, -1.f);
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-              for (int j = 0; j < V; ++j) {
-                x[m][v][j] *= inv;
-                acc[sd][m][v][j] += d[m][v][j] * x[m][v][j];
-                d[m][v][j] *= w[m][v][j];
-                dot += d[m][v][j] * x[m][v][j];
-              }
-          }
-          dot = a.norm == GDN_NORM_NONE ? 0.f : group_sum(dot, G) * mean;
-#pragma unroll
-          for (int m = 0; m < NU; ++m) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-              for (int j = 0; j < V; ++j) d[m][v][j] = inv * (d[m][v][j] - x[m][v][j] * dot);
-            if (here && unit[m].on) store<T, V>(out + unit[m].o1, d[m][0]);
-            if (here && unit[m].second) store<T, V>(out + unit[m].o2, d[m][1]);
-          }
+            for (int j = 0; j < V; ++j)
+              d[m][v][j] = a.norm == GDN_NORM_NONE ? d[m][v][j] : inv * fmaf(-x[m][v][j], dot, d[m][v][j]);
+          if (here && unit[m].on) store<T, V>(out + unit[m].o1, d[m][0]);
+          if (here && unit[m].second) store<T, V>(out + unit[m].o2, d[m][1]);
         }
       }
+      if (++slot == R::kDepth) slot = 0;
     }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   if (!kBwd || !part) return;
-  // this CTA's sums: over the heads side by side in a warp, then over the warps in order
-#pragma unroll
-  for (int sd = 0; sd < 2; ++sd)
-#pragma unroll
-    for (int m = 0; m < NU; ++m)
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float x = acc[sd][m][v][j];
-          for (int o = 16; o >= G; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          if (hs == 0 && (v ? unit[m].second : unit[m].on))
-            total[(warp * 2 + sd) * GDN_MAX_ROTATE_DIM + (v ? unit[m].o2 : unit[m].o1) + j] = x;
-        }
+  // this CTA's sums: over the groups of a warp, then over the warps in order
   __syncthreads();
-  for (int e = threadIdx.x; e < 2 * a.K; e += kThreads) {
-    const int sd = e >= a.K, d = e - sd * a.K;
+  float(*const total)[GDN_MAX_ROTATE_DIM] = reinterpret_cast<float(*)[GDN_MAX_ROTATE_DIM]>(shared_bytes);
+  static_assert(sizeof(R) >= kWarps * GDN_MAX_ROTATE_DIM * sizeof(float) || !kBwd, "the ring holds the sums");
+#pragma unroll
+  for (int m = 0; m < NU; ++m)
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float x = acc[m][v][j];
+        for (int o = 16; o >= G; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (hs == 0 && (v ? unit[m].second : unit[m].on)) total[warp][(v ? unit[m].o2 : unit[m].o1) + j] = x;
+      }
+  __syncthreads();
+  for (int d = threadIdx.x; d < a.K; d += kThreads) {
     float x = 0.f;
-    for (int w = 0; w < kWarps; ++w) x += total[(w * 2 + sd) * GDN_MAX_ROTATE_DIM + d];
-    part[(size_t)blockIdx.x * 2 * a.K + e] = x;
+    for (int k = 0; k < kWarps; ++k) x += total[k][d];
+    part[(size_t)blockIdx.x * a.K + d] = x;
   }
 }
 
-// The weights' gradients: CTAs' parts, eight runs of them side by side, added in order.
-__global__ void __launch_bounds__(kThreads) qk_rotate_dw_kernel(QkRotateArgs a, const float* part, int parts) {
-  __shared__ float run[kWarps][32];
-  const int e = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+// The weights' gradients: CTAs' parts, 32 runs of them side by side, added in order.
+__global__ void __launch_bounds__(1024) qk_rotate_dw_kernel(QkRotateArgs a, Plan plan, const float* part) {
+  __shared__ float run[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, d = blockIdx.x * 32 + lane, sd = blockIdx.y;
+  const SidePlan& sp = plan.side[sd];
+  next_may_start();
+  wait_for_previous();
   float x = 0.f;
-  if (e < 2 * a.K) {
-    const int from = (int)((long long)parts * w / kWarps), to = (int)((long long)parts * (w + 1) / kWarps);
-    for (int p = from; p < to; ++p) x += part[(size_t)p * 2 * a.K + e];
-  }
-  run[w][threadIdx.x & 31] = x;
+  if (d < a.K)
+    for (int p = sp.ctas * w / 32; p < sp.ctas * (w + 1) / 32; ++p) x += part[(size_t)(sp.first + p) * a.K + d];
+  run[w][lane] = x;
   __syncthreads();
-  if (w > 0 || e >= 2 * a.K) return;
+  if (w > 0 || d >= a.K || !a.side[sd].dw) return;
   x = 0.f;
-  for (int i = 0; i < kWarps; ++i) x += run[i][threadIdx.x];
-  float* const dw = a.side[e >= a.K].dw;
-  if (dw) dw[e >= a.K ? e - a.K : e] = x;
+  for (int k = 0; k < 32; ++k) x += run[k][lane];
+  a.side[sd].dw[d] = x;
 }
 
 // The widest vectors that every row and pair allows.
@@ -282,28 +383,54 @@ int vector_width(const QkRotateArgs& a, bool bwd) {
   return 1;
 }
 
-struct Plan {
-  int G, splits;
-  unsigned ctas;
-};
-
+// CTAs for queries and keys in proportion to their heads (a token's angles count as one and a half), each
+// side's heads shared out until a group of lanes has some items to even the last ones out.
 Plan plan_of(const QkRotateArgs& a, int v) {
   Plan p;
   const int units = a.R / (2 * v) + (a.K - a.R + 2 * v - 1) / (2 * v);
   p.G = 1;
   while (p.G < units && p.G < 32) p.G *= 2;
-  const int heads = 32 / p.G;
-  const int all = (a.side[0].H + heads - 1) / heads + (a.side[1].H + heads - 1) / heads;
-  const long long tokens = (long long)a.B * a.T;
   const int sms = current_sm_count();
-  // a token's heads are shared out where tokens do not fill the SMs' warps
-  const long long want = (long long)(sms > 0 ? sms : 1) * 16;
-  p.splits = tokens >= want ? 1 : (int)((want + tokens - 1) / tokens);
-  if (p.splits > all) p.splits = all;
-  const long long ctas = (tokens * p.splits + kWarps - 1) / kWarps;
-  const long long most = (sms > 0 ? sms : 1) * 4 < kMaxParts ? (sms > 0 ? sms : 1) * 4 : kMaxParts;
-  p.ctas = (unsigned)(ctas < most ? ctas : most);
+  const long long tokens = (long long)a.B * a.T, per_cta = (long long)kWarps * (32 / p.G);
+  int ctas = (sms > 0 ? sms : 1) * kPerSm;
+  if (ctas > kMaxParts) ctas = kMaxParts;
+  const double q = a.side[0].H + 1.5, k = a.side[1].H + 1.5;
+  int share[2];
+  share[0] = (int)(ctas * q / (q + k) + 0.5);
+  share[0] = share[0] < 1 ? 1 : share[0] > ctas - 1 ? ctas - 1 : share[0];
+  if (share[0] < 1) share[0] = 1;
+  share[1] = ctas - share[0] < 1 ? 1 : ctas - share[0];
+  for (int i = 0; i < 2; ++i) {
+    const int H = a.side[i].H;
+    SidePlan& s = p.side[i];
+    s.splits = H;
+    for (int n = 1; n < H; ++n)
+      if (H % n == 0 && tokens * n >= kFewItems * per_cta * share[i]) {
+        s.splits = n;
+        break;
+      }
+    s.nh = H / s.splits;
+    const long long need = (tokens * s.splits + per_cta - 1) / per_cta;
+    s.ctas = (int)(need < share[i] ? need : share[i]);
+  }
+  p.side[0].first = 0;
+  p.side[1].first = p.side[0].ctas;
   return p;
+}
+
+template <typename T, int V, int NU, bool kAdjacent, bool kBwd>
+cudaError_t launch(const QkRotateArgs& a, const Plan& p, float* part) {
+  auto* const kernel = qk_rotate_kernel<T, V, NU, kAdjacent, kBwd>;
+  const size_t shared = sizeof(Ring<T, V, NU, kBwd>);
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+  if (err != cudaSuccess) return err;
+  kernel<<<p.side[0].ctas + p.side[1].ctas, kThreads, shared, a.stream>>>(a, p, part);
+  return cudaGetLastError();
+}
+
+template <typename T, int V, int NU, bool kBwd>
+cudaError_t launch(const QkRotateArgs& a, const Plan& p, float* part) {
+  return a.interleaved ? launch<T, V, NU, true, kBwd>(a, p, part) : launch<T, V, NU, false, kBwd>(a, p, part);
 }
 
 template <typename T, bool kBwd>
@@ -311,18 +438,13 @@ cudaError_t launch(const QkRotateArgs& a) {
   const int v = vector_width(a, kBwd);
   const Plan p = plan_of(a, v);
   float* const part = kBwd && (a.side[0].dw || a.side[1].dw) ? static_cast<float*>(a.workspace) : nullptr;
-  switch (v) {
-    case 8:
-      if constexpr (sizeof(T) == 2)
-        qk_rotate_kernel<T, 8, 1, kBwd><<<p.ctas, kThreads, 0, a.stream>>>(a, p.G, p.splits, part);
-      break;
-    case 4: qk_rotate_kernel<T, 4, 1, kBwd><<<p.ctas, kThreads, 0, a.stream>>>(a, p.G, p.splits, part); break;
-    case 2: qk_rotate_kernel<T, 2, 2, kBwd><<<p.ctas, kThreads, 0, a.stream>>>(a, p.G, p.splits, part); break;
-    default: qk_rotate_kernel<T, 1, 4, kBwd><<<p.ctas, kThreads, 0, a.stream>>>(a, p.G, p.splits, part);
-  }
-  const cudaError_t err = cudaGetLastError();
+  cudaError_t err;
+  if (v == 8 && sizeof(T) == 2) err = launch<T, sizeof(T) == 2 ? 8 : 4, 1, kBwd>(a, p, part);
+  else if (v == 4) err = launch<T, 4, 1, kBwd>(a, p, part);
+  else if (v == 2) err = launch<T, 2, 2, kBwd>(a, p, part);
+  else err = launch<T, 1, 4, kBwd>(a, p, part);
   if (err != cudaSuccess || !part) return err;
-  qk_rotate_dw_kernel<<<(2 * a.K + 31) / 32, kThreads, 0, a.stream>>>(a, part, (int)p.ctas);
+  qk_rotate_dw_kernel<<<dim3((a.K + 31) / 32, 2), 1024, 0, a.stream>>>(a, p, part);
   return cudaGetLastError();
 }
 
@@ -330,7 +452,7 @@ cudaError_t launch(const QkRotateArgs& a) {
 
 size_t qk_rotate_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int K, bool need_weights) {
   if (!need_weights || (long long)B * T == 0) return 0;
-  return (size_t)kMaxParts * 2 * K * sizeof(float);
+  return (size_t)kMaxParts * K * sizeof(float);
 }
 
 cudaError_t launch_qk_rotate_fwd(const QkRotateArgs& a) {
