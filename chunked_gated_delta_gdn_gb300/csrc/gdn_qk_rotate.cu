@@ -26,7 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPerSm = 2;
 constexpr int kMaxParts = 1024;   // CTAs of a backward that sums weights' gradients
-constexpr int kFewItems = 8;      // a group's items below which heads are shared out further
+constexpr double kAngles = 1.5;   // the time of a token's angles, in heads
 
 template <typename T, int V> struct alignas(V * sizeof(T)) Vec { T e[V]; };
 
@@ -192,6 +192,21 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
   for (int m = 0; m < NU; ++m)
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[m][0][j] = acc[m][1][j] = 0.f;
+  // the positions of an item's token on every axis, read an item ahead
+  int at[GDN_MAX_AXES] = {0, 0, 0, 0};
+  auto positions_of = [&](long long item) {
+    if (item >= items) return;
+    const long long token = sp.splits == 1 ? item : item / sp.splits;
+    if (!a.positions) {
+#pragma unroll
+      for (int i = 0; i < GDN_MAX_AXES; ++i) at[i] = (int)token % a.T;
+    } else {
+#pragma unroll
+      for (int i = 0; i < GDN_MAX_AXES; ++i)
+        if (i < a.num_axes) at[i] = a.positions[i * tokens + token];
+    }
+  };
+  positions_of(base0 + hs);
   int slot = 0;
   for (long long n = 0; n < turns; ++n) {
     const long long item = base0 + hs + n * stride;
@@ -207,12 +222,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
         s[m][j] = 0.f;
         if (unit[m].turns) {
           const int pair = unit[m].pair + j;
-          const int axis = (pair >= a.axis_end[0]) + (pair >= a.axis_end[1]) + (pair >= a.axis_end[2]);
-          const int position = a.positions ? a.positions[axis * tokens + token] : (int)(token % a.T);
+          int position = at[0];
+#pragma unroll
+          for (int i = 1; i < GDN_MAX_AXES; ++i) position = pair >= a.axis_end[i - 1] ? at[i] : position;
           angle<kFast>(rates[pair], position, &s[m][j], &c[m][j]);
         }
       }
-    // forward: the turn's four factors with the weights in them, y1 = r (x1 f1 - x2 f2), y2 = r (x2 f3 + x1 f4)
+    positions_of(item + stride);
     T* out = static_cast<T*>(side.out) + (token * side.H + h0) * a.K;
     for (int h = 0; h < sp.nh; ++h, out += a.K) {
       copy_head();
@@ -383,8 +399,8 @@ int vector_width(const QkRotateArgs& a, bool bwd) {
   return 1;
 }
 
-// CTAs for queries and keys in proportion to their heads (a token's angles count as one and a half), each
-// side's heads shared out until a group of lanes has some items to even the last ones out.
+// CTAs for queries and keys in proportion to their heads (a token's angles count as kAngles more); a token's
+// heads are shared out as far as the longest run of a group of lanes gets shorter by it.
 Plan plan_of(const QkRotateArgs& a, int v) {
   Plan p;
   const int units = a.R / (2 * v) + (a.K - a.R + 2 * v - 1) / (2 * v);
@@ -394,7 +410,7 @@ Plan plan_of(const QkRotateArgs& a, int v) {
   const long long tokens = (long long)a.B * a.T, per_cta = (long long)kWarps * (32 / p.G);
   int ctas = (sms > 0 ? sms : 1) * kPerSm;
   if (ctas > kMaxParts) ctas = kMaxParts;
-  const double q = a.side[0].H + 1.5, k = a.side[1].H + 1.5;
+  const double q = a.side[0].H + kAngles, k = a.side[1].H + kAngles;
   int share[2];
   share[0] = (int)(ctas * q / (q + k) + 0.5);
   share[0] = share[0] < 1 ? 1 : share[0] > ctas - 1 ? ctas - 1 : share[0];
@@ -403,12 +419,16 @@ Plan plan_of(const QkRotateArgs& a, int v) {
   for (int i = 0; i < 2; ++i) {
     const int H = a.side[i].H;
     SidePlan& s = p.side[i];
-    s.splits = H;
-    for (int n = 1; n < H; ++n)
-      if (H % n == 0 && tokens * n >= kFewItems * per_cta * share[i]) {
+    double least = 1e300;
+    for (int n = 1; n <= H; ++n) {
+      if (H % n) continue;
+      const long long turns = (tokens * n + per_cta * share[i] - 1) / (per_cta * share[i]);
+      const double time = (double)turns * (H / n + kAngles);
+      if (time < 0.99 * least) {
+        least = time;
         s.splits = n;
-        break;
       }
+    }
     s.nh = H / s.splits;
     const long long need = (tokens * s.splits + per_cta - 1) / per_cta;
     s.ctas = (int)(need < share[i] ? need : share[i]);

@@ -28,6 +28,7 @@ struct QkRotateArgs {
   float eps;
   const float* inv_freq;     // [R / 2]
   const int32_t* positions;  // [num_axes, B, T] or NULL
+  int num_axes;
   int axis_end[GDN_MAX_AXES];  // pairs below axis_end[0] turn by axis 0, below axis_end[1] by axis 1 ...
   int interleaved;
   void* workspace;

@@ -68,6 +68,7 @@ gdn_status_t prepare(gdn::QkRotateArgs* a, const void* q, const void* k, const l
   a->eps = eps;
   a->inv_freq = inv_freq;
   a->positions = positions;
+  a->num_axes = num_axes;
   a->interleaved = interleaved != 0;
   a->stream = reinterpret_cast<cudaStream_t>(stream);
   return GDN_OK;
