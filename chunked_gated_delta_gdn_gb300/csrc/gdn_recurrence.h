@@ -9,9 +9,9 @@
 
 namespace gdn {
 
-// Tokens from one saved state to the next (`carries`): the state that enters token 128 m of the flat
-// token axis, for every m.  The backward's tiles start there.
-constexpr int kRecCarry = 128;
+// Tokens from one saved state to the next (`carries`): the state that enters token 32 m of the flat
+// token axis, for every m.  The backward starts there.
+constexpr int kRecCarry = 32;
 
 struct RecurrenceArgs {
   const void* x;        // [tokens, D] io_dtype, rows x_pitch apart

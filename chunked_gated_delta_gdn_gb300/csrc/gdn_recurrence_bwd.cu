@@ -9,8 +9,8 @@
 //     dlam = sum of d(log a) sigmoid(r), times -c sigmoid(lam).
 //
 // The forward's shape from right to left, one reading of the inputs: a CTA walks tiles of kWarps windows,
-// each from the state that the forward saved in front of it.  A window hands on its effects on the state
-// (to the right, inside the tile) and on e (to the left).  The gates' sigmoids stay in shared memory for
+// with the states that the forward saved in front of every fourth one.  A window hands on its effects on
+// the state (to the right, up to the next saved one) and on e (to the left).  The gates' sigmoids stay in shared memory for
 // the second half.  Each lane sums its channels' dlam over its CTA's tokens; a second launch adds the CTAs
 // up in order.
 #include <algorithm>
@@ -24,7 +24,8 @@ constexpr int kTau = 8;
 constexpr int kWarps = 16;
 constexpr int kTile = kWarps * kTau;
 constexpr int kStages = 2;
-static_assert(kTile == kRecCarry, "a tile starts from a saved state");
+constexpr int kGroup = kRecCarry / kTau;   // windows from one saved state to the next
+static_assert(kRecCarry % kTau == 0 && kTile % kRecCarry == 0, "saved states stand in front of windows");
 
 template <typename T, typename G, bool kFused, int N>
 struct BwdShared {
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (int round = 0; round < rounds; ++round) {
     const int tile = tile_of(round), w0 = tile * kTile + warp * kTau;
     Values h = fill<N>(0.f);
-    if (warp == 0 && tile * (long long)kTile >= part.t0) h = read_state<N>(a.carries + (size_t)tile * a.D + ch, mine);
+    if (warp % kGroup == 0 && w0 >= part.t0 && w0 < part.t1) h = read_state<N>(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, mine);
     const Window w = finder.template find<kTau, true>(w0, lane);
     const unsigned reset = w.first | w.dead, reset_e = w.last | w.dead;
     if constexpr (kEngine) {
@@ -186,7 +187,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     if (w.plain) {
 #pragma unroll
-      for (int j = kTau - 1; j >= 0; --j) E = da[j] * (read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane) + E);
+      for (int j = kTau - 1; j >= 0; --j)   // (of delta; e is a of it)
+        E = fma(j + 1 < kTau ? da[j + 1] : E, E, read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane));
+      E = da[0] * E;
     } else {
 #pragma unroll
       for (int j = kTau - 1; j >= 0; --j) {
@@ -195,11 +198,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
     }
     // (a slot of the state is written again after e has come through its reader)
-    if (warp > 0) {
+    if (warp % kGroup > 0) {
       wait_or_report(&sh.state_full[warp], round & 1, &lost, a.dev_status);
       h = sh.state[warp][lane];
     }
-    if (warp + 1 < kWarps) {
+    if (warp % kGroup + 1 < kGroup) {
       sh.state[warp + 1][lane] = reset ? H : fma(ex2(L), h, H);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.state_full[warp + 1]);
@@ -238,13 +241,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
           const Values sr = sh.sigmoid[warp][0][j][lane], si = sh.sigmoid[warp][1][j][lane];
           const Values l = rate * sr, q = each(one_minus_square, l, da[j]);
-          // where nothing decays, s = 0; what multiplies 1 / s below goes to 0 faster
-          const Values inv = each([](float v) { return v >= 1.2e-38f ? rsqrt_approx(v) : 0.f; }, q);
+          // where nothing decays, s = 0; what multiplies 1 / s below is 0 then (bounded, it stays finite)
+          const Values inv = each([](float v) { return rsqrt_approx(fmaxf(v, 1.2e-38f)); }, q);
           const Values ds = delta * (q * inv), u = si * x;
           const Values dla = e * each([](float u, float a, float inv, float h) { return fmaf(-u * a, inv, h); }, u, da[j], inv, db[j]);
           ox = ds * si;
-          og = each([](float d, float l, float s) { return d * (l * kLn2) * (1.f - s); }, dla, l, sr);
-          oi = each([](float d, float u, float s) { return d * u * (1.f - s); }, ds, u, si);
+          og = each([](float d, float l, float s) { return d * fmaf(-l, s, l); }, dla, l, sr) * kLn2;
+          oi = each([](float d, float u, float s) { return d * fmaf(-u, s, u); }, ds, u, si);
           if (dead) ox = og = oi = fill<N>(0.f);
           else dlam = fma(dla, sr, dlam);
         } else {

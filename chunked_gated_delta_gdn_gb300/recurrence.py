@@ -177,13 +177,13 @@ def _backward(x, g, i, lam, c, d_y, d_final_state, initial_state, cu_seqlens, ne
     fused = lam is not None
     if d_y is None or not _fit(dev, (d_y, x.dtype, x.shape), (initial_state, torch.float32, (N, D)),
                                (d_final_state, torch.float32, (N, D)),
-                               (carries, torch.float32, (-(-B * T // 128), D))):
+                               (carries, torch.float32, (-(-B * T // 32), D))):
         _need(d_y, "d_y", x.dtype, dev, x.shape)
         for t, name in ((initial_state, "initial_state"), (d_final_state, "d_final_state")):
             if t is not None:
                 _need(t, name, torch.float32, dev, (N, D))
         if carries is not None:
-            _need(carries, "carries", torch.float32, dev, (-(-B * T // 128), D))
+            _need(carries, "carries", torch.float32, dev, (-(-B * T // 32), D))
     L = _lib.load()
     need = L.gdn_linear_recurrence_bwd_workspace_size(B, T, D, N, int(fused))
     workspace, ws_bytes = _scratch(need, "gdn_linear_recurrence_bwd", workspace, dev)

@@ -562,7 +562,7 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
  *   y           [B, T, D] io_dtype, contiguous, written completely: tokens past the last sequence
  *               get zeros.  NULL where only carries are wanted.
  *   carries     gdn_linear_recurrence_carries_size(...) bytes, or NULL: the state in front of
- *               every 128th token, which the backward starts from.
+ *               every 32nd token, which the backward starts from.
  * A cu_seqlens that is not monotone from 0 to at most T is reported as GDN_DEV_BAD_CU_SEQLENS: y
  * is zero then and no state is read or written.  A NaN or infinity reaches what follows in its
  * sequence and channel and nothing else; an infinity may arrive as a NaN.

@@ -19,6 +19,11 @@ TOL = {F32: 1e-6, BF16: 2.5e-3}
 NAN = float("nan")
 
 
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(0)
+
+
 def tol(x):
     """The tolerance of an output, of its type and count."""
     return 2.0 ** -8 + 1e-6 if x.dtype is BF16 and x.numel() < 500 else TOL[x.dtype]

@@ -21,6 +21,11 @@ TOL = {F32: 1e-5, BF16: 2.5e-3}
 NAN = float("nan")
 
 
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(0)
+
+
 def tol(x):
     """The tolerance of an output, of its type and count."""
     return 2.0 ** -8 + 1e-5 if x.dtype is BF16 and x.numel() < 500 else TOL[x.dtype]
@@ -301,9 +306,15 @@ def test_decode(n, D, fused, dtype, gdt):
     pick = lambda t: t[on].double()[:, None] if t.dim() == 2 else t.double()
     want, fin = recurrence(*(pick(t) for t in ins[:2]), *([pick(t) for t in ins[2:]] or (None, None)),
                            h0=before[idx[on].long()].double())
-    assert y is out and rel(y[on], want[:, 0]) <= tol(y[on])
-    assert not y[~on].any()
-    assert rel(cache[idx[on].long()], fin) <= 1e-6
+    # two terms, which may cancel: each is off by a few 2^-24 of itself, so the sum by 1e-6 of their sizes;
+    # the output is rounded once more
+    args64 = [pick(t) for t in ins]
+    args64[0] = args64[0].abs()
+    _, size = recurrence(*args64[:2], *(args64[2:] or (None, None)), h0=before[idx[on].long()].double().abs())
+    assert y is out and not y[~on].any()
+    assert ((cache[idx[on].long()].double() - fin).abs() <= 1e-6 * size).all()
+    half = 2.0 ** -8 if dtype is BF16 else 2.0 ** -24
+    assert ((y[on].double() - want[:, 0]).abs() <= 1e-6 * size + half * want[:, 0].abs()).all()
     rest = torch.ones(n + 3, dtype=torch.bool, device="cuda")
     rest[idx[on].long()] = False
     assert torch.equal(cache[rest], before[rest])

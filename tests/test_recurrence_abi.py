@@ -74,7 +74,7 @@ def test_recurrence_batches():
     need = lib.gdn_linear_recurrence_bwd_workspace_size(2, 16, 64, 2, 0)
     assert bwd(ws=FAKE, wsb=need - 1) == _lib.GDN_ERR_WORKSPACE
     assert bwd(ws=FAKE + 16, wsb=need) == _lib.GDN_ERR_LAYOUT
-    assert lib.gdn_linear_recurrence_carries_size(2, 65, 3) == 2 * 3 * 4
+    assert lib.gdn_linear_recurrence_carries_size(2, 65, 3) == 5 * 3 * 4
     assert lib.gdn_linear_recurrence_carries_size(2, 65, 0) == NONE
     assert lib.gdn_linear_recurrence_bwd_workspace_size(2, -1, 3, 2, 0) == NONE
 
