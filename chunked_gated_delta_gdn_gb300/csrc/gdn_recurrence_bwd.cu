@@ -10,7 +10,7 @@
 //
 // The forward's shape from right to left, one reading of the inputs: a CTA walks tiles of kWarps windows,
 // with the states that the forward saved in front of every fourth one.  A window hands on its effects on
-// the state (to the right, up to the next saved one) and on e (to the left).  The gates' sigmoids stay in shared memory for
+// the state (to the right, up to the next saved one) and on e (to the left).  The gates' sigmoids and s stay in shared memory for
 // the second half.  Each lane sums its channels' dlam over its CTA's tokens; a second launch adds the CTAs
 // up in order.
 #include <algorithm>
@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
   }
   const Values rate = each([&](float lam) { return gate_rate(a.c, lam); }, read_state<N>(kFused ? a.lam + ch : nullptr, mine));
+  const Values rate_e = rate * kLn2;   // of the natural logarithm
   Values dlam = fill<N>(0.f);
   auto state_of = [&](const float* states, int row) {   // of a sequence
     return read_state<N>(states ? states + (size_t)row * a.D + ch : nullptr, mine);
@@ -149,7 +150,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       copies_wait<kStages - 1>();
       __syncwarp();
     }
-    const char* const from = sh.ring[round % kStages][warp];
+    char* const from = sh.ring[round % kStages][warp];
+    // s of a token, for the second half, where its r (and i) were: each lane's values take the place of its own
+    auto keep = [&](int j, const Values& root) {
+      float* const at = reinterpret_cast<float*>(from + Shared::kAtG + j * Shared::kRowG) + lane;
+      at[0] = root.v[0];
+      if constexpr (N == 2) at[(Shared::kAtI - Shared::kAtG) / 4] = root.v[1];
+    };
+    auto kept = [&](int j) {
+      const float* const at = reinterpret_cast<const float*>(from + Shared::kAtG + j * Shared::kRowG) + lane;
+      Values root;
+      root.v[0] = at[0];
+      if constexpr (N == 2) root.v[1] = at[(Shared::kAtI - Shared::kAtG) / 4];
+      return root;
+    };
     // a and b of the window's tokens, and what they do together
     Values da[kTau], db[kTau], L = fill<N>(0.f), H = fill<N>(0.f), E = fill<N>(0.f);
 #pragma unroll
@@ -164,7 +178,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         sh.sigmoid[warp][1][j][lane] = si;
         l = rate * sr;
         da[j] = ex2(l);
-        db[j] = each([](float l, float a) { return sqrt_approx(one_minus_square(l, a)); }, l, da[j]) * si * x;
+        const Values root = each([](float l, float a) { return sqrt_approx(one_minus_square(l, a)); }, l, da[j]);
+        keep(j, root);
+        db[j] = root * si * x;
       } else {
         l = g * kLog2e;
         da[j] = ex2(l);
@@ -240,13 +256,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         if (kFused) {
           const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
           const Values sr = sh.sigmoid[warp][0][j][lane], si = sh.sigmoid[warp][1][j][lane];
-          const Values l = rate * sr, q = each(one_minus_square, l, da[j]);
           // where nothing decays, s = 0; what multiplies 1 / s below is 0 then (bounded, it stays finite)
-          const Values inv = each([](float v) { return rsqrt_approx(fmaxf(v, 1.2e-38f)); }, q);
-          const Values ds = delta * (q * inv), u = si * x;
+          const Values root = kept(j), inv = each([](float v) { return rcp(fmaxf(v, 1e-19f)); }, root);
+          const Values la = rate_e * sr, ds = delta * root, u = si * x;
           const Values dla = e * each([](float u, float a, float inv, float h) { return fmaf(-u * a, inv, h); }, u, da[j], inv, db[j]);
           ox = ds * si;
-          og = each([](float d, float l, float s) { return d * fmaf(-l, s, l); }, dla, l, sr) * kLn2;
+          og = each([](float d, float l, float s) { return d * fmaf(-l, s, l); }, dla, la, sr);
           oi = each([](float d, float u, float s) { return d * fmaf(-u, s, u); }, ds, u, si);
           if (dead) ox = og = oi = fill<N>(0.f);
           else dlam = fma(dla, sr, dlam);
