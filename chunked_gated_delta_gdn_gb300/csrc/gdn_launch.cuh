@@ -10,6 +10,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <utility>
 
 #include "gdn_internal.h"
@@ -28,6 +29,20 @@ inline int current_sm_count() {
     return 0;
   }
   return device_sm_count(dev);
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory, which it is told once for every device.
+template <auto kernel>
+cudaError_t allow_shared(size_t bytes) {
+  static std::atomic<unsigned long long> told{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (bit && (told.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (err == cudaSuccess) told.fetch_or(bit, std::memory_order_relaxed);
+  return err;
 }
 
 template <typename... Params, typename... Args>

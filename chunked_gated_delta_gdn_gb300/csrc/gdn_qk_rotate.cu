@@ -440,9 +440,9 @@ Plan plan_of(const QkRotateArgs& a, int v) {
 
 template <typename T, int V, int NU, bool kAdjacent, bool kBwd>
 cudaError_t launch(const QkRotateArgs& a, const Plan& p, float* part) {
-  auto* const kernel = qk_rotate_kernel<T, V, NU, kAdjacent, kBwd>;
+  constexpr auto kernel = qk_rotate_kernel<T, V, NU, kAdjacent, kBwd>;
   const size_t shared = sizeof(Ring<T, V, NU, kBwd>);
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+  const cudaError_t err = allow_shared<kernel>(shared);
   if (err != cudaSuccess) return err;
   kernel<<<p.side[0].ctas + p.side[1].ctas, kThreads, shared, a.stream>>>(a, p, part);
   return cudaGetLastError();

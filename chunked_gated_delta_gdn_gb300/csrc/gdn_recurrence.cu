@@ -15,35 +15,35 @@ namespace gdn {
 namespace {
 
 constexpr int kTau = 16;
-constexpr int kWarps = 16;
-constexpr int kTile = kWarps * kTau;
+constexpr int kTile = 16 * kTau;   // of a CTA alone
 constexpr int kStages = 2;
+constexpr int kMaxCluster = 8;
+template <int kWarps, int N> using Together = TogetherOf<kWarps, N, kMaxCluster>;
 
-template <typename T, typename G, bool kFused, int N>
+template <typename T, typename G, bool kFused, int N, int kWarps, template <int, int> class Links>
 struct FwdShared {
   static constexpr int W = 32 * N;
   static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
   static constexpr int kAtG = kTau * kRowX, kAtI = kAtG + kTau * kRowG;
   static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
-  Chain<kWarps, N> chain;
+  Links<kWarps, N> links;
   uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  kCluster: S may be above 1.
-template <typename T, typename G, bool kFused, int N, bool kEngine, bool kCluster>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  Links: Alone (S = 1) or Together.
+template <typename T, typename G, bool kFused, int N, bool kEngine, int kWarps, template <int, int> class Links>
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     recurrence_fwd_kernel(RecurrenceArgs a, int parts, int S, int x_unit, int g_unit, int i_unit,
                           const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
-  using Shared = FwdShared<T, G, kFused, N>;
+  using Shared = FwdShared<T, G, kFused, N, kWarps, Links>;
   using Values = Lanes<N>;
-  constexpr int W = Shared::W;
+  constexpr int W = Shared::W, kTile = kWarps * kTau;
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const bool clustered = kCluster && S > 1;
-  const int rank = clustered ? cluster_rank() : 0;
+  const int rank = Links<kWarps, N>::rank();
   const int part_index = blockIdx.x / S % parts, block = blockIdx.x / S / parts;
   const int ch = block * W + lane * N;   // this lane's first channel
   const int mine = max(0, min(N, a.D - ch));
@@ -106,10 +106,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   };
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages * kWarps; ++k) mbar_init(&sh.arrived[0][k], 1);
-    sh.chain.init();
+    sh.links.init();
   }
-  if (clustered) cluster_sync();   // (the peers' shared memory is there once they run)
-  else __syncthreads();
+  sh.links.start();
 #pragma unroll
   for (int k = 0; k < kStages; ++k) fetch(k);
 
@@ -163,8 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
       }
     }
-    Values h = clustered ? sh.chain.together(warp, round, S, rank, lane, L, H, reset != 0, &base, &lost, a.dev_status)
-                        : sh.chain.alone(warp, round, rounds, lane, L, H, reset != 0, &lost, a.dev_status);
+    Values h = sh.links.hand_over(warp, round, rounds, S, rank, lane, L, H, reset != 0, &base, &lost, a.dev_status);
     // the window's tokens from the state in front of it
     if (a.carries && w0 % kRecCarry == 0 && (w.in & 1)) write_state(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, h, mine);
     T* const y = static_cast<T*>(a.y) + (size_t)w0 * a.D + ch;
@@ -187,30 +185,35 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
   }
   if (!kEngine) copies_wait<0>();
-  if (clustered) cluster_sync();   // no CTA ends while a peer's stores are on their way
+  sh.links.finish();
+}
+
+template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
+cudaError_t launch_fwd(const RecurrencePlan& p, cudaStream_t stream, const Args&... args) {
+  if (p.S > 1)
+    return launch_clusters<recurrence_fwd_kernel<T, G, kFused, N, kEngine, 8, Together>>(p, 256,
+                           sizeof(FwdShared<T, G, kFused, N, 8, Together>), stream, args...);
+  return launch_clusters<recurrence_fwd_kernel<T, G, kFused, N, kEngine, 16, Alone>>(p, 512,
+                         sizeof(FwdShared<T, G, kFused, N, 16, Alone>), stream, args...);
 }
 
 template <typename T, typename G, bool kFused, int N>
 cudaError_t launch_fwd(const RecurrenceArgs& a) {
   constexpr int W = 32 * N;
   const long long tokens = (long long)a.B * a.T;
-  const RecurrencePlan p = recurrence_plan(tokens, a.D, a.num_seqs, a.cu_seqlens != nullptr, W, kTile);
-  const size_t shared = sizeof(FwdShared<T, G, kFused, N>);
+  const RecurrencePlan p = recurrence_plan(tokens, a.D, a.num_seqs, a.cu_seqlens != nullptr, W, kTile, kMaxCluster);
   const int x_unit = copy_unit(a.x, a.x_pitch, a.D, sizeof(T)), g_unit = copy_unit(a.g, a.g_pitch, a.D, sizeof(G)),
             i_unit = copy_unit(a.i, a.i_pitch, a.D, sizeof(G));
   CUtensorMap mx{}, mg{}, mi{};
   const bool engine = tokens > 0 && engine_rows(a.x, a.x_pitch, a.D, sizeof(T)) && engine_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
                       (!kFused || engine_rows(a.i, a.i_pitch, a.D, sizeof(G))) &&
                       reinterpret_cast<uintptr_t>(a.y) % (N * sizeof(T)) == 0;
-  if (!engine)
-    return launch_clusters(recurrence_fwd_kernel<T, G, kFused, N, false, true>, p, kWarps * 32, shared, a.stream, a, p.parts,
-                           p.S, x_unit, g_unit, i_unit, mx, mg, mi);
+  if (!engine) return launch_fwd<T, G, kFused, N, false>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, mx, mg, mi);
   if (!rows_map(&mx, a.x, tokens, a.D, a.x_pitch, sizeof(T), W, kTau) ||
       !rows_map(&mg, a.g, tokens, a.D, a.g_pitch, sizeof(G), W, kTau) ||
       (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau)))
     return cudaErrorInvalidValue;
-  return launch_clusters(p.S > 1 ? recurrence_fwd_kernel<T, G, kFused, N, true, true> : recurrence_fwd_kernel<T, G, kFused, N, true, false>,
-                         p, kWarps * 32, shared, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, mx, mg, mi);
+  return launch_fwd<T, G, kFused, N, true>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, mx, mg, mi);
 }
 
 template <typename T, typename G, int N>

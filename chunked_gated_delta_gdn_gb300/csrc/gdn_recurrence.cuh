@@ -10,7 +10,8 @@
 //
 // A window's warp knows L and H without its neighbours.  It then gets what is in front of it from the
 // warp of the window before, passes on what is behind it, and walks its tokens: no barrier of the
-// CTA, a chain of short hand-overs through shared memory that runs ahead of the walking.
+// CTA, a chain of short hand-overs through shared memory that runs ahead of the walking.  Where channels
+// and sequences are too few for the SMs, clusters of CTAs share a chain's tokens.
 #pragma once
 
 #include <algorithm>
@@ -352,105 +353,46 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
-constexpr int kMaxCluster = 8;
-constexpr float kReset = __builtin_huge_valf();   // in L's place: "reset"
-
-// What a CTA's warps hand to one another, and the CTAs of a cluster.
-//
-// Alone, windows stand in one chain: `front` goes from warp to warp and from the last one to the first
-// one's next round.  In a cluster the chain starts anew in every tile, from nothing; its end, the
-// tile's (L, H), goes to every CTA's box by asynchronous stores that the receiver's barrier counts (no
-// fence waits for the outputs on their way to memory).  Every warp joins the round's tiles for itself:
-// the state in front of its own CTA's tile and, behind them all, the next round's.
-//
-// A slot is written again one round later, by a warp that has had its own message of that round: for
-// that, the ring of messages (alone) or the round's boxes (which have passed through every warp) have
-// gone round since the slot was read.  Boxes stand in two sets in turn: a peer sends the round after the
-// next one only after it has had the next one's, which this CTA's warps sent on after reading.
+// A CTA alone: its windows stand in one chain, `front` goes from warp to warp and from the last one to the
+// first one's next round.  A slot is written again one round later, by a warp that has had its own
+// message of that round, for which the ring of messages has gone round since the slot was read.
 template <int kWarps, int N>
-struct Chain {
+struct Alone {
+  static constexpr int kPerSm = 16 / kWarps;
   Front<N> slot[kWarps][32];
-  struct alignas(8 * N) Box { Lanes<N> L, H; } box[2][kMaxCluster][32];
   alignas(8) uint64_t full[kWarps];
-  uint64_t boxes[2];
 
   __device__ __forceinline__ void init() {   // one thread; a barrier follows
     for (int k = 0; k < kWarps; ++k) mbar_init(&full[k], 1);
-    mbar_init(&boxes[0], 1);
-    mbar_init(&boxes[1], 1);
     fence_mbar_init();
   }
+  __device__ __forceinline__ void start() { __syncthreads(); }
+  __device__ __forceinline__ void finish() {}
+  static __device__ __forceinline__ int rank() { return 0; }
 
   // The state in front of this warp's window (L, H), after handing on what is behind it.  `order`: the
-  // window's place in its tile.
-  __device__ __forceinline__ Lanes<N> alone(int order, int round, int rounds, int lane, const Lanes<N>& L,
-                                            const Lanes<N>& H, bool reset, bool* lost, int* dev_status) {
+  // window's place in its tile; `base`: not used.
+  __device__ __forceinline__ Lanes<N> hand_over(int order, int round, int rounds, int, int, int lane, const Lanes<N>& L,
+                                                const Lanes<N>& H, bool reset, Lanes<N>*, bool* lost, int* dev_status) {
     Front<N> f{fill<N>(0.f), fill<N>(0.f), fill<N>(0.f)};
+    const Lanes<N> A = ex2(L);   // (the way from message to message is what the chain's speed depends on)
     if (order > 0 || round > 0) {
       wait_or_report(&full[order], (round - (order == 0)) & 1, lost, dev_status);
       f = slot[order][lane];
     }
-    const Lanes<N> h = f.value();
-    f.H = fma(ex2(L), f.H, H);
-    f.L = f.L + L;
+    Front<N> behind{f.base, f.L + L, fma(A, f.H, H)};
     if (reset) {
-      f.H = H;
-      f.L = f.base = fill<N>(0.f);
+      behind.H = H;
+      behind.L = behind.base = fill<N>(0.f);
     }
     if (order + 1 < kWarps) {
-      send(order + 1, lane, f);
+      send(order + 1, lane, behind);
     } else if (round + 1 < rounds) {
-      f.base = f.value();
-      f.L = f.H = fill<N>(0.f);
-      send(0, lane, f);
+      behind.base = behind.value();
+      behind.L = behind.H = fill<N>(0.f);
+      send(0, lane, behind);
     }
-    return h;
-  }
-
-  // The same in a cluster of S; `base`: the state in front of the round's tiles (kept from call to call, zero
-  // at first).
-  __device__ __forceinline__ Lanes<N> together(int order, int round, int S, int rank, int lane, const Lanes<N>& L,
-                                               const Lanes<N>& H, bool reset, Lanes<N>* base, bool* lost,
-                                               int* dev_status) {
-    Front<N> f{fill<N>(0.f), fill<N>(0.f), fill<N>(0.f)};
-    if (order > 0) {
-      wait_or_report(&full[order], round & 1, lost, dev_status);
-      f = slot[order][lane];
-    }
-    const Front<N> mine = f;
-    f.L = reset ? fill<N>(kReset) : sum(f.L, L);
-    f.H = reset ? H : fma(ex2(L), f.H, H);
-    const int set = round & 1;
-    if (order + 1 < kWarps) {
-      send(order + 1, lane, f);
-    } else {
-      if (lane == 0) mbar_arrive_expect_tx(&boxes[set], S * 32 * sizeof(Box));
-      const unsigned at = smem_u32(&box[set][rank][lane]), to = smem_u32(&boxes[set]);
-      for (int k = 0; k < S; ++k) {
-        unsigned peer_at, peer_bar;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_at) : "r"(at), "r"(k));
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_bar) : "r"(to), "r"(k));
-        if constexpr (N == 2)
-          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                           peer_at),
-                       "f"(f.L.v[0]), "f"(f.L.v[1]), "f"(f.H.v[0]), "f"(f.H.v[1]), "r"(peer_bar)
-                       : "memory");
-        else
-          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(peer_at),
-                       "f"(f.L.v[0]), "f"(f.H.v[0]), "r"(peer_bar)
-                       : "memory");
-      }
-    }
-    wait_or_report(&boxes[set], round >> 1 & 1, lost, dev_status);
-    Lanes<N> into = *base, run = fill<N>(0.f), all = fill<N>(0.f);
-    for (int k = 0; k < S; ++k) {
-      if (k == rank) into = joined(all, *base, run);
-      const Box o = box[set][k][lane];
-      run = joined(o.L, run, o.H);
-      all = sum(all, o.L);
-    }
-    *base = joined(all, *base, run);
-    return joined(mine.L, into, mine.H);
+    return f.value();
   }
 
  private:
@@ -459,11 +401,87 @@ struct Chain {
     __syncwarp();
     if (lane == 0) mbar_arrive(&full[to]);
   }
-  static __device__ __forceinline__ Lanes<N> sum(const Lanes<N>& a, const Lanes<N>& b) {
-    return each([](float x, float y) { return x == kReset || y == kReset ? kReset : x + y; }, a, b);
+};
+
+constexpr float kReset = __builtin_huge_valf();   // in L's place: "reset"
+
+// CTAs of a cluster (kMost at most), a tile each a round.  Every warp publishes its window's (L, H); with all of them there
+// each joins those in front of its own, and the last one sends the tile's to every CTA's box by
+// asynchronous stores that the receiver's barrier counts (no fence waits for the outputs on their way to
+// memory).  Every warp joins the round's tiles for itself: the state in front of its own CTA's tile
+// and, behind them all, the next round's.  Two of these CTAs an SM: one waits while the other works.
+//
+// Windows and boxes stand in two sets in turn.  A window's place is written again two rounds later, after
+// every warp has published in between and so has read it; a peer sends into a box again only after it
+// has had the round between, which this CTA's last warp sent after all its warps had published, and so
+// had left the box.
+template <int kWarps, int N, int kMost>
+struct TogetherOf {
+  static constexpr int kPerSm = 16 / kWarps;
+  struct alignas(8 * N) Step { Lanes<N> L, H; } window[2][kWarps][32], box[2][kMost][32];
+  alignas(8) uint64_t published[2];
+  uint64_t boxes[2];
+
+  __device__ __forceinline__ void init() {   // one thread; a barrier follows
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(&published[k], kWarps);
+      mbar_init(&boxes[k], 1);
+    }
+    fence_mbar_init();
   }
+  __device__ __forceinline__ void start() { cluster_sync(); }    // the peers' shared memory is there once they run
+  __device__ __forceinline__ void finish() { cluster_sync(); }   // no CTA ends while a peer's stores are on their way
+  static __device__ __forceinline__ int rank() { return cluster_rank(); }
+
+  // As Alone's; `base`: the state in front of the round's tiles (kept from call to call, zero at first).
+  __device__ __forceinline__ Lanes<N> hand_over(int order, int round, int, int S, int rank, int lane, const Lanes<N>& L,
+                                                const Lanes<N>& H, bool reset, Lanes<N>* base, bool* lost,
+                                                int* dev_status) {
+    const int set = round & 1;
+    window[set][order][lane] = Step{reset ? fill<N>(kReset) : L, H};
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&published[set]);
+    wait_or_report(&published[set], round >> 1 & 1, lost, dev_status);
+    Step front{fill<N>(0.f), fill<N>(0.f)};
+    for (int k = 0; k < order; ++k) join(&front, window[set][k][lane]);
+    if (order + 1 == kWarps) {
+      Step tile = front;
+      join(&tile, window[set][order][lane]);
+      if (lane == 0) mbar_arrive_expect_tx(&boxes[set], S * 32 * sizeof(Step));
+      const unsigned at = smem_u32(&box[set][rank][lane]), to = smem_u32(&boxes[set]);
+      for (int k = 0; k < S; ++k) {
+        unsigned peer_at, peer_bar;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_at) : "r"(at), "r"(k));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_bar) : "r"(to), "r"(k));
+        if constexpr (N == 2)
+          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                           peer_at),
+                       "f"(tile.L.v[0]), "f"(tile.L.v[1]), "f"(tile.H.v[0]), "f"(tile.H.v[1]), "r"(peer_bar)
+                       : "memory");
+        else
+          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(peer_at),
+                       "f"(tile.L.v[0]), "f"(tile.H.v[0]), "r"(peer_bar)
+                       : "memory");
+      }
+    }
+    wait_or_report(&boxes[set], round >> 1 & 1, lost, dev_status);
+    Lanes<N> into = *base;
+    Step all{fill<N>(0.f), fill<N>(0.f)};
+    for (int k = 0; k < S; ++k) {
+      if (k == rank) into = joined(all.L, *base, all.H);
+      join(&all, box[set][k][lane]);
+    }
+    *base = joined(all.L, *base, all.H);
+    return joined(front.L, into, front.H);
+  }
+
+ private:
   static __device__ __forceinline__ Lanes<N> joined(const Lanes<N>& L, const Lanes<N>& base, const Lanes<N>& H) {
     return each([](float l, float x, float h) { return l == kReset ? h : fmaf(ex2(l), x, h); }, L, base, H);
+  }
+  static __device__ __forceinline__ void join(Step* f, const Step& o) {
+    f->H = joined(o.L, f->H, o.H);
+    f->L = each([](float x, float y) { return x == kReset || y == kReset ? kReset : x + y; }, f->L, o.L);
   }
 };
 
@@ -474,24 +492,27 @@ struct RecurrencePlan {
   int blocks, parts, S;
 };
 
-// For kernels of `width` channels and `tile` tokens a CTA, one CTA an SM.  The plan with the least time: waves
-// of CTAs, each as many rounds as its longest part has (a round more than that to start), a round of a
-// cluster counting as two of a CTA alone (1 x 32768 x 2048: 6.4 us against 2.8).  Parts are whole
-// sequences: of equal ones the longest part is known, of packed ones (whose lengths the host does not
-// know) it is taken to be longer than the mean by half a mean sequence.
-inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile) {
-  const long long slots = std::max(1, current_sm_count());
+// For kernels of `width` channels, a tile of `tile` tokens for a CTA alone, half of that in clusters of `most` CTAs at
+// most (two of which go on an SM).  The plan with the least time: waves of CTAs, each as many rounds as its
+// longest part has (a round more than that to start).  A cluster's round, half as many tokens, takes as
+// long as a round of a CTA alone (16 warps and 8 keep an SM's issue slots busy for 3 us, 2 x 8192 and
+// 1 x 32768 x 2048 bf16), and half as long again where two CTAs share the SM.  Parts are whole sequences: of
+// equal ones the longest part is known, of packed ones (whose lengths the host does not know) it is
+// taken to be longer than the mean by half a mean sequence.
+inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile, int most) {
+  const long long sms = std::max(1, current_sm_count());
   RecurrencePlan best{(D + width - 1) / width, 1, 1};
   double least = 1e300;
   N = std::max(1, N);
-  const int most = (int)std::min<long long>({(long long)N, 64, std::max(1LL, 4 * slots / best.blocks), std::max(1LL, tokens / tile)});
-  for (int parts = 1; parts <= most; ++parts) {
+  const int most_parts =
+      (int)std::min<long long>({(long long)N, 64, std::max(1LL, 4 * sms / best.blocks), std::max(1LL, tokens / tile)});
+  for (int parts = 1; parts <= most_parts; parts += parts < 8 ? 1 : parts / 4) {
     const double each = packed ? (double)tokens / parts + (parts > 1 ? 0.5 * (double)tokens / N : 0.)
                                : (double)tokens / N * ((N + parts - 1) / parts);
-    for (int S = 1; S <= kMaxCluster; ++S) {
-      const long long rounds = (long long)(each / ((double)tile * S)) + 1;
-      const long long waves = ((long long)best.blocks * parts * S + slots - 1) / slots;
-      const double time = (double)waves * (double)(rounds + 1) * (S > 1 ? 2. : 1.);
+    for (int S = 1; S <= most; ++S) {
+      const long long ctas = (long long)best.blocks * parts * S, places = S > 1 ? 2 * sms : sms;
+      const long long rounds = (long long)(each / ((double)(S > 1 ? tile / 2 : tile) * S)) + 1;
+      const double time = (double)((ctas + places - 1) / places) * (double)(rounds + 1) * (S > 1 && ctas > sms ? 1.5 : 1.);
       if (time < 0.98 * least) {
         least = time;
         best.parts = parts;
@@ -532,10 +553,10 @@ inline bool rows_map(CUtensorMap* m, const void* p, long long tokens, int D, lon
 }
 
 // A launch of clusters of S CTAs with `shared` bytes of shared memory each.
-template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(Params...), const RecurrencePlan& p, int threads, size_t shared,
+template <auto kernel, typename... Args>
+cudaError_t launch_clusters(const RecurrencePlan& p, int threads, size_t shared,
                             cudaStream_t stream, Args&&... args) {
-  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+  const cudaError_t err = allow_shared<kernel>(shared);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;

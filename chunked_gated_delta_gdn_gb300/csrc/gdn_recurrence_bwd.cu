@@ -21,13 +21,14 @@ namespace gdn {
 namespace {
 
 constexpr int kTau = 8;
-constexpr int kWarps = 16;
-constexpr int kTile = kWarps * kTau;
+constexpr int kTile = 16 * kTau;   // of a CTA alone
 constexpr int kStages = 2;
+constexpr int kMaxCluster = 6;   // (more, and two CTAs would not fit an SM)
+template <int kWarps, int N> using Together = TogetherOf<kWarps, N, kMaxCluster>;
 constexpr int kGroup = kRecCarry / kTau;   // windows from one saved state to the next
-static_assert(kRecCarry % kTau == 0 && kTile % kRecCarry == 0, "saved states stand in front of windows");
+static_assert(kRecCarry % kTau == 0 && kTile / 2 % kRecCarry == 0, "saved states stand in front of windows");
 
-template <typename T, typename G, bool kFused, int N>
+template <typename T, typename G, bool kFused, int N, int kWarps, template <int, int> class Links>
 struct BwdShared {
   static constexpr int W = 32 * N;
   static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
@@ -35,27 +36,26 @@ struct BwdShared {
   static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
   Lanes<N> sigmoid[kFused ? kWarps : 1][2][kFused ? kTau : 1][32];   // (dlam's sums in the end)
-  Chain<kWarps, N> chain;              // of e, right to left
+  Links<kWarps, N> links;              // of e, right to left
   Lanes<N> state[kWarps][32];          // the state in front of each window, left to right in a tile
   uint64_t state_full[kWarps];
   uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  kCluster: S may be above 1.
-template <typename T, typename G, bool kFused, int N, bool kEngine, bool kCluster>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  Links: Alone (S = 1) or Together.
+template <typename T, typename G, bool kFused, int N, bool kEngine, int kWarps, template <int, int> class Links>
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     recurrence_bwd_kernel(RecurrenceArgs a, int parts, int S, int x_unit, int g_unit, int i_unit, int dy_unit,
                           float* dlam_part, const __grid_constant__ CUtensorMap x_map,
                           const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
-  using Shared = BwdShared<T, G, kFused, N>;
+  using Shared = BwdShared<T, G, kFused, N, kWarps, Links>;
   using Values = Lanes<N>;
-  constexpr int W = Shared::W;
+  constexpr int W = Shared::W, kTile = kWarps * kTau;
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const bool clustered = kCluster && S > 1;
-  const int rank = clustered ? cluster_rank() : 0;
+  const int rank = Links<kWarps, N>::rank();
   const int part_index = blockIdx.x / S % parts, block = blockIdx.x / S / parts;
   const int ch = block * W + lane * N;
   const int mine = max(0, min(N, a.D - ch));
@@ -129,10 +129,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages * kWarps; ++k) mbar_init(&sh.arrived[0][k], 1);
     for (int k = 0; k < kWarps; ++k) mbar_init(&sh.state_full[k], 1);
-    sh.chain.init();
+    sh.links.init();
   }
-  if (clustered) cluster_sync();   // (the peers' shared memory is there once they run)
-  else __syncthreads();
+  sh.links.start();
 #pragma unroll
   for (int k = 0; k < kStages; ++k) fetch(k);
 
@@ -224,8 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (lane == 0) mbar_arrive(&sh.state_full[warp + 1]);
     }
     const int order = kWarps - 1 - warp;
-    Values e = clustered ? sh.chain.together(order, round, S, rank, lane, L, E, reset_e != 0, &base, &lost, a.dev_status)
-                        : sh.chain.alone(order, round, rounds, lane, L, E, reset_e != 0, &lost, a.dev_status);
+    Values e = sh.links.hand_over(order, round, rounds, S, rank, lane, L, E, reset_e != 0, &base, &lost, a.dev_status);
     // the state in front of each token, in db's place; then the gradients, right to left
     auto gradients = [&](auto is_plain) {
       constexpr bool plain = decltype(is_plain)::value;
@@ -286,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     fetch(round + kStages);
   }
   if (!kEngine) copies_wait<0>();
-  if (clustered) cluster_sync();   // no CTA ends while a peer's stores are on their way
+  sh.links.finish();
   if (kFused && dlam_row) {
     Lanes<N>(*const sums)[32] = sh.sigmoid[0][0];
     __syncthreads();
@@ -319,7 +317,16 @@ __global__ void __launch_bounds__(1024) recurrence_dlam_kernel(RecurrenceArgs a,
 }
 
 RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
-  return recurrence_plan((long long)B * T, D, N, packed, width, kTile);
+  return recurrence_plan((long long)B * T, D, N, packed, width, kTile, kMaxCluster);
+}
+
+template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
+cudaError_t launch_bwd(const RecurrencePlan& p, cudaStream_t stream, const Args&... args) {
+  if (p.S > 1)
+    return launch_clusters<recurrence_bwd_kernel<T, G, kFused, N, kEngine, 8, Together>>(p, 256,
+                           sizeof(BwdShared<T, G, kFused, N, 8, Together>), stream, args...);
+  return launch_clusters<recurrence_bwd_kernel<T, G, kFused, N, kEngine, 16, Alone>>(p, 512,
+                         sizeof(BwdShared<T, G, kFused, N, 16, Alone>), stream, args...);
 }
 
 template <typename T, typename G, bool kFused, int N>
@@ -327,7 +334,6 @@ cudaError_t launch_bwd(const RecurrenceArgs& a, float* part) {
   constexpr int W = 32 * N;
   const long long tokens = (long long)a.B * a.T;
   const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, W);
-  const size_t shared = sizeof(BwdShared<T, G, kFused, N>);
   const int x_unit = copy_unit(a.x, a.x_pitch, a.D, sizeof(T)), g_unit = copy_unit(a.g, a.g_pitch, a.D, sizeof(G)),
             i_unit = copy_unit(a.i, a.i_pitch, a.D, sizeof(G)), dy_unit = copy_unit(a.dy, a.D, a.D, sizeof(T));
   auto whole = [&](const void* q, size_t elem) { return reinterpret_cast<uintptr_t>(q) % (N * elem) == 0; };
@@ -341,9 +347,8 @@ cudaError_t launch_bwd(const RecurrenceArgs& a, float* part) {
                  (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau))))
     return cudaErrorInvalidValue;
   const cudaError_t err =
-      launch_clusters(!engine ? recurrence_bwd_kernel<T, G, kFused, N, false, true>
-                      : p.S > 1 ? recurrence_bwd_kernel<T, G, kFused, N, true, true> : recurrence_bwd_kernel<T, G, kFused, N, true, false>,
-                      p, kWarps * 32, shared, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi);
+      engine ? launch_bwd<T, G, kFused, N, true>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi)
+             : launch_bwd<T, G, kFused, N, false>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi);
   if (err != cudaSuccess || !kFused || !part) return err;
   return launch_behind(recurrence_dlam_kernel, (a.D + 31) / 32, 1024, 0, a.stream, a, (const float*)part,
                        p.parts * p.S);

@@ -44,8 +44,7 @@ def _heads(t, name, dtype, dev):
 
 
 def _inputs(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections):
-    """Checks shared by the calls; returns the arguments that forward and backward share:
-    (device, (B, T, Hq, Hk, K, R), the C call's leading and trailing parts)."""
+    """Checks shared by the calls; returns (device, what forward's and backward's C calls share)."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dev = q.device
@@ -85,10 +84,19 @@ def _inputs(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections):
     eps = float(eps)
     if not eps >= 0.0:
         raise ValueError("eps must not be negative (got %r)" % eps)
-    lead_args = (_Strides(*qs), _Strides(*ks), B, T, Hq, Hk, K, R, _DT[q.dtype], _NORM[norm], eps,
-                 _ptr(q_weight), _ptr(k_weight), _DT[wb or torch.float32], _ptr(inv_freq) if R else None,
-                 _ptr(positions), axes, (ctypes.c_int * axes)(*sections) if axes > 1 else None)
-    return dev, (B, T, Hq, Hk, K), lead_args
+    return dev, _Call((_Strides(*qs), _Strides(*ks), B, T, Hq, Hk, K, R, _DT[q.dtype], _NORM[norm], eps),
+                      _DT[wb or torch.float32], (axes, (ctypes.c_int * axes)(*sections) if axes > 1 else None))
+
+
+class _Call:
+    """The arguments of a C call that are not tensors."""
+
+    def __init__(self, sizes, w_dtype, axes):
+        self.sizes, self.w_dtype, self.axes = sizes, w_dtype, axes
+
+    def args(self, inv_freq, positions, q_weight, k_weight, interleaved):
+        return (*self.sizes, _ptr(q_weight), _ptr(k_weight), self.w_dtype, _ptr(inv_freq), _ptr(positions), *self.axes,
+                interleaved)
 
 
 def qk_norm_rotate(q, k, inv_freq=None, positions=None, q_weight=None, k_weight=None, *, norm="rms", eps=1e-6,
@@ -102,18 +110,26 @@ def qk_norm_rotate(q, k, inv_freq=None, positions=None, q_weight=None, k_weight=
     [axes, B, T].  q_weight, k_weight [K] in fp32 or q's dtype, or None.  norm "rms", "l2" or None.
     ``out_q``, ``out_k``: contiguous, each may be its input.
     """
-    dev, _, args = _inputs(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections)
-    out = []
-    for t, o, name in ((q, out_q, "out_q"), (k, out_k, "out_k")):
-        if o is None:
-            o = torch.empty(t.shape, dtype=t.dtype, device=dev)
-        elif not _fit(dev, (o, t.dtype, t.shape)):
-            _need(o, name, t.dtype, dev, t.shape)
-        out.append(o)
-    st = _lib.load().gdn_qk_norm_rotate_fwd(_ptr(q), _ptr(k), *args, int(bool(interleaved)), _ptr(out[0]),
-                                            _ptr(out[1]), _stream(dev))
+    dev, call = _inputs(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections)
+    return _forward(q, k, inv_freq, positions, q_weight, k_weight, call, int(bool(interleaved)), out_q, out_k)
+
+
+def _forward(q, k, inv_freq, positions, q_weight, k_weight, call, interleaved, out_q=None, out_k=None):
+    """The forward's outputs and call, after the checks of its inputs."""
+    dev = q.device
+    if out_q is None:
+        out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif not _fit(dev, (out_q, q.dtype, q.shape)):
+        _need(out_q, "out_q", q.dtype, dev, q.shape)
+    if out_k is None:
+        out_k = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    elif not _fit(dev, (out_k, q.dtype, k.shape)):
+        _need(out_k, "out_k", q.dtype, dev, k.shape)
+    st = _lib.load().gdn_qk_norm_rotate_fwd(
+        q.data_ptr(), k.data_ptr(), *call.args(inv_freq, positions, q_weight, k_weight, interleaved),
+        out_q.data_ptr(), out_k.data_ptr(), _stream(dev))
     _lib.check("gdn_qk_norm_rotate_fwd", st)
-    return tuple(out)
+    return out_q, out_k
 
 
 def qk_norm_rotate_bwd(d_q, d_k, q, k, inv_freq=None, positions=None, q_weight=None, k_weight=None, *,
@@ -122,43 +138,59 @@ def qk_norm_rotate_bwd(d_q, d_k, q, k, inv_freq=None, positions=None, q_weight=N
     """Gradients of :func:`qk_norm_rotate` through ``gdn_qk_norm_rotate_bwd``: ``(dq, dk, dq_weight,
     dk_weight)`` from d_q, d_k (contiguous, like the outputs) and the forward's inputs; dq, dk in q's
     dtype, the weights' fp32 [K] (None without ``need_weights``)."""
-    dev, (B, T, Hq, Hk, K), args = _inputs(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections)
+    dev, call = _inputs(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections)
     if d_q is None or d_k is None or not _fit(dev, (d_q, q.dtype, q.shape), (d_k, q.dtype, k.shape)):
         _need(d_q, "d_q", q.dtype, dev, q.shape)
         _need(d_k, "d_k", q.dtype, dev, k.shape)
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-    dwq = dwk = None
-    if need_weights:
-        dwq, dwk = torch.empty((2, K), dtype=torch.float32, device=dev).unbind(0)
+    return _backward(d_q, d_k, q, k, inv_freq, positions, q_weight, k_weight, call, int(bool(interleaved)),
+                     need_weights, workspace)
+
+
+def _backward(d_q, d_k, q, k, inv_freq, positions, q_weight, k_weight, call, interleaved, need_weights, workspace):
+    """The backward's outputs, scratch and call, after the checks."""
+    dev = q.device
+    dq, dk = torch.empty_like(d_q), torch.empty_like(d_k)
     L = _lib.load()
-    need = L.gdn_qk_norm_rotate_bwd_workspace_size(B, T, Hq, Hk, K, int(bool(need_weights)))
-    workspace, ws_bytes = _scratch(need, "gdn_qk_norm_rotate_bwd", workspace, dev)
-    st = L.gdn_qk_norm_rotate_bwd(_ptr(d_q), _ptr(d_k), _ptr(q), _ptr(k), *args, int(bool(interleaved)),
-                                  _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(workspace), ws_bytes,
-                                  _stream(dev))
+    dwq = dwk = None
+    ws_bytes = 0
+    if need_weights:
+        B, T, Hq, Hk, K = call.sizes[2:7]
+        dwq, dwk = torch.empty((2, K), dtype=torch.float32, device=dev).unbind(0)
+        need = L.gdn_qk_norm_rotate_bwd_workspace_size(B, T, Hq, Hk, K, 1)
+        workspace, ws_bytes = _scratch(need, "gdn_qk_norm_rotate_bwd", workspace, dev)
+    elif workspace is not None:
+        _need(workspace, "workspace", None, dev)
+    st = L.gdn_qk_norm_rotate_bwd(
+        d_q.data_ptr(), d_k.data_ptr(), q.data_ptr(), k.data_ptr(),
+        *call.args(inv_freq, positions, q_weight, k_weight, interleaved), dq.data_ptr(), dk.data_ptr(), _ptr(dwq),
+        _ptr(dwk), _ptr(workspace), ws_bytes, _stream(dev))
     _lib.check("gdn_qk_norm_rotate_bwd", st)
     return dq, dk, dwq, dwk
 
 
 class _QkNormRotate(torch.autograd.Function):
-    """gdn_qk_norm_rotate_fwd forward, gdn_qk_norm_rotate_bwd backward."""
+    """gdn_qk_norm_rotate_fwd forward, gdn_qk_norm_rotate_bwd backward, which does not check again what the
+    forward has checked."""
 
     @staticmethod
     def forward(ctx, q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections, interleaved):
-        out = qk_norm_rotate(q, k, inv_freq, positions, q_weight, k_weight, norm=norm, eps=eps,
-                             sections=sections, interleaved=interleaved)
+        _, call = _inputs(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections)
+        out = _forward(q, k, inv_freq, positions, q_weight, k_weight, call, interleaved)
         ctx.save_for_backward(q, k, inv_freq, positions, q_weight, k_weight)
-        ctx.options = dict(norm=norm, eps=eps, sections=sections, interleaved=interleaved)
+        ctx.call = call, interleaved
+        ctx.strides = q.stride(), k.stride()
+        ctx.options = norm, eps, sections
         return out
 
     @staticmethod
     def backward(ctx, d_q, d_k):
         q, k, inv_freq, positions, q_weight, k_weight = ctx.saved_tensors
+        call, interleaved = ctx.call
+        if (q.stride(), k.stride()) != ctx.strides:   # (saved elsewhere, they may come back in another layout)
+            _, call = _inputs(q, k, inv_freq, positions, q_weight, k_weight, *ctx.options)
         need = ctx.needs_input_grad
-        grads = qk_norm_rotate_bwd(d_q.contiguous(), d_k.contiguous(), q, k, inv_freq, positions, q_weight,
-                                   k_weight, need_weights=need[4] or need[5], **ctx.options)
-        dq, dk, dwq, dwk = grads
+        dq, dk, dwq, dwk = _backward(d_q.contiguous(), d_k.contiguous(), q, k, inv_freq, positions, q_weight,
+                                     k_weight, call, interleaved, need[4] or need[5], None)
         grads = (dq, dk, dwq.to(q_weight.dtype) if need[4] else None,
                  dwk.to(k_weight.dtype) if need[5] else None)
         if torch.is_grad_enabled():
@@ -174,4 +206,4 @@ def qk_norm_rotate_trainable(q, k, inv_freq=None, positions=None, q_weight=None,
     if inv_freq is not None and inv_freq.requires_grad:
         raise ValueError("inv_freq is a constant of the layer: it has no gradient")
     return _QkNormRotate.apply(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections,
-                               bool(interleaved))
+                               int(bool(interleaved)))

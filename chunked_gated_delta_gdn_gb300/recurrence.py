@@ -94,6 +94,7 @@ def _sequences(x, cu_seqlens):
 
 def _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices, out,
              final_state, return_carries, dev_status, check, g_name):
+    """Checks and the forward's call: (y, final state, carries, (c, pitches, number of sequences))."""
     dev, pitches, c = _inputs(x, g, i, lam, c, 3, g_name)
     B, T, D = x.shape
     N = _sequences(x, cu_seqlens)
@@ -137,7 +138,7 @@ def _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, sta
                                      _ptr(dev_status), _stream(dev))
     _lib.check("gdn_linear_recurrence_fwd", st)
     _raise_on_status("gdn_linear_recurrence_fwd", dev_status, check)
-    return out, final_state, carries
+    return out, final_state, carries, (c, pitches, N)
 
 
 def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, cu_seqlens=None, *,
@@ -152,7 +153,7 @@ def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, 
     ``final_state``, ``dev_status`` and ``check`` as in :func:`chunk_gated_delta_rule`; a bad
     ``cu_seqlens`` leaves zero rows and every state as it was.
     """
-    y, fin, carries = _forward(x, g, None, None, 0.0, initial_state, output_final_state, cu_seqlens,
+    y, fin, carries, _ = _forward(x, g, None, None, 0.0, initial_state, output_final_state, cu_seqlens,
                                state_indices, out, final_state, return_carries, dev_status, check, "g")
     return (y, fin, carries) if return_carries else (y, fin)
 
@@ -164,7 +165,7 @@ def gated_linear_recurrence_fused_gates(x, r, i, lam, c=8.0, initial_state=None,
     """:func:`gated_linear_recurrence` with its gates computed in the kernel: r, i [B, T, D] in fp32 or
     x's dtype, lam [D] fp32, c a constant of the layer."""
     _need(lam, "lam")
-    y, fin, carries = _forward(x, r, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices,
+    y, fin, carries, _ = _forward(x, r, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices,
                                out, final_state, return_carries, dev_status, check, "r")
     return (y, fin, carries) if return_carries else (y, fin)
 
@@ -174,7 +175,6 @@ def _backward(x, g, i, lam, c, d_y, d_final_state, initial_state, cu_seqlens, ne
     dev, pitches, c = _inputs(x, g, i, lam, c, 3, g_name)
     B, T, D = x.shape
     N = _sequences(x, cu_seqlens)
-    fused = lam is not None
     if d_y is None or not _fit(dev, (d_y, x.dtype, x.shape), (initial_state, torch.float32, (N, D)),
                                (d_final_state, torch.float32, (N, D)),
                                (carries, torch.float32, (-(-B * T // 32), D))):
@@ -184,22 +184,36 @@ def _backward(x, g, i, lam, c, d_y, d_final_state, initial_state, cu_seqlens, ne
                 _need(t, name, torch.float32, dev, (N, D))
         if carries is not None:
             _need(carries, "carries", torch.float32, dev, (-(-B * T // 32), D))
-    L = _lib.load()
-    need = L.gdn_linear_recurrence_bwd_workspace_size(B, T, D, N, int(fused))
-    workspace, ws_bytes = _scratch(need, "gdn_linear_recurrence_bwd", workspace, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    dg = torch.empty(x.shape, dtype=g.dtype, device=dev)
-    di = torch.empty(x.shape, dtype=g.dtype, device=dev) if fused else None
-    dlam = torch.empty(D, dtype=torch.float32, device=dev) if fused and need_lam else None
-    dh0 = torch.empty((N, D), dtype=torch.float32, device=dev) if need_d_initial_state else None
     dev_status = _status(dev_status, check, dev)
+    grads = _gradients(x, g, i, lam, c, pitches, N, d_y, d_final_state, initial_state, cu_seqlens, need_lam,
+                       need_d_initial_state, carries, workspace, dev_status)
+    _raise_on_status("gdn_linear_recurrence_bwd", dev_status, check)
+    return grads
+
+
+def _gradients(x, g, i, lam, c, pitches, N, d_y, d_final_state, initial_state, cu_seqlens, need_lam,
+               need_d_initial_state, carries, workspace, dev_status):
+    """The backward's outputs, scratch and call, after the checks."""
+    dev = x.device
+    B, T, D = x.shape
+    L = _lib.load()
+    need = L.gdn_linear_recurrence_bwd_workspace_size(B, T, D, N, int(lam is not None))
+    workspace, ws_bytes = _scratch(need, "gdn_linear_recurrence_bwd", workspace, dev)
+    dx = torch.empty_like(d_y)
+    dg = torch.empty_like(d_y, dtype=g.dtype)
+    di = dlam = dh0 = None
+    if lam is not None:
+        di = torch.empty_like(dg)
+        if need_lam:
+            dlam = torch.empty_like(lam)
+    if need_d_initial_state:
+        dh0 = torch.empty((N, D), dtype=torch.float32, device=dev)
     st = L.gdn_linear_recurrence_bwd(_ptr(x), _ptr(g), _ptr(i), _ptr(lam), c, *pitches, B, T, D,
                                      _DT[x.dtype], _DT[g.dtype], _ptr(initial_state), _ptr(cu_seqlens), N,
                                      _ptr(d_y), _ptr(d_final_state), _ptr(carries), _ptr(dx), _ptr(dg),
                                      _ptr(di), _ptr(dlam), _ptr(dh0), _ptr(workspace), ws_bytes,
                                      _ptr(dev_status), _stream(dev))
     _lib.check("gdn_linear_recurrence_bwd", st)
-    _raise_on_status("gdn_linear_recurrence_bwd", dev_status, check)
     return dx, dg, di, dlam, dh0
 
 
@@ -225,31 +239,40 @@ def gated_linear_recurrence_bwd_fused_gates(x, r, i, lam, d_y, d_final_state=Non
                      need_d_initial_state, carries, workspace, dev_status, check, "r")
 
 
+def _strides(*ts):
+    return [None if t is None else t.stride() for t in ts]
+
+
 class _Recurrence(torch.autograd.Function):
-    """gdn_linear_recurrence_fwd forward, gdn_linear_recurrence_bwd backward."""
+    """gdn_linear_recurrence_fwd forward, gdn_linear_recurrence_bwd backward, which does not check again what
+    the forward has checked."""
 
     @staticmethod
     def forward(ctx, x, g, i, lam, initial_state, c, output_final_state, cu_seqlens):
-        y, fin, carries = _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, None, None,
-                                   None, any(ctx.needs_input_grad), None, False, "g" if lam is None else "r")
+        y, fin, carries, call = _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, None,
+                                         None, None, any(ctx.needs_input_grad), None, False,
+                                         "g" if lam is None else "r")
         ctx.save_for_backward(x, g, i, lam, initial_state, cu_seqlens, carries)
-        ctx.c = c
+        ctx.call = call
+        ctx.strides = _strides(x, g, i)
         ctx.set_materialize_grads(False)
         return y, fin
 
     @staticmethod
     def backward(ctx, d_y, d_fin):
         x, g, i, lam, init, cu, carries = ctx.saved_tensors
+        c, pitches, N = ctx.call
+        if _strides(x, g, i) != ctx.strides:   # (tensors that were saved elsewhere may come back in another layout)
+            _, pitches, _ = _inputs(x, g, i, lam, c, 3, "g")
+        need = ctx.needs_input_grad
         d_y = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if d_y is None else d_y.contiguous()
         if d_fin is not None:
             d_fin = d_fin.contiguous()
-        grads = _backward(x, g, i, lam, ctx.c, d_y, d_fin, init, cu, ctx.needs_input_grad[3],
-                          init is not None and ctx.needs_input_grad[4], carries, None, None, False,
-                          "g" if lam is None else "r")
+        grads = _gradients(x, g, i, lam, c, pitches, N, d_y, d_fin, init, cu, need[3], init is not None and need[4],
+                           carries, None, None)
         if torch.is_grad_enabled():
             grads = _first_only("gated_linear_recurrence_trainable", grads, (x, g, i, lam, init, d_y, d_fin))
-        dx, dg, di, dlam, dh0 = grads
-        return dx, dg, di, dlam, dh0, None, None, None
+        return (*grads, None, None, None)
 
 
 def gated_linear_recurrence_trainable(x, g, initial_state=None, output_final_state=False, cu_seqlens=None):
