@@ -32,7 +32,8 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_path"
            "gdn_linear_attn_decode",
            "gdn_group_norm_act_fwd", "gdn_group_norm_act_fwd_workspace_size",
            "gdn_group_norm_act_bwd", "gdn_group_norm_act_bwd_workspace_size",
-           "gdn_linear_recurrence_carries_size", "gdn_linear_recurrence_fwd",
+           "gdn_linear_recurrence_carries_size", "gdn_linear_recurrence_fwd_workspace_size",
+           "gdn_linear_recurrence_fwd",
            "gdn_linear_recurrence_bwd_workspace_size", "gdn_linear_recurrence_bwd",
            "gdn_linear_recurrence_decode",
            "gdn_qk_norm_rotate_fwd", "gdn_qk_norm_rotate_bwd_workspace_size", "gdn_qk_norm_rotate_bwd",
@@ -130,10 +131,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         ll = ctypes.c_longlong
         lib.gdn_linear_recurrence_carries_size.argtypes = [i, i, i]
         lib.gdn_linear_recurrence_carries_size.restype = sz
+        lib.gdn_linear_recurrence_fwd_workspace_size.argtypes = [i, i, i, i]
+        lib.gdn_linear_recurrence_fwd_workspace_size.restype = sz
         lib.gdn_linear_recurrence_bwd_workspace_size.argtypes = [i, i, i, i, i]
         lib.gdn_linear_recurrence_bwd_workspace_size.restype = sz
         lib.gdn_linear_recurrence_fwd.argtypes = [vp, vp, vp, vp, f, ll, ll, ll, i, i, i, i, i, vp, i, vp,
-                                                  vp, i, vp, i, vp, vp, vp, vp]
+                                                  vp, i, vp, i, vp, vp, vp, sz, vp, vp]
         lib.gdn_linear_recurrence_fwd.restype = i
         lib.gdn_linear_recurrence_bwd.argtypes = [vp, vp, vp, vp, f, ll, ll, ll, i, i, i, i, i, vp, vp, i,
                                                   vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]

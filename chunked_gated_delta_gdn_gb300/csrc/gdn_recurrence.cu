@@ -3,10 +3,11 @@
 //     h_t = a_t h_{t-1} + b_t   per channel, with a_t = exp(g_t), b_t = x_t, or
 //     a_t = exp(-c softplus(lam) sigmoid(r_t)),  b_t = sqrt(1 - a_t^2) sigmoid(i_t) x_t.
 //
-// Forward: one reading of the inputs.  A cluster of S CTAs walks a part's tokens S tiles at a time, a
-// CTA a tile of kWarps windows.  Each warp turns its window's inputs, which were copied ahead into
-// shared memory, into a and b in registers and into the window's (L, H), is handed the state in front of
-// its window and walks its tokens.
+// Forward: one reading of the inputs where there are channels and sequences for all SMs.  A CTA walks a part's
+// tokens a tile of kWarps windows at a time.  Each warp turns its window's inputs, which were copied ahead
+// into shared memory, into a and b in registers and into the window's (L, H), is handed the state in front
+// of its window and walks its tokens.  Few parts are cut into segments, for which a first launch
+// (kSteps) makes the segments' steps.
 #include <algorithm>
 
 #include "gdn_recurrence.cuh"
@@ -15,36 +16,36 @@ namespace gdn {
 namespace {
 
 constexpr int kTau = 16;
-constexpr int kTile = 16 * kTau;   // of a CTA alone
+constexpr int kWarps = 16;
+constexpr int kTile = kWarps * kTau;
+constexpr double kFirst = 0.7;   // the first launch's time, of the second's
 constexpr int kStages = 2;
-constexpr int kMaxCluster = 8;
-template <int kWarps, int N> using Together = TogetherOf<kWarps, N, kMaxCluster>;
 
-template <typename T, typename G, bool kFused, int N, int kWarps, template <int, int> class Links>
+template <typename T, typename G, bool kFused, int N>
 struct FwdShared {
   static constexpr int W = 32 * N;
   static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
   static constexpr int kAtG = kTau * kRowX, kAtI = kAtG + kTau * kRowG;
   static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
-  Links<kWarps, N> links;
+  Chain<kWarps, N> chain;
   uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  Links: Alone (S = 1) or Together.
-template <typename T, typename G, bool kFused, int N, bool kEngine, int kWarps, template <int, int> class Links>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
-    recurrence_fwd_kernel(RecurrenceArgs a, int parts, int S, int x_unit, int g_unit, int i_unit,
+// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  states: where the first launch
+// keeps the sequences' initial states for the second, whose final states may take their place.
+template <typename T, typename G, bool kFused, int N, bool kEngine, bool kSteps>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    recurrence_fwd_kernel(RecurrenceArgs a, int parts, int segments, float* steps, float* states, int x_unit, int g_unit, int i_unit,
                           const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
-  using Shared = FwdShared<T, G, kFused, N, kWarps, Links>;
+  using Shared = FwdShared<T, G, kFused, N>;
   using Values = Lanes<N>;
-  constexpr int W = Shared::W, kTile = kWarps * kTau;
+  constexpr int W = Shared::W;
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const int rank = Links<kWarps, N>::rank();
-  const int part_index = blockIdx.x / S % parts, block = blockIdx.x / S / parts;
+  const int segment = blockIdx.x % segments, part_index = blockIdx.x / segments % parts, block = blockIdx.x / segments / parts;
   const int ch = block * W + lane * N;   // this lane's first channel
   const int mine = max(0, min(N, a.D - ch));
   WindowFinder finder;
@@ -53,14 +54,16 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
   finder.num_slots = a.num_slots;
   if (a.cu_seqlens && !packed_lengths_fit(a.cu_seqlens, a.num_seqs, a.T)) {   // every row is zero
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.dev_status, GDN_DEV_BAD_CU_SEQLENS);
-    for (long long t = (part_index * S + rank) * kWarps + warp; t < a.T && a.y; t += parts * S * kWarps)
+    for (long long t = (part_index * segments + segment) * kWarps + warp; t < a.T && a.y && !kSteps;
+         t += parts * segments * kWarps)
       write_row<false>(static_cast<T*>(a.y) + (size_t)t * a.D + ch, fill<N>(0.f), mine);
+    wait_for_previous();
     return;
   }
   finder.part = part_of(finder.seq, part_index, parts);
   const Part part = finder.part;
   // empty sequences' states, and bad slots
-  for (int n = part.n0 + rank * kWarps + warp; n < part.n1; n += S * kWarps) {
+  for (int n = part.n0 + segment * kWarps + warp; n < part.n1 && !kSteps; n += segments * kWarps) {
     int row = n;
     if (a.state_indices) {
       row = a.state_indices[n];
@@ -75,9 +78,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
   }
   const Values rate = each([&](float lam) { return gate_rate(a.c, lam); }, read_state<N>(kFused ? a.lam + ch : nullptr, mine));
 
-  const int tile0 = part.t0 / kTile;
-  const int rounds = part.t1 > part.t0 ? ((part.t1 + kTile - 1) / kTile - tile0 + S - 1) / S : 0;
-  auto window_start = [&](int round) { return (tile0 + round * S + rank) * kTile + warp * kTau; };
+  const int tile0 = part.t0 / kTile, tiles = part.t1 > part.t0 ? (part.t1 - 1) / kTile - tile0 + 1 : 0;
+  const int first = tile0 + (int)((long long)tiles * segment / segments);
+  const int rounds = tile0 + (int)((long long)tiles * (segment + 1) / segments) - first;
+  auto window_start = [&](int round) { return (first + round) * kTile + warp * kTau; };
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
     if constexpr (kEngine) {
@@ -106,14 +110,26 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
   };
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages * kWarps; ++k) mbar_init(&sh.arrived[0][k], 1);
-    sh.links.init();
+    sh.chain.init();
   }
-  sh.links.start();
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < kStages; ++k) fetch(k);
 
-  Values base = fill<N>(0.f);
-  bool lost = false;
+  next_may_start();
+  if (!kSteps && segments > 1) wait_for_previous();
+  if (warp == 0)
+    sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments * 2 * a.D, segment, a.D, ch, mine));
+  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of kSteps: the logarithms' sum, the state behind the segment
+  bool lost = false, any_reset = false;
+  // a first token's initial state: lane j's sequence, of which lanes know the cache's row and the number
+  auto initial = [&](const Window& w, int j) {
+    const int row = __shfl_sync(~0u, !kSteps && states ? w.n : w.row, j);
+    const float* const from = !kSteps && states ? states : a.initial_state;
+    const Values h = read_state<N>(from ? from + (size_t)row * a.D + ch : nullptr, mine);
+    if (kSteps && states) write_state(states + (size_t)__shfl_sync(~0u, w.n, j) * a.D + ch, h, mine);
+    return h;
+  };
   for (int round = 0; round < rounds; ++round) {
     const int w0 = window_start(round);
     const Window w = finder.template find<kTau, false>(w0, lane);
@@ -152,17 +168,19 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
 #pragma unroll
       for (int j = 0; j < kTau; ++j) {
         if (reset >> j & 1) {
-          const int row = __shfl_sync(~0u, w.row, j);
-          db[j] = w.dead >> j & 1
-                      ? fill<N>(0.f)
-                      : fma(da[j], read_state<N>(a.initial_state ? a.initial_state + (size_t)row * a.D + ch : nullptr, mine), db[j]);
+          db[j] = w.dead >> j & 1 ? fill<N>(0.f) : fma(da[j], initial(w, j), db[j]);
           H = db[j];
         } else {
           H = fma(da[j], H, db[j]);
         }
       }
     }
-    Values h = sh.links.hand_over(warp, round, rounds, S, rank, lane, L, H, reset != 0, &base, &lost, a.dev_status);
+    Values h = sh.chain.hand_over(warp, round, rounds, lane, L, H, reset != 0, kSteps ? &end : nullptr, &lost, a.dev_status);
+    if (kSteps) {
+      sum = sum + L;
+      any_reset |= reset != 0;
+      continue;
+    }
     // the window's tokens from the state in front of it
     if (a.carries && w0 % kRecCarry == 0 && (w.in & 1)) write_state(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, h, mine);
     T* const y = static_cast<T*>(a.y) + (size_t)w0 * a.D + ch;
@@ -185,35 +203,64 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     }
   }
   if (!kEngine) copies_wait<0>();
-  sh.links.finish();
+  if (kSteps) {   // (a segment that resets takes nothing from in front of it, whatever L says)
+    Values(*const sums)[32] = reinterpret_cast<Values(*)[32]>(sh.ring);
+    any_reset = __syncthreads_or(any_reset);
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp + 1 < kWarps) return;
+    sum = fill<N>(0.f);
+    for (int k = 0; k < kWarps; ++k) sum = sum + sums[k][lane];
+    write_step(steps + ((size_t)part_index * segments + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
+    wait_for_previous();
+  }
+}
+
+RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
+  return recurrence_plan((long long)B * T, D, N, packed, width, kTile, kFirst);
 }
 
 template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
-cudaError_t launch_fwd(const RecurrencePlan& p, cudaStream_t stream, const Args&... args) {
-  if (p.S > 1)
-    return launch_clusters<recurrence_fwd_kernel<T, G, kFused, N, kEngine, 8, Together>>(p, 256,
-                           sizeof(FwdShared<T, G, kFused, N, 8, Together>), stream, args...);
-  return launch_clusters<recurrence_fwd_kernel<T, G, kFused, N, kEngine, 16, Alone>>(p, 512,
-                         sizeof(FwdShared<T, G, kFused, N, 16, Alone>), stream, args...);
+cudaError_t launch_fwd(const RecurrenceArgs& a, const RecurrencePlan& p, const Args&... args) {
+  constexpr auto run = recurrence_fwd_kernel<T, G, kFused, N, kEngine, false>;
+  constexpr auto make_steps = recurrence_fwd_kernel<T, G, kFused, N, kEngine, true>;
+  const size_t shared = sizeof(FwdShared<T, G, kFused, N>);
+  const unsigned ctas = (unsigned)((long long)p.blocks * p.parts * p.segments);
+  float* const steps = static_cast<float*>(a.workspace);
+  float* const states = p.segments > 1 && a.initial_state && a.final_state
+                            ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256(steps_bytes(p, a.D)))
+                            : nullptr;
+  cudaError_t err = allow_shared<run>(shared);
+  if (err != cudaSuccess) return err;
+  if (p.segments > 1) {
+    err = allow_shared<make_steps>(shared);
+    if (err != cudaSuccess) return err;
+    make_steps<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, states, args...);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return launch_behind(run, ctas, kWarps * 32, shared, a.stream, a, p.parts, p.segments, steps, states, args...);
+  }
+  run<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, states, args...);
+  return cudaGetLastError();
 }
 
 template <typename T, typename G, bool kFused, int N>
 cudaError_t launch_fwd(const RecurrenceArgs& a) {
   constexpr int W = 32 * N;
   const long long tokens = (long long)a.B * a.T;
-  const RecurrencePlan p = recurrence_plan(tokens, a.D, a.num_seqs, a.cu_seqlens != nullptr, W, kTile, kMaxCluster);
+  const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, W);
   const int x_unit = copy_unit(a.x, a.x_pitch, a.D, sizeof(T)), g_unit = copy_unit(a.g, a.g_pitch, a.D, sizeof(G)),
             i_unit = copy_unit(a.i, a.i_pitch, a.D, sizeof(G));
   CUtensorMap mx{}, mg{}, mi{};
   const bool engine = tokens > 0 && engine_rows(a.x, a.x_pitch, a.D, sizeof(T)) && engine_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
                       (!kFused || engine_rows(a.i, a.i_pitch, a.D, sizeof(G))) &&
                       reinterpret_cast<uintptr_t>(a.y) % (N * sizeof(T)) == 0;
-  if (!engine) return launch_fwd<T, G, kFused, N, false>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, mx, mg, mi);
+  if (!engine) return launch_fwd<T, G, kFused, N, false>(a, p, x_unit, g_unit, i_unit, mx, mg, mi);
   if (!rows_map(&mx, a.x, tokens, a.D, a.x_pitch, sizeof(T), W, kTau) ||
       !rows_map(&mg, a.g, tokens, a.D, a.g_pitch, sizeof(G), W, kTau) ||
       (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau)))
     return cudaErrorInvalidValue;
-  return launch_fwd<T, G, kFused, N, true>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, mx, mg, mi);
+  return launch_fwd<T, G, kFused, N, true>(a, p, x_unit, g_unit, i_unit, mx, mg, mi);
 }
 
 template <typename T, typename G, int N>
@@ -249,6 +296,17 @@ __global__ void recurrence_decode_kernel(RecurrenceArgs a) {
 
 size_t recurrence_carries_bytes(long long tokens, int D) {
   return (size_t)((tokens + kRecCarry - 1) / kRecCarry) * D * sizeof(float);
+}
+
+// Segments' steps, then the initial states of the sequences, for whichever plan the call will have.
+size_t recurrence_fwd_workspace_bytes(int B, int T, int D, int num_seqs) {
+  size_t most = 0;
+  for (int packed = 0; packed < 2; ++packed)
+    for (int width = 32; width <= 64; width *= 2) {
+      const RecurrencePlan p = plan_of(B, T, D, num_seqs, packed, width);
+      if (p.segments > 1) most = std::max(most, up256(steps_bytes(p, D)) + (size_t)num_seqs * D * sizeof(float));
+    }
+  return most;
 }
 
 cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a) {

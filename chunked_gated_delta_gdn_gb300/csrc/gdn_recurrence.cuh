@@ -10,8 +10,7 @@
 //
 // A window's warp knows L and H without its neighbours.  It then gets what is in front of it from the
 // warp of the window before, passes on what is behind it, and walks its tokens: no barrier of the
-// CTA, a chain of short hand-overs through shared memory that runs ahead of the walking.  Where channels
-// and sequences are too few for the SMs, clusters of CTAs share a chain's tokens.
+// CTA, a chain of short hand-overs through shared memory that runs ahead of the walking.
 #pragma once
 
 #include <algorithm>
@@ -181,6 +180,7 @@ struct Window {
   unsigned first;   // a sequence's first token
   unsigned last;    // ... last token
   int row;          // lane j: the state of token j's sequence
+  int n;            // lane j: that sequence
   bool plain;       // inside one sequence: none of the above but `in`
 };
 
@@ -198,7 +198,7 @@ struct WindowFinder {
     w.plain = w0 > bos && w0 + kTau < eos;
     w.in = (1u << kTau) - 1;
     w.dead = w.first = w.last = 0;
-    w.row = 0;
+    w.row = w.n = 0;
     if (!w.plain) look<kTau, kLeftwards>(w0, lane, &w);
     return w;
   }
@@ -223,6 +223,7 @@ struct WindowFinder {
     w->first = __ballot_sync(~0u, row >= 0 && t == b) & all;
     w->last = __ballot_sync(~0u, row >= 0 && t + 1 == e) & all;
     w->row = row;
+    w->n = n;
     const int at = kLeftwards ? 0 : kTau - 1;
     const bool live = __shfl_sync(~0u, row, at) >= 0;
     bos = __shfl_sync(~0u, b, at);
@@ -341,24 +342,11 @@ struct Front {
   __device__ __forceinline__ Lanes<N> value() const { return fma(ex2(L), base, H); }
 };
 
-__device__ __forceinline__ int cluster_rank() {
-  int r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// (Cluster instructions are for launches of clusters alone; of one CTA they are not.)
-__device__ __forceinline__ void cluster_sync() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// A CTA alone: its windows stand in one chain, `front` goes from warp to warp and from the last one to the
-// first one's next round.  A slot is written again one round later, by a warp that has had its own
-// message of that round, for which the ring of messages has gone round since the slot was read.
+// A CTA's windows stand in one chain: `front` goes from warp to warp and from the last one to the first one's
+// next round.  A slot is written again one round later, by a warp that has had its own message of that
+// round, for which the ring of messages has gone round since the slot was read.
 template <int kWarps, int N>
-struct Alone {
-  static constexpr int kPerSm = 16 / kWarps;
+struct Chain {
   Front<N> slot[kWarps][32];
   alignas(8) uint64_t full[kWarps];
 
@@ -366,20 +354,20 @@ struct Alone {
     for (int k = 0; k < kWarps; ++k) mbar_init(&full[k], 1);
     fence_mbar_init();
   }
-  __device__ __forceinline__ void start() { __syncthreads(); }
-  __device__ __forceinline__ void finish() {}
-  static __device__ __forceinline__ int rank() { return 0; }
+
+  // One warp: what is in front of the first window.
+  __device__ __forceinline__ void start(int lane, const Lanes<N>& state) {
+    send(0, lane, Front<N>{state, fill<N>(0.f), fill<N>(0.f)});
+  }
 
   // The state in front of this warp's window (L, H), after handing on what is behind it.  `order`: the
-  // window's place in its tile; `base`: not used.
-  __device__ __forceinline__ Lanes<N> hand_over(int order, int round, int rounds, int, int, int lane, const Lanes<N>& L,
-                                                const Lanes<N>& H, bool reset, Lanes<N>*, bool* lost, int* dev_status) {
-    Front<N> f{fill<N>(0.f), fill<N>(0.f), fill<N>(0.f)};
+  // window's place in its tile; `end`: where the last window's warp leaves what is behind it, or NULL.
+  __device__ __forceinline__ Lanes<N> hand_over(int order, int round, int rounds, int lane, const Lanes<N>& L,
+                                                const Lanes<N>& H, bool reset, Lanes<N>* end, bool* lost,
+                                                int* dev_status) {
     const Lanes<N> A = ex2(L);   // (the way from message to message is what the chain's speed depends on)
-    if (order > 0 || round > 0) {
-      wait_or_report(&full[order], (round - (order == 0)) & 1, lost, dev_status);
-      f = slot[order][lane];
-    }
+    wait_or_report(&full[order], round & 1, lost, dev_status);
+    const Front<N> f = slot[order][lane];
     Front<N> behind{f.base, f.L + L, fma(A, f.H, H)};
     if (reset) {
       behind.H = H;
@@ -391,6 +379,8 @@ struct Alone {
       behind.base = behind.value();
       behind.L = behind.H = fill<N>(0.f);
       send(0, lane, behind);
+    } else if (end) {
+      *end = behind.value();
     }
     return f.value();
   }
@@ -403,103 +393,46 @@ struct Alone {
   }
 };
 
+// ---------------------------------------------------------------- segments
+
+constexpr int kMaxSegments = 64;
 constexpr float kReset = __builtin_huge_valf();   // in L's place: "reset"
 
-// CTAs of a cluster (kMost at most), a tile each a round.  Every warp publishes its window's (L, H); with all of them there
-// each joins those in front of its own, and the last one sends the tile's to every CTA's box by
-// asynchronous stores that the receiver's barrier counts (no fence waits for the outputs on their way to
-// memory).  Every warp joins the round's tiles for itself: the state in front of its own CTA's tile
-// and, behind them all, the next round's.  Two of these CTAs an SM: one waits while the other works.
-//
-// Windows and boxes stand in two sets in turn.  A window's place is written again two rounds later, after
-// every warp has published in between and so has read it; a peer sends into a box again only after it
-// has had the round between, which this CTA's last warp sent after all its warps had published, and so
-// had left the box.
-template <int kWarps, int N, int kMost>
-struct TogetherOf {
-  static constexpr int kPerSm = 16 / kWarps;
-  struct alignas(8 * N) Step { Lanes<N> L, H; } window[2][kWarps][32], box[2][kMost][32];
-  alignas(8) uint64_t published[2];
-  uint64_t boxes[2];
-
-  __device__ __forceinline__ void init() {   // one thread; a barrier follows
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&published[k], kWarps);
-      mbar_init(&boxes[k], 1);
-    }
-    fence_mbar_init();
+// Where parts are too few for the SMs their tiles are cut into segments.  A first launch makes every segment's
+// step (L, H) from nothing in front of it, a second one runs each from the steps of those before it.
+// Steps: [parts][segments][2][D].
+template <int N>
+__device__ __forceinline__ void write_step(float* steps, int D, int ch, const Lanes<N>& L, const Lanes<N>& H, bool reset,
+                                           int mine) {
+  write_state(steps + ch, reset ? fill<N>(kReset) : L, mine);
+  write_state(steps + D + ch, H, mine);
+}
+// The state behind the first `count` segments.
+template <int N>
+__device__ __forceinline__ Lanes<N> behind_steps(const float* first, int count, int D, int ch, int mine) {
+  Lanes<N> h = fill<N>(0.f);
+#pragma unroll 4
+  for (int k = 0; k < count; ++k) {
+    const float* const at = first + (size_t)k * 2 * D + ch;
+    h = each([](float l, float x, float h) { return l == kReset ? h : fmaf(ex2(l), x, h); }, read_state<N>(at, mine), h,
+             read_state<N>(at + D, mine));
   }
-  __device__ __forceinline__ void start() { cluster_sync(); }    // the peers' shared memory is there once they run
-  __device__ __forceinline__ void finish() { cluster_sync(); }   // no CTA ends while a peer's stores are on their way
-  static __device__ __forceinline__ int rank() { return cluster_rank(); }
-
-  // As Alone's; `base`: the state in front of the round's tiles (kept from call to call, zero at first).
-  __device__ __forceinline__ Lanes<N> hand_over(int order, int round, int, int S, int rank, int lane, const Lanes<N>& L,
-                                                const Lanes<N>& H, bool reset, Lanes<N>* base, bool* lost,
-                                                int* dev_status) {
-    const int set = round & 1;
-    window[set][order][lane] = Step{reset ? fill<N>(kReset) : L, H};
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&published[set]);
-    wait_or_report(&published[set], round >> 1 & 1, lost, dev_status);
-    Step front{fill<N>(0.f), fill<N>(0.f)};
-    for (int k = 0; k < order; ++k) join(&front, window[set][k][lane]);
-    if (order + 1 == kWarps) {
-      Step tile = front;
-      join(&tile, window[set][order][lane]);
-      if (lane == 0) mbar_arrive_expect_tx(&boxes[set], S * 32 * sizeof(Step));
-      const unsigned at = smem_u32(&box[set][rank][lane]), to = smem_u32(&boxes[set]);
-      for (int k = 0; k < S; ++k) {
-        unsigned peer_at, peer_bar;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_at) : "r"(at), "r"(k));
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer_bar) : "r"(to), "r"(k));
-        if constexpr (N == 2)
-          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
-                           peer_at),
-                       "f"(tile.L.v[0]), "f"(tile.L.v[1]), "f"(tile.H.v[0]), "f"(tile.H.v[1]), "r"(peer_bar)
-                       : "memory");
-        else
-          asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(peer_at),
-                       "f"(tile.L.v[0]), "f"(tile.H.v[0]), "r"(peer_bar)
-                       : "memory");
-      }
-    }
-    wait_or_report(&boxes[set], round >> 1 & 1, lost, dev_status);
-    Lanes<N> into = *base;
-    Step all{fill<N>(0.f), fill<N>(0.f)};
-    for (int k = 0; k < S; ++k) {
-      if (k == rank) into = joined(all.L, *base, all.H);
-      join(&all, box[set][k][lane]);
-    }
-    *base = joined(all.L, *base, all.H);
-    return joined(front.L, into, front.H);
-  }
-
- private:
-  static __device__ __forceinline__ Lanes<N> joined(const Lanes<N>& L, const Lanes<N>& base, const Lanes<N>& H) {
-    return each([](float l, float x, float h) { return l == kReset ? h : fmaf(ex2(l), x, h); }, L, base, H);
-  }
-  static __device__ __forceinline__ void join(Step* f, const Step& o) {
-    f->H = joined(o.L, f->H, o.H);
-    f->L = each([](float x, float y) { return x == kReset || y == kReset ? kReset : x + y; }, f->L, o.L);
-  }
-};
+  return h;
+}
 
 // ---------------------------------------------------------------- launches
 
-// How the work is shared out: parts of whole sequences, clusters of S CTAs along each part's tokens.
+// How the work is shared out: blocks of channels, parts of whole sequences, segments of a part's tiles.
 struct RecurrencePlan {
-  int blocks, parts, S;
+  int blocks, parts, segments;
 };
 
-// For kernels of `width` channels, a tile of `tile` tokens for a CTA alone, half of that in clusters of `most` CTAs at
-// most (two of which go on an SM).  The plan with the least time: waves of CTAs, each as many rounds as its
-// longest part has (a round more than that to start).  A cluster's round, half as many tokens, takes as
-// long as a round of a CTA alone (16 warps and 8 keep an SM's issue slots busy for 3 us, 2 x 8192 and
-// 1 x 32768 x 2048 bf16), and half as long again where two CTAs share the SM.  Parts are whole sequences: of
-// equal ones the longest part is known, of packed ones (whose lengths the host does not know) it is
-// taken to be longer than the mean by half a mean sequence.
-inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile, int most) {
+// The plan with the least time, for CTAs (one an SM) of `width` channels and tiles of `tile` tokens: waves of CTAs, each as
+// many rounds as its longest part has and one more to start.  Parts are whole sequences: of equal ones the
+// longest part is known, of packed ones (whose lengths the host does not know) it is taken to be longer
+// than the mean by half a mean sequence.  The segments' first launch takes `first` of the second's time, and
+// another launch some two rounds.
+inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile, double first) {
   const long long sms = std::max(1, current_sm_count());
   RecurrencePlan best{(D + width - 1) / width, 1, 1};
   double least = 1e300;
@@ -509,19 +442,27 @@ inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packe
   for (int parts = 1; parts <= most_parts; parts += parts < 8 ? 1 : parts / 4) {
     const double each = packed ? (double)tokens / parts + (parts > 1 ? 0.5 * (double)tokens / N : 0.)
                                : (double)tokens / N * ((N + parts - 1) / parts);
-    for (int S = 1; S <= most; ++S) {
-      const long long ctas = (long long)best.blocks * parts * S, places = S > 1 ? 2 * sms : sms;
-      const long long rounds = (long long)(each / ((double)(S > 1 ? tile / 2 : tile) * S)) + 1;
-      const double time = (double)((ctas + places - 1) / places) * (double)(rounds + 1) * (S > 1 && ctas > sms ? 1.5 : 1.);
+    const long long tiles = (long long)(each / tile) + 1;
+    for (int waves = 0; waves <= 4; ++waves) {   // as many segments as fill so many waves
+      const long long fill = waves * sms / ((long long)best.blocks * parts);
+      const int segments = (int)std::min<long long>({std::max(1LL, fill), tiles, (long long)kMaxSegments});
+      const long long ctas = (long long)best.blocks * parts * segments;
+      const double run = (double)((ctas + sms - 1) / sms) * (double)((tiles + segments - 1) / segments + 1);
+      const double time = segments > 1 ? run * (1. + first) + 2. : run;
       if (time < 0.98 * least) {
         least = time;
         best.parts = parts;
-        best.S = S;
+        best.segments = segments;
       }
     }
   }
   return best;
 }
+
+inline size_t steps_bytes(const RecurrencePlan& p, int D) {
+  return p.segments > 1 ? (size_t)p.parts * p.segments * 2 * D * sizeof(float) : 0;
+}
+inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 inline int copy_unit(const void* p, long long pitch, int D, int elem) {
   const unsigned long long all = reinterpret_cast<uintptr_t>(p) | (unsigned long long)pitch * elem |
@@ -550,25 +491,6 @@ inline bool rows_map(CUtensorMap* m, const void* p, long long tokens, int D, lon
   // a thread that has made no runtime call yet (autograd's, say) has no current context
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
-}
-
-// A launch of clusters of S CTAs with `shared` bytes of shared memory each.
-template <auto kernel, typename... Args>
-cudaError_t launch_clusters(const RecurrencePlan& p, int threads, size_t shared,
-                            cudaStream_t stream, Args&&... args) {
-  const cudaError_t err = allow_shared<kernel>(shared);
-  if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {(unsigned)p.S, 1, 1};
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((long long)p.blocks * p.parts * p.S));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = shared;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = p.S > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 }  // namespace

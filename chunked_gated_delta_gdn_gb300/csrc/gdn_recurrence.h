@@ -38,7 +38,7 @@ struct RecurrenceArgs {
   void* di;                     // [tokens, D] g_dtype, with lam
   float* dlam;                  // [D] or NULL
   float* d_initial_state;       // [N, D] or NULL
-  void* workspace;
+  void* workspace;              // (forward: segments' steps and states; backward: more)
   // decode
   float* state;                 // [num_slots, D]
   const int32_t* batch_indices; // [n] or NULL
@@ -48,6 +48,7 @@ struct RecurrenceArgs {
 };
 
 size_t recurrence_carries_bytes(long long tokens, int D);
+size_t recurrence_fwd_workspace_bytes(int B, int T, int D, int num_seqs);
 size_t recurrence_bwd_workspace_bytes(int B, int T, int D, int num_seqs, bool fused);
 cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a);
 cudaError_t launch_recurrence_bwd(const RecurrenceArgs& a);

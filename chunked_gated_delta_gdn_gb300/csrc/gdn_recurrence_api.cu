@@ -48,12 +48,18 @@ size_t gdn_linear_recurrence_carries_size(int B, int T, int D) {
   return gdn::recurrence_carries_bytes((long long)B * T, D);
 }
 
+size_t gdn_linear_recurrence_fwd_workspace_size(int B, int T, int D, int num_seqs) {
+  if (B < 0 || T < 0 || D <= 0 || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
+  return gdn::recurrence_fwd_workspace_bytes(B, T, D, num_seqs);
+}
+
 gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void* i, const float* lam, float c,
                                        long long x_pitch, long long g_pitch, long long i_pitch, int B, int T,
                                        int D, gdn_dtype_t io_dtype, gdn_dtype_t g_dtype,
                                        const float* initial_state, int output_final_state, float* final_state,
                                        const int32_t* cu_seqlens, int num_seqs, const int32_t* state_indices,
-                                       int num_slots, void* y, float* carries, int* dev_status, void* stream) {
+                                       int num_slots, void* y, float* carries, void* workspace,
+                                       size_t workspace_bytes, int* dev_status, void* stream) {
   int N = 0;
   gdn_status_t st = check_batch(B, T, cu_seqlens, num_seqs, state_indices, &N);
   if (st != GDN_OK) return st;
@@ -67,6 +73,11 @@ gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void*
       !aligned_to(carries, 4))
     return GDN_ERR_LAYOUT;
   if (N == 0 && tokens == 0) return GDN_OK;
+  const size_t need = gdn::recurrence_fwd_workspace_bytes(B, T, D, N);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return GDN_ERR_WORKSPACE;
+    if (!aligned_to(workspace, 256)) return GDN_ERR_LAYOUT;
+  }
   gdn::RecurrenceArgs a{};
   a.x = x; a.g = g; a.i = i; a.lam = lam; a.c = c;
   a.x_pitch = x_pitch; a.g_pitch = g_pitch; a.i_pitch = i_pitch;
@@ -80,6 +91,7 @@ gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void*
   a.num_slots = num_slots;
   a.y = y;
   a.carries = carries;
+  a.workspace = workspace;
   a.dev_status = dev_status;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   return gdn::status_of(gdn::launch_recurrence_fwd(a));

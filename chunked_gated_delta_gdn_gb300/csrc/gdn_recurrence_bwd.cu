@@ -21,14 +21,14 @@ namespace gdn {
 namespace {
 
 constexpr int kTau = 8;
-constexpr int kTile = 16 * kTau;   // of a CTA alone
+constexpr int kWarps = 16;
+constexpr int kTile = kWarps * kTau;
+constexpr double kFirst = 0.4;   // the segments' first launch's time, of the second's
 constexpr int kStages = 2;
-constexpr int kMaxCluster = 6;   // (more, and two CTAs would not fit an SM)
-template <int kWarps, int N> using Together = TogetherOf<kWarps, N, kMaxCluster>;
 constexpr int kGroup = kRecCarry / kTau;   // windows from one saved state to the next
-static_assert(kRecCarry % kTau == 0 && kTile / 2 % kRecCarry == 0, "saved states stand in front of windows");
+static_assert(kRecCarry % kTau == 0 && kTile % kRecCarry == 0, "saved states stand in front of windows");
 
-template <typename T, typename G, bool kFused, int N, int kWarps, template <int, int> class Links>
+template <typename T, typename G, bool kFused, int N>
 struct BwdShared {
   static constexpr int W = 32 * N;
   static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
@@ -36,37 +36,37 @@ struct BwdShared {
   static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
   Lanes<N> sigmoid[kFused ? kWarps : 1][2][kFused ? kTau : 1][32];   // (dlam's sums in the end)
-  Links<kWarps, N> links;              // of e, right to left
+  Chain<kWarps, N> chain;              // of e, right to left
   Lanes<N> state[kWarps][32];          // the state in front of each window, left to right in a tile
   uint64_t state_full[kWarps];
   uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  Links: Alone (S = 1) or Together.
-template <typename T, typename G, bool kFused, int N, bool kEngine, int kWarps, template <int, int> class Links>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
-    recurrence_bwd_kernel(RecurrenceArgs a, int parts, int S, int x_unit, int g_unit, int i_unit, int dy_unit,
+// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.
+template <typename T, typename G, bool kFused, int N, bool kEngine, bool kSteps>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    recurrence_bwd_kernel(RecurrenceArgs a, int parts, int segments, float* steps, int x_unit, int g_unit, int i_unit, int dy_unit,
                           float* dlam_part, const __grid_constant__ CUtensorMap x_map,
                           const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
-  using Shared = BwdShared<T, G, kFused, N, kWarps, Links>;
+  using Shared = BwdShared<T, G, kFused, N>;
   using Values = Lanes<N>;
-  constexpr int W = Shared::W, kTile = kWarps * kTau;
+  constexpr int W = Shared::W;
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const int rank = Links<kWarps, N>::rank();
-  const int part_index = blockIdx.x / S % parts, block = blockIdx.x / S / parts;
+  const int segment = blockIdx.x % segments, part_index = blockIdx.x / segments % parts, block = blockIdx.x / segments / parts;
   const int ch = block * W + lane * N;
   const int mine = max(0, min(N, a.D - ch));
   WindowFinder finder;
   finder.seq = Sequences{a.cu_seqlens, a.num_seqs, a.T, a.cu_seqlens ? a.T : a.B * a.T};
   finder.slots = nullptr;
   finder.num_slots = 0;
-  float* const dlam_row = dlam_part ? dlam_part + ((size_t)part_index * S + rank) * a.D + ch : nullptr;
+  float* const dlam_row = dlam_part ? dlam_part + ((size_t)part_index * segments + segment) * a.D + ch : nullptr;
   if (a.cu_seqlens && !packed_lengths_fit(a.cu_seqlens, a.num_seqs, a.T)) {   // every gradient is zero
+    if (kSteps) return;
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.dev_status, GDN_DEV_BAD_CU_SEQLENS);
-    const int step = parts * S * kWarps, first = (part_index * S + rank) * kWarps + warp;
+    const int step = parts * segments * kWarps, first = (part_index * segments + segment) * kWarps + warp;
     const Values zero = fill<N>(0.f);
     for (long long t = first; t < a.T; t += step) {
       const size_t at = (size_t)t * a.D + ch;
@@ -77,12 +77,13 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     for (long long n = first; n < a.num_seqs && a.d_initial_state; n += step)
       write_state(a.d_initial_state + (size_t)n * a.D + ch, zero, mine);
     if (dlam_row && warp == 0) write_state(dlam_row, zero, mine);
+    wait_for_previous();
     return;
   }
   finder.part = part_of(finder.seq, part_index, parts);
   const Part part = finder.part;
-  if (a.d_initial_state) {   // empty sequences
-    for (int n = part.n0 + rank * kWarps + warp; n < part.n1; n += S * kWarps) {
+  if (a.d_initial_state && !kSteps) {   // empty sequences
+    for (int n = part.n0 + segment * kWarps + warp; n < part.n1; n += segments * kWarps) {
       if (finder.seq.end(n) > finder.seq.begin(n)) continue;
       const size_t at = (size_t)n * a.D + ch;
       write_state(a.d_initial_state + at, read_state<N>(a.d_final_state ? a.d_final_state + at : nullptr, mine), mine);
@@ -95,20 +96,22 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     return read_state<N>(states ? states + (size_t)row * a.D + ch : nullptr, mine);
   };
 
-  const int tile_end = part.t1 > part.t0 ? (part.t1 - 1) / kTile : 0;
-  const int rounds = part.t1 > part.t0 ? (tile_end - part.t0 / kTile + S) / S : 0;
-  auto tile_of = [&](int round) { return tile_end - (round * S + rank); };
+  // segment 0 is the rightmost one
+  const int tile0 = part.t0 / kTile, tiles = part.t1 > part.t0 ? (part.t1 - 1) / kTile - tile0 + 1 : 0;
+  const int first = tile0 + tiles - 1 - (int)((long long)tiles * segment / segments);
+  const int rounds = first - (tile0 + tiles - 1 - (int)((long long)tiles * (segment + 1) / segments));
+  auto tile_of = [&](int round) { return first - round; };
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
     if constexpr (kEngine) {
       if (round < rounds && lane == 0) {
         uint64_t* const bar = &sh.arrived[round % kStages][warp];
         const int w0 = tile_of(round) * kTile + warp * kTau;
-        mbar_arrive_expect_tx(bar, Shared::kWindow);
-        tma_window(to, &x_map, bar, block * W, w0);
+        mbar_arrive_expect_tx(bar, kSteps ? kTau * (Shared::kRowX + Shared::kRowG) : Shared::kWindow);
         tma_window(to + Shared::kAtDy, &dy_map, bar, block * W, w0);
         tma_window(to + Shared::kAtG, &g_map, bar, block * W, w0);
-        if (kFused) tma_window(to + Shared::kAtI, &i_map, bar, block * W, w0);
+        if (!kSteps) tma_window(to, &x_map, bar, block * W, w0);
+        if (kFused && !kSteps) tma_window(to + Shared::kAtI, &i_map, bar, block * W, w0);
       }
     } else {
       if (round < rounds) {
@@ -118,10 +121,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
           copy_window<kTau, W * sizeof(E)>(to + at, reinterpret_cast<const char*>(static_cast<const E*>(base) + w0 * pitch + block * W),
                                            pitch * (long long)sizeof(E), lo, hi, left * (int)sizeof(E), unit, lane);
         };
-        copy(T{}, 0, a.x, a.x_pitch, x_unit);
         copy(T{}, Shared::kAtDy, a.dy, a.D, dy_unit);
         copy(G{}, Shared::kAtG, a.g, a.g_pitch, g_unit);
-        if (kFused) copy(G{}, Shared::kAtI, a.i, a.i_pitch, i_unit);
+        if (!kSteps) copy(T{}, 0, a.x, a.x_pitch, x_unit);
+        if (kFused && !kSteps) copy(G{}, Shared::kAtI, a.i, a.i_pitch, i_unit);
       }
       copies_close();
     }
@@ -129,18 +132,22 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
   if (threadIdx.x == 0) {
     for (int k = 0; k < kStages * kWarps; ++k) mbar_init(&sh.arrived[0][k], 1);
     for (int k = 0; k < kWarps; ++k) mbar_init(&sh.state_full[k], 1);
-    sh.links.init();
+    sh.chain.init();
   }
-  sh.links.start();
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < kStages; ++k) fetch(k);
 
-  Values base = fill<N>(0.f);
-  bool lost = false;
+  next_may_start();
+  if (!kSteps && segments > 1) wait_for_previous();
+  if (warp + 1 == kWarps)
+    sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments * 2 * a.D, segment, a.D, ch, mine));
+  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of kSteps: the logarithms' sum, e in front of the segment
+  bool lost = false, any_reset = false;
   for (int round = 0; round < rounds; ++round) {
     const int tile = tile_of(round), w0 = tile * kTile + warp * kTau;
     Values h = fill<N>(0.f);
-    if (warp % kGroup == 0 && w0 >= part.t0 && w0 < part.t1) h = read_state<N>(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, mine);
+    if (!kSteps && warp % kGroup == 0 && w0 >= part.t0 && w0 < part.t1) h = read_state<N>(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, mine);
     const Window w = finder.template find<kTau, true>(w0, lane);
     const unsigned reset = w.first | w.dead, reset_e = w.last | w.dead;
     if constexpr (kEngine) {
@@ -167,9 +174,15 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     Values da[kTau], db[kTau], L = fill<N>(0.f), H = fill<N>(0.f), E = fill<N>(0.f);
 #pragma unroll
     for (int j = 0; j < kTau; ++j) {
-      const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
       const Values g = read_row<G, N>(from + Shared::kAtG + j * Shared::kRowG, lane);
       Values l;
+      if (kSteps) {
+        l = kFused ? rate * each(gate_sigmoid, g) : g * kLog2e;
+        da[j] = ex2(l);
+        L = L + l;
+        continue;
+      }
+      const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
       if (kFused) {
         const Values i = read_row<G, N>(from + Shared::kAtI + j * Shared::kRowG, lane);
         const Values sr = each(gate_sigmoid, g), si = each(gate_sigmoid, i);
@@ -188,7 +201,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
       L = L + l;
       H = fma(da[j], H, db[j]);
     }
-    if (reset) {   // a first token takes its sequence's state in, a dead one nothing
+    if (reset && !kSteps) {   // a first token takes its sequence's state in, a dead one nothing
 #pragma unroll
       for (int j = 0; j < kTau; ++j) {
         if (reset >> j & 1) {
@@ -213,17 +226,24 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
       }
     }
     // (a slot of the state is written again after e has come through its reader)
-    if (warp % kGroup > 0) {
+    if (!kSteps && warp % kGroup > 0) {
       wait_or_report(&sh.state_full[warp], round & 1, &lost, a.dev_status);
       h = sh.state[warp][lane];
     }
-    if (warp % kGroup + 1 < kGroup) {
+    if (!kSteps && warp % kGroup + 1 < kGroup) {
       sh.state[warp + 1][lane] = reset ? H : fma(ex2(L), h, H);
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.state_full[warp + 1]);
     }
     const int order = kWarps - 1 - warp;
-    Values e = sh.links.hand_over(order, round, rounds, S, rank, lane, L, E, reset_e != 0, &base, &lost, a.dev_status);
+    Values e = sh.chain.hand_over(order, round, rounds, lane, L, E, reset_e != 0, kSteps ? &end : nullptr, &lost, a.dev_status);
+    if (kSteps) {
+      sum = sum + L;
+      any_reset |= reset_e != 0;
+      __syncwarp();
+      fetch(round + kStages);
+      continue;
+    }
     // the state in front of each token, in db's place; then the gradients, right to left
     auto gradients = [&](auto is_plain) {
       constexpr bool plain = decltype(is_plain)::value;
@@ -284,7 +304,18 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
     fetch(round + kStages);
   }
   if (!kEngine) copies_wait<0>();
-  sh.links.finish();
+  if (kSteps) {   // (a segment that resets takes nothing from behind it, whatever L says)
+    Values(*const sums)[32] = reinterpret_cast<Values(*)[32]>(sh.ring);
+    any_reset = __syncthreads_or(any_reset);
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp > 0) return;   // the last one of the chain
+    sum = fill<N>(0.f);
+    for (int k = 0; k < kWarps; ++k) sum = sum + sums[k][lane];
+    write_step(steps + ((size_t)part_index * segments + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
+    wait_for_previous();
+    return;
+  }
   if (kFused && dlam_row) {
     Lanes<N>(*const sums)[32] = sh.sigmoid[0][0];
     __syncthreads();
@@ -317,20 +348,31 @@ __global__ void __launch_bounds__(1024) recurrence_dlam_kernel(RecurrenceArgs a,
 }
 
 RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
-  return recurrence_plan((long long)B * T, D, N, packed, width, kTile, kMaxCluster);
+  return recurrence_plan((long long)B * T, D, N, packed, width, kTile, kFirst);
 }
 
 template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
-cudaError_t launch_bwd(const RecurrencePlan& p, cudaStream_t stream, const Args&... args) {
-  if (p.S > 1)
-    return launch_clusters<recurrence_bwd_kernel<T, G, kFused, N, kEngine, 8, Together>>(p, 256,
-                           sizeof(BwdShared<T, G, kFused, N, 8, Together>), stream, args...);
-  return launch_clusters<recurrence_bwd_kernel<T, G, kFused, N, kEngine, 16, Alone>>(p, 512,
-                         sizeof(BwdShared<T, G, kFused, N, 16, Alone>), stream, args...);
+cudaError_t launch_bwd(const RecurrenceArgs& a, const RecurrencePlan& p, float* steps, const Args&... args) {
+  constexpr auto run = recurrence_bwd_kernel<T, G, kFused, N, kEngine, false>;
+  constexpr auto make_steps = recurrence_bwd_kernel<T, G, kFused, N, kEngine, true>;
+  const size_t shared = sizeof(BwdShared<T, G, kFused, N>);
+  const unsigned ctas = (unsigned)((long long)p.blocks * p.parts * p.segments);
+  cudaError_t err = allow_shared<run>(shared);
+  if (err != cudaSuccess) return err;
+  if (p.segments > 1) {
+    err = allow_shared<make_steps>(shared);
+    if (err != cudaSuccess) return err;
+    make_steps<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, args...);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    return launch_behind(run, ctas, kWarps * 32, shared, a.stream, a, p.parts, p.segments, steps, args...);
+  }
+  run<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, args...);
+  return cudaGetLastError();
 }
 
 template <typename T, typename G, bool kFused, int N>
-cudaError_t launch_bwd(const RecurrenceArgs& a, float* part) {
+cudaError_t launch_bwd(const RecurrenceArgs& a, float* steps, float* part) {
   constexpr int W = 32 * N;
   const long long tokens = (long long)a.B * a.T;
   const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, W);
@@ -347,50 +389,57 @@ cudaError_t launch_bwd(const RecurrenceArgs& a, float* part) {
                  (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau))))
     return cudaErrorInvalidValue;
   const cudaError_t err =
-      engine ? launch_bwd<T, G, kFused, N, true>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi)
-             : launch_bwd<T, G, kFused, N, false>(p, a.stream, a, p.parts, p.S, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi);
+      engine ? launch_bwd<T, G, kFused, N, true>(a, p, steps, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi)
+             : launch_bwd<T, G, kFused, N, false>(a, p, steps, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi);
   if (err != cudaSuccess || !kFused || !part) return err;
   return launch_behind(recurrence_dlam_kernel, (a.D + 31) / 32, 1024, 0, a.stream, a, (const float*)part,
-                       p.parts * p.S);
+                       p.parts * p.segments);
 }
 
 template <typename T, typename G, int N>
-cudaError_t launch_bwd(const RecurrenceArgs& a, float* part) {
-  return a.lam ? launch_bwd<T, G, true, N>(a, part) : launch_bwd<T, G, false, N>(a, part);
+cudaError_t launch_bwd(const RecurrenceArgs& a, float* steps, float* part) {
+  return a.lam ? launch_bwd<T, G, true, N>(a, steps, part) : launch_bwd<T, G, false, N>(a, steps, part);
 }
-
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-// The carries (where the caller has none), then the CTAs' rows of dlam.
+// The carries and the forward's workspace (where the caller has no carries), segments' steps, the CTAs' rows of
+// dlam, for whichever plan the call will have.
 size_t recurrence_bwd_workspace_bytes(int B, int T, int D, int num_seqs, bool fused) {
-  size_t rows = 0;
-  if (fused)
-    for (int packed = 0; packed < 2; ++packed)
-      for (int width = 32; width <= 64; width *= 2) {
-        const RecurrencePlan p = plan_of(B, T, D, num_seqs, packed, width);
-        rows = std::max(rows, (size_t)p.parts * p.S);
-      }
-  return up256(recurrence_carries_bytes((long long)B * T, D)) + rows * D * sizeof(float);
+  size_t steps = 0, rows = 0;
+  for (int packed = 0; packed < 2; ++packed)
+    for (int width = 32; width <= 64; width *= 2) {
+      const RecurrencePlan p = plan_of(B, T, D, num_seqs, packed, width);
+      steps = std::max(steps, steps_bytes(p, D));
+      if (fused) rows = std::max(rows, (size_t)p.parts * p.segments);
+    }
+  return up256(recurrence_carries_bytes((long long)B * T, D)) + up256(recurrence_fwd_workspace_bytes(B, T, D, num_seqs)) +
+         up256(steps) + rows * D * sizeof(float);
 }
 
 cudaError_t launch_recurrence_bwd(const RecurrenceArgs& args) {
   RecurrenceArgs a = args;
-  char* const ws = static_cast<char*>(a.workspace);
-  float* const part = a.dlam ? reinterpret_cast<float*>(ws + up256(recurrence_carries_bytes((long long)a.B * a.T, a.D)))
-                             : nullptr;
+  char* ws = static_cast<char*>(a.workspace);
+  float* const carries = reinterpret_cast<float*>(ws);
+  ws += up256(recurrence_carries_bytes((long long)a.B * a.T, a.D));
+  void* const forward = ws;
+  ws += up256(recurrence_fwd_workspace_bytes(a.B, a.T, a.D, a.num_seqs));
+  float* const steps = reinterpret_cast<float*>(ws);
+  const int width = a.io_dtype == GDN_BF16 && a.g_dtype == GDN_BF16 ? 64 : 32;
+  ws += up256(steps_bytes(plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, width), a.D));
+  float* const part = a.dlam ? reinterpret_cast<float*>(ws) : nullptr;
   if (!a.carries && (long long)a.B * a.T > 0) {
     RecurrenceArgs f = a;
-    f.carries = a.carries = reinterpret_cast<float*>(ws);
+    f.carries = a.carries = carries;
+    f.workspace = forward;
     f.y = nullptr;
     f.dev_status = nullptr;
     const cudaError_t err = launch_recurrence_fwd(f);
     if (err != cudaSuccess) return err;
   }
-  if (a.io_dtype == GDN_F32) return launch_bwd<float, float, 1>(a, part);
-  return a.g_dtype == GDN_F32 ? launch_bwd<__nv_bfloat16, float, 1>(a, part)
-                              : launch_bwd<__nv_bfloat16, __nv_bfloat16, 2>(a, part);
+  if (a.io_dtype == GDN_F32) return launch_bwd<float, float, 1>(a, steps, part);
+  return a.g_dtype == GDN_F32 ? launch_bwd<__nv_bfloat16, float, 1>(a, steps, part)
+                              : launch_bwd<__nv_bfloat16, __nv_bfloat16, 2>(a, steps, part);
 }
 
 }  // namespace gdn

@@ -93,7 +93,7 @@ def _sequences(x, cu_seqlens):
 
 
 def _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices, out,
-             final_state, return_carries, dev_status, check, g_name):
+             final_state, return_carries, workspace, dev_status, check, g_name):
     """Checks and the forward's call: (y, final state, carries, (c, pitches, number of sequences))."""
     dev, pitches, c = _inputs(x, g, i, lam, c, 3, g_name)
     B, T, D = x.shape
@@ -130,12 +130,14 @@ def _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, sta
         if need == (1 << 64) - 1:
             raise ValueError("sizes rejected by gdn_linear_recurrence_fwd")
         carries = torch.empty((need // (4 * D), D), dtype=torch.float32, device=dev)
+    need = L.gdn_linear_recurrence_fwd_workspace_size(B, T, D, N)
+    workspace, ws_bytes = _scratch(need, "gdn_linear_recurrence_fwd", workspace, dev)
     dev_status = _status(dev_status, check, dev)
     st = L.gdn_linear_recurrence_fwd(_ptr(x), _ptr(g), _ptr(i), _ptr(lam), c, *pitches, B, T, D,
                                      _DT[x.dtype], _DT[g.dtype], _ptr(initial_state),
                                      int(bool(output_final_state)), _ptr(final_state), _ptr(cu_seqlens),
                                      N, _ptr(state_indices), num_slots, _ptr(out), _ptr(carries),
-                                     _ptr(dev_status), _stream(dev))
+                                     _ptr(workspace), ws_bytes, _ptr(dev_status), _stream(dev))
     _lib.check("gdn_linear_recurrence_fwd", st)
     _raise_on_status("gdn_linear_recurrence_fwd", dev_status, check)
     return out, final_state, carries, (c, pitches, N)
@@ -143,30 +145,30 @@ def _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, sta
 
 def gated_linear_recurrence(x, g, initial_state=None, output_final_state=False, cu_seqlens=None, *,
                             state_indices=None, out=None, final_state=None, return_carries=False,
-                            dev_status=None, check=False
+                            workspace=None, dev_status=None, check=False
                             ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Forward through ``gdn_linear_recurrence_fwd`` with given log-decays g (at most 0).
 
     x [B, T, D]; g [B, T, D] in fp32 or x's dtype.  Returns ``(y, final_state or None)``, and with
     ``return_carries`` also what :func:`gated_linear_recurrence_bwd` starts from.  Also with a slot
     cache ``state_indices`` [N] (-1 = padding) on states [num_slots, D], ``cu_seqlens``, ``out``,
-    ``final_state``, ``dev_status`` and ``check`` as in :func:`chunk_gated_delta_rule`; a bad
+    ``final_state``, ``workspace``, ``dev_status`` and ``check`` as in :func:`chunk_gated_delta_rule`; a bad
     ``cu_seqlens`` leaves zero rows and every state as it was.
     """
     y, fin, carries, _ = _forward(x, g, None, None, 0.0, initial_state, output_final_state, cu_seqlens,
-                               state_indices, out, final_state, return_carries, dev_status, check, "g")
+                               state_indices, out, final_state, return_carries, workspace, dev_status, check, "g")
     return (y, fin, carries) if return_carries else (y, fin)
 
 
 def gated_linear_recurrence_fused_gates(x, r, i, lam, c=8.0, initial_state=None, output_final_state=False,
                                         cu_seqlens=None, *, state_indices=None, out=None, final_state=None,
-                                        return_carries=False, dev_status=None, check=False
+                                        return_carries=False, workspace=None, dev_status=None, check=False
                                         ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """:func:`gated_linear_recurrence` with its gates computed in the kernel: r, i [B, T, D] in fp32 or
     x's dtype, lam [D] fp32, c a constant of the layer."""
     _need(lam, "lam")
     y, fin, carries, _ = _forward(x, r, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices,
-                               out, final_state, return_carries, dev_status, check, "r")
+                               out, final_state, return_carries, workspace, dev_status, check, "r")
     return (y, fin, carries) if return_carries else (y, fin)
 
 
@@ -250,7 +252,7 @@ class _Recurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, g, i, lam, initial_state, c, output_final_state, cu_seqlens):
         y, fin, carries, call = _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, None,
-                                         None, None, any(ctx.needs_input_grad), None, False,
+                                         None, None, any(ctx.needs_input_grad), None, None, False,
                                          "g" if lam is None else "r")
         ctx.save_for_backward(x, g, i, lam, initial_state, cu_seqlens, carries)
         ctx.call = call

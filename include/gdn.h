@@ -563,11 +563,15 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
  *               get zeros.  NULL where only carries are wanted.
  *   carries     gdn_linear_recurrence_carries_size(...) bytes, or NULL: the state in front of
  *               every 32nd token, which the backward starts from.
+ *   workspace   gdn_linear_recurrence_fwd_workspace_size(...) bytes, 256-byte aligned; NULL when that
+ *               is 0.
  * A cu_seqlens that is not monotone from 0 to at most T is reported as GDN_DEV_BAD_CU_SEQLENS: y
  * is zero then and no state is read or written.  A NaN or infinity reaches what follows in its
  * sequence and channel and nothing else; an infinity may arrive as a NaN.
  */
 size_t gdn_linear_recurrence_carries_size(int B, int T, int D);
+
+size_t gdn_linear_recurrence_fwd_workspace_size(int B, int T, int D, int num_seqs);
 
 gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void* i, const float* lam,
                                        float c, long long x_pitch, long long g_pitch,
@@ -576,7 +580,8 @@ gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void*
                                        int output_final_state, float* final_state,
                                        const int32_t* cu_seqlens, int num_seqs,
                                        const int32_t* state_indices, int num_slots, void* y,
-                                       float* carries, int* dev_status, void* stream);
+                                       float* carries, void* workspace, size_t workspace_bytes,
+                                       int* dev_status, void* stream);
 
 /*
  * gdn_linear_recurrence_bwd -- gradients of gdn_linear_recurrence_fwd (no slot cache).

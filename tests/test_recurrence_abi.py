@@ -14,7 +14,7 @@ NONE = (1 << 64) - 1
 def fwd(**kw):
     a = dict(x=FAKE, g=FAKE, i=None, lam=None, c=8.0, px=64, pg=64, pi=64, B=2, T=16, D=64, io=_lib.GDN_BF16,
              gd=_lib.GDN_F32, init=None, ofs=0, fin=None, cu=None, N=0, si=None, slots=0, y=FAKE, carries=None,
-             status=None, stream=None)
+             ws=None, wsb=0, status=None, stream=None)
     a.update(kw)
     return _lib.load().gdn_linear_recurrence_fwd(*a.values())
 
@@ -76,6 +76,14 @@ def test_recurrence_batches():
     assert bwd(ws=FAKE + 16, wsb=need) == _lib.GDN_ERR_LAYOUT
     assert lib.gdn_linear_recurrence_carries_size(2, 65, 3) == 5 * 3 * 4
     assert lib.gdn_linear_recurrence_carries_size(2, 65, 0) == NONE
+    assert lib.gdn_linear_recurrence_fwd_workspace_size(2, 16, 64, 2) == 0      # one tile a sequence
+    long = dict(B=1, T=1 << 20, D=64, px=64, pg=64)                             # a chain that is cut into segments
+    need = lib.gdn_linear_recurrence_fwd_workspace_size(1, 1 << 20, 64, 1)
+    if need:                                                                    # (not where there is one SM, or none)
+        assert fwd(**long) == _lib.GDN_ERR_WORKSPACE
+        assert fwd(**long, ws=FAKE, wsb=need - 1) == _lib.GDN_ERR_WORKSPACE
+        assert fwd(**long, ws=FAKE + 128, wsb=need) == _lib.GDN_ERR_LAYOUT
+    assert lib.gdn_linear_recurrence_fwd_workspace_size(1, 1 << 20, 0, 1) == NONE
     assert lib.gdn_linear_recurrence_bwd_workspace_size(2, -1, 3, 2, 0) == NONE
 
 
