@@ -6,8 +6,8 @@
 // Forward: one reading of the inputs where there are channels and sequences for all SMs.  A CTA walks a part's
 // tokens a tile of kWarps windows at a time.  Each warp turns its window's inputs, which were copied ahead
 // into shared memory, into a and b in registers and into the window's (L, H), is handed the state in front
-// of its window and walks its tokens.  Few parts are cut into segments, for which a first launch
-// (kSteps) makes the segments' steps.
+// of its window and walks its tokens.  Few parts are cut into segments, whose steps a launch of their own
+// (kSteps) makes.
 #include <algorithm>
 
 #include "gdn_recurrence.cuh"
@@ -18,7 +18,7 @@ namespace {
 constexpr int kTau = 16;
 constexpr int kWarps = 16;
 constexpr int kTile = kWarps * kTau;
-constexpr double kFirst = 0.7;   // the first launch's time, of the second's
+constexpr double kFirst = 0.7;   // the time of a step, of running
 constexpr int kStages = 2;
 
 template <typename T, typename G, bool kFused, int N>
@@ -32,11 +32,11 @@ struct FwdShared {
   uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  states: where the first launch
-// keeps the sequences' initial states for the second, whose final states may take their place.
+// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  states: where the steps' launch
+// keeps sequences' initial states for the later one, whose final states may take their place.
 template <typename T, typename G, bool kFused, int N, bool kEngine, bool kSteps>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-    recurrence_fwd_kernel(RecurrenceArgs a, int parts, int segments, float* steps, float* states, int x_unit, int g_unit, int i_unit,
+    recurrence_fwd_kernel(RecurrenceArgs a, int parts, Segments segments, float* steps, float* states, int x_unit, int g_unit, int i_unit,
                           const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
   using Shared = FwdShared<T, G, kFused, N>;
@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const int segment = blockIdx.x % segments, part_index = blockIdx.x / segments % parts, block = blockIdx.x / segments / parts;
+  const int segment = segments.from + blockIdx.x % segments.here, part_index = blockIdx.x / segments.here % parts,
+            block = blockIdx.x / segments.here / parts;
   const int ch = block * W + lane * N;   // this lane's first channel
   const int mine = max(0, min(N, a.D - ch));
   WindowFinder finder;
@@ -54,8 +55,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   finder.num_slots = a.num_slots;
   if (a.cu_seqlens && !packed_lengths_fit(a.cu_seqlens, a.num_seqs, a.T)) {   // every row is zero
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.dev_status, GDN_DEV_BAD_CU_SEQLENS);
-    for (long long t = (part_index * segments + segment) * kWarps + warp; t < a.T && a.y && !kSteps;
-         t += parts * segments * kWarps)
+    for (long long t = (part_index * segments.count + segment) * kWarps + warp; t < a.T && a.y && !kSteps;
+         t += parts * segments.count * kWarps)
       write_row<false>(static_cast<T*>(a.y) + (size_t)t * a.D + ch, fill<N>(0.f), mine);
     wait_for_previous();
     return;
@@ -63,7 +64,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   finder.part = part_of(finder.seq, part_index, parts);
   const Part part = finder.part;
   // empty sequences' states, and bad slots
-  for (int n = part.n0 + segment * kWarps + warp; n < part.n1 && !kSteps; n += segments * kWarps) {
+  for (int n = part.n0 + segment * kWarps + warp; n < part.n1 && !kSteps; n += segments.count * kWarps) {
     int row = n;
     if (a.state_indices) {
       row = a.state_indices[n];
@@ -79,8 +80,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const Values rate = each([&](float lam) { return gate_rate(a.c, lam); }, read_state<N>(kFused ? a.lam + ch : nullptr, mine));
 
   const int tile0 = part.t0 / kTile, tiles = part.t1 > part.t0 ? (part.t1 - 1) / kTile - tile0 + 1 : 0;
-  const int first = tile0 + (int)((long long)tiles * segment / segments);
-  const int rounds = tile0 + (int)((long long)tiles * (segment + 1) / segments) - first;
+  const int first = tile0 + segments.tile(segment, tiles), rounds = tile0 + segments.tile(segment + 1, tiles) - first;
   auto window_start = [&](int round) { return (first + round) * kTile + warp * kTau; };
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
@@ -117,15 +117,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (int k = 0; k < kStages; ++k) fetch(k);
 
   next_may_start();
-  if (!kSteps && segments > 1) wait_for_previous();
+  if (!kSteps && segment > 0) wait_for_previous();
   if (warp == 0)
-    sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments * 2 * a.D, segment, a.D, ch, mine));
-  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of kSteps: the logarithms' sum, the state behind the segment
+    sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine));
+  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of a segment: the logarithms' sum, the state behind it
   bool lost = false, any_reset = false;
   // a first token's initial state: lane j's sequence, of which lanes know the cache's row and the number
+  const bool saved = !kSteps && states && segment > 0 && segment + 1 < segments.count;
   auto initial = [&](const Window& w, int j) {
-    const int row = __shfl_sync(~0u, !kSteps && states ? w.n : w.row, j);
-    const float* const from = !kSteps && states ? states : a.initial_state;
+    const int row = __shfl_sync(~0u, saved ? w.n : w.row, j);
+    const float* const from = saved ? states : a.initial_state;
     const Values h = read_state<N>(from ? from + (size_t)row * a.D + ch : nullptr, mine);
     if (kSteps && states) write_state(states + (size_t)__shfl_sync(~0u, w.n, j) * a.D + ch, h, mine);
     return h;
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
       }
     }
-    Values h = sh.chain.hand_over(warp, round, rounds, lane, L, H, reset != 0, kSteps ? &end : nullptr, &lost, a.dev_status);
+    Values h = sh.chain.hand_over(warp, round, rounds, lane, L, H, reset != 0, &end, &lost, a.dev_status);
     if (kSteps) {
       sum = sum + L;
       any_reset |= reset != 0;
@@ -203,6 +204,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
   }
   if (!kEngine) copies_wait<0>();
+  if (!kSteps && segment + 1 < segments.count && segment == 0 && warp + 1 == kWarps)   // (nothing is in front of it)
+    write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, end, end, true, mine);
   if (kSteps) {   // (a segment that resets takes nothing from in front of it, whatever L says)
     Values(*const sums)[32] = reinterpret_cast<Values(*)[32]>(sh.ring);
     any_reset = __syncthreads_or(any_reset);
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (warp + 1 < kWarps) return;
     sum = fill<N>(0.f);
     for (int k = 0; k < kWarps; ++k) sum = sum + sums[k][lane];
-    write_step(steps + ((size_t)part_index * segments + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
+    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
     wait_for_previous();
   }
 }
@@ -222,26 +225,12 @@ RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
 
 template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
 cudaError_t launch_fwd(const RecurrenceArgs& a, const RecurrencePlan& p, const Args&... args) {
-  constexpr auto run = recurrence_fwd_kernel<T, G, kFused, N, kEngine, false>;
-  constexpr auto make_steps = recurrence_fwd_kernel<T, G, kFused, N, kEngine, true>;
-  const size_t shared = sizeof(FwdShared<T, G, kFused, N>);
-  const unsigned ctas = (unsigned)((long long)p.blocks * p.parts * p.segments);
   float* const steps = static_cast<float*>(a.workspace);
   float* const states = p.segments > 1 && a.initial_state && a.final_state
                             ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256(steps_bytes(p, a.D)))
                             : nullptr;
-  cudaError_t err = allow_shared<run>(shared);
-  if (err != cudaSuccess) return err;
-  if (p.segments > 1) {
-    err = allow_shared<make_steps>(shared);
-    if (err != cudaSuccess) return err;
-    make_steps<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, states, args...);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    return launch_behind(run, ctas, kWarps * 32, shared, a.stream, a, p.parts, p.segments, steps, states, args...);
-  }
-  run<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, states, args...);
-  return cudaGetLastError();
+  return launch_segments<recurrence_fwd_kernel<T, G, kFused, N, kEngine, false>, recurrence_fwd_kernel<T, G, kFused, N, kEngine, true>>(
+      a, p, kFirst, kWarps * 32, sizeof(FwdShared<T, G, kFused, N>), steps, states, args...);
 }
 
 template <typename T, typename G, bool kFused, int N>

@@ -398,9 +398,20 @@ struct Chain {
 constexpr int kMaxSegments = 64;
 constexpr float kReset = __builtin_huge_valf();   // in L's place: "reset"
 
-// Where parts are too few for the SMs their tiles are cut into segments.  A first launch makes every segment's
-// step (L, H) from nothing in front of it, a second one runs each from the steps of those before it.
-// Steps: [parts][segments][2][D].
+// Where parts are too few for the SMs their tiles are cut into segments.  A first launch runs segment 0 of each,
+// which has nothing in front of it; beside it a second one makes the steps (L, H) of the others but the
+// last from nothing in front of them; a third one runs those and the last from the steps of the
+// segments before them.  Steps: [parts][segments][2][D].
+struct Segments {
+  int count, from, here;   // of a part; this launch's: [from, from + here)
+  float first;             // segment 0's length, of another's: what making a step takes, of running
+
+  // The first of a part's tiles that segment s has, of `tiles` from 0.
+  __host__ __device__ __forceinline__ int tile(int s, int tiles) const {
+    if (s == 0) return 0;
+    return s == count ? tiles : (int)((float)tiles * (first + (float)(s - 1)) / (first + (float)(count - 1)));
+  }
+};
 template <int N>
 __device__ __forceinline__ void write_step(float* steps, int D, int ch, const Lanes<N>& L, const Lanes<N>& H, bool reset,
                                            int mine) {
@@ -430,8 +441,8 @@ struct RecurrencePlan {
 // The plan with the least time, for CTAs (one an SM) of `width` channels and tiles of `tile` tokens: waves of CTAs, each as
 // many rounds as its longest part has and one more to start.  Parts are whole sequences: of equal ones the
 // longest part is known, of packed ones (whose lengths the host does not know) it is taken to be longer
-// than the mean by half a mean sequence.  The segments' first launch takes `first` of the second's time, and
-// another launch some two rounds.
+// than the mean by half a mean sequence.  With segments the launches side by side take `first` of the third
+// one's time; two more launches take some two rounds.
 inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packed, int width, int tile, double first) {
   const long long sms = std::max(1, current_sm_count());
   RecurrencePlan best{(D + width - 1) / width, 1, 1};
@@ -443,12 +454,12 @@ inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packe
     const double each = packed ? (double)tokens / parts + (parts > 1 ? 0.5 * (double)tokens / N : 0.)
                                : (double)tokens / N * ((N + parts - 1) / parts);
     const long long tiles = (long long)(each / tile) + 1;
-    for (int waves = 0; waves <= 4; ++waves) {   // as many segments as fill so many waves
+    for (int waves = 0; waves <= 4; ++waves) {   // as many segments a launch as fill so many waves
       const long long fill = waves * sms / ((long long)best.blocks * parts);
-      const int segments = (int)std::min<long long>({std::max(1LL, fill), tiles, (long long)kMaxSegments});
-      const long long ctas = (long long)best.blocks * parts * segments;
-      const double run = (double)((ctas + sms - 1) / sms) * (double)((tiles + segments - 1) / segments + 1);
-      const double time = segments > 1 ? run * (1. + first) + 2. : run;
+      const int segments = fill < 2 ? 1 : (int)std::min<long long>({fill + 1, tiles, (long long)kMaxSegments});
+      const long long ctas = (long long)best.blocks * parts * (segments > 1 ? segments - 1 : 1);
+      const double turns = (double)((ctas + sms - 1) / sms);
+      const double time = segments > 1 ? turns * (tiles * (1. + first) / (segments - 1 + first) + 2.) + 2. : turns * (double)(tiles + 1);
       if (time < 0.98 * least) {
         least = time;
         best.parts = parts;
@@ -462,6 +473,29 @@ inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packe
 inline size_t steps_bytes(const RecurrencePlan& p, int D) {
   return p.segments > 1 ? (size_t)p.parts * p.segments * 2 * D * sizeof(float) : 0;
 }
+// The launches of a plan: `run` and `make_steps` take a RecurrenceArgs, the parts, the Segments and what follows.
+template <auto run, auto make_steps, typename... Args>
+cudaError_t launch_segments(const RecurrenceArgs& a, const RecurrencePlan& p, double first, int threads, size_t shared,
+                            const Args&... args) {
+  cudaError_t err = allow_shared<run>(shared);
+  if (err != cudaSuccess) return err;
+  const long long chains = (long long)p.blocks * p.parts;
+  Segments s{p.segments, 0, 1, (float)first};
+  run<<<(unsigned)chains, threads, shared, a.stream>>>(a, p.parts, s, args...);
+  err = cudaGetLastError();
+  if (err != cudaSuccess || p.segments == 1) return err;
+  err = allow_shared<make_steps>(shared);
+  if (err != cudaSuccess) return err;
+  s.from = 1;
+  s.here = p.segments - 2;
+  if (s.here > 0) {
+    err = launch_behind(make_steps, (unsigned)(chains * s.here), threads, shared, a.stream, a, p.parts, s, args...);
+    if (err != cudaSuccess) return err;
+  }
+  s.here = p.segments - 1;
+  return launch_behind(run, (unsigned)(chains * s.here), threads, shared, a.stream, a, p.parts, s, args...);
+}
+
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 inline int copy_unit(const void* p, long long pitch, int D, int elem) {

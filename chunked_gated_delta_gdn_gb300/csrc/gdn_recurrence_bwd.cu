@@ -23,7 +23,7 @@ namespace {
 constexpr int kTau = 8;
 constexpr int kWarps = 16;
 constexpr int kTile = kWarps * kTau;
-constexpr double kFirst = 0.4;   // the segments' first launch's time, of the second's
+constexpr double kFirst = 0.4;   // the time of a step, of running
 constexpr int kStages = 2;
 constexpr int kGroup = kRecCarry / kTau;   // windows from one saved state to the next
 static_assert(kRecCarry % kTau == 0 && kTile % kRecCarry == 0, "saved states stand in front of windows");
@@ -45,7 +45,7 @@ struct BwdShared {
 // kEngine: the copy engine takes the inputs' rows, and outputs go out whole.
 template <typename T, typename G, bool kFused, int N, bool kEngine, bool kSteps>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-    recurrence_bwd_kernel(RecurrenceArgs a, int parts, int segments, float* steps, int x_unit, int g_unit, int i_unit, int dy_unit,
+    recurrence_bwd_kernel(RecurrenceArgs a, int parts, Segments segments, float* steps, int x_unit, int g_unit, int i_unit, int dy_unit,
                           float* dlam_part, const __grid_constant__ CUtensorMap x_map,
                           const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
@@ -55,18 +55,20 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const int segment = blockIdx.x % segments, part_index = blockIdx.x / segments % parts, block = blockIdx.x / segments / parts;
+  const int segment = segments.from + blockIdx.x % segments.here, part_index = blockIdx.x / segments.here % parts,
+            block = blockIdx.x / segments.here / parts;
   const int ch = block * W + lane * N;
   const int mine = max(0, min(N, a.D - ch));
   WindowFinder finder;
   finder.seq = Sequences{a.cu_seqlens, a.num_seqs, a.T, a.cu_seqlens ? a.T : a.B * a.T};
   finder.slots = nullptr;
   finder.num_slots = 0;
-  float* const dlam_row = dlam_part ? dlam_part + ((size_t)part_index * segments + segment) * a.D + ch : nullptr;
+  float* const dlam_row = dlam_part ? dlam_part + ((size_t)part_index * segments.count + segment) * a.D + ch : nullptr;
   if (a.cu_seqlens && !packed_lengths_fit(a.cu_seqlens, a.num_seqs, a.T)) {   // every gradient is zero
+    wait_for_previous();
     if (kSteps) return;
     if (blockIdx.x == 0 && threadIdx.x == 0) report(a.dev_status, GDN_DEV_BAD_CU_SEQLENS);
-    const int step = parts * segments * kWarps, first = (part_index * segments + segment) * kWarps + warp;
+    const int step = parts * segments.count * kWarps, first = (part_index * segments.count + segment) * kWarps + warp;
     const Values zero = fill<N>(0.f);
     for (long long t = first; t < a.T; t += step) {
       const size_t at = (size_t)t * a.D + ch;
@@ -77,13 +79,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     for (long long n = first; n < a.num_seqs && a.d_initial_state; n += step)
       write_state(a.d_initial_state + (size_t)n * a.D + ch, zero, mine);
     if (dlam_row && warp == 0) write_state(dlam_row, zero, mine);
-    wait_for_previous();
     return;
   }
   finder.part = part_of(finder.seq, part_index, parts);
   const Part part = finder.part;
   if (a.d_initial_state && !kSteps) {   // empty sequences
-    for (int n = part.n0 + segment * kWarps + warp; n < part.n1; n += segments * kWarps) {
+    for (int n = part.n0 + segment * kWarps + warp; n < part.n1; n += segments.count * kWarps) {
       if (finder.seq.end(n) > finder.seq.begin(n)) continue;
       const size_t at = (size_t)n * a.D + ch;
       write_state(a.d_initial_state + at, read_state<N>(a.d_final_state ? a.d_final_state + at : nullptr, mine), mine);
@@ -98,8 +99,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 
   // segment 0 is the rightmost one
   const int tile0 = part.t0 / kTile, tiles = part.t1 > part.t0 ? (part.t1 - 1) / kTile - tile0 + 1 : 0;
-  const int first = tile0 + tiles - 1 - (int)((long long)tiles * segment / segments);
-  const int rounds = first - (tile0 + tiles - 1 - (int)((long long)tiles * (segment + 1) / segments));
+  const int first = tile0 + tiles - 1 - segments.tile(segment, tiles);
+  const int rounds = segments.tile(segment + 1, tiles) - segments.tile(segment, tiles);
   auto tile_of = [&](int round) { return first - round; };
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
@@ -139,10 +140,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (int k = 0; k < kStages; ++k) fetch(k);
 
   next_may_start();
-  if (!kSteps && segments > 1) wait_for_previous();
+  if (!kSteps && segment > 0) wait_for_previous();
   if (warp + 1 == kWarps)
-    sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments * 2 * a.D, segment, a.D, ch, mine));
-  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of kSteps: the logarithms' sum, e in front of the segment
+    sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine));
+  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of a segment: the logarithms' sum, e in front of it
   bool lost = false, any_reset = false;
   for (int round = 0; round < rounds; ++round) {
     const int tile = tile_of(round), w0 = tile * kTile + warp * kTau;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (lane == 0) mbar_arrive(&sh.state_full[warp + 1]);
     }
     const int order = kWarps - 1 - warp;
-    Values e = sh.chain.hand_over(order, round, rounds, lane, L, E, reset_e != 0, kSteps ? &end : nullptr, &lost, a.dev_status);
+    Values e = sh.chain.hand_over(order, round, rounds, lane, L, E, reset_e != 0, &end, &lost, a.dev_status);
     if (kSteps) {
       sum = sum + L;
       any_reset |= reset_e != 0;
@@ -304,6 +305,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     fetch(round + kStages);
   }
   if (!kEngine) copies_wait<0>();
+  if (!kSteps && segment + 1 < segments.count && segment == 0 && warp == 0)   // (nothing is behind it)
+    write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, end, end, true, mine);
   if (kSteps) {   // (a segment that resets takes nothing from behind it, whatever L says)
     Values(*const sums)[32] = reinterpret_cast<Values(*)[32]>(sh.ring);
     any_reset = __syncthreads_or(any_reset);
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (warp > 0) return;   // the last one of the chain
     sum = fill<N>(0.f);
     for (int k = 0; k < kWarps; ++k) sum = sum + sums[k][lane];
-    write_step(steps + ((size_t)part_index * segments + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
+    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
     wait_for_previous();
     return;
   }
@@ -353,22 +356,8 @@ RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
 
 template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
 cudaError_t launch_bwd(const RecurrenceArgs& a, const RecurrencePlan& p, float* steps, const Args&... args) {
-  constexpr auto run = recurrence_bwd_kernel<T, G, kFused, N, kEngine, false>;
-  constexpr auto make_steps = recurrence_bwd_kernel<T, G, kFused, N, kEngine, true>;
-  const size_t shared = sizeof(BwdShared<T, G, kFused, N>);
-  const unsigned ctas = (unsigned)((long long)p.blocks * p.parts * p.segments);
-  cudaError_t err = allow_shared<run>(shared);
-  if (err != cudaSuccess) return err;
-  if (p.segments > 1) {
-    err = allow_shared<make_steps>(shared);
-    if (err != cudaSuccess) return err;
-    make_steps<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, args...);
-    err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    return launch_behind(run, ctas, kWarps * 32, shared, a.stream, a, p.parts, p.segments, steps, args...);
-  }
-  run<<<ctas, kWarps * 32, shared, a.stream>>>(a, p.parts, p.segments, steps, args...);
-  return cudaGetLastError();
+  return launch_segments<recurrence_bwd_kernel<T, G, kFused, N, kEngine, false>, recurrence_bwd_kernel<T, G, kFused, N, kEngine, true>>(
+      a, p, kFirst, kWarps * 32, sizeof(BwdShared<T, G, kFused, N>), steps, args...);
 }
 
 template <typename T, typename G, bool kFused, int N>
