@@ -259,26 +259,71 @@ cudaError_t launch_fwd(const RecurrenceArgs& a) {
 
 constexpr int kDecodeThreads = 128;
 
-__global__ void recurrence_decode_kernel(RecurrenceArgs a) {
-  const int n = blockIdx.y, d = blockIdx.x * kDecodeThreads + threadIdx.x;
-  if (d >= a.D) return;
-  const int slot = a.batch_indices ? a.batch_indices[n] : n;
-  if (slot < 0 || slot >= a.num_slots) {
-    if (slot != -1 && d == 0) report(a.dev_status, GDN_DEV_BAD_SLOT);
-    store_elem(a.y, (size_t)n * a.D + d, 0.f, a.io_dtype);
-    return;
+// A thread has V channels of a few requests; what a channel's gates have in common it makes once.
+template <typename T, typename G, bool kFused, int V>
+__global__ void __launch_bounds__(kDecodeThreads) recurrence_decode_kernel(RecurrenceArgs a, int requests) {
+  const int ch = (blockIdx.x * kDecodeThreads + threadIdx.x) * V;
+  if (ch >= a.D) return;
+  struct alignas(V * sizeof(T)) PackT { T e[V]; };
+  struct alignas(V * sizeof(G)) PackG { G e[V]; };
+  struct alignas(V * sizeof(float)) PackF { float e[V]; };
+  float rate[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) rate[j] = kFused ? -a.c * softplus_f(a.lam[ch + j]) : 0.f;
+  const int first = blockIdx.y * requests;
+#pragma unroll 2
+  for (int n = first; n < min(first + requests, a.n); ++n) {
+    const int slot = a.batch_indices ? a.batch_indices[n] : n;
+    PackT out;
+    if (slot < 0 || slot >= a.num_slots) {
+      if (slot != -1 && ch == 0) report(a.dev_status, GDN_DEV_BAD_SLOT);
+#pragma unroll
+      for (int j = 0; j < V; ++j) out.e[j] = (T)0.f;
+    } else {
+      PackF* const at = reinterpret_cast<PackF*>(a.state + (size_t)slot * a.D + ch);
+      PackF h = *at;
+      const PackT x = *reinterpret_cast<const PackT*>(static_cast<const T*>(a.x) + (size_t)n * a.x_pitch + ch);
+      const PackG g = *reinterpret_cast<const PackG*>(static_cast<const G*>(a.g) + (size_t)n * a.g_pitch + ch);
+      PackG i = g;
+      if (kFused) i = *reinterpret_cast<const PackG*>(static_cast<const G*>(a.i) + (size_t)n * a.i_pitch + ch);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        float la = (float)g.e[j], b = (float)x.e[j];
+        if (kFused) la = rate[j] * gate_sigmoid(la);
+        // a - 1, not a: rounding a would err in the same direction at every token of a long memory.  Short
+        // memories take a itself, as h + (a - 1) h would lose what is left of h there.
+        const float less = expm1f(la);
+        if (kFused) b *= sqrtf(-less * (2.f + less)) * gate_sigmoid((float)i.e[j]);
+        h.e[j] = la < -0.7f ? fmaf(expf(la), h.e[j], b) : h.e[j] + fmaf(less, h.e[j], b);
+        out.e[j] = (T)h.e[j];
+      }
+      *at = h;
+    }
+    *reinterpret_cast<PackT*>(static_cast<T*>(a.y) + (size_t)n * a.D + ch) = out;
   }
-  float la = load_elem(a.g, (size_t)n * a.g_pitch + d, a.g_dtype);
-  float b = load_elem(a.x, (size_t)n * a.x_pitch + d, a.io_dtype);
-  if (a.lam) {
-    const DecodeGate f(la, load_elem(a.i, (size_t)n * a.i_pitch + d, a.g_dtype), -a.c * softplus_f(a.lam[d]));
-    la = f.la;
-    b *= f.into;
-  }
-  float* const state = a.state + (size_t)slot * a.D + d;
-  const float h = decayed(la, *state, b);
-  *state = h;
-  store_elem(a.y, (size_t)n * a.D + d, h, a.io_dtype);
+}
+
+template <typename T, typename G, bool kFused>
+cudaError_t launch_decode(const RecurrenceArgs& a) {
+  const bool four = a.D % 4 == 0 && reinterpret_cast<uintptr_t>(a.state) % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.x) % (4 * sizeof(T)) == 0 && a.x_pitch % 4 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.y) % (4 * sizeof(T)) == 0 &&
+                    reinterpret_cast<uintptr_t>(a.g) % (4 * sizeof(G)) == 0 && a.g_pitch % 4 == 0 &&
+                    (!kFused || (reinterpret_cast<uintptr_t>(a.i) % (4 * sizeof(G)) == 0 && a.i_pitch % 4 == 0));
+  const int per = kDecodeThreads * (four ? 4 : 1);
+  const unsigned blocks = (unsigned)(((long long)a.D + per - 1) / per);
+  // as many requests a CTA as leave eight CTAs an SM, and no more than 65535 rows of them
+  const long long want = std::max(1LL, 8LL * std::max(1, current_sm_count()) / blocks);
+  const int requests = (int)std::max<long long>((a.n + want - 1) / want, (a.n + 65534) / 65535);
+  const dim3 grid(blocks, (unsigned)((a.n + requests - 1) / requests));
+  if (four) recurrence_decode_kernel<T, G, kFused, 4><<<grid, kDecodeThreads, 0, a.stream>>>(a, requests);
+  else recurrence_decode_kernel<T, G, kFused, 1><<<grid, kDecodeThreads, 0, a.stream>>>(a, requests);
+  return cudaGetLastError();
+}
+
+template <typename T, typename G>
+cudaError_t launch_decode(const RecurrenceArgs& a) {
+  return a.lam ? launch_decode<T, G, true>(a) : launch_decode<T, G, false>(a);
 }
 
 }  // namespace
@@ -304,8 +349,8 @@ cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a) {
 }
 
 cudaError_t launch_recurrence_decode(const RecurrenceArgs& a) {
-  recurrence_decode_kernel<<<dim3((a.D + kDecodeThreads - 1) / kDecodeThreads, a.n), kDecodeThreads, 0, a.stream>>>(a);
-  return cudaGetLastError();
+  if (a.io_dtype == GDN_F32) return launch_decode<float, float>(a);
+  return a.g_dtype == GDN_F32 ? launch_decode<__nv_bfloat16, float>(a) : launch_decode<__nv_bfloat16, __nv_bfloat16>(a);
 }
 
 }  // namespace gdn

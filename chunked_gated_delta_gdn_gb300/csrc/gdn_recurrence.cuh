@@ -80,12 +80,6 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float rsqrt_approx(float x) {
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // 1 / (1 + e^-x).
 __device__ __forceinline__ float gate_sigmoid(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
 
@@ -99,23 +93,6 @@ __device__ __forceinline__ float one_minus_square(float l, float a) {
 
 // The logarithm (to base 2) of a_t at an open recurrence gate.
 __device__ __forceinline__ float gate_rate(float c, float lam) { return -c * softplus_f(lam) * kLog2e; }
-
-// Decode's token of one channel, by the full functions: log a = la, and s sigmoid(i).
-struct DecodeGate {
-  float la, into;
-  __device__ __forceinline__ DecodeGate(float r, float i, float minus_c_softplus) {
-    la = minus_c_softplus * sigmoid_f(r);
-    into = sqrtf(-expm1f(2.f * la)) * sigmoid_f(i);
-  }
-};
-
-// a h + b, a = exp(la), for a state that is rounded at every token (decode): without the error that
-// rounding a makes in the same direction at every token of a long memory (1 - a to 24 bits instead of
-// a); short memories take a itself, as h + (a - 1) h would lose what is left of h there.
-__device__ __forceinline__ float decayed(float la, float h, float b) {
-  if (la < -0.7f) return fmaf(expf(la), h, b);
-  return h + fmaf(expm1f(la), h, b);
-}
 
 // ---------------------------------------------------------------- sequences
 

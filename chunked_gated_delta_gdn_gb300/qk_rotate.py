@@ -155,7 +155,7 @@ def _backward(d_q, d_k, q, k, inv_freq, positions, q_weight, k_weight, call, int
     ws_bytes = 0
     if need_weights:
         B, T, Hq, Hk, K = call.sizes[2:7]
-        dwq, dwk = torch.empty((2, K), dtype=torch.float32, device=dev).unbind(0)
+        dwq, dwk = torch.empty(K, dtype=torch.float32, device=dev), torch.empty(K, dtype=torch.float32, device=dev)
         need = L.gdn_qk_norm_rotate_bwd_workspace_size(B, T, Hq, Hk, K, 1)
         workspace, ws_bytes = _scratch(need, "gdn_qk_norm_rotate_bwd", workspace, dev)
     elif workspace is not None:
