@@ -8,8 +8,8 @@
 // them, where tokens are few), whose sines and cosines they make once; the 32 / G groups of a warp have
 // tokens of their own.  CTAs work on queries or on keys, in proportion, so that weights and their
 // gradients stay in registers.  A lane's unit is two vectors of V values whose pairs are complete: of the two
-// halves, or, interleaved, two in a row; behind the rotated part two in a row.  Lanes copy heads ahead
-// into rings of their own in shared memory (asynchronous copies, no barrier).
+// halves, or, interleaved, any two.  Lanes copy heads ahead into rings of their own in shared memory
+// (asynchronous copies, no barrier).
 //
 // Angles: phi / 2 pi as a fraction of 2^64, position * round(2^64 frac(inv_freq / 2 pi)) in integers
 // that wrap, is exact to 2^-11 of fp32's rounding for every position.  What is left is less than half a
@@ -31,48 +31,72 @@ constexpr double kAngles = 1.5;   // the time of a token's angles, in heads
 template <typename T, int V> struct alignas(V * sizeof(T)) Vec { T e[V]; };
 
 template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V>& raw, float (&x)[V]) {
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    const unsigned* const two = reinterpret_cast<const unsigned*>(&raw);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      x[j] = __uint_as_float(two[j / 2] << 16);
+      x[j + 1] = __uint_as_float(two[j / 2] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = (float)raw.e[j];
+  }
+}
+template <typename T, int V>
 __device__ __forceinline__ void store(T* p, const float (&x)[V]) {
   Vec<T, V> v;
+  if constexpr (sizeof(T) == 2 && V > 1) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) v.e[j] = (T)x[j];
+    for (int j = 0; j < V; j += 2) reinterpret_cast<__nv_bfloat162*>(&v)[j / 2] = __floats2bfloat162_rn(x[j], x[j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v.e[j] = (T)x[j];
+  }
   *reinterpret_cast<Vec<T, V>*>(p) = v;
 }
 
-// V values from global to shared memory, asynchronously (but for two bytes, which such copies do not have).
+// V values from global to shared memory, asynchronously.
 template <typename T, int V>
 __device__ __forceinline__ void copy_ahead(Vec<T, V>* dst, const T* src) {
   constexpr int kBytes = V * sizeof(T);
+  static_assert(kBytes >= 4, "asynchronous copies have at least four bytes");
   if constexpr (kBytes == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
-  else if constexpr (kBytes >= 4)
+  else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src), "n"(kBytes)
                  : "memory");
-  else
-    *dst = *reinterpret_cast<const Vec<T, V>*>(src);
 }
 
-// What a lane holds of a head: unit u's two vectors start at o1 and o2.
+// What a lane holds of a head: unit u's two vectors start at o1 and o2, so that neighbouring lanes' vectors
+// are neighbours in memory.  (V = 1, interleaved: the two values of a pair.)
 struct Unit {
   int o1, o2;
   bool on, second, turns;
-  int pair;
 };
 template <int V>
 __device__ __forceinline__ Unit unit_of(const QkRotateArgs& a, int u) {
-  const int turning = a.R / (2 * V);
+  const int turning = a.R / (2 * V), behind = ((a.K - a.R) / V + 1) / 2;
   Unit r;
   r.turns = u < turning;
   if (r.turns) {
-    r.o1 = a.interleaved ? 2 * u * V : u * V;
-    r.o2 = a.interleaved ? r.o1 + V : r.o1 + a.R / 2;
+    const bool apart = V > 1 || !a.interleaved;
+    r.o1 = apart ? u * V : 2 * u;
+    r.o2 = apart ? r.o1 + a.R / 2 : r.o1 + 1;
+    r.on = r.second = true;
   } else {
-    r.o1 = a.R + 2 * (u - turning) * V;
-    r.o2 = r.o1 + V;
+    r.o1 = a.R + (u - turning) * V;
+    r.o2 = r.o1 + behind * V;
+    r.on = u - turning < behind;
+    r.second = r.on && r.o2 < a.K;
   }
-  r.pair = u * V;
-  r.on = r.o1 < a.K;
-  r.second = r.on && r.o2 < a.K;
   return r;
+}
+// The j-th of a unit's V pairs.
+template <int V, bool kInVector>
+__device__ __forceinline__ int pair_of(const Unit& u, int j) {
+  return kInVector ? (j < V / 2 ? u.o1 / 2 + j : u.o2 / 2 + j - V / 2) : V == 1 && u.o2 == u.o1 + 1 ? u.o1 / 2 : u.o1 + j;
 }
 
 // frac(f / 2 pi) in units of 2^-64.
@@ -101,9 +125,14 @@ __device__ __forceinline__ float group_sum(float x, int G) {
   return x;
 }
 
-// One side's share of a launch: CTAs [first, first + ctas), items of nh heads.
+// One side's share of a launch: CTAs [first, first + ctas).  Tokens [from, to) in items of nh heads, `splits` of them
+// a token; then the tokens that do not fill a turn of all groups, in smaller items.
+struct Run {
+  int from, to, splits, nh;
+};
 struct SidePlan {
-  int first, ctas, splits, nh;
+  int first, ctas;
+  Run run[2];
 };
 struct Plan {
   int G;
@@ -112,7 +141,7 @@ struct Plan {
 
 template <typename T, int V, int NU, bool kBwd>
 struct Ring {
-  static constexpr int kDepth = kBwd ? 4 : 6;
+  static constexpr int kDepth = 3;   // (deeper, DRAM does less: 4 x 32768 x 32 x 128 forward 328 us with 3, 375 with 4 or 6)
   static constexpr int kVecs = NU * 2 * (kBwd ? 2 : 1);
   Vec<T, V> slot[kWarps][kDepth][kVecs][32];
 };
@@ -143,40 +172,67 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
       w[m][1][j] = side.w && unit[m].second ? load_elem(side.w, unit[m].o2 + j, a.w_dtype) : 1.f;
     }
   }
+  for (int k = 0; k < R::kDepth * R::kVecs; ++k) {   // what no copy writes is zero
+    const int v = k % R::kVecs % (2 * NU);
+    bool on = false;
+#pragma unroll
+    for (int m = 0; m < NU; ++m) on |= v == 2 * m ? unit[m].on : v == 2 * m + 1 && unit[m].second;
+    if (!on) ring.slot[warp][k / R::kVecs][k % R::kVecs][lane] = Vec<T, V>{};
+  }
   const float mean = a.norm == GDN_NORM_RMS ? 1.f / (float)a.K : 1.f;
-  const long long tokens = (long long)a.B * a.T, items = tokens * sp.splits;
-  const long long stride = (long long)sp.ctas * kWarps * groups;
+  const long long tokens = (long long)a.B * a.T, stride = (long long)sp.ctas * kWarps * groups;
   const long long base0 = ((long long)(blockIdx.x - sp.first) * kWarps + warp) * groups;
+  float acc[NU][2][V];
+#pragma unroll
+  for (int m = 0; m < NU; ++m)
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[m][0][j] = acc[m][1][j] = 0.f;
+  for (int which = 0; which < 2; ++which) {
+  const Run run = which ? sp.run[1] : sp.run[0];
+  const long long items = (long long)(run.to - run.from) * run.splits;
   const long long turns = base0 < items ? (items - base0 + stride - 1) / stride : 0;   // items of the warp's first group
 
   // the copies run kDepth - 1 heads ahead of the work
   long long ahead_item = base0 + hs;
   int ahead_h = 0, ahead_slot = 0;
-  long long ahead_left = turns * sp.nh;
+  long long ahead_left = turns * run.nh;
   const T* ahead_x = nullptr;
   const T* ahead_dy = nullptr;
   auto copy_head = [&]() {
     if (ahead_left > 0) {
       if (ahead_h == 0) {
         const long long item = ahead_item < items ? ahead_item : items - 1;   // (a spare group reads the last one)
-        const long long token = sp.splits == 1 ? item : item / sp.splits;
-        const int h0 = (int)(item - token * sp.splits) * sp.nh;
+        const int part = run.splits == 1 ? 0 : (int)(item % run.splits), h0 = part * run.nh;
+        const long long token = run.from + (run.splits == 1 ? item : item / run.splits);
         const int b = (int)token / a.T, t = (int)token - b * a.T;
         ahead_x = static_cast<const T*>(side.x) + b * side.sb + t * side.st + h0 * side.sh;
         if (kBwd) ahead_dy = static_cast<const T*>(side.dy) + (token * side.H + h0) * a.K;
       }
+      Vec<T, V>(*const to)[32] = ring.slot[warp][ahead_slot];
+      if constexpr (V * sizeof(T) >= 4) {
 #pragma unroll
-      for (int m = 0; m < NU; ++m) {
-        if (unit[m].on) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * m][lane], ahead_x + unit[m].o1);
-        if (unit[m].second) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * m + 1][lane], ahead_x + unit[m].o2);
-        if (kBwd) {
-          if (unit[m].on) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * (NU + m)][lane], ahead_dy + unit[m].o1);
-          if (unit[m].second) copy_ahead<T, V>(&ring.slot[warp][ahead_slot][2 * (NU + m) + 1][lane], ahead_dy + unit[m].o2);
+        for (int m = 0; m < NU; ++m) {
+          if (unit[m].on) copy_ahead<T, V>(&to[2 * m][lane], ahead_x + unit[m].o1);
+          if (unit[m].second) copy_ahead<T, V>(&to[2 * m + 1][lane], ahead_x + unit[m].o2);
+          if (kBwd) {
+            if (unit[m].on) copy_ahead<T, V>(&to[2 * (NU + m)][lane], ahead_dy + unit[m].o1);
+            if (unit[m].second) copy_ahead<T, V>(&to[2 * (NU + m) + 1][lane], ahead_dy + unit[m].o2);
+          }
         }
+      } else {   // two bytes: by loads, all of them before the first store
+        T one[R::kVecs];
+#pragma unroll
+        for (int v = 0; v < R::kVecs; ++v) {
+          const Unit& u = unit[v % (2 * NU) / 2];
+          const T* const from = v < 2 * NU ? ahead_x : ahead_dy;
+          one[v] = (v & 1 ? u.second : u.on) ? from[v & 1 ? u.o2 : u.o1] : (T)0.f;
+        }
+#pragma unroll
+        for (int v = 0; v < R::kVecs; ++v) to[v][lane].e[0] = one[v];
       }
       ahead_x += side.sh;
       if (kBwd) ahead_dy += a.K;
-      if (++ahead_h == sp.nh) {
+      if (++ahead_h == run.nh) {
         ahead_h = 0;
         ahead_item += stride;
       }
@@ -187,16 +243,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
   };
   for (int k = 0; k < R::kDepth - 1; ++k) copy_head();
 
-  float acc[NU][2][V];
-#pragma unroll
-  for (int m = 0; m < NU; ++m)
-#pragma unroll
-    for (int j = 0; j < V; ++j) acc[m][0][j] = acc[m][1][j] = 0.f;
   // the positions of an item's token on every axis, read an item ahead
   int at[GDN_MAX_AXES] = {0, 0, 0, 0};
   auto positions_of = [&](long long item) {
     if (item >= items) return;
-    const long long token = sp.splits == 1 ? item : item / sp.splits;
+    const long long token = run.from + (run.splits == 1 ? item : item / run.splits);
     if (!a.positions) {
 #pragma unroll
       for (int i = 0; i < GDN_MAX_AXES; ++i) at[i] = (int)token % a.T;
@@ -211,8 +262,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
   for (long long n = 0; n < turns; ++n) {
     const long long item = base0 + hs + n * stride;
     const bool here = item < items;
-    const long long token = here ? (sp.splits == 1 ? item : item / sp.splits) : 0;
-    const int h0 = here ? (int)(item - token * sp.splits) * sp.nh : 0;
+    const long long token = here ? run.from + (run.splits == 1 ? item : item / run.splits) : 0;
+    const int h0 = here && run.splits > 1 ? (int)(item % run.splits) * run.nh : 0;
     float c[NU][V], s[NU][V];
 #pragma unroll
     for (int m = 0; m < NU; ++m)
@@ -221,16 +272,31 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
         c[m][j] = 1.f;
         s[m][j] = 0.f;
         if (unit[m].turns) {
-          const int pair = unit[m].pair + j;
+          const int pair = pair_of<V, kInVector>(unit[m], j);
           int position = at[0];
 #pragma unroll
           for (int i = 1; i < GDN_MAX_AXES; ++i) position = pair >= a.axis_end[i - 1] ? at[i] : position;
           angle<kFast>(rates[pair], position, &s[m][j], &c[m][j]);
         }
       }
+    // forward: the turn's factors with the weights in them, y1 = r (x1 f1 - x2 f2), y2 = r (x2 f3 + x1 f4)
+    float f[kBwd ? 1 : NU][4][V];
+    if constexpr (!kBwd) {
+#pragma unroll
+      for (int m = 0; m < NU; ++m)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float w1 = kInVector ? w[m][2 * j / V][2 * j % V] : w[m][0][j];
+          const float w2 = kInVector ? w[m][2 * j / V][2 * j % V + 1] : w[m][1][j];
+          f[m][0][j] = w1 * c[m][j];
+          f[m][1][j] = w2 * s[m][j];
+          f[m][2][j] = w2 * c[m][j];
+          f[m][3][j] = w1 * s[m][j];
+        }
+    }
     positions_of(item + stride);
     T* out = static_cast<T*>(side.out) + (token * side.H + h0) * a.K;
-    for (int h = 0; h < sp.nh; ++h, out += a.K) {
+    for (int h = 0; h < run.nh; ++h, out += a.K) {
       copy_head();
       asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
       float x[NU][2][V], ss = 0.f;
@@ -238,13 +304,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
       for (int m = 0; m < NU; ++m)
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const Vec<T, V> raw = ring.slot[warp][slot][2 * m + v][lane];
-          const bool on = v ? unit[m].second : unit[m].on;
+          unpack<T, V>(ring.slot[warp][slot][2 * m + v][lane], x[m][v]);
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            x[m][v][j] = on ? (float)raw.e[j] : 0.f;
-            ss = fmaf(x[m][v][j], x[m][v][j], ss);
-          }
+          for (int j = 0; j < V; ++j) ss = fmaf(x[m][v][j], x[m][v][j], ss);
         }
       const float inv = a.norm == GDN_NORM_NONE ? 1.f : rsqrtf(fmaf(group_sum(ss, G), mean, a.eps));
       if constexpr (!kBwd) {
@@ -252,88 +314,52 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
         for (int m = 0; m < NU; ++m) {
           float y[2][V];
 #pragma unroll
-          for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[m][v][j] *= inv * w[m][v][j];
-          if (kInVector) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-              for (int j = 0; j < V; j += 2) {
-                const float cc = c[m][(v * V + j) / 2], sn = s[m][(v * V + j) / 2];
-                y[v][j] = x[m][v][j] * cc - x[m][v][j + 1] * sn;
-                y[v][j + 1] = x[m][v][j + 1] * cc + x[m][v][j] * sn;
-              }
-          } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              y[0][j] = x[m][0][j] * c[m][j] - x[m][1][j] * s[m][j];
-              y[1][j] = x[m][1][j] * c[m][j] + x[m][0][j] * s[m][j];
-            }
-          }
-          if (!unit[m].turns) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              y[0][j] = x[m][0][j];
-              y[1][j] = x[m][1][j];
-            }
+          for (int j = 0; j < V; ++j) {   // pair j (behind the rotated part: an angle of 0)
+            const int v1 = kInVector ? 2 * j / V : 0, v2 = kInVector ? v1 : 1, j1 = kInVector ? 2 * j % V : j,
+                      j2 = kInVector ? j1 + 1 : j;
+            y[v1][j1] = inv * fmaf(x[m][v1][j1], f[m][0][j], -x[m][v2][j2] * f[m][1][j]);
+            y[v2][j2] = inv * fmaf(x[m][v2][j2], f[m][2][j], x[m][v1][j1] * f[m][3][j]);
           }
           if (here && unit[m].on) store<T, V>(out + unit[m].o1, y[0]);
           if (here && unit[m].second) store<T, V>(out + unit[m].o2, y[1]);
         }
       } else {
+        // with d r in d's place: dw += d x,  dx = d w - x r^2 mean(d w x)
         float d[NU][2][V], dot = 0.f;
 #pragma unroll
         for (int m = 0; m < NU; ++m) {
           float r[2][V];
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
-            const Vec<T, V> raw = ring.slot[warp][slot][2 * (NU + m) + v][lane];
-            const bool on = here && (v ? unit[m].second : unit[m].on);
+            unpack<T, V>(ring.slot[warp][slot][2 * (NU + m) + v][lane], r[v]);
 #pragma unroll
-            for (int j = 0; j < V; ++j) r[v][j] = on ? (float)raw.e[j] : 0.f;
+            for (int j = 0; j < V; ++j) r[v][j] *= inv;
           }
-          if (kInVector) {
 #pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-              for (int j = 0; j < V; j += 2) {
-                const float cc = c[m][(v * V + j) / 2], sn = s[m][(v * V + j) / 2];
-                d[m][v][j] = r[v][j] * cc + r[v][j + 1] * sn;
-                d[m][v][j + 1] = r[v][j + 1] * cc - r[v][j] * sn;
-              }
-          } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              d[m][0][j] = r[0][j] * c[m][j] + r[1][j] * s[m][j];
-              d[m][1][j] = r[1][j] * c[m][j] - r[0][j] * s[m][j];
-            }
-          }
-          if (!unit[m].turns) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              d[m][0][j] = r[0][j];
-              d[m][1][j] = r[1][j];
-            }
+          for (int j = 0; j < V; ++j) {
+            const int v1 = kInVector ? 2 * j / V : 0, v2 = kInVector ? v1 : 1, j1 = kInVector ? 2 * j % V : j,
+                      j2 = kInVector ? j1 + 1 : j;
+            d[m][v1][j1] = fmaf(r[v1][j1], c[m][j], r[v2][j2] * s[m][j]);
+            d[m][v2][j2] = fmaf(r[v2][j2], c[m][j], -r[v1][j1] * s[m][j]);
           }
 #pragma unroll
           for (int v = 0; v < 2; ++v)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-              x[m][v][j] *= inv;
               if (here) acc[m][v][j] = fmaf(d[m][v][j], x[m][v][j], acc[m][v][j]);
               d[m][v][j] *= w[m][v][j];
               dot = fmaf(d[m][v][j], x[m][v][j], dot);
             }
         }
-        dot = a.norm == GDN_NORM_NONE ? 0.f : group_sum(dot, G) * mean;
+        const float k = a.norm == GDN_NORM_NONE ? 0.f : group_sum(dot, G) * mean * inv * inv;
 #pragma unroll
         for (int m = 0; m < NU; ++m) {
+          if (a.norm != GDN_NORM_NONE) {
 #pragma unroll
-          for (int v = 0; v < 2; ++v)
+            for (int v = 0; v < 2; ++v)
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-              d[m][v][j] = a.norm == GDN_NORM_NONE ? d[m][v][j] : inv * fmaf(-x[m][v][j], dot, d[m][v][j]);
+              for (int j = 0; j < V; ++j) d[m][v][j] = fmaf(-x[m][v][j], k, d[m][v][j]);
+          }
           if (here && unit[m].on) store<T, V>(out + unit[m].o1, d[m][0]);
           if (here && unit[m].second) store<T, V>(out + unit[m].o2, d[m][1]);
         }
@@ -342,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+  }
   if (!kBwd || !part) return;
   // this CTA's sums: over the groups of a warp, then over the warps in order
   __syncthreads();
@@ -400,7 +427,8 @@ int vector_width(const QkRotateArgs& a, bool bwd) {
 }
 
 // CTAs for queries and keys in proportion to their heads (a token's angles count as kAngles more); a token's
-// heads are shared out as far as the longest run of a group of lanes gets shorter by it.
+// heads are shared out as far as the longest run of a group of lanes gets shorter by it (19462 tokens of
+// 12 heads: 65 us with a fifth turn for 6 of them, see run[1]).
 Plan plan_of(const QkRotateArgs& a, int v) {
   Plan p;
   const int units = a.R / (2 * v) + (a.K - a.R + 2 * v - 1) / (2 * v);
@@ -419,18 +447,46 @@ Plan plan_of(const QkRotateArgs& a, int v) {
   for (int i = 0; i < 2; ++i) {
     const int H = a.side[i].H;
     SidePlan& s = p.side[i];
+    // tokens in full turns of n items each, and those behind them in items of their own
+    const long long groups = per_cta * share[i];
+    int divisors[64], count = 0;
+    for (int n = 1; n <= H / n && count < 63; ++n)
+      if (H % n == 0) {
+        divisors[count++] = n;
+        if (n != H / n) divisors[count++] = H / n;
+      }
+    auto turn = [&](int n) { return H / n + kAngles; };
+    auto turns = [&](long long items) { return (double)((items + groups - 1) / groups); };
+    auto rest = [&](long long left, int* best) {
+      double least = left ? 1e300 : 0.;
+      *best = 1;
+      for (int d = 0; d < count && left; ++d) {
+        const int n = divisors[d];
+        const double time = turns(left * n) * turn(n);
+        if (time < 0.99 * least) {
+          least = time;
+          *best = n;
+        }
+      }
+      return least;
+    };
     double least = 1e300;
-    for (int n = 1; n <= H; ++n) {
-      if (H % n) continue;
-      const long long turns = (tokens * n + per_cta * share[i] - 1) / (per_cta * share[i]);
-      const double time = (double)turns * (H / n + kAngles);
+    for (int d = 0; d < count; ++d) {
+      const int n = divisors[d];
+      const long long full = tokens * n / groups * groups / n;
+      int n2;
+      const double time = turns(full * n) * turn(n) + rest(tokens - full, &n2);
       if (time < 0.99 * least) {
         least = time;
-        s.splits = n;
+        s.run[0] = Run{0, (int)full, n, H / n};
+        s.run[1] = Run{(int)full, (int)tokens, n2, H / n2};
       }
     }
-    s.nh = H / s.splits;
-    const long long need = (tokens * s.splits + per_cta - 1) / per_cta;
+    long long need = 0;
+    for (const Run& r : s.run) {
+      const long long ctas_of = ((long long)(r.to - r.from) * r.splits + per_cta - 1) / per_cta;
+      need = ctas_of > need ? ctas_of : need;
+    }
     s.ctas = (int)(need < share[i] ? need : share[i]);
   }
   p.side[0].first = 0;
