@@ -84,11 +84,11 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 __device__ __forceinline__ float gate_sigmoid(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
 
 // 1 - a^2 of a = 2^l.  Where a is near 1 the difference would lose its digits: there (1 - e^-z) / z, z = -2 ln a
-// in [0, 1/8], as the polynomial of degree 2 with the least error (2.4e-6 of it), here in powers of l.
-// Behind the border a's own error, 2^-22, makes at most 4e-6 of it.  (Its root has half of either.)
+// in [0, 1/2], as the polynomial of degree 4 with the least relative error (8e-8), here in powers of l.
+// Behind the border a's own error, 2^-22, makes at most 8e-7 of it.  (Its root has half of either.)
 __device__ __forceinline__ float one_minus_square(float l, float a) {
-  const float near = l * fmaf(l, fmaf(l, -0.42383318f, -0.96023068f), -1.386291f);
-  return l > -0.09016844f ? near : fmaf(-a, a, 1.f);
+  const float near = l * fmaf(l, fmaf(l, fmaf(l, fmaf(l, -0.034668292f, -0.15143253f), -0.44371712f), -0.96089161f), -1.3862943f);
+  return l > -0.36067376f ? near : fmaf(-a, a, 1.f);
 }
 
 // The logarithm (to base 2) of a_t at an open recurrence gate.
@@ -136,8 +136,8 @@ struct Sequences {
   }
 };
 
-// A run of whole sequences [n0, n1) and their tokens [t0, t1), the part of one cluster.  The last part
-// has the tokens behind the last sequence too.
+// A run of whole sequences [n0, n1) and their tokens [t0, t1): what one CTA of a block of channels walks, or
+// several, a segment each.  The last part has the tokens behind the last sequence too.
 struct Part {
   int n0, n1, t0, t1;
 };
