@@ -15,6 +15,7 @@ import torch
 from . import _lib
 from .api import _DT, _need, _ptr
 from .linear_attn import _first_only, _fit, _int32, _scratch, _stream
+from .recurrence import _elsewhere
 
 __all__ = ["qk_norm_rotate", "qk_norm_rotate_bwd", "qk_norm_rotate_trainable"]
 
@@ -117,6 +118,9 @@ def qk_norm_rotate(q, k, inv_freq=None, positions=None, q_weight=None, k_weight=
 def _forward(q, k, inv_freq, positions, q_weight, k_weight, call, interleaved, out_q=None, out_k=None):
     """The forward's outputs and call, after the checks of its inputs."""
     dev = q.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _forward(q, k, inv_freq, positions, q_weight, k_weight, call, interleaved, out_q, out_k)
     if out_q is None:
         out_q = torch.empty(q.shape, dtype=q.dtype, device=dev)
     elif not _fit(dev, (out_q, q.dtype, q.shape)):
@@ -149,6 +153,10 @@ def qk_norm_rotate_bwd(d_q, d_k, q, k, inv_freq=None, positions=None, q_weight=N
 def _backward(d_q, d_k, q, k, inv_freq, positions, q_weight, k_weight, call, interleaved, need_weights, workspace):
     """The backward's outputs, scratch and call, after the checks."""
     dev = q.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _backward(d_q, d_k, q, k, inv_freq, positions, q_weight, k_weight, call, interleaved,
+                             need_weights, workspace)
     dq, dk = torch.empty_like(d_q), torch.empty_like(d_k)
     L = _lib.load()
     dwq = dwk = None
@@ -202,7 +210,8 @@ class _QkNormRotate(torch.autograd.Function):
 def qk_norm_rotate_trainable(q, k, inv_freq=None, positions=None, q_weight=None, k_weight=None, *, norm="rms",
                              eps=1e-6, sections=None, interleaved=False):
     """:func:`qk_norm_rotate` as a differentiable op (torch autograd) in q, k, q_weight and k_weight; a
-    second derivative is refused."""
+    second derivative is refused.  Captured into a CUDA graph with its backward as
+    :func:`gated_linear_recurrence_trainable` says."""
     if inv_freq is not None and inv_freq.requires_grad:
         raise ValueError("inv_freq is a constant of the layer: it has no gradient")
     return _QkNormRotate.apply(q, k, inv_freq, positions, q_weight, k_weight, norm, eps, sections,

@@ -24,6 +24,11 @@ __all__ = ["gated_linear_recurrence", "gated_linear_recurrence_fused_gates",
            "gated_linear_recurrence_decode", "gated_linear_recurrence_decode_fused_gates"]
 
 
+def _elsewhere(dev) -> bool:
+    """Whether the tensors' device is not the current one, which launches and their plans go by."""
+    return torch._C._cuda_getDevice() != dev.index
+
+
 def _pitch(t, name, dtype, dev, shape):
     """Elements from one token of t to the next, after the checks: t [..., D] of ``shape`` whose rows
     are evenly spaced over all its leading axes."""
@@ -96,6 +101,10 @@ def _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, sta
              final_state, return_carries, workspace, dev_status, check, g_name):
     """Checks and the forward's call: (y, final state, carries, (c, pitches, number of sequences))."""
     dev, pitches, c = _inputs(x, g, i, lam, c, 3, g_name)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _forward(x, g, i, lam, c, initial_state, output_final_state, cu_seqlens, state_indices, out,
+                            final_state, return_carries, workspace, dev_status, check, g_name)
     B, T, D = x.shape
     N = _sequences(x, cu_seqlens)
     num_slots = 0
@@ -197,6 +206,10 @@ def _gradients(x, g, i, lam, c, pitches, N, d_y, d_final_state, initial_state, c
                need_d_initial_state, carries, workspace, dev_status):
     """The backward's outputs, scratch and call, after the checks."""
     dev = x.device
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _gradients(x, g, i, lam, c, pitches, N, d_y, d_final_state, initial_state, cu_seqlens, need_lam,
+                              need_d_initial_state, carries, workspace, dev_status)
     B, T, D = x.shape
     L = _lib.load()
     need = L.gdn_linear_recurrence_bwd_workspace_size(B, T, D, N, int(lam is not None))
@@ -279,20 +292,28 @@ class _Recurrence(torch.autograd.Function):
 
 def gated_linear_recurrence_trainable(x, g, initial_state=None, output_final_state=False, cu_seqlens=None):
     """:func:`gated_linear_recurrence` as a differentiable op (torch autograd) in x, g and
-    ``initial_state``; a second derivative is refused.  Returns ``(y, final_state or None)``."""
+    ``initial_state``; a second derivative is refused.  Returns ``(y, final_state or None)``.
+
+    To capture a step with its backward into a CUDA graph, let no graph of an eager call on the same leaves be alive:
+    autograd's engine would join the captured stream to the eager one, and the capture fails.
+    """
     return _Recurrence.apply(x, g, None, None, initial_state, 0.0, bool(output_final_state), cu_seqlens)
 
 
 def gated_linear_recurrence_fused_gates_trainable(x, r, i, lam, c=8.0, initial_state=None,
                                                   output_final_state=False, cu_seqlens=None):
     """:func:`gated_linear_recurrence_fused_gates` as a differentiable op in x, r, i, lam and
-    ``initial_state``; a second derivative is refused.  Returns ``(y, final_state or None)``."""
+    ``initial_state``; a second derivative is refused.  Returns ``(y, final_state or None)``; captured as
+    :func:`gated_linear_recurrence_trainable` says."""
     _need(lam, "lam")
     return _Recurrence.apply(x, r, i, lam, initial_state, float(c), bool(output_final_state), cu_seqlens)
 
 
 def _decode(x, g, i, lam, c, state, batch_indices, out, dev_status, check, g_name):
     dev, pitches, c = _inputs(x, g, i, lam, c, 2, g_name)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return _decode(x, g, i, lam, c, state, batch_indices, out, dev_status, check, g_name)
     n, D = x.shape
     if not (isinstance(state, torch.Tensor) and state.dim() == 2
             and _fit(dev, (state, torch.float32, (state.shape[0], D)), (batch_indices, torch.int32, (n,)),
