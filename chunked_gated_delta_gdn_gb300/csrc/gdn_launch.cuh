@@ -46,13 +46,13 @@ cudaError_t allow_shared(size_t bytes) {
 }
 
 template <typename... Params, typename... Args>
-cudaError_t launch_behind(void (*kernel)(Params...), unsigned grid, int threads, size_t shared, cudaStream_t stream,
+cudaError_t launch_behind(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream,
                           Args&&... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = shared;
   cfg.stream = stream;

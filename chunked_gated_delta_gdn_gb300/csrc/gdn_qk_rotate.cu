@@ -188,186 +188,186 @@ __global__ void __launch_bounds__(kThreads, kPerSm) qk_rotate_kernel(QkRotateArg
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[m][0][j] = acc[m][1][j] = 0.f;
   for (int which = 0; which < 2; ++which) {
-  const Run run = which ? sp.run[1] : sp.run[0];
-  const long long items = (long long)(run.to - run.from) * run.splits;
-  const long long turns = base0 < items ? (items - base0 + stride - 1) / stride : 0;   // items of the warp's first group
+    const Run run = which ? sp.run[1] : sp.run[0];
+    const long long items = (long long)(run.to - run.from) * run.splits;
+    const long long turns = base0 < items ? (items - base0 + stride - 1) / stride : 0;   // items of the warp's first group
 
-  // the copies run kDepth - 1 heads ahead of the work
-  long long ahead_item = base0 + hs;
-  int ahead_h = 0, ahead_slot = 0;
-  long long ahead_left = turns * run.nh;
-  const T* ahead_x = nullptr;
-  const T* ahead_dy = nullptr;
-  auto copy_head = [&]() {
-    if (ahead_left > 0) {
-      if (ahead_h == 0) {
-        const long long item = ahead_item < items ? ahead_item : items - 1;   // (a spare group reads the last one)
-        const int part = run.splits == 1 ? 0 : (int)(item % run.splits), h0 = part * run.nh;
-        const long long token = run.from + (run.splits == 1 ? item : item / run.splits);
-        const int b = (int)token / a.T, t = (int)token - b * a.T;
-        ahead_x = static_cast<const T*>(side.x) + b * side.sb + t * side.st + h0 * side.sh;
-        if (kBwd) ahead_dy = static_cast<const T*>(side.dy) + (token * side.H + h0) * a.K;
-      }
-      Vec<T, V>(*const to)[32] = ring.slot[warp][ahead_slot];
-      if constexpr (V * sizeof(T) >= 4) {
-#pragma unroll
-        for (int m = 0; m < NU; ++m) {
-          if (unit[m].on) copy_ahead<T, V>(&to[2 * m][lane], ahead_x + unit[m].o1);
-          if (unit[m].second) copy_ahead<T, V>(&to[2 * m + 1][lane], ahead_x + unit[m].o2);
-          if (kBwd) {
-            if (unit[m].on) copy_ahead<T, V>(&to[2 * (NU + m)][lane], ahead_dy + unit[m].o1);
-            if (unit[m].second) copy_ahead<T, V>(&to[2 * (NU + m) + 1][lane], ahead_dy + unit[m].o2);
-          }
+    // the copies run kDepth - 1 heads ahead of the work
+    long long ahead_item = base0 + hs;
+    int ahead_h = 0, ahead_slot = 0;
+    long long ahead_left = turns * run.nh;
+    const T* ahead_x = nullptr;
+    const T* ahead_dy = nullptr;
+    auto copy_head = [&]() {
+      if (ahead_left > 0) {
+        if (ahead_h == 0) {
+          const long long item = ahead_item < items ? ahead_item : items - 1;   // (a spare group reads the last one)
+          const int part = run.splits == 1 ? 0 : (int)(item % run.splits), h0 = part * run.nh;
+          const long long token = run.from + (run.splits == 1 ? item : item / run.splits);
+          const int b = (int)token / a.T, t = (int)token - b * a.T;
+          ahead_x = static_cast<const T*>(side.x) + b * side.sb + t * side.st + h0 * side.sh;
+          if (kBwd) ahead_dy = static_cast<const T*>(side.dy) + (token * side.H + h0) * a.K;
         }
-      } else {   // two bytes: by loads, all of them before the first store
-        T one[R::kVecs];
-#pragma unroll
-        for (int v = 0; v < R::kVecs; ++v) {
-          const Unit& u = unit[v % (2 * NU) / 2];
-          const T* const from = v < 2 * NU ? ahead_x : ahead_dy;
-          one[v] = (v & 1 ? u.second : u.on) ? from[v & 1 ? u.o2 : u.o1] : (T)0.f;
-        }
-#pragma unroll
-        for (int v = 0; v < R::kVecs; ++v) to[v][lane].e[0] = one[v];
-      }
-      ahead_x += side.sh;
-      if (kBwd) ahead_dy += a.K;
-      if (++ahead_h == run.nh) {
-        ahead_h = 0;
-        ahead_item += stride;
-      }
-      if (++ahead_slot == R::kDepth) ahead_slot = 0;
-      --ahead_left;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int k = 0; k < R::kDepth - 1; ++k) copy_head();
-
-  // the positions of an item's token on every axis, read an item ahead
-  int at[GDN_MAX_AXES] = {0, 0, 0, 0};
-  auto positions_of = [&](long long item) {
-    if (item >= items) return;
-    const long long token = run.from + (run.splits == 1 ? item : item / run.splits);
-    if (!a.positions) {
-#pragma unroll
-      for (int i = 0; i < GDN_MAX_AXES; ++i) at[i] = (int)token % a.T;
-    } else {
-#pragma unroll
-      for (int i = 0; i < GDN_MAX_AXES; ++i)
-        if (i < a.num_axes) at[i] = a.positions[i * tokens + token];
-    }
-  };
-  positions_of(base0 + hs);
-  int slot = 0;
-  for (long long n = 0; n < turns; ++n) {
-    const long long item = base0 + hs + n * stride;
-    const bool here = item < items;
-    const long long token = here ? run.from + (run.splits == 1 ? item : item / run.splits) : 0;
-    const int h0 = here && run.splits > 1 ? (int)(item % run.splits) * run.nh : 0;
-    float c[NU][V], s[NU][V];
-#pragma unroll
-    for (int m = 0; m < NU; ++m)
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        c[m][j] = 1.f;
-        s[m][j] = 0.f;
-        if (unit[m].turns) {
-          const int pair = pair_of<V, kInVector>(unit[m], j);
-          int position = at[0];
-#pragma unroll
-          for (int i = 1; i < GDN_MAX_AXES; ++i) position = pair >= a.axis_end[i - 1] ? at[i] : position;
-          angle<kFast>(rates[pair], position, &s[m][j], &c[m][j]);
-        }
-      }
-    // forward: the turn's factors with the weights in them, y1 = r (x1 f1 - x2 f2), y2 = r (x2 f3 + x1 f4)
-    float f[kBwd ? 1 : NU][4][V];
-    if constexpr (!kBwd) {
-#pragma unroll
-      for (int m = 0; m < NU; ++m)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float w1 = kInVector ? w[m][2 * j / V][2 * j % V] : w[m][0][j];
-          const float w2 = kInVector ? w[m][2 * j / V][2 * j % V + 1] : w[m][1][j];
-          f[m][0][j] = w1 * c[m][j];
-          f[m][1][j] = w2 * s[m][j];
-          f[m][2][j] = w2 * c[m][j];
-          f[m][3][j] = w1 * s[m][j];
-        }
-    }
-    positions_of(item + stride);
-    T* out = static_cast<T*>(side.out) + (token * side.H + h0) * a.K;
-    for (int h = 0; h < run.nh; ++h, out += a.K) {
-      copy_head();
-      asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
-      float x[NU][2][V], ss = 0.f;
-#pragma unroll
-      for (int m = 0; m < NU; ++m)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          unpack<T, V>(ring.slot[warp][slot][2 * m + v][lane], x[m][v]);
-#pragma unroll
-          for (int j = 0; j < V; ++j) ss = fmaf(x[m][v][j], x[m][v][j], ss);
-        }
-      const float inv = a.norm == GDN_NORM_NONE ? 1.f : rsqrtf(fmaf(group_sum(ss, G), mean, a.eps));
-      if constexpr (!kBwd) {
-#pragma unroll
-        for (int m = 0; m < NU; ++m) {
-          float y[2][V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) {   // pair j (behind the rotated part: an angle of 0)
-            const int v1 = kInVector ? 2 * j / V : 0, v2 = kInVector ? v1 : 1, j1 = kInVector ? 2 * j % V : j,
-                      j2 = kInVector ? j1 + 1 : j;
-            y[v1][j1] = inv * fmaf(x[m][v1][j1], f[m][0][j], -x[m][v2][j2] * f[m][1][j]);
-            y[v2][j2] = inv * fmaf(x[m][v2][j2], f[m][2][j], x[m][v1][j1] * f[m][3][j]);
-          }
-          if (here && unit[m].on) store<T, V>(out + unit[m].o1, y[0]);
-          if (here && unit[m].second) store<T, V>(out + unit[m].o2, y[1]);
-        }
-      } else {
-        // with d r in d's place: dw += d x,  dx = d w - x r^2 mean(d w x)
-        float d[NU][2][V], dot = 0.f;
-#pragma unroll
-        for (int m = 0; m < NU; ++m) {
-          float r[2][V];
-#pragma unroll
-          for (int v = 0; v < 2; ++v) {
-            unpack<T, V>(ring.slot[warp][slot][2 * (NU + m) + v][lane], r[v]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) r[v][j] *= inv;
-          }
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const int v1 = kInVector ? 2 * j / V : 0, v2 = kInVector ? v1 : 1, j1 = kInVector ? 2 * j % V : j,
-                      j2 = kInVector ? j1 + 1 : j;
-            d[m][v1][j1] = fmaf(r[v1][j1], c[m][j], r[v2][j2] * s[m][j]);
-            d[m][v2][j2] = fmaf(r[v2][j2], c[m][j], -r[v1][j1] * s[m][j]);
-          }
-#pragma unroll
-          for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              if (here) acc[m][v][j] = fmaf(d[m][v][j], x[m][v][j], acc[m][v][j]);
-              d[m][v][j] *= w[m][v][j];
-              dot = fmaf(d[m][v][j], x[m][v][j], dot);
+        Vec<T, V>(*const to)[32] = ring.slot[warp][ahead_slot];
+        if constexpr (V * sizeof(T) >= 4) {
+  #pragma unroll
+          for (int m = 0; m < NU; ++m) {
+            if (unit[m].on) copy_ahead<T, V>(&to[2 * m][lane], ahead_x + unit[m].o1);
+            if (unit[m].second) copy_ahead<T, V>(&to[2 * m + 1][lane], ahead_x + unit[m].o2);
+            if (kBwd) {
+              if (unit[m].on) copy_ahead<T, V>(&to[2 * (NU + m)][lane], ahead_dy + unit[m].o1);
+              if (unit[m].second) copy_ahead<T, V>(&to[2 * (NU + m) + 1][lane], ahead_dy + unit[m].o2);
             }
-        }
-        const float k = a.norm == GDN_NORM_NONE ? 0.f : group_sum(dot, G) * mean * inv * inv;
-#pragma unroll
-        for (int m = 0; m < NU; ++m) {
-          if (a.norm != GDN_NORM_NONE) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v)
-#pragma unroll
-              for (int j = 0; j < V; ++j) d[m][v][j] = fmaf(-x[m][v][j], k, d[m][v][j]);
           }
-          if (here && unit[m].on) store<T, V>(out + unit[m].o1, d[m][0]);
-          if (here && unit[m].second) store<T, V>(out + unit[m].o2, d[m][1]);
+        } else {   // two bytes: by loads, all of them before the first store
+          T one[R::kVecs];
+  #pragma unroll
+          for (int v = 0; v < R::kVecs; ++v) {
+            const Unit& u = unit[v % (2 * NU) / 2];
+            const T* const from = v < 2 * NU ? ahead_x : ahead_dy;
+            one[v] = (v & 1 ? u.second : u.on) ? from[v & 1 ? u.o2 : u.o1] : (T)0.f;
+          }
+  #pragma unroll
+          for (int v = 0; v < R::kVecs; ++v) to[v][lane].e[0] = one[v];
         }
+        ahead_x += side.sh;
+        if (kBwd) ahead_dy += a.K;
+        if (++ahead_h == run.nh) {
+          ahead_h = 0;
+          ahead_item += stride;
+        }
+        if (++ahead_slot == R::kDepth) ahead_slot = 0;
+        --ahead_left;
       }
-      if (++slot == R::kDepth) slot = 0;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int k = 0; k < R::kDepth - 1; ++k) copy_head();
+
+    // the positions of an item's token on every axis, read an item ahead
+    int at[GDN_MAX_AXES] = {0, 0, 0, 0};
+    auto positions_of = [&](long long item) {
+      if (item >= items) return;
+      const long long token = run.from + (run.splits == 1 ? item : item / run.splits);
+      if (!a.positions) {
+  #pragma unroll
+        for (int i = 0; i < GDN_MAX_AXES; ++i) at[i] = (int)token % a.T;
+      } else {
+  #pragma unroll
+        for (int i = 0; i < GDN_MAX_AXES; ++i)
+          if (i < a.num_axes) at[i] = a.positions[i * tokens + token];
+      }
+    };
+    positions_of(base0 + hs);
+    int slot = 0;
+    for (long long n = 0; n < turns; ++n) {
+      const long long item = base0 + hs + n * stride;
+      const bool here = item < items;
+      const long long token = here ? run.from + (run.splits == 1 ? item : item / run.splits) : 0;
+      const int h0 = here && run.splits > 1 ? (int)(item % run.splits) * run.nh : 0;
+      float c[NU][V], s[NU][V];
+  #pragma unroll
+      for (int m = 0; m < NU; ++m)
+  #pragma unroll
+        for (int j = 0; j < V; ++j) {
+          c[m][j] = 1.f;
+          s[m][j] = 0.f;
+          if (unit[m].turns) {
+            const int pair = pair_of<V, kInVector>(unit[m], j);
+            int position = at[0];
+  #pragma unroll
+            for (int i = 1; i < GDN_MAX_AXES; ++i) position = pair >= a.axis_end[i - 1] ? at[i] : position;
+            angle<kFast>(rates[pair], position, &s[m][j], &c[m][j]);
+          }
+        }
+      // forward: the turn's factors with the weights in them, y1 = r (x1 f1 - x2 f2), y2 = r (x2 f3 + x1 f4)
+      float f[kBwd ? 1 : NU][4][V];
+      if constexpr (!kBwd) {
+  #pragma unroll
+        for (int m = 0; m < NU; ++m)
+  #pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float w1 = kInVector ? w[m][2 * j / V][2 * j % V] : w[m][0][j];
+            const float w2 = kInVector ? w[m][2 * j / V][2 * j % V + 1] : w[m][1][j];
+            f[m][0][j] = w1 * c[m][j];
+            f[m][1][j] = w2 * s[m][j];
+            f[m][2][j] = w2 * c[m][j];
+            f[m][3][j] = w1 * s[m][j];
+          }
+      }
+      positions_of(item + stride);
+      T* out = static_cast<T*>(side.out) + (token * side.H + h0) * a.K;
+      for (int h = 0; h < run.nh; ++h, out += a.K) {
+        copy_head();
+        asm volatile("cp.async.wait_group %0;" ::"n"(R::kDepth - 1) : "memory");
+        float x[NU][2][V], ss = 0.f;
+  #pragma unroll
+        for (int m = 0; m < NU; ++m)
+  #pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            unpack<T, V>(ring.slot[warp][slot][2 * m + v][lane], x[m][v]);
+  #pragma unroll
+            for (int j = 0; j < V; ++j) ss = fmaf(x[m][v][j], x[m][v][j], ss);
+          }
+        const float inv = a.norm == GDN_NORM_NONE ? 1.f : rsqrtf(fmaf(group_sum(ss, G), mean, a.eps));
+        if constexpr (!kBwd) {
+  #pragma unroll
+          for (int m = 0; m < NU; ++m) {
+            float y[2][V];
+  #pragma unroll
+            for (int j = 0; j < V; ++j) {   // pair j (behind the rotated part: an angle of 0)
+              const int v1 = kInVector ? 2 * j / V : 0, v2 = kInVector ? v1 : 1, j1 = kInVector ? 2 * j % V : j,
+                        j2 = kInVector ? j1 + 1 : j;
+              y[v1][j1] = inv * fmaf(x[m][v1][j1], f[m][0][j], -x[m][v2][j2] * f[m][1][j]);
+              y[v2][j2] = inv * fmaf(x[m][v2][j2], f[m][2][j], x[m][v1][j1] * f[m][3][j]);
+            }
+            if (here && unit[m].on) store<T, V>(out + unit[m].o1, y[0]);
+            if (here && unit[m].second) store<T, V>(out + unit[m].o2, y[1]);
+          }
+        } else {
+          // with d r in d's place: dw += d x,  dx = d w - x r^2 mean(d w x)
+          float d[NU][2][V], dot = 0.f;
+  #pragma unroll
+          for (int m = 0; m < NU; ++m) {
+            float r[2][V];
+  #pragma unroll
+            for (int v = 0; v < 2; ++v) {
+              unpack<T, V>(ring.slot[warp][slot][2 * (NU + m) + v][lane], r[v]);
+  #pragma unroll
+              for (int j = 0; j < V; ++j) r[v][j] *= inv;
+            }
+  #pragma unroll
+            for (int j = 0; j < V; ++j) {
+              const int v1 = kInVector ? 2 * j / V : 0, v2 = kInVector ? v1 : 1, j1 = kInVector ? 2 * j % V : j,
+                        j2 = kInVector ? j1 + 1 : j;
+              d[m][v1][j1] = fmaf(r[v1][j1], c[m][j], r[v2][j2] * s[m][j]);
+              d[m][v2][j2] = fmaf(r[v2][j2], c[m][j], -r[v1][j1] * s[m][j]);
+            }
+  #pragma unroll
+            for (int v = 0; v < 2; ++v)
+  #pragma unroll
+              for (int j = 0; j < V; ++j) {
+                if (here) acc[m][v][j] = fmaf(d[m][v][j], x[m][v][j], acc[m][v][j]);
+                d[m][v][j] *= w[m][v][j];
+                dot = fmaf(d[m][v][j], x[m][v][j], dot);
+              }
+          }
+          const float k = a.norm == GDN_NORM_NONE ? 0.f : group_sum(dot, G) * mean * inv * inv;
+  #pragma unroll
+          for (int m = 0; m < NU; ++m) {
+            if (a.norm != GDN_NORM_NONE) {
+  #pragma unroll
+              for (int v = 0; v < 2; ++v)
+  #pragma unroll
+                for (int j = 0; j < V; ++j) d[m][v][j] = fmaf(-x[m][v][j], k, d[m][v][j]);
+            }
+            if (here && unit[m].on) store<T, V>(out + unit[m].o1, d[m][0]);
+            if (here && unit[m].second) store<T, V>(out + unit[m].o2, d[m][1]);
+          }
+        }
+        if (++slot == R::kDepth) slot = 0;
+      }
     }
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
   if (!kBwd || !part) return;
   // this CTA's sums: over the groups of a warp, then over the warps in order
@@ -520,8 +520,7 @@ cudaError_t launch(const QkRotateArgs& a) {
   else if (v == 2) err = launch<T, 2, 2, kBwd>(a, p, part);
   else err = launch<T, 1, 4, kBwd>(a, p, part);
   if (err != cudaSuccess || !part) return err;
-  qk_rotate_dw_kernel<<<dim3((a.K + 31) / 32, 2), 1024, 0, a.stream>>>(a, p, part);
-  return cudaGetLastError();
+  return launch_behind(qk_rotate_dw_kernel, dim3((a.K + 31) / 32, 2), 1024, 0, a.stream, a, p, (const float*)part);
 }
 
 }  // namespace

@@ -82,10 +82,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int tile0 = part.t0 / kTile, tiles = part.t1 > part.t0 ? (part.t1 - 1) / kTile - tile0 + 1 : 0;
   const int first = tile0 + segments.tile(segment, tiles), rounds = tile0 + segments.tile(segment + 1, tiles) - first;
   auto window_start = [&](int round) { return (first + round) * kTile + warp * kTau; };
+  Lost lost;
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
     if constexpr (kEngine) {
-      if (round < rounds && lane == 0) {
+      if (round < rounds && lane == 0 && !lost.copy) {
         uint64_t* const bar = &sh.arrived[round % kStages][warp];
         const int w0 = window_start(round);
         mbar_arrive_expect_tx(bar, Shared::kWindow);
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (warp == 0)
     sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine));
   Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of a segment: the logarithms' sum, the state behind it
-  bool lost = false, any_reset = false;
+  bool any_reset = false;
   // a first token's initial state: lane j's sequence, of which lanes know the cache's row and the number
   const bool saved = !kSteps && states && segment > 0 && segment + 1 < segments.count;
   auto initial = [&](const Window& w, int j) {
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const Window w = finder.template find<kTau, false>(w0, lane);
     const unsigned reset = w.first | w.dead;
     if constexpr (kEngine) {
-      wait_or_report(&sh.arrived[round % kStages][warp], round / kStages & 1, &lost, a.dev_status);
+      wait_for_copies<kStages>(sh.arrived, warp, round, rounds, &lost, a.dev_status);
     } else {
       copies_wait<kStages - 1>();
       __syncwarp();

@@ -301,15 +301,31 @@ __device__ __forceinline__ void write_state(float* row, const Lanes<N>& x, int n
 
 // ---------------------------------------------------------------- hand-overs
 
-// A wait of at most this many tries (seconds); one that has run out is reported, and none follows it:
-// what the launch writes is then not to be used.
+// A wait of at most this many tries (seconds).  One that has run out is reported, and none of its kind
+// follows it: what the launch writes is then not to be used.
 constexpr int kTries = 1 << 25;
-__device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, bool* lost, int* dev_status) {
-  if (*lost) return;
+__device__ __forceinline__ bool wait_some(uint64_t* bar, unsigned parity) {
   for (int k = 0; k < kTries; ++k)
-    if (mbar_try_wait(bar, parity)) return;
-  *lost = true;
+    if (mbar_try_wait(bar, parity)) return true;
+  return false;
+}
+struct Lost {
+  bool message = false, copy = false;
+};
+__device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, Lost* lost, int* dev_status) {
+  if (lost->message || wait_some(bar, parity)) return;
+  lost->message = true;
   report(dev_status, GDN_DEV_TIMEOUT);
+}
+// A round's copies.  Behind one that does not arrive nothing is fetched any more, and those under way are given the
+// same time again: no copy outlives its CTA.
+template <int kStages, int kWarps>
+__device__ __forceinline__ void wait_for_copies(uint64_t (*arrived)[kWarps], int warp, int round, int rounds, Lost* lost,
+                                                int* dev_status) {
+  if (lost->copy || wait_some(&arrived[round % kStages][warp], round / kStages & 1)) return;
+  lost->copy = true;
+  report(dev_status, GDN_DEV_TIMEOUT);
+  for (int k = round; k < min(round + kStages, rounds); ++k) wait_some(&arrived[k % kStages][warp], k / kStages & 1);
 }
 
 // The state in front of a window: 2^L base + H.
@@ -340,7 +356,7 @@ struct Chain {
   // The state in front of this warp's window (L, H), after handing on what is behind it.  `order`: the
   // window's place in its tile; `end`: where the last window's warp leaves what is behind it, or NULL.
   __device__ __forceinline__ Lanes<N> hand_over(int order, int round, int rounds, int lane, const Lanes<N>& L,
-                                                const Lanes<N>& H, bool reset, Lanes<N>* end, bool* lost,
+                                                const Lanes<N>& H, bool reset, Lanes<N>* end, Lost* lost,
                                                 int* dev_status) {
     const Lanes<N> A = ex2(L);   // (the way from message to message is what the chain's speed depends on)
     wait_or_report(&full[order], round & 1, lost, dev_status);

@@ -102,10 +102,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int first = tile0 + tiles - 1 - segments.tile(segment, tiles);
   const int rounds = segments.tile(segment + 1, tiles) - segments.tile(segment, tiles);
   auto tile_of = [&](int round) { return first - round; };
+  Lost lost;
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
     if constexpr (kEngine) {
-      if (round < rounds && lane == 0) {
+      if (round < rounds && lane == 0 && !lost.copy) {
         uint64_t* const bar = &sh.arrived[round % kStages][warp];
         const int w0 = tile_of(round) * kTile + warp * kTau;
         mbar_arrive_expect_tx(bar, kSteps ? kTau * (Shared::kRowX + Shared::kRowG) : Shared::kWindow);
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (warp + 1 == kWarps)
     sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine));
   Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of a segment: the logarithms' sum, e in front of it
-  bool lost = false, any_reset = false;
+  bool any_reset = false;
   for (int round = 0; round < rounds; ++round) {
     const int tile = tile_of(round), w0 = tile * kTile + warp * kTau;
     Values h = fill<N>(0.f);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const Window w = finder.template find<kTau, true>(w0, lane);
     const unsigned reset = w.first | w.dead, reset_e = w.last | w.dead;
     if constexpr (kEngine) {
-      wait_or_report(&sh.arrived[round % kStages][warp], round / kStages & 1, &lost, a.dev_status);
+      wait_for_copies<kStages>(sh.arrived, warp, round, rounds, &lost, a.dev_status);
     } else {
       copies_wait<kStages - 1>();
       __syncwarp();
@@ -301,6 +302,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     };
     if (w.plain) gradients(std::true_type{});
     else gradients(std::false_type{});
+    if (kEngine && kFused) fence_proxy_async_smem();   // (s was written where the next copies go)
     __syncwarp();
     fetch(round + kStages);
   }

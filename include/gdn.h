@@ -549,12 +549,11 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
  *               elements behind the one before it (x_pitch >= D), so x may be a part of a wider
  *               projection.
  *   g, i        [B, T, D] g_dtype (GDN_F32 or io_dtype), likewise with g_pitch, i_pitch.  Given g
- *               are log-decays: at most 0, -inf keeps nothing (larger ones are taken as they are;
- *               the product of any 4096 successive a_t has to stay finite).
+ *               are log-decays: at most 0, -inf keeps nothing.  Larger ones are taken as they are,
+ *               where the product of any successive a_t of a sequence stays finite.
  *   lam         [D] fp32, device, and c >= 0: the fused gates' form.
  *   B, T, D     with cu_seqlens B is 1 and T the packed token count.  Any D >= 1; element
- *               alignment serves, and rows of whole 4-byte (fp32: 8-byte) pairs that start on their size
- *               are read faster.
+ *               alignment serves, and rows that start and end on 16-byte boundaries are read faster.
  *   initial_state, output_final_state, final_state, cu_seqlens, num_seqs, state_indices,
  *   num_slots, stream  as gdn_chunk_fwd, states [N, D] or slots [num_slots, D] fp32: slot -1 is
  *               padding (zero rows, no state access), sequences may be empty, final_state may be
