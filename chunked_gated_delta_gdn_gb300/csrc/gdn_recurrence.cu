@@ -82,11 +82,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int tile0 = part.t0 / kTile, tiles = part.t1 > part.t0 ? (part.t1 - 1) / kTile - tile0 + 1 : 0;
   const int first = tile0 + segments.tile(segment, tiles), rounds = tile0 + segments.tile(segment + 1, tiles) - first;
   auto window_start = [&](int round) { return (first + round) * kTile + warp * kTau; };
-  Lost lost;
+  unsigned lost = 0;   // kinds of waits that have run out
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
     if constexpr (kEngine) {
-      if (round < rounds && lane == 0 && !lost.copy) {
+      if (round < rounds && lane == 0 && !(lost & kCopy)) {
         uint64_t* const bar = &sh.arrived[round % kStages][warp];
         const int w0 = window_start(round);
         mbar_arrive_expect_tx(bar, Shared::kWindow);
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (!kSteps && segment > 0) wait_for_previous();
   if (warp == 0)
     sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine));
-  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of a segment: the logarithms' sum, the state behind it
+  Values sum = fill<N>(0.f);   // of a segment's logarithms
   bool any_reset = false;
   // a first token's initial state: lane j's sequence, of which lanes know the cache's row and the number
   const bool saved = !kSteps && states && segment > 0 && segment + 1 < segments.count;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
       }
     }
-    Values h = sh.chain.hand_over(warp, round, rounds, lane, L, H, reset != 0, &end, &lost, a.dev_status);
+    Values h = sh.chain.hand_over(warp, round, rounds, lane, L, H, reset != 0, &lost, a.dev_status);
     if (kSteps) {
       sum = sum + L;
       any_reset |= reset != 0;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
   if (!kEngine) copies_wait<0>();
   if (!kSteps && segment + 1 < segments.count && segment == 0 && warp + 1 == kWarps)   // (nothing is in front of it)
-    write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, end, end, true, mine);
+    write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane), true, mine);
   if (kSteps) {   // (a segment that resets takes nothing from in front of it, whatever L says)
     Values(*const sums)[32] = reinterpret_cast<Values(*)[32]>(sh.ring);
     any_reset = __syncthreads_or(any_reset);
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (warp + 1 < kWarps) return;
     sum = fill<N>(0.f);
     for (int k = 0; k < kWarps; ++k) sum = sum + sums[k][lane];
-    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
+    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane), any_reset, mine);
     wait_for_previous();
   }
 }

@@ -309,21 +309,19 @@ __device__ __forceinline__ bool wait_some(uint64_t* bar, unsigned parity) {
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
-struct Lost {
-  bool message = false, copy = false;
-};
-__device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, Lost* lost, int* dev_status) {
-  if (lost->message || wait_some(bar, parity)) return;
-  lost->message = true;
+constexpr unsigned kMessage = 1, kCopy = 2;   // the kinds
+__device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, unsigned* lost, int* dev_status) {
+  if (*lost & kMessage || wait_some(bar, parity)) return;
+  *lost |= kMessage;
   report(dev_status, GDN_DEV_TIMEOUT);
 }
 // A round's copies.  Behind one that does not arrive nothing is fetched any more, and those under way are given the
 // same time again: no copy outlives its CTA.
 template <int kStages, int kWarps>
-__device__ __forceinline__ void wait_for_copies(uint64_t (*arrived)[kWarps], int warp, int round, int rounds, Lost* lost,
+__device__ __forceinline__ void wait_for_copies(uint64_t (*arrived)[kWarps], int warp, int round, int rounds, unsigned* lost,
                                                 int* dev_status) {
-  if (lost->copy || wait_some(&arrived[round % kStages][warp], round / kStages & 1)) return;
-  lost->copy = true;
+  if (*lost & kCopy || wait_some(&arrived[round % kStages][warp], round / kStages & 1)) return;
+  *lost |= kCopy;
   report(dev_status, GDN_DEV_TIMEOUT);
   for (int k = round; k < min(round + kStages, rounds); ++k) wait_some(&arrived[k % kStages][warp], k / kStages & 1);
 }
@@ -341,6 +339,7 @@ struct Front {
 template <int kWarps, int N>
 struct Chain {
   Front<N> slot[kWarps][32];
+  Lanes<N> last[32];   // what is behind the last window
   alignas(8) uint64_t full[kWarps];
 
   __device__ __forceinline__ void init() {   // one thread; a barrier follows
@@ -354,9 +353,9 @@ struct Chain {
   }
 
   // The state in front of this warp's window (L, H), after handing on what is behind it.  `order`: the
-  // window's place in its tile; `end`: where the last window's warp leaves what is behind it, or NULL.
+  // window's place in its tile.
   __device__ __forceinline__ Lanes<N> hand_over(int order, int round, int rounds, int lane, const Lanes<N>& L,
-                                                const Lanes<N>& H, bool reset, Lanes<N>* end, Lost* lost,
+                                                const Lanes<N>& H, bool reset, unsigned* lost,
                                                 int* dev_status) {
     const Lanes<N> A = ex2(L);   // (the way from message to message is what the chain's speed depends on)
     wait_or_report(&full[order], round & 1, lost, dev_status);
@@ -372,11 +371,14 @@ struct Chain {
       behind.base = behind.value();
       behind.L = behind.H = fill<N>(0.f);
       send(0, lane, behind);
-    } else if (end) {
-      *end = behind.value();
+    } else {
+      last[lane] = behind.value();
     }
     return f.value();
   }
+
+  // Behind the last of `rounds`, for the last window's warp.
+  __device__ __forceinline__ Lanes<N> end(int rounds, int lane) const { return rounds > 0 ? last[lane] : fill<N>(0.f); }
 
  private:
   __device__ __forceinline__ void send(int to, int lane, const Front<N>& f) {

@@ -102,11 +102,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int first = tile0 + tiles - 1 - segments.tile(segment, tiles);
   const int rounds = segments.tile(segment + 1, tiles) - segments.tile(segment, tiles);
   auto tile_of = [&](int round) { return first - round; };
-  Lost lost;
+  unsigned lost = 0;   // kinds of waits that have run out
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
     if constexpr (kEngine) {
-      if (round < rounds && lane == 0 && !lost.copy) {
+      if (round < rounds && lane == 0 && !(lost & kCopy)) {
         uint64_t* const bar = &sh.arrived[round % kStages][warp];
         const int w0 = tile_of(round) * kTile + warp * kTau;
         mbar_arrive_expect_tx(bar, kSteps ? kTau * (Shared::kRowX + Shared::kRowG) : Shared::kWindow);
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   if (!kSteps && segment > 0) wait_for_previous();
   if (warp + 1 == kWarps)
     sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine));
-  Values sum = fill<N>(0.f), end = fill<N>(0.f);   // of a segment: the logarithms' sum, e in front of it
+  Values sum = fill<N>(0.f);   // of a segment's logarithms
   bool any_reset = false;
   for (int round = 0; round < rounds; ++round) {
     const int tile = tile_of(round), w0 = tile * kTile + warp * kTau;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       if (lane == 0) mbar_arrive(&sh.state_full[warp + 1]);
     }
     const int order = kWarps - 1 - warp;
-    Values e = sh.chain.hand_over(order, round, rounds, lane, L, E, reset_e != 0, &end, &lost, a.dev_status);
+    Values e = sh.chain.hand_over(order, round, rounds, lane, L, E, reset_e != 0, &lost, a.dev_status);
     if (kSteps) {
       sum = sum + L;
       any_reset |= reset_e != 0;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   }
   if (!kEngine) copies_wait<0>();
   if (!kSteps && segment + 1 < segments.count && segment == 0 && warp == 0)   // (nothing is behind it)
-    write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, end, end, true, mine);
+    write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane), true, mine);
   if (kSteps) {   // (a segment that resets takes nothing from behind it, whatever L says)
     Values(*const sums)[32] = reinterpret_cast<Values(*)[32]>(sh.ring);
     any_reset = __syncthreads_or(any_reset);
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (warp > 0) return;   // the last one of the chain
     sum = fill<N>(0.f);
     for (int k = 0; k < kWarps; ++k) sum = sum + sums[k][lane];
-    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, end, any_reset, mine);
+    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane), any_reset, mine);
     wait_for_previous();
     return;
   }
