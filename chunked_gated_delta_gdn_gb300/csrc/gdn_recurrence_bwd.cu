@@ -9,10 +9,15 @@
 //     dlam = sum of d(log a) sigmoid(r), times -c sigmoid(lam).
 //
 // The forward's shape from right to left, one reading of the inputs: a CTA walks tiles of kWarps windows,
-// with the states that the forward saved in front of every fourth one.  A window hands on its effects on
-// the state (to the right, up to the next saved one) and on e (to the left).  The gates' sigmoids and s stay in shared memory for
-// the second half.  Each lane sums its channels' dlam over its CTA's tokens; a second launch adds the CTAs
-// up in order.
+// with the states that the forward saved in front of every fourth one (every 32nd token: 1/16 of a bf16 tensor's
+// bytes).  A window hands on its effects on the state (to the right, up to the next saved one) and on e (to
+// the left).  The gates' sigmoids and s stay in shared memory for the second half.  Each lane sums its
+// channels' dlam over its CTA's tokens; a second launch adds the CTAs up in order.
+//
+// 5 or (fused) 7 values an element to read and write; with fused gates bound by what an SM issues, 76
+// instructions an element.  bf16, 2 x 8192 x 4096 (128 CTAs on 152 SMs): fused 210 us, 4.5 TB/s, 74% of the
+// issue slots used; given 142 us, 4.7 TB/s.  4 x 32768 x 4096 given: 1.04 ms, 5.2 TB/s.  With s made
+// again from a in the second half instead of kept it took 258 us.
 #include <algorithm>
 
 #include "gdn_recurrence.cuh"
