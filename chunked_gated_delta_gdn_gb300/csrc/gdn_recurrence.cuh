@@ -91,6 +91,25 @@ __device__ __forceinline__ float one_minus_square(float l, float a) {
   return l > -0.36067376f ? near : fmaf(-a, a, 1.f);
 }
 
+// ... of a lane's channels, two at a time where there are two.
+template <int N> __device__ __forceinline__ Lanes<N> one_minus_square(const Lanes<N>& l, const Lanes<N>& a) {
+  if constexpr (N == 2) {
+    auto both = [](float x) { return make_float2(x, x); };
+    const float2 z = make_float2(l.v[0], l.v[1]);
+    float2 p = __ffma2_rn(z, both(-0.034668292f), both(-0.15143253f));
+    p = __ffma2_rn(z, p, both(-0.44371712f));
+    p = __ffma2_rn(z, p, both(-0.96089161f));
+    p = __ffma2_rn(z, p, both(-1.3862943f));
+    p = __fmul2_rn(z, p);
+    Lanes<N> r;
+    r.v[0] = z.x > -0.36067376f ? p.x : fmaf(-a.v[0], a.v[0], 1.f);
+    r.v[1] = z.y > -0.36067376f ? p.y : fmaf(-a.v[1], a.v[1], 1.f);
+    return r;
+  } else {
+    return each([](float l, float a) { return one_minus_square(l, a); }, l, a);
+  }
+}
+
 // The logarithm (to base 2) of a_t at an open recurrence gate.
 __device__ __forceinline__ float gate_rate(float c, float lam) { return -c * softplus_f(lam) * kLog2e; }
 

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         sh.sigmoid[warp][1][j][lane] = si;
         l = rate * sr;
         da[j] = ex2(l);
-        const Values root = each([](float l, float a) { return sqrt_approx(one_minus_square(l, a)); }, l, da[j]);
+        const Values root = each(sqrt_approx, one_minus_square(l, da[j]));
         keep(j, root);
         db[j] = root * si * x;
       } else {
