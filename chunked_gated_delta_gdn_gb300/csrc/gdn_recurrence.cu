@@ -159,10 +159,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       Values l;
       if (kFused) {
         const Values i = read_row<G, N>(from + Shared::kAtI + j * Shared::kRowG, lane);
-        l = each([](float r, float rt) { return rt * gate_sigmoid(r); }, g, rate);
+        l = times(rate, gate_sigmoid(g));
         da[j] = ex2(l);
-        db[j] = each([](float s, float i, float x) { return sqrt_approx(s) * gate_sigmoid(i) * x; },
-                     one_minus_square(l, da[j]), i, x);
+        db[j] = times(times(each(sqrt_approx, one_minus_square(l, da[j])), gate_sigmoid(i)), x);
       } else {
         l = g * kLog2e;
         da[j] = ex2(l);

@@ -91,20 +91,34 @@ __device__ __forceinline__ float one_minus_square(float l, float a) {
   return l > -0.36067376f ? near : fmaf(-a, a, 1.f);
 }
 
-// ... of a lane's channels, two at a time where there are two.
+// The gates' arithmetic of a lane's channels, packed where there are two (the rest is not: pairs that live long
+// spill).
+__device__ __forceinline__ float2 pair(const Lanes<2>& x) { return make_float2(x.v[0], x.v[1]); }
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Lanes<2> lanes(float2 x) { return Lanes<2>{{x.x, x.y}}; }
+template <int N> __device__ __forceinline__ Lanes<N> times(const Lanes<N>& a, const Lanes<N>& b) {
+  if constexpr (N == 2) return lanes(__fmul2_rn(pair(a), pair(b)));
+  else return a * b;
+}
+template <int N> __device__ __forceinline__ Lanes<N> gate_sigmoid(const Lanes<N>& x) {
+  if constexpr (N == 2) {
+    const float2 y = __fmul2_rn(pair(x), pair(-kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2(y.x), ex2(y.y)), pair(1.f));
+    return lanes(make_float2(rcp(d.x), rcp(d.y)));
+  } else {
+    return each([](float v) { return gate_sigmoid(v); }, x);
+  }
+}
 template <int N> __device__ __forceinline__ Lanes<N> one_minus_square(const Lanes<N>& l, const Lanes<N>& a) {
   if constexpr (N == 2) {
-    auto both = [](float x) { return make_float2(x, x); };
-    const float2 z = make_float2(l.v[0], l.v[1]);
-    float2 p = __ffma2_rn(z, both(-0.034668292f), both(-0.15143253f));
-    p = __ffma2_rn(z, p, both(-0.44371712f));
-    p = __ffma2_rn(z, p, both(-0.96089161f));
-    p = __ffma2_rn(z, p, both(-1.3862943f));
+    const float2 z = pair(l);
+    float2 p = __ffma2_rn(z, pair(-0.034668292f), pair(-0.15143253f));
+    p = __ffma2_rn(z, p, pair(-0.44371712f));
+    p = __ffma2_rn(z, p, pair(-0.96089161f));
+    p = __ffma2_rn(z, p, pair(-1.3862943f));
     p = __fmul2_rn(z, p);
-    Lanes<N> r;
-    r.v[0] = z.x > -0.36067376f ? p.x : fmaf(-a.v[0], a.v[0], 1.f);
-    r.v[1] = z.y > -0.36067376f ? p.y : fmaf(-a.v[1], a.v[1], 1.f);
-    return r;
+    const float2 far = __ffma2_rn(make_float2(-a.v[0], -a.v[1]), pair(a), pair(1.f));
+    return lanes(make_float2(z.x > -0.36067376f ? p.x : far.x, z.y > -0.36067376f ? p.y : far.y));
   } else {
     return each([](float l, float a) { return one_minus_square(l, a); }, l, a);
   }
