@@ -9,10 +9,10 @@
 // of its window and walks its tokens.  Few parts are cut into segments, whose steps a launch of their own
 // (kSteps) makes.
 //
-// Bound by bytes: 3 or (fused) 4 values an element.  bf16, 4 x 32768 x 4096: fused 718 us, 6.0 TB/s; given 557 us, 5.8
+// Bound by bytes: 3 or (fused) 4 values an element.  bf16, 4 x 32768 x 4096: fused 703 us, 6.1 TB/s; given 557 us, 5.8
 // TB/s.  2 x 8192 x 4096 has 128 CTAs for 152 SMs and is bound by what they issue (37 instructions an
-// element with fused gates, three exponentials, two reciprocals and a root among them; 77% of the issue slots):
-// 104 us, 5.1 TB/s, given 79 us.  One channel a lane (twice the CTAs, half as wide rows): 122 and 107 us; 8-token
+// element with fused gates before some were packed, three exponentials, two reciprocals and a root among them; 77% of the issue slots):
+// 102 us, 5.3 TB/s, given 79 us.  One channel a lane (twice the CTAs, half as wide rows): 122 and 107 us; 8-token
 // windows with three CTAs an SM, and pairs in packed arithmetic (113 us, spilled registers), were slower too.
 // In two segments or more, one 32768 x 2048: 113 us for 59 us of bytes, some of which are read twice.
 #include <algorithm>
@@ -28,10 +28,9 @@ constexpr int kTile = kWarps * kTau;
 constexpr double kFirst = 0.7;   // the time of a step, of running
 constexpr int kStages = 2;
 
-template <typename T, typename G, bool kFused, int N>
+template <typename T, typename G, bool kFused, int N, bool kBoxes>
 struct FwdShared {
-  static constexpr int W = 32 * N;
-  static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
+  static constexpr int kRowX = kRowBytes<T, N, kBoxes>, kRowG = kRowBytes<G, N, kBoxes>;
   static constexpr int kAtG = kTau * kRowX, kAtI = kAtG + kTau * kRowG;
   static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
@@ -39,23 +38,23 @@ struct FwdShared {
   uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.  states: where the steps' launch
+// kBoxes: a window's inputs come in boxes, and outputs go out whole; else row by row.  states: where the steps' launch
 // keeps sequences' initial states for the later one, whose final states may take their place.
-template <typename T, typename G, bool kFused, int N, bool kEngine, bool kSteps>
+template <typename T, typename G, bool kFused, int N, bool kBoxes, bool kSteps>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-    recurrence_fwd_kernel(RecurrenceArgs a, int parts, Segments segments, float* steps, float* states, int x_unit, int g_unit, int i_unit,
+    recurrence_fwd_kernel(RecurrenceArgs a, int parts, Segments segments, float* steps, float* states,
                           const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
-  using Shared = FwdShared<T, G, kFused, N>;
+  using Shared = FwdShared<T, G, kFused, N, kBoxes>;
   using Values = Lanes<N>;
-  constexpr int W = Shared::W;
+  constexpr int W = kLanes<kBoxes> * N;
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   const int segment = segments.from + blockIdx.x % segments.here, part_index = blockIdx.x / segments.here % parts,
             block = blockIdx.x / segments.here / parts;
   const int ch = block * W + lane * N;   // this lane's first channel
-  const int mine = max(0, min(N, a.D - ch));
+  const int mine = lane < kLanes<kBoxes> ? max(0, min(N, a.D - ch)) : 0;
   WindowFinder finder;
   finder.seq = Sequences{a.cu_seqlens, a.num_seqs, a.T, a.cu_seqlens ? a.T : a.B * a.T};
   finder.slots = a.state_indices;
@@ -90,9 +89,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int first = tile0 + segments.tile(segment, tiles), rounds = tile0 + segments.tile(segment + 1, tiles) - first;
   auto window_start = [&](int round) { return (first + round) * kTile + warp * kTau; };
   unsigned lost = 0;   // kinds of waits that have run out
+  const Rows rows_x = Rows::of<T>(a.x, a.x_pitch, finder.seq.tokens, a.D), rows_g = Rows::of<G>(a.g, a.g_pitch, finder.seq.tokens, a.D),
+             rows_i = Rows::of<G>(a.i, a.i_pitch, finder.seq.tokens, a.D);
+  auto shift = [&](const Rows& rows, int token, int elem) { return kBoxes ? 0 : rows.shift(token, block * W * elem); };
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
-    if constexpr (kEngine) {
+    if constexpr (kBoxes) {
       if (round < rounds && lane == 0 && !(lost & kCopy)) {
         uint64_t* const bar = &sh.arrived[round % kStages][warp];
         const int w0 = window_start(round);
@@ -103,15 +105,15 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
     } else {
       if (round < rounds) {
-        const int w0 = window_start(round), lo = part.t0 - w0, hi = part.t1 - w0, left = a.D - block * W;
-        auto copy = [&](auto type, int at, const void* base, long long pitch, int unit) {
-          using E = decltype(type);
-          copy_window<kTau, W * sizeof(E)>(to + at, reinterpret_cast<const char*>(static_cast<const E*>(base) + w0 * pitch + block * W),
-                                           pitch * (long long)sizeof(E), lo, hi, left * (int)sizeof(E), unit, lane);
+        const int start = window_start(round), values = min(W, a.D - block * W);
+        auto copy = [&](auto elem, const Rows& rows, int at) {
+          using E = decltype(elem);
+          rows.template copy<E, kTau, kRowBytes<E, N, kBoxes>>(to + at, start, part.t0, part.t1, block * W * (int)sizeof(E),
+                                                               values * (int)sizeof(E), lane);
         };
-        copy(T{}, 0, a.x, a.x_pitch, x_unit);
-        copy(G{}, Shared::kAtG, a.g, a.g_pitch, g_unit);
-        if (kFused) copy(G{}, Shared::kAtI, a.i, a.i_pitch, i_unit);
+        copy(T{}, rows_x, 0);
+        copy(G{}, rows_g, Shared::kAtG);
+        if (kFused) copy(G{}, rows_i, Shared::kAtI);
       }
       copies_close();
     }
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const int w0 = window_start(round);
     const Window w = finder.template find<kTau, false>(w0, lane);
     const unsigned reset = w.first | w.dead;
-    if constexpr (kEngine) {
+    if constexpr (kBoxes) {
       wait_for_copies<kStages>(sh.arrived, warp, round, rounds, &lost, a.dev_status);
     } else {
       copies_wait<kStages - 1>();
@@ -154,11 +156,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     const char* const from = sh.ring[round % kStages][warp];
 #pragma unroll
     for (int j = 0; j < kTau; ++j) {
-      const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
-      const Values g = read_row<G, N>(from + Shared::kAtG + j * Shared::kRowG, lane);
+      const Values x = read_row<kBoxes, T, N>(from + j * Shared::kRowX + shift(rows_x, w0 + j, sizeof(T)), lane);
+      const Values g = read_row<kBoxes, G, N>(from + Shared::kAtG + j * Shared::kRowG + shift(rows_g, w0 + j, sizeof(G)), lane);
       Values l;
       if (kFused) {
-        const Values i = read_row<G, N>(from + Shared::kAtI + j * Shared::kRowG, lane);
+        const Values i = read_row<kBoxes, G, N>(from + Shared::kAtI + j * Shared::kRowG + shift(rows_i, w0 + j, sizeof(G)), lane);
         l = times(rate, gate_sigmoid(g));
         da[j] = ex2(l);
         db[j] = times(times(each(sqrt_approx, one_minus_square(l, da[j])), gate_sigmoid(i)), x);
@@ -196,13 +198,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 #pragma unroll
       for (int j = 0; j < kTau; ++j) {
         h = fma(da[j], h, db[j]);
-        write_row<kEngine>(y + (size_t)j * a.D, h, mine);
+        write_row<kBoxes>(y + (size_t)j * a.D, h, mine);
       }
     } else if (!w.plain) {
 #pragma unroll
       for (int j = 0; j < kTau; ++j) {
         h = reset >> j & 1 ? db[j] : fma(da[j], h, db[j]);
-        if (a.y && (w.in >> j & 1)) write_row<kEngine>(y + (size_t)j * a.D, h, mine);
+        if (a.y && (w.in >> j & 1)) write_row<kBoxes>(y + (size_t)j * a.D, h, mine);
         if (w.last >> j & 1) {
           const int row = __shfl_sync(~0u, w.row, j);
           if (a.final_state) write_state(a.final_state + (size_t)row * a.D + ch, h, mine);
@@ -210,7 +212,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
     }
   }
-  if (!kEngine) copies_wait<0>();
+  if (!kBoxes) copies_wait<0>();
   if (!kSteps && segment + 1 < segments.count && segment == 0 && warp + 1 == kWarps)   // (nothing is in front of it)
     write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane), true, mine);
   if (kSteps) {   // (a segment that resets takes nothing from in front of it, whatever L says)
@@ -230,33 +232,31 @@ RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
   return recurrence_plan((long long)B * T, D, N, packed, width, kTile, kFirst);
 }
 
-template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
+template <typename T, typename G, bool kFused, int N, bool kBoxes, typename... Args>
 cudaError_t launch_fwd(const RecurrenceArgs& a, const RecurrencePlan& p, const Args&... args) {
   float* const steps = static_cast<float*>(a.workspace);
   float* const states = p.segments > 1 && a.initial_state && a.final_state
                             ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + up256(steps_bytes(p, a.D)))
                             : nullptr;
-  return launch_segments<recurrence_fwd_kernel<T, G, kFused, N, kEngine, false>, recurrence_fwd_kernel<T, G, kFused, N, kEngine, true>>(
-      a, p, kFirst, kWarps * 32, sizeof(FwdShared<T, G, kFused, N>), steps, states, args...);
+  return launch_segments<recurrence_fwd_kernel<T, G, kFused, N, kBoxes, false>, recurrence_fwd_kernel<T, G, kFused, N, kBoxes, true>>(
+      a, p, kFirst, kWarps * 32, sizeof(FwdShared<T, G, kFused, N, kBoxes>), steps, states, args...);
 }
 
 template <typename T, typename G, bool kFused, int N>
 cudaError_t launch_fwd(const RecurrenceArgs& a) {
-  constexpr int W = 32 * N;
   const long long tokens = (long long)a.B * a.T;
+  const bool boxes = tokens > 0 && box_rows(a.x, a.x_pitch, a.D, sizeof(T)) && box_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
+                     (!kFused || box_rows(a.i, a.i_pitch, a.D, sizeof(G))) &&
+                     reinterpret_cast<uintptr_t>(a.y) % (N * sizeof(T)) == 0;
+  const int W = (boxes ? kLanes<true> : kLanes<false>)*N;
   const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, W);
-  const int x_unit = copy_unit(a.x, a.x_pitch, a.D, sizeof(T)), g_unit = copy_unit(a.g, a.g_pitch, a.D, sizeof(G)),
-            i_unit = copy_unit(a.i, a.i_pitch, a.D, sizeof(G));
   CUtensorMap mx{}, mg{}, mi{};
-  const bool engine = tokens > 0 && engine_rows(a.x, a.x_pitch, a.D, sizeof(T)) && engine_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
-                      (!kFused || engine_rows(a.i, a.i_pitch, a.D, sizeof(G))) &&
-                      reinterpret_cast<uintptr_t>(a.y) % (N * sizeof(T)) == 0;
-  if (!engine) return launch_fwd<T, G, kFused, N, false>(a, p, x_unit, g_unit, i_unit, mx, mg, mi);
+  if (!boxes) return launch_fwd<T, G, kFused, N, false>(a, p, mx, mg, mi);
   if (!rows_map(&mx, a.x, tokens, a.D, a.x_pitch, sizeof(T), W, kTau) ||
       !rows_map(&mg, a.g, tokens, a.D, a.g_pitch, sizeof(G), W, kTau) ||
       (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau)))
     return cudaErrorInvalidValue;
-  return launch_fwd<T, G, kFused, N, true>(a, p, x_unit, g_unit, i_unit, mx, mg, mi);
+  return launch_fwd<T, G, kFused, N, true>(a, p, mx, mg, mi);
 }
 
 template <typename T, typename G, int N>
@@ -344,7 +344,7 @@ size_t recurrence_carries_bytes(long long tokens, int D) {
 size_t recurrence_fwd_workspace_bytes(int B, int T, int D, int num_seqs) {
   size_t most = 0;
   for (int packed = 0; packed < 2; ++packed)
-    for (int width = 32; width <= 64; width *= 2) {
+    for (int width : kWidths) {
       const RecurrencePlan p = plan_of(B, T, D, num_seqs, packed, width);
       if (p.segments > 1) most = std::max(most, up256(steps_bytes(p, D)) + (size_t)num_seqs * D * sizeof(float));
     }

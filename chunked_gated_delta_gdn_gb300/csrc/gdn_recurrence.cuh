@@ -243,47 +243,58 @@ struct WindowFinder {
 
 // ---------------------------------------------------------------- copies
 
-__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
+// The lanes that have channels: where rows do not start on 16 bytes, 28, so that the 16-byte blocks that a row of
+// bf16 pairs or fp32 values lies in are no more than the 128 bytes of a whole one.
+template <bool kBoxes> constexpr int kLanes = kBoxes ? 32 : 28;
+// What a row of E, N a lane, takes in shared memory.
+template <typename E, int N, bool kBoxes>
+constexpr int kRowBytes = kBoxes ? 32 * N * (int)sizeof(E) : (kLanes<false> * N * (int)sizeof(E) + 30 - (int)sizeof(E) + 1) / 16 * 16;
+
+// A tensor's rows where they do not come in boxes.  (bf16 with fused gates, 4 x 8192 x 1001: forward 134 us, backward
+// 214; a bulk copy a row 151 and 234; copies of 4 bytes, 2 where rows are odd, 275 and 408.  1000 channels, in
+// boxes: 88 and 152.)
+struct Rows {
+  const char* base;
+  long long pitch;   // bytes
+  const char* end;   // of the last row
+
+  template <typename E>
+  static __device__ __forceinline__ Rows of(const void* p, long long pitch, int tokens, int D) {
+    const char* const base = static_cast<const char*>(p);
+    return Rows{base, pitch * (long long)sizeof(E), base + ((tokens - 1) * pitch + D) * (long long)sizeof(E)};
+  }
+  // Where in its 16-byte block row `token` has its byte `at`.
+  __device__ __forceinline__ int shift(int token, int at) const {
+    return (int)((reinterpret_cast<uintptr_t>(base) + token * pitch + at) & 15);
+  }
+  // Bytes [at, at + bytes) of the rows of tokens w0 <= t < w0 + kTau that are in [t0, t1), to dst [kTau][kRow]: the
+  // 16-byte blocks that they lie in, asynchronously; one warp.  Of blocks that reach beyond the tensor, the row's
+  // values alone.
+  template <typename E, int kTau, int kRow>
+  __device__ __forceinline__ void copy(char* dst, int w0, int t0, int t1, int at, int bytes, int lane) const {
+    constexpr int kBlocks = kRow / 16;
+#pragma unroll 2
+    for (int k = lane; k < kTau * kBlocks; k += 32) {
+      const int row = k / kBlocks, token = w0 + row;
+      const char* const from = base + token * pitch + at;
+      const int shift = (int)(reinterpret_cast<uintptr_t>(from) & 15), c = k % kBlocks * 16 - shift;   // in the row
+      if (token < t0 || token >= t1 || c >= bytes) continue;
+      char* const to = dst + row * kRow + shift;
+      if (from + c >= base && from + c + 16 <= end) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to + c)), "l"(from + c) : "memory");
+      } else {
+        for (int v = max(c, 0); v < min(c + 16, bytes); v += sizeof(E))
+          *reinterpret_cast<E*>(to + v) = *reinterpret_cast<const E*>(from + v);
+      }
+    }
+  }
+};
 __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft> __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// One warp's window of one tensor where its rows do not allow the copy engine: rows lo <= j < hi of kTau, kRow
-// bytes each (`left` of them inside the tensor), to dst [kTau][kRow].  unit: the bytes that every row's
-// start and end is a multiple of, 16, 4 or 2 (then by loads and stores: asynchronous copies have at
-// least four bytes).
-template <int kTau, int kRow>
-__device__ __forceinline__ void copy_window(char* dst, const char* src, long long pitch, int lo, int hi, int left,
-                                            int unit, int lane) {
-  if (unit == 16) {
-    constexpr int kPer = kRow / 16;
-    const int c = lane % kPer * 16;
-#pragma unroll 2
-    for (int row = lane / kPer; row < kTau; row += 32 / kPer)
-      if (row >= lo && row < hi && c < left) copy_async16(dst + row * kRow + c, src + row * pitch + c);
-  } else if (unit == 4) {
-    constexpr int kPer = kRow / 4;
-    const int c = lane % kPer * 4;
-#pragma unroll 4
-    for (int row = lane / kPer; row < kTau; row += 32 / kPer)
-      if (row >= lo && row < hi && c < left) copy_async4(dst + row * kRow + c, src + row * pitch + c);
-  } else {
-#pragma unroll 4
-    for (int row = max(lo, 0); row < min(hi, kTau); ++row)
-#pragma unroll
-      for (int c = lane * 2; c < kRow; c += 64)
-        if (c < left)
-          *reinterpret_cast<uint16_t*>(dst + row * kRow + c) = *reinterpret_cast<const uint16_t*>(src + row * pitch + c);
-  }
-}
-
-// The same by the copy engine: the box [kTau][W] of a map made by rows_map; one thread.
+// Rows that start and end on 16 bytes: the box [kTau][W] of a map made by rows_map; one thread.
 __device__ __forceinline__ void tma_window(char* dst, const CUtensorMap* map, uint64_t* bar, int channel, int token) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
@@ -293,11 +304,11 @@ __device__ __forceinline__ void tma_window(char* dst, const CUtensorMap* map, ui
 }
 
 // A lane's values of a row in shared memory, and to global memory: n of them are inside the tensor; whole:
-// all or none, and they may go in one store.
-template <typename T, int N>
+// all or none, and they may go in one access.
+template <bool kWhole, typename T, int N>
 __device__ __forceinline__ Lanes<N> read_row(const char* row, int lane) {
   Lanes<N> x;
-  if constexpr (N == 2 && sizeof(T) == 2) {
+  if constexpr (kWhole && N == 2 && sizeof(T) == 2) {
     const float2 v = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162*>(row)[lane]);
     x.v[0] = v.x;
     x.v[1] = v.y;
@@ -500,6 +511,9 @@ inline RecurrencePlan recurrence_plan(long long tokens, int D, int N, bool packe
   return best;
 }
 
+// Every width of a CTA that a call may have.
+constexpr int kWidths[] = {28, 32, 56, 64};
+
 inline size_t steps_bytes(const RecurrencePlan& p, int D) {
   return p.segments > 1 ? (size_t)p.parts * p.segments * 2 * D * sizeof(float) : 0;
 }
@@ -528,15 +542,11 @@ cudaError_t launch_segments(const RecurrenceArgs& a, const RecurrencePlan& p, do
 
 inline size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-inline int copy_unit(const void* p, long long pitch, int D, int elem) {
+// Whether rows start and end on 16 bytes, as boxes of them have to.
+inline bool box_rows(const void* p, long long pitch, int D, int elem) {
   const unsigned long long all = reinterpret_cast<uintptr_t>(p) | (unsigned long long)pitch * elem |
                                  (unsigned long long)D * elem;
-  return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : 2;
-}
-
-// Whether the copy engine takes rows as they are: starts, ends and distances in multiples of 16 bytes.
-inline bool engine_rows(const void* p, long long pitch, int D, int elem) {
-  return copy_unit(p, pitch, D, elem) == 16 && pitch * elem < (1LL << 40);
+  return all % 16 == 0 && pitch * elem < (1LL << 40);
 }
 
 // The map of rows [tokens, D] `pitch` elements apart for boxes of `box` tokens of `width` channels.

@@ -33,10 +33,9 @@ constexpr int kStages = 2;
 constexpr int kGroup = kRecCarry / kTau;   // windows from one saved state to the next
 static_assert(kRecCarry % kTau == 0 && kTile % kRecCarry == 0, "saved states stand in front of windows");
 
-template <typename T, typename G, bool kFused, int N>
+template <typename T, typename G, bool kFused, int N, bool kBoxes>
 struct BwdShared {
-  static constexpr int W = 32 * N;
-  static constexpr int kRowX = W * sizeof(T), kRowG = W * sizeof(G);
+  static constexpr int kRowX = kRowBytes<T, N, kBoxes>, kRowG = kRowBytes<G, N, kBoxes>;
   static constexpr int kAtDy = kTau * kRowX, kAtG = 2 * kTau * kRowX, kAtI = kAtG + kTau * kRowG;
   static constexpr int kWindow = kAtG + (kFused ? 2 : 1) * kTau * kRowG;
   alignas(128) char ring[kStages][kWarps][kWindow];
@@ -47,23 +46,22 @@ struct BwdShared {
   uint64_t arrived[kStages][kWarps];   // the copy engine's
 };
 
-// kEngine: the copy engine takes the inputs' rows, and outputs go out whole.
-template <typename T, typename G, bool kFused, int N, bool kEngine, bool kSteps>
+// kBoxes: a window's inputs come in boxes, and outputs go out whole; else row by row.
+template <typename T, typename G, bool kFused, int N, bool kBoxes, bool kSteps>
 __global__ void __launch_bounds__(kWarps * 32, 1)
-    recurrence_bwd_kernel(RecurrenceArgs a, int parts, Segments segments, float* steps, int x_unit, int g_unit, int i_unit, int dy_unit,
-                          float* dlam_part, const __grid_constant__ CUtensorMap x_map,
+    recurrence_bwd_kernel(RecurrenceArgs a, int parts, Segments segments, float* steps, float* dlam_part, const __grid_constant__ CUtensorMap x_map,
                           const __grid_constant__ CUtensorMap dy_map, const __grid_constant__ CUtensorMap g_map,
                           const __grid_constant__ CUtensorMap i_map) {
-  using Shared = BwdShared<T, G, kFused, N>;
+  using Shared = BwdShared<T, G, kFused, N, kBoxes>;
   using Values = Lanes<N>;
-  constexpr int W = Shared::W;
+  constexpr int W = kLanes<kBoxes> * N;
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   const int segment = segments.from + blockIdx.x % segments.here, part_index = blockIdx.x / segments.here % parts,
             block = blockIdx.x / segments.here / parts;
   const int ch = block * W + lane * N;
-  const int mine = max(0, min(N, a.D - ch));
+  const int mine = lane < kLanes<kBoxes> ? max(0, min(N, a.D - ch)) : 0;
   WindowFinder finder;
   finder.seq = Sequences{a.cu_seqlens, a.num_seqs, a.T, a.cu_seqlens ? a.T : a.B * a.T};
   finder.slots = nullptr;
@@ -108,9 +106,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int rounds = segments.tile(segment + 1, tiles) - segments.tile(segment, tiles);
   auto tile_of = [&](int round) { return first - round; };
   unsigned lost = 0;   // kinds of waits that have run out
+  const int tokens = finder.seq.tokens;
+  const Rows rows_x = Rows::of<T>(a.x, a.x_pitch, tokens, a.D), rows_dy = Rows::of<T>(a.dy, a.D, tokens, a.D),
+             rows_g = Rows::of<G>(a.g, a.g_pitch, tokens, a.D), rows_i = Rows::of<G>(a.i, a.i_pitch, tokens, a.D);
+  auto shift = [&](const Rows& rows, int token, int elem) { return kBoxes ? 0 : rows.shift(token, block * W * elem); };
   auto fetch = [&](int round) {
     char* const to = sh.ring[round % kStages][warp];
-    if constexpr (kEngine) {
+    if constexpr (kBoxes) {
       if (round < rounds && lane == 0 && !(lost & kCopy)) {
         uint64_t* const bar = &sh.arrived[round % kStages][warp];
         const int w0 = tile_of(round) * kTile + warp * kTau;
@@ -122,16 +124,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       }
     } else {
       if (round < rounds) {
-        const int w0 = tile_of(round) * kTile + warp * kTau, lo = part.t0 - w0, hi = part.t1 - w0, left = a.D - block * W;
-        auto copy = [&](auto type, int at, const void* base, long long pitch, int unit) {
-          using E = decltype(type);
-          copy_window<kTau, W * sizeof(E)>(to + at, reinterpret_cast<const char*>(static_cast<const E*>(base) + w0 * pitch + block * W),
-                                           pitch * (long long)sizeof(E), lo, hi, left * (int)sizeof(E), unit, lane);
+        const int start = tile_of(round) * kTile + warp * kTau, values = min(W, a.D - block * W);
+        auto copy = [&](auto elem, const Rows& rows, int at) {
+          using E = decltype(elem);
+          rows.template copy<E, kTau, kRowBytes<E, N, kBoxes>>(to + at, start, part.t0, part.t1, block * W * (int)sizeof(E),
+                                                               values * (int)sizeof(E), lane);
         };
-        copy(T{}, Shared::kAtDy, a.dy, a.D, dy_unit);
-        copy(G{}, Shared::kAtG, a.g, a.g_pitch, g_unit);
-        if (!kSteps) copy(T{}, 0, a.x, a.x_pitch, x_unit);
-        if (kFused && !kSteps) copy(G{}, Shared::kAtI, a.i, a.i_pitch, i_unit);
+        copy(T{}, rows_dy, Shared::kAtDy);
+        copy(G{}, rows_g, Shared::kAtG);
+        if (!kSteps) copy(T{}, rows_x, 0);
+        if (kFused && !kSteps) copy(G{}, rows_i, Shared::kAtI);
       }
       copies_close();
     }
@@ -157,15 +159,21 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (!kSteps && warp % kGroup == 0 && w0 >= part.t0 && w0 < part.t1) h = read_state<N>(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, mine);
     const Window w = finder.template find<kTau, true>(w0, lane);
     const unsigned reset = w.first | w.dead, reset_e = w.last | w.dead;
-    if constexpr (kEngine) {
+    if constexpr (kBoxes) {
       wait_for_copies<kStages>(sh.arrived, warp, round, rounds, &lost, a.dev_status);
     } else {
       copies_wait<kStages - 1>();
       __syncwarp();
     }
     char* const from = sh.ring[round % kStages][warp];
-    // s of a token, for the second half, where its r (and i) were: each lane's values take the place of its own
+    auto row_x = [&](int j) { return read_row<kBoxes, T, N>(from + j * Shared::kRowX + shift(rows_x, w0 + j, sizeof(T)), lane); };
+    auto row_dy = [&](int j) {
+      return read_row<kBoxes, T, N>(from + Shared::kAtDy + j * Shared::kRowX + shift(rows_dy, w0 + j, sizeof(T)), lane);
+    };
+    // s of a token, for the second half, where its r (and i) were: each lane's values take the place of its own (or,
+    // of rows that are shifted, of a neighbour's, which has read them)
     auto keep = [&](int j, const Values& root) {
+      if (!kBoxes) __syncwarp();
       float* const at = reinterpret_cast<float*>(from + Shared::kAtG + j * Shared::kRowG) + lane;
       at[0] = root.v[0];
       if constexpr (N == 2) at[(Shared::kAtI - Shared::kAtG) / 4] = root.v[1];
@@ -181,7 +189,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     Values da[kTau], db[kTau], L = fill<N>(0.f), H = fill<N>(0.f), E = fill<N>(0.f);
 #pragma unroll
     for (int j = 0; j < kTau; ++j) {
-      const Values g = read_row<G, N>(from + Shared::kAtG + j * Shared::kRowG, lane);
+      const Values g = read_row<kBoxes, G, N>(from + Shared::kAtG + j * Shared::kRowG + shift(rows_g, w0 + j, sizeof(G)), lane);
       Values l;
       if (kSteps) {
         l = kFused ? times(rate, gate_sigmoid(g)) : g * kLog2e;
@@ -189,9 +197,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         L = L + l;
         continue;
       }
-      const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
+      const Values x = row_x(j);
       if (kFused) {
-        const Values i = read_row<G, N>(from + Shared::kAtI + j * Shared::kRowG, lane);
+        const Values i = read_row<kBoxes, G, N>(from + Shared::kAtI + j * Shared::kRowG + shift(rows_i, w0 + j, sizeof(G)), lane);
         auto sigmoid = [](float x) { return gate_sigmoid(x); };   // (packed, 1% slower here)
         const Values sr = each(sigmoid, g), si = each(sigmoid, i);
         sh.sigmoid[warp][0][j][lane] = sr;
@@ -224,13 +232,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (w.plain) {
 #pragma unroll
       for (int j = kTau - 1; j >= 0; --j)   // (of delta; e is a of it)
-        E = fma(j + 1 < kTau ? da[j + 1] : E, E, read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane));
+        E = fma(j + 1 < kTau ? da[j + 1] : E, E, row_dy(j));
       E = da[0] * E;
     } else {
 #pragma unroll
       for (int j = kTau - 1; j >= 0; --j) {
         if (w.last >> j & 1) E = state_of(a.d_final_state, __shfl_sync(~0u, w.row, j));
-        E = w.dead >> j & 1 ? fill<N>(0.f) : da[j] * (read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane) + E);
+        E = w.dead >> j & 1 ? fill<N>(0.f) : da[j] * (row_dy(j) + E);
       }
     }
     // (a slot of the state is written again after e has come through its reader)
@@ -277,10 +285,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         const bool dead = !plain && (w.dead >> j & 1);
         Values ox, og, oi;
         if (!plain && (w.last >> j & 1)) e = state_of(a.d_final_state, __shfl_sync(~0u, w.row, j));
-        const Values delta = read_row<T, N>(from + Shared::kAtDy + j * Shared::kRowX, lane) + e;
+        const Values delta = row_dy(j) + e;
         e = da[j] * delta;
         if (kFused) {
-          const Values x = read_row<T, N>(from + j * Shared::kRowX, lane);
+          const Values x = row_x(j);
           const Values sr = sh.sigmoid[warp][0][j][lane], si = sh.sigmoid[warp][1][j][lane];
           // where nothing decays, s = 0; what multiplies 1 / s below is 0 then (bounded, it stays finite)
           const Values root = kept(j), inv = each([](float v) { return rcp(fmaxf(v, 1e-19f)); }, root);
@@ -301,18 +309,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
           const int row = __shfl_sync(~0u, w.row, j);
           if (a.d_initial_state) write_state(a.d_initial_state + (size_t)row * a.D + ch, e, mine);
         }
-        write_row<kEngine>(dx + (size_t)j * a.D, ox, mine);
-        write_row<kEngine>(dg + (size_t)j * a.D, og, mine);
-        if (kFused) write_row<kEngine>(di + (size_t)j * a.D, oi, mine);
+        write_row<kBoxes>(dx + (size_t)j * a.D, ox, mine);
+        write_row<kBoxes>(dg + (size_t)j * a.D, og, mine);
+        if (kFused) write_row<kBoxes>(di + (size_t)j * a.D, oi, mine);
       }
     };
     if (w.plain) gradients(std::true_type{});
     else gradients(std::false_type{});
-    if (kEngine && kFused) fence_proxy_async_smem();   // (s was written where the next copies go)
+    if (kBoxes && kFused) fence_proxy_async_smem();   // (s was written where the next copies go)
     __syncwarp();
     fetch(round + kStages);
   }
-  if (!kEngine) copies_wait<0>();
+  if (!kBoxes) copies_wait<0>();
   if (!kSteps && segment + 1 < segments.count && segment == 0 && warp == 0)   // (nothing is behind it)
     write_step(steps + (size_t)part_index * segments.count * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane), true, mine);
   if (kSteps) {   // (a segment that resets takes nothing from behind it, whatever L says)
@@ -362,40 +370,39 @@ RecurrencePlan plan_of(int B, int T, int D, int N, bool packed, int width) {
   return recurrence_plan((long long)B * T, D, N, packed, width, kTile, kFirst);
 }
 
-template <typename T, typename G, bool kFused, int N, bool kEngine, typename... Args>
+template <typename T, typename G, bool kFused, int N, bool kBoxes, typename... Args>
 cudaError_t launch_bwd(const RecurrenceArgs& a, const RecurrencePlan& p, float* steps, const Args&... args) {
-  return launch_segments<recurrence_bwd_kernel<T, G, kFused, N, kEngine, false>, recurrence_bwd_kernel<T, G, kFused, N, kEngine, true>>(
-      a, p, kFirst, kWarps * 32, sizeof(BwdShared<T, G, kFused, N>), steps, args...);
+  return launch_segments<recurrence_bwd_kernel<T, G, kFused, N, kBoxes, false>, recurrence_bwd_kernel<T, G, kFused, N, kBoxes, true>>(
+      a, p, kFirst, kWarps * 32, sizeof(BwdShared<T, G, kFused, N, kBoxes>), steps, args...);
 }
 
 template <typename T, typename G, bool kFused, int N>
-cudaError_t launch_bwd(const RecurrenceArgs& a, float* steps, float* part) {
-  constexpr int W = 32 * N;
+cudaError_t launch_bwd(const RecurrenceArgs& a, float* steps) {
   const long long tokens = (long long)a.B * a.T;
-  const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, W);
-  const int x_unit = copy_unit(a.x, a.x_pitch, a.D, sizeof(T)), g_unit = copy_unit(a.g, a.g_pitch, a.D, sizeof(G)),
-            i_unit = copy_unit(a.i, a.i_pitch, a.D, sizeof(G)), dy_unit = copy_unit(a.dy, a.D, a.D, sizeof(T));
   auto whole = [&](const void* q, size_t elem) { return reinterpret_cast<uintptr_t>(q) % (N * elem) == 0; };
-  const bool engine = tokens > 0 && engine_rows(a.x, a.x_pitch, a.D, sizeof(T)) && engine_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
-                      (!kFused || engine_rows(a.i, a.i_pitch, a.D, sizeof(G))) && engine_rows(a.dy, a.D, a.D, sizeof(T)) &&
-                      whole(a.dx, sizeof(T)) && whole(a.dg, sizeof(G)) && whole(a.di, sizeof(G));
+  const bool boxes = tokens > 0 && box_rows(a.x, a.x_pitch, a.D, sizeof(T)) && box_rows(a.g, a.g_pitch, a.D, sizeof(G)) &&
+                     (!kFused || box_rows(a.i, a.i_pitch, a.D, sizeof(G))) && box_rows(a.dy, a.D, a.D, sizeof(T)) &&
+                     whole(a.dx, sizeof(T)) && whole(a.dg, sizeof(G)) && whole(a.di, sizeof(G));
+  const int W = (boxes ? kLanes<true> : kLanes<false>)*N;
+  const RecurrencePlan p = plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, W);
+  float* const part = a.dlam ? reinterpret_cast<float*>(reinterpret_cast<char*>(steps) + up256(steps_bytes(p, a.D))) : nullptr;
   CUtensorMap mx{}, md{}, mg{}, mi{};
-  if (engine && (!rows_map(&mx, a.x, tokens, a.D, a.x_pitch, sizeof(T), W, kTau) ||
+  if (boxes && (!rows_map(&mx, a.x, tokens, a.D, a.x_pitch, sizeof(T), W, kTau) ||
                  !rows_map(&md, a.dy, tokens, a.D, a.D, sizeof(T), W, kTau) ||
                  !rows_map(&mg, a.g, tokens, a.D, a.g_pitch, sizeof(G), W, kTau) ||
                  (kFused && !rows_map(&mi, a.i, tokens, a.D, a.i_pitch, sizeof(G), W, kTau))))
     return cudaErrorInvalidValue;
   const cudaError_t err =
-      engine ? launch_bwd<T, G, kFused, N, true>(a, p, steps, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi)
-             : launch_bwd<T, G, kFused, N, false>(a, p, steps, x_unit, g_unit, i_unit, dy_unit, part, mx, md, mg, mi);
+      boxes ? launch_bwd<T, G, kFused, N, true>(a, p, steps, part, mx, md, mg, mi)
+             : launch_bwd<T, G, kFused, N, false>(a, p, steps, part, mx, md, mg, mi);
   if (err != cudaSuccess || !kFused || !part) return err;
   return launch_behind(recurrence_dlam_kernel, (a.D + 31) / 32, 1024, 0, a.stream, a, (const float*)part,
                        p.parts * p.segments);
 }
 
 template <typename T, typename G, int N>
-cudaError_t launch_bwd(const RecurrenceArgs& a, float* steps, float* part) {
-  return a.lam ? launch_bwd<T, G, true, N>(a, steps, part) : launch_bwd<T, G, false, N>(a, steps, part);
+cudaError_t launch_bwd(const RecurrenceArgs& a, float* steps) {
+  return a.lam ? launch_bwd<T, G, true, N>(a, steps) : launch_bwd<T, G, false, N>(a, steps);
 }
 
 }  // namespace
@@ -405,7 +412,7 @@ cudaError_t launch_bwd(const RecurrenceArgs& a, float* steps, float* part) {
 size_t recurrence_bwd_workspace_bytes(int B, int T, int D, int num_seqs, bool fused) {
   size_t steps = 0, rows = 0;
   for (int packed = 0; packed < 2; ++packed)
-    for (int width = 32; width <= 64; width *= 2) {
+    for (int width : kWidths) {
       const RecurrencePlan p = plan_of(B, T, D, num_seqs, packed, width);
       steps = std::max(steps, steps_bytes(p, D));
       if (fused) rows = std::max(rows, (size_t)p.parts * p.segments);
@@ -422,9 +429,6 @@ cudaError_t launch_recurrence_bwd(const RecurrenceArgs& args) {
   void* const forward = ws;
   ws += up256(recurrence_fwd_workspace_bytes(a.B, a.T, a.D, a.num_seqs));
   float* const steps = reinterpret_cast<float*>(ws);
-  const int width = a.io_dtype == GDN_BF16 && a.g_dtype == GDN_BF16 ? 64 : 32;
-  ws += up256(steps_bytes(plan_of(a.B, a.T, a.D, a.num_seqs, a.cu_seqlens != nullptr, width), a.D));
-  float* const part = a.dlam ? reinterpret_cast<float*>(ws) : nullptr;
   if (!a.carries && (long long)a.B * a.T > 0) {
     RecurrenceArgs f = a;
     f.carries = a.carries = carries;
@@ -434,9 +438,9 @@ cudaError_t launch_recurrence_bwd(const RecurrenceArgs& args) {
     const cudaError_t err = launch_recurrence_fwd(f);
     if (err != cudaSuccess) return err;
   }
-  if (a.io_dtype == GDN_F32) return launch_bwd<float, float, 1>(a, steps, part);
-  return a.g_dtype == GDN_F32 ? launch_bwd<__nv_bfloat16, float, 1>(a, steps, part)
-                              : launch_bwd<__nv_bfloat16, __nv_bfloat16, 2>(a, steps, part);
+  if (a.io_dtype == GDN_F32) return launch_bwd<float, float, 1>(a, steps);
+  return a.g_dtype == GDN_F32 ? launch_bwd<__nv_bfloat16, float, 1>(a, steps)
+                              : launch_bwd<__nv_bfloat16, __nv_bfloat16, 2>(a, steps);
 }
 
 }  // namespace gdn
