@@ -127,9 +127,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (int k = 0; k < kStages; ++k) fetch(k);
 
   next_may_start();
-  if (!kSteps && segment > 0) wait_for_previous();
-  if (warp == 0)
-    sh.chain.start(lane, kSteps ? fill<N>(0.f) : behind_steps<N>(steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine));
+  Values start = fill<N>(0.f);
+  if (!kSteps && segment > 0) {
+    wait_for_previous();
+    start = behind_steps(sh.chain, steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine, warp, lane);
+  }
+  if (warp == 0) sh.chain.start(lane, start);
   Values sum = fill<N>(0.f);   // of a segment's logarithms
   bool any_reset = false;
   // a first token's initial state: lane j's sequence, of which lanes know the cache's row and the number

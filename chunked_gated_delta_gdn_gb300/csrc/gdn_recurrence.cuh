@@ -434,7 +434,7 @@ struct Chain {
 
 // ---------------------------------------------------------------- segments
 
-constexpr int kMaxSegments = 64;
+constexpr int kMaxSegments = 160;
 constexpr float kReset = __builtin_huge_valf();   // in L's place: "reset"
 
 // Where parts are too few for the SMs their tiles are cut into segments.  A first launch runs segment 0 of each,
@@ -459,17 +459,27 @@ __device__ __forceinline__ void write_step(float* steps, int D, int ch, const La
   write_state(steps + ch, reset ? fill<N>(kReset) : L, mine);
   write_state(steps + D + ch, H, mine);
 }
-// The state behind the first `count` segments.
-template <int N>
-__device__ __forceinline__ Lanes<N> behind_steps(const float* first, int count, int D, int ch, int mine) {
-  Lanes<N> h = fill<N>(0.f);
+// The state behind the first `count` segments, for the warp that starts the chain; every warp joins a share of the
+// steps, which stand in the chain's slots for a moment.
+template <int kWarps, int N>
+__device__ __forceinline__ Lanes<N> behind_steps(Chain<kWarps, N>& chain, const float* first, int count, int D, int ch, int mine,
+                                                 int warp, int lane) {
+  Lanes<N> L = fill<N>(0.f), H = fill<N>(0.f);
 #pragma unroll 4
-  for (int k = 0; k < count; ++k) {
+  for (int k = count * warp / kWarps; k < count * (warp + 1) / kWarps; ++k) {
     const float* const at = first + (size_t)k * 2 * D + ch;
-    h = each([](float l, float x, float h) { return l == kReset ? h : fmaf(ex2(l), x, h); }, read_state<N>(at, mine), h,
-             read_state<N>(at + D, mine));
+    const Lanes<N> l = read_state<N>(at, mine), x = read_state<N>(at + D, mine);
+    H = each([](float l, float x, float h) { return l == kReset ? x : fmaf(ex2(l), h, x); }, l, x, H);
+    L = each([](float l, float s) { return l == kReset || s == kReset ? kReset : s + l; }, l, L);
   }
-  return h;
+  chain.slot[warp][lane].L = L;
+  chain.slot[warp][lane].H = H;
+  __syncthreads();
+  H = fill<N>(0.f);
+  for (int k = 0; k < kWarps; ++k)
+    H = each([](float l, float x, float h) { return l == kReset ? x : fmaf(ex2(l), h, x); }, chain.slot[k][lane].L,
+             chain.slot[k][lane].H, H);
+  return H;
 }
 
 // ---------------------------------------------------------------- launches
