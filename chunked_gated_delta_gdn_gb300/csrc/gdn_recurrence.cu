@@ -9,12 +9,13 @@
 // of its window and walks its tokens.  Few parts are cut into segments, whose steps a launch of their own
 // (kSteps) makes.
 //
-// Bound by bytes: 3 or (fused) 4 values an element.  bf16, 4 x 32768 x 4096: fused 703 us, 6.1 TB/s; given 557 us, 5.8
-// TB/s.  2 x 8192 x 4096 has 128 CTAs for 152 SMs and is bound by what they issue (37 instructions an
-// element with fused gates before some were packed, three exponentials, two reciprocals and a root among them; 77% of the issue slots):
-// 102 us, 5.3 TB/s, given 79 us.  One channel a lane (twice the CTAs, half as wide rows): 122 and 107 us; 8-token
-// windows with three CTAs an SM, and pairs in packed arithmetic (113 us, spilled registers), were slower too.
-// In two segments or more, one 32768 x 2048: 113 us for 59 us of bytes, some of which are read twice.
+// Bound by bytes: 3 or (fused) 4 values an element.  bf16, 4 x 32768 x 4096: fused 700 us, 6.1 TB/s; given 605 us, 5.3
+// TB/s (three stages instead of two 664 us: the further CTAs run apart, the less DRAM does).  2 x 8192 x
+// 4096 has 128 CTAs for 152 SMs; with fused gates they are bound by what they issue (three exponentials, two
+// reciprocals and a root among 37 instructions an element, before some were packed; 77% of the issue slots):
+// 102 us, 5.3 TB/s; given 73 us, 5.5 TB/s.  One channel a lane (twice the CTAs, half as wide rows): 122 and 107 us;
+// 8-token windows with three CTAs an SM, and all of it in packed arithmetic (113 us, spilled registers), were
+// slower too.  In segments, one 32768 x 2048 given: 102 us for 59 us of bytes, some of which are read twice.
 #include <algorithm>
 
 #include "gdn_recurrence.cuh"

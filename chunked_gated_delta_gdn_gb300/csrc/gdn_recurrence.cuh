@@ -441,7 +441,7 @@ constexpr float kReset = __builtin_huge_valf();   // in L's place: "reset"
 // which has nothing in front of it; beside it a second one makes the steps (L, H) of the others but the
 // last from nothing in front of them; a third one runs those and the last from the steps of the
 // segments before them.  Steps: [parts][segments][2][D].  (Clusters of up to 16 CTAs with the chain in their shared
-// memory: 103 us against 113 for one 32768 x 2048, but two to four times as slow where a cluster's CTAs
+// memory: 103 us against 102 for one 32768 x 2048, but two to four times as slow where a cluster's CTAs
 // have little to do, and of no use to more than 16 segments.)
 struct Segments {
   int count, from, here;   // of a part; this launch's: [from, from + here)
