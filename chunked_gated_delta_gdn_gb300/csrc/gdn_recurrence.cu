@@ -52,8 +52,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const int segment = segments.from + blockIdx.x % segments.here, part_index = blockIdx.x / segments.here % parts,
-            block = blockIdx.x / segments.here / parts;
+  // blocks next to one another read the same tokens' rows at about the same time (32 packed prompts of 100 to 4096
+  // tokens: 388 us; with the parts next to one another 430)
+  const int blocks = (a.D + W - 1) / W, block = blockIdx.x % blocks, segment = segments.from + blockIdx.x / blocks % segments.here,
+            part_index = blockIdx.x / blocks / segments.here;
   const int ch = block * W + lane * N;   // this lane's first channel
   const int mine = lane < kLanes<kBoxes> ? max(0, min(N, a.D - ch)) : 0;
   WindowFinder finder;

@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   extern __shared__ __align__(1024) char shared_bytes[];
   Shared& sh = *reinterpret_cast<Shared*>(shared_bytes);
   const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
-  const int segment = segments.from + blockIdx.x % segments.here, part_index = blockIdx.x / segments.here % parts,
-            block = blockIdx.x / segments.here / parts;
+  const int blocks = (a.D + W - 1) / W, block = blockIdx.x % blocks, segment = segments.from + blockIdx.x / blocks % segments.here,
+            part_index = blockIdx.x / blocks / segments.here;
   const int ch = block * W + lane * N;
   const int mine = lane < kLanes<kBoxes> ? max(0, min(N, a.D - ch)) : 0;
   WindowFinder finder;
