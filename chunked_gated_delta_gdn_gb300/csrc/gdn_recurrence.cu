@@ -9,13 +9,13 @@
 // of its window and walks its tokens.  Few parts are cut into segments, whose steps a launch of their own
 // (kSteps) makes.
 //
-// Bound by bytes: 3 or (fused) 4 values an element.  bf16, 4 x 32768 x 4096: fused 700 us, 6.1 TB/s; given 605 us, 5.3
-// TB/s (three stages instead of two 664 us: the further CTAs run apart, the less DRAM does).  2 x 8192 x
-// 4096 has 128 CTAs for 152 SMs; with fused gates they are bound by what they issue (three exponentials, two
-// reciprocals and a root among 37 instructions an element, before some were packed; 77% of the issue slots):
-// 102 us, 5.3 TB/s; given 73 us, 5.5 TB/s.  One channel a lane (twice the CTAs, half as wide rows): 122 and 107 us;
-// 8-token windows with three CTAs an SM, and all of it in packed arithmetic (113 us, spilled registers), were
-// slower too.  In segments, one 32768 x 2048 given: 102 us for 59 us of bytes, some of which are read twice.
+// Bound by bytes: 3 or (fused) 4 values an element.  bf16, 4 x 32768 x 4096: given 473 us, 6.8 TB/s (a plain copy's
+// rate); fused 692 us, 6.2 TB/s.  2 x 8192 x 4096 has 128 CTAs for 152 SMs; with fused gates they are bound by
+// what they issue (three exponentials, two reciprocals and a root among 37 instructions an element, before some
+// were packed; 77% of the issue slots): 101 us, 5.3 TB/s; given 66 us, 6.1 TB/s.  One channel a lane (twice the CTAs,
+// half as wide rows): 122 and 107 us; three stages with given gates, 523 and 68 us; 8-token windows with three CTAs an
+// SM, and all of it in packed arithmetic (113 us, spilled registers), were slower too.  In segments, one 32768 x
+// 2048 given: 103 us for 59 us of bytes, some of which are read twice.
 #include <algorithm>
 
 #include "gdn_recurrence.cuh"
@@ -178,8 +178,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
       L = L + l;
       H = fma(da[j], H, db[j]);
     }
-    __syncwarp();
-    fetch(round + kStages);
+    if (kSteps) {
+      __syncwarp();
+      fetch(round + kStages);
+    }
     if (reset) {   // a first token takes its sequence's state in, a dead one nothing
 #pragma unroll
       for (int j = 0; j < kTau; ++j) {
@@ -217,6 +219,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         }
       }
     }
+    // (before the hand-over, as soon as its slot is free, the copy is too early where there are outputs: CTAs run
+    // apart, and DRAM does less: 4 x 32768 x 4096 given 590 us against 473, 2 x 8192 77 against 66)
+    __syncwarp();
+    fetch(round + kStages);
   }
   if (!kBoxes) copies_wait<0>();
   if (!kSteps && segment + 1 < segments.count && segment == 0 && warp + 1 == kWarps)   // (nothing is in front of it)
