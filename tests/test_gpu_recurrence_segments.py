@@ -9,7 +9,8 @@ from chunked_gated_delta_gdn_gb300 import _lib
 from tests.test_gpu_recurrence import BF16, F32, NAN, backward, check, forward, make, reference, rel, seeded, tol  # noqa: F401
 
 pytestmark = pytest.mark.gpu
-LENS = [700, 1, 0, 2500, 300, 0, 5, 2400, 40]
+LENS = [700, 1, 0, 2500, 300, 0, 5, 2400, 40]       # whole forwards, cut backwards
+LONG = [3000, 1, 0, 9000, 1300, 0, 5, 9600, 40]     # both cut
 
 
 def cut(T, D, N):
@@ -19,10 +20,10 @@ def cut(T, D, N):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("fused", [False, True])
-@pytest.mark.parametrize("lens,tail,D", [(LENS, 77, 24), ([5000], 0, 70), ([1, 4097, 0], 3, 8), ([256] * 16, 0, 40),
+@pytest.mark.parametrize("lens,tail,D", [(LENS, 77, 24), (LONG, 77, 24), ([5000], 0, 70), ([1, 4097, 0], 3, 8), ([256] * 16, 0, 40),
                                          ([2100, 2100], 0, 40), ([40] * 90, 500, 33), ([0, 3000], 3000, 16)])
 def test_packed(lens, tail, D, fused, dtype):
-    if len(lens) < 10:   # (many sequences are parts enough, and stay whole)
+    if len(lens) < 4 or lens is LONG:   # (many sequences are parts enough, and stay whole)
         assert cut(sum(lens) + tail, D, len(lens))
     check((1, sum(lens) + tail, D), dtype, None, fused, lens=lens)
 
@@ -34,19 +35,20 @@ def test_dense(shape, fused):
     check(shape, F32, F32, fused, state=False)
 
 
+@pytest.mark.parametrize("lens", [LENS, LONG])
 @pytest.mark.parametrize("fused", [False, True])
-def test_slots_in_place(fused):
+def test_slots_in_place(fused, lens):
     """States come from and go to the same slots, which sequences of several segments share in time."""
-    T, D = sum(LENS) + 50, 40
+    T, D = sum(lens) + 50, 40
     ins = make((1, T, D), F32, fused=fused)
-    cu = torch.tensor([sum(LENS[:n]) for n in range(len(LENS) + 1)], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([sum(lens[:n]) for n in range(len(lens) + 1)], dtype=torch.int32, device="cuda")
     slots = torch.tensor([3, 9, 1, 0, 7, -1, 5, 2, -1], dtype=torch.int32, device="cuda")
     start = torch.randn(11, D, device="cuda")
-    assert cut(T, D, len(LENS))
-    live = [n for n in range(len(LENS)) if slots[n] >= 0]
+    assert cut(T, D, len(lens)) == (lens is LONG)
+    live = [n for n in range(len(lens)) if slots[n] >= 0]
     rows = torch.cat([torch.arange(int(cu[n]), int(cu[n + 1]), device="cuda") for n in live])
     want, fin, _ = reference([t[:, rows] if t.dim() == 3 else t for t in ins], start[slots[live].long()],
-                             [LENS[n] for n in live])
+                             [lens[n] for n in live])
     for t in ins[:3]:
         if t.dim() == 3:
             t[:, int(cu[8]):] = NAN      # padding's and no sequence's
@@ -111,10 +113,10 @@ def test_bad_packed_lengths():
         assert not any(t.any() for t in grads)
 
 
-def test_non_finite_values_stay_in_their_sequence():
-    lens = [900, 1300, 700, 1800]
-    cu = torch.tensor([0, 900, 2200, 2900, 4700], dtype=torch.int32, device="cuda")
-    x, g = make((1, 4700, 16), F32)
+@pytest.mark.parametrize("tail", [0, 9000])     # (the longer one is cut in the forward, too)
+def test_non_finite_values_stay_in_their_sequence(tail):
+    cu = torch.tensor([0, 900, 2200, 2900, 4700 + tail], dtype=torch.int32, device="cuda")
+    x, g = make((1, 4700 + tail, 16), F32)
     dy = torch.randn_like(x)
     y, fin = gdn.gated_linear_recurrence(x, g, None, True, cu)
     dx, dg, _ = gdn.gated_linear_recurrence_bwd(x, g, dy, cu_seqlens=cu)
