@@ -12,6 +12,7 @@ namespace {
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 size_t elem_size(int d) { return d == GDN_BF16 ? 2 : 4; }
+constexpr int kMaxChannels = 1 << 28;   // (a row's bytes are counted in 32 bits)
 bool is_dtype(int d) { return d == GDN_F32 || d == GDN_BF16; }
 
 // Sizes, and the gates' form: lam and i come together.
@@ -19,7 +20,7 @@ gdn_status_t check(const void* x, const void* g, const void* i, const float* lam
                    long long g_pitch, long long i_pitch, long long tokens, int D, int io_dtype, int g_dtype) {
   if (!is_dtype(io_dtype) || !is_dtype(g_dtype) || (g_dtype != GDN_F32 && g_dtype != io_dtype))
     return GDN_ERR_DTYPE;
-  if (D <= 0 || tokens < 0 || tokens > 0x7fff0000LL) return GDN_ERR_SHAPE;
+  if (D <= 0 || D > kMaxChannels || tokens < 0 || tokens > 0x7fff0000LL) return GDN_ERR_SHAPE;
   if (tokens > 0 && (x_pitch < D || g_pitch < D || (lam && i_pitch < D))) return GDN_ERR_SHAPE;
   if (lam && !(c >= 0.f && c <= 3.0e38f)) return GDN_ERR_SHAPE;
   if (tokens > 0 && (!x || !g || (lam && !i))) return GDN_ERR_NULL;
@@ -44,12 +45,12 @@ gdn_status_t check_batch(int B, int T, const int32_t* cu_seqlens, int num_seqs, 
 extern "C" {
 
 size_t gdn_linear_recurrence_carries_size(int B, int T, int D) {
-  if (B < 0 || T < 0 || D <= 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
+  if (B < 0 || T < 0 || D <= 0 || D > kMaxChannels || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
   return gdn::recurrence_carries_bytes((long long)B * T, D);
 }
 
 size_t gdn_linear_recurrence_fwd_workspace_size(int B, int T, int D, int num_seqs) {
-  if (B < 0 || T < 0 || D <= 0 || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
+  if (B < 0 || T < 0 || D <= 0 || D > kMaxChannels || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
   return gdn::recurrence_fwd_workspace_bytes(B, T, D, num_seqs);
 }
 
@@ -98,7 +99,7 @@ gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void*
 }
 
 size_t gdn_linear_recurrence_bwd_workspace_size(int B, int T, int D, int num_seqs, int fused_gates) {
-  if (B < 0 || T < 0 || D <= 0 || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
+  if (B < 0 || T < 0 || D <= 0 || D > kMaxChannels || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
   return gdn::recurrence_bwd_workspace_bytes(B, T, D, num_seqs, fused_gates != 0);
 }
 

@@ -68,8 +68,8 @@ def _inputs(x, g, i, lam, c, dims, g_name):
     if x.dim() != dims:
         raise ValueError("x must be %s" % ("[B, T, D]" if dims == 3 else "[n, D]"))
     dev, shape = x.device, x.shape
-    if shape[-1] < 1:
-        raise ValueError("x has no channels")
+    if not 1 <= shape[-1] <= 1 << 28:
+        raise ValueError("x needs 1 to 2^28 channels (got %d)" % shape[-1])
     _int32("gated linear recurrence", *shape)
     px = _pitch(x, "x", (torch.float32, torch.bfloat16), dev, shape)
     pg = _pitch(g, g_name, (x.dtype, torch.float32), dev, shape)

@@ -552,7 +552,7 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
  *               are log-decays: at most 0, -inf keeps nothing.  Larger ones are taken as they are,
  *               where the product of any successive a_t of a sequence stays finite.
  *   lam         [D] fp32, device, and c >= 0: the fused gates' form.
- *   B, T, D     with cu_seqlens B is 1 and T the packed token count.  Any D >= 1; element
+ *   B, T, D     with cu_seqlens B is 1 and T the packed token count.  D 1 .. 2^28; element
  *               alignment serves, and rows that start and end on 16-byte boundaries are read faster.
  *   initial_state, output_final_state, final_state, cu_seqlens, num_seqs, state_indices,
  *   num_slots, stream  as gdn_chunk_fwd, states [N, D] or slots [num_slots, D] fp32: slot -1 is

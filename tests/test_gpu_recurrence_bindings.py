@@ -106,3 +106,20 @@ def test_two_calls_at_once():
     for runs in results.values():
         for got in runs:
             assert len(got) == len(want) and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_widest_rows():
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("not enough free memory")
+    x = torch.empty(1, (1 << 28) + 1, dtype=BF16, device="cuda")
+    state = torch.empty(1, 1, device="cuda")
+    for call in (lambda: gdn.gated_linear_recurrence(x[None], x[None]),
+                 lambda: gdn.gated_linear_recurrence_bwd(x[None], x[None], x[None]),
+                 lambda: gdn.gated_linear_recurrence_decode(x, x, state)):
+        with pytest.raises(ValueError, match="channels"):
+            call()
+    x = torch.randn(2, 1 << 28, device="cuda").to(BF16)[:, :]
+    g = torch.full_like(x, -1.0)
+    y, _ = gdn.gated_linear_recurrence(x[None], g[None])
+    want = x[0, -1000:].double() * torch.exp(torch.tensor(-1.0, dtype=torch.float64)).item() + x[1, -1000:].double()
+    assert ((y[0, 1, -1000:].double() - want).norm() / want.norm()).item() <= 2.5e-3

@@ -157,3 +157,14 @@ def test_bindings_refuse_cpu_tensors():
         gdn.gated_linear_recurrence(None, x)
     with pytest.raises(TypeError, match="torch.Tensor"):
         gdn.qk_norm_rotate(None, x)
+
+
+@pytest.mark.parametrize("call", [fwd, bwd, dec])
+def test_widest_rows(call):
+    """A row's bytes are counted in 32 bits: rows beyond 2^28 channels are refused."""
+    wide = (1 << 28) + 1
+    assert call(D=wide, px=wide, pg=wide) == _lib.GDN_ERR_SHAPE
+    L = _lib.load()
+    assert L.gdn_linear_recurrence_carries_size(1, 1, wide) == (1 << 64) - 1
+    assert L.gdn_linear_recurrence_fwd_workspace_size(1, 1, wide, 1) == (1 << 64) - 1
+    assert L.gdn_linear_recurrence_bwd_workspace_size(1, 1, wide, 1, 1) == (1 << 64) - 1
