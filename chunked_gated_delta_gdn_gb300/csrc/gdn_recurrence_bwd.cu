@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   for (int round = 0; round < rounds; ++round) {
     const int tile = tile_of(round), w0 = tile * kTile + warp * kTau;
     Values h = fill<N>(0.f);
-    if (!kSteps && warp % kGroup == 0 && w0 >= part.t0 && w0 < part.t1) h = read_state<N>(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, mine);
+    if (!kSteps && warp % kGroup == 0 && w0 >= part.t0 && w0 < part.t1)
+      h = read_state<N>(a.carries + (size_t)(w0 / kRecCarry) * a.D + ch, mine);
     const Window w = finder.template find<kTau, true>(w0, lane);
     const unsigned reset = w.first | w.dead, reset_e = w.last | w.dead;
     if constexpr (kBoxes) {
@@ -334,7 +335,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     if (warp > 0) return;   // the last one of the chain
     sum = fill<N>(0.f);
     for (int k = 0; k < kWarps; ++k) sum = sum + sums[k][lane];
-    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane), any_reset, mine);
+    write_step(steps + ((size_t)part_index * segments.count + segment) * 2 * a.D, a.D, ch, sum, sh.chain.end(rounds, lane),
+               any_reset, mine);
     wait_for_previous();
     return;
   }
