@@ -73,8 +73,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   finder.part = part_of(finder.seq, part_index, parts);
   const Part part = finder.part;
   // empty sequences' states, and bad slots
-  for (int n = part.n0 + segment * kWarps + warp; n < part.n1 && !kSteps; n += segments.count * kWarps) {
-    int row = n;
+  for (long long n = part.n0 + segment * kWarps + warp; n < part.n1 && !kSteps; n += segments.count * kWarps) {
+    int row = (int)n;
     if (a.state_indices) {
       row = a.state_indices[n];
       if (row < 0 || row >= a.num_slots) {
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
         continue;
       }
     }
-    if (finder.seq.end(n) > finder.seq.begin(n) || !a.final_state) continue;
+    if (finder.seq.end((int)n) > finder.seq.begin((int)n) || !a.final_state) continue;
     const size_t at = (size_t)row * a.D + ch;
     write_state(a.final_state + at, read_state<N>(a.initial_state ? a.initial_state + at : nullptr, mine), mine);
   }

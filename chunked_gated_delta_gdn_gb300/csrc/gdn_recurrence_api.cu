@@ -13,6 +13,7 @@ namespace {
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 size_t elem_size(int d) { return d == GDN_BF16 ? 2 : 4; }
 constexpr int kMaxChannels = 1 << 28;   // (a row's bytes are counted in 32 bits)
+constexpr int kMaxPacked = 1 << 30;     // packed sequences (the search for one halves sums of two counts in 32 bits)
 bool is_dtype(int d) { return d == GDN_F32 || d == GDN_BF16; }
 
 // Sizes, and the gates' form: lam and i come together.
@@ -34,10 +35,16 @@ gdn_status_t check(const void* x, const void* g, const void* i, const float* lam
 gdn_status_t check_batch(int B, int T, const int32_t* cu_seqlens, int num_seqs, const int32_t* state_indices,
                          int* N) {
   if (B < 0 || T < 0 || num_seqs < 0) return GDN_ERR_SHAPE;
-  if (cu_seqlens && B != 1) return GDN_ERR_SHAPE;
+  if (cu_seqlens && (B != 1 || num_seqs > kMaxPacked)) return GDN_ERR_SHAPE;
   *N = cu_seqlens ? num_seqs : B;
   if (!aligned_to(cu_seqlens, 4) || !aligned_to(state_indices, 4)) return GDN_ERR_LAYOUT;
   return GDN_OK;
+}
+
+// The sizes of a question for scratch, whose num_seqs is B where sequences are rows.
+bool sizes_fit(int B, int T, int D, int num_seqs) {
+  return B >= 0 && T >= 0 && D > 0 && D <= kMaxChannels && num_seqs >= 0 && (num_seqs <= kMaxPacked || num_seqs == B) &&
+         (long long)B * T <= 0x7fff0000LL;
 }
 
 }  // namespace
@@ -45,12 +52,12 @@ gdn_status_t check_batch(int B, int T, const int32_t* cu_seqlens, int num_seqs, 
 extern "C" {
 
 size_t gdn_linear_recurrence_carries_size(int B, int T, int D) {
-  if (B < 0 || T < 0 || D <= 0 || D > kMaxChannels || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
+  if (!sizes_fit(B, T, D, 0)) return (size_t)-1;
   return gdn::recurrence_carries_bytes((long long)B * T, D);
 }
 
 size_t gdn_linear_recurrence_fwd_workspace_size(int B, int T, int D, int num_seqs) {
-  if (B < 0 || T < 0 || D <= 0 || D > kMaxChannels || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
+  if (!sizes_fit(B, T, D, num_seqs)) return (size_t)-1;
   return gdn::recurrence_fwd_workspace_bytes(B, T, D, num_seqs);
 }
 
@@ -99,7 +106,7 @@ gdn_status_t gdn_linear_recurrence_fwd(const void* x, const void* g, const void*
 }
 
 size_t gdn_linear_recurrence_bwd_workspace_size(int B, int T, int D, int num_seqs, int fused_gates) {
-  if (B < 0 || T < 0 || D <= 0 || D > kMaxChannels || num_seqs < 0 || (long long)B * T > 0x7fff0000LL) return (size_t)-1;
+  if (!sizes_fit(B, T, D, num_seqs)) return (size_t)-1;
   return gdn::recurrence_bwd_workspace_bytes(B, T, D, num_seqs, fused_gates != 0);
 }
 

@@ -87,8 +87,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   finder.part = part_of(finder.seq, part_index, parts);
   const Part part = finder.part;
   if (a.d_initial_state && !kSteps) {   // empty sequences
-    for (int n = part.n0 + segment * kWarps + warp; n < part.n1; n += segments.count * kWarps) {
-      if (finder.seq.end(n) > finder.seq.begin(n)) continue;
+    for (long long n = part.n0 + segment * kWarps + warp; n < part.n1; n += segments.count * kWarps) {
+      if (finder.seq.end((int)n) > finder.seq.begin((int)n)) continue;
       const size_t at = (size_t)n * a.D + ch;
       write_state(a.d_initial_state + at, read_state<N>(a.d_final_state ? a.d_final_state + at : nullptr, mine), mine);
     }

@@ -93,7 +93,8 @@ def _sequences(x, cu_seqlens):
         raise ValueError("cu_seqlens requires B == 1")
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be [num_seqs + 1]")
-    _int32("gated linear recurrence", cu_seqlens.numel())
+    if cu_seqlens.numel() - 1 > 1 << 30:
+        raise ValueError("cu_seqlens packs at most 2^30 sequences (got %d)" % (cu_seqlens.numel() - 1))
     return cu_seqlens.numel() - 1
 
 

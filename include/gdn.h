@@ -557,7 +557,7 @@ gdn_status_t gdn_group_norm_act_bwd(const void* dy, const void* x, const void* w
  *   initial_state, output_final_state, final_state, cu_seqlens, num_seqs, state_indices,
  *   num_slots, stream  as gdn_chunk_fwd, states [N, D] or slots [num_slots, D] fp32: slot -1 is
  *               padding (zero rows, no state access), sequences may be empty, final_state may be
- *               initial_state.
+ *               initial_state.  At most 2^30 packed sequences.
  *   y           [B, T, D] io_dtype, contiguous, written completely: tokens past the last sequence
  *               get zeros.  NULL where only carries are wanted.
  *   carries     gdn_linear_recurrence_carries_size(...) bytes, or NULL: the state in front of
