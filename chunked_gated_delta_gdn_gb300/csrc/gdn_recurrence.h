@@ -47,6 +47,16 @@ struct RecurrenceArgs {
   cudaStream_t stream;
 };
 
+// The forward's launch that makes a backward's carries again.  What goes wrong in it is the caller's to know: wrong
+// carries are wrong gradients, and the backward's own kernel cannot tell.
+inline RecurrenceArgs carries_again(const RecurrenceArgs& a, float* carries, void* workspace) {
+  RecurrenceArgs f = a;
+  f.carries = carries;
+  f.workspace = workspace;
+  f.y = nullptr;
+  return f;
+}
+
 size_t recurrence_carries_bytes(long long tokens, int D);
 size_t recurrence_fwd_workspace_bytes(int B, int T, int D, int num_seqs);
 size_t recurrence_bwd_workspace_bytes(int B, int T, int D, int num_seqs, bool fused);

@@ -435,13 +435,9 @@ cudaError_t launch_recurrence_bwd(const RecurrenceArgs& args) {
   ws += up256(recurrence_fwd_workspace_bytes(a.B, a.T, a.D, a.num_seqs));
   float* const steps = reinterpret_cast<float*>(ws);
   if (!a.carries && (long long)a.B * a.T > 0) {
-    RecurrenceArgs f = a;
-    f.carries = a.carries = carries;
-    f.workspace = forward;
-    f.y = nullptr;
-    f.dev_status = nullptr;
-    const cudaError_t err = launch_recurrence_fwd(f);
+    const cudaError_t err = launch_recurrence_fwd(carries_again(a, carries, forward));
     if (err != cudaSuccess) return err;
+    a.carries = carries;
   }
   if (a.io_dtype == GDN_F32) return launch_bwd<float, float, 1>(a, steps);
   return a.g_dtype == GDN_F32 ? launch_bwd<__nv_bfloat16, float, 1>(a, steps)
