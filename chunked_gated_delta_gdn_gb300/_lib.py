@@ -27,6 +27,7 @@ EXPORTS = ("gdn_chunk_fwd", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd_path"
            "gdn_product_chunk_fwd", "gdn_product_chunk_fwd_workspace_size", "gdn_product_decode",
            "gdn_chunk_bwd", "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd_gated",
            "gdn_chunk_bwd_gated_workspace_size", "gdn_selftest_wait_timeout",
+           "gdn_selftest_recurrence_wait",
            "gdn_linear_attn_chunk_fwd", "gdn_linear_attn_chunk_fwd_workspace_size",
            "gdn_linear_attn_chunk_bwd", "gdn_linear_attn_chunk_bwd_workspace_size",
            "gdn_linear_attn_decode",
@@ -105,6 +106,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.gdn_chunk_bwd_gated_workspace_size.restype = sz
         lib.gdn_selftest_wait_timeout.argtypes = [vp, ctypes.c_ulonglong, i, vp, vp]
         lib.gdn_selftest_wait_timeout.restype = i
+        lib.gdn_selftest_recurrence_wait.argtypes = [vp, i, i, vp, vp]
+        lib.gdn_selftest_recurrence_wait.restype = i
         lib.gdn_linear_attn_chunk_fwd.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, i, f, vp, i, vp,
                                                   vp, i, vp, i, vp, vp, sz, vp, vp]
         lib.gdn_linear_attn_chunk_fwd.restype = i

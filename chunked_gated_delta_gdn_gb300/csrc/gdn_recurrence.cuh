@@ -345,17 +345,18 @@ __device__ __forceinline__ void write_state(float* row, const Lanes<N>& x, int n
 
 // ---------------------------------------------------------------- hand-overs
 
-// A wait of at most this many tries (seconds).  One that has run out is reported, and none of its kind
-// follows it: what the launch writes is then not to be used.
-constexpr int kTries = 1 << 25;
-__device__ __forceinline__ bool wait_some(uint64_t* bar, unsigned parity) {
-  for (int k = 0; k < kTries; ++k)
+// A wait of at most this many tries, 2 s: the hardware gives one that finds nothing 3.8 us.  One that has run out is
+// reported, and none of its kind follows it: what the launch writes is then not to be used.
+constexpr int kTries = 1 << 19;
+__device__ __forceinline__ bool wait_some(uint64_t* bar, unsigned parity, int tries = kTries) {
+  for (int k = 0; k < tries; ++k)
     if (mbar_try_wait(bar, parity)) return true;
   return false;
 }
 constexpr unsigned kMessage = 1, kCopy = 2;   // the kinds
-__device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, unsigned* lost, int* dev_status) {
-  if (*lost & kMessage || wait_some(bar, parity)) return;
+__device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, unsigned* lost, int* dev_status,
+                                               int tries = kTries) {
+  if (*lost & kMessage || wait_some(bar, parity, tries)) return;
   *lost |= kMessage;
   report(dev_status, GDN_DEV_TIMEOUT);
 }
@@ -363,11 +364,12 @@ __device__ __forceinline__ void wait_or_report(uint64_t* bar, unsigned parity, u
 // same time again: no copy outlives its CTA.
 template <int kStages, int kWarps>
 __device__ __forceinline__ void wait_for_copies(uint64_t (*arrived)[kWarps], int warp, int round, int rounds, unsigned* lost,
-                                                int* dev_status) {
-  if (*lost & kCopy || wait_some(&arrived[round % kStages][warp], round / kStages & 1)) return;
+                                                int* dev_status, int tries = kTries) {
+  if (*lost & kCopy || wait_some(&arrived[round % kStages][warp], round / kStages & 1, tries)) return;
   *lost |= kCopy;
   report(dev_status, GDN_DEV_TIMEOUT);
-  for (int k = round; k < min(round + kStages, rounds); ++k) wait_some(&arrived[k % kStages][warp], k / kStages & 1);
+  for (int k = round; k < min(round + kStages, rounds); ++k)
+    wait_some(&arrived[k % kStages][warp], k / kStages & 1, tries);
 }
 
 // The state in front of a window: 2^L base + H.

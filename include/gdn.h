@@ -697,6 +697,21 @@ gdn_status_t gdn_selftest_wait_timeout(int* dev_status, unsigned long long limit
                                        int arrive_first, unsigned long long* waited_ns,
                                        void* stream);
 
+/*
+ * gdn_selftest_recurrence_wait -- the same for the gated linear recurrence, whose waits end after a number of tries:
+ * one thread waits for a message and then for copies, each twice, on mbarriers that nobody arrives on or
+ * (arrive_first = 1) that it has arrived on.  A wait that runs out sets GDN_DEV_TIMEOUT, and none of its
+ * kind follows it.
+ *
+ *   dev_status  device int (required) receiving GDN_DEV_* bits.
+ *   tries       1 .. 10000 (else GDN_ERR_SHAPE).
+ *   waited_ns   device unsigned long long[5] (required): the time of the first and second wait for a message, and for
+ *               copies (global timer); then the tries that the recurrence's own waits have.
+ *   stream      as above.
+ */
+gdn_status_t gdn_selftest_recurrence_wait(int* dev_status, int tries, int arrive_first,
+                                          unsigned long long* waited_ns, void* stream);
+
 /* Static, NUL-terminated name of a status code ("GDN_OK", ...). */
 const char* gdn_status_string(gdn_status_t status);
 

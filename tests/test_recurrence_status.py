@@ -6,7 +6,7 @@ import subprocess
 
 import pytest
 
-from chunked_gated_delta_gdn_gb300 import build
+from chunked_gated_delta_gdn_gb300 import _lib, build
 
 AGAIN = r"""
 #include <stdio.h>
@@ -39,3 +39,50 @@ def test_the_forward_run_again_reports_to_the_caller(tmp_path):
                    check=True)
     got = subprocess.run([str(exe)], capture_output=True, text=True)
     assert got.returncode == 0, got.stdout
+
+
+def test_waits_selftest_validates_on_the_host():
+    L = _lib.load()
+    assert L.gdn_selftest_recurrence_wait(None, 10, 0, None, None) == _lib.GDN_ERR_NULL
+    assert L.gdn_selftest_recurrence_wait(1 << 20, 10, 0, None, None) == _lib.GDN_ERR_NULL
+    for tries in (0, -1, 10001):
+        assert L.gdn_selftest_recurrence_wait(1 << 20, tries, 0, 1 << 20, None) == _lib.GDN_ERR_SHAPE
+
+
+def waits(tries, arrive_first):
+    """(status bits, nanoseconds of the four waits and the tries of the kernels' own)."""
+    torch = pytest.importorskip("torch")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    waited = torch.zeros(5, dtype=torch.int64, device="cuda")
+    rc = _lib.load().gdn_selftest_recurrence_wait(status.data_ptr(), tries, arrive_first, waited.data_ptr(),
+                                                  torch.cuda.current_stream().cuda_stream)
+    assert rc == _lib.GDN_OK, _lib.status_string(rc)
+    torch.cuda.synchronize()
+    return status.item(), waited.tolist()
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out_are_reported_once():
+    """The time goes with the tries; the second wait of a kind does not wait, and the copies' one gives those under
+    way their time as well."""
+    few, many = waits(10, 0), waits(1000, 0)
+    print("10 tries %s ns, 1000 tries %s ns" % (few[1], many[1]))
+    for bits, waited in (few, many):
+        assert bits == _lib.GDN_DEV_TIMEOUT
+    first, again, copies, none, _ = many[1]
+    assert 0 < first < 1e9 and again < first / 10 and none < first / 10 and copies > 1.5 * first
+    assert many[1][0] > 5 * few[1][0]
+
+
+@pytest.mark.gpu
+def test_waits_for_what_has_come_report_nothing():
+    bits, waited = waits(1000, 1)
+    assert bits == 0 and max(waited[:4]) < 1e6
+
+
+@pytest.mark.gpu
+def test_the_kernels_waits_end_within_seconds():
+    _, waited = waits(1000, 0)
+    limit = waited[0] / 1000 * waited[4] * 1e-9
+    print("a wait of the kernels ends after %.2f s" % limit)
+    assert 0.2 < limit < 5
