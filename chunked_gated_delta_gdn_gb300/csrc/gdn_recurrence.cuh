@@ -461,11 +461,11 @@ __device__ __forceinline__ void write_step(float* steps, int D, int ch, const La
   write_state(steps + ch, reset ? fill<N>(kReset) : L, mine);
   write_state(steps + D + ch, H, mine);
 }
-// The state behind the first `count` segments, for the warp that starts the chain; every warp joins a share of the
-// steps, which stand in the chain's slots for a moment.
+// The state behind the first `count` segments, for the warp that starts the chain (`starts`; nothing for the others):
+// every warp joins a share of the steps, which stand in the chain's slots until that warp sends its first message.
 template <int kWarps, int N>
 __device__ __forceinline__ Lanes<N> behind_steps(Chain<kWarps, N>& chain, const float* first, int count, int D, int ch, int mine,
-                                                 int warp, int lane) {
+                                                 int warp, int lane, bool starts) {
   Lanes<N> L = fill<N>(0.f), H = fill<N>(0.f);
 #pragma unroll 4
   for (int k = count * warp / kWarps; k < count * (warp + 1) / kWarps; ++k) {
@@ -478,7 +478,7 @@ __device__ __forceinline__ Lanes<N> behind_steps(Chain<kWarps, N>& chain, const 
   chain.slot[warp][lane].H = H;
   __syncthreads();
   H = fill<N>(0.f);
-  for (int k = 0; k < kWarps; ++k)
+  for (int k = 0; k < kWarps && starts; ++k)
     H = each([](float l, float x, float h) { return l == kReset ? x : fmaf(ex2(l), h, x); }, chain.slot[k][lane].L,
              chain.slot[k][lane].H, H);
   return H;

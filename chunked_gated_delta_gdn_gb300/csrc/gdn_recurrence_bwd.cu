@@ -151,7 +151,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   Values start = fill<N>(0.f);
   if (!kSteps && segment > 0) {
     wait_for_previous();
-    start = behind_steps(sh.chain, steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine, warp, lane);
+    start = behind_steps(sh.chain, steps + (size_t)part_index * segments.count * 2 * a.D, segment, a.D, ch, mine, warp, lane,
+                         warp + 1 == kWarps);
   }
   if (warp + 1 == kWarps) sh.chain.start(lane, start);
   Values sum = fill<N>(0.f);   // of a segment's logarithms
