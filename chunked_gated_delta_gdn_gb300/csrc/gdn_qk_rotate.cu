@@ -14,10 +14,10 @@
 // sums (7 us) are what is missing; three axes, 2 x 9731 x (12 + 12): 44 us, 5.4 TB/s.  Three CTAs an SM instead
 // of two, or streaming stores, were slower.
 //
-// Angles: phi / 2 pi as a fraction of 2^64, position * round(2^64 frac(inv_freq / 2 pi)) in integers
-// that wrap, is exact to 2^-11 of fp32's rounding for every position.  What is left is less than half a
-// turn: there the hardware's sine and cosine are off by 2^-21 of a unit at most, which is enough for bf16;
-// fp32 takes the full functions.
+// Angles: phi / 2 pi as a fraction of 2^64, position * floor(2^64 frac(inv_freq / 2 pi)) in integers that wrap,
+// of which the upper 32 bits are kept: off by less than 2^-31 of a turn for every position and finite frequency.
+// What is left is rounded to fp32 and less than half a turn: there the hardware's sine and cosine are off by
+// 2^-21 of a unit at most, which is enough for bf16; fp32 takes the full functions.
 #include "gdn_common.cuh"
 #include "gdn_launch.cuh"
 #include "gdn_qk_rotate.h"
@@ -102,10 +102,22 @@ __device__ __forceinline__ int pair_of(const Unit& u, int j) {
   return kInVector ? (j < V / 2 ? u.o1 / 2 + j : u.o2 / 2 + j - V / 2) : V == 1 && u.o2 == u.o1 + 1 ? u.o1 / 2 : u.o1 + j;
 }
 
-// frac(f / 2 pi) in units of 2^-64.
+// frac(f / 2 pi) in units of 2^-64, to one of them, for every finite f = m 2^e: m (24 bits) times the 96 bits of
+// 1 / 2 pi behind its first e ones, all that matters (after Payne and Hanek, "Radian reduction for trigonometric
+// functions", 1983; the bits are those of Machin's formula for pi).
+__constant__ unsigned kTurnsPerRadian[7] = {0x28be60dbu, 0x9391054au, 0x7f09d5f4u, 0x7d4d3770u,
+                                            0x36d8a566u, 0x4f10e410u, 0x7f9458eau};
 __device__ __forceinline__ unsigned long long turn_rate(float f) {
-  const double t = (double)f * 0.15915494309189533577;
-  return (unsigned long long)((t - floor(t)) * 18446744073709551616.0);
+  const unsigned bits = __float_as_uint(f), exponent = bits >> 23 & 0xff;
+  const unsigned long long m = (bits & 0x7fffff) | (exponent ? 0x800000 : 0);
+  const int e = (int)max(exponent, 1u) - 150, word = e >> 5, shift = e & 31;
+  unsigned w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w[k] = (unsigned)(word + k) < 7u ? kTurnsPerRadian[word + k] : 0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) w[k] = __funnelshift_l(w[k + 1], w[k], shift);
+  const unsigned long long rate = (m * w[0] << 32) + m * w[1] + (m * w[2] >> 32);
+  return bits >> 31 ? 0 - rate : rate;
 }
 
 // The angle of a position, as sine and cosine.
