@@ -11,7 +11,8 @@
 // halves, or, interleaved, any two.  Lanes copy heads ahead into rings of their own in shared memory
 // (asynchronous copies, no barrier).  bf16, heads of 128: forward of 4 x 32768 x (16 + 16) 320 us, 6.7 TB/s;
 // 2 x 8192 x (32 + 8) 64 us forward, 91 us backward, 5.2 and 5.5 TB/s, of which launch, first loads and the weights'
-// sums (7 us) are what is missing; three axes, 2 x 9731 x (12 + 12): 44 us, 5.4 TB/s.  Three CTAs an SM instead
+// sums (7 us) are what is missing; three axes, 2 x 9731 x (12 + 12): 45 us, 5.3 TB/s.  fp32,
+// 4 x 8192 x (16 + 16): 170 us forward, 269 backward, 6.3 and 6.0 TB/s.  Three CTAs an SM instead
 // of two, or streaming stores, were slower.
 //
 // Angles: phi / 2 pi as a fraction of 2^64, position * floor(2^64 frac(inv_freq / 2 pi)) in integers that wrap,

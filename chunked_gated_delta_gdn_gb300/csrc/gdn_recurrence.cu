@@ -12,9 +12,9 @@
 // Bound by bytes: 3 or (fused) 4 values an element.  bf16, 4 x 32768 x 4096: given 473 us, 6.8 TB/s (a plain copy's
 // rate); fused 690 us, 6.2 TB/s.  2 x 8192 x 4096 has 128 CTAs for 152 SMs; with fused gates what they issue
 // counts, too (three exponentials, two reciprocals and a root among 31 instructions an element; 68% of the issue
-// slots): 101 us, 5.3 TB/s; given 66 us, 6.1 TB/s.  One channel a lane (twice the CTAs, half as wide rows): 122 and
+// slots): 101 us, 5.3 TB/s; given 66 us, 6.1 TB/s.  fp32: 4 x 32768 x 4096 fused 1.24 ms, 6.9 TB/s; given 0.99 ms, 6.5.  One channel a lane (twice the CTAs, half as wide rows): 122 and
 // 107 us; three stages with given gates, 523 and 68 us; 8-token windows with three CTAs an SM, and all of it in
-// packed arithmetic (113 us, spilled registers), were slower too.  In segments, one 32768 x 2048 given: 102 us for
+// packed arithmetic (113 us, spilled registers), were slower too.  In segments, one 32768 x 2048 given: 101 us for
 // 59 us of bytes, some of which are read twice.
 #include <algorithm>
 
@@ -280,8 +280,9 @@ cudaError_t launch_fwd(const RecurrenceArgs& a) {
 
 constexpr int kDecodeThreads = 128;
 
-// Bound by bytes, 8 a state and 6 or 8 (bf16) of the token's; 2048 x 4096 given: 32 us, 3.7 TB/s.  256 x 4096 takes
-// 11 us of a captured graph, 8 of which an empty one takes.
+// 8 bytes a state and 6 or 8 (bf16) of the token's.  2048 x 4096 takes 32 us given and 34 fused of a captured graph, of
+// which one small kernel takes 7: 3.7 TB/s, 4.7 without those 7, so not the bytes' rate (17 us).  A thread has two
+// requests under way, each of them a slot's index and, behind it, the state.  256 x 4096 takes 11 us.
 // A thread has V channels of a few requests; what a channel's gates have in common it makes once.
 template <typename T, typename G, bool kFused, int V>
 __global__ void __launch_bounds__(kDecodeThreads) recurrence_decode_kernel(RecurrenceArgs a, int requests) {
